@@ -234,7 +234,7 @@ def _own_mx4_trip(s):
 def _own_mx4_fwd(s):
     from ragged_grouped_gemm_device_gb300 import _lib as L
     T, E, k, d, h = (s[n] for n in ("T", "E", "k", "d", "h"))
-    L.moe_permute_mxfp4(s["x"], s["sorted_src"], s["offsets"], T, k, E, d, s["xq"], s["xsf"])
+    L.moe_permute_mxfp4(s["x"], s["inv_map"], s["offsets"], T, k, E, d, s["xq"], s["xsf"])
     L.moe_grouped_swiglu_fwd_mxfp4(s["xq"], s["xsf"], s["offsets"], E, T * k, d, h, s["mxw"], s["y"], s["ws"])
     L.moe_unpermute_combine(s["y"], s["inv_map"], s["weights"], T, k, d, s["out"])
     return s["out"]
