@@ -70,6 +70,12 @@ typedef enum {
 #define MOE_DEV_TIMEOUT 0x1
 #define MOE_DEV_BAD_OFFSETS 0x2
 
+/* element types of the calls that take more than bf16 (layer norm, gate) */
+typedef enum {
+  MOE_DTYPE_BF16 = 0,
+  MOE_DTYPE_F32 = 1
+} moe_dtype_t;
+
 /* operations for moe_workspace_bytes */
 typedef enum {
   MOE_OP_ROUTE = 0,       /* moe_route_offsets */
@@ -81,7 +87,12 @@ typedef enum {
   MOE_OP_MX_WEIGHTS = 6,  /* moe_mx_prepare_weights: the prepared MXFP8 weights */
   MOE_OP_MX_FWD = 7,      /* moe_grouped_swiglu_fwd_mxfp8 */
   MOE_OP_MX_BWD = 8,      /* moe_grouped_bwd_mxfp8 */
-  MOE_OP_MX_ROW_SCALES = 9 /* moe_mx_quantize_rows: scale bytes for T*top_k rows of K = d */
+  MOE_OP_MX_ROW_SCALES = 9, /* moe_mx_quantize_rows: scale bytes for T*top_k rows of K = d */
+  MOE_OP_MX4_WEIGHTS = 10, /* moe_mx4_prepare_weights: the prepared MXFP4 weights */
+  MOE_OP_MX4_FWD = 11,     /* moe_grouped_swiglu_fwd_mxfp4 */
+  MOE_OP_MX4_ROW_SCALES = 12, /* moe_mx4_quantize_rows: scale bytes for T*top_k rows of K = d */
+  MOE_OP_GATE = 13,        /* moe_gate_fwd with its statistics (d and h ignored) */
+  MOE_OP_LAYER_NORM_BWD = 14 /* moe_layer_norm_bwd: T rows of width d (E = top_k = 1, h ignored) */
 } moe_op_t;
 
 /* Bytes of caller workspace that `op` needs for these sizes (0 when none). Pure host
@@ -428,6 +439,113 @@ moe_status_t moe_grouped_bwd_mxfp8(const moe_bf16* dy, const uint8_t* dyq, const
 moe_status_t moe_route_offsets_noalloc(const int32_t* ids, int T, int top_k, int E,
                                        int32_t* counts, int32_t* offsets, int32_t* sorted_src,
                                        int32_t* inv_map, moe_stream_t stream);
+
+/*
+ * MXFP4 variant (serving) -- the SwiGLU experts with both operands of every product in 4 bits.
+ * Format: OCP Microscaling MXFP4 -- blocks of 32 consecutive elements along the contraction
+ * dimension share one power-of-two scale 2^s stored as E8M0 (s + 127), each element is E2M1 (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives); s = floor(log2(max |v|)) - 2, not below -127 (-127 for an
+ * all-zero block); elements are v / 2^s rounded to nearest, ties to even, saturated to +-6. A block
+ * with a NaN or an infinity gets the scale 0xFF: it reads as NaN and every product with it is NaN.
+ * x is quantized along d and W_ug along d, the SwiGLU output and W_down along h. Products
+ * accumulate in fp32 in tensor memory (tcgen05.mma kind::mxf4.block_scale). There is no backward:
+ * training runs the BF16 or the MXFP8 path. Shapes: d and h multiples of 32, 1 <= E <= 1024;
+ * others return MOE_ERR_UNSUPPORTED_SHAPE.
+ *
+ * Layouts. Codes of an operand [rows, K] are K / 2 bytes a row, row-major, element 2i in the low
+ * half of byte i. Scales come in the 512-byte atoms of the MXFP8 variant, one per (128-row tile,
+ * 128-element chunk of K), tile * KC + chunk, with KC = 2 ceil(K / 256) chunks a row (the scales
+ * past K are 2^0). For an activation the tiles are the problem list's 128-row tiles.
+ *
+ * moe_mx4_prepare_weights -- quantize W_ug [E, 2h, d] and W_down [E, h, d] (bf16) into `mxw`
+ *   (moe_workspace_bytes(MOE_OP_MX4_WEIGHTS, 0, 1, E, d, h, 0) bytes, 256-byte aligned): codes and
+ *   scales of W_ug along d, then of W_down^T [E, d, h] along h, each piece on a 256-byte boundary.
+ *   Scale tiles of W_ug: (2e + half) * ceil(h / 128) + n / 128 (half 0 gate, 1 up, n the row within
+ *   it); of W_down^T: e * NTp + n / 128 with NTp = ceil(d / 128) rounded up to even. Run once per
+ *   weight update.
+ * moe_mx4_quantize_rows -- quantize rows p < M = offsets[E-1] of x [cap, K] (bf16) into codes q
+ *   [cap, K / 2] and scale atoms sf (moe_workspace_bytes(MOE_OP_MX4_ROW_SCALES, T, top_k, E, K, 32,
+ *   0) bytes for cap = T*top_k; h only has to be valid). K a multiple of 32.
+ * moe_mx4_dequantize_rows -- the bf16 values that the codes and scales of rows p < M stand for
+ *   (exact: no rounding). Rows at or past M are not written.
+ * moe_permute_mxfp4 -- the permute's gather and the quantization along d in one pass: row
+ *   inv_map[t*top_k + j] of q and sf gets x[t] quantized, for every slot that is not dropped
+ *   (inv_map < 0). x [T, d] bf16, q [T*top_k, d / 2], sf as for moe_mx4_quantize_rows.
+ * moe_grouped_swiglu_fwd_mxfp4 -- Eq. 13 with 4-bit products: U = q(x) q(W_ug)^T, A = SwiGLU(U) in
+ *   fp32, quantized along h from fp32 in the same epilogue, y = q(A) q(W_down), rounded once to
+ *   bf16 (rows < M). xq, xsf as the two calls above wrote them; routing weights go to the combine.
+ *   ws = moe_workspace_bytes(MOE_OP_MX4_FWD, ...) bytes (256-byte aligned): codes and scales of A.
+ * Offsets that decrease or exceed cap set MOE_DEV_BAD_OFFSETS and nothing is written.
+ */
+moe_status_t moe_mx4_prepare_weights(const moe_bf16* w_ug, const moe_bf16* w_down, int E, int d, int h, void* mxw,
+                                     size_t mxw_bytes, moe_stream_t stream);
+moe_status_t moe_mx4_quantize_rows(const moe_bf16* x, const int32_t* offsets, int E, int cap, int K, uint8_t* q,
+                                   uint8_t* sf, int32_t* dev_status, moe_stream_t stream);
+moe_status_t moe_mx4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const int32_t* offsets, int E, int cap,
+                                     int K, moe_bf16* x, int32_t* dev_status, moe_stream_t stream);
+moe_status_t moe_permute_mxfp4(const moe_bf16* x, const int32_t* inv_map, const int32_t* offsets, int T, int top_k,
+                               int E, int d, uint8_t* q, uint8_t* sf, int32_t* dev_status, moe_stream_t stream);
+moe_status_t moe_grouped_swiglu_fwd_mxfp4(const uint8_t* xq, const uint8_t* xsf, const int32_t* offsets, int E,
+                                          int cap, int d, int h, const void* mxw, moe_bf16* y, void* ws,
+                                          size_t ws_bytes, int32_t* dev_status, moe_stream_t stream);
+
+/*
+ * moe_gate_fwd, moe_gate_bwd -- the router's gate: from router logits to the expert ids and routing
+ * weights that moe_route_offsets and the combine take, with the auxiliary losses of training.
+ *   p = softmax(logits[t, :]);  lse_t = log sum_e exp(logits[t, e])
+ *   ids[t, :] = the top_k experts by logit, larger first, ties to the lower expert
+ *   weights[t, j] = p[ids[t, j]], or with MOE_GATE_RENORM divided by their sum over the token's slots
+ *   N = tokens that take part;  counts[e] = slots routed to e;  prob_sum[e] = sum_t p[t, e]
+ *   loss[0] = E sum_e counts[e] / (top_k N) * prob_sum[e] / N  (balance);  loss[1] = sum_t lse_t^2 / N  (z)
+ * A token takes no part when token_mask is given and 0 for it, or when all its logits are -inf: its
+ * ids are -1 (moe_route_offsets drops them), its weights 0, its lse -inf, its gradient 0. An expert
+ * with logit -inf is never selected: a token with fewer than top_k others gets id -1 and weight 0
+ * in its last slots. A NaN is never selected either, but makes the token's weights, and the losses
+ * and gradients that depend on it, NaN. N = 0 gives losses of 0.
+ *
+ *  logits  [T, E] of `dtype` (moe_dtype_t), rows `ld` elements apart (0: one row for all tokens).
+ *  ids, weights  [T*top_k] int32 / fp32 out.   lse  nullable [T] fp32 out (the backward needs it).
+ *  counts [E] int32, n_valid [1] int32, prob_sum [E] fp32, loss [2] fp32  out, all given or all NULL.
+ *  ws      moe_workspace_bytes(MOE_OP_GATE, T, top_k, E, 0, 0, 0) bytes with them, else unused.
+ * Backward: d_weights [T*top_k] fp32 (the gradient of weights; nullable, then ids and weights may
+ * be NULL) and d_loss [2] fp32 on the device (the gradients of the two losses; nullable, then
+ * counts and n_valid may be NULL) -> dlogits [T, E] of `dtype`, rows `ldd` >= E elements apart, every
+ * row written. The counts are constants of the gradient. All sums are fp32 and their order is
+ * fixed. Limits: top_k <= min(32, E), E <= 1024; pointers aligned to their element size.
+ */
+#define MOE_GATE_RENORM 0x1
+moe_status_t moe_gate_fwd(const void* logits, int dtype, long long ld, const uint8_t* token_mask, int T, int top_k,
+                          int E, int flags, int32_t* ids, float* weights, float* lse, int32_t* counts,
+                          int32_t* n_valid, float* prob_sum, float* loss, void* ws, size_t ws_bytes,
+                          moe_stream_t stream);
+moe_status_t moe_gate_bwd(const void* logits, int dtype, long long ld, const float* lse, const int32_t* ids,
+                          const float* weights, const int32_t* counts, const int32_t* n_valid, const float* d_weights,
+                          const float* d_loss, int T, int top_k, int E, int flags, void* dlogits, long long ldd,
+                          moe_stream_t stream);
+
+/*
+ * moe_layer_norm_fwd, moe_layer_norm_bwd -- layer norm over the last dimension (the pre-norm of the
+ * expert block): y = (x - mean) rstd gamma + beta with mean = sum x / d, rstd = 1 / sqrt(sum (x -
+ * mean)^2 / d + eps), in fp32, y rounded once.
+ *  x, y    [T, d] of `dtype` (moe_dtype_t); rows of x are ldx elements apart, of y ldy >= d. A row
+ *          pitch of 0 reads one row for all (x, dy).
+ *  gamma, beta  nullable (ones, zeros) [d] of `w_dtype`.
+ *  mean, rstd   nullable [T] fp32 out (the backward needs both).
+ * Backward: dx = rstd (gamma dy - mean(gamma dy) - xhat mean(gamma dy xhat)), rounded once to
+ * `dtype`; dgamma = sum_t dy xhat and dbeta = sum_t dy, fp32 [d], each nullable, summed in a fixed
+ * order (zeros for T = 0).
+ *  ws      moe_workspace_bytes(MOE_OP_LAYER_NORM_BWD, T, 1, 1, d, 0, 0) bytes when dgamma or dbeta
+ *          is wanted.
+ * Limits: 1 <= d <= 2^20; pointers aligned to their element size (rows whose bases and pitches are
+ * multiples of 16 bytes move 16 bytes at a time, others one element); eps >= 0.
+ */
+moe_status_t moe_layer_norm_fwd(const void* x, int dtype, long long ldx, const void* gamma, const void* beta,
+                                int w_dtype, int T, int d, float eps, void* y, long long ldy, float* mean,
+                                float* rstd, moe_stream_t stream);
+moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, long long ldx, int dtype,
+                                const void* gamma, int w_dtype, const float* mean, const float* rstd, int T, int d,
+                                void* dx, long long lddx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                moe_stream_t stream);
 
 /* Human-readable text of a status (static storage). */
 const char* moe_status_string(moe_status_t status);

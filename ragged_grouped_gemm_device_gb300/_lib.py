@@ -24,8 +24,11 @@ MOE_DEV_TIMEOUT = 0x1
 MOE_DEV_BAD_OFFSETS = 0x2
 OP_ROUTE, OP_FWD, OP_BWD, OP_PADDED_BMM, OP_LOOP, OP_SAVED, OP_MX_WEIGHTS, OP_MX_FWD, OP_MX_BWD, OP_MX_ROW_SCALES = \
     range(10)
+OP_MX4_WEIGHTS, OP_MX4_FWD, OP_MX4_ROW_SCALES, OP_GATE, OP_LAYER_NORM_BWD = range(10, 15)
+DTYPE_BF16, DTYPE_F32 = 0, 1
+GATE_RENORM = 0x1
 
-_P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _S, _L, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
 _PI32, _PI64 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_longlong)
 SIGNATURES = {
     "moe_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I, _I]),
@@ -53,6 +56,15 @@ SIGNATURES = {
     "moe_grouped_swiglu_fwd_top1_combine": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P,
                                                  _P]),
     "moe_route_offsets_noalloc": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "moe_mx4_prepare_weights": (_I, [_P, _P, _I, _I, _I, _P, _S, _P]),
+    "moe_mx4_quantize_rows": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_mx4_dequantize_rows": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_permute_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P]),
+    "moe_grouped_swiglu_fwd_mxfp4": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _S, _P, _P]),
+    "moe_gate_fwd": (_I, [_P, _I, _L, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "moe_gate_bwd": (_I, [_P, _I, _L, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _L, _P]),
+    "moe_layer_norm_fwd": (_I, [_P, _I, _L, _P, _P, _I, _I, _I, _F, _P, _L, _P, _P, _P]),
+    "moe_layer_norm_bwd": (_I, [_P, _L, _P, _L, _I, _P, _I, _P, _P, _I, _I, _P, _L, _P, _P, _P, _S, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
     "moe_abi_version": (_I, []),
@@ -113,6 +125,30 @@ def _ptr(t):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("tensors passed to the library must be contiguous CUDA tensors")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _rows(t, T, width):
+    """(pointer, row pitch in elements) of a [T, width] view whose rows are contiguous. A view with
+    one row repeated (row stride 0) is a pitch of 0."""
+    if not t.is_cuda or t.dim() != 2 or t.shape[0] < T or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"expected a CUDA tensor of at least {T} rows of {width} contiguous elements")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if T > 1 else width
+
+
+def _dtype(t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise ValueError(f"expected a bfloat16 or float32 tensor, not {t.dtype}")
+
+
+def _typed(t, dtype, numel, name):
+    """Pointer of a contiguous CUDA tensor of `dtype` with at least `numel` elements (None passes)."""
+    if t is not None and (t.dtype != dtype or t.numel() < numel):
+        raise ValueError(f"{name}: expected at least {numel} elements of {dtype}")
+    return _ptr(t)
 
 
 def _stream(stream):
@@ -290,6 +326,97 @@ def moe_loop_swiglu_fwd(xp, offsets, E, cap, d, h, w_ug, w_down, y, a_save, save
     _check("moe_loop_swiglu_fwd", load().moe_loop_swiglu_fwd(
         _ptr(xp), _ptr(offsets), E, cap, d, h, _ptr(w_ug), _ptr(w_down), _ptr(y), _ptr(a_save),
         _ptr(saved), _ptr(dev_status), _stream(stream)))
+
+
+def moe_mx4_prepare_weights(w_ug, w_down, E, d, h, mxw, stream=None):
+    _check("moe_mx4_prepare_weights", load().moe_mx4_prepare_weights(
+        _ptr(w_ug), _ptr(w_down), E, d, h, _ptr(mxw), _nbytes(mxw), _stream(stream)))
+
+
+def moe_mx4_quantize_rows(x, offsets, E, cap, K, q, sf, dev_status=None, stream=None):
+    _check("moe_mx4_quantize_rows", load().moe_mx4_quantize_rows(
+        _ptr(x), _ptr(offsets), E, cap, K, _ptr(q), _ptr(sf), _ptr(dev_status), _stream(stream)))
+
+
+def moe_mx4_dequantize_rows(q, sf, offsets, E, cap, K, x, dev_status=None, stream=None):
+    _check("moe_mx4_dequantize_rows", load().moe_mx4_dequantize_rows(
+        _ptr(q), _ptr(sf), _ptr(offsets), E, cap, K, _ptr(x), _ptr(dev_status), _stream(stream)))
+
+
+def moe_permute_mxfp4(x, inv_map, offsets, T, top_k, E, d, q, sf, dev_status=None, stream=None):
+    _check("moe_permute_mxfp4", load().moe_permute_mxfp4(
+        _ptr(x), _ptr(inv_map), _ptr(offsets), T, top_k, E, d, _ptr(q), _ptr(sf), _ptr(dev_status), _stream(stream)))
+
+
+def moe_grouped_swiglu_fwd_mxfp4(xq, xsf, offsets, E, cap, d, h, mxw, y, ws, dev_status=None, stream=None):
+    _check("moe_grouped_swiglu_fwd_mxfp4", load().moe_grouped_swiglu_fwd_mxfp4(
+        _ptr(xq), _ptr(xsf), _ptr(offsets), E, cap, d, h, _ptr(mxw), _ptr(y), _ptr(ws), _nbytes(ws),
+        _ptr(dev_status), _stream(stream)))
+
+
+def moe_gate_fwd(logits, token_mask, T, top_k, E, flags, ids, weights, lse=None, counts=None, n_valid=None,
+                 prob_sum=None, loss=None, ws=None, stream=None):
+    """logits [T, E] bf16 or fp32 (any row pitch); token_mask nullable [T] uint8 or bool."""
+    import torch
+    p, ld = _rows(logits, T, E)
+    if token_mask is not None and token_mask.dtype == torch.bool:
+        token_mask = token_mask.view(torch.uint8)
+    i32, f32 = torch.int32, torch.float32
+    _check("moe_gate_fwd", load().moe_gate_fwd(
+        p, _dtype(logits), ld, _typed(token_mask, torch.uint8, T, "token_mask"), T, top_k, E, flags,
+        _typed(ids, i32, T * top_k, "ids"), _typed(weights, f32, T * top_k, "weights"), _typed(lse, f32, T, "lse"),
+        _typed(counts, i32, E, "counts"), _typed(n_valid, i32, 1, "n_valid"), _typed(prob_sum, f32, E, "prob_sum"),
+        _typed(loss, f32, 2, "loss"), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_gate_bwd(logits, lse, ids, weights, counts, n_valid, d_weights, d_loss, T, top_k, E, flags, dlogits,
+                 stream=None):
+    import torch
+    p, ld = _rows(logits, T, E)
+    o, ldd = _rows(dlogits, T, E)
+    if dlogits.dtype != logits.dtype:
+        raise ValueError("dlogits has to have the logits' type")
+    i32, f32 = torch.int32, torch.float32
+    _check("moe_gate_bwd", load().moe_gate_bwd(
+        p, _dtype(logits), ld, _typed(lse, f32, T, "lse"), _typed(ids, i32, T * top_k, "ids"),
+        _typed(weights, f32, T * top_k, "weights"), _typed(counts, i32, E, "counts"),
+        _typed(n_valid, i32, 1, "n_valid"), _typed(d_weights, f32, T * top_k, "d_weights"),
+        _typed(d_loss, f32, 2, "d_loss"), T, top_k, E, flags, o, ldd, _stream(stream)))
+
+
+def _norm_weight(d, *ws):
+    """The type of the given weights (all bf16 or all fp32, [d] each; fp32 when there are none)."""
+    ws = [w for w in ws if w is not None]
+    if any(w.numel() != d for w in ws) or len({w.dtype for w in ws}) > 1:
+        raise ValueError(f"the weights have to be [{d}] and of one type")
+    return _dtype(ws[0]) if ws else DTYPE_F32
+
+
+def moe_layer_norm_fwd(x, gamma, beta, T, d, eps, y, mean=None, rstd=None, stream=None):
+    """x, y [T, d] bf16 or fp32 (any row pitch); gamma, beta nullable [d] bf16 or fp32."""
+    import torch
+    px, ldx = _rows(x, T, d)
+    py, ldy = _rows(y, T, d)
+    if x.dtype != y.dtype:
+        raise ValueError("y has to have x's type")
+    f32 = torch.float32
+    _check("moe_layer_norm_fwd", load().moe_layer_norm_fwd(
+        px, _dtype(x), ldx, _ptr(gamma), _ptr(beta), _norm_weight(d, gamma, beta), T, d, eps, py, ldy,
+        _typed(mean, f32, T, "mean"), _typed(rstd, f32, T, "rstd"), _stream(stream)))
+
+
+def moe_layer_norm_bwd(dy, x, gamma, mean, rstd, T, d, dx, dgamma=None, dbeta=None, ws=None, stream=None):
+    import torch
+    pdy, lddy = _rows(dy, T, d)
+    px, ldx = _rows(x, T, d)
+    pdx, lddx = _rows(dx, T, d)
+    if x.dtype != dy.dtype or x.dtype != dx.dtype:
+        raise ValueError("x, dy and dx have to have one type")
+    f32 = torch.float32
+    _check("moe_layer_norm_bwd", load().moe_layer_norm_bwd(
+        pdy, lddy, px, ldx, _dtype(x), _ptr(gamma), _norm_weight(d, gamma), _typed(mean, f32, T, "mean"),
+        _typed(rstd, f32, T, "rstd"), T, d, pdx, lddx, _typed(dgamma, f32, d, "dgamma"),
+        _typed(dbeta, f32, d, "dbeta"), _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

@@ -223,6 +223,13 @@ __device__ __forceinline__ void st_cluster_zero16(uint32_t cluster_addr) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(cluster_addr), "r"(0u) : "memory");
 }
 
+// 32-byte store (sm_100+ global vector width); the address must be 32-byte aligned
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------------- tcgen05
 // The allocation instructions take the CTA group of the kernel's MMAs (every tcgen05
 // instruction of a kernel names the same group). With CG = 2 one warp of each CTA of the pair
@@ -390,6 +397,26 @@ __host__ __device__ constexpr uint32_t idesc_mxf8_e4m3(int M, int N) {
   return ((static_cast<uint32_t>(N) >> 3) << 17) | (1u << 23) | ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t idesc_sf_ids(uint32_t ks) { return (ks << 29) | (ks << 4); }
+
+// As mma_mxf8_ss for kind::mxf4: 4-bit E2M1 operands, two per byte, K = 64 a step; each 32-bit scale
+// word holds four K blocks of 32, and the scale ids (0 or 2) pick the two bytes of the step.
+__device__ __forceinline__ void mma_mxf4_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+          d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::mxf4 with block scaling: E2M1 A and B (format 1), both
+// K-major, fp32 accumulator (implied), E8M0 scales (bit 23), N, M, dense K = 64.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N) {
+  return (1u << 7) | (1u << 10) | ((static_cast<uint32_t>(N) >> 3) << 17) | (1u << 23) |
+         ((static_cast<uint32_t>(M) >> 4) << 24);
+}
 
 // Instruction descriptor for kind::f16: fp32 accumulator, bf16 A and B, operand majors, N, M.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn_major,

@@ -280,13 +280,6 @@ __device__ __forceinline__ void u24_unpack(const uint4 (&p)[3], float (&f)[16]) 
   }
 }
 
-// 32-byte store (sm_100+ global vector width); the address must be 32-byte aligned
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
 __device__ __forceinline__ void st_global_v4(void* p, uint32_t a, uint32_t b, uint32_t c,
                                              uint32_t d) {
   *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);

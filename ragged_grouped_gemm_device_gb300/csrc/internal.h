@@ -162,7 +162,7 @@ enum DbgSite : int {
   DBG_COMBINE_ROW = 7,  // combine: an inverse-map row against T*top_k
   DBG_RWG_ROW = 8,      // routing-weight gradient: an inverse-map row against the slots
   DBG_ROUTE_POS = 9,    // route scatter: a slot's placed row against T*top_k
-  DBG_MX_TILE = 10,     // MXFP8 quantization: a scale-atom tile against the atoms buffer
+  DBG_MX_TILE = 10,     // MX quantization: a scale-atom tile against the atoms buffer
   DBG_SITES = 11
 };
 
@@ -179,6 +179,7 @@ cudaError_t dbg_collect_grouped(DbgRecord* acc, bool reset);
 cudaError_t dbg_collect_permute(DbgRecord* acc, bool reset);
 cudaError_t dbg_collect_route(DbgRecord* acc, bool reset);
 cudaError_t dbg_collect_mx(DbgRecord* acc, bool reset);
+cudaError_t dbg_collect_mx4(DbgRecord* acc, bool reset);
 
 // ------------------------------------------------------------------ helpers
 int device_sm_count();              // SMs of the current device (cached per device)
@@ -226,6 +227,10 @@ moe_status_t launch_mx_permute_quant(const void* x, const int32_t* sorted_src, c
                                     int n, int k, int d, void* xp, void* q, void* sf, int32_t* status,
                                     cudaStream_t s);
 moe_status_t launch_mx_quant_cols(const void* w, int E, int R, int C, void* q, void* sf, cudaStream_t s);
+// Workspace sizes of the calls whose entry points live beside their kernels
+size_t layer_norm_bwd_workspace_bytes(int T, int d);                 // layer_norm.cu
+size_t gate_workspace_bytes(int T, int E);                           // gate.cu
+size_t mx4_workspace_bytes(int op, long long n, int E, int d, int h);  // mx4.cu: the MOE_OP_MX4_* sizes
 moe_status_t launch_unpad_rows(const void* src, const int32_t* offsets, int E, int C, int cap,
                                int cols, void* dst, cudaStream_t s);
 

@@ -376,6 +376,7 @@ moe_status_t moe_debug_report(int32_t* site_mask, int32_t* first_site, long long
   if (err == cudaSuccess) err = dbg_collect_permute(&acc, reset != 0);
   if (err == cudaSuccess) err = dbg_collect_route(&acc, reset != 0);
   if (err == cudaSuccess) err = dbg_collect_mx(&acc, reset != 0);
+  if (err == cudaSuccess) err = dbg_collect_mx4(&acc, reset != 0);
   if (err != cudaSuccess) return cuda_fail(err);
   if (g_dbg_call_error) acc.mask |= 1 << MOE_DEBUG_CALL_ERROR_BIT;
   if (reset) g_dbg_call_error = false;
@@ -394,7 +395,7 @@ const char* moe_debug_site_name(int site) {
       "grouped: epilogue row", "grouped: saved U row tile", "grouped: row slot",
       "grouped: destination row", "grouped: activation scale tile", "grouped: weight scale tile",
       "grouped: written scale tile", "combine: inverse-map row", "routing-weight grad: inverse-map row",
-      "route: placed row", "mxfp8 quantization: scale tile"};
+      "route: placed row", "mx quantization: scale tile"};
   return (site >= 0 && site < DBG_SITES) ? names[site] : "?";
 }
 
@@ -435,6 +436,11 @@ size_t moe_workspace_bytes(int op, int T, int top_k, int E, int d, int h, int ca
     case MOE_OP_MX_FWD:
     case MOE_OP_MX_BWD:
     case MOE_OP_MX_ROW_SCALES: return mx_workspace_bytes(op, n, E, d, h);
+    case MOE_OP_MX4_WEIGHTS:
+    case MOE_OP_MX4_FWD:
+    case MOE_OP_MX4_ROW_SCALES: return mx4_workspace_bytes(op, n, E, d, h);
+    case MOE_OP_LAYER_NORM_BWD: return layer_norm_bwd_workspace_bytes(T, d);
+    case MOE_OP_GATE: return gate_workspace_bytes(T, E);
   }
   return 0;
 }

@@ -1,0 +1,856 @@
+// MXFP4 experts: quantization of rows and weights to 4-bit floating point, and the grouped SwiGLU
+// forward with both operands of every product in MXFP4 (serving: weights and activations take
+// an eighth of the bytes of fp32 and a quarter of those of bf16).
+//
+// Format (OCP Microscaling MXFP4): blocks of 32 consecutive elements along the contraction
+// dimension share one power-of-two scale 2^s stored as E8M0 (s + 127); each element is E2M1, one
+// of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign. s = floor(log2(max |v|)) - 2 (2: the exponent of
+// E2M1's largest value), not below -127 (-127 for an all-zero block); elements are v / 2^s rounded
+// to nearest, ties to the even code, saturated at 6. E2M1 has no NaN or infinity: a block
+// that holds one gets the scale 0xFF (E8M0's NaN), so everything computed from it is NaN.
+//
+// Layouts. Codes of an operand [rows, K]: K / 2 bytes a row, element 2i in the low half of byte i.
+// Scales in the 512-byte atoms of the MXFP8 operands (mx_quant.cu), one per (128-row tile,
+// 128-element chunk of K), with the chunks of a row padded to an even number KC = 2 ceil(K / 256):
+// a pipeline stage of the product is 256 elements of K (128 bytes of codes, one swizzle row)
+// and takes two atoms a tile. The scales of blocks past K are 2^0 (their codes are TMA zero fill).
+//   activations: tiles are the problem list's 128-row tiles;
+//   W_ug [E, 2h, d]: the gate and the up half of an expert are cut into tiles separately, tile
+//     (2e + half) NTh + n / 128 with NTh = ceil(h / 128), so h needs no alignment beyond 32;
+//   W_down^T [E, d, h]: tile e NTd + n / 128 with NTd = ceil(d / 128) rounded up to even.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "problem_tiles.cuh"
+#include "trace.h"
+
+namespace moe {
+namespace {
+
+constexpr int MXB = 32;  // elements per scale block
+constexpr int MAX_E = 1024;
+constexpr int MAX_TOPK = 32;
+
+__host__ __device__ constexpr int mx4_kc(int K) { return 2 * ((K + 255) / 256); }
+
+// ------------------------------------------------------------------------------ quantization
+// E8M0 code of a block from the largest magnitude's bit pattern (as an unsigned number, which
+// orders magnitudes, with infinity and NaN above all others).
+__device__ __forceinline__ uint32_t mx4_scale_code(uint32_t abs_bits) {
+  const int eb = static_cast<int>(abs_bits >> 23);
+  if (eb == 255) return 255u;
+  return static_cast<uint32_t>(max(eb - 2, 0));  // floor(log2) = eb - 127; subnormals: 0
+}
+
+// 1 / 2^s of an E8M0 code in [0, 252]: a normal power of two (1 for the NaN code, whose element
+// codes carry nothing)
+__device__ __forceinline__ float mx4_inv_scale(uint32_t code) {
+  return code == 255u ? 1.0f : __uint_as_float((254u - code) << 23);
+}
+
+// 8 values (already divided by the scale) -> 8 E2M1 codes, the first in the low four bits
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n\t"
+      "mov.b32 %0, {t0, t1, t2, t3};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+__device__ __forceinline__ void unpack8(uint4 q, float (&f)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    f[2 * t] = bf16_lo(w[t]);
+    f[2 * t + 1] = bf16_hi(w[t]);
+  }
+}
+
+// A warp quantizes 256 consecutive elements, 8 a lane (four lanes hold a block): returns this
+// lane's 8 codes and, in lanes 0 and 16, the scale codes of the four blocks of its 128-element
+// chunk. Lanes past the row's end (act false) count as blocks of scale 2^0.
+__device__ __forceinline__ uint32_t quant256(uint4 q, bool act, uint32_t& chunk_scales) {
+  float f[8];
+  unpack8(q, f);
+  uint32_t m = 0u;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) m = max(m, abs_bits(f[t]));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t code = mx4_scale_code(m);
+  const float inv = mx4_inv_scale(code);
+#pragma unroll
+  for (int t = 0; t < 8; ++t) f[t] *= inv;
+  uint32_t w = (act ? code : 127u) << (8 * ((threadIdx.x >> 2) & 3));
+  w |= __shfl_xor_sync(0xffffffffu, w, 4);
+  w |= __shfl_xor_sync(0xffffffffu, w, 8);
+  chunk_scales = w;
+  return e2m1x8(f);
+}
+
+// Address of the four scale bytes of row r of tile G in chunk kc.
+__device__ __forceinline__ uint32_t* chunk_word(uint8_t* sf, long long G, int KC, int kc, int r) {
+  return reinterpret_cast<uint32_t*>(sf + static_cast<size_t>(G * KC + kc) * 512 + (r & 31) * 16 + (r >> 5) * 4);
+}
+
+// Rows along K, one warp a row. With offsets: the rows p < M of a problem list; else `rows` rows
+// of weights in groups of `sub` rows, ntpad tiles a group.
+__global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __restrict__ src, long long rows, int K,
+                                                             const int32_t* __restrict__ offsets, int E, int sub,
+                                                             int ntpad, uint32_t* __restrict__ q,
+                                                             uint8_t* __restrict__ sf, long long sf_tiles,
+                                                             int32_t* status) {
+  __shared__ int s_end[MAX_E];
+  __shared__ int s_pre[MAX_E];
+  const bool list = offsets != nullptr;
+  if (list && !load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
+  const long long M = list ? s_end[E - 1] : rows;
+  const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
+  for (long long p = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); p < M;
+       p += static_cast<long long>(gridDim.x) * 8) {
+    long long G;
+    int r;
+    if (list) {
+      row_tile(s_end, s_pre, E, p, G, r);
+    } else {
+      const long long g = p / sub, n = p - g * sub;
+      G = g * ntpad + n / 128;
+      r = static_cast<int>(n % 128);
+    }
+    const bool tile_ok = MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles);
+    for (int v0 = 0; v0 < vec; v0 += 32) {  // every lane runs every pass: the shuffles need the warp
+      const int v = v0 + lane;
+      const bool act = v < vec;
+      uint32_t word;
+      const uint32_t codes = quant256(act ? __ldg(src + p * vec + v) : make_uint4(0u, 0u, 0u, 0u), act, word);
+      if (act) q[p * vec + v] = codes;
+      if ((lane & 15) == 0 && tile_ok) *chunk_word(sf, G, KC, v >> 4, r) = word;
+    }
+  }
+}
+
+// The permute's gather and the quantization along d in one pass, token by token: a token's row is
+// read and quantized once and its codes and scales are written to the rows of its top_k slots.
+__global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* __restrict__ x,
+                                                          const int32_t* __restrict__ inv_map,
+                                                          const int32_t* __restrict__ offsets, int E, int T, int k,
+                                                          int d, uint32_t* __restrict__ q, uint8_t* __restrict__ sf,
+                                                          long long sf_tiles, int32_t* status) {
+  __shared__ int s_end[MAX_E];
+  __shared__ int s_pre[MAX_E];
+  const long long n = static_cast<long long>(T) * k;
+  if (!load_problem_tiles(offsets, E, n, s_end, s_pre, status)) return;
+  const int M = s_end[E - 1];
+  const int lane = threadIdx.x & 31, vec = d / 8, KC = mx4_kc(d);
+  for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T;
+       t += static_cast<long long>(gridDim.x) * 8) {
+    // lane j < k holds slot j's row, its tile and the row within the tile
+    int my_p = -1, my_r = 0, my_g = 0;
+    if (lane < k) {
+      const int p = __ldg(inv_map + t * k + lane);
+      if (p >= 0 && p < M) {
+        long long G;
+        row_tile(s_end, s_pre, E, p, G, my_r);
+        if (MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles)) {
+          my_p = p;
+          my_g = static_cast<int>(G);
+        }
+      }
+    }
+    for (int v0 = 0; v0 < vec; v0 += 32) {
+      const int v = v0 + lane;
+      const bool act = v < vec;
+      uint32_t word;
+      const uint32_t codes = quant256(act ? __ldg(x + t * vec + v) : make_uint4(0u, 0u, 0u, 0u), act, word);
+      for (int j = 0; j < k; ++j) {
+        const int p = __shfl_sync(0xffffffffu, my_p, j);
+        const int g = __shfl_sync(0xffffffffu, my_g, j), r = __shfl_sync(0xffffffffu, my_r, j);
+        if (p < 0) continue;  // warp-uniform
+        if (act) q[static_cast<size_t>(p) * vec + v] = codes;
+        if ((lane & 15) == 0) *chunk_word(sf, g, KC, v >> 4, r) = word;
+      }
+    }
+  }
+}
+
+// The bf16 values that rows p < M of codes and scales stand for (exact: an E2M1 value times a
+// power of two has two significant bits); a block with a NaN scale reads as NaN.
+__global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* __restrict__ q,
+                                                               const uint8_t* __restrict__ sf, long long rows, int K,
+                                                               const int32_t* __restrict__ offsets, int E,
+                                                               uint4* __restrict__ x, long long sf_tiles,
+                                                               int32_t* status) {
+  __shared__ int s_end[MAX_E];
+  __shared__ int s_pre[MAX_E];
+  if (!load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
+  const int M = s_end[E - 1];
+  const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
+  for (long long p = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); p < M;
+       p += static_cast<long long>(gridDim.x) * 8) {
+    long long G;
+    int r;
+    row_tile(s_end, s_pre, E, p, G, r);
+    if (!MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles)) continue;
+    for (int v = lane; v < vec; v += 32) {
+      const uint32_t codes = __ldg(q + p * vec + v);
+      const uint32_t sc = __ldg(sf + atom_byte(G, KC, v >> 2, r));
+      // 2^(sc - 127): 2^-127 is the subnormal 0x00400000
+      const float scale = sc == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(sc == 0u ? 0x00400000u : sc << 23);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t c = (codes >> (8 * i + 4 * j)) & 15u;
+          const uint32_t mag = c & 7u;
+          // exponent field e and mantissa bit m: e = 0 is m / 2, else (2 + m) 2^(e - 2)
+          const float v8 = mag < 2u ? 0.5f * static_cast<float>(mag)
+                                    : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
+          f[j] = ((c & 8u) ? -v8 : v8) * scale;
+        }
+        w[i] = pack_bf16x2(f[0], f[1]);
+      }
+      x[p * vec + v] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
+// A weight [E, R, C] quantized along R: codes [E, C, R / 2], tiles by expert and 128 columns of
+// C. One thread per (expert, 32-block of R, column), columns fastest: the strided reads of a
+// thread are coalesced across the warp. The blocks past R of the padded chunks get scale 2^0.
+__global__ void __launch_bounds__(256) mx4_quant_cols_kernel(const bf16* __restrict__ w, int E, int R, int C, int ntpad,
+                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ sf) {
+  const int nb = R / MXB, KC = mx4_kc(R), nbp = 4 * KC;
+  const long long items = static_cast<long long>(E) * nbp * C;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < items;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int c = static_cast<int>(i % C);
+    const long long rest = i / C;
+    const int b = static_cast<int>(rest % nbp);
+    const int e = static_cast<int>(rest / nbp);
+    uint32_t code = 127u;
+    if (b < nb) {
+      const bf16* col = w + (static_cast<long long>(e) * R + static_cast<long long>(b) * MXB) * C + c;
+      float v[MXB];
+      uint32_t m = 0u;
+#pragma unroll
+      for (int j = 0; j < MXB; ++j) {
+        v[j] = __bfloat162float(col[static_cast<long long>(j) * C]);
+        m = max(m, abs_bits(v[j]));
+      }
+      code = mx4_scale_code(m);
+      const float inv = mx4_inv_scale(code);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float f[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) f[t] = v[8 * j + t] * inv;
+        o[j] = e2m1x8(f);
+      }
+      *reinterpret_cast<uint4*>(q + ((static_cast<long long>(e) * C + c) * R + b * MXB) / 2) =
+          make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    sf[atom_byte(static_cast<long long>(e) * ntpad + c / 128, KC, b, c % 128)] = static_cast<uint8_t>(code);
+  }
+}
+
+// ------------------------------------------------------------------------------ the product
+// Persistent grouped GEMM on block-scaled 4-bit operands: the problem list, tile order, roles and
+// bounded waits of the grouped GEMM (grouped_gemm.cu), one CTA per SM on 128 x 256 tiles.
+//   warp 0      TMA producer of A (128 rows x 256 elements of K, its scale atoms)
+//   warp 1      tensor-memory allocator and MMA issuer: per stage, the scale atoms into tensor
+//               memory and four block-scaled MMAs of K = 64
+//   warps 2..9  epilogue, two per lane quadrant
+//   warp 10     TMA producer of B
+// MX4_UP:   B = 128 gate and 128 up rows of W_ug; the epilogue computes A = silu(gate) up in fp32
+//           and quantizes it along h from fp32 (no bf16 rounding in between).
+// MX4_DOWN: B = 256 rows of W_down^T; bf16 store, one rounding.
+enum { MX4_UP = 0, MX4_DOWN = 1 };
+
+constexpr int BM = 128;
+constexpr int BN = 256;
+constexpr int STAGES = 4;
+constexpr int STAGE_K = 256;                 // elements of K per stage: 128 bytes of codes
+constexpr int UK = 64;                       // K of one MMA
+constexpr int A_BYTES = BM * STAGE_K / 2;    // 16 KB
+constexpr int B_BYTES = BN * STAGE_K / 2;    // 32 KB
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int SF_A_BYTES = 2 * 512;          // two chunks of one 128-row tile
+constexpr int SF_B_BYTES = 2 * SF_A_BYTES;   // ... of two tiles
+constexpr int SF_STAGE_BYTES = SF_A_BYTES + SF_B_BYTES;
+constexpr int EPI_WARPS = 8;
+constexpr int PRODUCER_B_WARP = 2 + EPI_WARPS;
+constexpr int THREADS = 32 * (PRODUCER_B_WARP + 1);
+constexpr int TMEM_COLS = 512;
+constexpr int SF_TMEM_COL = 256;             // 32 columns of scales per stage after the accumulator
+constexpr int RASTER_M = 16;                 // row tiles per raster group
+constexpr int CTL_BYTES = 256;
+
+struct Ctl {
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
+  uint64_t tfull;
+  uint64_t tempty;
+  uint64_t done;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(Ctl) <= CTL_BYTES, "control block too large");
+
+constexpr size_t smem_bytes_for(int E) {
+  return 1024 + static_cast<size_t>(STAGES) * (STAGE_BYTES + SF_STAGE_BYTES) + CTL_BYTES +
+         2 * sizeof(int) * static_cast<size_t>(E + 2);
+}
+
+struct Maps {
+  CUtensorMap a, b;
+};
+
+struct Args {
+  const int32_t* offsets;
+  int E, cap;
+  int N;               // output columns (MX4_UP: h)
+  int K;
+  int h;               // MX4_UP: half width of W_ug
+  const uint8_t* sfa;  // scale atoms of A by the problem list's tiles
+  const uint8_t* sfb;  // of B, tiles_b tiles per expert (MX4_UP: per half)
+  int kc;              // chunks per row, even
+  int tiles_b;
+  bf16* y;             // MX4_DOWN
+  int vec32;           // its rows are 32-byte aligned
+  uint8_t* pq;         // MX4_UP: codes [cap, h / 2] and scale atoms of A = silu(gate) up
+  uint8_t* psf;
+  int pkc;
+  long long dbg_a_tiles, dbg_b_tiles;
+  int32_t* status;
+  long long timeout_ns, drain_ns;
+};
+
+struct Tile {
+  int e, g, row0, rows, n0;
+};
+
+struct Sched {
+  const int* offs;
+  const int* pre;
+  int E, nt, total;
+};
+
+// Tile t of the problem list; inside an expert, groups of up to RASTER_M row tiles are walked
+// column tile by column tile (row tile fastest).
+__device__ __forceinline__ Tile decode_tile(const Sched& s, int t, int cols_per_tile) {
+  Tile ti;
+  const int gq = t / s.nt;
+  int lo = 0, hi = s.E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.pre[mid] <= gq) lo = mid; else hi = mid;
+  }
+  ti.e = lo;
+  const int mt_e = s.pre[lo + 1] - s.pre[lo];
+  const int l = t - s.pre[lo] * s.nt;
+  const int grp = l / (RASTER_M * s.nt);
+  const int gm = min(RASTER_M, mt_e - grp * RASTER_M);
+  const int within = l - grp * RASTER_M * s.nt;
+  const int m_local = grp * RASTER_M + within % gm;
+  ti.g = s.pre[lo] + m_local;
+  ti.row0 = s.offs[lo] + m_local * BM;
+  ti.rows = min(BM, s.offs[lo + 1] - ti.row0);
+  ti.n0 = (within / gm) * cols_per_tile;
+  return ti;
+}
+
+__device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+template <int MODE>
+__global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
+  constexpr int COLS = MODE == MX4_UP ? 128 : BN;  // output columns per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sf_ring = smem + STAGES * STAGE_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sf_ring + STAGES * SF_STAGE_BYTES);
+  int* offs = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + CTL_BYTES);
+  const int E = args.E;
+  int* pre = offs + (E + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // ---- problem list
+  for (int i = tid; i <= E; i += THREADS) offs[i] = i == 0 ? 0 : __ldg(args.offsets + i - 1);
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < E; i += THREADS) bad |= (offs[i + 1] < offs[i]) || (offs[i] < 0);
+  if (tid == 0) bad |= offs[E] > args.cap;
+  if (__syncthreads_or(bad)) {
+    if (tid == 0 && blockIdx.x == 0) record_status(args.status, MOE_DEV_BAD_OFFSETS);
+    return;  // uniform across the CTA, before any barrier or tensor memory exists
+  }
+  if (warp == 0) {
+    int carry = 0;
+    if (lane == 0) pre[0] = 0;
+    for (int base = 0; base < E; base += 32) {
+      const int e = base + lane;
+      int v = (e < E) ? (offs[e + 1] - offs[e] + BM - 1) / BM : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int nb = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += nb;
+      }
+      if (e < E) pre[e + 1] = carry + v;
+      carry += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+
+  // ---- barriers and tensor memory
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 2);  // both producers
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl->tfull), 1);
+    mbar_init(smem_u32(&ctl->tempty), 32 * EPI_WARPS);
+    mbar_init(smem_u32(&ctl->done), 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  Sched sc;
+  sc.offs = offs;
+  sc.pre = pre;
+  sc.E = E;
+  sc.nt = (args.N + COLS - 1) / COLS;
+  sc.total = pre[E] * sc.nt;
+  const int kblocks = (args.K + STAGE_K - 1) / STAGE_K;
+  const uint32_t tmem_base = ctl->tmem_base;
+  volatile int* abort_flag = &ctl->abort_flag;
+  const long long tmo = args.timeout_ns;
+  const uint32_t stage0 = smem_u32(smem);
+  const uint32_t sf0 = smem_u32(sf_ring);
+
+  if (warp == 0 || warp == PRODUCER_B_WARP) {
+    // =========================================================== TMA producers
+    if (lane == 0) {
+      const bool is_a = warp == 0;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x) {
+        const Tile ti = decode_tile(sc, t, COLS);
+        // first scale atoms of the tile(s): consecutive chunks of a tile are consecutive atoms
+        long long s0, s1 = 0;
+        if (is_a) {
+          s0 = ti.g;
+          if (!MOE_DBG_IN(DBG_GG_SFA, s0, args.dbg_a_tiles)) s0 = 0;
+        } else {
+          if constexpr (MODE == MX4_UP) {
+            s0 = static_cast<long long>(2 * ti.e) * args.tiles_b + ti.n0 / 128;
+            s1 = s0 + args.tiles_b;
+          } else {
+            s0 = static_cast<long long>(ti.e) * args.tiles_b + ti.n0 / 128;
+            s1 = s0 + 1;
+          }
+          if (!MOE_DBG_IN(DBG_GG_SFB, s0, args.dbg_b_tiles)) s0 = 0;
+          if (!MOE_DBG_IN(DBG_GG_SFB, s1, args.dbg_b_tiles)) s1 = 0;
+        }
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          const int s = it % STAGES;
+          if (!mbar_wait(smem_u32(&ctl->empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, args.status, tmo)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&ctl->full[s]);
+          const uint32_t sa = stage0 + s * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
+          const int k0 = kb * (STAGE_K / 2);  // in bytes of codes
+          if (is_a) {
+            mbar_arrive_expect_tx(fb, A_BYTES + SF_A_BYTES);
+            tma_load_2d(sa, &maps.a, k0, ti.row0, fb);
+            bulk_load(sfs, args.sfa + (s0 * args.kc + 2 * kb) * 512, SF_A_BYTES, fb);
+          } else {
+            mbar_arrive_expect_tx(fb, B_BYTES + SF_B_BYTES);
+            if constexpr (MODE == MX4_UP) {
+              tma_load_3d(sb, &maps.b, k0, ti.n0, ti.e, fb);                         // gate rows
+              tma_load_3d(sb + B_BYTES / 2, &maps.b, k0, args.h + ti.n0, ti.e, fb);  // up rows
+            } else {
+              tma_load_3d(sb, &maps.b, k0, ti.n0, ti.e, fb);
+            }
+            bulk_load(sfs + SF_A_BYTES, args.sfb + (s0 * args.kc + 2 * kb) * 512, SF_A_BYTES, fb);
+            bulk_load(sfs + 2 * SF_A_BYTES, args.sfb + (s1 * args.kc + 2 * kb) * 512, SF_A_BYTES, fb);
+          }
+        }
+      }
+      // the copies this thread issued must land before the CTA can exit (see grouped_gemm.cu)
+      const uint32_t first = it > STAGES ? it - STAGES : 0u;
+      for (uint32_t j = first; j < it; ++j)
+        if (!mbar_wait(smem_u32(&ctl->full[j % STAGES]), (j / STAGES) & 1u, abort_flag, args.status, args.drain_ns, false))
+          break;
+    }
+  } else if (warp == 1) {
+    // =========================================================== MMA issuer
+    constexpr uint32_t idesc = idesc_mxf4(BM, BN);
+    uint32_t it = 0, use = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x, ++use) {
+      ok = warp_all(mbar_wait(smem_u32(&ctl->tempty), (use & 1u) ^ 1u, abort_flag, args.status, tmo));
+      if (!ok) break;
+      tc_fence_after();
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
+        const int s = it % STAGES;
+        ok = warp_all(mbar_wait(smem_u32(&ctl->full[s]), (it / STAGES) & 1u, abort_flag, args.status, tmo));
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          // scale atoms into this stage's 32 columns: per 128-element chunk 4 columns of A, then
+          // 8 of B; a copy and the MMAs after it from one thread execute in issue order
+          const uint32_t sa = stage0 + s * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
+          const uint32_t sft = tmem_base + SF_TMEM_COL + s * 32;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            tmem_cp_32x128b_x4(sft + 12 * c, smem_desc_rows16(sfs + 512 * c));
+            tmem_cp_32x128b_x4(sft + 12 * c + 4, smem_desc_rows16(sfs + SF_A_BYTES + 512 * c));
+            tmem_cp_32x128b_x4(sft + 12 * c + 8, smem_desc_rows16(sfs + 2 * SF_A_BYTES + 512 * c));
+          }
+#pragma unroll
+          for (int ks = 0; ks < STAGE_K / UK; ++ks) {
+            const uint64_t ad = smem_desc_sw128(sa + ks * (UK / 2), 16, 1024);
+            const uint64_t bd = smem_desc_sw128(sb + ks * (UK / 2), 16, 1024);
+            const uint32_t sfc = sft + 12 * (ks >> 1);
+            mma_mxf4_ss(tmem_base, ad, bd, idesc | idesc_sf_ids(2u * (ks & 1)), sfc, sfc + 4, (kb | ks) != 0 ? 1u : 0u);
+          }
+          mma_commit(smem_u32(&ctl->empty[s]));
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (lane == 0) mma_commit(smem_u32(&ctl->tfull));
+      __syncwarp();
+    }
+    // every MMA this thread issued must finish before tensor memory is released
+    if (lane == 0) mma_commit(smem_u32(&ctl->done));
+    __syncwarp();
+    mbar_wait(smem_u32(&ctl->done), 0u, abort_flag, args.status, args.drain_ns, false);
+  } else {
+    // =========================================================== epilogue (warps 2..9)
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int r_in = q * 32 + lane;
+    const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    uint32_t use = 0;
+    for (int t = blockIdx.x; t < sc.total; t += gridDim.x, ++use) {
+      const Tile ti = decode_tile(sc, t, COLS);
+      if (!warp_all(mbar_wait(smem_u32(&ctl->tfull), use & 1u, abort_flag, args.status, tmo))) break;
+      tc_fence_after();
+      const long long row = static_cast<long long>(ti.row0) + r_in;
+      bool rv = r_in < ti.rows;
+      if (rv && !MOE_DBG_IN(DBG_GG_ROW, row, args.cap)) rv = false;
+      if constexpr (MODE == MX4_UP) {
+        // this warp's 64 gate and 64 up columns into registers, so that the accumulator goes
+        // back to the MMA issuer before they are worked on
+        uint32_t g[4][16], u[4][16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          tmem_ld16(tb + half * 64 + i * 16, g[i]);
+          tmem_ld16(tb + 128 + half * 64 + i * 16, u[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld_wait2(g[i], u[i]);
+        tc_fence_before();
+        mbar_arrive(smem_u32(&ctl->tempty));
+        if (!rv || !MOE_DBG_IN(DBG_GG_MXSF, ti.g, args.dbg_a_tiles)) continue;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const int col = ti.n0 + half * 64 + b * 32;  // h % 32 == 0: a block is all in or all out
+          uint8_t* sfp = args.psf + atom_byte(ti.g, args.pkc, col >> 5, r_in);
+          if (col >= args.h) {
+            *sfp = 127;
+            continue;
+          }
+          float p[32];
+          uint32_t m = 0u;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            p[j] = silu_f(__uint_as_float(g[2 * b + (j >> 4)][j & 15])) * __uint_as_float(u[2 * b + (j >> 4)][j & 15]);
+            m = max(m, abs_bits(p[j]));
+          }
+          const uint32_t code = mx4_scale_code(m);
+          const float inv = mx4_inv_scale(code);
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = p[8 * j + i] * inv;
+            o[j] = e2m1x8(f);
+          }
+          *reinterpret_cast<uint4*>(args.pq + row * (args.h / 2) + col / 2) = make_uint4(o[0], o[1], o[2], o[3]);
+          *sfp = static_cast<uint8_t>(code);
+        }
+        // an odd number of chunks: the padding chunk of the last stage
+        if (ti.n0 + COLS >= args.h && (ti.n0 / 128 + 1) < args.pkc) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            args.psf[atom_byte(ti.g, args.pkc, (ti.n0 + 128) / 32 + half * 2 + b, r_in)] = 127;
+        }
+      } else {
+        uint32_t p[64];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          uint32_t v0[16], v1[16];
+          tmem_ld16(tb + half * 128 + i * 16, v0);
+          tmem_ld16(tb + half * 128 + (i + 1) * 16, v1);
+          tmem_ld_wait2(v0, v1);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            p[8 * i + j] = pack_bf16x2(__uint_as_float(v0[2 * j]), __uint_as_float(v0[2 * j + 1]));
+            p[8 * i + 8 + j] = pack_bf16x2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(smem_u32(&ctl->tempty));
+        if (!rv) continue;
+        bf16* yrow = args.y + row * args.N;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int col = ti.n0 + half * 128 + i * 32;  // N % 32 == 0
+          if (col >= args.N) break;
+          if (args.vec32) {
+            st_global_v8(yrow + col, p + 16 * i);
+            st_global_v8(yrow + col + 16, p + 16 * i + 8);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4*>(yrow + col + 8 * j) =
+                  make_uint4(p[16 * i + 4 * j], p[16 * i + 4 * j + 1], p[16 * i + 4 * j + 2], p[16 * i + 4 * j + 3]);
+          }
+        }
+      }
+    }
+  }
+
+  // ---- teardown: every role has finished (or given up); release tensor memory
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+bool width_ok(int v) { return v > 0 && v % MXB == 0 && v <= (1 << 20); }
+bool shape_ok(int E, int d, int h) { return E >= 1 && E <= MAX_E && width_ok(d) && width_ok(h); }
+
+// 128-row tiles of any problem list with at most `rows` rows
+long long list_tiles(long long rows, int E) { return (rows + 127LL * E) / 128; }
+int tiles128(int n) { return (n + 127) / 128; }
+int down_tiles(int d) { return 2 * ((tiles128(d) + 1) / 2); }
+
+size_t codes_bytes(long long rows, int K) { return round256(static_cast<size_t>(rows) * (K / 2)); }
+size_t atoms_bytes(long long tiles, int K) { return round256(static_cast<size_t>(tiles) * mx4_kc(K) * 512); }
+
+struct Weights {
+  uint8_t *ug_q, *ug_sf, *dn_q, *dn_sf;
+};
+size_t ug_sf_bytes(int E, int d, int h) { return atoms_bytes(2LL * E * tiles128(h), d); }
+size_t dn_sf_bytes(int E, int d, int h) { return atoms_bytes(static_cast<long long>(E) * down_tiles(d), h); }
+size_t weights_bytes(int E, int d, int h) {
+  return codes_bytes(2LL * E * h, d) + ug_sf_bytes(E, d, h) + codes_bytes(static_cast<long long>(E) * d, h) +
+         dn_sf_bytes(E, d, h);
+}
+Weights carve_weights(const void* base, int E, int d, int h) {
+  Weights w;
+  w.ug_q = const_cast<uint8_t*>(static_cast<const uint8_t*>(base));
+  w.ug_sf = w.ug_q + codes_bytes(2LL * E * h, d);
+  w.dn_q = w.ug_sf + ug_sf_bytes(E, d, h);
+  w.dn_sf = w.dn_q + codes_bytes(static_cast<long long>(E) * d, h);
+  return w;
+}
+size_t fwd_ws_bytes(long long cap, int E, int h) { return codes_bytes(cap, h) + atoms_bytes(list_tiles(cap, E), h); }
+
+moe_status_t launched() {
+  const cudaError_t err = cudaGetLastError();
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
+}
+
+int row_blocks(long long rows) {
+  return static_cast<int>(std::max(1LL, std::min((rows + 7) / 8, 8LL * device_sm_count())));
+}
+
+template <int MODE>
+moe_status_t launch_gemm(const Maps& maps, Args a, cudaStream_t s) {
+  const cudaError_t aerr = ensure_max_dynamic_smem(reinterpret_cast<const void*>(mx4_gemm_kernel<MODE>),
+                                                   static_cast<int>(smem_bytes_for(MAX_E)));
+  if (aerr != cudaSuccess) return cuda_fail(aerr);
+  a.timeout_ns = wait_timeout_ns();
+  a.drain_ns = std::max(a.timeout_ns, 2000000000LL);
+  const int cols = MODE == MX4_UP ? 128 : BN;
+  const long long tiles = list_tiles(a.cap, a.E) * ((a.N + cols - 1) / cols);
+  const int grid = static_cast<int>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
+  mx4_gemm_kernel<MODE><<<grid, THREADS, smem_bytes_for(a.E), s>>>(maps, a);
+  return launched();
+}
+
+}  // namespace
+
+MOE_DBG_DEFINE_COLLECTOR(dbg_collect_mx4)
+
+size_t mx4_workspace_bytes(int op, long long n, int E, int d, int h) {
+  if (!shape_ok(E, d, h)) return 0;
+  switch (op) {
+    case MOE_OP_MX4_WEIGHTS: return weights_bytes(E, d, h);
+    case MOE_OP_MX4_FWD: return fwd_ws_bytes(n, E, h);
+    case MOE_OP_MX4_ROW_SCALES: return atoms_bytes(list_tiles(n, E), d);
+  }
+  return 0;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_mx4_prepare_weights(const moe_bf16* w_ug, const moe_bf16* w_down, int E, int d, int h, void* mxw,
+                                     size_t mxw_bytes, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (E < 1 || d <= 0 || h <= 0) return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(E, d, h)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!w_ug || !w_down || !mxw || !aligned(w_ug, 16) || !aligned(w_down, 16) || !aligned(mxw, 256))
+    return MOE_ERR_INVALID_ARG;
+  if (mxw_bytes < weights_bytes(E, d, h)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  moe_status_t st = check_device();
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Weights w = carve_weights(mxw, E, d, h);
+  const long long ug_rows = 2LL * E * h;
+  mx4_quant_rows_kernel<<<row_blocks(ug_rows), 256, 0, s>>>(reinterpret_cast<const uint4*>(w_ug), ug_rows, d, nullptr, E,
+                                                            h, tiles128(h), reinterpret_cast<uint32_t*>(w.ug_q), w.ug_sf,
+                                                            2LL * E * tiles128(h), nullptr);
+  if ((st = launched()) != MOE_OK) return st;
+  const long long items = static_cast<long long>(E) * d * 4 * mx4_kc(h);
+  const int blocks = static_cast<int>(std::max(1LL, std::min((items + 255) / 256, 16LL * device_sm_count())));
+  mx4_quant_cols_kernel<<<blocks, 256, 0, s>>>(reinterpret_cast<const bf16*>(w_down), E, h, d, down_tiles(d), w.dn_q,
+                                               w.dn_sf);
+  return launched();
+}
+
+moe_status_t moe_mx4_quantize_rows(const moe_bf16* x, const int32_t* offsets, int E, int cap, int K, uint8_t* q,
+                                   uint8_t* sf, int32_t* dev_status, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (cap < 0 || K <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (E > MAX_E || !width_ok(K)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets || (cap > 0 && (!x || !q || !sf))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_device();
+  if (st != MOE_OK || cap == 0) return st;
+  mx4_quant_rows_kernel<<<row_blocks(cap), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<const uint4*>(x), cap, K, offsets, E, 0, 0, reinterpret_cast<uint32_t*>(q), sf,
+      list_tiles(cap, E), dev_status);
+  return launched();
+}
+
+moe_status_t moe_mx4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const int32_t* offsets, int E, int cap, int K,
+                                     moe_bf16* x, int32_t* dev_status, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (cap < 0 || K <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (E > MAX_E || !width_ok(K)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets || (cap > 0 && (!x || !q || !sf))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_device();
+  if (st != MOE_OK || cap == 0) return st;
+  mx4_dequant_rows_kernel<<<row_blocks(cap), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<const uint32_t*>(q), sf, cap, K, offsets, E, reinterpret_cast<uint4*>(x), list_tiles(cap, E),
+      dev_status);
+  return launched();
+}
+
+moe_status_t moe_permute_mxfp4(const moe_bf16* x, const int32_t* inv_map, const int32_t* offsets, int T, int top_k,
+                               int E, int d, uint8_t* q, uint8_t* sf, int32_t* dev_status, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (T < 0 || top_k < 1 || d <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (top_k > MAX_TOPK || E > MAX_E || !width_ok(d)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const long long n = static_cast<long long>(T) * top_k;
+  if (n >= (1LL << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets || (n > 0 && (!x || !inv_map || !q || !sf))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_device();
+  if (st != MOE_OK || n == 0) return st;
+  mx4_permute_kernel<<<row_blocks(T), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+      reinterpret_cast<const uint4*>(x), inv_map, offsets, E, T, top_k, d, reinterpret_cast<uint32_t*>(q), sf,
+      list_tiles(n, E), dev_status);
+  return launched();
+}
+
+moe_status_t moe_grouped_swiglu_fwd_mxfp4(const uint8_t* xq, const uint8_t* xsf, const int32_t* offsets, int E, int cap,
+                                          int d, int h, const void* mxw, moe_bf16* y, void* ws, size_t ws_bytes,
+                                          int32_t* dev_status, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (cap < 0 || d <= 0 || h <= 0 || E < 1) return MOE_ERR_INVALID_ARG;
+  if (!shape_ok(E, d, h)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (!offsets || !mxw || !aligned(mxw, 256) || (cap > 0 && (!xq || !xsf || !y || !ws))) return MOE_ERR_INVALID_ARG;
+  if (!aligned(xq, 16) || !aligned(xsf, 16) || !aligned(y, 16) || !aligned(ws, 256)) return MOE_ERR_INVALID_ARG;
+  // tile indices are int
+  if (list_tiles(cap, E) * std::max(tiles128(h), (d + BN - 1) / BN) >= (1LL << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < fwd_ws_bytes(cap, E, h)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  moe_status_t st = check_device();
+  if (st != MOE_OK || cap == 0) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const Weights w = carve_weights(mxw, E, d, h);
+  uint8_t* pq = static_cast<uint8_t*>(ws);
+  uint8_t* psf = pq + codes_bytes(cap, h);
+  Maps up, down;
+  if (!make_map_u8_rows2d(&up.a, xq, cap, d / 2, BM) || !make_map_u8_weight3d(&up.b, w.ug_q, E, 2LL * h, d / 2, 128) ||
+      !make_map_u8_rows2d(&down.a, pq, cap, h / 2, BM) || !make_map_u8_weight3d(&down.b, w.dn_q, E, d, h / 2, BN))
+    return cuda_fail(cudaErrorInvalidValue);
+  Args a{};
+  a.offsets = offsets;
+  a.E = E;
+  a.cap = cap;
+  a.N = h;
+  a.K = d;
+  a.h = h;
+  a.sfa = xsf;
+  a.sfb = w.ug_sf;
+  a.kc = mx4_kc(d);
+  a.tiles_b = tiles128(h);
+  a.pq = pq;
+  a.psf = psf;
+  a.pkc = mx4_kc(h);
+  a.dbg_a_tiles = list_tiles(cap, E);
+  a.dbg_b_tiles = 2LL * E * tiles128(h);
+  a.status = dev_status;
+  if ((st = launch_gemm<MX4_UP>(up, a, s)) != MOE_OK) return st;
+  a.N = d;
+  a.K = h;
+  a.sfa = psf;
+  a.sfb = w.dn_sf;
+  a.kc = mx4_kc(h);
+  a.tiles_b = down_tiles(d);
+  a.dbg_b_tiles = static_cast<long long>(E) * down_tiles(d);
+  a.y = reinterpret_cast<bf16*>(y);
+  a.vec32 = aligned(y, 32) ? 1 : 0;
+  return launch_gemm<MX4_DOWN>(down, a, s);
+}
+
+}  // extern "C"

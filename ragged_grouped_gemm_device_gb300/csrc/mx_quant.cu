@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "problem_tiles.cuh"
 
 namespace moe {
 namespace {
@@ -53,68 +54,6 @@ __device__ __forceinline__ uint8_t mx_block(const float (&v)[MXB], uint32_t (&co
 // After the last block of a row: scales of the chunk's 32-blocks past K are 2^0.
 __device__ __forceinline__ void fill_chunk_tail(uint8_t* sf, long long G, int KC, int nb, int r) {
   for (int kb = nb; kb < ((nb + 3) & ~3); ++kb) sf[atom_byte(G, KC, kb, r)] = 127;
-}
-
-// The problem list as the grouped GEMM derives it from the offsets: s_end[e] = inclusive end of
-// expert e's rows, s_pre[e] = 128-row tiles of the experts before e (block-wide scan, 256
-// threads). Offsets that decrease or end past `rows` would place rows outside the scale atoms:
-// they are flagged (MOE_DEV_BAD_OFFSETS) and the function returns false in every thread.
-__device__ bool load_problem_tiles(const int32_t* __restrict__ offsets, int E, long long rows, int* s_end,
-                                   int* s_pre, int32_t* status) {
-  __shared__ int s_carry;
-  __shared__ int wsum[8];
-  if (threadIdx.x == 0) s_carry = 0;
-  __syncthreads();
-  for (int base = 0; base < E; base += blockDim.x) {
-    const int e = base + threadIdx.x;
-    int tiles = 0;
-    if (e < E) {
-      const int end = __ldg(offsets + e);
-      const int start = e > 0 ? __ldg(offsets + e - 1) : 0;
-      s_end[e] = end;
-      tiles = (end - start + 127) / 128;
-    }
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int nb = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += nb;
-    }
-    if (lane == 31) wsum[warp] = incl;
-    __syncthreads();
-    int before = s_carry;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (e < E) s_pre[e] = before + incl - tiles;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int tot = 0;
-      for (int w = 0; w < 8; ++w) tot += wsum[w];
-      s_carry += tot;
-    }
-    __syncthreads();
-  }
-  bool bad = false;
-  for (int e = threadIdx.x; e < E; e += blockDim.x)
-    bad |= (s_end[e] < (e > 0 ? s_end[e - 1] : 0)) || (e == E - 1 && s_end[e] > rows);
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) record_status(status, MOE_DEV_BAD_OFFSETS);
-    return false;
-  }
-  return true;
-}
-
-// Tile (G) and row within the tile (r) of row p of the problem list.
-__device__ __forceinline__ void row_tile(const int* s_end, const int* s_pre, int E, long long p, long long& G,
-                                         int& r) {
-  int lo = 0, hi = E - 1;  // first expert whose segment ends after p
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (s_end[mid] > p) hi = mid; else lo = mid + 1;
-  }
-  const long long start = lo > 0 ? s_end[lo - 1] : 0;
-  G = s_pre[lo] + (p - start) / 128;
-  r = static_cast<int>((p - start) % 128);
 }
 
 // Rows along K (the contraction), one thread per (row, 32-block). With offsets: rows p < M of a
