@@ -124,37 +124,43 @@ def _ptr(t):
         return None
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("tensors passed to the library must be contiguous CUDA tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _rows(t, T, width):
     """(pointer, row pitch in elements) of a [T, width] view whose rows are contiguous. A view with
     one row repeated (row stride 0) is a pitch of 0."""
-    if not t.is_cuda or t.dim() != 2 or t.shape[0] < T or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda or len(shape) != 2 or shape[0] < T or shape[1] != width or (stride[1] != 1 and width > 1):
         raise ValueError(f"expected a CUDA tensor of at least {T} rows of {width} contiguous elements")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if T > 1 else width
+    return t.data_ptr(), stride[0] if T > 1 else width
 
 
 def _dtype(t):
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return DTYPE_F32
     raise ValueError(f"expected a bfloat16 or float32 tensor, not {t.dtype}")
 
 
 def _typed(t, dtype, numel, name):
     """Pointer of a contiguous CUDA tensor of `dtype` with at least `numel` elements (None passes)."""
-    if t is not None and (t.dtype != dtype or t.numel() < numel):
-        raise ValueError(f"{name}: expected at least {numel} elements of {dtype}")
-    return _ptr(t)
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < numel or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {numel} elements of {dtype}")
+    return t.data_ptr()
 
 
 def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    # the handle of torch.cuda.current_stream() without its Python object: that takes 3 us, as long
+    # as the C call and its launch together
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _check(fn: str, status: int):
@@ -386,10 +392,14 @@ def moe_gate_bwd(logits, lse, ids, weights, counts, n_valid, d_weights, d_loss, 
 
 def _norm_weight(d, *ws):
     """The type of the given weights (all bf16 or all fp32, [d] each; fp32 when there are none)."""
-    ws = [w for w in ws if w is not None]
-    if any(w.numel() != d for w in ws) or len({w.dtype for w in ws}) > 1:
-        raise ValueError(f"the weights have to be [{d}] and of one type")
-    return _dtype(ws[0]) if ws else DTYPE_F32
+    one = None
+    for w in ws:
+        if w is None:
+            continue
+        if w.numel() != d or (one is not None and w.dtype is not one.dtype):
+            raise ValueError(f"the weights have to be [{d}] and of one type")
+        one = w
+    return DTYPE_F32 if one is None else _dtype(one)
 
 
 def moe_layer_norm_fwd(x, gamma, beta, T, d, eps, y, mean=None, rstd=None, stream=None):

@@ -10,11 +10,17 @@
 // with c_e = dL_bal E counts_e / (top_k N^2); without renormalisation s = sum_j w_j dw_j and
 // s' = 0, with it s = 0 and s' = sum_j w_j dw_j.
 //
-// One warp a token, its logits in registers: expert e = 32 j + lane is element j of lane e % 32.
-// Each logit is read once by the forward and once by the backward. The per-expert sums over the
-// tokens of a warp stay in registers (lane and element own an expert), a block adds its warps'
-// sums in order and leaves one partial row in the workspace, and a second kernel adds those in
-// block order: no floating-point atomics, so results do not depend on scheduling.
+// G lanes a token (8, 16 or 32: several tokens a warp when there are few experts), eight consecutive
+// experts a lane, its logits in registers: each logit is read once by the forward and once by
+// the backward, 16 bytes at a time where the rows allow it. Each lane sorts its eight (logit,
+// expert) keys with a 19-comparator network; a round of the top_k is then one maximum over the
+// lanes' heads and a shift of the winner's list. Both kernels are bound by instruction issue, not
+// by memory, so the count per token is what the layout minimises (rescanning a lane's values in
+// each round instead of sorting once took four times as long).
+// The per-expert sums over the tokens of a lane group stay in registers (lane and element own
+// an expert), a block adds its groups' sums in order and leaves one partial row in the workspace,
+// and a second kernel adds those in block order: no floating-point atomics, so results do not
+// depend on scheduling.
 #include <algorithm>
 #include <cmath>
 
@@ -34,22 +40,151 @@ constexpr int MAX_TOPK = 32;
 constexpr int MAX_BLOCKS = 608;
 constexpr unsigned FULL = 0xffffffffu;
 
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load_logit(const bf16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// Unsigned key with the order of the floats. A logit of -inf or NaN gets 0, below every other
-// value: it is never selected.
-__device__ __forceinline__ uint32_t order_key(float f) {
-  if (!(f > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(f == 0.f ? 0.f : f);  // -0 and +0 tie
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+// Eight consecutive logits from expert e0 of a row; -inf past the last expert. VEC: the row is
+// 16-byte aligned and E a multiple of 8.
+template <bool VEC>
+__device__ __forceinline__ void load8(const float* row, int e0, int E, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (e0 < E) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(row + e0)), b = __ldg(reinterpret_cast<const float4*>(row + e0) + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = e0 + j < E ? __ldg(row + e0 + j) : -INFINITY;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const bf16* row, int e0, int E, float (&v)[8]) {
+  if constexpr (VEC) {
+    if (e0 < E) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(row + e0));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = bf16_lo(w[j]);
+        v[2 * j + 1] = bf16_hi(w[j]);
+      }
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = -INFINITY;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = e0 + j < E ? __bfloat162float(row[e0 + j]) : -INFINITY;
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float* row, int e0, int E, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (e0 >= E) return;
+    reinterpret_cast<float4*>(row + e0)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(row + e0)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e0 + j < E) row[e0 + j] = v[j];
+  }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(bf16* row, int e0, int E, const float (&v)[8]) {
+  if constexpr (VEC) {
+    if (e0 < E)
+      *reinterpret_cast<uint4*>(row + e0) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e0 + j < E) row[e0 + j] = __float2bfloat16_rn(v[j]);
+  }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// Unsigned number with the order of the floats. A logit of -inf or NaN gets 0, below every other
+// value: it is never selected.
+__device__ __forceinline__ uint32_t order_bits(float f) {
+  if (!(f > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(f + 0.f);  // -0 + 0 = +0: the two zeros tie
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k); }
+
+// Keys that order by logit, then by lower expert, and are unique (0: not selectable). A bf16 logit
+// has 16 bits, so that one 32-bit word holds it with the expert; an fp32 logit takes 64.
+template <typename T>
+struct Key;
+template <>
+struct Key<bf16> {
+  typedef uint32_t type;
+  static __device__ __forceinline__ type make(float f, int e) {
+    const uint32_t o = order_bits(f);  // of a bf16 value: the low 16 bits are all zeros or all ones
+    return o == 0u ? 0u : ((o & 0xffff0000u) | static_cast<uint32_t>(0xffff - e));
+  }
+  static __device__ __forceinline__ int expert(type k) { return 0xffff - static_cast<int>(k & 0xffffu); }
+  static __device__ __forceinline__ float value(type k) {
+    return order_value((k & 0x80000000u) ? (k & 0xffff0000u) : (k | 0xffffu));
+  }
+  template <int G>
+  static __device__ __forceinline__ type group_max(type k) {
+    if constexpr (G == 32) {
+      return __reduce_max_sync(FULL, k);
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+      for (int o = G / 2; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(FULL, k, o));
+      return k;
+    }
+  }
+};
+template <>
+struct Key<float> {
+  typedef unsigned long long type;
+  static __device__ __forceinline__ type make(float f, int e) {
+    const uint32_t o = order_bits(f);
+    return o == 0u ? 0ull : ((static_cast<type>(o) << 32) | static_cast<uint32_t>(0xffff - e));
+  }
+  static __device__ __forceinline__ int expert(type k) { return 0xffff - static_cast<int>(k & 0xffffu); }
+  static __device__ __forceinline__ float value(type k) { return order_value(static_cast<uint32_t>(k >> 32)); }
+  template <int G>
+  static __device__ __forceinline__ type group_max(type k) {
+    if constexpr (G == 32) {
+      const uint32_t hi = static_cast<uint32_t>(k >> 32);
+      const uint32_t top = __reduce_max_sync(FULL, hi);
+      const uint32_t lo = __reduce_max_sync(FULL, hi == top ? static_cast<uint32_t>(k) : 0u);
+      return (static_cast<type>(top) << 32) | lo;
+    } else {
+#pragma unroll
+      for (int o = G / 2; o > 0; o >>= 1) k = max(k, __shfl_xor_sync(FULL, k, o));
+      return k;
+    }
+  }
+};
+
+// Descending order of eight keys: Batcher's odd-even merge sort.
+template <typename K>
+__device__ __forceinline__ void sort8(K (&k)[8]) {
+  constexpr int net[19][2] = {{0, 1}, {2, 3}, {4, 5}, {6, 7}, {0, 2}, {1, 3}, {4, 6}, {5, 7}, {1, 2}, {5, 6},
+                              {0, 4}, {1, 5}, {2, 6}, {3, 7}, {2, 4}, {3, 5}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+  for (int i = 0; i < 19; ++i) {
+    const K a = k[net[i][0]], b = k[net[i][1]];
+    k[net[i][0]] = max(a, b);
+    k[net[i][1]] = min(a, b);
+  }
+}
+
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
   return v;
 }
 
@@ -63,127 +198,133 @@ struct GateArgs {
   float* weights;
   float* lse;           // nullable
   float* part;          // nullable: per block [P_e (E) | counts_e (E) | sum lse^2 | tokens], 4-byte words
+  unsigned* ticket;     // with part: the statistics kernel's block counter, cleared here
 };
 
 constexpr int part_words(int E) { return 2 * E + 2; }
 
-template <typename T, int NV>
+// NL lists of eight experts a lane: expert 8 (32 l + lane) + j (NL = 1: 8 lane_in_group + j).
+template <typename T, int NL, int G, bool VEC>
 __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
-  extern __shared__ float sh[];  // [WARPS][E] probability sums, then [E] counts
+  typedef Key<T> KT;
+  typedef typename KT::type K;
+  constexpr int GROUPS = 32 / G;           // tokens a warp
+  constexpr int NS = 32 / G;               // slots a lane keeps (top_k <= 32)
+  extern __shared__ float sh[];            // [WARPS * GROUPS][E] probability sums, then [E] counts
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gl = lane % G, grp = warp * GROUPS + lane / G;
   const bool stats = a.part != nullptr;
-  int* s_cnt = reinterpret_cast<int*>(sh + WARPS * a.E);
+  int* s_cnt = reinterpret_cast<int*>(sh + WARPS * GROUPS * a.E);
   if (stats) {
     for (int e = threadIdx.x; e < a.E; e += THREADS) s_cnt[e] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
     __syncthreads();
   }
-  float psum[NV];
+  float psum[NL][8];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) psum[j] = 0.f;
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) psum[l][j] = 0.f;
   float z = 0.f;
   int tokens = 0;
-  for (long long t = static_cast<long long>(blockIdx.x) * WARPS + warp; t < a.T;
-       t += static_cast<long long>(gridDim.x) * WARPS) {
-    int32_t* ids = a.ids + t * a.k;
-    float* wt = a.weights + t * a.k;
-    const bool on = a.mask == nullptr || __ldg(a.mask + t) != 0;  // warp-uniform
-    float v[NV];
+  // warp-uniform loop: the shuffles need every lane
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * WARPS + warp) * GROUPS; t0 < a.T;
+       t0 += static_cast<long long>(gridDim.x) * WARPS * GROUPS) {
+    const long long t = t0 + lane / G;
+    const bool in = t < a.T;
+    const bool live = in && (a.mask == nullptr || __ldg(a.mask + t) != 0);
+    const T* row = static_cast<const T*>(a.logits) + (live ? t : 0) * a.ld;
+    float v[NL][8];
     float m = -INFINITY;
-    if (on) {
-      const T* row = static_cast<const T*>(a.logits) + t * a.ld;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int e = 32 * j + lane;
-        v[j] = e < a.E ? load_logit(row + e) : -INFINITY;
-        m = fmaxf(m, v[j]);  // ignores NaN
-      }
+    for (int l = 0; l < NL; ++l) {
+      load8<VEC>(row, live ? 8 * (32 * l + gl) : a.E, a.E, v[l]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, v[l][j]);  // ignores NaN
     }
+    m = group_max<G>(m);
     const float base = m > -INFINITY ? m : 0.f;
-    float p[NV];
+    K key[NL][8];
     float sum = 0.f;
-    if (on) {
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        p[j] = __expf(v[j] - base);
-        sum += p[j];
+    for (int l = 0; l < NL; ++l)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        key[l][j] = KT::make(v[l][j], 8 * (32 * l + gl) + j);
+        v[l][j] = __expf(v[l][j] - base);
+        sum += v[l][j];
       }
-      sum = warp_sum(sum);
-    }
+    sum = group_sum<G>(sum);
     // a token without any logit above -inf takes no part, like a masked one; one with a NaN
     // does, and its probabilities are NaN
-    if (!on || sum == 0.f) {
-      if (lane < a.k) {
-        ids[lane] = -1;
-        wt[lane] = 0.f;
-      }
-      if (a.lse != nullptr && lane == 0) a.lse[t] = -INFINITY;
-      continue;
-    }
-    const float inv = 1.0f / sum;
-    const float lse = base + logf(sum);
-    if (a.lse != nullptr && lane == 0) a.lse[t] = lse;
-    if (stats) {
+    const bool part = live && !(sum == 0.f);
+    const float lse = part ? base + logf(sum) : -INFINITY;
+    if (a.lse != nullptr && gl == 0 && in) a.lse[t] = lse;
+    if (stats && part) {
+      const float inv = 1.0f / sum;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) psum[j] = fmaf(p[j], inv, psum[j]);
+      for (int l = 0; l < NL; ++l)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) psum[l][j] = fmaf(v[l][j], inv, psum[l][j]);
       z = fmaf(lse, lse, z);
       ++tokens;
     }
-    // top_k: k rounds of a warp-wide maximum; ties go to the lower expert
-    uint32_t key[NV];
-    uint32_t best = 0u;
-    int at = 0;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      key[j] = order_key(v[j]);
-      if (key[j] > best) {
-        best = key[j];
-        at = j;
-      }
-    }
-    int my_id = -1;
-    float my_e = 0.f;
-    for (int r = 0; r < a.k; ++r) {
-      const uint32_t top = __reduce_max_sync(FULL, best);
-      if (top == 0u) break;  // warp-uniform: fewer than k selectable experts
-      const int id = static_cast<int>(__reduce_min_sync(FULL, best == top ? static_cast<unsigned>(32 * at + lane) : FULL));
-      if (lane == r) {
-        my_id = id;
-        const uint32_t b = (top & 0x80000000u) ? (top & 0x7fffffffu) : ~top;  // the logit again
-        my_e = __expf(__uint_as_float(b) - base);
-      }
-      if (lane == (id & 31)) {
-        best = 0u;
+    for (int l = 0; l < NL; ++l) sort8(key[l]);
+    int my_id[NS];
+    float my_e[NS];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          if (32 * j + lane == id) key[j] = 0u;
-          if (key[j] > best) {
-            best = key[j];
-            at = j;
-          }
+    for (int s = 0; s < NS; ++s) {
+      my_id[s] = -1;
+      my_e[s] = 0.f;
+      for (int r = 0; r < G && s * G + r < a.k; ++r) {
+        K head = key[0][0];
+#pragma unroll
+        for (int l = 1; l < NL; ++l) head = max(head, key[l][0]);
+        const K top = KT::template group_max<G>(head);
+        if (gl == r && top != 0) {
+          my_id[s] = KT::expert(top);
+          my_e[s] = __expf(KT::value(top) - base);
+        }
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+          const bool won = key[l][0] == top;  // keys are unique; an empty list stays empty
+#pragma unroll
+          for (int j = 0; j < 7; ++j) key[l][j] = won ? key[l][j + 1] : key[l][j];
+          key[l][7] = won ? 0 : key[l][7];
         }
       }
     }
-    const float norm = a.renorm ? warp_sum(my_e) : sum;
-    // a NaN anywhere in the row makes every weight of the row NaN, renormalised or not
-    const float w = sum != sum ? sum : my_e / norm;
-    if (lane < a.k) {
-      ids[lane] = my_id;
-      wt[lane] = my_id >= 0 ? w : 0.f;
-      if (stats && my_id >= 0) atomicAdd(s_cnt + my_id, 1);
+    float norm = sum;
+    if (a.renorm) {
+      norm = 0.f;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) norm += my_e[s];
+      norm = group_sum<G>(norm);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int slot = s * G + gl;
+      if (!in || slot >= a.k) continue;
+      // a NaN anywhere in the row makes every weight of the row NaN, renormalised or not
+      const float w = sum != sum ? sum : my_e[s] / norm;
+      a.ids[t * a.k + slot] = my_id[s];
+      a.weights[t * a.k + slot] = my_id[s] >= 0 ? w : 0.f;
+      if (stats && my_id[s] >= 0) atomicAdd(s_cnt + my_id[s], 1);
     }
   }
   if (!stats) return;
-  __shared__ float s_z[WARPS];
-  __shared__ int s_n[WARPS];
-  float* mine = sh + warp * a.E;
+  __shared__ float s_z[WARPS * GROUPS];
+  __shared__ int s_n[WARPS * GROUPS];
+  float* mine = sh + grp * a.E;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (32 * j + lane < a.E) mine[32 * j + lane] = psum[j];
-  if (lane == 0) {
-    s_z[warp] = z;
-    s_n[warp] = tokens;
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (8 * (32 * l + gl) + j < a.E) mine[8 * (32 * l + gl) + j] = psum[l][j];
+  if (gl == 0) {
+    s_z[grp] = z;
+    s_n[grp] = tokens;
   }
   __syncthreads();
   float* out = a.part + static_cast<size_t>(blockIdx.x) * part_words(a.E);
@@ -191,14 +332,14 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
   for (int e = threadIdx.x; e < a.E; e += THREADS) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) s += sh[w * a.E + e];
+    for (int w = 0; w < WARPS * GROUPS; ++w) s += sh[w * a.E + e];
     out[e] = s;
     iout[a.E + e] = s_cnt[e];
   }
   if (threadIdx.x == 0) {
     float sz = 0.f;
     int n = 0;
-    for (int w = 0; w < WARPS; ++w) {
+    for (int w = 0; w < WARPS * GROUPS; ++w) {
       sz += s_z[w];
       n += s_n[w];
     }
@@ -207,63 +348,66 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
   }
 }
 
-// Adds the blocks' partial rows in order: one block, thread e over the blocks (coalesced over
-// the experts), then the two losses from the totals.
+__device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
+
+// Adds the blocks' partial rows in order: 32 experts a block, 32 threads an expert over the rows
+// (coalesced over the experts), added in thread order. The last block to finish adds the blocks'
+// shares of the balance loss in block order and writes the losses.
 __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* __restrict__ part, int blocks, int k, int E,
                                                           int32_t* __restrict__ counts, int32_t* __restrict__ n_valid,
-                                                          float* __restrict__ prob_sum, float* __restrict__ loss) {
+                                                          float* __restrict__ prob_sum, float* __restrict__ loss,
+                                                          unsigned* ticket, float* share) {
   __shared__ float s_p[32][33];
   __shared__ int s_c[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int words = part_words(E);
   const int* ipart = reinterpret_cast<const int*>(part);
+  const int e = blockIdx.x * 32 + cx;
+  float p = 0.f;
+  int c = 0;
+  if (e < E)
+    for (int b = ry; b < blocks; b += 32) {
+      p += part[static_cast<size_t>(b) * words + e];
+      c += ipart[static_cast<size_t>(b) * words + E + e];
+    }
+  s_p[ry][cx] = p;
+  s_c[ry][cx] = c;
+  __syncthreads();
+  if (ry != 0) return;
+  p = 0.f;
+  c = 0;
+#pragma unroll
+  for (int r = 0; r < 32; ++r) {
+    p += s_p[r][cx];
+    c += s_c[r][cx];
+  }
+  if (e < E) {
+    prob_sum[e] = p;
+    counts[e] = c;
+  }
+  const float bal = warp_sum(e < E ? static_cast<float>(c) * p : 0.f);
+  unsigned last = 0u;
+  if (cx == 0) {
+    share[blockIdx.x] = bal;
+    __threadfence();
+    last = atomicAdd(ticket, 1u) == gridDim.x - 1 ? 1u : 0u;
+  }
+  if (__shfl_sync(FULL, last, 0) == 0u) return;
+  __threadfence();
   float z = 0.f;
   int n = 0;
-  if (threadIdx.x < 32) {
-    for (int b = cx; b < blocks; b += 32) {
-      z += part[static_cast<size_t>(b) * words + 2 * E];
-      n += ipart[static_cast<size_t>(b) * words + 2 * E + 1];
-    }
-    z = warp_sum(z);
-    n = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(n)));
+  for (int b = cx; b < blocks; b += 32) {
+    z += part[static_cast<size_t>(b) * words + 2 * E];
+    n += ipart[static_cast<size_t>(b) * words + 2 * E + 1];
   }
-  float bal = 0.f;  // sum of counts_e P_e (first warp)
-  for (int e0 = 0; e0 < E; e0 += 32) {
-    const int e = e0 + cx;
-    float p = 0.f;
-    int c = 0;
-    if (e < E)
-      for (int b = ry; b < blocks; b += 32) {
-        p += part[static_cast<size_t>(b) * words + e];
-        c += ipart[static_cast<size_t>(b) * words + E + e];
-      }
-    s_p[ry][cx] = p;
-    s_c[ry][cx] = c;
-    __syncthreads();
-    if (ry == 0) {
-      p = 0.f;
-      c = 0;
-#pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        p += s_p[r][cx];
-        c += s_c[r][cx];
-      }
-      if (e < E) {
-        prob_sum[e] = p;
-        counts[e] = c;
-      }
-      bal = fmaf(static_cast<float>(c), p, bal);
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x < 32) {
-    bal = warp_sum(bal);
-    if (threadIdx.x == 0) {
-      const float nf = static_cast<float>(n);
-      *n_valid = n;
-      loss[0] = n > 0 ? static_cast<float>(E) / (static_cast<float>(k) * nf) * (bal / nf) : 0.f;
-      loss[1] = n > 0 ? z / nf : 0.f;
-    }
+  z = warp_sum(z);
+  n = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(n)));
+  const float total = warp_sum(cx < gridDim.x ? __ldcg(share + cx) : 0.f);  // E <= 1024: at most 32 blocks
+  if (cx == 0) {
+    const float nf = static_cast<float>(n);
+    *n_valid = n;
+    loss[0] = n > 0 ? static_cast<float>(E) / (static_cast<float>(k) * nf) * (total / nf) : 0.f;
+    loss[1] = n > 0 ? z / nf : 0.f;
   }
 }
 
@@ -283,15 +427,23 @@ struct GateBwdArgs {
   long long ldd;
 };
 
-template <typename T, int NV>
+template <typename T, int NL, int G, bool VEC>
 __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) {
-  extern __shared__ float sh[];  // [WARPS][E] what the selected experts of the warp's token get on top
+  constexpr int GROUPS = 32 / G;
+  constexpr int NS = 32 / G;
+  extern __shared__ __align__(16) float bsh[];  // [WARPS * GROUPS][8 G NL] what a token's selected experts get on top
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* mine = sh + warp * a.E;
-  float c[NV];
+  const int gl = lane % G;
+  float* mine = bsh + (warp * GROUPS + lane / G) * (8 * G * NL);
+  float c[NL][8];
   float cz = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) c[j] = 0.f;
+  for (int l = 0; l < NL; ++l)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[l][j] = 0.f;
+      mine[8 * (32 * l + gl) + j] = 0.f;
+    }
   if (a.d_loss != nullptr) {
     const int n = __ldg(a.n_valid);
     if (n > 0) {
@@ -299,81 +451,115 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
       const float cb = __ldg(a.d_loss) * static_cast<float>(a.E) / (static_cast<float>(a.k) * nf) / nf;
       cz = 2.0f * __ldg(a.d_loss + 1) / nf;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (32 * j + lane < a.E) c[j] = cb * static_cast<float>(__ldg(a.counts + 32 * j + lane));
+      for (int l = 0; l < NL; ++l)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = 8 * (32 * l + gl) + j;
+          if (e < a.E) c[l][j] = cb * static_cast<float>(__ldg(a.counts + e));
+        }
     }
   }
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (32 * j + lane < a.E) mine[32 * j + lane] = 0.f;
   __syncwarp();
-  for (long long t = static_cast<long long>(blockIdx.x) * WARPS + warp; t < a.T;
-       t += static_cast<long long>(gridDim.x) * WARPS) {
-    T* out = static_cast<T*>(a.dlogits) + t * a.ldd;
-    const float lse = __ldg(a.lse + t);
-    if (lse == -INFINITY) {  // the token took no part (warp-uniform)
+  for (long long t0 = (static_cast<long long>(blockIdx.x) * WARPS + warp) * GROUPS; t0 < a.T;
+       t0 += static_cast<long long>(gridDim.x) * WARPS * GROUPS) {
+    const long long t = t0 + lane / G;
+    const bool in = t < a.T;
+    const float lse = in ? __ldg(a.lse + t) : -INFINITY;
+    const bool part = lse != -INFINITY;  // else the token took no part: its gradient is 0
+    const T* row = static_cast<const T*>(a.logits) + (part ? t : 0) * a.ld;
+    float p[NL][8];
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (32 * j + lane < a.E) store_logit(out + 32 * j + lane, 0.f);
-      continue;
+    for (int l = 0; l < NL; ++l) load8<VEC>(row, part ? 8 * (32 * l + gl) : a.E, a.E, p[l]);
+    int id[NS];
+    float w[NS], dw[NS], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      const int slot = i * G + gl;
+      id[i] = -1;
+      w[i] = dw[i] = 0.f;
+      if (part && slot < a.k && a.d_weights != nullptr) {
+        id[i] = __ldg(a.ids + t * a.k + slot);
+        w[i] = __ldg(a.weights + t * a.k + slot);
+        dw[i] = __ldg(a.d_weights + t * a.k + slot);
+        if (id[i] < 0 || id[i] >= a.E) id[i] = -1;
+        else s = fmaf(w[i], dw[i], s);
+      }
     }
-    int id = -1;
-    float w = 0.f, dw = 0.f;
-    if (lane < a.k && a.d_weights != nullptr) {
-      id = __ldg(a.ids + t * a.k + lane);
-      w = __ldg(a.weights + t * a.k + lane);
-      dw = __ldg(a.d_weights + t * a.k + lane);
-      if (id < 0 || id >= a.E) id = -1;
-    }
-    const float s = warp_sum(id >= 0 ? w * dw : 0.f);
-    if (id >= 0) mine[id] = w * (a.renorm ? dw - s : dw);
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float p[NV];
+    s = group_sum<G>(s);
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (id[i] >= 0) mine[id[i]] = w[i] * (a.renorm ? dw[i] - s : dw[i]);
     float dot = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = 32 * j + lane;
-      p[j] = e < a.E ? __expf(load_logit(row + e) - lse) : 0.f;
-      dot = fmaf(p[j], c[j], dot);
-    }
-    dot = warp_sum(dot) + (a.renorm ? 0.f : s);  // warp_sum orders the writes of `mine` too
-    __syncwarp();
-    const float shift = fmaf(cz, lse, -dot);
+    for (int l = 0; l < NL; ++l)
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = 32 * j + lane;
-      if (e < a.E) store_logit(out + e, fmaf(p[j], c[j] + shift, mine[e]));
+      for (int j = 0; j < 8; ++j) {
+        p[l][j] = part ? __expf(p[l][j] - lse) : 0.f;
+        dot = fmaf(p[l][j], c[l][j], dot);
+      }
+    dot = group_sum<G>(dot) + (a.renorm ? 0.f : s);
+    __syncwarp();
+    const float shift = part ? fmaf(cz, lse, -dot) : 0.f;
+    T* out = static_cast<T*>(a.dlogits) + (in ? t : 0) * a.ldd;
+#pragma unroll
+    for (int l = 0; l < NL; ++l) {
+      const float4* add = reinterpret_cast<const float4*>(mine + 8 * (32 * l + gl));
+      const float4 x = add[0], y = add[1];
+      const float top[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) p[l][j] = fmaf(p[l][j], c[l][j] + shift, top[j]);
+      store8<VEC>(out, in ? 8 * (32 * l + gl) : a.E, a.E, p[l]);
     }
     __syncwarp();
-    if (id >= 0) mine[id] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (id[i] >= 0) mine[id[i]] = 0.f;
     __syncwarp();
   }
 }
 
-template <typename T, int NV>
+template <typename T, int NL, int G, bool VEC>
 void launch_fwd(const GateArgs& a, int blocks, cudaStream_t s) {
-  const size_t smem = a.part != nullptr ? sizeof(float) * (WARPS + 1) * a.E : 0;
-  gate_fwd_kernel<T, NV><<<blocks, THREADS, smem, s>>>(a);
+  const size_t smem = a.part != nullptr ? sizeof(float) * (WARPS * (32 / G) + 1) * a.E : 0;
+  gate_fwd_kernel<T, NL, G, VEC><<<blocks, THREADS, smem, s>>>(a);
 }
-template <typename T, int NV>
+template <typename T, int NL, int G, bool VEC>
 void launch_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
-  gate_bwd_kernel<T, NV><<<blocks, THREADS, sizeof(float) * WARPS * a.E, s>>>(a);
+  gate_bwd_kernel<T, NL, G, VEC><<<blocks, THREADS, sizeof(float) * WARPS * 32 * 8 * NL, s>>>(a);
 }
 
-#define MOE_GATE_BY_WIDTH(fn, T, args, blocks, s)        \
-  do {                                                   \
-    if (args.E <= 32) fn<T, 1>(args, blocks, s);         \
-    else if (args.E <= 64) fn<T, 2>(args, blocks, s);    \
-    else if (args.E <= 128) fn<T, 4>(args, blocks, s);   \
-    else if (args.E <= 256) fn<T, 8>(args, blocks, s);   \
-    else if (args.E <= 512) fn<T, 16>(args, blocks, s);  \
-    else fn<T, 32>(args, blocks, s);                     \
-  } while (0)
+// Lanes a token: the fewest that hold its experts at eight each, so that a warp works on several
+// tokens; more than 256 experts take two or four lists of eight a lane.
+template <typename T, bool VEC>
+void by_width_fwd(const GateArgs& a, int blocks, cudaStream_t s) {
+  if (a.E <= 64) launch_fwd<T, 1, 8, VEC>(a, blocks, s);
+  else if (a.E <= 128) launch_fwd<T, 1, 16, VEC>(a, blocks, s);
+  else if (a.E <= 256) launch_fwd<T, 1, 32, VEC>(a, blocks, s);
+  else if (a.E <= 512) launch_fwd<T, 2, 32, VEC>(a, blocks, s);
+  else launch_fwd<T, 4, 32, VEC>(a, blocks, s);
+}
+template <typename T, bool VEC>
+void by_width_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
+  if (a.E <= 64) launch_bwd<T, 1, 8, VEC>(a, blocks, s);
+  else if (a.E <= 128) launch_bwd<T, 1, 16, VEC>(a, blocks, s);
+  else if (a.E <= 256) launch_bwd<T, 1, 32, VEC>(a, blocks, s);
+  else if (a.E <= 512) launch_bwd<T, 2, 32, VEC>(a, blocks, s);
+  else launch_bwd<T, 4, 32, VEC>(a, blocks, s);
+}
 
-int blocks_for(int T) { return static_cast<int>(std::max(1LL, std::min<long long>((static_cast<long long>(T) + WARPS - 1) / WARPS, MAX_BLOCKS))); }
+int tokens_per_block(int E) { return WARPS * (E <= 64 ? 4 : E <= 128 ? 2 : 1); }
+int blocks_for(int T, int E) {
+  const int per = tokens_per_block(E);
+  return static_cast<int>(std::max(1LL, std::min<long long>((static_cast<long long>(T) + per - 1) / per, MAX_BLOCKS)));
+}
 
 bool dtype_ok(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
 bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// rows that start on 16-byte boundaries and hold whole groups of eight experts
+bool rows16(const void* p, long long ld, int E, int dtype) {
+  return aligned(p, 16) && E % 8 == 0 && ld % (dtype == MOE_DTYPE_BF16 ? 8 : 4) == 0;
+}
 
 moe_status_t launched() {
   const cudaError_t err = cudaGetLastError();
@@ -382,8 +568,9 @@ moe_status_t launched() {
 
 }  // namespace
 
+// the blocks' partial rows, then the statistics kernel's block counter and shares
 size_t gate_workspace_bytes(int T, int E) {
-  return static_cast<size_t>(blocks_for(T)) * part_words(E) * sizeof(float);
+  return (static_cast<size_t>(blocks_for(T, E)) * part_words(E) + 1 + 32) * sizeof(float);
 }
 
 }  // namespace moe
@@ -425,11 +612,14 @@ moe_status_t moe_gate_fwd(const void* logits, int dtype, long long ld, const uin
   a.weights = weights;
   a.lse = lse;
   a.part = stats ? static_cast<float*>(ws) : nullptr;
-  const int blocks = blocks_for(T);
-  if (dtype == MOE_DTYPE_BF16) MOE_GATE_BY_WIDTH(launch_fwd, bf16, a, blocks, s);
-  else MOE_GATE_BY_WIDTH(launch_fwd, float, a, blocks, s);
+  const int blocks = blocks_for(T, E);
+  a.ticket = stats ? static_cast<unsigned*>(ws) + static_cast<size_t>(blocks) * part_words(E) : nullptr;
+  const bool vec = rows16(logits, ld, E, dtype);
+  if (dtype == MOE_DTYPE_BF16) vec ? by_width_fwd<bf16, true>(a, blocks, s) : by_width_fwd<bf16, false>(a, blocks, s);
+  else vec ? by_width_fwd<float, true>(a, blocks, s) : by_width_fwd<float, false>(a, blocks, s);
   if ((st = launched()) != MOE_OK || !stats) return st;
-  gate_stats_kernel<<<1, 1024, 0, s>>>(a.part, blocks, top_k, E, counts, n_valid, prob_sum, loss);
+  gate_stats_kernel<<<(E + 31) / 32, 1024, 0, s>>>(a.part, blocks, top_k, E, counts, n_valid, prob_sum, loss, a.ticket,
+                                                   reinterpret_cast<float*>(a.ticket + 1));
   return launched();
 }
 
@@ -467,10 +657,11 @@ moe_status_t moe_gate_bwd(const void* logits, int dtype, long long ld, const flo
   a.renorm = (flags & MOE_GATE_RENORM) != 0;
   a.dlogits = dlogits;
   a.ldd = ldd;
-  const int blocks = blocks_for(T);
+  const int blocks = blocks_for(T, E);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MOE_DTYPE_BF16) MOE_GATE_BY_WIDTH(launch_bwd, bf16, a, blocks, s);
-  else MOE_GATE_BY_WIDTH(launch_bwd, float, a, blocks, s);
+  const bool vec = rows16(logits, ld, E, dtype) && rows16(dlogits, ldd, E, dtype);
+  if (dtype == MOE_DTYPE_BF16) vec ? by_width_bwd<bf16, true>(a, blocks, s) : by_width_bwd<bf16, false>(a, blocks, s);
+  else vec ? by_width_bwd<float, true>(a, blocks, s) : by_width_bwd<float, false>(a, blocks, s);
   return launched();
 }
 
