@@ -14,9 +14,10 @@
 // experts a lane, its logits in registers: each logit is read once by the forward and once by
 // the backward, 16 bytes at a time where the rows allow it. Each lane sorts its eight (logit,
 // expert) keys with a 19-comparator network; a round of the top_k is then one maximum over the
-// lanes' heads and a shift of the winner's list. Both kernels are bound by instruction issue, not
+// lanes' heads and a step in the winner's list. Both kernels are bound by instruction issue, not
 // by memory, so the count per token is what the layout minimises (rescanning a lane's values in
-// each round instead of sorting once took four times as long).
+// each round instead of sorting once took four times as long). The sorted lists lie in shared
+// memory, where taking a list's next head is one load instead of a shift of eight registers.
 // The per-expert sums over the tokens of a lane group stay in registers (lane and element own
 // an expert), a block adds its groups' sums in order and leaves one partial row in the workspace,
 // and a second kernel adds those in block order: no floating-point atomics, so results do not
@@ -38,6 +39,8 @@ constexpr int MAX_TOPK = 32;
 // Blocks at most, and so rows of partial sums: four for each of the 152 SMs. A constant, because
 // the size of the workspace is host arithmetic.
 constexpr int MAX_BLOCKS = 608;
+// Blocks of the backward at most, ten for each SM: it leaves no partial sums.
+constexpr int BWD_BLOCKS = 1520;
 constexpr unsigned FULL = 0xffffffffu;
 
 // Eight consecutive logits from expert e0 of a row; -inf past the last expert. VEC: the row is
@@ -103,25 +106,30 @@ __device__ __forceinline__ void store8(bf16* row, int e0, int E, const float (&v
   }
 }
 
-// Unsigned number with the order of the floats. A logit of -inf or NaN gets 0, below every other
-// value: it is never selected.
+// e^x without the subnormal range's scaling instructions (results below 2^-126 are 0)
+__device__ __forceinline__ float exp_f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+
+// Unsigned number with the order of the floats; NaN orders as -inf, -0 as 0.
 __device__ __forceinline__ uint32_t order_bits(float f) {
-  if (!(f > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(f + 0.f);  // -0 + 0 = +0: the two zeros tie
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  const int b = __float_as_int(fmaxf(f, -INFINITY) + 0.f);
+  return static_cast<uint32_t>(b ^ ((b >> 31) | static_cast<int>(0x80000000u)));
 }
 __device__ __forceinline__ float order_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k); }
 
-// Keys that order by logit, then by lower expert, and are unique (0: not selectable). A bf16 logit
-// has 16 bits, so that one 32-bit word holds it with the expert; an fp32 logit takes 64.
+// Keys that order by logit, then by lower expert, and are unique and not 0. A bf16 logit has 16
+// bits, so that one 32-bit word holds it with the expert; an fp32 logit takes 64.
 template <typename T>
 struct Key;
 template <>
 struct Key<bf16> {
   typedef uint32_t type;
   static __device__ __forceinline__ type make(float f, int e) {
-    const uint32_t o = order_bits(f);  // of a bf16 value: the low 16 bits are all zeros or all ones
-    return o == 0u ? 0u : ((o & 0xffff0000u) | static_cast<uint32_t>(0xffff - e));
+    // of a bf16 value the low 16 order bits are all zeros or all ones
+    return (order_bits(f) & 0xffff0000u) | static_cast<uint32_t>(0xffff - e);
   }
   static __device__ __forceinline__ int expert(type k) { return 0xffff - static_cast<int>(k & 0xffffu); }
   static __device__ __forceinline__ float value(type k) {
@@ -142,8 +150,7 @@ template <>
 struct Key<float> {
   typedef unsigned long long type;
   static __device__ __forceinline__ type make(float f, int e) {
-    const uint32_t o = order_bits(f);
-    return o == 0u ? 0ull : ((static_cast<type>(o) << 32) | static_cast<uint32_t>(0xffff - e));
+    return (static_cast<type>(order_bits(f)) << 32) | static_cast<uint32_t>(0xffff - e);
   }
   static __device__ __forceinline__ int expert(type k) { return 0xffff - static_cast<int>(k & 0xffffu); }
   static __device__ __forceinline__ float value(type k) { return order_value(static_cast<uint32_t>(k >> 32)); }
@@ -202,24 +209,31 @@ struct GateArgs {
 };
 
 constexpr int part_words(int E) { return 2 * E + 2; }
+__host__ __device__ constexpr int count_bytes(int E) { return (4 * E + 15) & ~15; }
+constexpr int LIST = 9;  // a lane's eight sorted keys and a 0; odd, so that lanes use different banks
 
-// NL lists of eight experts a lane: expert 8 (32 l + lane) + j (NL = 1: 8 lane_in_group + j).
+// NL lists of eight experts a lane: expert 8 (G l + lane_in_group) + j.
 template <typename T, int NL, int G, bool VEC>
 __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
   typedef Key<T> KT;
   typedef typename KT::type K;
   constexpr int GROUPS = 32 / G;           // tokens a warp
   constexpr int NS = 32 / G;               // slots a lane keeps (top_k <= 32)
-  extern __shared__ float sh[];            // [WARPS * GROUPS][E] probability sums, then [E] counts
+  // [E] counts, then the lists, over which the block's sums are staged at the end
+  extern __shared__ __align__(16) uint8_t fsh[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = warp * GROUPS + lane / G;
   const bool stats = a.part != nullptr;
-  int* s_cnt = reinterpret_cast<int*>(sh + WARPS * GROUPS * a.E);
+  int* s_cnt = reinterpret_cast<int*>(fsh);
+  uint8_t* body = fsh + count_bytes(a.E);
+  K* list = reinterpret_cast<K*>(body) + threadIdx.x * (NL * LIST);
   if (stats) {
     for (int e = threadIdx.x; e < a.E; e += THREADS) s_cnt[e] = 0;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
     __syncthreads();
   }
+#pragma unroll
+  for (int l = 0; l < NL; ++l) list[l * LIST + 8] = 0;
   float psum[NL][8];
 #pragma unroll
   for (int l = 0; l < NL; ++l)
@@ -238,22 +252,28 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
     float m = -INFINITY;
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
-      load8<VEC>(row, live ? 8 * (32 * l + gl) : a.E, a.E, v[l]);
+      load8<VEC>(row, live ? 8 * (G * l + gl) : a.E, a.E, v[l]);
 #pragma unroll
       for (int j = 0; j < 8; ++j) m = fmaxf(m, v[l][j]);  // ignores NaN
     }
     m = group_max<G>(m);
     const float base = m > -INFINITY ? m : 0.f;
-    K key[NL][8];
+    K head[NL];
     float sum = 0.f;
 #pragma unroll
-    for (int l = 0; l < NL; ++l)
+    for (int l = 0; l < NL; ++l) {
+      K key[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        key[l][j] = KT::make(v[l][j], 8 * (32 * l + gl) + j);
-        v[l][j] = __expf(v[l][j] - base);
+        key[j] = KT::make(v[l][j], 8 * (G * l + gl) + j);
+        v[l][j] = exp_f(v[l][j] - base);
         sum += v[l][j];
       }
+      sort8(key);
+      head[l] = key[0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) list[l * LIST + j] = key[j];
+    }
     sum = group_sum<G>(sum);
     // a token without any logit above -inf takes no part, like a masked one; one with a NaN
     // does, and its probabilities are NaN
@@ -269,31 +289,30 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
       z = fmaf(lse, lse, z);
       ++tokens;
     }
-#pragma unroll
-    for (int l = 0; l < NL; ++l) sort8(key[l]);
     int my_id[NS];
     float my_e[NS];
+    int next[NL];
+#pragma unroll
+    for (int l = 0; l < NL; ++l) next[l] = l * LIST + 1;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      my_id[s] = -1;
-      my_e[s] = 0.f;
+      K mine = 0;
+      // a round takes the group's largest key. Keys are unique and the group has at least twice as
+      // many as there are rounds, so an empty list's 0 never wins
       for (int r = 0; r < G && s * G + r < a.k; ++r) {
-        K head = key[0][0];
+        K best = head[0];
 #pragma unroll
-        for (int l = 1; l < NL; ++l) head = max(head, key[l][0]);
-        const K top = KT::template group_max<G>(head);
-        if (gl == r && top != 0) {
-          my_id[s] = KT::expert(top);
-          my_e[s] = __expf(KT::value(top) - base);
-        }
+        for (int l = 1; l < NL; ++l) best = max(best, head[l]);
+        const K top = KT::template group_max<G>(best);
+        if (gl == r) mine = top;
 #pragma unroll
-        for (int l = 0; l < NL; ++l) {
-          const bool won = key[l][0] == top;  // keys are unique; an empty list stays empty
-#pragma unroll
-          for (int j = 0; j < 7; ++j) key[l][j] = won ? key[l][j + 1] : key[l][j];
-          key[l][7] = won ? 0 : key[l][7];
-        }
+        for (int l = 0; l < NL; ++l)
+          if (head[l] == top) head[l] = list[next[l]++];
       }
+      const float logit = KT::value(mine);
+      const bool chosen = part && mine != 0 && logit > -INFINITY;
+      my_id[s] = chosen ? KT::expert(mine) : -1;
+      my_e[s] = chosen ? exp_f(logit - base) : 0.f;
     }
     float norm = sum;
     if (a.renorm) {
@@ -316,12 +335,14 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
   if (!stats) return;
   __shared__ float s_z[WARPS * GROUPS];
   __shared__ int s_n[WARPS * GROUPS];
+  float* sh = reinterpret_cast<float*>(body);  // [WARPS * GROUPS][E] probability sums
   float* mine = sh + grp * a.E;
+  __syncthreads();  // every list has been read
 #pragma unroll
   for (int l = 0; l < NL; ++l)
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (8 * (32 * l + gl) + j < a.E) mine[8 * (32 * l + gl) + j] = psum[l][j];
+      if (8 * (G * l + gl) + j < a.E) mine[8 * (G * l + gl) + j] = psum[l][j];
   if (gl == 0) {
     s_z[grp] = z;
     s_n[grp] = tokens;
@@ -442,7 +463,7 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       c[l][j] = 0.f;
-      mine[8 * (32 * l + gl) + j] = 0.f;
+      mine[8 * (G * l + gl) + j] = 0.f;
     }
   if (a.d_loss != nullptr) {
     const int n = __ldg(a.n_valid);
@@ -454,7 +475,7 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
       for (int l = 0; l < NL; ++l)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const int e = 8 * (32 * l + gl) + j;
+          const int e = 8 * (G * l + gl) + j;
           if (e < a.E) c[l][j] = cb * static_cast<float>(__ldg(a.counts + e));
         }
     }
@@ -469,7 +490,7 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
     const T* row = static_cast<const T*>(a.logits) + (part ? t : 0) * a.ld;
     float p[NL][8];
 #pragma unroll
-    for (int l = 0; l < NL; ++l) load8<VEC>(row, part ? 8 * (32 * l + gl) : a.E, a.E, p[l]);
+    for (int l = 0; l < NL; ++l) load8<VEC>(row, part ? 8 * (G * l + gl) : a.E, a.E, p[l]);
     int id[NS];
     float w[NS], dw[NS], s = 0.f;
 #pragma unroll
@@ -494,7 +515,7 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
     for (int l = 0; l < NL; ++l)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        p[l][j] = part ? __expf(p[l][j] - lse) : 0.f;
+        p[l][j] = part ? exp_f(p[l][j] - lse) : 0.f;
         dot = fmaf(p[l][j], c[l][j], dot);
       }
     dot = group_sum<G>(dot) + (a.renorm ? 0.f : s);
@@ -503,12 +524,12 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
     T* out = static_cast<T*>(a.dlogits) + (in ? t : 0) * a.ldd;
 #pragma unroll
     for (int l = 0; l < NL; ++l) {
-      const float4* add = reinterpret_cast<const float4*>(mine + 8 * (32 * l + gl));
+      const float4* add = reinterpret_cast<const float4*>(mine + 8 * (G * l + gl));
       const float4 x = add[0], y = add[1];
       const float top[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) p[l][j] = fmaf(p[l][j], c[l][j] + shift, top[j]);
-      store8<VEC>(out, in ? 8 * (32 * l + gl) : a.E, a.E, p[l]);
+      store8<VEC>(out, in ? 8 * (G * l + gl) : a.E, a.E, p[l]);
     }
     __syncwarp();
 #pragma unroll
@@ -518,39 +539,73 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
   }
 }
 
+moe_status_t launched() {
+  const cudaError_t err = cudaGetLastError();
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
+}
+
 template <typename T, int NL, int G, bool VEC>
-void launch_fwd(const GateArgs& a, int blocks, cudaStream_t s) {
-  const size_t smem = a.part != nullptr ? sizeof(float) * (WARPS * (32 / G) + 1) * a.E : 0;
+moe_status_t launch_fwd(const GateArgs& a, int blocks, cudaStream_t s) {
+  constexpr int lists = THREADS * NL * LIST * static_cast<int>(sizeof(typename Key<T>::type));
+  constexpr int widest = 8 * G * NL;
+  constexpr int most = count_bytes(widest) + std::max(lists, WARPS * (32 / G) * widest * 4);
+  const int smem = count_bytes(a.E) + std::max(lists, WARPS * (32 / G) * a.E * 4);
+  if (most > 48 * 1024) {
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(gate_fwd_kernel<T, NL, G, VEC>), most);
+    if (err != cudaSuccess) return cuda_fail(err);
+  }
   gate_fwd_kernel<T, NL, G, VEC><<<blocks, THREADS, smem, s>>>(a);
+  return launched();
 }
 template <typename T, int NL, int G, bool VEC>
-void launch_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
+moe_status_t launch_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
   gate_bwd_kernel<T, NL, G, VEC><<<blocks, THREADS, sizeof(float) * WARPS * 32 * 8 * NL, s>>>(a);
+  return launched();
 }
 
-// Lanes a token: the fewest that hold its experts at eight each, so that a warp works on several
-// tokens; more than 256 experts take two or four lists of eight a lane.
-template <typename T, bool VEC>
-void by_width_fwd(const GateArgs& a, int blocks, cudaStream_t s) {
-  if (a.E <= 64) launch_fwd<T, 1, 8, VEC>(a, blocks, s);
-  else if (a.E <= 128) launch_fwd<T, 1, 16, VEC>(a, blocks, s);
-  else if (a.E <= 256) launch_fwd<T, 1, 32, VEC>(a, blocks, s);
-  else if (a.E <= 512) launch_fwd<T, 2, 32, VEC>(a, blocks, s);
-  else launch_fwd<T, 4, 32, VEC>(a, blocks, s);
-}
-template <typename T, bool VEC>
-void by_width_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
-  if (a.E <= 64) launch_bwd<T, 1, 8, VEC>(a, blocks, s);
-  else if (a.E <= 128) launch_bwd<T, 1, 16, VEC>(a, blocks, s);
-  else if (a.E <= 256) launch_bwd<T, 1, 32, VEC>(a, blocks, s);
-  else if (a.E <= 512) launch_bwd<T, 2, 32, VEC>(a, blocks, s);
-  else launch_bwd<T, 4, 32, VEC>(a, blocks, s);
+// Lanes a token and lists a lane. The forward gives many tokens few lanes each, two or four lists a
+// lane: what a token costs besides its experts (sums, rounds, addresses) is then shared by more
+// tokens of the warp (131072 x 256 bf16: 63 us, against 69 at full width). Few tokens (less than
+// one for each warp of the grid) take as many lanes as hold eight experts each, which keeps more
+// warps at work, and so do rows that are read one element at a time. The backward has no rounds
+// and waits for its loads: always full width (37 us, against 44).
+struct Width {
+  int lists, lanes;
+};
+Width width_for(int E, bool many) {
+  if (E <= 64) return {1, 8};
+  if (E <= 128) return many ? Width{2, 8} : Width{1, 16};
+  if (E <= 256) return many ? Width{2, 16} : Width{1, 32};
+  if (E <= 512) return many ? Width{4, 16} : Width{2, 32};
+  return {4, 32};
 }
 
-int tokens_per_block(int E) { return WARPS * (E <= 64 ? 4 : E <= 128 ? 2 : 1); }
-int blocks_for(int T, int E) {
-  const int per = tokens_per_block(E);
-  return static_cast<int>(std::max(1LL, std::min<long long>((static_cast<long long>(T) + per - 1) / per, MAX_BLOCKS)));
+template <typename T, bool VEC>
+moe_status_t by_width_fwd(const GateArgs& a, Width w, int blocks, cudaStream_t s) {
+  if constexpr (VEC) {
+    if (w.lists == 2 && w.lanes == 8) return launch_fwd<T, 2, 8, VEC>(a, blocks, s);
+    if (w.lists == 2 && w.lanes == 16) return launch_fwd<T, 2, 16, VEC>(a, blocks, s);
+    if (w.lists == 4 && w.lanes == 16) return launch_fwd<T, 4, 16, VEC>(a, blocks, s);
+  }
+  if (w.lanes == 8) return launch_fwd<T, 1, 8, VEC>(a, blocks, s);
+  if (w.lanes == 16) return launch_fwd<T, 1, 16, VEC>(a, blocks, s);
+  if (w.lists == 1) return launch_fwd<T, 1, 32, VEC>(a, blocks, s);
+  if (w.lists == 2) return launch_fwd<T, 2, 32, VEC>(a, blocks, s);
+  return launch_fwd<T, 4, 32, VEC>(a, blocks, s);
+}
+template <typename T, bool VEC>
+moe_status_t by_width_bwd(const GateBwdArgs& a, Width w, int blocks, cudaStream_t s) {
+  if (w.lanes == 8) return launch_bwd<T, 1, 8, VEC>(a, blocks, s);
+  if (w.lanes == 16) return launch_bwd<T, 1, 16, VEC>(a, blocks, s);
+  if (w.lists == 1) return launch_bwd<T, 1, 32, VEC>(a, blocks, s);
+  if (w.lists == 2) return launch_bwd<T, 2, 32, VEC>(a, blocks, s);
+  return launch_bwd<T, 4, 32, VEC>(a, blocks, s);
+}
+
+// blocks for tokens of `lanes` lanes each
+int blocks_for(int T, int lanes, int most) {
+  const int per = WARPS * (32 / lanes);
+  return static_cast<int>(std::max(1LL, std::min<long long>((static_cast<long long>(T) + per - 1) / per, most)));
 }
 
 bool dtype_ok(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
@@ -561,16 +616,11 @@ bool rows16(const void* p, long long ld, int E, int dtype) {
   return aligned(p, 16) && E % 8 == 0 && ld % (dtype == MOE_DTYPE_BF16 ? 8 : 4) == 0;
 }
 
-moe_status_t launched() {
-  const cudaError_t err = cudaGetLastError();
-  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
-}
-
 }  // namespace
 
 // the blocks' partial rows, then the statistics kernel's block counter and shares
 size_t gate_workspace_bytes(int T, int E) {
-  return (static_cast<size_t>(blocks_for(T, E)) * part_words(E) + 1 + 32) * sizeof(float);
+  return (static_cast<size_t>(blocks_for(T, 32, MAX_BLOCKS)) * part_words(E) + 1 + 32) * sizeof(float);
 }
 
 }  // namespace moe
@@ -612,12 +662,13 @@ moe_status_t moe_gate_fwd(const void* logits, int dtype, long long ld, const uin
   a.weights = weights;
   a.lse = lse;
   a.part = stats ? static_cast<float*>(ws) : nullptr;
-  const int blocks = blocks_for(T, E);
-  a.ticket = stats ? static_cast<unsigned*>(ws) + static_cast<size_t>(blocks) * part_words(E) : nullptr;
   const bool vec = rows16(logits, ld, E, dtype);
-  if (dtype == MOE_DTYPE_BF16) vec ? by_width_fwd<bf16, true>(a, blocks, s) : by_width_fwd<bf16, false>(a, blocks, s);
-  else vec ? by_width_fwd<float, true>(a, blocks, s) : by_width_fwd<float, false>(a, blocks, s);
-  if ((st = launched()) != MOE_OK || !stats) return st;
+  const Width w = width_for(E, vec && T >= MAX_BLOCKS * WARPS);
+  const int blocks = blocks_for(T, w.lanes, MAX_BLOCKS);
+  a.ticket = stats ? static_cast<unsigned*>(ws) + static_cast<size_t>(blocks) * part_words(E) : nullptr;
+  if (dtype == MOE_DTYPE_BF16) st = vec ? by_width_fwd<bf16, true>(a, w, blocks, s) : by_width_fwd<bf16, false>(a, w, blocks, s);
+  else st = vec ? by_width_fwd<float, true>(a, w, blocks, s) : by_width_fwd<float, false>(a, w, blocks, s);
+  if (st != MOE_OK || !stats) return st;
   gate_stats_kernel<<<(E + 31) / 32, 1024, 0, s>>>(a.part, blocks, top_k, E, counts, n_valid, prob_sum, loss, a.ticket,
                                                    reinterpret_cast<float*>(a.ticket + 1));
   return launched();
@@ -657,12 +708,12 @@ moe_status_t moe_gate_bwd(const void* logits, int dtype, long long ld, const flo
   a.renorm = (flags & MOE_GATE_RENORM) != 0;
   a.dlogits = dlogits;
   a.ldd = ldd;
-  const int blocks = blocks_for(T, E);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool vec = rows16(logits, ld, E, dtype) && rows16(dlogits, ldd, E, dtype);
-  if (dtype == MOE_DTYPE_BF16) vec ? by_width_bwd<bf16, true>(a, blocks, s) : by_width_bwd<bf16, false>(a, blocks, s);
-  else vec ? by_width_bwd<float, true>(a, blocks, s) : by_width_bwd<float, false>(a, blocks, s);
-  return launched();
+  const Width w = width_for(E, false);
+  const int blocks = blocks_for(T, w.lanes, BWD_BLOCKS);
+  if (dtype == MOE_DTYPE_BF16) return vec ? by_width_bwd<bf16, true>(a, w, blocks, s) : by_width_bwd<bf16, false>(a, w, blocks, s);
+  return vec ? by_width_bwd<float, true>(a, w, blocks, s) : by_width_bwd<float, false>(a, w, blocks, s);
 }
 
 }  // extern "C"

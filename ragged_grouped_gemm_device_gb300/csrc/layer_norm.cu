@@ -9,7 +9,10 @@
 // x and dy and write dx. A row is held in the registers of the TPR threads that own it, so each
 // value is read once and the variance is the exact two-pass one (the sum of squared differences
 // from the mean, not a difference of two large sums). All arithmetic is fp32; y and dx are rounded
-// once. The weight gradients are sums over all rows: each block adds the rows it owns in
+// once. The forward gives a row to one warp as long as it fits (eight chunks a lane, 2048 bf16):
+// no barriers, and the weights come from L1, which they stay in. The backward gives it to as many
+// threads as it has 16-byte chunks, which keeps the weight, the two gradients' sums and the next
+// row's loads in registers. The weight gradients are sums over all rows: each block adds the rows it owns in
 // registers (a thread always owns the same columns), leaves one partial row of each gradient in
 // the workspace, and a second small kernel adds the partials in block order. No atomics: the
 // results do not depend on scheduling.
@@ -211,17 +214,20 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_kernel(const Norm
   __shared__ float2 red[2][32];
   const int t = threadIdx.x % TPR;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  float dg[NCH][VB], db[NCH][VB];
+  float dg[NCH][VB], db[NCH][VB], g[NCH][VB];
 #pragma unroll
-  for (int i = 0; i < NCH; ++i)
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (i * TPR + t) * VB;
+    if (c < a.d) load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g[i]);
 #pragma unroll
     for (int j = 0; j < VB; ++j) dg[i][j] = db[i][j] = 0.f;
-  int par = 0;
-  for (long long row = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / TPR; row < a.T;
-       row += static_cast<long long>(gridDim.x) * ROWS) {
+  }
+  // the next row's loads are in flight while this one is worked on
+  Chunk<T, VB> qx[NCH], qd[NCH];
+  float mean = 0.f, rstd = 0.f;
+  auto fetch = [&](long long row) {
     const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
     const T* dr = static_cast<const T*>(a.dy) + row * a.lddy;
-    Chunk<T, VB> qx[NCH], qd[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (i * TPR + t) * VB;
@@ -230,19 +236,32 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_kernel(const Norm
         qd[i].load(dr + c);
       }
     }
-    const float mean = __ldg(a.mean + row), rstd = __ldg(a.rstd + row);
+    mean = __ldg(a.mean + row);
+    rstd = __ldg(a.rstd + row);
+  };
+  const long long step = static_cast<long long>(gridDim.x) * ROWS;
+  long long row = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / TPR;
+  if (row < a.T) fetch(row);
+  int par = 0;
+  for (; row < a.T; row += step) {
+    Chunk<T, VB> cx[NCH], cd[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      cx[i] = qx[i];
+      cd[i] = qd[i];
+    }
+    const float mu = mean, rs = rstd;
+    if (row + step < a.T) fetch(row + step);
     float s1 = 0.f, s2 = 0.f;  // sums of gamma dy and of gamma dy xhat
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = (i * TPR + t) * VB;
-      if (c >= a.d) continue;
-      float fx[VB], fd[VB], g[VB];
-      qx[i].unpack(fx);
-      qd[i].unpack(fd);
-      load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g);
+      if ((i * TPR + t) * VB >= a.d) continue;
+      float fx[VB], fd[VB];
+      cx[i].unpack(fx);
+      cd[i].unpack(fd);
 #pragma unroll
       for (int j = 0; j < VB; ++j) {
-        const float xh = (fx[j] - mean) * rstd, gd = g[j] * fd[j];
+        const float xh = (fx[j] - mu) * rs, gd = g[i][j] * fd[j];
         s1 += gd;
         s2 = fmaf(gd, xh, s2);
         dg[i][j] = fmaf(fd[j], xh, dg[i][j]);
@@ -257,15 +276,11 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_kernel(const Norm
     for (int i = 0; i < NCH; ++i) {
       const int c = (i * TPR + t) * VB;
       if (c >= a.d) continue;
-      float fx[VB], fd[VB], g[VB];
-      qx[i].unpack(fx);
-      qd[i].unpack(fd);
-      load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g);
+      float fx[VB], fd[VB];
+      cx[i].unpack(fx);
+      cd[i].unpack(fd);
 #pragma unroll
-      for (int j = 0; j < VB; ++j) {
-        const float xh = (fx[j] - mean) * rstd;
-        fx[j] = rstd * (fmaf(g[j], fd[j], -m1) - xh * m2);
-      }
+      for (int j = 0; j < VB; ++j) fx[j] = rs * (fmaf(g[i][j], fd[j], -m1) - (fx[j] - mu) * rs * m2);
       Chunk<T, VB>::store(orow + c, fx);
     }
   }
@@ -405,22 +420,24 @@ __global__ void __launch_bounds__(256) norm_wgrad_wide_kernel(const NormArgs a) 
   pg[a.d + c] = b;
 }
 
-// out[c] = sum of the partials of column c in block order, for both gradients: 32 columns a
-// block, 16 threads a column that take every 16th partial and are added in thread order.
-__global__ void __launch_bounds__(512) norm_partials_kernel(const float* __restrict__ part, int blocks, int d,
-                                                            float* __restrict__ dgamma, float* __restrict__ dbeta) {
-  __shared__ float acc[16][32];
+// out[c] = sum of the partials of column c, for both gradients: 32 columns a block, 32 threads a
+// column that take every 32nd partial and are added in thread order.
+__global__ void __launch_bounds__(1024) norm_partials_kernel(const float* __restrict__ part, int blocks, int d,
+                                                             float* __restrict__ dgamma, float* __restrict__ dbeta) {
+  __shared__ float acc[32][33];
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + cx;  // of 2d: dgamma's, then dbeta's columns
   float s = 0.f;
-  if (c < 2LL * d)
-    for (int r = ry; r < blocks; r += 16) s += part[static_cast<size_t>(r) * 2 * d + c];
+  if (c < 2LL * d) {
+#pragma unroll 10
+    for (int r = ry; r < blocks; r += 32) s += __ldcs(part + static_cast<size_t>(r) * 2 * d + c);
+  }
   acc[ry][cx] = s;
   __syncthreads();
   if (ry == 0 && c < 2LL * d) {
     float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) sum += acc[r][cx];
+    for (int r = 0; r < 32; ++r) sum += acc[r][cx];
     float* out = c < d ? dgamma : dbeta;
     if (out != nullptr) out[c < d ? c : c - d] = sum;
   }
@@ -434,39 +451,57 @@ moe_status_t launched() {
 }
 
 template <typename T, int VB, int NCH, int TPR>
-int launch_row_kernel(const NormArgs& a, bool bwd, cudaStream_t s) {
+int launch_fwd_rows(const NormArgs& a, cudaStream_t s) {
   constexpr int ROWS = block_threads(TPR) / TPR;
-  const long long groups = (static_cast<long long>(a.T) + ROWS - 1) / ROWS;
-  if (bwd) {
-    const int grid = static_cast<int>(std::min<long long>(groups, BWD_MAX_BLOCKS));
-    norm_bwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), 0, s>>>(a);
-    return grid;
-  }
-  const int grid = static_cast<int>(std::min<long long>(groups, 1 << 20));
+  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, 1 << 20));
   norm_fwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), 0, s>>>(a);
   return grid;
 }
+template <typename T, int VB, int NCH, int TPR>
+int launch_bwd_rows(const NormArgs& a, cudaStream_t s) {
+  constexpr int ROWS = block_threads(TPR) / TPR;
+  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, BWD_MAX_BLOCKS));
+  norm_bwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), 0, s>>>(a);
+  return grid;
+}
 
-// Threads per row and chunks per thread: the fewest threads that hold the row in at most four
-// 16-byte chunks each (sixteen elements without alignment), so that narrow rows need no shared
-// memory and wide ones keep their registers. Returns the blocks launched, 0 for a row wider than
-// any of them.
-template <typename T, int VB, int N1, int N2, int N3>
-int launch_by_width(const NormArgs& a, bool bwd, cudaStream_t s) {
+// Threads per row and chunks (16 bytes, or one element) per thread. The functions return the blocks
+// launched, 0 for a row wider than any layout.
+// Forward: a warp a row up to eight chunks a lane; fewer rows than four for each SM take four
+// warps a row from three chunks a lane on, for latency.
+template <typename T, int VB, int U>
+int fwd_by_width(const NormArgs& a, cudaStream_t s) {
   const int chunks = (a.d + VB - 1) / VB;
-  if (chunks <= 32 * N1) return launch_row_kernel<T, VB, N1, 32>(a, bwd, s);
-  if (chunks <= 32 * N2) return launch_row_kernel<T, VB, N2, 32>(a, bwd, s);
-  if (chunks <= 128 * N2) return launch_row_kernel<T, VB, N2, 128>(a, bwd, s);
-  if (chunks <= 128 * N3) return launch_row_kernel<T, VB, N3, 128>(a, bwd, s);
-  if (chunks <= 512 * N2) return launch_row_kernel<T, VB, N2, 512>(a, bwd, s);
-  if (chunks <= 512 * N3) return launch_row_kernel<T, VB, N3, 512>(a, bwd, s);
+  const bool few = a.T <= 608;
+  if (chunks <= 32 * U) return launch_fwd_rows<T, VB, U, 32>(a, s);
+  if (chunks <= 64 * U) return launch_fwd_rows<T, VB, 2 * U, 32>(a, s);
+  if (few && chunks <= 256 * U) return launch_fwd_rows<T, VB, 2 * U, 128>(a, s);
+  if (chunks <= 128 * U) return launch_fwd_rows<T, VB, 4 * U, 32>(a, s);
+  if (U == 1 && chunks <= 256) return launch_fwd_rows<T, VB, 8, 32>(a, s);
+  if (chunks <= 512 * U) return launch_fwd_rows<T, VB, 4 * U, 128>(a, s);
+  if (chunks <= 1024 * U) return launch_fwd_rows<T, VB, 2 * U, 512>(a, s);
+  if (chunks <= 2048 * U) return launch_fwd_rows<T, VB, 4 * U, 512>(a, s);
+  return 0;
+}
+// Backward: one chunk a thread (four elements without alignment) as long as a block has the threads.
+template <typename T, int VB, int U>
+int bwd_by_width(const NormArgs& a, cudaStream_t s) {
+  const int chunks = (a.d + VB - 1) / VB;
+  if (chunks <= 32 * U) return launch_bwd_rows<T, VB, U, 32>(a, s);
+  if (chunks <= 64 * U) return launch_bwd_rows<T, VB, 2 * U, 32>(a, s);
+  if (chunks <= 128 * U) return launch_bwd_rows<T, VB, U, 128>(a, s);
+  if (chunks <= 256 * U) return launch_bwd_rows<T, VB, U, 256>(a, s);
+  if (chunks <= 512 * U) return launch_bwd_rows<T, VB, U, 512>(a, s);
+  if (chunks <= 1024 * U) return launch_bwd_rows<T, VB, U, 1024>(a, s);
+  if (U == 1 && chunks <= 2048) return launch_bwd_rows<T, VB, 4, 512>(a, s);
   return 0;
 }
 
 template <typename T>
 int launch_norm(const NormArgs& a, bool bwd, bool vec, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int grid = vec ? launch_by_width<T, V, 1, 2, 4>(a, bwd, s) : launch_by_width<T, 1, 4, 8, 16>(a, bwd, s);
+  const int grid = bwd ? (vec ? bwd_by_width<T, V, 1>(a, s) : bwd_by_width<T, 1, 4>(a, s))
+                       : (vec ? fwd_by_width<T, V, 1>(a, s) : fwd_by_width<T, 1, 4>(a, s));
   if (grid > 0) return grid;
   const int wide = static_cast<int>(std::min<long long>(a.T, 1 << 20));
   if (!bwd) {
@@ -578,7 +613,7 @@ moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, l
     if ((st = launched()) != MOE_OK) return st;
   }
   if (!wgrad) return MOE_OK;
-  norm_partials_kernel<<<(2 * d + 31) / 32, 512, 0, s>>>(static_cast<const float*>(ws), blocks, d, dgamma, dbeta);
+  norm_partials_kernel<<<(2 * d + 31) / 32, 1024, 0, s>>>(static_cast<const float*>(ws), blocks, d, dgamma, dbeta);
   return launched();
 }
 
