@@ -9,13 +9,15 @@
 // x and dy and write dx. A row is held in the registers of the TPR threads that own it, so each
 // value is read once and the variance is the exact two-pass one (the sum of squared differences
 // from the mean, not a difference of two large sums). All arithmetic is fp32; y and dx are rounded
-// once. The forward gives a row to one warp as long as it fits (eight chunks a lane, 2048 bf16):
-// no barriers, and the weights come from L1, which they stay in. The backward gives it to as many
-// threads as it has 16-byte chunks, which keeps the weight, the two gradients' sums and the next
-// row's loads in registers. The weight gradients are sums over all rows: each block adds the rows it owns in
-// registers (a thread always owns the same columns), leaves one partial row of each gradient in
-// the workspace, and a second small kernel adds the partials in block order. No atomics: the
-// results do not depend on scheduling.
+// once. A block works on one row after another: the weights (and the backward's gradient sums) stay
+// in its registers, and the next rows are on their way into shared memory by asynchronous
+// copies. Each thread copies exactly the chunks that it will read, so the ring needs no barrier;
+// what it is for is bytes in flight, which registers cannot hold (with one row of prefetch in
+// registers the backward took 47 us for 16384 x 2048 bf16, 41.5 now).
+// The weight gradients are sums over all rows: each block adds the rows it owns in registers (a
+// thread always owns the same columns), leaves one partial row of each gradient in the workspace,
+// and a second small kernel adds the partials in block order. No atomics: the results do not
+// depend on scheduling.
 #include <algorithm>
 #include <cmath>
 
@@ -26,8 +28,8 @@
 namespace moe {
 namespace {
 
-// Blocks of the backward at most, and so rows of partial weight gradients: four for each of the
-// 152 SMs. A constant, because the size of the workspace is host arithmetic.
+// Rows of partial weight gradients at most: four for each of the 152 SMs. A constant, because the
+// size of the workspace is host arithmetic.
 constexpr int BWD_MAX_BLOCKS = 608;
 constexpr int MAX_WIDTH = 1 << 20;
 
@@ -38,6 +40,9 @@ struct Chunk;
 template <>
 struct Chunk<bf16, 8> {
   uint4 v;
+  __device__ __forceinline__ void from_shared(uint32_t a) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  }
   __device__ __forceinline__ void load(const bf16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void unpack(float (&f)[8]) const {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -55,6 +60,9 @@ struct Chunk<bf16, 8> {
 template <>
 struct Chunk<float, 4> {
   float4 v;
+  __device__ __forceinline__ void from_shared(uint32_t a) {
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  }
   __device__ __forceinline__ void load(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
   __device__ __forceinline__ void unpack(float (&f)[4]) const {
     f[0] = v.x;
@@ -87,53 +95,163 @@ __device__ __forceinline__ void load_weight(const void* w, bool w_bf16, int c, f
   if (w == nullptr) {
 #pragma unroll
     for (int i = 0; i < VB; ++i) o[i] = fill;
+  } else if constexpr (VB == 1) {
+    o[0] = w_bf16 ? __bfloat162float(static_cast<const bf16*>(w)[c]) : __ldg(static_cast<const float*>(w) + c);
   } else if (w_bf16) {
-    if constexpr (VB == 8) {
-      Chunk<bf16, 8> q;
-      q.load(static_cast<const bf16*>(w) + c);
-      q.unpack(o);
-    } else {
 #pragma unroll
-      for (int i = 0; i < VB; ++i) o[i] = __bfloat162float(static_cast<const bf16*>(w)[c + i]);
+    for (int i = 0; i < VB; i += 4) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(static_cast<const bf16*>(w) + c + i));
+      o[i] = bf16_lo(q.x);
+      o[i + 1] = bf16_hi(q.x);
+      o[i + 2] = bf16_lo(q.y);
+      o[i + 3] = bf16_hi(q.y);
     }
   } else {
-    if constexpr (VB % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < VB; i += 4) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + i));
-        o[i] = q.x;
-        o[i + 1] = q.y;
-        o[i + 2] = q.z;
-        o[i + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VB; ++i) o[i] = __ldg(static_cast<const float*>(w) + c + i);
+    for (int i = 0; i < VB; i += 4) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + i));
+      o[i] = q.x;
+      o[i + 1] = q.y;
+      o[i + 2] = q.z;
+      o[i + 3] = q.w;
     }
   }
 }
 
-// Sum of a (and b) over the TPR threads of a row. For rows wider than a warp, `buf` is one of two
-// alternating buffers: a thread that is a reduction ahead writes the other one.
-template <int TPR>
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* buf) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
-  }
-  if constexpr (TPR == 32) return make_float2(a, b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (lane == 0) buf[warp] = make_float2(a, b);
-  __syncthreads();
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < TPR / 32; ++w) {
-    s.x += buf[w].x;
-    s.y += buf[w].y;
-  }
-  return s;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
+
+// Sum over the TPR threads of a row. For rows wider than a warp, `buf` is one of two alternating
+// buffers: a thread that is a reduction ahead writes the other one.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float a, float* buf) {
+  a = warp_sum(a);
+  if constexpr (TPR == 32) {
+    return a;
+  } else {
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = a;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < TPR / 32; w += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(buf + w);
+      s += (q.x + q.y) + (q.z + q.w);
+    }
+    return s;
+  }
+}
+
+// ... of a and b: the lower half of the warp adds up a, the upper half b
+template <int TPR>
+__device__ __forceinline__ float2 row_sum(float a, float b, float* buf) {
+  const bool up = (threadIdx.x & 16) != 0;
+  float v = (up ? b : a) + __shfl_xor_sync(0xffffffffu, up ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (TPR == 32) {
+    return make_float2(__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16));
+  } else {
+    if ((threadIdx.x & 15) == 0) buf[(up ? TPR / 32 : 0) + (threadIdx.x >> 5)] = v;
+    __syncthreads();
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < TPR / 32; w += 4) {
+      const float4 p = *reinterpret_cast<const float4*>(buf + w), q = *reinterpret_cast<const float4*>(buf + TPR / 32 + w);
+      s.x += (p.x + p.y) + (p.z + p.w);
+      s.y += (q.x + q.y) + (q.z + q.w);
+    }
+    return s;
+  }
+}
+
+// threads of a block: a row's TPR, or four rows of one warp each
+__host__ __device__ constexpr int block_threads(int tpr) { return tpr == 32 ? 128 : tpr; }
+
+// Blocks on an SM, which size the grids and bound the registers. Forward: 768 threads (16384 x 2048
+// bf16: 20.8 us, the speed of a copy; 27 us with 1024, which spill). Backward: 384 threads with two
+// chunks each (41.5 us; one chunk each on 512 threads 44 us, on 1024 threads 54 us: each
+// row's reduction and addresses cost a warp as much as its chunks).
+constexpr int fwd_blocks_per_sm(int tpr) { return tpr >= 512 ? 1 : 768 / block_threads(tpr); }
+constexpr int bwd_blocks_per_sm(int tpr) { return tpr <= 128 ? 3 : tpr == 256 ? 2 : 1; }
+
+// Asynchronous 16-byte copy global -> shared, and the group it is waited for by.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// The chunks of one thread in the next rows of NT tensors (x; x and dy). 16-byte rows: a ring of
+// asynchronous copies in shared memory; rows of single elements: one row ahead in registers. The
+// row pointers advance by a constant, so that a row costs few address instructions.
+template <typename T, int VB, int NCH, int TPR, int NT>
+struct Feed {
+  static constexpr bool ring = VB > 1;
+  static constexpr int piece = block_threads(TPR) * 16;  // one chunk of every thread
+  static constexpr int slot_bytes = NT * NCH * piece;
+  static constexpr int depth = !ring ? 1 : slot_bytes <= 32 * 1024 ? 4 : 2;  // rows on their way
+  static constexpr int smem_bytes = ring ? depth * slot_bytes : 0;
+  Chunk<T, VB> q[NT][NCH];
+  const T* at[NT];       // the next row to start
+  long long step[NT];    // elements from one row of this block to its next
+  int c0;                // this thread's first column
+  uint32_t base, slot;   // shared-memory address of this thread, byte offset of the oldest row
+  int left;              // rows not started yet
+  bool in[NCH];
+
+  __device__ __forceinline__ void init(uint8_t* smem, int t, int d, int rows) {
+    if constexpr (ring) base = smem_u32(smem) + threadIdx.x * 16;
+    slot = 0;
+    left = rows;
+    c0 = t * VB;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) in[i] = (i * TPR + t) * VB < d;
+  }
+  // start the copies of the next row into the slot at byte offset `to` (past the last row: none,
+  // but a group of copies all the same)
+  __device__ __forceinline__ void start(uint32_t to) {
+    if (left > 0) {
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          if (!in[i]) continue;
+          if constexpr (ring) copy16_async(base + to + (k * NCH + i) * piece, at[k] + c0 + i * (TPR * VB));
+          else q[k][i].load(at[k] + c0 + i * (TPR * VB));
+        }
+        at[k] += step[k];
+      }
+      --left;
+    }
+    if constexpr (ring) copy_commit();
+  }
+  __device__ __forceinline__ void prime() {
+#pragma unroll
+    for (int s = 0; s < depth; ++s) start(s * slot_bytes);
+  }
+  // the oldest row's copies have landed: its chunks into q
+  __device__ __forceinline__ void take() {
+    if constexpr (ring) {
+      copy_wait<depth - 1>();
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+          if (in[i]) q[k][i].from_shared(base + slot + (k * NCH + i) * piece);
+    }
+  }
+  // q has been unpacked: start the row that takes its place
+  __device__ __forceinline__ void next() {
+    start(slot);
+    slot = slot == (depth - 1) * slot_bytes ? 0 : slot + slot_bytes;
+  }
+};
 
 struct NormArgs {
   const void* x;
@@ -150,69 +268,76 @@ struct NormArgs {
   float* part;         // backward: [blocks][2][d] partial dgamma, dbeta (nullable: not wanted)
 };
 
-// threads of a block: a row's TPR, or four rows of one warp each
-constexpr int block_threads(int tpr) { return tpr == 32 ? 128 : tpr; }
-
 template <typename T, int VB, int NCH, int TPR>
-__global__ void __launch_bounds__(block_threads(TPR)) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(block_threads(TPR), fwd_blocks_per_sm(TPR)) norm_fwd_kernel(const NormArgs a) {
   constexpr int ROWS = block_threads(TPR) / TPR;
-  __shared__ float2 red[2][32];
-  const int t = threadIdx.x % TPR;
+  __shared__ __align__(16) float red[2][32];
+  const int t = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  for (long long row = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / TPR; row < a.T;
-       row += static_cast<long long>(gridDim.x) * ROWS) {
-    const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
-    Chunk<T, VB> q[NCH];
+  float g[NCH][VB], b[NCH][VB];
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = (i * TPR + t) * VB;
-      if (c < a.d) q[i].load(xr + c);
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (i * TPR + t) * VB;
+    if (c < a.d) {
+      load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g[i]);
+      load_weight<VB>(a.beta, a.w_bf16, c, 0.0f, b[i]);
     }
+  }
+  extern __shared__ __align__(16) uint8_t ring[];
+  Feed<T, VB, NCH, TPR, 1> feed;
+  const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
+  const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
+  feed.init(ring, t, a.d, rows);
+  feed.at[0] = static_cast<const T*>(a.x) + row0 * a.ldx;
+  feed.step[0] = step * a.ldx;
+  feed.prime();
+  T* yr = static_cast<T*>(a.out) + row0 * a.ldo;
+  const long long ystep = step * a.ldo;
+  for (int k = 0; k < rows; ++k, yr += ystep) {
+    float f[NCH][VB];
     float sum = 0.f;
+    feed.take();
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (feed.in[i]) feed.q[0][i].unpack(f[i]);
+    feed.next();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      if ((i * TPR + t) * VB >= a.d) continue;
-      float f[VB];
-      q[i].unpack(f);
+      if (!feed.in[i]) continue;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) sum += f[j];
+      for (int j = 0; j < VB; ++j) sum += f[i][j];
     }
-    const float mean = row_sum<TPR>(sum, 0.f, red[0]).x * inv_d;
+    const float mean = row_sum<TPR>(sum, red[0]) * inv_d;
     float sq = 0.f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      if ((i * TPR + t) * VB >= a.d) continue;
-      float f[VB];
-      q[i].unpack(f);
+      if (!feed.in[i]) continue;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) sq = fmaf(f[j] - mean, f[j] - mean, sq);
+      for (int j = 0; j < VB; ++j) {
+        f[i][j] -= mean;
+        sq = fmaf(f[i][j], f[i][j], sq);
+      }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, 0.f, red[1]).x * inv_d + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(sq, red[1]) * inv_d + a.eps);
     if (t == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
+      if (a.mean) a.mean[row0 + static_cast<long long>(k) * step] = mean;
+      if (a.rstd) a.rstd[row0 + static_cast<long long>(k) * step] = rstd;
     }
-    T* yr = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = (i * TPR + t) * VB;
-      if (c >= a.d) continue;
-      float f[VB], g[VB], b[VB];
-      q[i].unpack(f);
-      load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g);
-      load_weight<VB>(a.beta, a.w_bf16, c, 0.0f, b);
+      if (!feed.in[i]) continue;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) f[j] = fmaf((f[j] - mean) * rstd, g[j], b[j]);
-      Chunk<T, VB>::store(yr + c, f);
+      for (int j = 0; j < VB; ++j) f[i][j] = fmaf(f[i][j] * rstd, g[i][j], b[i][j]);
+      Chunk<T, VB>::store(yr + feed.c0 + i * (TPR * VB), f[i]);
     }
   }
 }
 
 template <typename T, int VB, int NCH, int TPR>
-__global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(block_threads(TPR), bwd_blocks_per_sm(TPR)) norm_bwd_kernel(const NormArgs a) {
   constexpr int ROWS = block_threads(TPR) / TPR;
-  __shared__ float2 red[2][32];
-  const int t = threadIdx.x % TPR;
+  __shared__ __align__(16) float red[2][64];
+  const int t = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
   const float inv_d = 1.0f / static_cast<float>(a.d);
   float dg[NCH][VB], db[NCH][VB], g[NCH][VB];
 #pragma unroll
@@ -222,106 +347,92 @@ __global__ void __launch_bounds__(block_threads(TPR)) norm_bwd_kernel(const Norm
 #pragma unroll
     for (int j = 0; j < VB; ++j) dg[i][j] = db[i][j] = 0.f;
   }
-  // the next row's loads are in flight while this one is worked on
-  Chunk<T, VB> qx[NCH], qd[NCH];
-  float mean = 0.f, rstd = 0.f;
-  auto fetch = [&](long long row) {
-    const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
-    const T* dr = static_cast<const T*>(a.dy) + row * a.lddy;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      const int c = (i * TPR + t) * VB;
-      if (c < a.d) {
-        qx[i].load(xr + c);
-        qd[i].load(dr + c);
-      }
-    }
-    mean = __ldg(a.mean + row);
-    rstd = __ldg(a.rstd + row);
-  };
-  const long long step = static_cast<long long>(gridDim.x) * ROWS;
-  long long row = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / TPR;
-  if (row < a.T) fetch(row);
+  extern __shared__ __align__(16) uint8_t ring[];
+  Feed<T, VB, NCH, TPR, 2> feed;
+  const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
+  const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
+  feed.init(ring, t, a.d, rows);
+  feed.at[0] = static_cast<const T*>(a.x) + row0 * a.ldx;
+  feed.step[0] = step * a.ldx;
+  feed.at[1] = static_cast<const T*>(a.dy) + row0 * a.lddy;
+  feed.step[1] = step * a.lddy;
+  feed.prime();
+  T* orow = static_cast<T*>(a.out) + row0 * a.ldo;
+  const long long ostep = step * a.ldo;
+  // lane l holds the statistics of rows l, l + 32, ... of this block: one wait in 32 rows
+  const int lane = threadIdx.x & 31;
+  float mean32 = 0.f, rstd32 = 0.f;
   int par = 0;
-  for (; row < a.T; row += step) {
-    Chunk<T, VB> cx[NCH], cd[NCH];
-#pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      cx[i] = qx[i];
-      cd[i] = qd[i];
+  for (int k = 0; k < rows; ++k, orow += ostep) {
+    float xh[NCH][VB], gd[NCH][VB];  // xhat, and dy, then gamma dy
+    float s1 = 0.f, s2 = 0.f;
+    if ((k & 31) == 0 && k + lane < rows) {
+      mean32 = __ldg(a.mean + row0 + static_cast<long long>(k + lane) * step);
+      rstd32 = __ldg(a.rstd + row0 + static_cast<long long>(k + lane) * step);
     }
-    const float mu = mean, rs = rstd;
-    if (row + step < a.T) fetch(row + step);
-    float s1 = 0.f, s2 = 0.f;  // sums of gamma dy and of gamma dy xhat
+    const float mu = __shfl_sync(0xffffffffu, mean32, k & 31), rs = __shfl_sync(0xffffffffu, rstd32, k & 31);
+    feed.take();
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (feed.in[i]) {
+        feed.q[0][i].unpack(xh[i]);
+        feed.q[1][i].unpack(gd[i]);
+      }
+    feed.next();
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      if ((i * TPR + t) * VB >= a.d) continue;
-      float fx[VB], fd[VB];
-      cx[i].unpack(fx);
-      cd[i].unpack(fd);
+      if (!feed.in[i]) continue;
 #pragma unroll
       for (int j = 0; j < VB; ++j) {
-        const float xh = (fx[j] - mu) * rs, gd = g[i][j] * fd[j];
-        s1 += gd;
-        s2 = fmaf(gd, xh, s2);
-        dg[i][j] = fmaf(fd[j], xh, dg[i][j]);
-        db[i][j] += fd[j];
+        xh[i][j] = (xh[i][j] - mu) * rs;
+        dg[i][j] = fmaf(gd[i][j], xh[i][j], dg[i][j]);
+        db[i][j] += gd[i][j];
+        gd[i][j] *= g[i][j];
+        s1 += gd[i][j];
+        s2 = fmaf(gd[i][j], xh[i][j], s2);
       }
     }
     const float2 s = row_sum<TPR>(s1, s2, red[par]);
     par ^= 1;
+    // dx = rstd (gd - m1 - xhat m2)
     const float m1 = s.x * inv_d, m2 = s.y * inv_d;
-    T* orow = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = (i * TPR + t) * VB;
-      if (c >= a.d) continue;
-      float fx[VB], fd[VB];
-      cx[i].unpack(fx);
-      cd[i].unpack(fd);
+      if (!feed.in[i]) continue;
 #pragma unroll
-      for (int j = 0; j < VB; ++j) fx[j] = rs * (fmaf(g[i][j], fd[j], -m1) - (fx[j] - mu) * rs * m2);
-      Chunk<T, VB>::store(orow + c, fx);
+      for (int j = 0; j < VB; ++j) xh[i][j] = rs * (gd[i][j] - m1 - xh[i][j] * m2);
+      Chunk<T, VB>::store(orow + feed.c0 + i * (TPR * VB), xh[i]);
     }
   }
   if (a.part == nullptr) return;
   float* pg = a.part + static_cast<size_t>(blockIdx.x) * 2 * a.d;
   float* pb = pg + a.d;
-  if constexpr (ROWS == 1) {
+  // a block of several rows: its warps own the same columns; they are added in warp order
+  __shared__ float2 acc[ROWS > 1 ? ROWS - 1 : 1][32];
+  const int w = threadIdx.x / TPR;
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
+  for (int i = 0; i < NCH; ++i)
 #pragma unroll
-      for (int j = 0; j < VB; ++j) {
-        const int c = (i * TPR + t) * VB + j;
-        if (c < a.d) {
-          pg[c] = dg[i][j];
-          pb[c] = db[i][j];
-        }
-      }
-  } else {
-    // the block's warps own different rows of the same columns: add them in warp order
-    __shared__ float2 acc[ROWS - 1][32];
-    const int w = threadIdx.x / TPR;
-#pragma unroll
-    for (int i = 0; i < NCH; ++i)
-#pragma unroll
-      for (int j = 0; j < VB; ++j) {
-        const int c = (i * TPR + t) * VB + j;
+    for (int j = 0; j < VB; ++j) {
+      float vg = dg[i][j], vb = db[i][j];
+      if constexpr (ROWS > 1) {
         __syncthreads();
-        if (w > 0) acc[w - 1][t] = make_float2(dg[i][j], db[i][j]);
+        if (w > 0) acc[w - 1][t] = make_float2(vg, vb);
         __syncthreads();
-        if (w == 0 && c < a.d) {
-          float g = dg[i][j], b = db[i][j];
+        if (w == 0) {
 #pragma unroll
           for (int r = 0; r < ROWS - 1; ++r) {
-            g += acc[r][t].x;
-            b += acc[r][t].y;
+            vg += acc[r][t].x;
+            vb += acc[r][t].y;
           }
-          pg[c] = g;
-          pb[c] = b;
         }
       }
-  }
+      const int c = (i * TPR + t) * VB + j;
+      if (w == 0 && c < a.d) {
+        pg[c] = vg;
+        pb[c] = vb;
+      }
+    }
 }
 
 // Rows too wide for registers: three passes over the row (the later ones from L2), one block a row.
@@ -329,7 +440,7 @@ constexpr int WIDE_THREADS = 1024;
 
 template <typename T>
 __global__ void __launch_bounds__(WIDE_THREADS) norm_fwd_wide_kernel(const NormArgs a) {
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float red[2][32];
   const float inv_d = 1.0f / static_cast<float>(a.d);
   for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
     const T* xr = static_cast<const T*>(a.x) + row * a.ldx;
@@ -341,14 +452,14 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_fwd_wide_kernel(const NormA
       q.unpack(f);
       s += f[0];
     }
-    const float mean = row_sum<WIDE_THREADS>(s, 0.f, red[0]).x * inv_d;
+    const float mean = row_sum<WIDE_THREADS>(s, red[0]) * inv_d;
     s = 0.f;
     for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
       q.load(xr + c);
       q.unpack(f);
       s = fmaf(f[0] - mean, f[0] - mean, s);
     }
-    const float rstd = 1.0f / sqrtf(row_sum<WIDE_THREADS>(s, 0.f, red[1]).x * inv_d + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<WIDE_THREADS>(s, red[1]) * inv_d + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -366,7 +477,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) norm_fwd_wide_kernel(const NormA
 
 template <typename T>
 __global__ void __launch_bounds__(WIDE_THREADS) norm_bwd_wide_kernel(const NormArgs a) {
-  __shared__ float2 red[2][32];
+  __shared__ __align__(16) float red[2][64];
   const float inv_d = 1.0f / static_cast<float>(a.d);
   int par = 0;
   for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
@@ -453,47 +564,53 @@ moe_status_t launched() {
 template <typename T, int VB, int NCH, int TPR>
 int launch_fwd_rows(const NormArgs& a, cudaStream_t s) {
   constexpr int ROWS = block_threads(TPR) / TPR;
-  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, 1 << 20));
-  norm_fwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), 0, s>>>(a);
+  const long long most = fwd_blocks_per_sm(TPR) * static_cast<long long>(device_sm_count());
+  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, most));
+  constexpr int smem = Feed<T, VB, NCH, TPR, 1>::smem_bytes;
+  if (smem > 48 * 1024 &&
+      ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_fwd_kernel<T, VB, NCH, TPR>), smem) != cudaSuccess)
+    return grid;  // the launch below the limit would fail too: the caller reads the error
+  norm_fwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), smem, s>>>(a);
   return grid;
 }
 template <typename T, int VB, int NCH, int TPR>
 int launch_bwd_rows(const NormArgs& a, cudaStream_t s) {
   constexpr int ROWS = block_threads(TPR) / TPR;
-  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, BWD_MAX_BLOCKS));
-  norm_bwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), 0, s>>>(a);
+  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, std::min(bwd_blocks_per_sm(TPR) * device_sm_count(), BWD_MAX_BLOCKS)));
+  constexpr int smem = Feed<T, VB, NCH, TPR, 2>::smem_bytes;
+  if (smem > 48 * 1024 &&
+      ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_bwd_kernel<T, VB, NCH, TPR>), smem) != cudaSuccess)
+    return grid;
+  norm_bwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), smem, s>>>(a);
   return grid;
 }
 
 // Threads per row and chunks (16 bytes, or one element) per thread. The functions return the blocks
 // launched, 0 for a row wider than any layout.
-// Forward: a warp a row up to eight chunks a lane; fewer rows than four for each SM take four
-// warps a row from three chunks a lane on, for latency.
+// Forward: two chunks a thread (eight elements without alignment), so that a row takes few warps.
 template <typename T, int VB, int U>
 int fwd_by_width(const NormArgs& a, cudaStream_t s) {
   const int chunks = (a.d + VB - 1) / VB;
-  const bool few = a.T <= 608;
   if (chunks <= 32 * U) return launch_fwd_rows<T, VB, U, 32>(a, s);
   if (chunks <= 64 * U) return launch_fwd_rows<T, VB, 2 * U, 32>(a, s);
-  if (few && chunks <= 256 * U) return launch_fwd_rows<T, VB, 2 * U, 128>(a, s);
-  if (chunks <= 128 * U) return launch_fwd_rows<T, VB, 4 * U, 32>(a, s);
-  if (U == 1 && chunks <= 256) return launch_fwd_rows<T, VB, 8, 32>(a, s);
-  if (chunks <= 512 * U) return launch_fwd_rows<T, VB, 4 * U, 128>(a, s);
+  if (chunks <= 128 * U) return launch_fwd_rows<T, VB, U, 128>(a, s);
+  if (chunks <= 256 * U) return launch_fwd_rows<T, VB, 2 * U, 128>(a, s);
+  if (chunks <= 512 * U) return launch_fwd_rows<T, VB, 2 * U, 256>(a, s);
   if (chunks <= 1024 * U) return launch_fwd_rows<T, VB, 2 * U, 512>(a, s);
-  if (chunks <= 2048 * U) return launch_fwd_rows<T, VB, 4 * U, 512>(a, s);
+  if (chunks <= 2048 * U) return launch_fwd_rows<T, VB, 2 * U, 1024>(a, s);
   return 0;
 }
-// Backward: one chunk a thread (four elements without alignment) as long as a block has the threads.
+// Backward: the same.
 template <typename T, int VB, int U>
 int bwd_by_width(const NormArgs& a, cudaStream_t s) {
   const int chunks = (a.d + VB - 1) / VB;
   if (chunks <= 32 * U) return launch_bwd_rows<T, VB, U, 32>(a, s);
   if (chunks <= 64 * U) return launch_bwd_rows<T, VB, 2 * U, 32>(a, s);
   if (chunks <= 128 * U) return launch_bwd_rows<T, VB, U, 128>(a, s);
-  if (chunks <= 256 * U) return launch_bwd_rows<T, VB, U, 256>(a, s);
-  if (chunks <= 512 * U) return launch_bwd_rows<T, VB, U, 512>(a, s);
-  if (chunks <= 1024 * U) return launch_bwd_rows<T, VB, U, 1024>(a, s);
-  if (U == 1 && chunks <= 2048) return launch_bwd_rows<T, VB, 4, 512>(a, s);
+  if (chunks <= 256 * U) return launch_bwd_rows<T, VB, 2 * U, 128>(a, s);
+  if (chunks <= 512 * U) return launch_bwd_rows<T, VB, 2 * U, 256>(a, s);
+  if (chunks <= 1024 * U) return launch_bwd_rows<T, VB, 2 * U, 512>(a, s);
+  if (chunks <= 2048 * U) return launch_bwd_rows<T, VB, 4 * U, 512>(a, s);
   return 0;
 }
 
