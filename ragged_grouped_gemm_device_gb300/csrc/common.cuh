@@ -33,6 +33,36 @@ __device__ __forceinline__ void record_status(int32_t* status, int bits) {
   if (status != nullptr) atomicOr(status, bits);
 }
 
+// ---------------------------------------------------------------------------------- dependent launch
+// Programmatic dependent launch: a kernel launched by launch_dependent() may start before the one
+// ahead of it in the stream has finished. It has to call grid_wait() before it touches anything
+// that kernel may write or still read; grid_release() in the kernel ahead lets it start early.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A pointer to read through after grid_wait(): the compiler takes reads through a const __restrict__
+// pointer, and __ldg, for reads of memory that nothing writes, and may move them above the wait.
+template <typename T>
+__device__ __forceinline__ T* after_wait(T* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... Params, typename... Given>
+inline cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                                    cudaStream_t stream, Given... given) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...);
+}
+
 // ---------------------------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");

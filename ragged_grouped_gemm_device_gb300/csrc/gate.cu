@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gl = lane % G, grp = warp * GROUPS + lane / G;
   const bool stats = a.part != nullptr;
+  grid_release();
   int* s_cnt = reinterpret_cast<int*>(fsh);
   uint8_t* body = fsh + count_bytes(a.E);
   K* list = reinterpret_cast<K*>(body) + threadIdx.x * (NL * LIST);
@@ -374,12 +375,14 @@ __device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
 // Adds the blocks' partial rows in order: 32 experts a block, 32 threads an expert over the rows
 // (coalesced over the experts), added in thread order. The last block to finish adds the blocks'
 // shares of the balance loss in block order and writes the losses.
-__global__ void __launch_bounds__(1024) gate_stats_kernel(const float* __restrict__ part, int blocks, int k, int E,
+__global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int blocks, int k, int E,
                                                           int32_t* __restrict__ counts, int32_t* __restrict__ n_valid,
                                                           float* __restrict__ prob_sum, float* __restrict__ loss,
                                                           unsigned* ticket, float* share) {
   __shared__ float s_p[32][33];
   __shared__ int s_c[32][33];
+  grid_wait();  // launched ahead of the end of the forward kernel
+  part = after_wait(part);
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int words = part_words(E);
   const int* ipart = reinterpret_cast<const int*>(part);
@@ -669,9 +672,9 @@ moe_status_t moe_gate_fwd(const void* logits, int dtype, long long ld, const uin
   if (dtype == MOE_DTYPE_BF16) st = vec ? by_width_fwd<bf16, true>(a, w, blocks, s) : by_width_fwd<bf16, false>(a, w, blocks, s);
   else st = vec ? by_width_fwd<float, true>(a, w, blocks, s) : by_width_fwd<float, false>(a, w, blocks, s);
   if (st != MOE_OK || !stats) return st;
-  gate_stats_kernel<<<(E + 31) / 32, 1024, 0, s>>>(a.part, blocks, top_k, E, counts, n_valid, prob_sum, loss, a.ticket,
-                                                   reinterpret_cast<float*>(a.ticket + 1));
-  return launched();
+  const cudaError_t err = launch_dependent(gate_stats_kernel, (E + 31) / 32, 1024, 0, s, a.part, blocks, top_k, E, counts,
+                                           n_valid, prob_sum, loss, a.ticket, reinterpret_cast<float*>(a.ticket + 1));
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
 moe_status_t moe_gate_bwd(const void* logits, int dtype, long long ld, const float* lse, const int32_t* ids,

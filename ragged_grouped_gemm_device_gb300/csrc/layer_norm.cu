@@ -347,6 +347,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks_per_sm(TPR)) no
 #pragma unroll
     for (int j = 0; j < VB; ++j) dg[i][j] = db[i][j] = 0.f;
   }
+  grid_release();
   extern __shared__ __align__(16) uint8_t ring[];
   Feed<T, VB, NCH, TPR, 2> feed;
   const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
@@ -533,9 +534,11 @@ __global__ void __launch_bounds__(256) norm_wgrad_wide_kernel(const NormArgs a) 
 
 // out[c] = sum of the partials of column c, for both gradients: 32 columns a block, 32 threads a
 // column that take every 32nd partial and are added in thread order.
-__global__ void __launch_bounds__(1024) norm_partials_kernel(const float* __restrict__ part, int blocks, int d,
+__global__ void __launch_bounds__(1024) norm_partials_kernel(const float* part, int blocks, int d,
                                                              float* __restrict__ dgamma, float* __restrict__ dbeta) {
   __shared__ float acc[32][33];
+  grid_wait();  // launched ahead of the end of the kernel that writes the partials
+  part = after_wait(part);
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + cx;  // of 2d: dgamma's, then dbeta's columns
   float s = 0.f;
@@ -730,8 +733,9 @@ moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, l
     if ((st = launched()) != MOE_OK) return st;
   }
   if (!wgrad) return MOE_OK;
-  norm_partials_kernel<<<(2 * d + 31) / 32, 1024, 0, s>>>(static_cast<const float*>(ws), blocks, d, dgamma, dbeta);
-  return launched();
+  const cudaError_t err = launch_dependent(norm_partials_kernel, (2 * d + 31) / 32, 1024, 0, s,
+                                           static_cast<const float*>(ws), blocks, d, dgamma, dbeta);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
 }  // extern "C"

@@ -65,34 +65,28 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-__device__ __forceinline__ void unpack8(uint4 q, float (&f)[8]) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    f[2 * t] = bf16_lo(w[t]);
-    f[2 * t + 1] = bf16_hi(w[t]);
-  }
-}
-
 // A warp quantizes 256 consecutive elements, 8 a lane (four lanes hold a block): returns this
 // lane's 8 codes and, in lanes 0 and 16, the scale codes of the four blocks of its 128-element
 // chunk. Lanes past the row's end (act false) count as blocks of scale 2^0.
 __device__ __forceinline__ uint32_t quant256(uint4 q, bool act, uint32_t& chunk_scales) {
-  float f[8];
-  unpack8(q, f);
-  uint32_t m = 0u;
-#pragma unroll
-  for (int t = 0; t < 8; ++t) m = max(m, abs_bits(f[t]));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t code = mx4_scale_code(m);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  // largest magnitude as a bf16 bit pattern, two at a time (patterns without the sign order as
+  // numbers, infinity and NaN above all others)
+  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const uint32_t code = mx4_scale_code(max(m >> 16, m & 0xffffu) << 16);
   const float inv = mx4_inv_scale(code);
+  float f[8];
 #pragma unroll
-  for (int t = 0; t < 8; ++t) f[t] *= inv;
-  uint32_t w = (act ? code : 127u) << (8 * ((threadIdx.x >> 2) & 3));
-  w |= __shfl_xor_sync(0xffffffffu, w, 4);
-  w |= __shfl_xor_sync(0xffffffffu, w, 8);
-  chunk_scales = w;
+  for (int t = 0; t < 4; ++t) {
+    f[2 * t] = bf16_lo(w[t]) * inv;
+    f[2 * t + 1] = bf16_hi(w[t]) * inv;
+  }
+  uint32_t s = (act ? code : 127u) << (8 * ((threadIdx.x >> 2) & 3));
+  s |= __shfl_xor_sync(0xffffffffu, s, 4);
+  s |= __shfl_xor_sync(0xffffffffu, s, 8);
+  chunk_scales = s;
   return e2m1x8(f);
 }
 
@@ -101,8 +95,20 @@ __device__ __forceinline__ uint32_t* chunk_word(uint8_t* sf, long long G, int KC
   return reinterpret_cast<uint32_t*>(sf + static_cast<size_t>(G * KC + kc) * 512 + (r & 31) * 16 + (r >> 5) * 4);
 }
 
-// Rows along K, one warp a row. With offsets: the rows p < M of a problem list; else `rows` rows
-// of weights in groups of `sub` rows, ntpad tiles a group.
+// The row kernels below are bound by memory (they read 2 bytes an element and write about half of
+// one, or the reverse). A warp takes PASSES * 256 elements of a row at a time, all of its loads in
+// flight before it works on them: 4 passes when there are rows enough for every warp of the
+// GPU, 1 for few rows, so that a row is spread over more warps.
+constexpr int ROW_PASSES = 4;
+
+// Row and piece of item `it` (32-bit division unless there are 2^32 items).
+__device__ __forceinline__ long long item_row(long long it, int pieces, bool small) {
+  return small ? static_cast<long long>(static_cast<uint32_t>(it) / static_cast<uint32_t>(pieces)) : it / pieces;
+}
+
+// Rows along K. With offsets: the rows p < M of a problem list; else `rows` rows of weights in
+// groups of `sub` rows, ntpad tiles a group.
+template <int PASSES>
 __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __restrict__ src, long long rows, int K,
                                                              const int32_t* __restrict__ offsets, int E, int sub,
                                                              int ntpad, uint32_t* __restrict__ q,
@@ -110,12 +116,21 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __rest
                                                              int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
+  grid_release();  // the product's prologue may start
   const bool list = offsets != nullptr;
   if (list && !load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
   const long long M = list ? s_end[E - 1] : rows;
   const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
-  for (long long p = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); p < M;
-       p += static_cast<long long>(gridDim.x) * 8) {
+  const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
+  const long long items = M * pieces;
+  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += static_cast<long long>(gridDim.x) * 8) {
+    const long long p = item_row(it, pieces, items <= 0xffffffffll);
+    const int v0 = static_cast<int>(it - p * pieces) * (32 * PASSES) + lane;
+    uint4 w[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      w[i] = v0 + 32 * i < vec ? __ldcs(src + p * vec + v0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     long long G;
     int r;
     if (list) {
@@ -126,12 +141,13 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __rest
       r = static_cast<int>(n % 128);
     }
     const bool tile_ok = MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles);
-    for (int v0 = 0; v0 < vec; v0 += 32) {  // every lane runs every pass: the shuffles need the warp
-      const int v = v0 + lane;
-      const bool act = v < vec;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {  // every lane runs every pass: the shuffles need the warp
+      const int v = v0 + 32 * i;
+      if (v - lane >= vec) break;
       uint32_t word;
-      const uint32_t codes = quant256(act ? __ldg(src + p * vec + v) : make_uint4(0u, 0u, 0u, 0u), act, word);
-      if (act) q[p * vec + v] = codes;
+      const uint32_t codes = quant256(w[i], v < vec, word);
+      if (v < vec) q[p * vec + v] = codes;
       if ((lane & 15) == 0 && tile_ok) *chunk_word(sf, G, KC, v >> 4, r) = word;
     }
   }
@@ -139,6 +155,7 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __rest
 
 // The permute's gather and the quantization along d in one pass, token by token: a token's row is
 // read and quantized once and its codes and scales are written to the rows of its top_k slots.
+template <int PASSES>
 __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* __restrict__ x,
                                                           const int32_t* __restrict__ inv_map,
                                                           const int32_t* __restrict__ offsets, int E, int T, int k,
@@ -146,12 +163,21 @@ __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* __restric
                                                           long long sf_tiles, int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
+  grid_release();  // the product's prologue may start
   const long long n = static_cast<long long>(T) * k;
   if (!load_problem_tiles(offsets, E, n, s_end, s_pre, status)) return;
   const int M = s_end[E - 1];
   const int lane = threadIdx.x & 31, vec = d / 8, KC = mx4_kc(d);
-  for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T;
-       t += static_cast<long long>(gridDim.x) * 8) {
+  const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
+  const long long items = static_cast<long long>(T) * pieces;
+  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += static_cast<long long>(gridDim.x) * 8) {
+    const long long t = item_row(it, pieces, items <= 0xffffffffll);
+    const int v0 = static_cast<int>(it - t * pieces) * (32 * PASSES) + lane;
+    uint4 w[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      w[i] = v0 + 32 * i < vec ? __ldg(x + t * vec + v0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
     // lane j < k holds slot j's row, its tile and the row within the tile
     int my_p = -1, my_r = 0, my_g = 0;
     if (lane < k) {
@@ -165,24 +191,35 @@ __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* __restric
         }
       }
     }
-    for (int v0 = 0; v0 < vec; v0 += 32) {
-      const int v = v0 + lane;
-      const bool act = v < vec;
-      uint32_t word;
-      const uint32_t codes = quant256(act ? __ldg(x + t * vec + v) : make_uint4(0u, 0u, 0u, 0u), act, word);
-      for (int j = 0; j < k; ++j) {
-        const int p = __shfl_sync(0xffffffffu, my_p, j);
-        const int g = __shfl_sync(0xffffffffu, my_g, j), r = __shfl_sync(0xffffffffu, my_r, j);
-        if (p < 0) continue;  // warp-uniform
-        if (act) q[static_cast<size_t>(p) * vec + v] = codes;
-        if ((lane & 15) == 0) *chunk_word(sf, g, KC, v >> 4, r) = word;
+    uint32_t codes[PASSES], word[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) codes[i] = quant256(w[i], v0 + 32 * i < vec, word[i]);
+    for (int j = 0; j < k; ++j) {
+      const int p = __shfl_sync(0xffffffffu, my_p, j);
+      const int g = __shfl_sync(0xffffffffu, my_g, j), r = __shfl_sync(0xffffffffu, my_r, j);
+      if (p < 0) continue;  // warp-uniform
+#pragma unroll
+      for (int i = 0; i < PASSES; ++i) {
+        const int v = v0 + 32 * i;
+        if (v < vec) q[static_cast<size_t>(p) * vec + v] = codes[i];
+        if ((lane & 15) == 0 && v - lane < vec) *chunk_word(sf, g, KC, v >> 4, r) = word[i];
       }
     }
   }
 }
 
+// The value of a 4-bit code.
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+  const uint32_t mag = c & 7u;
+  // exponent field e and mantissa bit m: e = 0 is m / 2, else (2 + m) 2^(e - 2)
+  const float v = mag < 2u ? 0.5f * static_cast<float>(mag)
+                           : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
+  return (c & 8u) ? -v : v;
+}
+
 // The bf16 values that rows p < M of codes and scales stand for (exact: an E2M1 value times a
 // power of two has two significant bits); a block with a NaN scale reads as NaN.
+template <int PASSES>
 __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* __restrict__ q,
                                                                const uint8_t* __restrict__ sf, long long rows, int K,
                                                                const int32_t* __restrict__ offsets, int E,
@@ -190,36 +227,41 @@ __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* _
                                                                int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
+  __shared__ uint32_t pair[256];  // the bf16 values of the two codes of a byte
   if (!load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
+  pair[threadIdx.x] = pack_bf16x2(e2m1_value(threadIdx.x & 15u), e2m1_value(threadIdx.x >> 4));
+  __syncthreads();
   const int M = s_end[E - 1];
   const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
-  for (long long p = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); p < M;
-       p += static_cast<long long>(gridDim.x) * 8) {
+  const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
+  const long long items = static_cast<long long>(M) * pieces;
+  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
+       it += static_cast<long long>(gridDim.x) * 8) {
+    const long long p = item_row(it, pieces, items <= 0xffffffffll);
+    const int v0 = static_cast<int>(it - p * pieces) * (32 * PASSES) + lane;
+    uint32_t codes[PASSES], sc[PASSES];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) codes[i] = v0 + 32 * i < vec ? __ldcs(q + p * vec + v0 + 32 * i) : 0u;
     long long G;
     int r;
     row_tile(s_end, s_pre, E, p, G, r);
     if (!MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles)) continue;
-    for (int v = lane; v < vec; v += 32) {
-      const uint32_t codes = __ldg(q + p * vec + v);
-      const uint32_t sc = __ldg(sf + atom_byte(G, KC, v >> 2, r));
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      sc[i] = v0 + 32 * i < vec ? __ldg(sf + atom_byte(G, KC, (v0 + 32 * i) >> 2, r)) : 0u;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+      const int v = v0 + 32 * i;
+      if (v >= vec) break;
       // 2^(sc - 127): 2^-127 is the subnormal 0x00400000
-      const float scale = sc == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(sc == 0u ? 0x00400000u : sc << 23);
+      const float scale = sc[i] == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(sc[i] == 0u ? 0x00400000u : sc[i] << 23);
       uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t c = (codes >> (8 * i + 4 * j)) & 15u;
-          const uint32_t mag = c & 7u;
-          // exponent field e and mantissa bit m: e = 0 is m / 2, else (2 + m) 2^(e - 2)
-          const float v8 = mag < 2u ? 0.5f * static_cast<float>(mag)
-                                    : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-          f[j] = ((c & 8u) ? -v8 : v8) * scale;
-        }
-        w[i] = pack_bf16x2(f[0], f[1]);
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t two = pair[(codes[i] >> (8 * b)) & 0xffu];
+        w[b] = pack_bf16x2(bf16_lo(two) * scale, bf16_hi(two) * scale);
       }
-      x[p * vec + v] = make_uint4(w[0], w[1], w[2], w[3]);
+      __stcs(x + p * vec + v, make_uint4(w[0], w[1], w[2], w[3]));
     }
   }
 }
@@ -266,39 +308,58 @@ __global__ void __launch_bounds__(256) mx4_quant_cols_kernel(const bf16* __restr
 
 // ------------------------------------------------------------------------------ the product
 // Persistent grouped GEMM on block-scaled 4-bit operands: the problem list, tile order, roles and
-// bounded waits of the grouped GEMM (grouped_gemm.cu), one CTA per SM on 128 x 256 tiles.
-//   warp 0      TMA producer of A (128 rows x 256 elements of K, its scale atoms)
+// bounded waits of the grouped GEMM (grouped_gemm.cu), one CTA per SM.
+//   warp 0      TMA producer of A (the tile's rows x 256 elements of K, and their scale atoms)
 //   warp 1      tensor-memory allocator and MMA issuer: per stage, the scale atoms into tensor
 //               memory and four block-scaled MMAs of K = 64
 //   warps 2..9  epilogue, two per lane quadrant
 //   warp 10     TMA producer of B
-// MX4_UP:   B = 128 gate and 128 up rows of W_ug; the epilogue computes A = silu(gate) up in fp32
-//           and quantizes it along h from fp32 (no bf16 rounding in between).
-// MX4_DOWN: B = 256 rows of W_down^T; bf16 store, one rounding.
+// MX4_UP:   B = BN / 2 gate and BN / 2 up rows of W_ug; the epilogue computes A = silu(gate) up in
+//           fp32 and quantizes it along h from fp32 (no bf16 rounding in between).
+// MX4_DOWN: B = BN rows of W_down^T; bf16 store, one rounding, staged through shared memory so
+//           that a warp writes whole 128-byte lines.
+// Tiles are 128 x 256: the products of many rows are held by the L2's output to the SMs, 51 KB of
+// codes and scales for each 128 x 256 x 256, and a wider tile has no room in tensor memory; those
+// of few rows by the weights' way from HBM (128-column tiles for them, twice as many, took 57 us
+// instead of 39 for 128 rows over 128 experts: an MMA of half the columns takes about as long).
+// A row tile that its expert does not fill loads only its own rows, 16 at a time; the other rows
+// of the stage hold what was there before, and nothing reads the rows of the product that they
+// give (the rows of a product are independent).
 enum { MX4_UP = 0, MX4_DOWN = 1 };
 
 constexpr int BM = 128;
 constexpr int BN = 256;
-constexpr int STAGES = 4;
 constexpr int STAGE_K = 256;                 // elements of K per stage: 128 bytes of codes
 constexpr int UK = 64;                       // K of one MMA
 constexpr int A_BYTES = BM * STAGE_K / 2;    // 16 KB
-constexpr int B_BYTES = BN * STAGE_K / 2;    // 32 KB
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int SF_A_BYTES = 2 * 512;          // two chunks of one 128-row tile
-constexpr int SF_B_BYTES = 2 * SF_A_BYTES;   // ... of two tiles
-constexpr int SF_STAGE_BYTES = SF_A_BYTES + SF_B_BYTES;
+constexpr int A_BOX = 16;                    // rows of the small box of A
+constexpr int SF_BYTES = 2 * 512;            // scale atoms of a 128-row tile: two chunks
+constexpr int SF_STAGE_BYTES = 3 * SF_BYTES; // A, and two tiles of B
 constexpr int EPI_WARPS = 8;
 constexpr int PRODUCER_B_WARP = 2 + EPI_WARPS;
 constexpr int THREADS = 32 * (PRODUCER_B_WARP + 1);
 constexpr int TMEM_COLS = 512;
 constexpr int SF_TMEM_COL = 256;             // 32 columns of scales per stage after the accumulator
 constexpr int RASTER_M = 16;                 // row tiles per raster group
+constexpr int MAX_STAGES = 4;
+constexpr int OUT_BYTES = 32 * 128;          // MX4_DOWN: a warp's staging, 32 rows of 64 bf16
 constexpr int CTL_BYTES = 256;
 
+template <int MODE>
+struct Shape {
+  static constexpr int cols = MODE == MX4_UP ? BN / 2 : BN;  // output columns per tile
+  static constexpr int b_bytes = BN * STAGE_K / 2;
+  static constexpr int stage_bytes = A_BYTES + b_bytes;
+  static constexpr int stages = MODE == MX4_UP ? 4 : 3;
+  static constexpr int out_bytes = MODE == MX4_DOWN ? EPI_WARPS * OUT_BYTES : 0;
+  static constexpr int fixed = 1024 + stages * (stage_bytes + SF_STAGE_BYTES) + out_bytes + CTL_BYTES;
+  static_assert(stages <= MAX_STAGES && SF_TMEM_COL + 32 * stages <= TMEM_COLS, "stages");
+  static size_t smem(int E) { return fixed + 2 * sizeof(int) * static_cast<size_t>(E + 2); }
+};
+
 struct Ctl {
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
   uint64_t tfull;
   uint64_t tempty;
   uint64_t done;
@@ -307,13 +368,8 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= CTL_BYTES, "control block too large");
 
-constexpr size_t smem_bytes_for(int E) {
-  return 1024 + static_cast<size_t>(STAGES) * (STAGE_BYTES + SF_STAGE_BYTES) + CTL_BYTES +
-         2 * sizeof(int) * static_cast<size_t>(E + 2);
-}
-
 struct Maps {
-  CUtensorMap a, b;
+  CUtensorMap a, a16, b;  // boxes of 128 and of 16 rows of A
 };
 
 struct Args {
@@ -327,7 +383,6 @@ struct Args {
   int kc;              // chunks per row, even
   int tiles_b;
   bf16* y;             // MX4_DOWN
-  int vec32;           // its rows are 32-byte aligned
   uint8_t* pq;         // MX4_UP: codes [cap, h / 2] and scale atoms of A = silu(gate) up
   uint8_t* psf;
   int pkc;
@@ -376,26 +431,52 @@ __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + _
 
 template <int MODE>
 __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
-  constexpr int COLS = MODE == MX4_UP ? 128 : BN;  // output columns per tile
+  typedef Shape<MODE> S;
+  constexpr int COLS = S::cols;
+  constexpr int STAGES = S::stages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* sf_ring = smem + STAGES * STAGE_BYTES;
-  Ctl* ctl = reinterpret_cast<Ctl*>(sf_ring + STAGES * SF_STAGE_BYTES);
+  uint8_t* sf_ring = smem + STAGES * S::stage_bytes;
+  uint8_t* staging = sf_ring + STAGES * SF_STAGE_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(staging + S::out_bytes);
   int* offs = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(ctl) + CTL_BYTES);
   const int E = args.E;
   int* pre = offs + (E + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
+  // ---- barriers and tensor memory, which do not depend on the kernel before this one
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&ctl->full[s]), 2);  // both producers
+      mbar_init(smem_u32(&ctl->empty[s]), 1);
+    }
+    mbar_init(smem_u32(&ctl->tfull), 1);
+    mbar_init(smem_u32(&ctl->tempty), 32 * EPI_WARPS);
+    mbar_init(smem_u32(&ctl->done), 1);
+    ctl->abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.a16);
+    prefetch_tmap(&maps.b);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
+    tmem_relinquish();
+  }
+  // The up product waits here for everything before it; what the down product reads before its own
+  // wait (offsets, weights) is then complete, because the up product releases it after this wait.
+  if constexpr (MODE == MX4_UP) {
+    grid_wait();
+    grid_release();
+  }
+
   // ---- problem list
-  for (int i = tid; i <= E; i += THREADS) offs[i] = i == 0 ? 0 : __ldg(args.offsets + i - 1);
+  const int32_t* offsets = after_wait(args.offsets);
+  for (int i = tid; i <= E; i += THREADS) offs[i] = i == 0 ? 0 : __ldg(offsets + i - 1);
   __syncthreads();
   bool bad = false;
   for (int i = tid; i < E; i += THREADS) bad |= (offs[i + 1] < offs[i]) || (offs[i] < 0);
   if (tid == 0) bad |= offs[E] > args.cap;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0 && blockIdx.x == 0) record_status(args.status, MOE_DEV_BAD_OFFSETS);
-    return;  // uniform across the CTA, before any barrier or tensor memory exists
-  }
   if (warp == 0) {
     int carry = 0;
     if (lane == 0) pre[0] = 0;
@@ -411,35 +492,17 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
       carry += __shfl_sync(0xffffffffu, v, 31);
     }
   }
-
-  // ---- barriers and tensor memory
-  if (tid == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&ctl->full[s]), 2);  // both producers
-      mbar_init(smem_u32(&ctl->empty[s]), 1);
-    }
-    mbar_init(smem_u32(&ctl->tfull), 1);
-    mbar_init(smem_u32(&ctl->tempty), 32 * EPI_WARPS);
-    mbar_init(smem_u32(&ctl->done), 1);
-    ctl->abort_flag = 0;
-    fence_mbar_init();
-    prefetch_tmap(&maps.a);
-    prefetch_tmap(&maps.b);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&ctl->tmem_base), TMEM_COLS);
-    tmem_relinquish();
-  }
   tc_fence_before();
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   tc_fence_after();
+  if (bad && tid == 0 && blockIdx.x == 0) record_status(args.status, MOE_DEV_BAD_OFFSETS);
 
   Sched sc;
   sc.offs = offs;
   sc.pre = pre;
   sc.E = E;
   sc.nt = (args.N + COLS - 1) / COLS;
-  sc.total = pre[E] * sc.nt;
+  sc.total = bad ? 0 : pre[E] * sc.nt;  // bad offsets: no work, only the teardown
   const int kblocks = (args.K + STAGE_K - 1) / STAGE_K;
   const uint32_t tmem_base = ctl->tmem_base;
   volatile int* abort_flag = &ctl->abort_flag;
@@ -451,6 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
     // =========================================================== TMA producers
     if (lane == 0) {
       const bool is_a = warp == 0;
+      if (MODE == MX4_DOWN && is_a) grid_wait();  // A is the up product's output
       uint32_t it = 0;
       bool ok = true;
       for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x) {
@@ -471,30 +535,37 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
           if (!MOE_DBG_IN(DBG_GG_SFB, s0, args.dbg_b_tiles)) s0 = 0;
           if (!MOE_DBG_IN(DBG_GG_SFB, s1, args.dbg_b_tiles)) s1 = 0;
         }
+        const int boxes = ti.rows > BM - A_BOX ? 0 : (ti.rows + A_BOX - 1) / A_BOX;  // 0: the whole tile
+        const uint32_t a_bytes = boxes == 0 ? A_BYTES : boxes * (A_BYTES / (BM / A_BOX));
         for (int kb = 0; kb < kblocks; ++kb, ++it) {
           const int s = it % STAGES;
+          // the weights of the first stages load while the up product still runs; the clock of
+          // this thread's waits starts after it
+          if (MODE == MX4_DOWN && !is_a && it == STAGES) grid_wait();
           if (!mbar_wait(smem_u32(&ctl->empty[s]), ((it / STAGES) & 1u) ^ 1u, abort_flag, args.status, tmo)) {
             ok = false;
             break;
           }
           const uint32_t fb = smem_u32(&ctl->full[s]);
-          const uint32_t sa = stage0 + s * STAGE_BYTES, sb = sa + A_BYTES;
+          const uint32_t sa = stage0 + s * S::stage_bytes, sb = sa + A_BYTES;
           const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
           const int k0 = kb * (STAGE_K / 2);  // in bytes of codes
           if (is_a) {
-            mbar_arrive_expect_tx(fb, A_BYTES + SF_A_BYTES);
-            tma_load_2d(sa, &maps.a, k0, ti.row0, fb);
-            bulk_load(sfs, args.sfa + (s0 * args.kc + 2 * kb) * 512, SF_A_BYTES, fb);
+            mbar_arrive_expect_tx(fb, a_bytes + SF_BYTES);
+            if (boxes == 0) tma_load_2d(sa, &maps.a, k0, ti.row0, fb);
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(sa + i * (A_BYTES / (BM / A_BOX)), &maps.a16, k0, ti.row0 + i * A_BOX, fb);
+            bulk_load(sfs, args.sfa + (s0 * args.kc + 2 * kb) * 512, SF_BYTES, fb);
           } else {
-            mbar_arrive_expect_tx(fb, B_BYTES + SF_B_BYTES);
+            mbar_arrive_expect_tx(fb, S::b_bytes + 2 * SF_BYTES);
             if constexpr (MODE == MX4_UP) {
-              tma_load_3d(sb, &maps.b, k0, ti.n0, ti.e, fb);                         // gate rows
-              tma_load_3d(sb + B_BYTES / 2, &maps.b, k0, args.h + ti.n0, ti.e, fb);  // up rows
+              tma_load_3d(sb, &maps.b, k0, ti.n0, ti.e, fb);                            // gate rows
+              tma_load_3d(sb + S::b_bytes / 2, &maps.b, k0, args.h + ti.n0, ti.e, fb);  // up rows
             } else {
               tma_load_3d(sb, &maps.b, k0, ti.n0, ti.e, fb);
             }
-            bulk_load(sfs + SF_A_BYTES, args.sfb + (s0 * args.kc + 2 * kb) * 512, SF_A_BYTES, fb);
-            bulk_load(sfs + 2 * SF_A_BYTES, args.sfb + (s1 * args.kc + 2 * kb) * 512, SF_A_BYTES, fb);
+            bulk_load(sfs + SF_BYTES, args.sfb + (s0 * args.kc + 2 * kb) * 512, SF_BYTES, fb);
+            bulk_load(sfs + 2 * SF_BYTES, args.sfb + (s1 * args.kc + 2 * kb) * 512, SF_BYTES, fb);
           }
         }
       }
@@ -506,11 +577,27 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
     }
   } else if (warp == 1) {
     // =========================================================== MMA issuer
-    constexpr uint32_t idesc = idesc_mxf4(BM, BN);
-    uint32_t it = 0, use = 0;
+    if (MODE == MX4_DOWN) {
+      grid_wait();     // the clock of its waits starts after the up product
+      grid_release();  // the combine may start
+    }
+    // scale atoms of stage s into its 32 columns: per 128-element chunk 4 columns of A, then 8 of B;
+    // a copy and the MMAs after it from one thread execute in issue order (copying a stage ahead of
+    // the MMAs was slower: the ring's stages are then held longer)
+    auto copy_scales = [&](int s) {
+      const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
+      const uint32_t sft = tmem_base + SF_TMEM_COL + s * 32;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        tmem_cp_32x128b_x4(sft + 12 * c, smem_desc_rows16(sfs + 512 * c));
+        tmem_cp_32x128b_x4(sft + 12 * c + 4, smem_desc_rows16(sfs + SF_BYTES + 512 * c));
+        tmem_cp_32x128b_x4(sft + 12 * c + 8, smem_desc_rows16(sfs + 2 * SF_BYTES + 512 * c));
+      }
+    };
+    uint32_t it = 0, n = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x, ++use) {
-      ok = warp_all(mbar_wait(smem_u32(&ctl->tempty), (use & 1u) ^ 1u, abort_flag, args.status, tmo));
+    for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x, ++n) {
+      ok = warp_all(mbar_wait(smem_u32(&ctl->tempty), (n & 1u) ^ 1u, abort_flag, args.status, tmo));
       if (!ok) break;
       tc_fence_after();
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
@@ -519,19 +606,12 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
         if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
-          // scale atoms into this stage's 32 columns: per 128-element chunk 4 columns of A, then
-          // 8 of B; a copy and the MMAs after it from one thread execute in issue order
-          const uint32_t sa = stage0 + s * STAGE_BYTES, sb = sa + A_BYTES;
-          const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
+          const uint32_t sa = stage0 + s * S::stage_bytes, sb = sa + A_BYTES;
           const uint32_t sft = tmem_base + SF_TMEM_COL + s * 32;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            tmem_cp_32x128b_x4(sft + 12 * c, smem_desc_rows16(sfs + 512 * c));
-            tmem_cp_32x128b_x4(sft + 12 * c + 4, smem_desc_rows16(sfs + SF_A_BYTES + 512 * c));
-            tmem_cp_32x128b_x4(sft + 12 * c + 8, smem_desc_rows16(sfs + 2 * SF_A_BYTES + 512 * c));
-          }
+          copy_scales(s);
 #pragma unroll
           for (int ks = 0; ks < STAGE_K / UK; ++ks) {
+            constexpr uint32_t idesc = idesc_mxf4(BM, BN);
             const uint64_t ad = smem_desc_sw128(sa + ks * (UK / 2), 16, 1024);
             const uint64_t bd = smem_desc_sw128(sb + ks * (UK / 2), 16, 1024);
             const uint32_t sfc = sft + 12 * (ks >> 1);
@@ -551,34 +631,41 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
     mbar_wait(smem_u32(&ctl->done), 0u, abort_flag, args.status, args.drain_ns, false);
   } else {
     // =========================================================== epilogue (warps 2..9)
+    if (MODE == MX4_DOWN) grid_wait();  // the clock of its waits starts after the up product
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int r_in = q * 32 + lane;
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-    uint32_t use = 0;
-    for (int t = blockIdx.x; t < sc.total; t += gridDim.x, ++use) {
+    uint32_t n = 0;
+    for (int t = blockIdx.x; t < sc.total; t += gridDim.x, ++n) {
       const Tile ti = decode_tile(sc, t, COLS);
-      if (!warp_all(mbar_wait(smem_u32(&ctl->tfull), use & 1u, abort_flag, args.status, tmo))) break;
+      if (!warp_all(mbar_wait(smem_u32(&ctl->tfull), n & 1u, abort_flag, args.status, tmo))) break;
       tc_fence_after();
+      if (q * 32 >= ti.rows) {  // warp-uniform: none of this quadrant's rows
+        tc_fence_before();
+        mbar_arrive(smem_u32(&ctl->tempty));
+        continue;
+      }
       const long long row = static_cast<long long>(ti.row0) + r_in;
       bool rv = r_in < ti.rows;
       if (rv && !MOE_DBG_IN(DBG_GG_ROW, row, args.cap)) rv = false;
       if constexpr (MODE == MX4_UP) {
-        // this warp's 64 gate and 64 up columns into registers, so that the accumulator goes
-        // back to the MMA issuer before they are worked on
-        uint32_t g[4][16], u[4][16];
+        // this warp's gate and up columns into registers, so that the accumulator goes back to the
+        // MMA issuer before they are worked on
+        constexpr int BLOCKS = 2;  // blocks of 32 output columns per warp
+        uint32_t g[2 * BLOCKS][16], u[2 * BLOCKS][16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          tmem_ld16(tb + half * 64 + i * 16, g[i]);
-          tmem_ld16(tb + 128 + half * 64 + i * 16, u[i]);
+        for (int i = 0; i < 2 * BLOCKS; ++i) {
+          tmem_ld16(tb + half * (32 * BLOCKS) + i * 16, g[i]);
+          tmem_ld16(tb + COLS + half * (32 * BLOCKS) + i * 16, u[i]);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld_wait2(g[i], u[i]);
+        for (int i = 0; i < 2 * BLOCKS; ++i) tmem_ld_wait2(g[i], u[i]);
         tc_fence_before();
         mbar_arrive(smem_u32(&ctl->tempty));
         if (!rv || !MOE_DBG_IN(DBG_GG_MXSF, ti.g, args.dbg_a_tiles)) continue;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const int col = ti.n0 + half * 64 + b * 32;  // h % 32 == 0: a block is all in or all out
+        for (int b = 0; b < BLOCKS; ++b) {
+          const int col = ti.n0 + half * (32 * BLOCKS) + b * 32;  // h % 32 == 0: a block is all in or all out
           uint8_t* sfp = args.psf + atom_byte(ti.g, args.pkc, col >> 5, r_in);
           if (col >= args.h) {
             *sfp = 127;
@@ -604,19 +691,22 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
           *reinterpret_cast<uint4*>(args.pq + row * (args.h / 2) + col / 2) = make_uint4(o[0], o[1], o[2], o[3]);
           *sfp = static_cast<uint8_t>(code);
         }
-        // an odd number of chunks: the padding chunk of the last stage
-        if (ti.n0 + COLS >= args.h && (ti.n0 / 128 + 1) < args.pkc) {
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            args.psf[atom_byte(ti.g, args.pkc, (ti.n0 + 128) / 32 + half * 2 + b, r_in)] = 127;
-        }
+        // the last column tile also writes the scales of the blocks that no tile covers, up to
+        // the end of the row's last (256-element) stage
+        if (ti.n0 + COLS >= args.h)
+          for (int kb = (ti.n0 + COLS) / 32 + half; kb < 4 * args.pkc; kb += 2)
+            args.psf[atom_byte(ti.g, args.pkc, kb, r_in)] = 127;
       } else {
-        uint32_t p[64];
+        // 64 columns at a time: packed into this warp's staging (16-byte piece j of row r at
+        // piece j ^ (r & 7): no bank conflicts either way), then out in whole 128-byte lines,
+        // four rows an instruction
+        constexpr int CHUNKS = 2;
+        uint32_t p[32 * CHUNKS];
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
+        for (int i = 0; i < 4 * CHUNKS; i += 2) {
           uint32_t v0[16], v1[16];
-          tmem_ld16(tb + half * 128 + i * 16, v0);
-          tmem_ld16(tb + half * 128 + (i + 1) * 16, v1);
+          tmem_ld16(tb + half * (BN / 2) + i * 16, v0);
+          tmem_ld16(tb + half * (BN / 2) + (i + 1) * 16, v1);
           tmem_ld_wait2(v0, v1);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -626,20 +716,27 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
         }
         tc_fence_before();
         mbar_arrive(smem_u32(&ctl->tempty));
-        if (!rv) continue;
-        bf16* yrow = args.y + row * args.N;
+        uint8_t* sbuf = staging + (warp - 2) * OUT_BYTES;
+        const int rows_here = min(32, ti.rows - q * 32);
+        const unsigned valid = __ballot_sync(0xffffffffu, rv);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = ti.n0 + half * 128 + i * 32;  // N % 32 == 0
-          if (col >= args.N) break;
-          if (args.vec32) {
-            st_global_v8(yrow + col, p + 16 * i);
-            st_global_v8(yrow + col + 16, p + 16 * i + 8);
-          } else {
+        for (int c = 0; c < CHUNKS; ++c) {
+          const int col0 = ti.n0 + half * (BN / 2) + c * 64;
+          if (col0 >= args.N) break;  // warp-uniform
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(yrow + col + 8 * j) =
-                  make_uint4(p[16 * i + 4 * j], p[16 * i + 4 * j + 1], p[16 * i + 4 * j + 2], p[16 * i + 4 * j + 3]);
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(sbuf + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(p[32 * c + 4 * j], p[32 * c + 4 * j + 1], p[32 * c + 4 * j + 2], p[32 * c + 4 * j + 3]);
+          __syncwarp();
+          const int piece = lane & 7, col = col0 + piece * 8;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = i * 4 + (lane >> 3);
+            if (i * 4 >= rows_here) break;
+            if (col < args.N && ((valid >> r) & 1u))  // N % 32 == 0: a piece is all in or all out
+              *reinterpret_cast<uint4*>(args.y + (static_cast<long long>(ti.row0) + q * 32 + r) * args.N + col) =
+                  *reinterpret_cast<const uint4*>(sbuf + r * 128 + ((piece ^ (r & 7)) << 4));
           }
         }
       }
@@ -693,22 +790,37 @@ moe_status_t launched() {
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
-int row_blocks(long long rows) {
-  return static_cast<int>(std::max(1LL, std::min((rows + 7) / 8, 8LL * device_sm_count())));
+// Whether `rows` rows of K elements are at least 16 pieces of ROW_PASSES passes for each SM
+bool many_rows(long long rows, int K) {
+  return rows * ((K + 256 * ROW_PASSES - 1) / (256 * ROW_PASSES)) >= 16LL * device_sm_count();
 }
+// blocks of eight warps for the pieces of `rows` rows
+int row_blocks(long long rows, int K, int passes) {
+  const long long items = rows * ((K + 256 * passes - 1) / (256 * passes));
+  return static_cast<int>(std::max(1LL, std::min((items + 7) / 8, 8LL * device_sm_count())));
+}
+#define MOE_MX4_ROWS(kernel, rows, K, s, ...)                                                    \
+  do {                                                                                           \
+    if (many_rows(rows, K)) kernel<ROW_PASSES><<<row_blocks(rows, K, ROW_PASSES), 256, 0, s>>>(__VA_ARGS__); \
+    else kernel<1><<<row_blocks(rows, K, 1), 256, 0, s>>>(__VA_ARGS__);                          \
+  } while (0)
 
 template <int MODE>
-moe_status_t launch_gemm(const Maps& maps, Args a, cudaStream_t s) {
-  const cudaError_t aerr = ensure_max_dynamic_smem(reinterpret_cast<const void*>(mx4_gemm_kernel<MODE>),
-                                                   static_cast<int>(smem_bytes_for(MAX_E)));
-  if (aerr != cudaSuccess) return cuda_fail(aerr);
+moe_status_t launch_gemm(const uint8_t* a_codes, const uint8_t* b_codes, long long b_rows, Args a, cudaStream_t s) {
+  typedef Shape<MODE> S;
   a.timeout_ns = wait_timeout_ns();
   a.drain_ns = std::max(a.timeout_ns, 2000000000LL);
-  const int cols = MODE == MX4_UP ? 128 : BN;
-  const long long tiles = list_tiles(a.cap, a.E) * ((a.N + cols - 1) / cols);
-  const int grid = static_cast<int>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
-  mx4_gemm_kernel<MODE><<<grid, THREADS, smem_bytes_for(a.E), s>>>(maps, a);
-  return launched();
+  Maps m;
+  if (!make_map_u8_rows2d(&m.a, a_codes, a.cap, a.K / 2, BM) || !make_map_u8_rows2d(&m.a16, a_codes, a.cap, a.K / 2, A_BOX) ||
+      !make_map_u8_weight3d(&m.b, b_codes, a.E, b_rows, a.K / 2, MODE == MX4_UP ? BN / 2 : BN))
+    return cuda_fail(cudaErrorInvalidValue);
+  const cudaError_t aerr = ensure_max_dynamic_smem(reinterpret_cast<const void*>(mx4_gemm_kernel<MODE>),
+                                                   static_cast<int>(S::smem(MAX_E)));
+  if (aerr != cudaSuccess) return cuda_fail(aerr);
+  const long long tiles = list_tiles(a.cap, a.E) * ((a.N + S::cols - 1) / S::cols);
+  const unsigned grid = static_cast<unsigned>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
+  const cudaError_t err = launch_dependent(mx4_gemm_kernel<MODE>, grid, THREADS, S::smem(a.E), s, m, a);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
 }  // namespace
@@ -744,9 +856,8 @@ moe_status_t moe_mx4_prepare_weights(const moe_bf16* w_ug, const moe_bf16* w_dow
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Weights w = carve_weights(mxw, E, d, h);
   const long long ug_rows = 2LL * E * h;
-  mx4_quant_rows_kernel<<<row_blocks(ug_rows), 256, 0, s>>>(reinterpret_cast<const uint4*>(w_ug), ug_rows, d, nullptr, E,
-                                                            h, tiles128(h), reinterpret_cast<uint32_t*>(w.ug_q), w.ug_sf,
-                                                            2LL * E * tiles128(h), nullptr);
+  MOE_MX4_ROWS(mx4_quant_rows_kernel, ug_rows, d, s, reinterpret_cast<const uint4*>(w_ug), ug_rows, d, nullptr, E, h,
+               tiles128(h), reinterpret_cast<uint32_t*>(w.ug_q), w.ug_sf, 2LL * E * tiles128(h), nullptr);
   if ((st = launched()) != MOE_OK) return st;
   const long long items = static_cast<long long>(E) * d * 4 * mx4_kc(h);
   const int blocks = static_cast<int>(std::max(1LL, std::min((items + 255) / 256, 16LL * device_sm_count())));
@@ -764,9 +875,9 @@ moe_status_t moe_mx4_quantize_rows(const moe_bf16* x, const int32_t* offsets, in
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_device();
   if (st != MOE_OK || cap == 0) return st;
-  mx4_quant_rows_kernel<<<row_blocks(cap), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      reinterpret_cast<const uint4*>(x), cap, K, offsets, E, 0, 0, reinterpret_cast<uint32_t*>(q), sf,
-      list_tiles(cap, E), dev_status);
+  MOE_MX4_ROWS(mx4_quant_rows_kernel, static_cast<long long>(cap), K, reinterpret_cast<cudaStream_t>(stream),
+               reinterpret_cast<const uint4*>(x), cap, K, offsets, E, 0, 0, reinterpret_cast<uint32_t*>(q), sf,
+               list_tiles(cap, E), dev_status);
   return launched();
 }
 
@@ -779,9 +890,9 @@ moe_status_t moe_mx4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const 
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_device();
   if (st != MOE_OK || cap == 0) return st;
-  mx4_dequant_rows_kernel<<<row_blocks(cap), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      reinterpret_cast<const uint32_t*>(q), sf, cap, K, offsets, E, reinterpret_cast<uint4*>(x), list_tiles(cap, E),
-      dev_status);
+  MOE_MX4_ROWS(mx4_dequant_rows_kernel, static_cast<long long>(cap), K, reinterpret_cast<cudaStream_t>(stream),
+               reinterpret_cast<const uint32_t*>(q), sf, cap, K, offsets, E, reinterpret_cast<uint4*>(x),
+               list_tiles(cap, E), dev_status);
   return launched();
 }
 
@@ -796,9 +907,9 @@ moe_status_t moe_permute_mxfp4(const moe_bf16* x, const int32_t* inv_map, const 
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_device();
   if (st != MOE_OK || n == 0) return st;
-  mx4_permute_kernel<<<row_blocks(T), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      reinterpret_cast<const uint4*>(x), inv_map, offsets, E, T, top_k, d, reinterpret_cast<uint32_t*>(q), sf,
-      list_tiles(n, E), dev_status);
+  MOE_MX4_ROWS(mx4_permute_kernel, static_cast<long long>(T), d, reinterpret_cast<cudaStream_t>(stream),
+               reinterpret_cast<const uint4*>(x), inv_map, offsets, E, T, top_k, d, reinterpret_cast<uint32_t*>(q), sf,
+               list_tiles(n, E), dev_status);
   return launched();
 }
 
@@ -819,10 +930,6 @@ moe_status_t moe_grouped_swiglu_fwd_mxfp4(const uint8_t* xq, const uint8_t* xsf,
   const Weights w = carve_weights(mxw, E, d, h);
   uint8_t* pq = static_cast<uint8_t*>(ws);
   uint8_t* psf = pq + codes_bytes(cap, h);
-  Maps up, down;
-  if (!make_map_u8_rows2d(&up.a, xq, cap, d / 2, BM) || !make_map_u8_weight3d(&up.b, w.ug_q, E, 2LL * h, d / 2, 128) ||
-      !make_map_u8_rows2d(&down.a, pq, cap, h / 2, BM) || !make_map_u8_weight3d(&down.b, w.dn_q, E, d, h / 2, BN))
-    return cuda_fail(cudaErrorInvalidValue);
   Args a{};
   a.offsets = offsets;
   a.E = E;
@@ -840,7 +947,7 @@ moe_status_t moe_grouped_swiglu_fwd_mxfp4(const uint8_t* xq, const uint8_t* xsf,
   a.dbg_a_tiles = list_tiles(cap, E);
   a.dbg_b_tiles = 2LL * E * tiles128(h);
   a.status = dev_status;
-  if ((st = launch_gemm<MX4_UP>(up, a, s)) != MOE_OK) return st;
+  if ((st = launch_gemm<MX4_UP>(xq, w.ug_q, 2LL * h, a, s)) != MOE_OK) return st;
   a.N = d;
   a.K = h;
   a.sfa = psf;
@@ -849,8 +956,7 @@ moe_status_t moe_grouped_swiglu_fwd_mxfp4(const uint8_t* xq, const uint8_t* xsf,
   a.tiles_b = down_tiles(d);
   a.dbg_b_tiles = static_cast<long long>(E) * down_tiles(d);
   a.y = reinterpret_cast<bf16*>(y);
-  a.vec32 = aligned(y, 32) ? 1 : 0;
-  return launch_gemm<MX4_DOWN>(down, a, s);
+  return launch_gemm<MX4_DOWN>(pq, w.dn_q, d, a, s);
 }
 
 }  // extern "C"

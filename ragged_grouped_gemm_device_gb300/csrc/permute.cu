@@ -68,15 +68,23 @@ __global__ void __launch_bounds__(THREADS) zero_dropped_rows_kernel(const int32_
 
 // out[t] = sum_j w[t,j] * y[inv[t,j]] over slots with inv >= 0, fp32 in slot order, one bf16
 // rounding (gather + reduction in place of the scatter-add, "grouped_mm" agent doc).
-__global__ void __launch_bounds__(THREADS) combine_kernel(const uint4* __restrict__ y,
-                                                          const int32_t* __restrict__ inv,
-                                                          const float* __restrict__ weights,
-                                                          int T, int k, int vec,
-                                                          uint4* __restrict__ out) {
+__global__ void __launch_bounds__(THREADS, 4) combine_kernel(const uint4* y,
+                                                          const int32_t* inv,
+                                                          const float* weights,
+                                                          int T, int k, int vec, int split,
+                                                          uint4* out) {
   const int lane = threadIdx.x & 31;
   const int gw = blockIdx.x * WARPS + (threadIdx.x >> 5);
   const int nw = gridDim.x * WARPS;
-  for (long long t = gw; t < T; t += nw) {
+  grid_wait();  // launched ahead of the end of the kernel that writes y
+  y = after_wait(y);
+  inv = after_wait(inv);
+  weights = after_wait(weights);
+  // `split` warps a token, each `per` of its vectors (1: the whole row)
+  const int per = ((vec + 32 * split - 1) / (32 * split)) * 32;
+  for (long long it = gw; it < static_cast<long long>(T) * split; it += nw) {
+    const long long t = it / split;
+    const int first = static_cast<int>(it - t * split) * per, end = min(vec, first + per);
     // lane j < k holds slot j's row and weight
     int my_p = -1;
     float my_w = 0.f;
@@ -85,9 +93,9 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const uint4* __restric
       my_w = weights ? __ldg(weights + static_cast<size_t>(t) * k + lane) : 1.0f;
     }
     // every lane runs the same number of iterations: the shuffles need the whole warp
-    for (int v0 = 0; v0 < vec; v0 += 32) {
+    for (int v0 = first; v0 < end; v0 += 32) {
       const int v = v0 + lane;
-      const bool active = v < vec;
+      const bool active = v < end;
       float acc[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] = 0.f;
@@ -323,9 +331,16 @@ moe_status_t launch_combine(const void* y, const int32_t* inv_map, const float* 
         static_cast<const bf16*>(y), inv_map, weights, T, k, d, static_cast<bf16*>(out));
     return last_launch();
   }
-  combine_kernel<<<grid_for_rows(combine_kernel, T), THREADS, 0, s>>>(
-      static_cast<const uint4*>(y), inv_map, weights, T, k, d / 8, static_cast<uint4*>(out));
-  return last_launch();
+  // A token's row is one warp's, which takes it 256 columns at a time, each a wait for y; with
+  // fewer tokens than 64 for each SM, several warps share a row (T = 1, d = 2048: 6.8 us with one
+  // warp, 2.3 with eight). The sums are per element, so the result is the same.
+  const int vec = d / 8;
+  const int split = std::max(1, std::min((vec + 31) / 32, 64 * device_sm_count() / T));
+  const long long rows = static_cast<long long>(T) * split;  // below 2^31: at most max(T, 64 SMs)
+  const cudaError_t err = launch_dependent(combine_kernel, grid_for_rows(combine_kernel, rows), THREADS, 0, s,
+                                           static_cast<const uint4*>(y), inv_map, weights, T, k, vec, split,
+                                           static_cast<uint4*>(out));
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
 moe_status_t launch_pitch_repack(const void* src, void* dst, bool fp32, long long rows_out,
