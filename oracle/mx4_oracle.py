@@ -11,7 +11,7 @@ MAGNITUDES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 def quantize(v):
     """[..., K] -> (codes uint8 [..., K] in 0..15, scale codes uint8 [..., K / 32])."""
     v = np.asarray(v, np.float64)
-    b = v.reshape(*v.shape[:-1], -1, BLOCK)
+    b = v.reshape(*v.shape[:-1], v.shape[-1] // BLOCK, BLOCK)
     bad = ~np.isfinite(b).all(axis=-1)
     b = np.where(bad[..., None], 0.0, b)
     top = np.abs(b).max(axis=-1)
@@ -30,7 +30,7 @@ def quantize(v):
 
 def values(codes, scale):
     """What codes and scale codes stand for; NaN where the scale is 255."""
-    b = codes.reshape(*codes.shape[:-1], -1, BLOCK)
+    b = codes.reshape(*codes.shape[:-1], codes.shape[-1] // BLOCK, BLOCK)
     x = np.where(scale == 255, np.nan, np.exp2(np.minimum(scale, 254).astype(np.float64) - 127.0))
     v = MAGNITUDES[b & 7] * np.where(b & 8, -1.0, 1.0) * x[..., None]
     return v.reshape(codes.shape)

@@ -95,3 +95,50 @@ class ExpertLayer:
                              stream, inv_map=self.inv_map, dw_route=self.dw_route)
         _lib.moe_unpermute_combine(self.dxp, self.inv_map, None, T, k, d, self.dx, stream)
         return self.dx, self.dw_ug, self.dw_down, self.dw_route
+
+
+class Mxfp4ExpertLayer:
+    """The forward of one SwiGLU expert layer on 4-bit weights and activations (serving; no backward).
+
+    Takes the bf16 weights of ExpertLayer, quantizes them once (`weights` holds the codes and
+    scales; the bf16 tensors are not kept) and runs route -> gather + quantize -> grouped products
+    -> combine. d and h multiples of 32."""
+
+    def __init__(self, w_ug: torch.Tensor, w_down: torch.Tensor, stream=None):
+        E, two_h, d = w_ug.shape
+        assert w_down.shape == (E, two_h // 2, d)
+        assert w_ug.dtype == torch.bfloat16 and w_down.dtype == torch.bfloat16
+        self.E, self.d, self.h = E, d, two_h // 2
+        self.device = w_ug.device
+        n = _lib.moe_workspace_bytes(_lib.OP_MX4_WEIGHTS, 0, 1, E, d, self.h)
+        self.weights = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        _lib.moe_mx4_prepare_weights(w_ug.contiguous(), w_down.contiguous(), E, d, self.h, self.weights, stream)
+        self._key = None
+        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def _buffers(self, T: int, k: int):
+        if self._key == (T, k):
+            return
+        E, d, h, n = self.E, self.d, self.h, T * k
+        new = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device=self.device)  # noqa: E731
+        room = lambda op: new(max(1, _lib.moe_workspace_bytes(op, T, k, E, d, h)), dtype=torch.uint8)  # noqa: E731
+        self.counts, self.offsets = new(E, dtype=torch.int32), new(E, dtype=torch.int32)
+        self.sorted_src, self.inv_map = new(max(n, 1), dtype=torch.int32), new(max(n, 1), dtype=torch.int32)
+        self.route_ws, self.fwd_ws = room(_lib.OP_ROUTE), room(_lib.OP_MX4_FWD)
+        self.xq, self.xsf = new(max(n, 1), d // 2, dtype=torch.uint8), room(_lib.OP_MX4_ROW_SCALES)
+        self.y, self.out = new(max(n, 1), d, dtype=torch.bfloat16), new(T, d, dtype=torch.bfloat16)
+        self._key = (T, k)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, stream=None):
+        """x [T, d] bf16, ids [T, k] int32, weights [T, k] fp32 -> out [T, d] bf16."""
+        x, ids, weights = _dense(x), _dense(ids), _dense(weights)
+        T, k = ids.shape
+        self._buffers(T, k)
+        E, d, h, n = self.E, self.d, self.h, T * k
+        _lib.moe_route_offsets(ids, T, k, E, self.counts, self.offsets, self.sorted_src, self.inv_map,
+                               self.route_ws, stream)
+        _lib.moe_permute_mxfp4(x, self.inv_map, self.offsets, T, k, E, d, self.xq, self.xsf, self.status, stream)
+        _lib.moe_grouped_swiglu_fwd_mxfp4(self.xq, self.xsf, self.offsets, E, n, d, h, self.weights, self.y,
+                                          self.fwd_ws, self.status, stream)
+        _lib.moe_unpermute_combine(self.y, self.inv_map, weights, T, k, d, self.out, stream)
+        return self.out

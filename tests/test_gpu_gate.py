@@ -80,6 +80,14 @@ def test_matches_the_reference(lib, T, E, k, dtype, renorm):
     Gate(_logits(T, E, dtype), None, k, renorm).run().check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E,k", [(128, 8), (200, 9), (512, 4), (1000, 3), (100, 5)])
+def test_many_tokens_at_every_width(lib, E, k, dtype):
+    """Enough tokens for the narrow lane groups of the forward (E = 100: rows that are read one element at
+    a time stay at full width)."""
+    Gate(_logits(5000, E, dtype), None, k, E % 200 == 0).run().check()
+
+
 @pytest.mark.parametrize("renorm", [True, False])
 def test_masked_tokens_and_excluded_experts(lib, renorm):
     """Padding tokens, experts at -inf (fewer than k left in some rows, none in one), the type's lowest
