@@ -3,7 +3,8 @@
 Argument marshalling only: each function takes torch tensors (or None for nullable pointers),
 passes their device pointers and the current CUDA stream to the C entry point of the same name,
 and raises MoEError on a non-OK status. Every step runs in the library's CUDA kernels; there is
-no fallback of any kind, and loading fails loudly when the library has not been built.
+no fallback of any kind, and loading fails loudly when the library has not been built. The calls of
+a decode step are marshalled by a small CPython extension where it has been built (_install_binding).
 """
 from __future__ import annotations
 
@@ -116,7 +117,36 @@ def load(path: str = None):
         if path is None:
             path = DEBUG_LIB_PATH if os.environ.get("MOE_GG_DEBUG_LIB") == "1" else LIB_PATH
         _lib = open_library(path)
+        _install_binding()
     return _lib
+
+
+# calls that the compiled binding takes over (csrc/binding.c)
+COMPILED = ("moe_layer_norm_fwd", "moe_layer_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_mx4_quantize_rows",
+            "moe_mx4_dequantize_rows", "moe_permute_mxfp4", "moe_grouped_swiglu_fwd_mxfp4", "moe_unpermute_combine",
+            "moe_route_offsets")
+PYTHON_BINDING = {}  # the functions that they replaced
+
+
+def _install_binding():
+    """Replace the functions of COMPILED by the CPython extension's, which make the same checks and call
+    the same entry points of the loaded library with less marshalling time. Without the extension (or
+    without torch, when only host functions are called) the Python functions below stay."""
+    import sys
+    torch = sys.modules.get("torch")
+    if torch is None or not torch.cuda.is_available():
+        return
+    try:
+        from . import _binding
+    except ImportError:
+        return
+
+    _binding.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in COMPILED}, torch.bfloat16,
+                  torch.float32, torch.int32, torch.uint8, torch.bool, _check, torch._C._cuda_getCurrentRawStream,
+                  torch._C._cuda_getDevice)
+    for n in COMPILED:
+        PYTHON_BINDING[n] = globals()[n]
+        globals()[n] = getattr(_binding, n)
 
 
 def _ptr(t):

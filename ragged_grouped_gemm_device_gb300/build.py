@@ -4,7 +4,10 @@ newer than the library (or when forced).
 
 build(debug=True) compiles the same sources with -DMOE_GG_DEBUG into libmoe_gg_debug.so (same
 ABI): device-side bounds checks at the data-dependent global accesses and a wait for the stream
-at the end of every entry point, read back with moe_debug_report()."""
+at the end of every entry point, read back with moe_debug_report().
+
+build_binding() compiles csrc/binding.c, the CPython extension that marshals the calls of a decode
+step, next to this file; without a C compiler or Python's headers the ctypes binding does it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -12,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -79,6 +83,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), debug: boo
     return lib
 
 
+BINDING = os.path.join(PKG, "_binding.so")
+
+
+def build_binding(force: bool = False):
+    """Path of the CPython extension, or None where it cannot be built (no compiler or headers)."""
+    src = os.path.join(CSRC, "binding.c")
+    deps = [src, os.path.join(ROOT, "include", "moe_gg.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
+        return BINDING
+    cc, inc = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
+    if cc is None or not os.path.exists(os.path.join(inc, "Python.h")):
+        return None
+    tmp = BINDING + ".tmp"
+    r = subprocess.run([cc, "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I", inc, src, "-o", tmp],
+                       capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 if __name__ == "__main__":
     import sys
     print(build(force="--force" in sys.argv, verbose=True, debug="--debug" in sys.argv))
+    print(build_binding(force="--force" in sys.argv))
