@@ -247,16 +247,17 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
        t0 += static_cast<long long>(gridDim.x) * WARPS * GROUPS) {
     const long long t = t0 + lane / G;
     const bool in = t < a.T;
-    const bool live = in && (a.mask == nullptr || __ldg(a.mask + t) != 0);
-    const T* row = static_cast<const T*>(a.logits) + (live ? t : 0) * a.ld;
+    // the row is loaded whether the token takes part or not: the two loads then wait together
+    const T* row = static_cast<const T*>(a.logits) + (in ? t : 0) * a.ld;
     float v[NL][8];
+#pragma unroll
+    for (int l = 0; l < NL; ++l) load8<VEC>(row, in ? 8 * (G * l + gl) : a.E, a.E, v[l]);
+    const bool live = in && (a.mask == nullptr || __ldg(a.mask + t) != 0);
     float m = -INFINITY;
 #pragma unroll
-    for (int l = 0; l < NL; ++l) {
-      load8<VEC>(row, live ? 8 * (G * l + gl) : a.E, a.E, v[l]);
+    for (int l = 0; l < NL; ++l)
 #pragma unroll
       for (int j = 0; j < 8; ++j) m = fmaxf(m, v[l][j]);  // ignores NaN
-    }
     m = group_max<G>(m);
     const float base = m > -INFINITY ? m : 0.f;
     K head[NL];
@@ -372,46 +373,63 @@ __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(const GateArgs a) {
 
 __device__ __forceinline__ float warp_sum(float v) { return group_sum<32>(v); }
 
-// Adds the blocks' partial rows in order: 32 experts a block, 32 threads an expert over the rows
-// (coalesced over the experts), added in thread order. The last block to finish adds the blocks'
-// shares of the balance loss in block order and writes the losses.
+// Adds the blocks' partial rows in a fixed order: eight experts a block, 128 threads an expert over
+// the rows (a 32-byte sector a row). The last block to finish adds the blocks' shares of the
+// balance loss in block order and writes the losses.
+constexpr int STAT_COLS = 8;
 __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int blocks, int k, int E,
                                                           int32_t* __restrict__ counts, int32_t* __restrict__ n_valid,
                                                           float* __restrict__ prob_sum, float* __restrict__ loss,
                                                           unsigned* ticket, float* share) {
-  __shared__ float s_p[32][33];
-  __shared__ int s_c[32][33];
+  __shared__ float s_p[32][STAT_COLS];
+  __shared__ int s_c[32][STAT_COLS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int cx = threadIdx.x % STAT_COLS, ry = threadIdx.x / STAT_COLS;
+  const int words = part_words(E);
+  const int e = blockIdx.x * STAT_COLS + cx;
   grid_wait();  // launched ahead of the end of the forward kernel
   part = after_wait(part);
-  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
-  const int words = part_words(E);
   const int* ipart = reinterpret_cast<const int*>(part);
-  const int e = blockIdx.x * 32 + cx;
   float p = 0.f;
   int c = 0;
-  if (e < E)
-    for (int b = ry; b < blocks; b += 32) {
+  if (e < E) {
+#pragma unroll 5
+    for (int b = ry; b < blocks; b += 1024 / STAT_COLS) {
       p += part[static_cast<size_t>(b) * words + e];
       c += ipart[static_cast<size_t>(b) * words + E + e];
     }
-  s_p[ry][cx] = p;
-  s_c[ry][cx] = c;
+  }
+#pragma unroll
+  for (int o = STAT_COLS; o < 32; o <<= 1) {
+    p += __shfl_xor_sync(FULL, p, o);
+    c += __shfl_xor_sync(FULL, c, o);
+  }
+  if (lane < STAT_COLS) {
+    s_p[warp][lane] = p;
+    s_c[warp][lane] = c;
+  }
   __syncthreads();
-  if (ry != 0) return;
+  if (warp != 0) return;
   p = 0.f;
   c = 0;
 #pragma unroll
-  for (int r = 0; r < 32; ++r) {
-    p += s_p[r][cx];
-    c += s_c[r][cx];
+  for (int r = 0; r < 8; ++r) {  // lane group g adds warps 8g..8g+7
+    p += s_p[(lane / STAT_COLS) * 8 + r][cx];
+    c += s_c[(lane / STAT_COLS) * 8 + r][cx];
   }
-  if (e < E) {
+#pragma unroll
+  for (int o = STAT_COLS; o < 32; o <<= 1) {
+    p += __shfl_xor_sync(FULL, p, o);
+    c += __shfl_xor_sync(FULL, c, o);
+  }
+  const bool mine = lane < STAT_COLS && e < E;
+  if (mine) {
     prob_sum[e] = p;
     counts[e] = c;
   }
-  const float bal = warp_sum(e < E ? static_cast<float>(c) * p : 0.f);
+  const float bal = warp_sum(mine ? static_cast<float>(c) * p : 0.f);
   unsigned last = 0u;
-  if (cx == 0) {
+  if (lane == 0) {
     share[blockIdx.x] = bal;
     __threadfence();
     last = atomicAdd(ticket, 1u) == gridDim.x - 1 ? 1u : 0u;
@@ -420,14 +438,16 @@ __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int
   __threadfence();
   float z = 0.f;
   int n = 0;
-  for (int b = cx; b < blocks; b += 32) {
+  for (int b = lane; b < blocks; b += 32) {
     z += part[static_cast<size_t>(b) * words + 2 * E];
     n += ipart[static_cast<size_t>(b) * words + 2 * E + 1];
   }
   z = warp_sum(z);
   n = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(n)));
-  const float total = warp_sum(cx < gridDim.x ? __ldcg(share + cx) : 0.f);  // E <= 1024: at most 32 blocks
-  if (cx == 0) {
+  float total = 0.f;
+  for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) total += __ldcg(share + b);
+  total = warp_sum(total);
+  if (lane == 0) {
     const float nf = static_cast<float>(n);
     *n_valid = n;
     loss[0] = n > 0 ? static_cast<float>(E) / (static_cast<float>(k) * nf) * (total / nf) : 0.f;
@@ -488,12 +508,12 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
        t0 += static_cast<long long>(gridDim.x) * WARPS * GROUPS) {
     const long long t = t0 + lane / G;
     const bool in = t < a.T;
-    const float lse = in ? __ldg(a.lse + t) : -INFINITY;
-    const bool part = lse != -INFINITY;  // else the token took no part: its gradient is 0
-    const T* row = static_cast<const T*>(a.logits) + (part ? t : 0) * a.ld;
+    // every load of the token before any of them is waited for
+    const T* row = static_cast<const T*>(a.logits) + (in ? t : 0) * a.ld;
     float p[NL][8];
 #pragma unroll
-    for (int l = 0; l < NL; ++l) load8<VEC>(row, part ? 8 * (G * l + gl) : a.E, a.E, p[l]);
+    for (int l = 0; l < NL; ++l) load8<VEC>(row, in ? 8 * (G * l + gl) : a.E, a.E, p[l]);
+    const float lse = in ? __ldg(a.lse + t) : -INFINITY;
     int id[NS];
     float w[NS], dw[NS], s = 0.f;
 #pragma unroll
@@ -501,13 +521,17 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
       const int slot = i * G + gl;
       id[i] = -1;
       w[i] = dw[i] = 0.f;
-      if (part && slot < a.k && a.d_weights != nullptr) {
+      if (in && slot < a.k && a.d_weights != nullptr) {
         id[i] = __ldg(a.ids + t * a.k + slot);
         w[i] = __ldg(a.weights + t * a.k + slot);
         dw[i] = __ldg(a.d_weights + t * a.k + slot);
-        if (id[i] < 0 || id[i] >= a.E) id[i] = -1;
-        else s = fmaf(w[i], dw[i], s);
       }
+    }
+    const bool part = lse != -INFINITY;  // else the token took no part: its gradient is 0
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+      if (!part || id[i] < 0 || id[i] >= a.E) id[i] = -1;
+      else s = fmaf(w[i], dw[i], s);
     }
     s = group_sum<G>(s);
 #pragma unroll
@@ -531,7 +555,7 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(const GateBwdArgs a) 
       const float4 x = add[0], y = add[1];
       const float top[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[l][j] = fmaf(p[l][j], c[l][j] + shift, top[j]);
+      for (int j = 0; j < 8; ++j) p[l][j] = part ? fmaf(p[l][j], c[l][j] + shift, top[j]) : 0.f;
       store8<VEC>(out, in ? 8 * (G * l + gl) : a.E, a.E, p[l]);
     }
     __syncwarp();
@@ -578,7 +602,7 @@ struct Width {
 Width width_for(int E, bool many) {
   if (E <= 64) return {1, 8};
   if (E <= 128) return many ? Width{2, 8} : Width{1, 16};
-  if (E <= 256) return many ? Width{2, 16} : Width{1, 32};
+  if (E <= 256) return many ? Width{4, 8} : Width{1, 32};
   if (E <= 512) return many ? Width{4, 16} : Width{2, 32};
   return {4, 32};
 }
@@ -588,6 +612,7 @@ moe_status_t by_width_fwd(const GateArgs& a, Width w, int blocks, cudaStream_t s
   if constexpr (VEC) {
     if (w.lists == 2 && w.lanes == 8) return launch_fwd<T, 2, 8, VEC>(a, blocks, s);
     if (w.lists == 2 && w.lanes == 16) return launch_fwd<T, 2, 16, VEC>(a, blocks, s);
+    if (w.lists == 4 && w.lanes == 8) return launch_fwd<T, 4, 8, VEC>(a, blocks, s);
     if (w.lists == 4 && w.lanes == 16) return launch_fwd<T, 4, 16, VEC>(a, blocks, s);
   }
   if (w.lanes == 8) return launch_fwd<T, 1, 8, VEC>(a, blocks, s);
@@ -623,7 +648,7 @@ bool rows16(const void* p, long long ld, int E, int dtype) {
 
 // the blocks' partial rows, then the statistics kernel's block counter and shares
 size_t gate_workspace_bytes(int T, int E) {
-  return (static_cast<size_t>(blocks_for(T, 32, MAX_BLOCKS)) * part_words(E) + 1 + 32) * sizeof(float);
+  return (static_cast<size_t>(blocks_for(T, 32, MAX_BLOCKS)) * part_words(E) + 1 + MAX_E / STAT_COLS) * sizeof(float);
 }
 
 }  // namespace moe
@@ -667,12 +692,13 @@ moe_status_t moe_gate_fwd(const void* logits, int dtype, long long ld, const uin
   a.part = stats ? static_cast<float*>(ws) : nullptr;
   const bool vec = rows16(logits, ld, E, dtype);
   const Width w = width_for(E, vec && T >= MAX_BLOCKS * WARPS);
-  const int blocks = blocks_for(T, w.lanes, MAX_BLOCKS);
+  // four lists a lane leave registers for two blocks on an SM
+  const int blocks = blocks_for(T, w.lanes, w.lists == 4 ? MAX_BLOCKS / 2 : MAX_BLOCKS);
   a.ticket = stats ? static_cast<unsigned*>(ws) + static_cast<size_t>(blocks) * part_words(E) : nullptr;
   if (dtype == MOE_DTYPE_BF16) st = vec ? by_width_fwd<bf16, true>(a, w, blocks, s) : by_width_fwd<bf16, false>(a, w, blocks, s);
   else st = vec ? by_width_fwd<float, true>(a, w, blocks, s) : by_width_fwd<float, false>(a, w, blocks, s);
   if (st != MOE_OK || !stats) return st;
-  const cudaError_t err = launch_dependent(gate_stats_kernel, (E + 31) / 32, 1024, 0, s, a.part, blocks, top_k, E, counts,
+  const cudaError_t err = launch_dependent(gate_stats_kernel, (E + STAT_COLS - 1) / STAT_COLS, 1024, 0, s, a.part, blocks, top_k, E, counts,
                                            n_valid, prob_sum, loss, a.ticket, reinterpret_cast<float*>(a.ticket + 1));
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }

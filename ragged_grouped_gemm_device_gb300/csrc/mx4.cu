@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
       mbar_init(smem_u32(&ctl->empty[s]), 1);
     }
     mbar_init(smem_u32(&ctl->tfull), 1);
-    mbar_init(smem_u32(&ctl->tempty), 32 * EPI_WARPS);
+    mbar_init(smem_u32(&ctl->tempty), EPI_WARPS);  // one arrival per epilogue warp
     mbar_init(smem_u32(&ctl->done), 1);
     ctl->abort_flag = 0;
     fence_mbar_init();
@@ -635,14 +635,18 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
     const int q = warp & 3, half = (warp - 2) >> 2;
     const int r_in = q * 32 + lane;
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    auto release_acc = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty));
+    };
     uint32_t n = 0;
     for (int t = blockIdx.x; t < sc.total; t += gridDim.x, ++n) {
       const Tile ti = decode_tile(sc, t, COLS);
       if (!warp_all(mbar_wait(smem_u32(&ctl->tfull), n & 1u, abort_flag, args.status, tmo))) break;
       tc_fence_after();
       if (q * 32 >= ti.rows) {  // warp-uniform: none of this quadrant's rows
-        tc_fence_before();
-        mbar_arrive(smem_u32(&ctl->tempty));
+        release_acc();
         continue;
       }
       const long long row = static_cast<long long>(ti.row0) + r_in;
@@ -660,8 +664,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
         }
 #pragma unroll
         for (int i = 0; i < 2 * BLOCKS; ++i) tmem_ld_wait2(g[i], u[i]);
-        tc_fence_before();
-        mbar_arrive(smem_u32(&ctl->tempty));
+        release_acc();
         if (!rv || !MOE_DBG_IN(DBG_GG_MXSF, ti.g, args.dbg_a_tiles)) continue;
 #pragma unroll
         for (int b = 0; b < BLOCKS; ++b) {
@@ -714,8 +717,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
             p[8 * i + 8 + j] = pack_bf16x2(__uint_as_float(v1[2 * j]), __uint_as_float(v1[2 * j + 1]));
           }
         }
-        tc_fence_before();
-        mbar_arrive(smem_u32(&ctl->tempty));
+        release_acc();
         uint8_t* sbuf = staging + (warp - 2) * OUT_BYTES;
         const int rows_here = min(32, ti.rows - q * 32);
         const unsigned valid = __ballot_sync(0xffffffffu, rv);

@@ -171,6 +171,14 @@ def test_many_tokens_repeat_bit_for_bit_and_route(lib):
     assert torch.equal(counts, g.counts) and int(offsets[-1]) == int(mask.sum()) * k
 
 
+def test_a_nan_loss_gradient_leaves_masked_tokens_alone(lib):
+    mask = torch.tensor([True, False, True, False], device="cuda")
+    g = Gate(_logits(4, 16, "bf16"), mask, 2, False)
+    g.d_loss[0] = float("nan")
+    g.run()
+    assert torch.isnan(g.dlogits[mask]).all() and (g.dlogits[~mask] == 0).all()
+
+
 def test_no_tokens(lib):
     g = Gate(torch.empty(0, 8, device="cuda"), None, 2, True).run()
     assert (g.counts == 0).all() and int(g.n) == 0 and (g.prob_sum == 0).all() and (g.loss == 0).all()
