@@ -109,14 +109,17 @@ __device__ __forceinline__ long long item_row(long long it, int pieces, bool sma
 // Rows along K. With offsets: the rows p < M of a problem list; else `rows` rows of weights in
 // groups of `sub` rows, ntpad tiles a group.
 template <int PASSES>
-__global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __restrict__ src, long long rows, int K,
-                                                             const int32_t* __restrict__ offsets, int E, int sub,
+__global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* src, long long rows, int K,
+                                                             const int32_t* offsets, int E, int sub,
                                                              int ntpad, uint32_t* __restrict__ q,
                                                              uint8_t* __restrict__ sf, long long sf_tiles,
                                                              int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
-  grid_release();  // the product's prologue may start
+  grid_release();
+  grid_wait();  // launched ahead of the end of the kernel before
+  src = after_wait(src);
+  offsets = after_wait(offsets);
   const bool list = offsets != nullptr;
   if (list && !load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
   const long long M = list ? s_end[E - 1] : rows;
@@ -156,14 +159,18 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* __rest
 // The permute's gather and the quantization along d in one pass, token by token: a token's row is
 // read and quantized once and its codes and scales are written to the rows of its top_k slots.
 template <int PASSES>
-__global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* __restrict__ x,
-                                                          const int32_t* __restrict__ inv_map,
-                                                          const int32_t* __restrict__ offsets, int E, int T, int k,
+__global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* x,
+                                                          const int32_t* inv_map,
+                                                          const int32_t* offsets, int E, int T, int k,
                                                           int d, uint32_t* __restrict__ q, uint8_t* __restrict__ sf,
                                                           long long sf_tiles, int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
-  grid_release();  // the product's prologue may start
+  grid_release();
+  grid_wait();  // launched ahead of the end of the kernel before
+  x = after_wait(x);
+  inv_map = after_wait(inv_map);
+  offsets = after_wait(offsets);
   const long long n = static_cast<long long>(T) * k;
   if (!load_problem_tiles(offsets, E, n, s_end, s_pre, status)) return;
   const int M = s_end[E - 1];
@@ -220,14 +227,19 @@ __device__ __forceinline__ float e2m1_value(uint32_t c) {
 // The bf16 values that rows p < M of codes and scales stand for (exact: an E2M1 value times a
 // power of two has two significant bits); a block with a NaN scale reads as NaN.
 template <int PASSES>
-__global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* __restrict__ q,
-                                                               const uint8_t* __restrict__ sf, long long rows, int K,
-                                                               const int32_t* __restrict__ offsets, int E,
+__global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* q,
+                                                               const uint8_t* sf, long long rows, int K,
+                                                               const int32_t* offsets, int E,
                                                                uint4* __restrict__ x, long long sf_tiles,
                                                                int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
   __shared__ uint32_t pair[256];  // the bf16 values of the two codes of a byte
+  grid_release();
+  grid_wait();  // launched ahead of the end of the kernel before
+  q = after_wait(q);
+  sf = after_wait(sf);
+  offsets = after_wait(offsets);
   if (!load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
   pair[threadIdx.x] = pack_bf16x2(e2m1_value(threadIdx.x & 15u), e2m1_value(threadIdx.x >> 4));
   __syncthreads();
@@ -310,18 +322,28 @@ __global__ void __launch_bounds__(256) mx4_quant_cols_kernel(const bf16* __restr
 // Persistent grouped GEMM on block-scaled 4-bit operands: the problem list, tile order, roles and
 // bounded waits of the grouped GEMM (grouped_gemm.cu), one CTA per SM.
 //   warp 0      TMA producer of A (the tile's rows x 256 elements of K, and their scale atoms)
-//   warp 1      tensor-memory allocator and MMA issuer: per stage, the scale atoms into tensor
-//               memory and four block-scaled MMAs of K = 64
-//   warps 2..9  epilogue, two per lane quadrant
-//   warp 10     TMA producer of B
+//   warp 1      tensor-memory allocator and MMA issuer: per stage four block-scaled MMAs of K = 64
+//               (MX4_DOWN: after copies of the scale atoms into tensor memory)
+//   warp 2      TMA producer of B
+//   warps 4..7  MX4_UP: scale atoms from the stage into tensor memory
+//   the last 8  epilogue, two per lane quadrant
 // MX4_UP:   B = BN / 2 gate and BN / 2 up rows of W_ug; the epilogue computes A = silu(gate) up in
 //           fp32 and quantizes it along h from fp32 (no bf16 rounding in between).
 // MX4_DOWN: B = BN rows of W_down^T; bf16 store, one rounding, staged through shared memory so
 //           that a warp writes whole 128-byte lines.
-// Tiles are 128 x 256: the products of many rows are held by the L2's output to the SMs, 51 KB of
-// codes and scales for each 128 x 256 x 256, and a wider tile has no room in tensor memory; those
-// of few rows by the weights' way from HBM (128-column tiles for them, twice as many, took 57 us
-// instead of 39 for 128 rows over 128 experts: an MMA of half the columns takes about as long).
+// What bounds it, at 131072 rows of 256 experts, d = 2048, h = 512 (up 153 us, 3.6 PFLOP/s; down
+// 149 us): up moves 1.7 GB of tiles through the L2's output to the SMs, 51 KB for each
+// 128 x 256 x 256, alone 116 us; its MMAs take 0.33 us a stage and about a microsecond a tile for
+// handing the accumulator over, alone 97 us; a ring of four stages does not hide one behind the
+// other entirely. Down writes 537 MB of y, 136 us at the rate of a kernel that only writes.
+// Tried and slower: pairs of CTAs (35 KB instead of 51, but 181 and 152 us, and 56 us against 36 for
+// 128 rows over 128 experts), 128-column tiles (57 us against 39 there: an MMA of half the columns
+// takes about as long), two accumulators of 192 columns (down 213 us), prefetching the next tile
+// into the L2 (up 186 us).
+// Scales: tcgen05.cp by the MMA issuer runs in order with the MMAs, 0.17 us a stage. In the up
+// product four warps write them with tcgen05.st while earlier MMAs run (up 162 -> 153 us; one row
+// in each of 8 experts 14.1 -> 13.4). In the down product, two or three stages a tile, the extra
+// hop costs more than it saves (149 against 160 us), so the issuer copies.
 // A row tile that its expert does not fill loads only its own rows, 16 at a time; the other rows
 // of the stage hold what was there before, and nothing reads the rows of the product that they
 // give (the rows of a product are independent).
@@ -336,8 +358,12 @@ constexpr int A_BOX = 16;                    // rows of the small box of A
 constexpr int SF_BYTES = 2 * 512;            // scale atoms of a 128-row tile: two chunks
 constexpr int SF_STAGE_BYTES = 3 * SF_BYTES; // A, and two tiles of B
 constexpr int EPI_WARPS = 8;
-constexpr int PRODUCER_B_WARP = 2 + EPI_WARPS;
-constexpr int THREADS = 32 * (PRODUCER_B_WARP + 1);
+constexpr int PRODUCER_B_WARP = 2;
+constexpr int SCALE_WARP = 4;                // MX4_UP: warps 4..7, one per lane quadrant
+// MX4_UP: registers a thread by warpgroup; the epilogue's two take over what the others leave of
+// the launch's 4 x 128.
+constexpr int ROLE_REGS = 72, SCALE_REGS = 56, EPI_REGS = 192;
+static_assert(ROLE_REGS + SCALE_REGS + 2 * EPI_REGS <= 4 * 128, "register shares");
 constexpr int TMEM_COLS = 512;
 constexpr int SF_TMEM_COL = 256;             // 32 columns of scales per stage after the accumulator
 constexpr int RASTER_M = 16;                 // row tiles per raster group
@@ -351,6 +377,9 @@ struct Shape {
   static constexpr int b_bytes = BN * STAGE_K / 2;
   static constexpr int stage_bytes = A_BYTES + b_bytes;
   static constexpr int stages = MODE == MX4_UP ? 4 : 3;
+  static constexpr bool scale_warps = MODE == MX4_UP;
+  static constexpr int epi_warp = scale_warps ? 8 : 4;
+  static constexpr int threads = 32 * (epi_warp + EPI_WARPS);
   static constexpr int out_bytes = MODE == MX4_DOWN ? EPI_WARPS * OUT_BYTES : 0;
   static constexpr int fixed = 1024 + stages * (stage_bytes + SF_STAGE_BYTES) + out_bytes + CTL_BYTES;
   static_assert(stages <= MAX_STAGES && SF_TMEM_COL + 32 * stages <= TMEM_COLS, "stages");
@@ -360,6 +389,7 @@ struct Shape {
 struct Ctl {
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
+  uint64_t scales[MAX_STAGES];
   uint64_t tfull;
   uint64_t tempty;
   uint64_t done;
@@ -430,7 +460,7 @@ __device__ __forceinline__ bool warp_all(bool v) { return __all_sync(0xffffffffu
 __device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 template <int MODE>
-__global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
+__global__ void __launch_bounds__(Shape<MODE>::threads, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
   typedef Shape<MODE> S;
   constexpr int COLS = S::cols;
   constexpr int STAGES = S::stages;
@@ -449,6 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&ctl->full[s]), 2);  // both producers
       mbar_init(smem_u32(&ctl->empty[s]), 1);
+      mbar_init(smem_u32(&ctl->scales[s]), 4);  // the scale warps
     }
     mbar_init(smem_u32(&ctl->tfull), 1);
     mbar_init(smem_u32(&ctl->tempty), EPI_WARPS);  // one arrival per epilogue warp
@@ -472,10 +503,10 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
 
   // ---- problem list
   const int32_t* offsets = after_wait(args.offsets);
-  for (int i = tid; i <= E; i += THREADS) offs[i] = i == 0 ? 0 : __ldg(offsets + i - 1);
+  for (int i = tid; i <= E; i += S::threads) offs[i] = i == 0 ? 0 : __ldg(offsets + i - 1);
   __syncthreads();
   bool bad = false;
-  for (int i = tid; i < E; i += THREADS) bad |= (offs[i + 1] < offs[i]) || (offs[i] < 0);
+  for (int i = tid; i < E; i += S::threads) bad |= (offs[i + 1] < offs[i]) || (offs[i] < 0);
   if (tid == 0) bad |= offs[E] > args.cap;
   if (warp == 0) {
     int carry = 0;
@@ -510,6 +541,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
   const uint32_t stage0 = smem_u32(smem);
   const uint32_t sf0 = smem_u32(sf_ring);
 
+  if (S::scale_warps && warp < SCALE_WARP) set_regs_down<ROLE_REGS>();
   if (warp == 0 || warp == PRODUCER_B_WARP) {
     // =========================================================== TMA producers
     if (lane == 0) {
@@ -581,19 +613,6 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
       grid_wait();     // the clock of its waits starts after the up product
       grid_release();  // the combine may start
     }
-    // scale atoms of stage s into its 32 columns: per 128-element chunk 4 columns of A, then 8 of B;
-    // a copy and the MMAs after it from one thread execute in issue order (copying a stage ahead of
-    // the MMAs was slower: the ring's stages are then held longer)
-    auto copy_scales = [&](int s) {
-      const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
-      const uint32_t sft = tmem_base + SF_TMEM_COL + s * 32;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        tmem_cp_32x128b_x4(sft + 12 * c, smem_desc_rows16(sfs + 512 * c));
-        tmem_cp_32x128b_x4(sft + 12 * c + 4, smem_desc_rows16(sfs + SF_BYTES + 512 * c));
-        tmem_cp_32x128b_x4(sft + 12 * c + 8, smem_desc_rows16(sfs + 2 * SF_BYTES + 512 * c));
-      }
-    };
     uint32_t it = 0, n = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x, ++n) {
@@ -602,13 +621,20 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
       tc_fence_after();
       for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const int s = it % STAGES;
-        ok = warp_all(mbar_wait(smem_u32(&ctl->full[s]), (it / STAGES) & 1u, abort_flag, args.status, tmo));
+        ok = warp_all(mbar_wait(smem_u32(&ctl->full[s]), (it / STAGES) & 1u, abort_flag, args.status, tmo) &&
+                      (!S::scale_warps ||
+                       mbar_wait(smem_u32(&ctl->scales[s]), (it / STAGES) & 1u, abort_flag, args.status, tmo)));
         if (!ok) break;
         tc_fence_after();
         if (lane == 0) {
           const uint32_t sa = stage0 + s * S::stage_bytes, sb = sa + A_BYTES;
           const uint32_t sft = tmem_base + SF_TMEM_COL + s * 32;
-          copy_scales(s);
+          if (!S::scale_warps) {
+            const uint32_t sfs = sf0 + s * SF_STAGE_BYTES;
+#pragma unroll
+            for (int i = 0; i < 6; ++i)
+              tmem_cp_32x128b_x4(sft + 4 * i, smem_desc_rows16(sfs + (i % 3) * SF_BYTES + (i / 3) * 512));
+          }
 #pragma unroll
           for (int ks = 0; ks < STAGE_K / UK; ++ks) {
             constexpr uint32_t idesc = idesc_mxf4(BM, BN);
@@ -629,10 +655,35 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
     if (lane == 0) mma_commit(smem_u32(&ctl->done));
     __syncwarp();
     mbar_wait(smem_u32(&ctl->done), 0u, abort_flag, args.status, args.drain_ns, false);
-  } else {
-    // =========================================================== epilogue (warps 2..9)
+  } else if (S::scale_warps && warp >= SCALE_WARP && warp < S::epi_warp) {
+    // =========================================================== scales
+    // The scale atoms of a stage into its 32 columns of tensor memory, per 128-element chunk 4 columns
+    // of A, then 8 of B; every lane quadrant holds all 32 rows of an atom. A stage that is full has
+    // columns that no MMA reads any more: its ring slot was free before it was loaded.
+    set_regs_down<SCALE_REGS>();
+    const uint32_t sft = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16) + SF_TMEM_COL;
+    const int mine = sc.total > static_cast<int>(blockIdx.x) ? (sc.total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    const uint32_t stages = static_cast<uint32_t>(mine) * kblocks;
+    for (uint32_t it = 0; it < stages; ++it) {
+      const int s = it % STAGES;
+      if (!warp_all(mbar_wait(smem_u32(&ctl->full[s]), (it / STAGES) & 1u, abort_flag, args.status, tmo))) break;
+      tc_fence_after();
+      const uint8_t* atoms = sf_ring + s * SF_STAGE_BYTES + lane * 16;
+      uint4 v[6];
+#pragma unroll
+      for (int i = 0; i < 6; ++i) v[i] = *reinterpret_cast<const uint4*>(atoms + (i % 3) * SF_BYTES + (i / 3) * 512);
+#pragma unroll
+      for (int i = 0; i < 6; i += 2) tmem_st8(sft + s * 32 + 4 * i, v[i], v[i + 1]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->scales[s]));
+    }
+  } else if (warp >= S::epi_warp) {
+    // =========================================================== epilogue
+    if (S::scale_warps) set_regs_up<EPI_REGS>();
     if (MODE == MX4_DOWN) grid_wait();  // the clock of its waits starts after the up product
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int q = warp & 3, half = (warp - S::epi_warp) >> 2;
     const int r_in = q * 32 + lane;
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     auto release_acc = [&]() {
@@ -718,7 +769,7 @@ __global__ void __launch_bounds__(THREADS, 1) mx4_gemm_kernel(const __grid_const
           }
         }
         release_acc();
-        uint8_t* sbuf = staging + (warp - 2) * OUT_BYTES;
+        uint8_t* sbuf = staging + (warp - S::epi_warp) * OUT_BYTES;
         const int rows_here = min(32, ti.rows - q * 32);
         const unsigned valid = __ballot_sync(0xffffffffu, rv);
 #pragma unroll
@@ -801,11 +852,13 @@ int row_blocks(long long rows, int K, int passes) {
   const long long items = rows * ((K + 256 * passes - 1) / (256 * passes));
   return static_cast<int>(std::max(1LL, std::min((items + 7) / 8, 8LL * device_sm_count())));
 }
-#define MOE_MX4_ROWS(kernel, rows, K, s, ...)                                                    \
-  do {                                                                                           \
-    if (many_rows(rows, K)) kernel<ROW_PASSES><<<row_blocks(rows, K, ROW_PASSES), 256, 0, s>>>(__VA_ARGS__); \
-    else kernel<1><<<row_blocks(rows, K, 1), 256, 0, s>>>(__VA_ARGS__);                          \
-  } while (0)
+template <typename Many, typename Few, typename... Given>
+moe_status_t launch_rows(Many many, Few few, long long rows, int K, cudaStream_t s, Given... given) {
+  const cudaError_t err = many_rows(rows, K)
+                              ? launch_dependent(many, row_blocks(rows, K, ROW_PASSES), 256, 0, s, given...)
+                              : launch_dependent(few, row_blocks(rows, K, 1), 256, 0, s, given...);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
+}
 
 template <int MODE>
 moe_status_t launch_gemm(const uint8_t* a_codes, const uint8_t* b_codes, long long b_rows, Args a, cudaStream_t s) {
@@ -821,7 +874,7 @@ moe_status_t launch_gemm(const uint8_t* a_codes, const uint8_t* b_codes, long lo
   if (aerr != cudaSuccess) return cuda_fail(aerr);
   const long long tiles = list_tiles(a.cap, a.E) * ((a.N + S::cols - 1) / S::cols);
   const unsigned grid = static_cast<unsigned>(std::max(1LL, std::min<long long>(device_sm_count(), tiles)));
-  const cudaError_t err = launch_dependent(mx4_gemm_kernel<MODE>, grid, THREADS, S::smem(a.E), s, m, a);
+  const cudaError_t err = launch_dependent(mx4_gemm_kernel<MODE>, grid, S::threads, S::smem(a.E), s, m, a);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
@@ -858,9 +911,10 @@ moe_status_t moe_mx4_prepare_weights(const moe_bf16* w_ug, const moe_bf16* w_dow
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Weights w = carve_weights(mxw, E, d, h);
   const long long ug_rows = 2LL * E * h;
-  MOE_MX4_ROWS(mx4_quant_rows_kernel, ug_rows, d, s, reinterpret_cast<const uint4*>(w_ug), ug_rows, d, nullptr, E, h,
-               tiles128(h), reinterpret_cast<uint32_t*>(w.ug_q), w.ug_sf, 2LL * E * tiles128(h), nullptr);
-  if ((st = launched()) != MOE_OK) return st;
+  st = launch_rows(mx4_quant_rows_kernel<ROW_PASSES>, mx4_quant_rows_kernel<1>, ug_rows, d, s,
+                   reinterpret_cast<const uint4*>(w_ug), ug_rows, d, nullptr, E, h, tiles128(h),
+                   reinterpret_cast<uint32_t*>(w.ug_q), w.ug_sf, 2LL * E * tiles128(h), nullptr);
+  if (st != MOE_OK) return st;
   const long long items = static_cast<long long>(E) * d * 4 * mx4_kc(h);
   const int blocks = static_cast<int>(std::max(1LL, std::min((items + 255) / 256, 16LL * device_sm_count())));
   mx4_quant_cols_kernel<<<blocks, 256, 0, s>>>(reinterpret_cast<const bf16*>(w_down), E, h, d, down_tiles(d), w.dn_q,
@@ -877,10 +931,9 @@ moe_status_t moe_mx4_quantize_rows(const moe_bf16* x, const int32_t* offsets, in
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_device();
   if (st != MOE_OK || cap == 0) return st;
-  MOE_MX4_ROWS(mx4_quant_rows_kernel, static_cast<long long>(cap), K, reinterpret_cast<cudaStream_t>(stream),
-               reinterpret_cast<const uint4*>(x), cap, K, offsets, E, 0, 0, reinterpret_cast<uint32_t*>(q), sf,
-               list_tiles(cap, E), dev_status);
-  return launched();
+  return launch_rows(mx4_quant_rows_kernel<ROW_PASSES>, mx4_quant_rows_kernel<1>, cap, K,
+                     reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const uint4*>(x), cap, K, offsets, E, 0, 0,
+                     reinterpret_cast<uint32_t*>(q), sf, list_tiles(cap, E), dev_status);
 }
 
 moe_status_t moe_mx4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const int32_t* offsets, int E, int cap, int K,
@@ -892,10 +945,9 @@ moe_status_t moe_mx4_dequantize_rows(const uint8_t* q, const uint8_t* sf, const 
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_device();
   if (st != MOE_OK || cap == 0) return st;
-  MOE_MX4_ROWS(mx4_dequant_rows_kernel, static_cast<long long>(cap), K, reinterpret_cast<cudaStream_t>(stream),
-               reinterpret_cast<const uint32_t*>(q), sf, cap, K, offsets, E, reinterpret_cast<uint4*>(x),
-               list_tiles(cap, E), dev_status);
-  return launched();
+  return launch_rows(mx4_dequant_rows_kernel<ROW_PASSES>, mx4_dequant_rows_kernel<1>, cap, K,
+                     reinterpret_cast<cudaStream_t>(stream), reinterpret_cast<const uint32_t*>(q), sf, cap, K, offsets, E,
+                     reinterpret_cast<uint4*>(x), list_tiles(cap, E), dev_status);
 }
 
 moe_status_t moe_permute_mxfp4(const moe_bf16* x, const int32_t* inv_map, const int32_t* offsets, int T, int top_k,
@@ -909,10 +961,9 @@ moe_status_t moe_permute_mxfp4(const moe_bf16* x, const int32_t* inv_map, const 
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(sf, 16)) return MOE_ERR_INVALID_ARG;
   moe_status_t st = check_device();
   if (st != MOE_OK || n == 0) return st;
-  MOE_MX4_ROWS(mx4_permute_kernel, static_cast<long long>(T), d, reinterpret_cast<cudaStream_t>(stream),
-               reinterpret_cast<const uint4*>(x), inv_map, offsets, E, T, top_k, d, reinterpret_cast<uint32_t*>(q), sf,
-               list_tiles(n, E), dev_status);
-  return launched();
+  return launch_rows(mx4_permute_kernel<ROW_PASSES>, mx4_permute_kernel<1>, T, d, reinterpret_cast<cudaStream_t>(stream),
+                     reinterpret_cast<const uint4*>(x), inv_map, offsets, E, T, top_k, d, reinterpret_cast<uint32_t*>(q),
+                     sf, list_tiles(n, E), dev_status);
 }
 
 moe_status_t moe_grouped_swiglu_fwd_mxfp4(const uint8_t* xq, const uint8_t* xsf, const int32_t* offsets, int E, int cap,
