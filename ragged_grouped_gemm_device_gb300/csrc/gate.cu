@@ -19,7 +19,7 @@
 // each round instead of sorting once took four times as long). The sorted lists lie in shared
 // memory, where taking a list's next head is one load instead of a shift of eight registers.
 // Measured: 131072 tokens x 256 experts, top 8 of bf16 logits, 51 us without statistics (67 MB of
-// logits, 1.5 TB/s) and 60 with them; its gradient 34 us (4.2 TB/s of logits read and gradient
+// logits, 1.5 TB/s) and 59 with them; its gradient 34 us (4.2 TB/s of logits read and gradient
 // written); 16 tokens x 128 experts 2.5 us, where the launch and the chain of rounds are the time.
 // The per-expert sums over the tokens of a lane group stay in registers (lane and element own
 // an expert), a block adds its groups' sums in order and leaves one partial row in the workspace,
@@ -389,6 +389,8 @@ __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int
                                                           unsigned* ticket, float* share) {
   __shared__ float s_p[32][STAT_COLS];
   __shared__ int s_c[32][STAT_COLS];
+  __shared__ float s_z[32];
+  __shared__ int s_n[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int cx = threadIdx.x % STAT_COLS, ry = threadIdx.x / STAT_COLS;
   const int words = part_words(E);
@@ -397,14 +399,34 @@ __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int
   grid_wait();  // launched ahead of the end of the forward kernel
   part = after_wait(part);
   const int* ipart = reinterpret_cast<const int*>(part);
+  // every load at once (a loop of a run-time length waits for each round of them)
+  constexpr int ROUNDS = (MAX_BLOCKS + 1024 / STAT_COLS - 1) / (1024 / STAT_COLS);
+  static_assert(MAX_BLOCKS <= 1024, "one thread a block");
+  float pv[ROUNDS], z = 0.f;
+  int cv[ROUNDS], n = 0;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int b = ry + i * (1024 / STAT_COLS);
+    const bool on = e < E && b < blocks;
+    pv[i] = on ? part[static_cast<size_t>(b) * words + e] : 0.f;
+    cv[i] = on ? ipart[static_cast<size_t>(b) * words + E + e] : 0;
+  }
+  if (threadIdx.x < blocks) {
+    z = part[static_cast<size_t>(threadIdx.x) * words + 2 * E];
+    n = ipart[static_cast<size_t>(threadIdx.x) * words + 2 * E + 1];
+  }
   float p = 0.f;
   int c = 0;
-  if (e < E) {
-#pragma unroll 5
-    for (int b = ry; b < blocks; b += 1024 / STAT_COLS) {
-      p += part[static_cast<size_t>(b) * words + e];
-      c += ipart[static_cast<size_t>(b) * words + E + e];
-    }
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    p += pv[i];
+    c += cv[i];
+  }
+  z = warp_sum(z);
+  n = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(n)));
+  if (lane == 0) {
+    s_z[warp] = z;
+    s_n[warp] = n;
   }
 #pragma unroll
   for (int o = STAT_COLS; o < 32; o <<= 1) {
@@ -443,14 +465,8 @@ __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int
   }
   if (__shfl_sync(FULL, last, 0) == 0u) return;
   __threadfence();
-  float z = 0.f;
-  int n = 0;
-  for (int b = lane; b < blocks; b += 32) {
-    z += part[static_cast<size_t>(b) * words + 2 * E];
-    n += ipart[static_cast<size_t>(b) * words + 2 * E + 1];
-  }
-  z = warp_sum(z);
-  n = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(n)));
+  z = warp_sum(s_z[lane]);
+  n = static_cast<int>(__reduce_add_sync(FULL, static_cast<unsigned>(s_n[lane])));
   float total = 0.f;
   for (int b = lane; b < static_cast<int>(gridDim.x); b += 32) total += __ldcg(share + b);
   total = warp_sum(total);
@@ -715,8 +731,9 @@ moe_status_t moe_gate_fwd(const void* logits, int dtype, long long ld, const uin
   if (dtype == MOE_DTYPE_BF16) st = vec ? by_width_fwd<bf16, true>(a, w, blocks, s) : by_width_fwd<bf16, false>(a, w, blocks, s);
   else st = vec ? by_width_fwd<float, true>(a, w, blocks, s) : by_width_fwd<float, false>(a, w, blocks, s);
   if (st != MOE_OK || !stats) return st;
-  const cudaError_t err = launch_dependent(gate_stats_kernel, (E + STAT_COLS - 1) / STAT_COLS, 1024, 0, s, a.part, blocks, top_k, E, counts,
-                                           n_valid, prob_sum, loss, a.ticket, reinterpret_cast<float*>(a.ticket + 1));
+  const cudaError_t err = launch_dependent(gate_stats_kernel, (E + STAT_COLS - 1) / STAT_COLS, 1024, 0, s, a.part, blocks,
+                                           top_k, E, counts, n_valid, prob_sum, loss, a.ticket,
+                                           reinterpret_cast<float*>(a.ticket + 1));
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 

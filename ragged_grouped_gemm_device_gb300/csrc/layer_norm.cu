@@ -541,11 +541,16 @@ __global__ void __launch_bounds__(1024) norm_partials_kernel(const float* part, 
   part = after_wait(part);
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const long long c = static_cast<long long>(blockIdx.x) * 32 + cx;  // of 2d: dgamma's, then dbeta's columns
-  float s = 0.f;
-  if (c < 2LL * d) {
-#pragma unroll 10
-    for (int r = ry; r < blocks; r += 32) s += __ldcs(part + static_cast<size_t>(r) * 2 * d + c);
+  // every load at once (a loop of a run-time length waits for each round of them)
+  constexpr int ROUNDS = (BWD_MAX_BLOCKS + 31) / 32;
+  float v[ROUNDS], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int r = ry + 32 * i;
+    v[i] = r < blocks && c < 2LL * d ? __ldcs(part + static_cast<size_t>(r) * 2 * d + c) : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) s += v[i];
   acc[ry][cx] = s;
   __syncthreads();
   if (ry == 0 && c < 2LL * d) {
