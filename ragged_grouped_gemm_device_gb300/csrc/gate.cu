@@ -19,7 +19,7 @@
 // each round instead of sorting once took four times as long). The sorted lists lie in shared
 // memory, where taking a list's next head is one load instead of a shift of eight registers.
 // Measured: 131072 tokens x 256 experts, top 8 of bf16 logits, 51 us without statistics (67 MB of
-// logits, 1.5 TB/s) and 59 with them; its gradient 34 us (4.2 TB/s of logits read and gradient
+// logits, 1.5 TB/s) and 59 with them; its gradient 34 us (3.9 TB/s of logits read and gradient
 // written); 16 tokens x 128 experts 2.5 us, where the launch and the chain of rounds are the time.
 // The per-expert sums over the tokens of a lane group stay in registers (lane and element own
 // an expert), a block adds its groups' sums in order and leaves one partial row in the workspace,

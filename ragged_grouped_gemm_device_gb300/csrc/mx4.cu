@@ -65,29 +65,62 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// A warp quantizes 256 consecutive elements, 8 a lane (four lanes hold a block): returns this
-// lane's 8 codes and, in lanes 0 and 16, the scale codes of the four blocks of its 128-element
-// chunk. Lanes past the row's end (act false) count as blocks of scale 2^0.
-__device__ __forceinline__ uint32_t quant256(uint4 q, bool act, uint32_t& chunk_scales) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  // largest magnitude as a bf16 bit pattern, two at a time (patterns without the sign order as
+// A warp quantizes PASSES x 256 consecutive elements, 8 a lane and pass (four lanes hold a block):
+// this lane's 8 codes of each pass, and a word of the four scale codes of a 128-element chunk: in
+// lane l with l % 16 < PASSES that of pass l % 16, its first chunk for l < 16, its second above.
+// Lanes past the row's end (pass i: v0 + 32 i >= vec) count as blocks of scale 2^0. What holds the
+// row kernels besides memory is the integer pipe, so the passes share their shuffles: the block
+// maxima go two to a word, and the four lanes of a block carry one pass's scale each.
+template <int PASSES>
+__device__ __forceinline__ uint32_t quantize(const uint4 (&in)[PASSES], int v0, int vec, uint32_t (&codes)[PASSES]) {
+  static_assert(PASSES == 1 || PASSES == 4, "one pass, or one for each lane of a block");
+  const int lane = threadIdx.x & 31;
+  // largest magnitudes as bf16 bit patterns, two at a time (patterns without the sign order as
   // numbers, infinity and NaN above all others)
-  uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t code = mx4_scale_code(max(m >> 16, m & 0xffffu) << 16);
-  const float inv = mx4_inv_scale(code);
-  float f[8];
+  uint32_t m[PASSES];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    f[2 * t] = bf16_lo(w[t]) * inv;
-    f[2 * t + 1] = bf16_hi(w[t]) * inv;
+  for (int i = 0; i < PASSES; ++i)
+    m[i] = __vmaxu2(__vmaxu2(in[i].x & 0x7fff7fffu, in[i].y & 0x7fff7fffu),
+                    __vmaxu2(in[i].z & 0x7fff7fffu, in[i].w & 0x7fff7fffu));
+  uint32_t top[PASSES];  // of this lane's block, as a bf16 bit pattern in the high half
+  if constexpr (PASSES == 1) {
+    m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1));
+    m[0] = __vmaxu2(m[0], __shfl_xor_sync(0xffffffffu, m[0], 2));
+    top[0] = max(m[0] & 0xffff0000u, m[0] << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < PASSES; i += 2) {
+      uint32_t two = __vmaxu2(__byte_perm(m[i], m[i + 1], 0x5410), __byte_perm(m[i], m[i + 1], 0x7632));
+      two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, 1));
+      two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, 2));
+      top[i] = two << 16;
+      top[i + 1] = two & 0xffff0000u;
+    }
   }
-  uint32_t s = (act ? code : 127u) << (8 * ((threadIdx.x >> 2) & 3));
-  s |= __shfl_xor_sync(0xffffffffu, s, 4);
-  s |= __shfl_xor_sync(0xffffffffu, s, 8);
-  chunk_scales = s;
-  return e2m1x8(f);
+  uint32_t mine = 0u;
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i) {
+    const uint32_t code = mx4_scale_code(top[i]);
+    const uint32_t s = v0 + 32 * i < vec ? code : 127u;
+    if ((lane & (PASSES - 1)) == i) mine = s;
+    // v / 2^s in bf16: exact, or below the smallest normal number, which rounds to code 0
+    const uint32_t inv = __float_as_uint(mx4_inv_scale(code)) >> 16;
+    const uint32_t inv2 = inv << 16 | inv;
+    const uint32_t w[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+    float f[8];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t v;
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(v) : "r"(w[t]), "r"(inv2));
+      f[2 * t] = bf16_lo(v);
+      f[2 * t + 1] = bf16_hi(v);
+    }
+    codes[i] = e2m1x8(f);
+  }
+  mine <<= 8 * ((lane >> 2) & 3);
+  mine |= __shfl_xor_sync(0xffffffffu, mine, 4);
+  mine |= __shfl_xor_sync(0xffffffffu, mine, 8);
+  return mine;
 }
 
 // Address of the four scale bytes of row r of tile G in chunk kc.
@@ -98,7 +131,11 @@ __device__ __forceinline__ uint32_t* chunk_word(uint8_t* sf, long long G, int KC
 // The row kernels below are bound by memory (they read 2 bytes an element and write about half of
 // one, or the reverse). A warp takes PASSES * 256 elements of a row at a time, all of its loads in
 // flight before it works on them: 4 passes when there are rows enough for every warp of the
-// GPU, 1 for few rows, so that a row is spread over more warps.
+// GPU, 1 for few rows, so that a row is spread over more warps. Measured, 131072 x 2048: quantize
+// 111 us (6.1 TB/s of reads and writes; 125 with the shuffles of each pass on their own), its
+// inverse 119 us (5.7 TB/s, four fifths of them writes; a table in shared memory was no slower);
+// the gather with quantization of 16384 tokens to 8 rows each 40 us (5.2 TB/s, two thirds writes);
+// 333 x 1024 2.8 and 2.5 us, a launch and a round trip to memory.
 constexpr int ROW_PASSES = 4;
 
 // Row and piece of item `it` (32-bit division unless there are 2^32 items).
@@ -144,15 +181,13 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* src, l
       r = static_cast<int>(n % 128);
     }
     const bool tile_ok = MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles);
+    uint32_t codes[PASSES];
+    const uint32_t word = quantize(w, v0, vec, codes);
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {  // every lane runs every pass: the shuffles need the warp
-      const int v = v0 + 32 * i;
-      if (v - lane >= vec) break;
-      uint32_t word;
-      const uint32_t codes = quant256(w[i], v < vec, word);
-      if (v < vec) q[p * vec + v] = codes;
-      if ((lane & 15) == 0 && tile_ok) *chunk_word(sf, G, KC, v >> 4, r) = word;
-    }
+    for (int i = 0; i < PASSES; ++i)
+      if (v0 + 32 * i < vec) q[p * vec + v0 + 32 * i] = codes[i];
+    const int vs = v0 - lane + 32 * (lane & 15);  // the first element group of the pass whose scales it holds
+    if ((lane & 15) < PASSES && vs < vec && tile_ok) *chunk_word(sf, G, KC, (vs + (lane & 16)) >> 4, r) = word;
   }
 }
 
@@ -198,30 +233,38 @@ __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* x,
         }
       }
     }
-    uint32_t codes[PASSES], word[PASSES];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) codes[i] = quant256(w[i], v0 + 32 * i < vec, word[i]);
+    uint32_t codes[PASSES];
+    const uint32_t word = quantize(w, v0, vec, codes);
+    const int vs = v0 - lane + 32 * (lane & 15);  // as in the kernel above
+    const bool scales = (lane & 15) < PASSES && vs < vec;
     for (int j = 0; j < k; ++j) {
       const int p = __shfl_sync(0xffffffffu, my_p, j);
       const int g = __shfl_sync(0xffffffffu, my_g, j), r = __shfl_sync(0xffffffffu, my_r, j);
       if (p < 0) continue;  // warp-uniform
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int v = v0 + 32 * i;
-        if (v < vec) q[static_cast<size_t>(p) * vec + v] = codes[i];
-        if ((lane & 15) == 0 && v - lane < vec) *chunk_word(sf, g, KC, v >> 4, r) = word[i];
-      }
+      for (int i = 0; i < PASSES; ++i)
+        if (v0 + 32 * i < vec) q[static_cast<size_t>(p) * vec + v0 + 32 * i] = codes[i];
+      if (scales) *chunk_word(sf, g, KC, (vs + (lane & 16)) >> 4, r) = word;
     }
   }
 }
 
-// The value of a 4-bit code.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-  const uint32_t mag = c & 7u;
-  // exponent field e and mantissa bit m: e = 0 is m / 2, else (2 + m) 2^(e - 2)
-  const float v = mag < 2u ? 0.5f * static_cast<float>(mag)
-                           : __uint_as_float(((mag >> 1) + 126u) << 23 | (mag & 1u) << 22);
-  return (c & 8u) ? -v : v;
+// Eight 4-bit codes times the bf16 pair scale2, in pairs of bf16. A byte permute is a table of
+// eight bytes: one looks up the low bytes of four magnitudes 0 0.5 1 1.5 2 3 4 6, one the high.
+__device__ __forceinline__ uint4 e2m1_scaled(uint32_t c, uint32_t scale2) {
+  constexpr uint32_t LO0 = 0xc0800000u, LO1 = 0xc0804000u, HI0 = 0x3f3f3f00u, HI1 = 0x40404040u;
+  const uint32_t mag = c & 0x77777777u, up = c << 4;  // byte j: code 2j + 1's sign in c, code 2j's in up
+  uint32_t w[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t sel = mag >> (16 * h);  // four nibbles
+    const uint32_t lo = __byte_perm(LO0, LO1, sel), hi = __byte_perm(HI0, HI1, sel);
+    w[2 * h] = __byte_perm(lo, hi, 0x5140) | (__byte_perm(up, c, h ? 0x6020 : 0x4000) & 0x80008000u);
+    w[2 * h + 1] = __byte_perm(lo, hi, 0x7362) | (__byte_perm(up, c, h ? 0x7030 : 0x5010) & 0x80008000u);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(w[i]) : "r"(w[i]), "r"(scale2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // The bf16 values that rows p < M of codes and scales stand for (exact: an E2M1 value times a
@@ -234,15 +277,12 @@ __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* q
                                                                int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
-  __shared__ uint32_t pair[256];  // the bf16 values of the two codes of a byte
   grid_release();
   grid_wait();  // launched ahead of the end of the kernel before
   q = after_wait(q);
   sf = after_wait(sf);
   offsets = after_wait(offsets);
   if (!load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
-  pair[threadIdx.x] = pack_bf16x2(e2m1_value(threadIdx.x & 15u), e2m1_value(threadIdx.x >> 4));
-  __syncthreads();
   const int M = s_end[E - 1];
   const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
   const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
@@ -258,22 +298,16 @@ __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* q
     int r;
     row_tile(s_end, s_pre, E, p, G, r);
     if (!MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles)) continue;
+    const uint8_t* scale = sf + atom_byte(G, KC, v0 >> 2, r);  // a pass is two chunks
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-      sc[i] = v0 + 32 * i < vec ? __ldg(sf + atom_byte(G, KC, (v0 + 32 * i) >> 2, r)) : 0u;
+    for (int i = 0; i < PASSES; ++i) sc[i] = v0 + 32 * i < vec ? __ldg(scale + 1024 * i) : 0u;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int v = v0 + 32 * i;
       if (v >= vec) break;
-      // 2^(sc - 127): 2^-127 is the subnormal 0x00400000
-      const float scale = sc[i] == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(sc[i] == 0u ? 0x00400000u : sc[i] << 23);
-      uint32_t w[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint32_t two = pair[(codes[i] >> (8 * b)) & 0xffu];
-        w[b] = pack_bf16x2(bf16_lo(two) * scale, bf16_hi(two) * scale);
-      }
-      __stcs(x + p * vec + v, make_uint4(w[0], w[1], w[2], w[3]));
+      // 2^(sc - 127) in bf16: 2^-127 is subnormal, 255 stands for NaN
+      const uint32_t s = sc[i] == 255u ? 0x7fc0u : sc[i] == 0u ? 0x0040u : sc[i] << 7;
+      __stcs(x + p * vec + v, e2m1_scaled(codes[i], s << 16 | s));
     }
   }
 }
