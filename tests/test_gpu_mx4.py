@@ -119,6 +119,47 @@ def test_permute_is_the_gather_quantized(lib, T, k, E, d):
     assert torch.equal(q, q2) and torch.equal(sf, sf2)
 
 
+@pytest.mark.parametrize("K", [32, 160, 288, 1056, 2080])
+def test_many_rows_bit_for_bit_and_back(lib, K):
+    """Rows enough that a warp takes 1024 elements at a time; special values in every part of a row."""
+    offsets = np.cumsum([1000, 0, 1601])
+    M, cap = int(offsets[-1]), int(offsets[-1]) + 2
+    g = torch.Generator().manual_seed(K)
+    x = torch.randn(cap, K, generator=g) * torch.exp(2 * torch.randn(cap, 1, generator=g))
+    x[3::11] *= 2.0 ** -127                                  # subnormal and tiny normal values
+    x[4::11] *= 2.0 ** 120
+    x[5::11, K - 1] = float("nan")
+    x[6::11, K // 2] = float("inf")
+    x[7::11, : K // 2] = 0.0
+    x = x.clamp(-3.3e38, 3.3e38).where(~x.isinf(), x).to(torch.bfloat16).cuda()
+    q = _u8(cap * (K // 2), 0x77).view(cap, K // 2)
+    sf = _u8(_lib.moe_workspace_bytes(_lib.OP_MX4_ROW_SCALES, cap, 1, 3, K, 32))
+    off = _i32(offsets)
+    _lib.moe_mx4_quantize_rows(x, off, 3, cap, K, q, sf)
+    back = torch.full_like(x, 5.0)
+    _lib.moe_mx4_dequantize_rows(q, sf, off, 3, cap, K, back)
+    torch.cuda.synchronize()
+    codes, scale = Q.quantize(_host(x)[:M])
+    assert (scale == 0).any() and (scale == 255).any() and (scale > 240).any()
+    G, r = _tiles(offsets)
+    got_s, pad = _scales(sf.cpu().numpy(), G, r, K)
+    live = np.repeat(scale != 255, 32, axis=1)
+    assert np.array_equal(got_s, scale) and (pad == 127).all()
+    assert np.array_equal(_unpack(q.cpu().numpy()[:M], K)[live], codes[live])
+    b = _host(back)
+    assert np.array_equal(np.nan_to_num(b[:M], nan=-9.0), np.nan_to_num(Q.values(codes, scale), nan=-9.0))
+    assert (b[M:] == 5.0).all() and (q[M:] == 0x77).all()
+
+
+@pytest.mark.parametrize("T,k,E,d", [(2500, 3, 5, 96), (2431, 1, 2, 1056), (2600, 8, 16, 288)])
+def test_permute_of_many_tokens(lib, T, k, E, d):
+    test_permute_is_the_gather_quantized(lib, T, k, E, d)
+
+
+def test_weights_of_many_rows(lib):
+    test_weights_bit_for_bit(lib, 5, 1056, 256)
+
+
 def _prepared(w_ug, w_down):
     E, h2, d = w_ug.shape
     h = h2 // 2
