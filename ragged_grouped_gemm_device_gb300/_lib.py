@@ -121,7 +121,7 @@ def load(path: str = None):
     return _lib
 
 
-# calls that the compiled binding takes over (csrc/binding.c)
+# calls that the compiled binding takes over (csrc/binding.cpp)
 COMPILED = ("moe_layer_norm_fwd", "moe_layer_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_mx4_quantize_rows",
             "moe_mx4_dequantize_rows", "moe_permute_mxfp4", "moe_grouped_swiglu_fwd_mxfp4", "moe_unpermute_combine",
             "moe_route_offsets")
@@ -141,9 +141,7 @@ def _install_binding():
     except ImportError:
         return
 
-    _binding.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in COMPILED}, torch.bfloat16,
-                  torch.float32, torch.int32, torch.uint8, torch.bool, _check, torch._C._cuda_getCurrentRawStream,
-                  torch._C._cuda_getDevice)
+    _binding.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in COMPILED}, _check)
     for n in COMPILED:
         PYTHON_BINDING[n] = globals()[n]
         globals()[n] = getattr(_binding, n)

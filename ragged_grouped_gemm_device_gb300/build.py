@@ -6,12 +6,13 @@ build(debug=True) compiles the same sources with -DMOE_GG_DEBUG into libmoe_gg_d
 ABI): device-side bounds checks at the data-dependent global accesses and a wait for the stream
 at the end of every entry point, read back with moe_debug_report().
 
-build_binding() compiles csrc/binding.c, the CPython extension that marshals the calls of a decode
-step, next to this file; without a C compiler or Python's headers the ctypes binding does it."""
+build_binding() compiles csrc/binding.cpp, the CPython extension that marshals the calls of a decode
+step, next to this file; without a C++ compiler or Python's headers the ctypes binding does it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -88,16 +89,21 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 def build_binding(force: bool = False):
     """Path of the CPython extension, or None where it cannot be built (no compiler or headers)."""
-    src = os.path.join(CSRC, "binding.c")
-    deps = [src, os.path.join(ROOT, "include", "moe_gg.h"), os.path.abspath(__file__)]
+    src = os.path.join(CSRC, "binding.cpp")
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    deps = [src, os.path.join(ROOT, "include", "moe_gg.h"), os.path.abspath(__file__), os.path.join(torch, "version.py")]
     if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
         return BINDING
-    cc, inc = shutil.which("gcc") or shutil.which("cc"), sysconfig.get_paths()["include"]
+    cc, inc = shutil.which("g++") or shutil.which("c++"), sysconfig.get_paths()["include"]
     if cc is None or not os.path.exists(os.path.join(inc, "Python.h")):
         return None
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    lib = os.path.join(torch, "lib")
     tmp = BINDING + ".tmp"
-    r = subprocess.run([cc, "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I", inc, src, "-o", tmp],
-                       capture_output=True, text=True)
+    cmd = [cc, "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", inc, "-I", os.path.join(torch, "include"), "-I",
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-I", cuda, src, "-o", tmp, "-L", lib,
+           "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cc} failed for {src}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
