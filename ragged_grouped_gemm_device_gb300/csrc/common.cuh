@@ -34,14 +34,15 @@ __device__ __forceinline__ void record_status(int32_t* status, int bits) {
 }
 
 // ---------------------------------------------------------------------------------- dependent launch
-// Programmatic dependent launch: a kernel launched by launch_dependent() may start before the one
-// ahead of it in the stream has finished, which hides its launch (a chain of gate calls of 16 tokens
-// takes 2.5 us a call, against 2.9). It has to call grid_wait() before it touches anything that a
-// kernel ahead may write or still read; grid_release() in the kernel ahead lets it start early. A
-// kernel may release before it waits: the next one's wait ends after this one, and so after
-// everything ahead of it. A grid of a block or more per SM gains nothing where its blocks are placed
-// while others still run and end up two to an SM (layer norm of 20000 x 1000 fp32 took 30.5 us a call
-// in a chain, against 27.7): launch_dependent_if() with the rule at its call.
+// Programmatic dependent launch: a kernel launched by launch_dependent() may be set up while the one
+// ahead of it in the stream ends, instead of after it: 2 to 3 us less for each kernel of a queue (gate
+// of 4096 x 128 with statistics and gradient, three kernels, 12.1 us against 16.7; layer norm of 16384 x
+// 2048 with its gradient 63.7 against 68.7). It has to call grid_wait() before it touches anything that
+// a kernel ahead may write or still read. grid_release() in the kernel ahead lets it start before
+// that one's blocks have ended, which pays where its prologue is long (the down product); elsewhere it
+// costs more than it gains: a full grid that is placed while others still run ends up two blocks to an
+// SM (layer norm of 20000 x 1000 fp32 30.5 us against 27.7), and small kernels queue up on the GPU
+// (MXFP4 round trip of 333 x 1024 7.1 us against 4.8).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // A pointer to read through after grid_wait(): the compiler takes reads through a const __restrict__
 // pointer, and __ldg, for reads of memory that nothing writes, and may move them above the wait.
@@ -53,8 +54,8 @@ __device__ __forceinline__ T* after_wait(T* p) {
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <typename... Params, typename... Given>
-inline cudaError_t launch_dependent_if(bool early, void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
-                                       cudaStream_t stream, Given... given) {
+inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
+                                    cudaStream_t stream, Given... given) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -64,13 +65,8 @@ inline cudaError_t launch_dependent_if(bool early, void (*kernel)(Params...), di
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = early ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...);
-}
-template <typename... Params, typename... Given>
-inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
-                                    cudaStream_t stream, Given... given) {
-  return launch_dependent_if(true, kernel, grid, block, smem, stream, given...);
 }
 
 // ---------------------------------------------------------------------------------- register shares

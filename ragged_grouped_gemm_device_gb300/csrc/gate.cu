@@ -218,8 +218,7 @@ constexpr int LIST = 9;  // a lane's eight sorted keys and a 0; odd, so that lan
 // NL lists of eight experts a lane: expert 8 (G l + lane_in_group) + j.
 template <typename T, int NL, int G, bool VEC>
 __global__ void __launch_bounds__(THREADS) gate_fwd_kernel(GateArgs a) {
-  grid_release();
-  grid_wait();  // launched ahead of the end of the kernel before
+  grid_wait();
   a.logits = after_wait(a.logits);
   a.mask = after_wait(a.mask);
   typedef Key<T> KT;
@@ -395,7 +394,6 @@ __global__ void __launch_bounds__(1024) gate_stats_kernel(const float* part, int
   const int cx = threadIdx.x % STAT_COLS, ry = threadIdx.x / STAT_COLS;
   const int words = part_words(E);
   const int e = blockIdx.x * STAT_COLS + cx;
-  grid_release();
   grid_wait();  // launched ahead of the end of the forward kernel
   part = after_wait(part);
   const int* ipart = reinterpret_cast<const int*>(part);
@@ -496,8 +494,7 @@ struct GateBwdArgs {
 
 template <typename T, int NL, int G, bool VEC>
 __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(GateBwdArgs a) {
-  grid_release();
-  grid_wait();  // launched ahead of the end of the kernel before
+  grid_wait();
   a.logits = after_wait(a.logits);
   a.lse = after_wait(a.lse);
   a.ids = after_wait(a.ids);
@@ -609,15 +606,13 @@ moe_status_t launch_fwd(const GateArgs& a, int blocks, cudaStream_t s) {
     const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(gate_fwd_kernel<T, NL, G, VEC>), most);
     if (err != cudaSuccess) return cuda_fail(err);
   }
-  // Ahead of the end of the kernel before where the blocks are fewer than the SMs: a full grid that is
-  // placed while others still run ends up two to an SM.
   const cudaError_t err =
-      launch_dependent_if(blocks < device_sm_count(), gate_fwd_kernel<T, NL, G, VEC>, blocks, THREADS, smem, s, a);
+      launch_dependent(gate_fwd_kernel<T, NL, G, VEC>, blocks, THREADS, smem, s, a);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 template <typename T, int NL, int G, bool VEC>
 moe_status_t launch_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
-  const cudaError_t err = launch_dependent_if(blocks < device_sm_count(), gate_bwd_kernel<T, NL, G, VEC>, blocks,
+  const cudaError_t err = launch_dependent(gate_bwd_kernel<T, NL, G, VEC>, blocks,
                                               THREADS, sizeof(float) * WARPS * 32 * 8 * NL, s, a);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }

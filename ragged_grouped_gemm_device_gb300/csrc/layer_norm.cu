@@ -270,6 +270,7 @@ struct NormArgs {
 
 template <typename T, int VB, int NCH, int TPR>
 __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks_per_sm(TPR)) norm_fwd_kernel(const NormArgs a) {
+  grid_wait();
   constexpr int ROWS = block_threads(TPR) / TPR;
   __shared__ __align__(16) float red[2][32];
   const int t = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
@@ -279,8 +280,8 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks_per_sm(TPR)) no
   for (int i = 0; i < NCH; ++i) {
     const int c = (i * TPR + t) * VB;
     if (c < a.d) {
-      load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g[i]);
-      load_weight<VB>(a.beta, a.w_bf16, c, 0.0f, b[i]);
+      load_weight<VB>(after_wait(a.gamma), a.w_bf16, c, 1.0f, g[i]);
+      load_weight<VB>(after_wait(a.beta), a.w_bf16, c, 0.0f, b[i]);
     }
   }
   extern __shared__ __align__(16) uint8_t ring[];
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks_per_sm(TPR)) no
   const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
   const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
   feed.init(ring, t, a.d, rows);
-  feed.at[0] = static_cast<const T*>(a.x) + row0 * a.ldx;
+  feed.at[0] = static_cast<const T*>(after_wait(a.x)) + row0 * a.ldx;
   feed.step[0] = step * a.ldx;
   feed.prime();
   T* yr = static_cast<T*>(a.out) + row0 * a.ldo;
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks_per_sm(TPR)) no
 
 template <typename T, int VB, int NCH, int TPR>
 __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks_per_sm(TPR)) norm_bwd_kernel(const NormArgs a) {
+  grid_wait();
   constexpr int ROWS = block_threads(TPR) / TPR;
   __shared__ __align__(16) float red[2][64];
   const int t = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
@@ -343,19 +345,18 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks_per_sm(TPR)) no
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = (i * TPR + t) * VB;
-    if (c < a.d) load_weight<VB>(a.gamma, a.w_bf16, c, 1.0f, g[i]);
+    if (c < a.d) load_weight<VB>(after_wait(a.gamma), a.w_bf16, c, 1.0f, g[i]);
 #pragma unroll
     for (int j = 0; j < VB; ++j) dg[i][j] = db[i][j] = 0.f;
   }
-  grid_release();
   extern __shared__ __align__(16) uint8_t ring[];
   Feed<T, VB, NCH, TPR, 2> feed;
   const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
   const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
   feed.init(ring, t, a.d, rows);
-  feed.at[0] = static_cast<const T*>(a.x) + row0 * a.ldx;
+  feed.at[0] = static_cast<const T*>(after_wait(a.x)) + row0 * a.ldx;
   feed.step[0] = step * a.ldx;
-  feed.at[1] = static_cast<const T*>(a.dy) + row0 * a.lddy;
+  feed.at[1] = static_cast<const T*>(after_wait(a.dy)) + row0 * a.lddy;
   feed.step[1] = step * a.lddy;
   feed.prime();
   T* orow = static_cast<T*>(a.out) + row0 * a.ldo;
@@ -368,8 +369,8 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks_per_sm(TPR)) no
     float xh[NCH][VB], gd[NCH][VB];  // xhat, and dy, then gamma dy
     float s1 = 0.f, s2 = 0.f;
     if ((k & 31) == 0 && k + lane < rows) {
-      mean32 = __ldg(a.mean + row0 + static_cast<long long>(k + lane) * step);
-      rstd32 = __ldg(a.rstd + row0 + static_cast<long long>(k + lane) * step);
+      mean32 = __ldg(after_wait(a.mean) + row0 + static_cast<long long>(k + lane) * step);
+      rstd32 = __ldg(after_wait(a.rstd) + row0 + static_cast<long long>(k + lane) * step);
     }
     const float mu = __shfl_sync(0xffffffffu, mean32, k & 31), rs = __shfl_sync(0xffffffffu, rstd32, k & 31);
     feed.take();
@@ -578,7 +579,7 @@ int launch_fwd_rows(const NormArgs& a, cudaStream_t s) {
   if (smem > 48 * 1024 &&
       ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_fwd_kernel<T, VB, NCH, TPR>), smem) != cudaSuccess)
     return grid;  // the launch below the limit would fail too: the caller reads the error
-  norm_fwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), smem, s>>>(a);
+  launch_dependent(norm_fwd_kernel<T, VB, NCH, TPR>, grid, block_threads(TPR), smem, s, a);
   return grid;
 }
 template <typename T, int VB, int NCH, int TPR>
@@ -589,7 +590,7 @@ int launch_bwd_rows(const NormArgs& a, cudaStream_t s) {
   if (smem > 48 * 1024 &&
       ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_bwd_kernel<T, VB, NCH, TPR>), smem) != cudaSuccess)
     return grid;
-  norm_bwd_kernel<T, VB, NCH, TPR><<<grid, block_threads(TPR), smem, s>>>(a);
+  launch_dependent(norm_bwd_kernel<T, VB, NCH, TPR>, grid, block_threads(TPR), smem, s, a);
   return grid;
 }
 

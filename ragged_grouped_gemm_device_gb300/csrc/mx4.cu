@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* src, l
                                                              int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
-  grid_release();
-  grid_wait();  // launched ahead of the end of the kernel before
+  grid_wait();
   src = after_wait(src);
   offsets = after_wait(offsets);
   const bool list = offsets != nullptr;
@@ -201,8 +200,7 @@ __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* x,
                                                           long long sf_tiles, int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
-  grid_release();
-  grid_wait();  // launched ahead of the end of the kernel before
+  grid_wait();
   x = after_wait(x);
   inv_map = after_wait(inv_map);
   offsets = after_wait(offsets);
@@ -277,8 +275,7 @@ __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* q
                                                                int32_t* status) {
   __shared__ int s_end[MAX_E];
   __shared__ int s_pre[MAX_E];
-  grid_release();
-  grid_wait();  // launched ahead of the end of the kernel before
+  grid_wait();
   q = after_wait(q);
   sf = after_wait(sf);
   offsets = after_wait(offsets);
@@ -529,7 +526,9 @@ __global__ void __launch_bounds__(Shape<MODE>::threads, 1) mx4_gemm_kernel(const
     tmem_relinquish();
   }
   // The up product waits here for everything before it; what the down product reads before its own
-  // wait (offsets, weights) is then complete, because the up product releases it after this wait.
+  // wait (offsets, weights) is then complete, because the up product releases it after this wait. The
+  // down product itself does not release: a combine placed while it still runs lands two blocks to an
+  // SM (16384 tokens 465 us instead of 430).
   if constexpr (MODE == MX4_UP) {
     grid_wait();
     grid_release();
@@ -643,10 +642,7 @@ __global__ void __launch_bounds__(Shape<MODE>::threads, 1) mx4_gemm_kernel(const
     }
   } else if (warp == 1) {
     // =========================================================== MMA issuer
-    if (MODE == MX4_DOWN) {
-      grid_wait();     // the clock of its waits starts after the up product
-      grid_release();  // the combine may start
-    }
+    if (MODE == MX4_DOWN) grid_wait();  // the clock of its waits starts after the up product
     uint32_t it = 0, n = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < sc.total && ok; t += gridDim.x, ++n) {
