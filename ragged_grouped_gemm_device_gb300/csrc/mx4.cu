@@ -135,7 +135,7 @@ __device__ __forceinline__ uint32_t* chunk_word(uint8_t* sf, long long G, int KC
 // 111 us (6.1 TB/s of reads and writes; 125 with the shuffles of each pass on their own), its
 // inverse 119 us (5.7 TB/s, four fifths of them writes; a table in shared memory was no slower);
 // the gather with quantization of 16384 tokens to 8 rows each 40 us (5.2 TB/s, two thirds writes);
-// 333 x 1024 2.8 and 2.5 us, a launch and a round trip to memory.
+// 333 x 1024 2.4 us each, a launch and a round trip to memory.
 constexpr int ROW_PASSES = 4;
 
 // Row and piece of item `it` (32-bit division unless there are 2^32 items).
