@@ -157,19 +157,27 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* src, l
   src = after_wait(src);
   offsets = after_wait(offsets);
   const bool list = offsets != nullptr;
-  if (list && !load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
-  const long long M = list ? s_end[E - 1] : rows;
   const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
   const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
-  const long long items = M * pieces;
-  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
-       it += static_cast<long long>(gridDim.x) * 8) {
-    const long long p = item_row(it, pieces, items <= 0xffffffffll);
-    const int v0 = static_cast<int>(it - p * pieces) * (32 * PASSES) + lane;
-    uint4 w[PASSES];
+  const bool narrow = rows * pieces <= 0xffffffffll;
+  const long long step = static_cast<long long>(gridDim.x) * 8;
+  long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5), p = 0;
+  int v0 = 0;
+  uint4 w[PASSES];
+  auto load = [&]() {
+    p = item_row(it, pieces, narrow);
+    v0 = static_cast<int>(it - p * pieces) * (32 * PASSES) + lane;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
       w[i] = v0 + 32 * i < vec ? __ldcs(src + p * vec + v0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  // the first loads do not wait for the problem list, and those of the next item go ahead of this
+  // one's stores
+  if (it < rows * pieces) load();
+  if (list && !load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
+  const long long M = list ? s_end[E - 1] : rows;
+  const long long items = M * pieces;
+  while (it < items) {
     long long G;
     int r;
     if (list) {
@@ -182,10 +190,14 @@ __global__ void __launch_bounds__(256) mx4_quant_rows_kernel(const uint4* src, l
     const bool tile_ok = MOE_DBG_IN(DBG_MX_TILE, G, sf_tiles);
     uint32_t codes[PASSES];
     const uint32_t word = quantize(w, v0, vec, codes);
+    uint32_t* out = q + p * vec + v0;
+    const int left = vec - v0;                    // element groups of the row from this lane's first
+    const int vs = v0 - lane + 32 * (lane & 15);  // the first element group of the pass whose scales it holds
+    it += step;
+    if (it < items) load();
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
-      if (v0 + 32 * i < vec) q[p * vec + v0 + 32 * i] = codes[i];
-    const int vs = v0 - lane + 32 * (lane & 15);  // the first element group of the pass whose scales it holds
+      if (32 * i < left) out[32 * i] = codes[i];
     if ((lane & 15) < PASSES && vs < vec && tile_ok) *chunk_word(sf, G, KC, (vs + (lane & 16)) >> 4, r) = word;
   }
 }
@@ -204,24 +216,30 @@ __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* x,
   x = after_wait(x);
   inv_map = after_wait(inv_map);
   offsets = after_wait(offsets);
-  const long long n = static_cast<long long>(T) * k;
-  if (!load_problem_tiles(offsets, E, n, s_end, s_pre, status)) return;
-  const int M = s_end[E - 1];
   const int lane = threadIdx.x & 31, vec = d / 8, KC = mx4_kc(d);
   const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
   const long long items = static_cast<long long>(T) * pieces;
-  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
-       it += static_cast<long long>(gridDim.x) * 8) {
+  const long long step = static_cast<long long>(gridDim.x) * 8;
+  long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  int v0 = 0, slot = -1;
+  uint4 w[PASSES];
+  auto load = [&]() {
     const long long t = item_row(it, pieces, items <= 0xffffffffll);
-    const int v0 = static_cast<int>(it - t * pieces) * (32 * PASSES) + lane;
-    uint4 w[PASSES];
+    v0 = static_cast<int>(it - t * pieces) * (32 * PASSES) + lane;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i)
       w[i] = v0 + 32 * i < vec ? __ldg(x + t * vec + v0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    slot = lane < k ? __ldg(inv_map + t * k + lane) : -1;
+  };
+  if (it < items) load();  // as in the kernel above
+  const long long n = static_cast<long long>(T) * k;
+  if (!load_problem_tiles(offsets, E, n, s_end, s_pre, status)) return;
+  const int M = s_end[E - 1];
+  while (it < items) {
     // lane j < k holds slot j's row, its tile and the row within the tile
     int my_p = -1, my_r = 0, my_g = 0;
     if (lane < k) {
-      const int p = __ldg(inv_map + t * k + lane);
+      const int p = slot;
       if (p >= 0 && p < M) {
         long long G;
         row_tile(s_end, s_pre, E, p, G, my_r);
@@ -233,15 +251,17 @@ __global__ void __launch_bounds__(256) mx4_permute_kernel(const uint4* x,
     }
     uint32_t codes[PASSES];
     const uint32_t word = quantize(w, v0, vec, codes);
-    const int vs = v0 - lane + 32 * (lane & 15);  // as in the kernel above
+    const int at = v0, vs = v0 - lane + 32 * (lane & 15);
     const bool scales = (lane & 15) < PASSES && vs < vec;
+    it += step;
+    if (it < items) load();
     for (int j = 0; j < k; ++j) {
       const int p = __shfl_sync(0xffffffffu, my_p, j);
       const int g = __shfl_sync(0xffffffffu, my_g, j), r = __shfl_sync(0xffffffffu, my_r, j);
       if (p < 0) continue;  // warp-uniform
 #pragma unroll
       for (int i = 0; i < PASSES; ++i)
-        if (v0 + 32 * i < vec) q[static_cast<size_t>(p) * vec + v0 + 32 * i] = codes[i];
+        if (at + 32 * i < vec) q[static_cast<size_t>(p) * vec + at + 32 * i] = codes[i];
       if (scales) *chunk_word(sf, g, KC, (vs + (lane & 16)) >> 4, r) = word;
     }
   }
@@ -279,18 +299,32 @@ __global__ void __launch_bounds__(256) mx4_dequant_rows_kernel(const uint32_t* q
   q = after_wait(q);
   sf = after_wait(sf);
   offsets = after_wait(offsets);
-  if (!load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
-  const int M = s_end[E - 1];
   const int lane = threadIdx.x & 31, vec = K / 8, KC = mx4_kc(K);
   const int pieces = (vec + 32 * PASSES - 1) / (32 * PASSES);
+  const bool narrow = rows * pieces <= 0xffffffffll;
+  const long long step = static_cast<long long>(gridDim.x) * 8;
+  long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5), next_p = 0;
+  int next_v0 = 0;
+  uint32_t next[PASSES];
+  auto load = [&]() {
+    next_p = item_row(it, pieces, narrow);
+    next_v0 = static_cast<int>(it - next_p * pieces) * (32 * PASSES) + lane;
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i)
+      next[i] = next_v0 + 32 * i < vec ? __ldcs(q + next_p * vec + next_v0 + 32 * i) : 0u;
+  };
+  if (it < rows * pieces) load();  // as in the quantizer
+  if (!load_problem_tiles(offsets, E, rows, s_end, s_pre, status)) return;
+  const int M = s_end[E - 1];
   const long long items = static_cast<long long>(M) * pieces;
-  for (long long it = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items;
-       it += static_cast<long long>(gridDim.x) * 8) {
-    const long long p = item_row(it, pieces, items <= 0xffffffffll);
-    const int v0 = static_cast<int>(it - p * pieces) * (32 * PASSES) + lane;
+  while (it < items) {
+    const long long p = next_p;
+    const int v0 = next_v0;
     uint32_t codes[PASSES], sc[PASSES];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) codes[i] = v0 + 32 * i < vec ? __ldcs(q + p * vec + v0 + 32 * i) : 0u;
+    for (int i = 0; i < PASSES; ++i) codes[i] = next[i];
+    it += step;
+    if (it < items) load();
     long long G;
     int r;
     row_tile(s_end, s_pre, E, p, G, r);
