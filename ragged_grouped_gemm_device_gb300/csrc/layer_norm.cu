@@ -13,7 +13,7 @@
 // in its registers, and the next rows are on their way into shared memory by asynchronous
 // copies. Each thread copies exactly the chunks that it will read, so the ring needs no barrier;
 // what it is for is bytes in flight, which registers cannot hold (with one row of prefetch in
-// registers the backward took 47 us for 16384 x 2048 bf16, 40.7 now: 4.9 TB/s; the forward 20.9: 6.4).
+// registers the backward took 47 us for 16384 x 2048 bf16, 34.6 now: 5.8 TB/s; the forward 20.9: 6.4).
 // The weight gradients are sums over all rows: each block adds the rows it owns in registers (a
 // thread always owns the same columns), leaves one partial row of each gradient in the workspace,
 // and a second small kernel adds the partials in block order. No atomics: the results do not
@@ -172,8 +172,9 @@ __host__ __device__ constexpr int block_threads(int tpr) { return tpr == 32 ? 12
 
 // Blocks on an SM, which size the grids and bound the registers. Forward: 768 threads (16384 x 2048
 // bf16: 20.8 us, the speed of a copy; 27 us with 1024, which spill). Backward: 384 threads with two
-// chunks each (41.5 us then; one chunk each on 512 threads 44 us, on 1024 threads 54 us: each
-// row's reduction and addresses cost a warp as much as its chunks).
+// chunks each (34.6 us, on 512 threads 35.8; at a time when it took 41.5, one chunk each on 512
+// threads took 44, on 1024 threads 54: each row's reduction and addresses cost a warp as much as
+// its chunks).
 constexpr int fwd_blocks_per_sm(int tpr) { return tpr >= 512 ? 1 : 768 / block_threads(tpr); }
 constexpr int bwd_blocks_per_sm(int tpr) { return tpr <= 128 ? 3 : tpr == 256 ? 2 : 1; }
 
@@ -413,28 +414,35 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks_per_sm(TPR)) no
   __shared__ float2 acc[ROWS > 1 ? ROWS - 1 : 1][32];
   const int w = threadIdx.x / TPR;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i)
+  for (int i = 0; i < NCH; ++i) {
+    if constexpr (ROWS > 1) {
 #pragma unroll
-    for (int j = 0; j < VB; ++j) {
-      float vg = dg[i][j], vb = db[i][j];
-      if constexpr (ROWS > 1) {
+      for (int j = 0; j < VB; ++j) {
         __syncthreads();
-        if (w > 0) acc[w - 1][t] = make_float2(vg, vb);
+        if (w > 0) acc[w - 1][t] = make_float2(dg[i][j], db[i][j]);
         __syncthreads();
         if (w == 0) {
 #pragma unroll
           for (int r = 0; r < ROWS - 1; ++r) {
-            vg += acc[r][t].x;
-            vb += acc[r][t].y;
+            dg[i][j] += acc[r][t].x;
+            db[i][j] += acc[r][t].y;
           }
         }
       }
-      const int c = (i * TPR + t) * VB + j;
-      if (w == 0 && c < a.d) {
-        pg[c] = vg;
-        pb[c] = vb;
-      }
     }
+    const int c = (i * TPR + t) * VB;
+    if (w != 0 || c >= a.d) continue;
+    if constexpr (VB > 1) {  // d is a multiple of VB: 16-byte rows of partials (one float at a time: 40 us, not 34.6)
+#pragma unroll
+      for (int j = 0; j < VB; j += 4) {
+        *reinterpret_cast<float4*>(pg + c + j) = make_float4(dg[i][j], dg[i][j + 1], dg[i][j + 2], dg[i][j + 3]);
+        *reinterpret_cast<float4*>(pb + c + j) = make_float4(db[i][j], db[i][j + 1], db[i][j + 2], db[i][j + 3]);
+      }
+    } else {
+      pg[c] = dg[i][0];
+      pb[c] = db[i][0];
+    }
+  }
 }
 
 // Rows too wide for registers: three passes over the row (the later ones from L2), one block a row.
@@ -733,7 +741,7 @@ moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, l
     a.rstd = const_cast<float*>(rstd);
     a.part = wgrad ? static_cast<float*>(ws) : nullptr;
     const int v = 16 / es;
-    const bool vec = d % v == 0 && ldx % v == 0 && lddy % v == 0 && lddx % v == 0 && aligned16(x) && aligned16(dy) &&
+    const bool vec = d % v == 0 && ldx % v == 0 && lddy % v == 0 && lddx % v == 0 && aligned16(ws) && aligned16(x) && aligned16(dy) &&
                      aligned16(dx) && aligned16(gamma);
     blocks = dtype == MOE_DTYPE_BF16 ? launch_norm<bf16>(a, true, vec, s) : launch_norm<float>(a, true, vec, s);
     if ((st = launched()) != MOE_OK) return st;
