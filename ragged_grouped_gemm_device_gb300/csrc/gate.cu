@@ -563,10 +563,6 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(GateBwdArgs a) {
       if (!part || id[i] < 0 || id[i] >= a.E) id[i] = -1;
       else s = fmaf(w[i], dw[i], s);
     }
-    s = group_sum<G>(s);
-#pragma unroll
-    for (int i = 0; i < NS; ++i)
-      if (id[i] >= 0) mine[id[i]] = w[i] * (a.renorm ? dw[i] - s : dw[i]);
     float dot = 0.f;
 #pragma unroll
     for (int l = 0; l < NL; ++l)
@@ -575,7 +571,17 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(GateBwdArgs a) {
         p[l][j] = part ? exp_f(p[l][j] - lse) : 0.f;
         dot = fmaf(p[l][j], c[l][j], dot);
       }
-    dot = group_sum<G>(dot) + (a.renorm ? 0.f : s);
+    // without renormalisation only the sum of the two is wanted
+    if (a.renorm) {
+      s = group_sum<G>(s);
+      dot = group_sum<G>(dot);
+    } else {
+      dot = group_sum<G>(dot + s);
+      s = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+      if (id[i] >= 0) mine[id[i]] = w[i] * (dw[i] - s);
     __syncwarp();
     const float shift = part ? fmaf(cz, lse, -dot) : 0.f;
     T* out = static_cast<T*>(a.dlogits) + (in ? t : 0) * a.ldd;
