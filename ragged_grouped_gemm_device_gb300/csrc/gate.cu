@@ -19,7 +19,7 @@
 // each round instead of sorting once took four times as long). The sorted lists lie in shared
 // memory, where taking a list's next head is one load instead of a shift of eight registers.
 // Measured: 131072 tokens x 256 experts, top 8 of bf16 logits, 51 us without statistics (67 MB of
-// logits, 1.5 TB/s) and 59 with them; its gradient 34 us (3.9 TB/s of logits read and gradient
+// logits, 1.3 TB/s) and 59 with them; its gradient 31.5 us (4.3 TB/s of logits read and gradient
 // written); 16 tokens x 128 experts 2.5 us, where the launch and the chain of rounds are the time.
 // The per-expert sums over the tokens of a lane group stay in registers (lane and element own
 // an expert), a block adds its groups' sums in order and leaves one partial row in the workspace,
@@ -42,8 +42,9 @@ constexpr int MAX_TOPK = 32;
 // Blocks at most, and so rows of partial sums: four for each of the 152 SMs. A constant, because
 // the size of the workspace is host arithmetic.
 constexpr int MAX_BLOCKS = 608;
-// Blocks of the backward at most, ten for each SM: it leaves no partial sums.
-constexpr int BWD_BLOCKS = 1520;
+// Blocks of the backward at most, five for each SM, which is what fits (131072 x 256 bf16: 31.5 us;
+// twice as many 32.2, four times 35.3; more blocks on an SM with fewer registers 33 to 46).
+constexpr int BWD_BLOCKS = 760;
 constexpr unsigned FULL = 0xffffffffu;
 
 // Eight consecutive logits from expert e0 of a row; -inf past the last expert. VEC: the row is
@@ -629,7 +630,7 @@ moe_status_t launch_bwd(const GateBwdArgs& a, int blocks, cudaStream_t s) {
 // 51 us with 4 lists on 8 lanes, 56 with 2 on 16 and 62 with 1 on 32. Few tokens (less than one for
 // each warp of the grid) take as many lanes as hold eight experts each, which keeps more warps at
 // work, and so do rows that are read one element at a time. The backward has no rounds and waits
-// for its loads: always full width (34 us, against 44 on 8 lanes).
+// for its loads: always full width (34 us then, against 44 on 8 lanes).
 struct Width {
   int lists, lanes;
 };
