@@ -7,7 +7,8 @@ with the balance and z losses of the gate, and the gradient of all of it. The ex
 ExpertLayer (BF16: training and serving) or an Mxfp4ExpertLayer (4-bit: serving). The router's
 projection and the residual additions are plain torch operations in fp32; every other step is a
 library kernel. Buffers are allocated once per shape and reused, so what forward() and
-backward() return is overwritten by the next call.
+backward() return is overwritten by the next call. The calls record no autograd history (what they return
+requires no gradient); the gradients are backward()'s.
 """
 from __future__ import annotations
 
@@ -46,6 +47,7 @@ class MoEBlock:
         self.dgamma, self.dbeta = new(d), new(d)
         self._T = T
 
+    @torch.no_grad()
     def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
         """x [T, d] bf16 (any row pitch) -> out [T, d] bf16. token_mask nullable [T] bool: padding tokens
         (False) are routed nowhere, count in no loss and pass through the residual unchanged. `loss`
@@ -59,6 +61,7 @@ class MoEBlock:
                           self.counts, self.n_valid, self.prob_sum, self.loss, self.gate_ws)
         return x + self.experts.forward(self.normed, self.ids, self.weights)
 
+    @torch.no_grad()
     def backward(self, dout: torch.Tensor, d_loss: torch.Tensor = None) -> dict:
         """dout [T, d] bf16, d_loss nullable [2] fp32 (the gradients of the two losses) -> the gradients
         dx (bf16), gamma, beta, w_router, w_ug, w_down (fp32) of the last forward."""

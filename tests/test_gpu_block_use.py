@@ -1,0 +1,38 @@
+"""How MoEBlock behaves in a user's program beside its numbers: under autograd and with inputs that change."""
+import pytest
+import torch
+
+from ragged_grouped_gemm_device_gb300.block import MoEBlock
+from ragged_grouped_gemm_device_gb300.layer import ExpertLayer
+
+pytestmark = pytest.mark.gpu
+
+T, E, k, d, h = 24, 6, 2, 64, 40
+
+
+def _block(parameters=False):
+    g = torch.Generator("cuda").manual_seed(1)
+    n = lambda *s, dtype=torch.float32: torch.randn(*s, generator=g, device="cuda").to(dtype)
+    wrap = torch.nn.Parameter if parameters else (lambda t: t)
+    w = [wrap(t) for t in (1 + 0.2 * n(d), 0.1 * n(d), n(E, d) / 8)]
+    experts = ExpertLayer(n(E, 2 * h, d, dtype=torch.bfloat16) / 8, n(E, h, d, dtype=torch.bfloat16) / 6)
+    return MoEBlock(*w, experts, k), n(T, d, dtype=torch.bfloat16), n(T, d, dtype=torch.bfloat16)
+
+
+def test_no_partial_autograd_history(lib):
+    """An output with the history of the residual alone would give x a gradient without the experts'."""
+    block, x, _ = _block()
+    want = block.forward(x)
+    out = block.forward(x.clone().requires_grad_(True))
+    assert torch.equal(out, want) and not out.requires_grad
+    with pytest.raises(RuntimeError):
+        out.sum().backward()
+
+
+def test_weights_that_are_parameters(lib):
+    block, x, dout = _block()
+    want, grads = block.forward(x).clone(), {n: g.clone() for n, g in block.backward(dout).items()}
+    block, _, _ = _block(parameters=True)
+    assert torch.equal(block.forward(x), want)
+    got = block.backward(dout)
+    assert all(torch.equal(got[n], grads[n]) and not got[n].requires_grad for n in grads)
