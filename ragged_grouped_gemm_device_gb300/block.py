@@ -18,6 +18,11 @@ from . import _lib
 from .layer import ExpertLayer, _dense
 
 
+def _version(t: torch.Tensor):
+    """The count of in-place changes that torch keeps of a tensor (None for an inference tensor, which has none)."""
+    return None if t.is_inference() else t._version
+
+
 class MoEBlock:
     """gamma, beta [d] (fp32 or bf16), w_router [E, d] fp32, experts over E experts of width d."""
 
@@ -51,10 +56,12 @@ class MoEBlock:
     def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
         """x [T, d] bf16 (any row pitch) -> out [T, d] bf16. token_mask nullable [T] bool: padding tokens
         (False) are routed nowhere, count in no loss and pass through the residual unchanged. `loss`
-        holds the balance and the z loss, `counts` the slots per expert."""
+        holds the balance and the z loss, `counts` the slots per expert. x, gamma and w_router are not copied:
+        backward() reads them again and refuses when one was changed in place since."""
         T = x.shape[0]
         self._buffers(T)
-        self.x = x
+        self.x = x  # read again by backward(), like gamma and w_router
+        self._read = [(t, _version(t)) for t in (x, self.gamma, self.w_router)]
         _lib.moe_layer_norm_fwd(x, self.gamma, self.beta, T, self.d, self.eps, self.normed, self.mean, self.rstd)
         torch.mm(self.normed.float(), self.w_router.t(), out=self.logits)
         _lib.moe_gate_fwd(self.logits, token_mask, T, self.k, self.E, self.flags, self.ids, self.weights, self.lse,
@@ -67,6 +74,8 @@ class MoEBlock:
         dx (bf16), gamma, beta, w_router, w_ug, w_down (fp32) of the last forward."""
         if not isinstance(self.experts, ExpertLayer):
             raise TypeError("4-bit experts have no backward: train on an ExpertLayer")
+        if any(_version(t) != v for t, v in self._read):
+            raise RuntimeError("x, gamma or w_router was changed in place since forward(): their gradients would be wrong")
         T, dout = self._T, _dense(dout)
         dn, dw_ug, dw_down, dweights = self.experts.backward(dout)
         _lib.moe_gate_bwd(self.logits, self.lse, self.ids, self.weights, self.counts, self.n_valid, dweights, d_loss, T,

@@ -36,3 +36,19 @@ def test_weights_that_are_parameters(lib):
     assert torch.equal(block.forward(x), want)
     got = block.backward(dout)
     assert all(torch.equal(got[n], grads[n]) and not got[n].requires_grad for n in grads)
+
+
+@pytest.mark.parametrize("which", ["x", "gamma", "w_router"])
+def test_inputs_changed_before_the_backward(lib, which):
+    """The backward reads x, gamma and w_router again: after a change in place its gradients would be those of
+    another forward."""
+    block, x, dout = _block()
+    block.forward(x)
+    {"x": x, "gamma": block.gamma, "w_router": block.w_router}[which].mul_(2.0)
+    with pytest.raises(RuntimeError, match="in place"):
+        block.backward(dout)
+    block.forward(x)
+    block.backward(dout)
+    with torch.inference_mode():  # tensors without a count of changes
+        block.forward(x.clone())
+        block.backward(dout)
