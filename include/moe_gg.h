@@ -534,6 +534,8 @@ moe_status_t moe_gate_bwd(const void* logits, int dtype, long long ld, const flo
  * Backward: dx = rstd (gamma dy - mean(gamma dy) - xhat mean(gamma dy xhat)), rounded once to
  * `dtype`; dgamma = sum_t dy xhat and dbeta = sum_t dy, fp32 [d], each nullable, summed in a fixed
  * order (zeros for T = 0).
+ * y may be x, and dx may be x or dy (the same base and pitch); other overlaps of inputs and outputs are
+ * not allowed.
  *  ws      moe_workspace_bytes(MOE_OP_LAYER_NORM_BWD, T, 1, 1, d, 0, 0) bytes when dgamma or dbeta
  *          is wanted.
  * Limits: 1 <= d <= 2^20; pointers aligned to their element size (rows whose bases and pitches are

@@ -642,10 +642,11 @@ int launch_norm(const NormArgs& a, bool bwd, bool vec, cudaStream_t s) {
     norm_fwd_wide_kernel<T><<<wide, WIDE_THREADS, 0, s>>>(a);
     return wide;
   }
-  norm_bwd_wide_kernel<T><<<wide, WIDE_THREADS, 0, s>>>(a);
+  // the weight gradients first: dx may lie over x or dy
   const int parts = std::min(a.T, BWD_MAX_BLOCKS);
   if (a.part != nullptr)
     norm_wgrad_wide_kernel<T><<<dim3((a.d + 255) / 256, parts), 256, 0, s>>>(a);
+  norm_bwd_wide_kernel<T><<<wide, WIDE_THREADS, 0, s>>>(a);
   return parts;
 }
 
