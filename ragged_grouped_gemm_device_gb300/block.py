@@ -58,7 +58,11 @@ class MoEBlock:
         (False) are routed nowhere, count in no loss and pass through the residual unchanged. `loss`
         holds the balance and the z loss, `counts` the slots per expert. x, gamma and w_router are not copied:
         backward() reads them again and refuses when one was changed in place since."""
+        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16 or x.device != self.device:
+            raise ValueError(f"x has to be [T, {self.d}] bfloat16 on {self.device}")
         T = x.shape[0]
+        if token_mask is not None and tuple(token_mask.shape) != (T,):
+            raise ValueError(f"token_mask has to be [{T}]")
         self._buffers(T)
         self.x = x  # read again by backward(), like gamma and w_router
         self._read = [(t, _version(t)) for t in (x, self.gamma, self.w_router)]
@@ -76,7 +80,10 @@ class MoEBlock:
             raise TypeError("4-bit experts have no backward: train on an ExpertLayer")
         if any(_version(t) != v for t, v in self._read):
             raise RuntimeError("x, gamma or w_router was changed in place since forward(): their gradients would be wrong")
-        T, dout = self._T, _dense(dout)
+        T = self._T
+        if tuple(dout.shape) != (T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:
+            raise ValueError(f"dout has to be [{T}, {self.d}] bfloat16 on {self.device}")
+        dout = _dense(dout)
         dn, dw_ug, dw_down, dweights = self.experts.backward(dout)
         _lib.moe_gate_bwd(self.logits, self.lse, self.ids, self.weights, self.counts, self.n_valid, dweights, d_loss, T,
                           self.k, self.E, self.flags, self.dlogits)

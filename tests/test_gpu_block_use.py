@@ -52,3 +52,22 @@ def test_inputs_changed_before_the_backward(lib, which):
     with torch.inference_mode():  # tensors without a count of changes
         block.forward(x.clone())
         block.backward(dout)
+
+
+def test_refusals(lib):
+    """What the experts' calls would read by its address alone is checked here: a gradient of another type or with
+    fewer rows, tokens of another width or type, a mask of another length."""
+    block, x, dout = _block()
+    block.forward(x)
+    for bad in (dout.float(), dout.half(), dout[:-1], dout[:, :-8], dout[0], dout.cpu()):
+        with pytest.raises(ValueError):
+            block.backward(bad)
+    block.backward(dout[:1].expand(T, d))
+    for bad in (x.float(), x[:, :-8], x[0], x.cpu()):
+        with pytest.raises(ValueError):
+            block.forward(bad)
+    mask = torch.ones(T, dtype=torch.bool, device="cuda")
+    for bad in (mask[:-1], torch.ones(T + 1, dtype=torch.bool, device="cuda"), mask[None], mask.float()):
+        with pytest.raises(ValueError):
+            block.forward(x, bad)
+    block.forward(x, mask.byte())
