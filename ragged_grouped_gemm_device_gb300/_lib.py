@@ -141,7 +141,8 @@ def _install_binding():
     except ImportError:
         return
 
-    _binding.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in COMPILED}, _check)
+    entry_points = COMPILED + ("moe_workspace_bytes",)
+    _binding.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in entry_points}, _check)
     for n in COMPILED:
         PYTHON_BINDING[n] = globals()[n]
         globals()[n] = getattr(_binding, n)
@@ -179,6 +180,16 @@ def _typed(t, dtype, numel, name):
         return None
     if t.dtype is not dtype or t.numel() < numel or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {numel} elements of {dtype}")
+    return t.data_ptr()
+
+
+def _bytes(t, nbytes, name):
+    """Pointer of a contiguous CUDA tensor of at least `nbytes` bytes, whatever its type: packed codes, scales,
+    prepared weights (None passes)."""
+    if t is None:
+        return None
+    if t.numel() * t.element_size() < nbytes or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of at least {nbytes} bytes")
     return t.data_ptr()
 
 
@@ -363,29 +374,53 @@ def moe_loop_swiglu_fwd(xp, offsets, E, cap, d, h, w_ug, w_down, y, a_save, save
 
 
 def moe_mx4_prepare_weights(w_ug, w_down, E, d, h, mxw, stream=None):
+    import torch
+    bf = torch.bfloat16
     _check("moe_mx4_prepare_weights", load().moe_mx4_prepare_weights(
-        _ptr(w_ug), _ptr(w_down), E, d, h, _ptr(mxw), _nbytes(mxw), _stream(stream)))
+        _typed(w_ug, bf, 2 * E * h * d, "w_ug"), _typed(w_down, bf, E * h * d, "w_down"), E, d, h, _ptr(mxw),
+        _nbytes(mxw), _stream(stream)))
+
+
+def _mx4_scale_bytes(rows, E, K):
+    """Bytes of the scale atoms of `rows` rows of K elements (0 without rows and for sizes that the library refuses)."""
+    return 0 if not 0 < rows < 1 << 31 else moe_workspace_bytes(OP_MX4_ROW_SCALES, rows, 1, E, K, 32)
 
 
 def moe_mx4_quantize_rows(x, offsets, E, cap, K, q, sf, dev_status=None, stream=None):
+    import torch
+    i32 = torch.int32
     _check("moe_mx4_quantize_rows", load().moe_mx4_quantize_rows(
-        _ptr(x), _ptr(offsets), E, cap, K, _ptr(q), _ptr(sf), _ptr(dev_status), _stream(stream)))
+        _typed(x, torch.bfloat16, cap * K, "x"), _typed(offsets, i32, E, "offsets"), E, cap, K,
+        _bytes(q, cap * K // 2, "q"), _bytes(sf, _mx4_scale_bytes(cap, E, K), "sf"),
+        _typed(dev_status, i32, 1, "dev_status"), _stream(stream)))
 
 
 def moe_mx4_dequantize_rows(q, sf, offsets, E, cap, K, x, dev_status=None, stream=None):
+    import torch
+    i32 = torch.int32
     _check("moe_mx4_dequantize_rows", load().moe_mx4_dequantize_rows(
-        _ptr(q), _ptr(sf), _ptr(offsets), E, cap, K, _ptr(x), _ptr(dev_status), _stream(stream)))
+        _bytes(q, cap * K // 2, "q"), _bytes(sf, _mx4_scale_bytes(cap, E, K), "sf"), _typed(offsets, i32, E, "offsets"),
+        E, cap, K, _typed(x, torch.bfloat16, cap * K, "x"), _typed(dev_status, i32, 1, "dev_status"), _stream(stream)))
 
 
 def moe_permute_mxfp4(x, inv_map, offsets, T, top_k, E, d, q, sf, dev_status=None, stream=None):
+    import torch
+    i32, n = torch.int32, T * top_k
     _check("moe_permute_mxfp4", load().moe_permute_mxfp4(
-        _ptr(x), _ptr(inv_map), _ptr(offsets), T, top_k, E, d, _ptr(q), _ptr(sf), _ptr(dev_status), _stream(stream)))
+        _typed(x, torch.bfloat16, T * d, "x"), _typed(inv_map, i32, n, "inv_map"), _typed(offsets, i32, E, "offsets"),
+        T, top_k, E, d, _bytes(q, n * d // 2, "q"), _bytes(sf, _mx4_scale_bytes(n, E, d), "sf"),
+        _typed(dev_status, i32, 1, "dev_status"), _stream(stream)))
 
 
 def moe_grouped_swiglu_fwd_mxfp4(xq, xsf, offsets, E, cap, d, h, mxw, y, ws, dev_status=None, stream=None):
+    import torch
+    i32 = torch.int32
     _check("moe_grouped_swiglu_fwd_mxfp4", load().moe_grouped_swiglu_fwd_mxfp4(
-        _ptr(xq), _ptr(xsf), _ptr(offsets), E, cap, d, h, _ptr(mxw), _ptr(y), _ptr(ws), _nbytes(ws),
-        _ptr(dev_status), _stream(stream)))
+        _bytes(xq, cap * d // 2, "xq"), _bytes(xsf, _mx4_scale_bytes(cap, E, d), "xsf"),
+        _typed(offsets, i32, E, "offsets"), E, cap, d, h,
+        _bytes(mxw, moe_workspace_bytes(OP_MX4_WEIGHTS, 0, 1, E, d, h), "mxw"),
+        _typed(y, torch.bfloat16, cap * d, "y"), _ptr(ws), _nbytes(ws), _typed(dev_status, i32, 1, "dev_status"),
+        _stream(stream)))
 
 
 def moe_gate_fwd(logits, token_mask, T, top_k, E, flags, ids, weights, lse=None, counts=None, n_valid=None,

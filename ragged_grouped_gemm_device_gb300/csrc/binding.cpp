@@ -21,7 +21,7 @@
 #define FUNCTIONS(X)                                                                                         \
   X(moe_layer_norm_fwd) X(moe_layer_norm_bwd) X(moe_gate_fwd) X(moe_gate_bwd) X(moe_mx4_quantize_rows)        \
   X(moe_mx4_dequantize_rows) X(moe_permute_mxfp4) X(moe_grouped_swiglu_fwd_mxfp4) X(moe_unpermute_combine)    \
-  X(moe_route_offsets)
+  X(moe_route_offsets) X(moe_workspace_bytes)
 #define DECLARE(f) static __typeof__(&f) p_##f;
 FUNCTIONS(DECLARE)
 
@@ -111,6 +111,30 @@ int typed(PyObject* o, at::ScalarType type, long long numel, const char* name, A
   }
   p->p = t->mutable_data_ptr();
   return 0;
+}
+
+// None, or a contiguous CUDA tensor of any type with at least `nbytes` bytes: codes, scales, prepared weights
+int raw(PyObject* o, long long nbytes, const char* name, Any* p) {
+  p->p = nullptr;
+  if (o == Py_None) return 0;
+  const at::Tensor* t = tensor(o);
+  if (t == nullptr) return -1;
+  if (static_cast<long long>(t->numel()) * static_cast<long long>(t->element_size()) < nbytes || !t->is_cuda() ||
+      !t->is_contiguous()) {
+    PyErr_Format(PyExc_ValueError, "%s: expected a contiguous CUDA tensor of at least %lld bytes", name, nbytes);
+    return -1;
+  }
+  p->p = t->mutable_data_ptr();
+  return 0;
+}
+
+// None, or a device status word
+int status(PyObject* o, Any* p) { return typed(o, at::kInt, 1, "dev_status", p); }
+
+// bytes of the scale atoms of `rows` rows of K elements (0 without rows and for sizes that the library refuses)
+long long scale_bytes(long long rows, int E, int K) {
+  if (rows <= 0 || rows > INT_MAX) return 0;
+  return static_cast<long long>(p_moe_workspace_bytes(MOE_OP_MX4_ROW_SCALES, static_cast<int>(rows), 1, E, K, 32, 0));
 }
 
 int bytes_of(PyObject* o, size_t* b) {
@@ -284,8 +308,11 @@ PyObject* mx4_quantize_rows(ARGS) {
   int E, cap, K;
   Any x, off, q, sf, st;
   moe_stream_t s;
-  if (plain(a[0], &x) < 0 || plain(a[1], &off) < 0 || as_int(a[2], &E) < 0 || as_int(a[3], &cap) < 0 || as_int(a[4], &K) < 0 ||
-      plain(a[5], &q) < 0 || plain(a[6], &sf) < 0 || plain(a[7], &st) < 0 || as_stream(a[8], &s) < 0)
+  if (as_int(a[2], &E) < 0 || as_int(a[3], &cap) < 0 || as_int(a[4], &K) < 0) return nullptr;
+  const long long n = (long long)cap * K;
+  if (typed(a[0], at::kBFloat16, n, "x", &x) < 0 || typed(a[1], at::kInt, E, "offsets", &off) < 0 ||
+      raw(a[5], n / 2, "q", &q) < 0 || raw(a[6], scale_bytes(cap, E, K), "sf", &sf) < 0 || status(a[7], &st) < 0 ||
+      as_stream(a[8], &s) < 0)
     return nullptr;
   return finish("moe_mx4_quantize_rows", p_moe_mx4_quantize_rows(x, off, E, cap, K, q, sf, st, s));
 }
@@ -295,8 +322,11 @@ PyObject* mx4_dequantize_rows(ARGS) {
   int E, cap, K;
   Any x, off, q, sf, st;
   moe_stream_t s;
-  if (plain(a[0], &q) < 0 || plain(a[1], &sf) < 0 || plain(a[2], &off) < 0 || as_int(a[3], &E) < 0 || as_int(a[4], &cap) < 0 ||
-      as_int(a[5], &K) < 0 || plain(a[6], &x) < 0 || plain(a[7], &st) < 0 || as_stream(a[8], &s) < 0)
+  if (as_int(a[3], &E) < 0 || as_int(a[4], &cap) < 0 || as_int(a[5], &K) < 0) return nullptr;
+  const long long n = (long long)cap * K;
+  if (raw(a[0], n / 2, "q", &q) < 0 || raw(a[1], scale_bytes(cap, E, K), "sf", &sf) < 0 ||
+      typed(a[2], at::kInt, E, "offsets", &off) < 0 || typed(a[6], at::kBFloat16, n, "x", &x) < 0 || status(a[7], &st) < 0 ||
+      as_stream(a[8], &s) < 0)
     return nullptr;
   return finish("moe_mx4_dequantize_rows", p_moe_mx4_dequantize_rows(q, sf, off, E, cap, K, x, st, s));
 }
@@ -306,9 +336,12 @@ PyObject* permute_mxfp4(ARGS) {
   int T, k, E, d;
   Any x, inv, off, q, sf, st;
   moe_stream_t s;
-  if (plain(a[0], &x) < 0 || plain(a[1], &inv) < 0 || plain(a[2], &off) < 0 || as_int(a[3], &T) < 0 || as_int(a[4], &k) < 0 ||
-      as_int(a[5], &E) < 0 || as_int(a[6], &d) < 0 || plain(a[7], &q) < 0 || plain(a[8], &sf) < 0 || plain(a[9], &st) < 0 ||
-      as_stream(a[10], &s) < 0)
+  if (as_int(a[3], &T) < 0 || as_int(a[4], &k) < 0 || as_int(a[5], &E) < 0 || as_int(a[6], &d) < 0) return nullptr;
+  const long long n = (long long)T * k;
+  const long long code_bytes = n > 0 && n <= INT_MAX ? n * d / 2 : 0;  // of other counts the library says what is wrong
+  if (typed(a[0], at::kBFloat16, (long long)T * d, "x", &x) < 0 || typed(a[1], at::kInt, n, "inv_map", &inv) < 0 ||
+      typed(a[2], at::kInt, E, "offsets", &off) < 0 || raw(a[7], code_bytes, "q", &q) < 0 ||
+      raw(a[8], scale_bytes(n, E, d), "sf", &sf) < 0 || status(a[9], &st) < 0 || as_stream(a[10], &s) < 0)
     return nullptr;
   return finish("moe_permute_mxfp4", p_moe_permute_mxfp4(x, inv, off, T, k, E, d, q, sf, st, s));
 }
@@ -320,9 +353,13 @@ PyObject* grouped_swiglu_fwd_mxfp4(ARGS) {
   Any xq, xsf, off, mxw, y, ws, st;
   size_t n;
   moe_stream_t s;
-  if (plain(a[0], &xq) < 0 || plain(a[1], &xsf) < 0 || plain(a[2], &off) < 0 || as_int(a[3], &E) < 0 || as_int(a[4], &cap) < 0 ||
-      as_int(a[5], &d) < 0 || as_int(a[6], &h) < 0 || plain(a[7], &mxw) < 0 || plain(a[8], &y) < 0 || plain(a[9], &ws) < 0 ||
-      bytes_of(a[9], &n) < 0 || plain(a[10], &st) < 0 || as_stream(a[11], &s) < 0)
+  if (as_int(a[3], &E) < 0 || as_int(a[4], &cap) < 0 || as_int(a[5], &d) < 0 || as_int(a[6], &h) < 0) return nullptr;
+  const long long items = (long long)cap * d;
+  if (raw(a[0], items / 2, "xq", &xq) < 0 || raw(a[1], scale_bytes(cap, E, d), "xsf", &xsf) < 0 ||
+      typed(a[2], at::kInt, E, "offsets", &off) < 0 ||
+      raw(a[7], static_cast<long long>(p_moe_workspace_bytes(MOE_OP_MX4_WEIGHTS, 0, 1, E, d, h, 0)), "mxw", &mxw) < 0 ||
+      typed(a[8], at::kBFloat16, items, "y", &y) < 0 || plain(a[9], &ws) < 0 || bytes_of(a[9], &n) < 0 ||
+      status(a[10], &st) < 0 || as_stream(a[11], &s) < 0)
     return nullptr;
   return finish("moe_grouped_swiglu_fwd_mxfp4",
                 p_moe_grouped_swiglu_fwd_mxfp4(xq, xsf, off, E, cap, d, h, mxw, y, ws, n, st, s));
