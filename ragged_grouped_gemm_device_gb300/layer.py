@@ -131,8 +131,14 @@ class Mxfp4ExpertLayer:
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, stream=None):
         """x [T, d] bf16, ids [T, k] int32, weights [T, k] fp32 -> out [T, d] bf16."""
-        x, ids, weights = _dense(x), _dense(ids), _dense(weights)
+        if ids.dim() != 2 or ids.dtype != torch.int32:
+            raise ValueError("ids has to be [T, k] int32")
         T, k = ids.shape
+        if tuple(x.shape) != (T, self.d) or x.dtype != torch.bfloat16:
+            raise ValueError(f"x has to be [{T}, {self.d}] bfloat16")
+        if tuple(weights.shape) != (T, k) or weights.dtype != torch.float32:
+            raise ValueError(f"weights has to be [{T}, {k}] float32")
+        x, ids, weights = _dense(x), _dense(ids), _dense(weights)
         self._buffers(T, k)
         E, d, h, n = self.E, self.d, self.h, T * k
         _lib.moe_route_offsets(ids, T, k, E, self.counts, self.offsets, self.sorted_src, self.inv_map,

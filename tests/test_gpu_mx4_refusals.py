@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from ragged_grouped_gemm_device_gb300 import _lib
+from ragged_grouped_gemm_device_gb300.layer import Mxfp4ExpertLayer
 from test_mx4_arguments import BF, E, F32, I32, NAMES, T, U8, _args, cap, d, h, k  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -30,3 +31,19 @@ def test_types_and_sizes_are_refused(lib, name):
             with pytest.raises(ValueError):
                 call(**sizes, **{**good, n: good[n].cpu()})
     torch.cuda.synchronize()
+
+
+def test_layer_refusals(lib):
+    layer = Mxfp4ExpertLayer(torch.zeros(E, 2 * h, d, dtype=BF, device="cuda"), torch.zeros(E, h, d, dtype=BF, device="cuda"))
+    x, ids = torch.ones(T, d, dtype=BF, device="cuda"), torch.zeros(T, k, dtype=I32, device="cuda")
+    w = torch.ones(T, k, device="cuda")
+    assert (layer.forward(x, ids, w) == 0).all()
+    good = dict(x=x, ids=ids, weights=w)
+    bad = dict(x=[x.float(), x[:-1], x[:, :-32], x[0]], ids=[ids.long(), ids[:-1], ids[0]],
+               weights=[w.double(), w.to(BF), w[:-1], w[:, :-1]])
+    for n, values in bad.items():
+        for v in values:
+            with pytest.raises(ValueError):
+                layer.forward(**{**good, n: v})
+    with pytest.raises(ValueError):
+        layer.forward(x.cpu(), ids, w)
