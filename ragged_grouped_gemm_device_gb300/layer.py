@@ -5,6 +5,8 @@ calls with new routing allocate nothing ("Section 09: Grouped GEMM" §9.4: fixed
 shapes, unpadded compute)."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import _lib
@@ -16,6 +18,13 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
     expanded [T, d] tensor with strides (0, 0)), which "Grouped expert GEMM" lists as an edge case
     of the grouped GEMM's backward -- is materialised once here; dense tensors pass through."""
     return t if t.is_contiguous() else t.contiguous()
+
+
+def _on(stream):
+    """`stream` (nullable) as torch's current one, for the dense copies and buffers of a call whose kernels run
+    on it: a copy made on another stream would be read before it is written, and its memory given away
+    while it is still read. The caller's own tensors have to be ready on `stream`."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class ExpertLayer:
@@ -62,9 +71,10 @@ class ExpertLayer:
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, stream=None):
         """x [T, d] bf16, ids [T, k] int32, weights [T, k] fp32 -> out [T, d] bf16."""
-        x, ids, weights = _dense(x), _dense(ids), _dense(weights)
         T, k = ids.shape
-        self._buffers(T, k)
+        with _on(stream):
+            x, ids, weights = _dense(x), _dense(ids), _dense(weights)
+            self._buffers(T, k)
         self.T, self.k, self.weights = T, k, weights
         E, d, h, n = self.E, self.d, self.h, T * k
         _lib.moe_route_offsets(ids, T, k, E, self.counts, self.offsets, self.sorted_src, self.inv_map,
@@ -87,7 +97,8 @@ class ExpertLayer:
         """dout [T, d] bf16 -> (dx [T, d] bf16, dW_ug [E, 2h, d] fp32, dW_down [E, h, d] fp32,
         d_weights [T, k] fp32: the gradient of the routing weights, 0 for dropped slots)."""
         T, k, E, d, h, n = self.T, self.k, self.E, self.d, self.h, self.T * self.k
-        dout = _dense(dout)
+        with _on(stream):
+            dout = _dense(dout)
         _lib.moe_permute(dout, self.sorted_src, self.offsets, None, T, k, E, d, self.dy, stream)
         _lib.moe_grouped_bwd(self.dy, self.xp, self.a, self.saved, self.offsets, self.sorted_src, self.weights,
                              E, n, d, h, self.w_ug,
@@ -111,10 +122,12 @@ class Mxfp4ExpertLayer:
         self.E, self.d, self.h = E, d, two_h // 2
         self.device = w_ug.device
         n = _lib.moe_workspace_bytes(_lib.OP_MX4_WEIGHTS, 0, 1, E, d, self.h)
-        self.weights = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
-        _lib.moe_mx4_prepare_weights(w_ug.contiguous(), w_down.contiguous(), E, d, self.h, self.weights, stream)
+        with _on(stream):
+            self.weights = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+            w_ug, w_down = _dense(w_ug), _dense(w_down)
+            self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
+        _lib.moe_mx4_prepare_weights(w_ug, w_down, E, d, self.h, self.weights, stream)
         self._key = None
-        self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def _buffers(self, T: int, k: int):
         if self._key == (T, k):
@@ -138,8 +151,9 @@ class Mxfp4ExpertLayer:
             raise ValueError(f"x has to be [{T}, {self.d}] bfloat16")
         if tuple(weights.shape) != (T, k) or weights.dtype != torch.float32:
             raise ValueError(f"weights has to be [{T}, {k}] float32")
-        x, ids, weights = _dense(x), _dense(ids), _dense(weights)
-        self._buffers(T, k)
+        with _on(stream):
+            x, ids, weights = _dense(x), _dense(ids), _dense(weights)
+            self._buffers(T, k)
         E, d, h, n = self.E, self.d, self.h, T * k
         _lib.moe_route_offsets(ids, T, k, E, self.counts, self.offsets, self.sorted_src, self.inv_map,
                                self.route_ws, stream)
