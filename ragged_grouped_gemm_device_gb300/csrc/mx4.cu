@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(256) mx4_quant_cols_kernel(const bf16* __restr
 // give (the rows of a product are independent).
 enum { MX4_UP = 0, MX4_DOWN = 1 };
 
-constexpr int BM = 128;
+constexpr int BM = 128;                        // as row_tiles() counts
 constexpr int BN = 256;
 constexpr int STAGE_K = 256;                 // elements of K per stage: 128 bytes of codes
 constexpr int UK = 64;                       // K of one MMA
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(Shape<MODE>::threads, 1) mx4_gemm_kernel(const
     if (lane == 0) pre[0] = 0;
     for (int base = 0; base < E; base += 32) {
       const int e = base + lane;
-      int v = (e < E) ? (offs[e + 1] - offs[e] + BM - 1) / BM : 0;
+      int v = (e < E) ? row_tiles(offs[e + 1] - offs[e]) : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int nb = __shfl_up_sync(0xffffffffu, v, o);

@@ -6,6 +6,12 @@
 
 namespace moe {
 
+// 128-row tiles of an expert's rows, which may be as many as an int holds (rows + 127 may not)
+__host__ __device__ constexpr int row_tiles(int rows) { return rows / 128 + (rows % 128 > 0 ? 1 : 0); }
+static_assert(row_tiles(0) == 0 && row_tiles(1) == 1 && row_tiles(128) == 1 && row_tiles(129) == 2 &&
+                  row_tiles(0x7fffffff) == 1 << 24,
+              "tiles of a row count");
+
 // The problem list as the grouped GEMM derives it from the offsets: s_end[e] = inclusive end of
 // expert e's rows, s_pre[e] = 128-row tiles of the experts before e (block-wide scan, 256
 // threads). Offsets that decrease or end past `rows` would place rows outside the scale atoms:
@@ -23,7 +29,7 @@ static __device__ bool load_problem_tiles(const int32_t* __restrict__ offsets, i
       const int end = __ldg(offsets + e);
       const int start = e > 0 ? __ldg(offsets + e - 1) : 0;
       s_end[e] = end;
-      tiles = (end - start + 127) / 128;
+      tiles = row_tiles(end - start);
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = tiles;
