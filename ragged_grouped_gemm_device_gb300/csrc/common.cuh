@@ -66,7 +66,10 @@ inline cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, unsign
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...);
+  const cudaError_t err = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(given)...);
+  // the caller reports it: left in the runtime, the next call that asks would report it again
+  if (err != cudaSuccess) (void)cudaGetLastError();
+  return err;
 }
 
 // ---------------------------------------------------------------------------------- register shares

@@ -573,81 +573,80 @@ __global__ void __launch_bounds__(1024) norm_partials_kernel(const float* part, 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-moe_status_t launched() {
-  const cudaError_t err = cudaGetLastError();
-  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
-}
-
+// The launches below leave the blocks launched in `grid`.
 template <typename T, int VB, int NCH, int TPR>
-int launch_fwd_rows(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_fwd_rows(const NormArgs& a, cudaStream_t s, int& grid) {
   constexpr int ROWS = block_threads(TPR) / TPR;
   const long long most = fwd_blocks_per_sm(TPR) * static_cast<long long>(device_sm_count());
-  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, most));
+  grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, most));
   constexpr int smem = Feed<T, VB, NCH, TPR, 1>::smem_bytes;
-  if (smem > 48 * 1024 &&
-      ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_fwd_kernel<T, VB, NCH, TPR>), smem) != cudaSuccess)
-    return grid;  // the launch below the limit would fail too: the caller reads the error
-  launch_dependent(norm_fwd_kernel<T, VB, NCH, TPR>, grid, block_threads(TPR), smem, s, a);
-  return grid;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_fwd_kernel<T, VB, NCH, TPR>), smem);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(norm_fwd_kernel<T, VB, NCH, TPR>, grid, block_threads(TPR), smem, s, a);
 }
 template <typename T, int VB, int NCH, int TPR>
-int launch_bwd_rows(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_bwd_rows(const NormArgs& a, cudaStream_t s, int& grid) {
   constexpr int ROWS = block_threads(TPR) / TPR;
-  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, std::min(bwd_blocks_per_sm(TPR) * device_sm_count(), BWD_MAX_BLOCKS)));
+  grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, std::min(bwd_blocks_per_sm(TPR) * device_sm_count(), BWD_MAX_BLOCKS)));
   constexpr int smem = Feed<T, VB, NCH, TPR, 2>::smem_bytes;
-  if (smem > 48 * 1024 &&
-      ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_bwd_kernel<T, VB, NCH, TPR>), smem) != cudaSuccess)
-    return grid;
-  launch_dependent(norm_bwd_kernel<T, VB, NCH, TPR>, grid, block_threads(TPR), smem, s, a);
-  return grid;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(norm_bwd_kernel<T, VB, NCH, TPR>), smem);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(norm_bwd_kernel<T, VB, NCH, TPR>, grid, block_threads(TPR), smem, s, a);
 }
 
-// Threads per row and chunks (16 bytes, or one element) per thread. The functions return the blocks
-// launched, 0 for a row wider than any layout.
+// Threads per row and chunks (16 bytes, or one element) per thread. A row wider than any layout launches
+// nothing and leaves `grid` 0.
 // Forward: two chunks a thread (eight elements without alignment), so that a row takes few warps.
 template <typename T, int VB, int U>
-int fwd_by_width(const NormArgs& a, cudaStream_t s) {
+cudaError_t fwd_by_width(const NormArgs& a, cudaStream_t s, int& grid) {
   const int chunks = (a.d + VB - 1) / VB;
-  if (chunks <= 32 * U) return launch_fwd_rows<T, VB, U, 32>(a, s);
-  if (chunks <= 64 * U) return launch_fwd_rows<T, VB, 2 * U, 32>(a, s);
-  if (chunks <= 128 * U) return launch_fwd_rows<T, VB, U, 128>(a, s);
-  if (chunks <= 256 * U) return launch_fwd_rows<T, VB, 2 * U, 128>(a, s);
-  if (chunks <= 512 * U) return launch_fwd_rows<T, VB, 2 * U, 256>(a, s);
-  if (chunks <= 1024 * U) return launch_fwd_rows<T, VB, 2 * U, 512>(a, s);
-  if (chunks <= 2048 * U) return launch_fwd_rows<T, VB, 2 * U, 1024>(a, s);
-  return 0;
+  if (chunks <= 32 * U) return launch_fwd_rows<T, VB, U, 32>(a, s, grid);
+  if (chunks <= 64 * U) return launch_fwd_rows<T, VB, 2 * U, 32>(a, s, grid);
+  if (chunks <= 128 * U) return launch_fwd_rows<T, VB, U, 128>(a, s, grid);
+  if (chunks <= 256 * U) return launch_fwd_rows<T, VB, 2 * U, 128>(a, s, grid);
+  if (chunks <= 512 * U) return launch_fwd_rows<T, VB, 2 * U, 256>(a, s, grid);
+  if (chunks <= 1024 * U) return launch_fwd_rows<T, VB, 2 * U, 512>(a, s, grid);
+  if (chunks <= 2048 * U) return launch_fwd_rows<T, VB, 2 * U, 1024>(a, s, grid);
+  grid = 0;
+  return cudaSuccess;
 }
 // Backward: the same.
 template <typename T, int VB, int U>
-int bwd_by_width(const NormArgs& a, cudaStream_t s) {
+cudaError_t bwd_by_width(const NormArgs& a, cudaStream_t s, int& grid) {
   const int chunks = (a.d + VB - 1) / VB;
-  if (chunks <= 32 * U) return launch_bwd_rows<T, VB, U, 32>(a, s);
-  if (chunks <= 64 * U) return launch_bwd_rows<T, VB, 2 * U, 32>(a, s);
-  if (chunks <= 128 * U) return launch_bwd_rows<T, VB, U, 128>(a, s);
-  if (chunks <= 256 * U) return launch_bwd_rows<T, VB, 2 * U, 128>(a, s);
-  if (chunks <= 512 * U) return launch_bwd_rows<T, VB, 2 * U, 256>(a, s);
-  if (chunks <= 1024 * U) return launch_bwd_rows<T, VB, 2 * U, 512>(a, s);
-  if (chunks <= 2048 * U) return launch_bwd_rows<T, VB, 4 * U, 512>(a, s);
-  return 0;
+  if (chunks <= 32 * U) return launch_bwd_rows<T, VB, U, 32>(a, s, grid);
+  if (chunks <= 64 * U) return launch_bwd_rows<T, VB, 2 * U, 32>(a, s, grid);
+  if (chunks <= 128 * U) return launch_bwd_rows<T, VB, U, 128>(a, s, grid);
+  if (chunks <= 256 * U) return launch_bwd_rows<T, VB, 2 * U, 128>(a, s, grid);
+  if (chunks <= 512 * U) return launch_bwd_rows<T, VB, 2 * U, 256>(a, s, grid);
+  if (chunks <= 1024 * U) return launch_bwd_rows<T, VB, 2 * U, 512>(a, s, grid);
+  if (chunks <= 2048 * U) return launch_bwd_rows<T, VB, 4 * U, 512>(a, s, grid);
+  grid = 0;
+  return cudaSuccess;
 }
 
+// `grid`: the blocks launched, or the rows of partial weight gradients that they leave
 template <typename T>
-int launch_norm(const NormArgs& a, bool bwd, bool vec, cudaStream_t s) {
+cudaError_t launch_norm(const NormArgs& a, bool bwd, bool vec, cudaStream_t s, int& grid) {
   constexpr int V = 16 / sizeof(T);
-  const int grid = bwd ? (vec ? bwd_by_width<T, V, 1>(a, s) : bwd_by_width<T, 1, 4>(a, s))
-                       : (vec ? fwd_by_width<T, V, 1>(a, s) : fwd_by_width<T, 1, 4>(a, s));
-  if (grid > 0) return grid;
+  const cudaError_t err = bwd ? (vec ? bwd_by_width<T, V, 1>(a, s, grid) : bwd_by_width<T, 1, 4>(a, s, grid))
+                              : (vec ? fwd_by_width<T, V, 1>(a, s, grid) : fwd_by_width<T, 1, 4>(a, s, grid));
+  if (err != cudaSuccess || grid > 0) return err;
   const int wide = static_cast<int>(std::min<long long>(a.T, 1 << 20));
   if (!bwd) {
     norm_fwd_wide_kernel<T><<<wide, WIDE_THREADS, 0, s>>>(a);
-    return wide;
+    return cudaGetLastError();
   }
   // the weight gradients first: dx may lie over x or dy
-  const int parts = std::min(a.T, BWD_MAX_BLOCKS);
+  grid = std::min(a.T, BWD_MAX_BLOCKS);
   if (a.part != nullptr)
-    norm_wgrad_wide_kernel<T><<<dim3((a.d + 255) / 256, parts), 256, 0, s>>>(a);
+    norm_wgrad_wide_kernel<T><<<dim3((a.d + 255) / 256, grid), 256, 0, s>>>(a);
   norm_bwd_wide_kernel<T><<<wide, WIDE_THREADS, 0, s>>>(a);
-  return parts;
+  return cudaGetLastError();
 }
 
 bool dtype_ok(int t) { return t == MOE_DTYPE_BF16 || t == MOE_DTYPE_F32; }
@@ -698,9 +697,10 @@ moe_status_t moe_layer_norm_fwd(const void* x, int dtype, long long ldx, const v
   const bool vec = d % v == 0 && ldx % v == 0 && ldy % v == 0 && aligned16(x) && aligned16(y) && aligned16(gamma) &&
                    aligned16(beta);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == MOE_DTYPE_BF16) launch_norm<bf16>(a, false, vec, s);
-  else launch_norm<float>(a, false, vec, s);
-  return launched();
+  int blocks = 0;
+  const cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_norm<bf16>(a, false, vec, s, blocks)
+                                                  : launch_norm<float>(a, false, vec, s, blocks);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
 moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, long long ldx, int dtype,
@@ -744,8 +744,9 @@ moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, l
     const int v = 16 / es;
     const bool vec = d % v == 0 && ldx % v == 0 && lddy % v == 0 && lddx % v == 0 && aligned16(ws) && aligned16(x) && aligned16(dy) &&
                      aligned16(dx) && aligned16(gamma);
-    blocks = dtype == MOE_DTYPE_BF16 ? launch_norm<bf16>(a, true, vec, s) : launch_norm<float>(a, true, vec, s);
-    if ((st = launched()) != MOE_OK) return st;
+    const cudaError_t err = dtype == MOE_DTYPE_BF16 ? launch_norm<bf16>(a, true, vec, s, blocks)
+                                                    : launch_norm<float>(a, true, vec, s, blocks);
+    if (err != cudaSuccess) return cuda_fail(err);
   }
   if (!wgrad) return MOE_OK;
   const cudaError_t err = launch_dependent(norm_partials_kernel, (2 * d + 31) / 32, 1024, 0, s,
