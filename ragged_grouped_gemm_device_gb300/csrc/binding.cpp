@@ -191,7 +191,20 @@ int as_stream(PyObject* o, moe_stream_t* s) {
   return *s == nullptr && PyErr_Occurred() ? -1 : 0;
 }
 
-PyObject* finish(const char* fn, moe_status_t st) {
+// The interpreter lock given up for a scope, which an exception may leave too
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
+// Calls the library without the interpreter lock, like ctypes: a launch waits while the stream's queue is full
+// (and in the debug build for the stream), and other threads have to run meanwhile.
+template <typename Call>
+PyObject* finish(const char* fn, Call call) {
+  const moe_status_t st = [&] {
+    Unlocked unlocked;
+    return call();
+  }();
   if (st == MOE_OK) Py_RETURN_NONE;
   PyObject* r = PyObject_CallFunction(g_raise, "si", fn, (int)st);
   Py_XDECREF(r);
@@ -239,7 +252,9 @@ PyObject* layer_norm_fwd(ARGS) {
       plain(a[2], &beta) < 0 || weight_type(a + 1, 2, d, &wt) < 0 || typed(a[7], at::kFloat, T, "mean", &mean) < 0 ||
       typed(a[8], at::kFloat, T, "rstd", &rstd) < 0 || as_stream(a[9], &s) < 0)
     return nullptr;
-  return finish("moe_layer_norm_fwd", p_moe_layer_norm_fwd(x, dt, ldx, gamma, beta, wt, T, d, (float)eps, y, ldy, mean, rstd, s));
+  return finish("moe_layer_norm_fwd", [&] {
+    return p_moe_layer_norm_fwd(x, dt, ldx, gamma, beta, wt, T, d, (float)eps, y, ldy, mean, rstd, s);
+  });
 }
 
 PyObject* layer_norm_bwd(ARGS) {
@@ -257,8 +272,9 @@ PyObject* layer_norm_bwd(ARGS) {
       typed(a[8], at::kFloat, d, "dgamma", &dgamma) < 0 || typed(a[9], at::kFloat, d, "dbeta", &dbeta) < 0 ||
       plain(a[10], &ws) < 0 || bytes_of(a[10], &n) < 0 || as_stream(a[11], &s) < 0)
     return nullptr;
-  return finish("moe_layer_norm_bwd", p_moe_layer_norm_bwd(dy, lddy, x, ldx, dt, gamma, wt, mean, rstd, T, d, dx, lddx, dgamma,
-                                                           dbeta, ws, n, s));
+  return finish("moe_layer_norm_bwd", [&] {
+    return p_moe_layer_norm_bwd(dy, lddy, x, ldx, dt, gamma, wt, mean, rstd, T, d, dx, lddx, dgamma, dbeta, ws, n, s);
+  });
 }
 
 PyObject* gate_fwd(ARGS) {
@@ -281,7 +297,9 @@ PyObject* gate_fwd(ARGS) {
       typed(a[11], at::kFloat, E, "prob_sum", &ps) < 0 || typed(a[12], at::kFloat, 2, "loss", &loss) < 0 || plain(a[13], &ws) < 0 ||
       bytes_of(a[13], &n) < 0 || as_stream(a[14], &s) < 0)
     return nullptr;
-  return finish("moe_gate_fwd", p_moe_gate_fwd(x, dt, ld, mask, T, k, E, flags, ids, w, lse, counts, nv, ps, loss, ws, n, s));
+  return finish("moe_gate_fwd", [&] {
+    return p_moe_gate_fwd(x, dt, ld, mask, T, k, E, flags, ids, w, lse, counts, nv, ps, loss, ws, n, s);
+  });
 }
 
 PyObject* gate_bwd(ARGS) {
@@ -300,7 +318,9 @@ PyObject* gate_bwd(ARGS) {
       typed(a[5], at::kInt, 1, "n_valid", &nv) < 0 || typed(a[6], at::kFloat, n_slots, "d_weights", &dw) < 0 ||
       typed(a[7], at::kFloat, 2, "d_loss", &dl) < 0 || as_stream(a[13], &s) < 0)
     return nullptr;
-  return finish("moe_gate_bwd", p_moe_gate_bwd(x, dt, ld, lse, ids, w, counts, nv, dw, dl, T, k, E, flags, o, ldd, s));
+  return finish("moe_gate_bwd", [&] {
+    return p_moe_gate_bwd(x, dt, ld, lse, ids, w, counts, nv, dw, dl, T, k, E, flags, o, ldd, s);
+  });
 }
 
 PyObject* mx4_quantize_rows(ARGS) {
@@ -314,7 +334,9 @@ PyObject* mx4_quantize_rows(ARGS) {
       raw(a[5], n / 2, "q", &q) < 0 || raw(a[6], scale_bytes(cap, E, K), "sf", &sf) < 0 || status(a[7], &st) < 0 ||
       as_stream(a[8], &s) < 0)
     return nullptr;
-  return finish("moe_mx4_quantize_rows", p_moe_mx4_quantize_rows(x, off, E, cap, K, q, sf, st, s));
+  return finish("moe_mx4_quantize_rows", [&] {
+    return p_moe_mx4_quantize_rows(x, off, E, cap, K, q, sf, st, s);
+  });
 }
 
 PyObject* mx4_dequantize_rows(ARGS) {
@@ -328,7 +350,9 @@ PyObject* mx4_dequantize_rows(ARGS) {
       typed(a[2], at::kInt, E, "offsets", &off) < 0 || typed(a[6], at::kBFloat16, n, "x", &x) < 0 || status(a[7], &st) < 0 ||
       as_stream(a[8], &s) < 0)
     return nullptr;
-  return finish("moe_mx4_dequantize_rows", p_moe_mx4_dequantize_rows(q, sf, off, E, cap, K, x, st, s));
+  return finish("moe_mx4_dequantize_rows", [&] {
+    return p_moe_mx4_dequantize_rows(q, sf, off, E, cap, K, x, st, s);
+  });
 }
 
 PyObject* permute_mxfp4(ARGS) {
@@ -343,7 +367,9 @@ PyObject* permute_mxfp4(ARGS) {
       typed(a[2], at::kInt, E, "offsets", &off) < 0 || raw(a[7], code_bytes, "q", &q) < 0 ||
       raw(a[8], scale_bytes(n, E, d), "sf", &sf) < 0 || status(a[9], &st) < 0 || as_stream(a[10], &s) < 0)
     return nullptr;
-  return finish("moe_permute_mxfp4", p_moe_permute_mxfp4(x, inv, off, T, k, E, d, q, sf, st, s));
+  return finish("moe_permute_mxfp4", [&] {
+    return p_moe_permute_mxfp4(x, inv, off, T, k, E, d, q, sf, st, s);
+  });
 }
 
 PyObject* grouped_swiglu_fwd_mxfp4(ARGS) {
@@ -361,8 +387,9 @@ PyObject* grouped_swiglu_fwd_mxfp4(ARGS) {
       typed(a[8], at::kBFloat16, items, "y", &y) < 0 || plain(a[9], &ws) < 0 || bytes_of(a[9], &n) < 0 ||
       status(a[10], &st) < 0 || as_stream(a[11], &s) < 0)
     return nullptr;
-  return finish("moe_grouped_swiglu_fwd_mxfp4",
-                p_moe_grouped_swiglu_fwd_mxfp4(xq, xsf, off, E, cap, d, h, mxw, y, ws, n, st, s));
+  return finish("moe_grouped_swiglu_fwd_mxfp4", [&] {
+    return p_moe_grouped_swiglu_fwd_mxfp4(xq, xsf, off, E, cap, d, h, mxw, y, ws, n, st, s);
+  });
 }
 
 PyObject* unpermute_combine(ARGS) {
@@ -373,7 +400,9 @@ PyObject* unpermute_combine(ARGS) {
   if (plain(a[0], &y) < 0 || plain(a[1], &inv) < 0 || plain(a[2], &w) < 0 || as_int(a[3], &T) < 0 || as_int(a[4], &k) < 0 ||
       as_int(a[5], &d) < 0 || plain(a[6], &out) < 0 || as_stream(a[7], &s) < 0)
     return nullptr;
-  return finish("moe_unpermute_combine", p_moe_unpermute_combine(y, inv, w, T, k, d, out, s));
+  return finish("moe_unpermute_combine", [&] {
+    return p_moe_unpermute_combine(y, inv, w, T, k, d, out, s);
+  });
 }
 
 PyObject* route_offsets(ARGS) {
@@ -386,7 +415,9 @@ PyObject* route_offsets(ARGS) {
       plain(a[5], &off) < 0 || plain(a[6], &src) < 0 || plain(a[7], &inv) < 0 || plain(a[8], &ws) < 0 ||
       bytes_of(a[8], &n) < 0 || as_stream(a[9], &s) < 0)
     return nullptr;
-  return finish("moe_route_offsets", p_moe_route_offsets(ids, T, k, E, counts, off, src, inv, ws, n, s));
+  return finish("moe_route_offsets", [&] {
+    return p_moe_route_offsets(ids, T, k, E, counts, off, src, inv, ws, n, s);
+  });
 }
 
 // ------------------------------------------------------------------ module
