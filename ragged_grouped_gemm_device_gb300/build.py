@@ -7,7 +7,8 @@ ABI): device-side bounds checks at the data-dependent global accesses and a wait
 at the end of every entry point, read back with moe_debug_report().
 
 build_binding() compiles csrc/binding.cpp, the CPython extension that marshals the calls of a decode
-step, next to this file; without a C++ compiler or Python's headers the ctypes binding does it."""
+step, next to this file; where it cannot be built (no C++ compiler, no headers of Python or torch, a failing
+compile) the ctypes binding does it."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -16,6 +17,7 @@ import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -88,15 +90,19 @@ BINDING = os.path.join(PKG, "_binding.so")
 
 
 def build_binding(force: bool = False):
-    """Path of the CPython extension, or None where it cannot be built (no compiler or headers)."""
+    """Path of the CPython extension, or None where it cannot be built: without torch, a compiler or headers, or
+    when the compile fails, which is printed. An extension of older sources does not stay behind then."""
     src = os.path.join(CSRC, "binding.cpp")
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None or spec.origin is None:
+        return None
+    torch = os.path.dirname(spec.origin)
     deps = [src, os.path.join(ROOT, "include", "moe_gg.h"), os.path.abspath(__file__), os.path.join(torch, "version.py")]
     if not force and os.path.exists(BINDING) and all(os.path.getmtime(p) <= os.path.getmtime(BINDING) for p in deps):
         return BINDING
     cc, inc = shutil.which("g++") or shutil.which("c++"), sysconfig.get_paths()["include"]
     if cc is None or not os.path.exists(os.path.join(inc, "Python.h")):
-        return None
+        return _without_binding()
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     lib = os.path.join(torch, "lib")
     tmp = BINDING + ".tmp"
@@ -105,12 +111,17 @@ def build_binding(force: bool = False):
            "-Wl,-rpath," + lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"{cc} failed for {src}:\n{r.stdout}\n{r.stderr}")
+        print(f"{cc} failed for {src}, the ctypes binding is used:\n{r.stdout}\n{r.stderr}", file=sys.stderr)
+        return _without_binding()
     os.replace(tmp, BINDING)
     return BINDING
 
 
+def _without_binding():
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
+
+
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True, debug="--debug" in sys.argv))
     print(build_binding(force="--force" in sys.argv))
