@@ -1,10 +1,11 @@
-"""Sizes at which the kernels of layer norm and the MXFP4 experts go round their loops: more tiles than SMs, more row
-pieces than warps, more rows than the ring holds and than one load of row statistics covers. The references and
+"""Sizes at which the kernels of layer norm, the gate and the MXFP4 experts go round their loops: more tiles than SMs,
+more row pieces or tokens than warps, more rows than the ring holds and than one load of row statistics covers. The references and
 tolerances are those of the smaller cases."""
 import numpy as np
 import pytest
 import torch
 
+import test_gpu_gate as G
 import test_gpu_layer_norm as N
 import test_gpu_mx4 as M
 from oracle import mx4_oracle as Q
@@ -43,8 +44,8 @@ def test_rows_and_back_of_more_pieces_than_warps(lib, K):
     back = torch.full_like(x, 5.0)
     _lib.moe_mx4_dequantize_rows(q, sf, off, E, cap, K, back)
     torch.cuda.synchronize()
-    G, r = M._tiles(offsets)
-    got_s, pad = M._scales(sf.cpu().numpy(), G, r, K)
+    tile, r = M._tiles(offsets)
+    got_s, pad = M._scales(sf.cpu().numpy(), tile, r, K)
     got_c, b = M._unpack(q.cpu().numpy()[:rows], K), M._host(back)
     assert (pad == 127).all() and (b[rows:] == 5.0).all() and (q[rows:] == 0x77).all()
     for i in range(0, rows, 2000):
@@ -87,3 +88,13 @@ def test_weights_of_more_pieces_than_threads(lib):
 def test_layer_norm_of_many_rows_a_block(lib, dtype, T, d):
     x, dy, gamma, beta = N._inputs(T, d, dtype)
     N._check(x, dy, gamma, beta, N._run(x, dy, gamma, beta))
+
+
+# a lane group has several tokens, in every layout of lanes and lists of both directions; E = 60 and 250 are read
+# one element at a time
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,E,k,renorm", [(40003, 64, 4, True), (40003, 60, 3, False), (30001, 128, 8, True), (25001, 256, 8, False),
+                                          (10007, 250, 6, True), (12001, 512, 4, True), (6007, 1000, 5, False), (6007, 1001, 5, True)])
+def test_gate_of_many_tokens_a_lane_group(lib, T, E, k, renorm, dtype):
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(E)).cuda() > 0.1
+    G.Gate(G._logits(T, E, dtype), mask, k, renorm).run().check()
