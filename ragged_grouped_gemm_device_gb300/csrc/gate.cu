@@ -646,7 +646,6 @@ template <typename T, bool VEC>
 moe_status_t by_width_fwd(const GateArgs& a, Width w, int blocks, cudaStream_t s) {
   if constexpr (VEC) {
     if (w.lists == 2 && w.lanes == 8) return launch_fwd<T, 2, 8, VEC>(a, blocks, s);
-    if (w.lists == 2 && w.lanes == 16) return launch_fwd<T, 2, 16, VEC>(a, blocks, s);
     if (w.lists == 4 && w.lanes == 8) return launch_fwd<T, 4, 8, VEC>(a, blocks, s);
     if (w.lists == 4 && w.lanes == 16) return launch_fwd<T, 4, 16, VEC>(a, blocks, s);
   }
