@@ -5,8 +5,10 @@
 
 with the balance and z losses of the gate, and the gradient of all of it. The experts are an
 ExpertLayer (BF16: training and serving) or an Mxfp4ExpertLayer (4-bit: serving). The router's
-projection and the residual additions are plain torch operations in fp32; every other step is a
-library kernel. Buffers are allocated once per shape and reused, so what forward() and
+projection and its gradients are torch products in fp32 (TF32 where torch is set to it), the residual
+additions torch additions; every other step is a library kernel. Rows are bf16 between the steps: out is
+the rounded sum of x and the rounded expert rows; in the backward the experts' gradient of n is rounded,
+then its sum with the router's, then the layer norm's dx, then dx + dout. Buffers are allocated once per shape and reused, so what forward() and
 backward() return is overwritten by the next call. The calls record no autograd history (what they return
 requires no gradient); the gradients are backward()'s.
 """

@@ -37,7 +37,7 @@ __device__ __forceinline__ void record_status(int32_t* status, int bits) {
 // Programmatic dependent launch: a kernel launched by launch_dependent() may be set up while the one
 // ahead of it in the stream ends, instead of after it: 2 to 3 us less for each kernel of a queue (gate
 // of 4096 x 128 with statistics and gradient, three kernels, 12.1 us against 16.7; layer norm of 16384 x
-// 2048 with its gradient 63.7 against 68.7). It has to call grid_wait() before it touches anything that
+// 2048 with its gradient 63.7 against 68.7, both before a later step made its backward 5 us faster). It has to call grid_wait() before it touches anything that
 // a kernel ahead may write or still read. grid_release() in the kernel ahead lets it start before
 // that one's blocks have ended, which pays where its prologue is long (the down product); elsewhere it
 // costs more than it gains: a full grid that is placed while others still run ends up two blocks to an

@@ -14,9 +14,11 @@
 // experts a lane, its logits in registers: each logit is read once by the forward and once by
 // the backward, 16 bytes at a time where the rows allow it. Each lane sorts its eight (logit,
 // expert) keys with a 19-comparator network; a round of the top_k is then one maximum over the
-// lanes' heads and a step in the winner's list. Both kernels are bound by instruction issue, not
-// by memory, so the count per token is what the layout minimises (rescanning a lane's values in
-// each round instead of sorting once took four times as long). The sorted lists lie in shared
+// lanes' heads and a step in the winner's list. Neither kernel is bound by memory: of many tokens the
+// forward keeps 58% of the issue slots busy and 14% of the memory, and waits for the loads of a token
+// between one token's work and the next's, on the 16 warps that its registers leave an SM. So the
+// instructions of a token are what the layout minimises (rescanning a lane's values in each round
+// instead of sorting once took four times as long). The sorted lists lie in shared
 // memory, where taking a list's next head is one load instead of a shift of eight registers.
 // Measured: 131072 tokens x 256 experts, top 8 of bf16 logits, 51 us without statistics (67 MB of
 // logits, 1.3 TB/s) and 59 with them; its gradient 31.5 us (4.3 TB/s of logits read and gradient
@@ -42,8 +44,9 @@ constexpr int MAX_TOPK = 32;
 // Blocks at most, and so rows of partial sums: four for each of the 152 SMs. A constant, because
 // the size of the workspace is host arithmetic.
 constexpr int MAX_BLOCKS = 608;
-// Blocks of the backward at most, five for each SM, which is what fits (131072 x 256 bf16: 31.5 us;
-// twice as many 32.2, four times 35.3; more blocks on an SM with fewer registers 33 to 46).
+// Blocks of the backward at most, five for each SM: what fits of one list on 32 lanes (131072 x 256 bf16:
+// 31.5 us; twice as many 32.2, four times 35.3; more blocks on an SM with fewer registers 33 to 46). Of the
+// other layouts fewer fit (two to four, by their registers) and the rest run after them.
 constexpr int BWD_BLOCKS = 760;
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -569,6 +572,7 @@ __global__ void __launch_bounds__(THREADS) gate_bwd_kernel(GateBwdArgs a) {
     for (int l = 0; l < NL; ++l)
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        // lse is rounded to fp32, so p is off by its last place as well: 6e-5 of p where |lse| is 1e3
         p[l][j] = part ? exp_f(p[l][j] - lse) : 0.f;
         dot = fmaf(p[l][j], c[l][j], dot);
       }
