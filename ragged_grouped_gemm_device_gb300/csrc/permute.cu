@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(THREADS) zero_dropped_rows_kernel(const int32_
 // out[t] = sum_j w[t,j] * y[inv[t,j]] over slots with inv >= 0, fp32 in slot order, one bf16
 // rounding (gather + reduction in place of the scatter-add, "grouped_mm" agent doc). SPLIT: `split`
 // warps a token, each `per` of its vectors; else one warp a token, without the division that finds
-// token and part (131072 tokens of 512 columns, top_k = 1: 104 us with it).
+// token and part (131072 tokens of 512 columns, top_k = 1: 86.8 us, 104 with it).
 template <bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 4) combine_kernel(const uint4* y,
                                                              const int32_t* inv,
