@@ -33,7 +33,8 @@ class MoEBlock:
         E, d = w_router.shape
         assert w_router.dtype == torch.float32 and (E, d) == (experts.E, experts.d)
         assert gamma.shape == (d,) and beta.shape == (d,) and 1 <= top_k <= min(E, 32)
-        self.gamma, self.beta, self.w_router = gamma.contiguous(), beta.contiguous(), w_router.contiguous()
+        # as given, views too: a dense copy made here would not follow an optimizer's updates
+        self.gamma, self.beta, self.w_router = gamma, beta, w_router
         self.experts, self.E, self.d, self.k, self.eps = experts, E, d, top_k, eps
         self.flags = _lib.GATE_RENORM if renorm else 0
         self.device = w_router.device
@@ -68,7 +69,7 @@ class MoEBlock:
         self._buffers(T)
         self.x = x  # read again by backward(), like gamma and w_router
         self._read = [(t, _version(t)) for t in (x, self.gamma, self.w_router)]
-        _lib.moe_layer_norm_fwd(x, self.gamma, self.beta, T, self.d, self.eps, self.normed, self.mean, self.rstd)
+        _lib.moe_layer_norm_fwd(x, _dense(self.gamma), _dense(self.beta), T, self.d, self.eps, self.normed, self.mean, self.rstd)
         torch.mm(self.normed.float(), self.w_router.t(), out=self.logits)
         _lib.moe_gate_fwd(self.logits, token_mask, T, self.k, self.E, self.flags, self.ids, self.weights, self.lse,
                           self.counts, self.n_valid, self.prob_sum, self.loss, self.gate_ws)
@@ -91,6 +92,6 @@ class MoEBlock:
                           self.k, self.E, self.flags, self.dlogits)
         dw_router = torch.mm(self.dlogits.t(), self.normed.float())
         self.dnormed.copy_(torch.addmm(dn.float(), self.dlogits, self.w_router))
-        _lib.moe_layer_norm_bwd(self.dnormed, self.x, self.gamma, self.mean, self.rstd, T, self.d, self.dx, self.dgamma,
+        _lib.moe_layer_norm_bwd(self.dnormed, self.x, _dense(self.gamma), self.mean, self.rstd, T, self.d, self.dx, self.dgamma,
                                 self.dbeta, self.norm_ws)
         return dict(dx=self.dx + dout, gamma=self.dgamma, beta=self.dbeta, w_router=dw_router, w_ug=dw_ug, w_down=dw_down)

@@ -71,3 +71,22 @@ def test_refusals(lib):
         with pytest.raises(ValueError):
             block.forward(x, bad)
     block.forward(x, mask.byte())
+
+
+def test_views_of_weights_follow_their_updates(lib):
+    """Weights given as strided views: an update of what they view is seen by the next call."""
+    block, x, dout = _block()
+    stored = [torch.stack([block.gamma, block.beta], 1), block.w_router.t().contiguous()]  # [d, 2], [d, E]
+    views = (stored[0][:, 0], stored[0][:, 1], stored[1].t())
+    viewing = MoEBlock(*views, block.experts, k)
+    viewing.forward(x)
+    viewing.backward(dout)
+    for t in stored:
+        t.mul_(0.75).add_(0.01)
+    fresh = MoEBlock(*(v.contiguous() for v in views), block.experts, k)
+    want, grads = fresh.forward(x).clone(), {n: g.clone() for n, g in fresh.backward(dout).items()}
+    assert not torch.equal(want, block.forward(x))
+    got, now = viewing.forward(x), viewing.backward(dout)
+    # the router's product may sum in another order for another layout: fp32 sums of d terms, bf16 rows
+    close = lambda a, b: float((a.double() - b.double()).norm()) <= 1e-3 * float(b.double().norm())
+    assert close(got, want) and all(close(now[n], grads[n]) for n in grads)
