@@ -92,7 +92,11 @@ typedef enum {
   MOE_OP_MX4_FWD = 11,     /* moe_grouped_swiglu_fwd_mxfp4 */
   MOE_OP_MX4_ROW_SCALES = 12, /* moe_mx4_quantize_rows: scale bytes for T*top_k rows of K = d */
   MOE_OP_GATE = 13,        /* moe_gate_fwd with its statistics (d and h ignored) */
-  MOE_OP_LAYER_NORM_BWD = 14 /* moe_layer_norm_bwd: T rows of width d (E = top_k = 1, h ignored) */
+  MOE_OP_LAYER_NORM_BWD = 14, /* moe_layer_norm_bwd: T rows of width d (E = top_k = 1, h ignored) */
+  MOE_OP_RESIDUAL_NORM_BWD = 15, /* moe_residual_norm_bwd: T rows of width d (E = top_k = 1, h ignored) */
+  MOE_OP_GRAD_NORM = 16,   /* moe_grad_norm (the sizes are ignored) */
+  MOE_OP_W4_WEIGHTS = 17,  /* moe_w4_pack: E matrices (up to 2048) of h rows of d elements, groups of capacity_C */
+  MOE_OP_W4_DECODE = 18    /* moe_w4_swiglu_decode */
 } moe_op_t;
 
 /* Bytes of caller workspace that `op` needs for these sizes (0 when none). Pure host
@@ -548,6 +552,146 @@ moe_status_t moe_layer_norm_bwd(const void* dy, long long lddy, const void* x, l
                                 const void* gamma, int w_dtype, const float* mean, const float* rstd, int T, int d,
                                 void* dx, long long lddx, float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
                                 moe_stream_t stream);
+
+/*
+ * moe_residual_norm_fwd, moe_residual_norm_bwd -- what stands between two blocks of a model, in one pass: the
+ * norm behind a block, its gate and scale, the residual addition, and the norm in front of the next block.
+ *   z = post(y);  r = res_scale x + branch_scale gate z;  n = pre(r as stored)
+ * post and pre are each MOE_NORM_NONE (the rows as they are), MOE_NORM_LAYER, (v - mean) rstd gamma + beta, or
+ * MOE_NORM_RMS, v rstd gamma with rstd = 1 / sqrt(sum v^2 / d + eps). All arithmetic is fp32; r and n are
+ * rounded once each, n from the rounded r: what a norm call on the stored r computes.
+ *  x, r    [T, d] of `x_dtype` (the residual stream);  y, n  [T, d] of `y_dtype`. Rows are `ld` elements
+ *          apart, of outputs at least d; a row pitch of 0 reads one row for all (inputs).
+ *          Types: both bf16, both fp32, or an fp32 stream with bf16 branches.
+ *  y       nullable: no branch, r = res_scale x (post is then MOE_NORM_NONE, gate NULL).
+ *  post_gamma, post_beta, gate, pre_gamma, pre_beta  nullable [d] of `w_dtype` (ones, zeros, ones, ...); the
+ *          betas go with MOE_NORM_LAYER only, the gammas with a norm.
+ *  r       nullable: not stored (n is still the norm of r rounded to x_dtype).
+ *  n       NULL with pre = MOE_NORM_NONE, required otherwise.
+ *  stats   nullable [4, T] fp32 out: mean and rstd of y, mean and rstd of r (mean 0 for RMS; 0 and 1 for
+ *          MOE_NORM_NONE); the backward needs them.
+ * Backward: dn (gradient of n; NULL with pre = MOE_NORM_NONE), dr (gradient of r from its other readers;
+ * nullable: zeros), and r and y as they were stored:
+ *   D = dr + pre'(dn);  dx = res_scale D;  dz = branch_scale gate D;  dy = post'(dz)
+ *   d_post_gamma = sum_t dz yhat;  d_post_beta = sum_t dz;  d_gate = sum_t branch_scale D z
+ *   d_pre_gamma = sum_t dn rhat;   d_pre_beta = sum_t dn
+ *  dn, y, dy of `y_dtype`; dr, r, dx of `x_dtype`. r may be NULL with pre = MOE_NORM_NONE. y and dy are NULL
+ *  together (no branch). dx nullable. The weight gradients are fp32 [d], each nullable, summed in a fixed
+ *  order (zeros for T = 0); one whose weight was NULL may be asked for all the same, but d_pre_* go with a
+ *  pre norm and d_post_*, d_gate with a branch (d_post_* with a post norm).
+ *  ws      moe_workspace_bytes(MOE_OP_RESIDUAL_NORM_BWD, T, 1, 1, d, 0, 0) bytes.
+ * An output may be an input of its type (the same base and pitch: r over x, n over y, dx over dr, dy over dn
+ * or y, ...); other overlaps are not allowed. Limits: 1 <= d <= 2^20; pointers aligned to their element size.
+ */
+typedef enum {
+  MOE_NORM_NONE = 0,
+  MOE_NORM_LAYER = 1,
+  MOE_NORM_RMS = 2
+} moe_norm_t;
+moe_status_t moe_residual_norm_fwd(const void* x, int x_dtype, long long ldx, const void* y, int y_dtype, long long ldy,
+                                   int post, const void* post_gamma, const void* post_beta, const void* gate, int pre,
+                                   const void* pre_gamma, const void* pre_beta, int w_dtype, int T, int d, float eps,
+                                   float res_scale, float branch_scale, void* r, long long ldr, void* n, long long ldn,
+                                   float* stats, moe_stream_t stream);
+moe_status_t moe_residual_norm_bwd(const void* dn, long long lddn, const void* dr, long long lddr, const void* r,
+                                   long long ldr, int x_dtype, const void* y, long long ldy, int y_dtype, int post,
+                                   const void* post_gamma, const void* post_beta, const void* gate, int pre,
+                                   const void* pre_gamma, int w_dtype, const float* stats, int T, int d, float res_scale,
+                                   float branch_scale, void* dx, long long lddx, void* dy, long long lddy,
+                                   float* d_post_gamma, float* d_post_beta, float* d_gate, float* d_pre_gamma,
+                                   float* d_pre_beta, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_grad_norm, moe_adamw_step -- the optimizer over many tensors at once.
+ *   g' = c g;  m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * with c = *grad_scale (1 when NULL) and t = steps[0] + 1.
+ *  tensors  `count` descriptors in HOST memory (read before the call returns); the pointers in them are device
+ *           pointers. n = 0 is allowed.
+ *    p      fp32, or bf16: then p is rounded stochastically (below), so that steps smaller than half a unit in
+ *           its last place are not lost.
+ *    copy   nullable bf16 [n] out: p rounded to nearest (p fp32: a master weight with the bf16 weight that the
+ *           products read).
+ *    g      bf16 or fp32.
+ *    m, v   state_bits 32: fp32. state_bits 8: E4M3 bytes of m and of sqrt(v), with m_scale and v_scale, one
+ *           byte s + 127 for each 32 elements: value = element * 2^s, s the smallest (not below -127) with
+ *           max |value| <= 448 * 2^s; the elements are rounded stochastically, and a v that is not 0 not to
+ *           0 (a step divides by it). Zero bytes are zeros. A block with a NaN or an infinity gets the scale 0xFF
+ *           and reads as NaN.
+ *  steps    [2] int32 on the device: steps done, and a counter that the call leaves at 0 (both start at 0). The
+ *           call adds 1 to steps[0].
+ *  lr_scale nullable fp32 on the device: the learning rate is lr * *lr_scale (a schedule under a captured graph).
+ *  A grad_scale that is NaN (of a norm that is not finite) skips the step: nothing is written.
+ * Stochastic rounding: up where the fraction of the last place and u in [0, 1) reach 1, u = 16 bits / 2^16 of
+ *   mix(key + i 0x9E3779B9 + (i >> 32) 0x85EBCA6B),  key = mix(seed ^ mix(0x9E3779B9 t + j))
+ * for element i of tensor j of the call, mod 2^32, mix the finalizer of MurmurHash3: the low 16 bits for m, the
+ * high for v, the middle for p. Results are deterministic. One tensor may not be updated by two calls at a time.
+ * moe_grad_norm: norm[0] = sqrt(sum of all g^2), norm[1] = min(1, max_norm / norm[0]) (NaN where norm[0] is not
+ * finite): a grad_scale that clips. Summed in a fixed order, in fp64 over pieces of 4096 summed in fp32; reads
+ * only g, g_dtype and n of the descriptors. ws: moe_workspace_bytes(MOE_OP_GRAD_NORM, 0, 1, 1, 0, 0, 0) bytes.
+ * Pointers are aligned to their element size. Elements in all: below 2^43.
+ */
+typedef struct {
+  void* p;
+  void* copy;
+  const void* g;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  long long n;
+  float weight_decay;
+  int p_dtype;
+  int g_dtype;
+  int reserved;  /* 0 */
+} moe_adamw_tensor_t;
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float max_norm, float* norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream);
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int state_bits, double lr, double beta1,
+                            double beta2, double eps, uint32_t seed, int32_t* steps, const float* lr_scale,
+                            const float* grad_scale, moe_stream_t stream);
+
+/*
+ * 4-bit integer weights with group scales (serving of few tokens): w = scale (code - zero), codes and zeros 0 to
+ * 15, one bf16 scale and one zero point for each `group` (32, 64 or 128) consecutive elements of a row along the
+ * contraction. Activations stay bf16; products of codes and activations are exact and summed in fp32, a group's
+ * sum is scaled in fp32.
+ *
+ * moe_w4_quantize_rows -- rows of a bf16 matrix w [rows, K] into codes [rows, ceil(K / 2)] (element 2i in the low
+ *   half of byte i; a last half byte is 0), scales and zeros [rows, ceil(K / group)]: with lo = min(0, min w) and
+ *   hi = max(0, max w) of the group, scale = bf16((hi - lo) / 15), zero = clamp(round(-lo / scale), 0, 15), code =
+ *   clamp(round(w / scale) + zero, 0, 15), round to nearest, ties to even. A group of zeros (or whose scale
+ *   rounds to 0) gets scale 0; a group with a NaN or an infinity a NaN scale.
+ * moe_w4_pack -- lay `matrices` matrices of N rows of K elements out for the products. zeros nullable (all 8).
+ *   `packed`: moe_workspace_bytes(MOE_OP_W4_WEIGHTS, 0, 1, matrices, K, N, group) bytes, 256-byte aligned. Any N
+ *   and K up to 2^20 (rows are padded to multiples of 16 with scale 0, K to multiples of 128). Layout: for
+ *   (matrix, 16-row tile, 128-element chunk) in this order 1024 bytes of codes: the word of row r and elements
+ *   32 q + 8 t ..+7 at byte (r / 8) 512 + ((r % 8) 4 + t) 16 + 4 q, elements 0 2 4 6 1 3 5 7 from its lowest four
+ *   bits up; then (256-byte aligned) 32 * 128 / group bytes of scales each: rows r and r + 8 of group j as a pair
+ *   of bf16 at ((r % 8) 128 / group + j) 4; then 8 * 128 / group bytes of zero points each, likewise, row r in
+ *   the low half of a byte.
+ * moe_w4_matvec -- y[s] = W[ids[s]] x[s / top_k] for every slot s < T * top_k: x [T, K] bf16 (rows ldx apart, 0: one
+ *   row for all), ids [T * top_k] int32 or NULL (matrix 0 for all), y [T * top_k, N] of y_dtype (rows ldy >= N
+ *   apart). A slot whose id is outside [0, matrices) gets a row of zeros.
+ * moe_w4_swiglu_decode -- out[t] = sum_j weights[t, j] SwiGLU(x[t] W_ug,e^T) W_down,e with e = ids[t, j]: w_ug packs 2 E
+ *   matrices of h rows of d elements (matrix 2e: gate of expert e, 2e + 1: up), w_down E matrices of d rows of h
+ *   elements (the transpose of W_down,e). SwiGLU's output is rounded to bf16, as in the BF16 forward; out [T, d]
+ *   bf16 is summed over the slots in order in fp32 and rounded once. weights [T * top_k] fp32, nullable (ones).
+ *   Slots with ids outside [0, E) are dropped. ws: moe_workspace_bytes(MOE_OP_W4_DECODE, T, top_k, E, d, h, 0)
+ *   bytes, 256-byte aligned; it may not be shared by calls that can overlap.
+ * Limits: T * top_k <= 4096 (prompts run in pieces), E <= 1024, matrices <= 2048, top_k <= 32. Results are
+ * deterministic; a token's row alone and in a batch may differ in the order of its sums.
+ */
+moe_status_t moe_w4_quantize_rows(const moe_bf16* w, long long rows, int K, int group, uint8_t* codes, moe_bf16* scales,
+                                  uint8_t* zeros, moe_stream_t stream);
+moe_status_t moe_w4_pack(const uint8_t* codes, const moe_bf16* scales, const uint8_t* zeros, int matrices, int N, int K,
+                         int group, void* packed, size_t packed_bytes, moe_stream_t stream);
+moe_status_t moe_w4_matvec(const moe_bf16* x, long long ldx, const int32_t* ids, int T, int top_k, int matrices, int N,
+                           int K, int group, const void* packed, void* y, int y_dtype, long long ldy,
+                           moe_stream_t stream);
+moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_t* ids, const float* weights, int T,
+                                  int top_k, int E, int d, int h, int group, const void* w_ug, const void* w_down,
+                                  moe_bf16* out, long long ldo, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Human-readable text of a status (static storage). */
 const char* moe_status_string(moe_status_t status);

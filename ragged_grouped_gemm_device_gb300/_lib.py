@@ -26,10 +26,22 @@ MOE_DEV_BAD_OFFSETS = 0x2
 OP_ROUTE, OP_FWD, OP_BWD, OP_PADDED_BMM, OP_LOOP, OP_SAVED, OP_MX_WEIGHTS, OP_MX_FWD, OP_MX_BWD, OP_MX_ROW_SCALES = \
     range(10)
 OP_MX4_WEIGHTS, OP_MX4_FWD, OP_MX4_ROW_SCALES, OP_GATE, OP_LAYER_NORM_BWD = range(10, 15)
+OP_RESIDUAL_NORM_BWD, OP_GRAD_NORM, OP_W4_WEIGHTS, OP_W4_DECODE = range(15, 19)
 DTYPE_BF16, DTYPE_F32 = 0, 1
 GATE_RENORM = 0x1
+NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2
+W4_MAX_SLOTS = 4096  # token slots of one call of the 4-bit integer products
 
 _P, _I, _S, _L, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong, ctypes.c_float
+_D, _U = ctypes.c_double, ctypes.c_uint32
+
+
+class AdamWTensor(ctypes.Structure):
+    """moe_adamw_tensor_t: one tensor of moe_grad_norm and moe_adamw_step (device pointers)."""
+    _fields_ = [("p", _P), ("copy", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P), ("n", _L),
+                ("weight_decay", _F), ("p_dtype", _I), ("g_dtype", _I), ("reserved", _I)]
+
+
 _PI32, _PI64 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_longlong)
 SIGNATURES = {
     "moe_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I, _I]),
@@ -66,6 +78,16 @@ SIGNATURES = {
     "moe_gate_bwd": (_I, [_P, _I, _L, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _L, _P]),
     "moe_layer_norm_fwd": (_I, [_P, _I, _L, _P, _P, _I, _I, _I, _F, _P, _L, _P, _P, _P]),
     "moe_layer_norm_bwd": (_I, [_P, _L, _P, _L, _I, _P, _I, _P, _P, _I, _I, _P, _L, _P, _P, _P, _S, _P]),
+    "moe_residual_norm_fwd": (_I, [_P, _I, _L, _P, _I, _L, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _F, _F, _F, _P, _L, _P, _L,
+                                   _P, _P]),
+    "moe_residual_norm_bwd": (_I, [_P, _L, _P, _L, _P, _L, _I, _P, _L, _I, _I, _P, _P, _P, _I, _P, _I, _P, _I, _I, _F, _F, _P,
+                                   _L, _P, _L, _P, _P, _P, _P, _P, _P, _S, _P]),
+    "moe_grad_norm": (_I, [_P, _I, _F, _P, _P, _S, _P]),
+    "moe_adamw_step": (_I, [_P, _I, _I, _D, _D, _D, _D, _U, _P, _P, _P, _P]),
+    "moe_w4_quantize_rows": (_I, [_P, _L, _I, _I, _P, _P, _P, _P]),
+    "moe_w4_pack": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _S, _P]),
+    "moe_w4_matvec": (_I, [_P, _L, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _L, _P]),
+    "moe_w4_swiglu_decode": (_I, [_P, _L, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _L, _P, _S, _P]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
     "moe_last_cuda_error": (ctypes.c_char_p, []),
     "moe_abi_version": (_I, []),
@@ -490,6 +512,128 @@ def moe_layer_norm_bwd(dy, x, gamma, mean, rstd, T, d, dx, dgamma=None, dbeta=No
         pdy, lddy, px, ldx, _dtype(x), _ptr(gamma), _norm_weight(d, gamma), _typed(mean, f32, T, "mean"),
         _typed(rstd, f32, T, "rstd"), T, d, pdx, lddx, _typed(dgamma, f32, d, "dgamma"),
         _typed(dbeta, f32, d, "dbeta"), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def _rows_or_none(t, T, width):
+    return (None, 0) if t is None else _rows(t, T, width)
+
+
+def _same_type(what, *ts):
+    if len({t.dtype for t in ts if t is not None}) > 1:
+        raise ValueError(f"{what} have to have one type")
+
+
+def moe_residual_norm_fwd(x, y, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta, T, d, eps, res_scale,
+                          branch_scale, r, n, stats=None, stream=None):
+    """r = res_scale x + branch_scale gate post(y), n = pre(r): x, r [T, d] of one type, y, n of one type (any row
+    pitch); the weights nullable [d] of one type; y, r or n nullable (see the header)."""
+    import torch
+    px, ldx = _rows(x, T, d)
+    py, ldy = _rows_or_none(y, T, d)
+    pr, ldr = _rows_or_none(r, T, d)
+    pn, ldn = _rows_or_none(n, T, d)
+    _same_type("x and r", x, r)
+    _same_type("y and n", y, n)
+    weights = (post_gamma, post_beta, gate, pre_gamma, pre_beta)
+    branch = y if y is not None else n if n is not None else x
+    _check("moe_residual_norm_fwd", load().moe_residual_norm_fwd(
+        px, _dtype(x), ldx, py, _dtype(branch), ldy, post, _ptr(post_gamma), _ptr(post_beta), _ptr(gate), pre,
+        _ptr(pre_gamma), _ptr(pre_beta), _norm_weight(d, *weights), T, d, eps, res_scale, branch_scale, pr, ldr, pn, ldn,
+        _typed(stats, torch.float32, 4 * T, "stats"), _stream(stream)))
+
+
+def moe_residual_norm_bwd(dn, dr, r, y, post, post_gamma, post_beta, gate, pre, pre_gamma, stats, T, d, res_scale,
+                          branch_scale, dx, dy, d_post_gamma=None, d_post_beta=None, d_gate=None, d_pre_gamma=None,
+                          d_pre_beta=None, ws=None, stream=None):
+    import torch
+    f32 = torch.float32
+    pdn, lddn = _rows_or_none(dn, T, d)
+    pdr, lddr = _rows_or_none(dr, T, d)
+    pr, ldr = _rows_or_none(r, T, d)
+    py, ldy = _rows_or_none(y, T, d)
+    pdx, lddx = _rows_or_none(dx, T, d)
+    pdy, lddy = _rows_or_none(dy, T, d)
+    _same_type("dr, r and dx", dr, r, dx)
+    _same_type("dn, y and dy", dn, y, dy)
+    first = lambda *ts: next((t for t in ts if t is not None), None)  # noqa: E731
+    stream_like, branch_like = first(dr, r, dx), first(dn, y, dy)
+    stream_like, branch_like = first(stream_like, branch_like), first(branch_like, stream_like)
+    if stream_like is None:
+        raise ValueError("neither gradients nor rows were given")
+    _check("moe_residual_norm_bwd", load().moe_residual_norm_bwd(
+        pdn, lddn, pdr, lddr, pr, ldr, _dtype(stream_like), py, ldy, _dtype(branch_like), post, _ptr(post_gamma),
+        _ptr(post_beta), _ptr(gate), pre, _ptr(pre_gamma), _norm_weight(d, post_gamma, post_beta, gate, pre_gamma),
+        _typed(stats, f32, 4 * T, "stats"), T, d, res_scale, branch_scale, pdx, lddx, pdy, lddy,
+        _typed(d_post_gamma, f32, d, "d_post_gamma"), _typed(d_post_beta, f32, d, "d_post_beta"),
+        _typed(d_gate, f32, d, "d_gate"), _typed(d_pre_gamma, f32, d, "d_pre_gamma"),
+        _typed(d_pre_beta, f32, d, "d_pre_beta"), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_grad_norm(tensors, max_norm, norm, ws, stream=None):
+    """tensors: a ctypes array of AdamWTensor; norm [2] fp32 out: the norm and the clipping coefficient."""
+    import torch
+    _check("moe_grad_norm", load().moe_grad_norm(tensors, len(tensors), max_norm, _typed(norm, torch.float32, 2, "norm"),
+                                                 _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def moe_adamw_step(tensors, state_bits, lr, beta1, beta2, eps, seed, steps, lr_scale=None, grad_scale=None, stream=None):
+    """tensors: a ctypes array of AdamWTensor; steps [2] int32; lr_scale, grad_scale nullable [1] fp32."""
+    import torch
+    f32 = torch.float32
+    _check("moe_adamw_step", load().moe_adamw_step(
+        tensors, len(tensors), state_bits, lr, beta1, beta2, eps, seed, _typed(steps, torch.int32, 2, "steps"),
+        _typed(lr_scale, f32, 1, "lr_scale"), _typed(grad_scale, f32, 1, "grad_scale"), _stream(stream)))
+
+
+def _w4_groups(K, group):
+    return (K + group - 1) // group if group > 0 else 0
+
+
+def moe_w4_quantize_rows(w, rows, K, group, codes, scales, zeros, stream=None):
+    import torch
+    n = rows * _w4_groups(K, group)
+    _check("moe_w4_quantize_rows", load().moe_w4_quantize_rows(
+        _typed(w, torch.bfloat16, rows * K, "w"), rows, K, group, _bytes(codes, rows * ((K + 1) // 2), "codes"),
+        _typed(scales, torch.bfloat16, n, "scales"), _typed(zeros, torch.uint8, n, "zeros"), _stream(stream)))
+
+
+def moe_w4_pack(codes, scales, zeros, matrices, N, K, group, packed, stream=None):
+    import torch
+    n = matrices * N * _w4_groups(K, group)
+    _check("moe_w4_pack", load().moe_w4_pack(
+        _bytes(codes, matrices * N * ((K + 1) // 2), "codes"), _typed(scales, torch.bfloat16, n, "scales"),
+        _typed(zeros, torch.uint8, n, "zeros"), matrices, N, K, group, _ptr(packed), _nbytes(packed), _stream(stream)))
+
+
+def _w4_weights(t, matrices, K, N, group, name):
+    return _bytes(t, moe_workspace_bytes(OP_W4_WEIGHTS, 0, 1, matrices, K, N, group), name)
+
+
+def moe_w4_matvec(x, ids, T, top_k, matrices, N, K, group, packed, y, stream=None):
+    """x [T, K] bf16, y [T * top_k, N] bf16 or fp32 (any row pitch); ids nullable [T * top_k] int32."""
+    import torch
+    if x.dtype != torch.bfloat16:
+        raise ValueError("x has to be bfloat16")
+    px, ldx = _rows(x, T, K)
+    py, ldy = _rows(y, T * top_k, N)
+    _check("moe_w4_matvec", load().moe_w4_matvec(
+        px, ldx, _typed(ids, torch.int32, T * top_k, "ids"), T, top_k, matrices, N, K, group,
+        _w4_weights(packed, matrices, K, N, group, "packed"), py, _dtype(y), ldy, _stream(stream)))
+
+
+def moe_w4_swiglu_decode(x, ids, weights, T, top_k, E, d, h, group, w_ug, w_down, out, ws, stream=None):
+    """x, out [T, d] bf16 (any row pitch), ids [T * top_k] int32, weights nullable [T * top_k] fp32; w_ug and w_down
+    as moe_w4_pack laid them out."""
+    import torch
+    if x.dtype != torch.bfloat16 or out.dtype != torch.bfloat16:
+        raise ValueError("x and out have to be bfloat16")
+    px, ldx = _rows(x, T, d)
+    po, ldo = _rows(out, T, d)
+    n = T * top_k
+    _check("moe_w4_swiglu_decode", load().moe_w4_swiglu_decode(
+        px, ldx, _typed(ids, torch.int32, n, "ids"), _typed(weights, torch.float32, n, "weights"), T, top_k, E, d, h, group,
+        _w4_weights(w_ug, 2 * E, d, h, group, "w_ug"), _w4_weights(w_down, E, h, d, group, "w_down"), po, ldo, _ptr(ws),
+        _nbytes(ws), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

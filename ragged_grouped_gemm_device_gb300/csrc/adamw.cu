@@ -1,0 +1,457 @@
+// AdamW over many tensors in one launch, with states in 32 or 8 bits, and the gradients' global norm.
+//
+//   g' = c g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
+//   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// Bound by memory: p, m and v are read and written once, g is read once. The tensors are cut into pieces of
+// CHUNK elements, one block each; the descriptors travel in the kernel's parameters, and a block finds its tensor
+// by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
+// pointers allow it. All arithmetic is fp32; the bias corrections are -expm1(t log b), whose error is a unit in the
+// last place for small t too, where 1 - b^t cancels.
+//
+// 8-bit states: blocks of 32 E4M3 elements share a power of two. v is kept as its square root, whose range the
+// elements' 4 exponent bits hold (2^18 within a block). Both are rounded stochastically: with round-to-nearest
+// an element that changes by less than half a step (3 to 6%) would never change, and v moves by 1 - b2 a step. A v that is
+// not zero is not rounded to zero, because the step divides by it. v gains the variance of its root's rounding:
+// about 5% at b2 = 0.999, which makes steps 2.5% shorter.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rows.cuh"
+#include "trace.h"
+
+namespace moe {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int VB = 8;         // elements of a thread in one round
+constexpr int CHUNK = 4096;   // elements of a block: two rounds
+constexpr int MAX_TENSORS = 128;  // of a launch: 11 KB of parameters
+constexpr int NORM_BLOCKS = 1216;
+
+struct Batch {
+  int count;
+  int first;                          // index of the first tensor in the call
+  unsigned chunk0[MAX_TENSORS + 1];   // first piece of each tensor, and the end
+  moe_adamw_tensor_t t[MAX_TENSORS];
+  unsigned char wide[MAX_TENSORS];    // 1: 16-byte accesses
+};
+
+// the tensor of piece c: the last one that starts at or before it and is not empty
+__device__ __forceinline__ int find_tensor(const Batch& b, unsigned c) {
+  int lo = 0, hi = b.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.chunk0[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The finalizer of MurmurHash3 (A. Appleby), a bijection of 32-bit words whose output bits all depend on all
+// input bits.
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x ^= x >> 16;
+  x *= 0x85EBCA6Bu;
+  x ^= x >> 13;
+  x *= 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+
+// eight elements from p, the first `k` of them (0 for the rest)
+__device__ __forceinline__ void load8(const float* p, int k, bool wide, float (&f)[VB]) {
+  if (wide && k == VB) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i) f[i] = i < k ? p[i] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const bf16* p, int k, bool wide, float (&f)[VB]) {
+  if (wide && k == VB) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16_lo(w[i]);
+      f[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i) f[i] = i < k ? __bfloat162float(p[i]) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(float* p, int k, bool wide, const float (&f)[VB]) {
+  if (wide && k == VB) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(f[0], f[1], f[2], f[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(f[4], f[5], f[6], f[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i)
+      if (i < k) p[i] = f[i];
+  }
+}
+// to nearest
+__device__ __forceinline__ void store8(bf16* p, int k, bool wide, const float (&f)[VB]) {
+  if (wide && k == VB) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                              pack_bf16x2(f[6], f[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i)
+      if (i < k) p[i] = __float2bfloat16_rn(f[i]);
+  }
+}
+__device__ __forceinline__ void load8(const uint8_t* p, int k, bool wide, uint32_t (&w)[2]) {
+  if (wide && k == VB) {
+    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(p));
+    w[0] = a.x, w[1] = a.y;
+  } else {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < VB; ++i)
+      if (i < k) w[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
+  }
+}
+__device__ __forceinline__ void store8(uint8_t* p, int k, bool wide, const uint32_t (&w)[2]) {
+  if (wide && k == VB) {
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(w[0], w[1]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i)
+      if (i < k) p[i] = static_cast<uint8_t>(w[i >> 2] >> (8 * (i & 3)));
+  }
+}
+
+// fp32 to bf16, up in magnitude where the fraction and u / 2^16 reach 1
+__device__ __forceinline__ float stochastic_bf16(float x, uint32_t u) {
+  return x == x ? __uint_as_float((__float_as_uint(x) + u) & 0xFFFF0000u) : x;
+}
+
+// ------------------------------------------------------------------ 8-bit states
+// An E4M3 magnitude is the top 7 bits below the sign of an fp32 value 2^120 times smaller: the exponent biases differ
+// by 120, and the subnormals of both types meet.
+constexpr float E4M3_UP = 0x1p120f, E4M3_DOWN = 0x1p-120f;
+
+__device__ __forceinline__ float block_scale(uint32_t byte) {
+  return byte == 0xFF ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
+}
+__device__ __forceinline__ float from_e4m3(uint32_t code, float scale) {
+  const float v = __uint_as_float((code & 0x7Fu) << 20) * E4M3_UP * scale;
+  return code & 0x80u ? -v : v;
+}
+// the scale byte of a block from the bits of its largest magnitude
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  if (top >= 0x7F800000u) return 0xFF;
+  const int b = static_cast<int>(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
+  return b > 0 ? b : 0;
+}
+
+// Eight values of this thread's quarter of a block into codes; returns the scale byte of the block. All threads of the warp call it.
+template <bool KEEP, int SHIFT>
+__device__ __forceinline__ uint32_t to_e4m3(const float (&x)[VB], const uint32_t (&rnd)[VB], uint32_t (&w)[2]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < VB; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);  // by bits: a NaN is the largest
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t byte = scale_byte(top);
+  w[0] = w[1] = 0;
+  if (byte == 0xFF) return byte;
+  const float inv = __uint_as_float((254u - byte) << 23);
+  uint32_t c[VB];
+#pragma unroll
+  for (int i = 0; i < VB; ++i) {
+    const float a = fabsf(x[i]) * inv;
+    c[i] = (__float_as_uint(a * E4M3_DOWN) + (((rnd[i] >> SHIFT) & 0xFFFFu) << 4)) >> 20;
+    if (KEEP) c[i] = a > 0.f ? max(c[i], 1u) : c[i];
+  }
+#pragma unroll
+  for (int i = 0; i < VB; i += 4) {
+    w[i >> 2] = __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
+    // The signs: the highest bytes of four values. (Joined to a code shifted left by 4 before the bytes are packed, nvcc 13.0.88
+    // lost the code.)
+    if (!KEEP) {
+      const uint32_t lo = __byte_perm(__float_as_uint(x[i]), __float_as_uint(x[i + 1]), 0x0073);
+      const uint32_t hi = __byte_perm(__float_as_uint(x[i + 2]), __float_as_uint(x[i + 3]), 0x0073);
+      w[i >> 2] |= __byte_perm(lo, hi, 0x5410) & 0x80808080u;
+    }
+  }
+  return byte;
+}
+
+struct StepArgs {
+  float lr, b1, omb1, b2, omb2, log_b1, log_b2, eps;
+  uint32_t seed;
+  int32_t* steps;
+  const float* lr_scale;
+  const float* grad_scale;
+  unsigned blocks;  // of this launch
+  bool last;        // the call's last launch counts the step
+};
+
+template <int BITS>
+__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Batch batch, const StepArgs a) {
+  grid_wait();
+  const float c = a.grad_scale ? *after_wait(a.grad_scale) : 1.0f;
+  if (c != c) return;  // the norm was not finite: the step is skipped
+  const int t = *reinterpret_cast<volatile int32_t*>(a.steps) + 1;
+  if (blockIdx.x < batch.chunk0[batch.count]) {
+    const int j = find_tensor(batch, blockIdx.x);
+    const moe_adamw_tensor_t& q = batch.t[j];
+    const float lr = a.lr_scale ? a.lr * *after_wait(a.lr_scale) : a.lr;
+    const float step = lr / -expm1f(static_cast<float>(t) * a.log_b1);
+    const float root = 1.0f / sqrtf(-expm1f(static_cast<float>(t) * a.log_b2));
+    const float keep = fmaf(-lr, q.weight_decay, 1.0f);
+    const bool wide = batch.wide[j] != 0;
+    const uint32_t key = mix(a.seed ^ mix(0x9E3779B9u * static_cast<uint32_t>(t) + static_cast<uint32_t>(batch.first + j)));
+    const long long base = static_cast<long long>(blockIdx.x - batch.chunk0[j]) * CHUNK;
+#pragma unroll
+    for (int round = 0; round < CHUNK / (THREADS * VB); ++round) {
+      const long long i0 = base + (round * THREADS + threadIdx.x) * VB;
+      const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), q.n - i0)));  // elements of this thread
+      float g[VB], m[VB], v[VB], p[VB];
+      if (q.g_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.g) + i0, k, wide, g);
+      else load8(static_cast<const float*>(q.g) + i0, k, wide, g);
+      if (q.p_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.p) + i0, k, wide, p);
+      else load8(static_cast<const float*>(q.p) + i0, k, wide, p);
+      if constexpr (BITS == 8) {
+        uint32_t wm[2], wv[2];
+        load8(static_cast<const uint8_t*>(q.m) + i0, k, wide, wm);
+        load8(static_cast<const uint8_t*>(q.v) + i0, k, wide, wv);
+        const float sm = k > 0 ? block_scale(q.m_scale[i0 >> 5]) : 0.f, sv = k > 0 ? block_scale(q.v_scale[i0 >> 5]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < VB; ++i) {
+          m[i] = from_e4m3(wm[i >> 2] >> (8 * (i & 3)), sm);
+          const float r = from_e4m3(wv[i >> 2] >> (8 * (i & 3)), sv);
+          v[i] = r * r;
+        }
+      } else {
+        load8(static_cast<const float*>(q.m) + i0, k, wide, m);
+        load8(static_cast<const float*>(q.v) + i0, k, wide, v);
+      }
+      float r[VB];
+#pragma unroll
+      for (int i = 0; i < VB; ++i) {
+        const float gc = g[i] * c;
+        m[i] = fmaf(a.b1, m[i], a.omb1 * gc);
+        v[i] = fmaf(a.b2, v[i], a.omb2 * gc * gc);
+        r[i] = sqrtf(v[i]);
+        p[i] = fmaf(p[i], keep, -(step * m[i]) / fmaf(r[i], root, a.eps));
+      }
+      uint32_t rnd[VB];
+      if (BITS == 8 || q.p_dtype == MOE_DTYPE_BF16) {
+        const uint32_t x0 = key + static_cast<uint32_t>(i0) * 0x9E3779B9u + static_cast<uint32_t>(i0 >> 32) * 0x85EBCA6Bu;
+#pragma unroll
+        for (int i = 0; i < VB; ++i) rnd[i] = mix(x0 + static_cast<uint32_t>(i) * 0x9E3779B9u);
+      }
+      if (q.p_dtype == MOE_DTYPE_BF16) {
+#pragma unroll
+        for (int i = 0; i < VB; ++i) p[i] = stochastic_bf16(p[i], (rnd[i] >> 8) & 0xFFFFu);
+        store8(static_cast<bf16*>(q.p) + i0, k, wide, p);
+      } else {
+        store8(static_cast<float*>(q.p) + i0, k, wide, p);
+        if (q.copy != nullptr) store8(static_cast<bf16*>(q.copy) + i0, k, wide, p);
+      }
+      if constexpr (BITS == 8) {
+#pragma unroll
+        for (int i = 0; i < VB; ++i) {  // what lies behind the tensor's end takes no part in its last block
+          m[i] = i < k ? m[i] : 0.f;
+          r[i] = i < k ? r[i] : 0.f;
+        }
+        uint32_t w[2];
+        uint32_t byte = to_e4m3<false, 0>(m, rnd, w);
+        store8(static_cast<uint8_t*>(q.m) + i0, k, wide, w);
+        if (k > 0 && (threadIdx.x & 3) == 0) q.m_scale[i0 >> 5] = static_cast<uint8_t>(byte);
+        byte = to_e4m3<true, 16>(r, rnd, w);
+        store8(static_cast<uint8_t*>(q.v) + i0, k, wide, w);
+        if (k > 0 && (threadIdx.x & 3) == 0) q.v_scale[i0 >> 5] = static_cast<uint8_t>(byte);
+      } else {
+        store8(static_cast<float*>(q.m) + i0, k, wide, m);
+        store8(static_cast<float*>(q.v) + i0, k, wide, v);
+      }
+    }
+  }
+  // The last block to end counts the step: by then every thread has read the count.
+  if (!a.last) return;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  __threadfence();
+  if (atomicAdd(a.steps + 1, 1) == static_cast<int>(a.blocks) - 1) {
+    a.steps[1] = 0;
+    a.steps[0] = t;
+  }
+}
+
+// Partial sums of g^2, one fp64 per block: the pieces blockIdx.x, blockIdx.x + gridDim.x, ... of a launch's tensors, added to
+// what the launches before it left.
+__global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Batch batch, double* part, bool first) {
+  __shared__ __align__(16) float red[2][32];
+  grid_wait();
+  double sum = 0.0;
+  int par = 0;
+  for (unsigned c = blockIdx.x; c < batch.chunk0[batch.count]; c += gridDim.x) {
+    const int j = find_tensor(batch, c);
+    const moe_adamw_tensor_t& q = batch.t[j];
+    const bool wide = batch.wide[j] != 0;
+    float s = 0.f;
+#pragma unroll
+    for (int round = 0; round < CHUNK / (THREADS * VB); ++round) {
+      const long long i0 = static_cast<long long>(c - batch.chunk0[j]) * CHUNK + (round * THREADS + threadIdx.x) * VB;
+      const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), q.n - i0)));
+      float g[VB];
+      if (q.g_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.g) + i0, k, wide, g);
+      else load8(static_cast<const float*>(q.g) + i0, k, wide, g);
+#pragma unroll
+      for (int i = 0; i < VB; ++i) s = fmaf(g[i], g[i], s);
+    }
+    sum += static_cast<double>(row_sum<THREADS>(s, red[par]));
+    par ^= 1;
+  }
+  if (threadIdx.x == 0) part[blockIdx.x] = first ? sum : part[blockIdx.x] + sum;
+}
+
+// The norm and the coefficient from the partial sums, in index order within each thread and by a fixed tree.
+__global__ void __launch_bounds__(1024) grad_norm_end_kernel(const double* part, int blocks, float max_norm, float* norm) {
+  __shared__ double acc[1024];
+  grid_wait();
+  part = after_wait(part);
+  double s = 0.0;
+  for (int b = threadIdx.x; b < blocks; b += 1024) s += part[b];
+  acc[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 512; o > 0; o >>= 1) {
+    if (threadIdx.x < o) acc[threadIdx.x] += acc[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x != 0) return;
+  const float n = static_cast<float>(sqrt(acc[0]));
+  norm[0] = n;
+  norm[1] = n <= 3.402823466e38f ? max_norm / fmaxf(n, max_norm) : __uint_as_float(0x7FC00000u);
+}
+
+bool aligned_to(const void* p, int b) { return (reinterpret_cast<uintptr_t>(p) & (b - 1)) == 0; }
+
+// What a call's tensors have to be; `grads` only g, g_dtype and n
+moe_status_t check_tensors(const moe_adamw_tensor_t* t, int count, bool grads, int bits) {
+  if (count < 0 || (count > 0 && !t)) return MOE_ERR_INVALID_ARG;
+  unsigned long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor_t& q = t[i];
+    if (q.n < 0 || !dtype_ok(q.g_dtype)) return MOE_ERR_INVALID_ARG;
+    if (q.n >= (1LL << 43)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    total += (static_cast<unsigned long long>(q.n) + CHUNK - 1) / CHUNK;
+    if (total >= (1ull << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned_to(q.g, dtype_bytes(q.g_dtype)) || (q.n > 0 && !q.g)) return MOE_ERR_INVALID_ARG;
+    if (grads) continue;
+    if (!dtype_ok(q.p_dtype) || q.reserved != 0 || !std::isfinite(q.weight_decay)) return MOE_ERR_INVALID_ARG;
+    if (q.copy && q.p_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+    if (!aligned_to(q.p, dtype_bytes(q.p_dtype)) || !aligned_to(q.copy, 2)) return MOE_ERR_INVALID_ARG;
+    if (bits == 32 && (!aligned_to(q.m, 4) || !aligned_to(q.v, 4))) return MOE_ERR_INVALID_ARG;
+    if (q.n > 0 && (!q.p || !q.m || !q.v || (bits == 8 && (!q.m_scale || !q.v_scale)))) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+// the tensors i, i + 1, ... that one launch takes
+int fill(Batch& b, const moe_adamw_tensor_t* t, int i, int count, bool grads, int bits) {
+  const int n = std::min(count - i, MAX_TENSORS);
+  b.count = n;
+  b.first = i;
+  unsigned at = 0;
+  for (int k = 0; k < n; ++k) {
+    const moe_adamw_tensor_t& q = t[i + k];
+    b.t[k] = q;
+    b.chunk0[k] = at;
+    at += static_cast<unsigned>((q.n + CHUNK - 1) / CHUNK);
+    b.wide[k] = aligned16(q.g) && (grads || (aligned16(q.p) && aligned16(q.copy) && aligned_to(q.m, bits == 8 ? 8 : 16) &&
+                                             aligned_to(q.v, bits == 8 ? 8 : 16)));
+  }
+  b.chunk0[n] = at;
+  return n;
+}
+
+}  // namespace
+
+size_t grad_norm_workspace_bytes() { return NORM_BLOCKS * sizeof(double); }
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float max_norm, float* norm, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (!(max_norm > 0.f) || std::isinf(max_norm) || !norm || !element_aligned(norm, 4) || !aligned_to(ws, 8)) return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_tensors(tensors, count, true, 0);
+  if (st != MOE_OK) return st;
+  if (ws_bytes < grad_norm_workspace_bytes()) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws) return MOE_ERR_INVALID_ARG;
+  st = check_device();
+  if (st != MOE_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  double* part = static_cast<double*>(ws);
+  unsigned most = 1;  // blocks: no more than the largest launch has pieces
+  for (int i = 0; i < count; i += MAX_TENSORS) {
+    unsigned chunks = 0;
+    for (int k = i; k < std::min(count, i + MAX_TENSORS); ++k) chunks += static_cast<unsigned>((tensors[k].n + CHUNK - 1) / CHUNK);
+    most = std::max(most, chunks);
+  }
+  const int blocks = static_cast<int>(std::min<unsigned>(most, NORM_BLOCKS));
+  cudaError_t err = cudaSuccess;
+  for (int i = 0; err == cudaSuccess && (i < count || i == 0);) {
+    Batch b;
+    const int n = fill(b, tensors, i, count, true, 0);
+    err = launch_dependent(grad_norm_kernel, blocks, THREADS, 0, s, b, part, i == 0);
+    i += std::max(n, 1);
+  }
+  if (err == cudaSuccess)
+    err = launch_dependent(grad_norm_end_kernel, 1, 1024, 0, s, static_cast<const double*>(part), blocks, max_norm, norm);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
+}
+
+moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int state_bits, double lr, double beta1,
+                            double beta2, double eps, uint32_t seed, int32_t* steps, const float* lr_scale,
+                            const float* grad_scale, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (state_bits != 32 && state_bits != 8) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(lr) || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps >= 0.0) || std::isinf(eps))
+    return MOE_ERR_INVALID_ARG;
+  if (!steps || !element_aligned(steps, 4) || !element_aligned(lr_scale, 4) || !element_aligned(grad_scale, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_tensors(tensors, count, false, state_bits);
+  if (st != MOE_OK) return st;
+  st = check_device();
+  if (st != MOE_OK) return st;
+  StepArgs a{};
+  a.lr = static_cast<float>(lr);
+  a.b1 = static_cast<float>(beta1);
+  a.omb1 = static_cast<float>(1.0 - beta1);
+  a.b2 = static_cast<float>(beta2);
+  a.omb2 = static_cast<float>(1.0 - beta2);
+  a.log_b1 = static_cast<float>(std::log(beta1));
+  a.log_b2 = static_cast<float>(std::log(beta2));
+  a.eps = static_cast<float>(eps);
+  a.seed = seed;
+  a.steps = steps;
+  a.lr_scale = lr_scale;
+  a.grad_scale = grad_scale;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  for (int i = 0; i < count || i == 0;) {
+    Batch b;
+    const int n = fill(b, tensors, i, count, false, state_bits);
+    a.blocks = std::max(b.chunk0[n], 1u);
+    a.last = i + n >= count;
+    const cudaError_t err = launch_dependent(state_bits == 8 ? adamw_kernel<8> : adamw_kernel<32>, a.blocks, THREADS, 0, s, b, a);
+    if (err != cudaSuccess) return cuda_fail(err);
+    i += std::max(n, 1);
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

@@ -230,6 +230,10 @@ moe_status_t launch_mx_quant_cols(const void* w, int E, int R, int C, void* q, v
 // Workspace sizes of the calls whose entry points live beside their kernels
 size_t layer_norm_bwd_workspace_bytes(int T, int d);                 // layer_norm.cu
 size_t gate_workspace_bytes(int T, int E);                           // gate.cu
+size_t residual_norm_bwd_workspace_bytes(int T, int d);              // residual_norm.cu
+size_t grad_norm_workspace_bytes();                                  // adamw.cu
+size_t w4_weights_bytes(int matrices, int K, int N, int group);      // w4.cu
+size_t w4_decode_workspace_bytes(long long slots, int E, int d, int h);
 size_t mx4_workspace_bytes(int op, long long n, int E, int d, int h);  // mx4.cu: the MOE_OP_MX4_* sizes
 moe_status_t launch_unpad_rows(const void* src, const int32_t* offsets, int E, int C, int cap,
                                int cols, void* dst, cudaStream_t s);

@@ -415,6 +415,7 @@ const char* moe_status_string(moe_status_t s) {
 }
 
 size_t moe_workspace_bytes(int op, int T, int top_k, int E, int d, int h, int capacity_C) {
+  if (op == MOE_OP_W4_WEIGHTS) return w4_weights_bytes(E, d, h, capacity_C);
   if (T < 0 || top_k < 1 || top_k > MAX_TOPK || E < 1 || E > MAX_E) return 0;
   const long long n = static_cast<long long>(T) * top_k;
   switch (op) {
@@ -441,6 +442,9 @@ size_t moe_workspace_bytes(int op, int T, int top_k, int E, int d, int h, int ca
     case MOE_OP_MX4_ROW_SCALES: return mx4_workspace_bytes(op, n, E, d, h);
     case MOE_OP_LAYER_NORM_BWD: return layer_norm_bwd_workspace_bytes(T, d);
     case MOE_OP_GATE: return gate_workspace_bytes(T, E);
+    case MOE_OP_RESIDUAL_NORM_BWD: return residual_norm_bwd_workspace_bytes(T, d);
+    case MOE_OP_GRAD_NORM: return grad_norm_workspace_bytes();
+    case MOE_OP_W4_DECODE: return w4_decode_workspace_bytes(n, E, d, h);
   }
   return 0;
 }

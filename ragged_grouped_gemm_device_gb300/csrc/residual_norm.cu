@@ -1,0 +1,458 @@
+// What stands between two blocks, in one pass: the norm behind a block, its gate and scale, the residual
+// addition and the norm in front of the next block.
+//
+//   z = post(y);  r = alpha x + beta gate z;  n = pre(r),  post and pre: none, layer norm or RMS norm
+//   D = dr + pre'(dn);  dx = alpha D;  dz = beta gate D;  dy = post'(dz)
+//
+// With yhat = (y - mean1) rstd1 and rhat = (r - mean2) rstd2 (mean 0 for RMS), every weight gradient comes
+// from four sums over the rows:  S1 = sum D yhat, S0 = sum D, P1 = sum dn rhat, P0 = sum dn:
+//   d_post_gamma = beta gate S1;  d_post_beta = beta gate S0;  d_gate = beta (post_gamma S1 + post_beta S0)
+//   d_pre_gamma = P1;  d_pre_beta = P0
+// Each block of rows leaves one partial row of each sum in the workspace; a second kernel adds them in
+// block order. No atomics: the results do not depend on scheduling.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rows.cuh"
+#include "trace.h"
+
+namespace moe {
+namespace {
+
+// Rows of partial weight gradients at most: four for each of the 152 SMs. A constant, because the size of
+// the workspace is host arithmetic.
+constexpr int BWD_MAX_BLOCKS = 608;
+constexpr int MAX_WIDTH = 1 << 20;
+constexpr int SUMS = 4;
+
+struct JoinArgs {
+  const void* x;   // forward
+  const void* y;   // nullable: no branch
+  void* r;         // forward: nullable output; backward: input
+  void* n;         // forward: nullable output
+  const void* dn;  // backward, nullable
+  const void* dr;  // backward, nullable
+  void* dx;        // backward, nullable outputs
+  void* dy;
+  long long ldx, ldy, ldr, ldn, lddn, lddr, lddx, lddy;
+  const void* g1;    // post gamma, post beta, gate, pre gamma, pre beta: nullable
+  const void* b1;
+  const void* gate;
+  const void* g2;
+  const void* b2;
+  bool w_bf16;
+  int post, pre;
+  int T, d;
+  float eps, alpha, beta;
+  float* stats;  // [4][T]: forward nullable outputs, backward inputs
+  float* part;   // backward: [blocks][4][d] partial sums (nullable: not wanted)
+  float* row;    // backward of wide rows: [T][2] means of the pre norm's gradient
+};
+
+// ------------------------------------------------------------------ rows of any width
+// One block a row, single elements, one pass over the row for each reduction (the later ones from L2).
+constexpr int WIDE_THREADS = 512;
+
+template <typename T>
+__device__ __forceinline__ float get(const T* p) {
+  Chunk<T, 1> q;
+  float f[1];
+  q.load(p);
+  q.unpack(f);
+  return f[0];
+}
+template <typename T>
+__device__ __forceinline__ float rounded(float v) {
+  if constexpr (sizeof(T) == 2) return __bfloat162float(__float2bfloat16_rn(v));
+  else return v;
+}
+template <typename T>
+__device__ __forceinline__ void put(T* p, float v) {
+  const float f[1] = {v};
+  Chunk<T, 1>::store(p, f);
+}
+__device__ __forceinline__ float weight(const void* w, bool w_bf16, int c, float fill) {
+  float o[1];
+  load_weight<1>(w, w_bf16, c, fill, o);
+  return o[0];
+}
+
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(WIDE_THREADS) join_fwd_wide_kernel(const JoinArgs a) {
+  __shared__ __align__(16) float red[2][32];
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  int par = 0;
+  const auto sum = [&](float v) {
+    const float s = row_sum<WIDE_THREADS>(v, red[par]);
+    par ^= 1;
+    return s;
+  };
+  for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const TX* x = static_cast<const TX*>(a.x) + row * a.ldx;
+    const TY* y = a.y ? static_cast<const TY*>(a.y) + row * a.ldy : nullptr;
+    TX* r = a.r ? static_cast<TX*>(a.r) + row * a.ldr : nullptr;
+    float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f, s = 0.f;
+    if (a.post == MOE_NORM_LAYER) {
+      for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) s += get(y + c);
+      mean1 = sum(s) * inv_d;
+    }
+    if (a.post != MOE_NORM_NONE) {
+      s = 0.f;
+      for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
+        const float v = get(y + c) - mean1;
+        s = fmaf(v, v, s);
+      }
+      rstd1 = 1.0f / sqrtf(sum(s) * inv_d + a.eps);
+    }
+    // the row as it is stored
+    const auto joined = [&](int c) {
+      float v = a.alpha * get(x + c);
+      if (y != nullptr) {
+        const float z = fmaf((get(y + c) - mean1) * rstd1, weight(a.g1, a.w_bf16, c, 1.f), weight(a.b1, a.w_bf16, c, 0.f));
+        v = fmaf(a.beta * weight(a.gate, a.w_bf16, c, 1.f), z, v);
+      }
+      return rounded<TX>(v);
+    };
+    s = 0.f;
+    if (r != nullptr || a.pre == MOE_NORM_LAYER) {
+      for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
+        const float v = joined(c);
+        if (r != nullptr) put(r + c, v);
+        s += v;
+      }
+    }
+    const auto again = [&](int c) { return r != nullptr ? get(r + c) : joined(c); };  // r may lie over x
+    if (a.pre == MOE_NORM_LAYER) mean2 = sum(s) * inv_d;
+    if (a.pre != MOE_NORM_NONE) {
+      s = 0.f;
+      for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
+        const float v = again(c) - mean2;
+        s = fmaf(v, v, s);
+      }
+      rstd2 = 1.0f / sqrtf(sum(s) * inv_d + a.eps);
+      for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS)
+        put(static_cast<TY*>(a.n) + row * a.ldn + c,
+            fmaf((again(c) - mean2) * rstd2, weight(a.g2, a.w_bf16, c, 1.f), weight(a.b2, a.w_bf16, c, 0.f)));
+    }
+    if (threadIdx.x == 0 && a.stats != nullptr) {
+      const size_t T = a.T;
+      a.stats[row] = mean1;
+      a.stats[T + row] = rstd1;
+      a.stats[2 * T + row] = mean2;
+      a.stats[3 * T + row] = rstd2;
+    }
+  }
+}
+
+// What the backward reads of one row
+template <typename TX, typename TY>
+struct WideRow {
+  const TY *dn, *y;
+  const TX *dr, *r;
+  float mean1, rstd1, mean2, rstd2, m1, m2;
+  __device__ __forceinline__ WideRow(const JoinArgs& a, long long row) {
+    dn = a.dn ? static_cast<const TY*>(a.dn) + row * a.lddn : nullptr;
+    y = a.y ? static_cast<const TY*>(a.y) + row * a.ldy : nullptr;
+    dr = a.dr ? static_cast<const TX*>(a.dr) + row * a.lddr : nullptr;
+    r = a.r ? static_cast<const TX*>(a.r) + row * a.ldr : nullptr;
+    const size_t T = a.T;
+    mean1 = a.post == MOE_NORM_LAYER ? __ldg(a.stats + row) : 0.f;
+    rstd1 = a.post != MOE_NORM_NONE ? __ldg(a.stats + T + row) : 1.f;
+    mean2 = a.pre == MOE_NORM_LAYER ? __ldg(a.stats + 2 * T + row) : 0.f;
+    rstd2 = a.pre != MOE_NORM_NONE ? __ldg(a.stats + 3 * T + row) : 1.f;
+  }
+  __device__ __forceinline__ float rhat(int c) const { return (get(r + c) - mean2) * rstd2; }
+  __device__ __forceinline__ float yhat(int c) const { return (get(y + c) - mean1) * rstd1; }
+  // the gradient of r, with the means m1 and m2 of the pre norm's gradient
+  __device__ __forceinline__ float grad(const JoinArgs& a, int c) const {
+    float v = dr ? get(dr + c) : 0.f;
+    if (a.pre != MOE_NORM_NONE) v += rstd2 * (weight(a.g2, a.w_bf16, c, 1.f) * get(dn + c) - m1 - rhat(c) * m2);
+    return v;
+  }
+};
+
+// The means of the pre norm's gradient, [T][2].
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(WIDE_THREADS) join_bwd_means_kernel(const JoinArgs a) {
+  __shared__ __align__(16) float red[2][64];
+  int par = 0;
+  for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
+    const WideRow<TX, TY> w(a, row);
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
+      const float g = weight(a.g2, a.w_bf16, c, 1.f) * get(w.dn + c);
+      s1 += g;
+      s2 = fmaf(g, w.rhat(c), s2);
+    }
+    const float2 s = row_sum<WIDE_THREADS>(s1, s2, red[par]);
+    par ^= 1;
+    if (threadIdx.x == 0) {
+      a.row[2 * row] = a.pre == MOE_NORM_LAYER ? s.x / static_cast<float>(a.d) : 0.f;
+      a.row[2 * row + 1] = s.y / static_cast<float>(a.d);
+    }
+  }
+}
+
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(WIDE_THREADS) join_bwd_wide_kernel(const JoinArgs a) {
+  __shared__ __align__(16) float red[2][64];
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  int par = 0;
+  for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
+    WideRow<TX, TY> w(a, row);
+    w.m1 = a.pre != MOE_NORM_NONE ? a.row[2 * row] : 0.f;
+    w.m2 = a.pre != MOE_NORM_NONE ? a.row[2 * row + 1] : 0.f;
+    const auto branch = [&](int c) { return a.beta * weight(a.gate, a.w_bf16, c, 1.f) * weight(a.g1, a.w_bf16, c, 1.f); };
+    float s1 = 0.f, s2 = 0.f;
+    if (a.post != MOE_NORM_NONE) {
+      for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
+        const float g = branch(c) * w.grad(a, c);
+        s1 += g;
+        s2 = fmaf(g, w.yhat(c), s2);
+      }
+      const float2 s = row_sum<WIDE_THREADS>(s1, s2, red[par]);
+      par ^= 1;
+      s1 = a.post == MOE_NORM_LAYER ? s.x * inv_d : 0.f;
+      s2 = s.y * inv_d;
+    }
+    for (int c = threadIdx.x; c < a.d; c += WIDE_THREADS) {
+      const float D = w.grad(a, c);
+      float g = 0.f;  // everything of this column is read before anything is written: dx and dy may lie over inputs
+      if (w.y != nullptr) {
+        g = branch(c) * D;
+        if (a.post != MOE_NORM_NONE) g = w.rstd1 * (g - s1 - w.yhat(c) * s2);
+      }
+      if (a.dx != nullptr) put(static_cast<TX*>(a.dx) + row * a.lddx + c, a.alpha * D);
+      if (w.y != nullptr) put(static_cast<TY*>(a.dy) + row * a.lddy + c, g);
+    }
+  }
+}
+
+// The four sums of wide rows: thread c of block (i, k) adds column c over the rows k, k + gridDim.y, ...
+template <typename TX, typename TY>
+__global__ void __launch_bounds__(256) join_wgrad_wide_kernel(const JoinArgs a) {
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.d) return;
+  float s[SUMS] = {0.f, 0.f, 0.f, 0.f};
+  for (long long row = blockIdx.y; row < a.T; row += gridDim.y) {
+    WideRow<TX, TY> w(a, row);
+    w.m1 = a.pre != MOE_NORM_NONE ? a.row[2 * row] : 0.f;
+    w.m2 = a.pre != MOE_NORM_NONE ? a.row[2 * row + 1] : 0.f;
+    if (w.y != nullptr) {
+      const float D = w.grad(a, c);
+      s[0] = fmaf(D, w.yhat(c), s[0]);
+      s[1] += D;
+    }
+    if (a.pre != MOE_NORM_NONE) {
+      const float g = get(w.dn + c);
+      s[2] = fmaf(g, w.rhat(c), s[2]);
+      s[3] += g;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < SUMS; ++k) a.part[(static_cast<size_t>(blockIdx.y) * SUMS + k) * a.d + c] = s[k];
+}
+
+struct GradOut {
+  float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
+};
+
+// The weight gradients from the partial sums: 32 columns a block, 8 threads for each of a column's four sums, which
+// take every 8th partial and are added in thread order.
+__global__ void __launch_bounds__(1024) join_partials_kernel(const JoinArgs a, int blocks, const GradOut o) {
+  __shared__ float acc[SUMS][8][33];
+  grid_wait();  // launched ahead of the end of the kernel that writes the partials
+  const float* part = after_wait(static_cast<const float*>(a.part));
+  const int cx = threadIdx.x & 31, k = (threadIdx.x >> 5) & 3, ry = threadIdx.x >> 7;
+  const int c = blockIdx.x * 32 + cx;
+  float s = 0.f;
+  if (c < a.d) {
+#pragma unroll 8
+    for (int b = ry; b < blocks; b += 8) s += __ldcs(part + (static_cast<size_t>(b) * SUMS + k) * a.d + c);
+  }
+  acc[k][ry][cx] = s;
+  __syncthreads();
+  if (threadIdx.x >= 32 || c >= a.d) return;
+  float t[SUMS];
+#pragma unroll
+  for (int q = 0; q < SUMS; ++q) {
+    t[q] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[q] += acc[q][i][cx];
+  }
+  const float g = a.beta * weight(a.gate, a.w_bf16, c, 1.f);
+  if (o.post_gamma) o.post_gamma[c] = g * t[0];
+  if (o.post_beta) o.post_beta[c] = g * t[1];
+  if (o.gate) o.gate[c] = a.beta * fmaf(weight(a.g1, a.w_bf16, c, 1.f), t[0], weight(a.b1, a.w_bf16, c, 0.f) * t[1]);
+  if (o.pre_gamma) o.pre_gamma[c] = t[2];
+  if (o.pre_beta) o.pre_beta[c] = t[3];
+}
+
+template <typename TX, typename TY>
+cudaError_t launch_fwd(const JoinArgs& a, cudaStream_t s) {
+  join_fwd_wide_kernel<TX, TY><<<std::min(a.T, 1 << 20), WIDE_THREADS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// `blocks`: the rows of partial sums that the launch leaves
+template <typename TX, typename TY>
+cudaError_t launch_bwd(const JoinArgs& a, cudaStream_t s, int& blocks) {
+  const int grid = std::min(a.T, 1 << 20);
+  blocks = std::min(a.T, BWD_MAX_BLOCKS);
+  if (a.pre != MOE_NORM_NONE) join_bwd_means_kernel<TX, TY><<<grid, WIDE_THREADS, 0, s>>>(a);
+  // the weight gradients first: dx and dy may lie over inputs
+  if (a.part != nullptr) join_wgrad_wide_kernel<TX, TY><<<dim3((a.d + 255) / 256, blocks), 256, 0, s>>>(a);
+  join_bwd_wide_kernel<TX, TY><<<grid, WIDE_THREADS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+size_t part_floats(int T, int d) { return static_cast<size_t>(std::min(T, BWD_MAX_BLOCKS)) * SUMS * d; }
+
+bool norm_ok(int k) { return k == MOE_NORM_NONE || k == MOE_NORM_LAYER || k == MOE_NORM_RMS; }
+bool types_ok(int x, int y) { return dtype_ok(x) && dtype_ok(y) && (x == MOE_DTYPE_F32 || y == MOE_DTYPE_BF16); }
+
+}  // namespace
+
+size_t residual_norm_bwd_workspace_bytes(int T, int d) {
+  if (T < 0 || d < 1 || d > MAX_WIDTH) return 0;
+  return (part_floats(T, d) + 2 * static_cast<size_t>(T)) * sizeof(float);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_residual_norm_fwd(const void* x, int x_dtype, long long ldx, const void* y, int y_dtype, long long ldy,
+                                   int post, const void* post_gamma, const void* post_beta, const void* gate, int pre,
+                                   const void* pre_gamma, const void* pre_beta, int w_dtype, int T, int d, float eps,
+                                   float res_scale, float branch_scale, void* r, long long ldr, void* n, long long ldn,
+                                   float* stats, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (T < 0 || d <= 0 || !types_ok(x_dtype, y_dtype) || !dtype_ok(w_dtype) || !norm_ok(post) || !norm_ok(pre))
+    return MOE_ERR_INVALID_ARG;
+  if (ldx < 0 || (y && ldy < 0) || (r && ldr < d) || (n && ldn < d)) return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || std::isinf(eps) || !std::isfinite(res_scale) || !std::isfinite(branch_scale)) return MOE_ERR_INVALID_ARG;
+  if (d > MAX_WIDTH) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (T > 0 && (!x || (!r && !n) || (pre == MOE_NORM_NONE) != (n == nullptr))) return MOE_ERR_INVALID_ARG;
+  if ((!y && T > 0 && (post != MOE_NORM_NONE || gate)) || (post == MOE_NORM_NONE && post_gamma) ||
+      (post != MOE_NORM_LAYER && post_beta) || (pre == MOE_NORM_NONE && pre_gamma) || (pre != MOE_NORM_LAYER && pre_beta))
+    return MOE_ERR_INVALID_ARG;
+  const int ex = dtype_bytes(x_dtype), ey = dtype_bytes(y_dtype), ew = dtype_bytes(w_dtype);
+  if (!element_aligned(x, ex) || !element_aligned(r, ex) || !element_aligned(y, ey) || !element_aligned(n, ey) ||
+      !element_aligned(post_gamma, ew) || !element_aligned(post_beta, ew) || !element_aligned(gate, ew) ||
+      !element_aligned(pre_gamma, ew) || !element_aligned(pre_beta, ew) || !element_aligned(stats, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe_status_t st = check_device();
+  if (st != MOE_OK || T == 0) return st;
+  JoinArgs a{};
+  a.x = x;
+  a.y = y;
+  a.r = r;
+  a.n = n;
+  a.ldx = ldx;
+  a.ldy = ldy;
+  a.ldr = ldr;
+  a.ldn = ldn;
+  a.g1 = post_gamma;
+  a.b1 = post_beta;
+  a.gate = gate;
+  a.g2 = pre_gamma;
+  a.b2 = pre_beta;
+  a.w_bf16 = w_dtype == MOE_DTYPE_BF16;
+  a.post = post;
+  a.pre = pre;
+  a.T = T;
+  a.d = d;
+  a.eps = eps;
+  a.alpha = res_scale;
+  a.beta = branch_scale;
+  a.stats = stats;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_fwd<bf16, bf16>(a, s)
+                          : y_dtype == MOE_DTYPE_BF16 ? launch_fwd<float, bf16>(a, s)
+                                                      : launch_fwd<float, float>(a, s);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
+}
+
+moe_status_t moe_residual_norm_bwd(const void* dn, long long lddn, const void* dr, long long lddr, const void* r,
+                                   long long ldr, int x_dtype, const void* y, long long ldy, int y_dtype, int post,
+                                   const void* post_gamma, const void* post_beta, const void* gate, int pre,
+                                   const void* pre_gamma, int w_dtype, const float* stats, int T, int d, float res_scale,
+                                   float branch_scale, void* dx, long long lddx, void* dy, long long lddy,
+                                   float* d_post_gamma, float* d_post_beta, float* d_gate, float* d_pre_gamma,
+                                   float* d_pre_beta, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  MOE_TRACE_CALL();
+  if (T < 0 || d <= 0 || !types_ok(x_dtype, y_dtype) || !dtype_ok(w_dtype) || !norm_ok(post) || !norm_ok(pre))
+    return MOE_ERR_INVALID_ARG;
+  if ((dn && lddn < 0) || (dr && lddr < 0) || (r && ldr < 0) || (y && ldy < 0) || (dx && lddx < d) || (dy && lddy < d))
+    return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(res_scale) || !std::isfinite(branch_scale)) return MOE_ERR_INVALID_ARG;
+  if (d > MAX_WIDTH) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const bool normed = post != MOE_NORM_NONE || pre != MOE_NORM_NONE;
+  if (T > 0 && ((pre == MOE_NORM_NONE) != (dn == nullptr) || (pre != MOE_NORM_NONE && !r) || (normed && !stats) ||
+                (y == nullptr) != (dy == nullptr) || (!y && (post != MOE_NORM_NONE || gate)) || (!dn && !dr) || (!dx && !dy)))
+    return MOE_ERR_INVALID_ARG;
+  if ((post == MOE_NORM_NONE && (post_gamma || d_post_gamma || d_post_beta)) || (post != MOE_NORM_LAYER && post_beta) ||
+      (pre == MOE_NORM_NONE && (pre_gamma || d_pre_gamma || d_pre_beta)) || (T > 0 && !y && d_gate))
+    return MOE_ERR_INVALID_ARG;
+  const int ex = dtype_bytes(x_dtype), ey = dtype_bytes(y_dtype), ew = dtype_bytes(w_dtype);
+  if (!element_aligned(dr, ex) || !element_aligned(r, ex) || !element_aligned(dx, ex) || !element_aligned(dn, ey) ||
+      !element_aligned(y, ey) || !element_aligned(dy, ey) || !element_aligned(post_gamma, ew) ||
+      !element_aligned(post_beta, ew) || !element_aligned(gate, ew) || !element_aligned(pre_gamma, ew) ||
+      !element_aligned(stats, 4) || !element_aligned(d_post_gamma, 4) || !element_aligned(d_post_beta, 4) ||
+      !element_aligned(d_gate, 4) || !element_aligned(d_pre_gamma, 4) || !element_aligned(d_pre_beta, 4) ||
+      !element_aligned(ws, 4))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (ws_bytes < residual_norm_bwd_workspace_bytes(T, d)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (!ws) return MOE_ERR_INVALID_ARG;
+  }
+  moe_status_t st = check_device();
+  if (st != MOE_OK) return st;
+  const GradOut o{d_post_gamma, d_post_beta, d_gate, d_pre_gamma, d_pre_beta};
+  const bool wgrad = d_post_gamma || d_post_beta || d_gate || d_pre_gamma || d_pre_beta;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  JoinArgs a{};
+  a.dn = dn;
+  a.dr = dr;
+  a.r = const_cast<void*>(r);
+  a.y = y;
+  a.dx = dx;
+  a.dy = dy;
+  a.lddn = lddn;
+  a.lddr = lddr;
+  a.ldr = ldr;
+  a.ldy = ldy;
+  a.lddx = lddx;
+  a.lddy = lddy;
+  a.g1 = post_gamma;
+  a.b1 = post_beta;
+  a.gate = gate;
+  a.g2 = pre_gamma;
+  a.w_bf16 = w_dtype == MOE_DTYPE_BF16;
+  a.post = post;
+  a.pre = pre;
+  a.T = T;
+  a.d = d;
+  a.alpha = res_scale;
+  a.beta = branch_scale;
+  a.stats = const_cast<float*>(stats);
+  a.part = wgrad && T > 0 ? static_cast<float*>(ws) : nullptr;
+  a.row = static_cast<float*>(ws) + (T > 0 ? part_floats(T, d) : 0);
+  int blocks = 0;
+  if (T > 0) {
+    const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_bwd<bf16, bf16>(a, s, blocks)
+                            : y_dtype == MOE_DTYPE_BF16 ? launch_bwd<float, bf16>(a, s, blocks)
+                                                        : launch_bwd<float, float>(a, s, blocks);
+    if (err != cudaSuccess) return cuda_fail(err);
+  }
+  if (!wgrad) return MOE_OK;
+  const cudaError_t err = launch_dependent(join_partials_kernel, (d + 31) / 32, 1024, 0, s, a, blocks, o);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
+}
+
+}  // extern "C"

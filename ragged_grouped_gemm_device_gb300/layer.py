@@ -162,3 +162,86 @@ class Mxfp4ExpertLayer:
                                           self.fwd_ws, self.status, stream)
         _lib.moe_unpermute_combine(self.y, self.inv_map, weights, T, k, d, self.out, stream)
         return self.out
+
+
+class Int4ExpertLayer:
+    """The forward of one SwiGLU expert layer on 4-bit integer weights with group scales and bf16 activations, for few
+    tokens (decoding; no backward).
+
+    Takes the bf16 weights of ExpertLayer and quantizes them once (the bf16 tensors are not kept), or, through
+    from_checkpoint, codes, scales and zero points. Any d and h. More than 4096 token slots run in pieces that
+    each read the weights: long prompts are Mxfp4ExpertLayer's and ExpertLayer's."""
+
+    def __init__(self, w_ug: torch.Tensor, w_down: torch.Tensor, group: int = 128, stream=None):
+        E, two_h, d = w_ug.shape
+        h = two_h // 2
+        assert w_down.shape == (E, h, d) and two_h == 2 * h
+        assert w_ug.dtype == torch.bfloat16 and w_down.dtype == torch.bfloat16
+        with _on(stream):
+            # contractions along d and along h: rows of W_down^T
+            parts = [self._quantize(w, group, stream) for w in (_dense(w_ug), w_down.transpose(1, 2).contiguous())]
+        self._pack(E, d, h, group, parts, stream)
+
+    @classmethod
+    def from_checkpoint(cls, ug, down, E: int, d: int, h: int, group: int, stream=None):
+        """ug, down: (codes uint8 [..., ceil(K / 2)], scales bf16 [..., groups], zeros uint8 [..., groups] or None) of
+        W_ug [E, 2h, d] along d and of W_down^T [E, d, h] along h."""
+        self = cls.__new__(cls)
+        with _on(stream):
+            parts = [tuple(None if t is None else _dense(t) for t in part) for part in (ug, down)]
+        self._pack(E, d, h, group, parts, stream)
+        return self
+
+    @staticmethod
+    def _quantize(w, group, stream):
+        K, rows, dev = w.shape[-1], w.numel() // w.shape[-1], w.device
+        groups = (K + group - 1) // group
+        codes = torch.empty(rows, (K + 1) // 2, dtype=torch.uint8, device=dev)
+        scales = torch.empty(rows, groups, dtype=torch.bfloat16, device=dev)
+        zeros = torch.empty(rows, groups, dtype=torch.uint8, device=dev)
+        _lib.moe_w4_quantize_rows(w, rows, K, group, codes, scales, zeros, stream)
+        return codes, scales, zeros
+
+    def _pack(self, E, d, h, group, parts, stream):
+        self.E, self.d, self.h, self.group = E, d, h, group
+        self.device = parts[0][0].device
+        packed = []
+        with _on(stream):
+            for (codes, scales, zeros), (matrices, N, K) in zip(parts, ((2 * E, h, d), (E, d, h))):
+                n = _lib.moe_workspace_bytes(_lib.OP_W4_WEIGHTS, 0, 1, matrices, K, N, group)
+                w = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+                _lib.moe_w4_pack(codes, scales, zeros, matrices, N, K, group, w, stream)
+                packed.append(w)
+        self.w_ug, self.w_down = packed
+        self._key = None
+
+    def _buffers(self, T: int, k: int):
+        if self._key == (T, k):
+            return
+        piece = min(T, _lib.W4_MAX_SLOTS // k)
+        n = _lib.moe_workspace_bytes(_lib.OP_W4_DECODE, piece, k, self.E, self.d, self.h)
+        self.ws = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
+        self.out = torch.empty(T, self.d, dtype=torch.bfloat16, device=self.device)
+        self._key = (T, k)
+
+    def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, stream=None):
+        """x [T, d] bf16 (any row pitch), ids [T, k] int32, weights [T, k] fp32 -> out [T, d] bf16."""
+        if ids.dim() != 2 or ids.dtype != torch.int32:
+            raise ValueError("ids has to be [T, k] int32")
+        T, k = ids.shape
+        if not 1 <= k <= 32:
+            raise ValueError("k has to be 1 to 32")
+        if tuple(x.shape) != (T, self.d) or x.dtype != torch.bfloat16:
+            raise ValueError(f"x has to be [{T}, {self.d}] bfloat16")
+        if tuple(weights.shape) != (T, k) or weights.dtype != torch.float32:
+            raise ValueError(f"weights has to be [{T}, {k}] float32")
+        with _on(stream):
+            ids, weights = _dense(ids), _dense(weights)
+            x = x if x.stride(1) == 1 else _dense(x)
+            self._buffers(T, k)
+        piece = _lib.W4_MAX_SLOTS // k
+        for t in range(0, T, piece):
+            n = min(piece, T - t)
+            _lib.moe_w4_swiglu_decode(x[t:t + n], ids[t:t + n], weights[t:t + n], n, k, self.E, self.d, self.h, self.group,
+                                      self.w_ug, self.w_down, self.out[t:t + n], self.ws, stream)
+        return self.out
