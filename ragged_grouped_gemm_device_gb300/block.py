@@ -11,6 +11,13 @@ the rounded sum of x and the rounded expert rows; in the backward the experts' g
 then its sum with the router's, then the layer norm's dx, then dx + dout. Buffers are allocated once per shape and reused, so what forward() and
 backward() return is overwritten by the next call. The calls record no autograd history (what they return
 requires no gradient); the gradients are backward()'s.
+
+A block may have another kind of norm in front, a norm behind it, a gate for each channel and scales:
+
+    n = pre(x);  y = sum_j weights[:, j] expert[ids[:, j]](n);  out = res_scale x + branch_scale gate post(y)
+
+and a MoEStack runs several such blocks, the join behind one and the norm in front of the next in one pass. There the
+residual additions are in fp32 and rounded once.
 """
 from __future__ import annotations
 
@@ -19,6 +26,8 @@ import torch
 from . import _lib
 from .layer import ExpertLayer, _dense
 
+_NORMS = {"none": _lib.NORM_NONE, "layer": _lib.NORM_LAYER, "rms": _lib.NORM_RMS}
+
 
 def _version(t: torch.Tensor):
     """The count of in-place changes that torch keeps of a tensor (None for an inference tensor, which has none)."""
@@ -26,19 +35,32 @@ def _version(t: torch.Tensor):
 
 
 class MoEBlock:
-    """gamma, beta [d] (fp32 or bf16), w_router [E, d] fp32, experts over E experts of width d."""
+    """gamma, beta [d] (fp32 or bf16; beta None with an RMS norm), w_router [E, d] fp32, experts over E experts of width d.
+    pre: "layer" or "rms"; post: "none", "layer" or "rms", with post_gamma and post_beta [d] (each nullable); gate
+    nullable [d]. All norm weights and the gate are of one type."""
 
     def __init__(self, gamma: torch.Tensor, beta: torch.Tensor, w_router: torch.Tensor, experts, top_k: int,
-                 renorm: bool = True, eps: float = 1e-5):
+                 renorm: bool = True, eps: float = 1e-5, *, pre: str = "layer", post: str = "none",
+                 post_gamma: torch.Tensor = None, post_beta: torch.Tensor = None, gate: torch.Tensor = None,
+                 res_scale: float = 1.0, branch_scale: float = 1.0):
         E, d = w_router.shape
         assert w_router.dtype == torch.float32 and (E, d) == (experts.E, experts.d)
-        assert gamma.shape == (d,) and beta.shape == (d,) and 1 <= top_k <= min(E, 32)
+        assert gamma.shape == (d,) and 1 <= top_k <= min(E, 32)
+        assert pre in ("layer", "rms") and post in _NORMS
+        assert (beta is None) if pre == "rms" else beta.shape == (d,)
+        assert post != "none" or post_gamma is None
+        assert post == "layer" or post_beta is None
+        assert all(t is None or t.shape == (d,) for t in (post_gamma, post_beta, gate))
         # as given, views too: a dense copy made here would not follow an optimizer's updates
         self.gamma, self.beta, self.w_router = gamma, beta, w_router
+        self.post_gamma, self.post_beta, self.gate = post_gamma, post_beta, gate
+        self.pre, self.post, self.res_scale, self.branch_scale = pre, post, res_scale, branch_scale
+        self.plain = pre == "layer" and post == "none" and gate is None and res_scale == 1.0 and branch_scale == 1.0
         self.experts, self.E, self.d, self.k, self.eps = experts, E, d, top_k, eps
         self.flags = _lib.GATE_RENORM if renorm else 0
         self.device = w_router.device
         self._T = None
+        self._alone = None if self.plain else MoEStack([self])
 
     def _buffers(self, T: int):
         if self._T == T:
@@ -61,37 +83,161 @@ class MoEBlock:
         (False) are routed nowhere, count in no loss and pass through the residual unchanged. `loss`
         holds the balance and the z loss, `counts` the slots per expert. x, gamma and w_router are not copied:
         backward() reads them again and refuses when one was changed in place since."""
-        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16 or x.device != self.device:
-            raise ValueError(f"x has to be [T, {self.d}] bfloat16 on {self.device}")
-        T = x.shape[0]
-        if token_mask is not None and tuple(token_mask.shape) != (T,):
-            raise ValueError(f"token_mask has to be [{T}]")
+        if not self.plain:
+            return self._alone.forward(x, token_mask)
+        T = self._check(x, token_mask)
         self._buffers(T)
         self.x = x  # read again by backward(), like gamma and w_router
         self._read = [(t, _version(t)) for t in (x, self.gamma, self.w_router)]
         _lib.moe_layer_norm_fwd(x, _dense(self.gamma), _dense(self.beta), T, self.d, self.eps, self.normed, self.mean, self.rstd)
+        return x + self._route(token_mask)
+
+    def _check(self, x, token_mask) -> int:
+        if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16 or x.device != self.device:
+            raise ValueError(f"x has to be [T, {self.d}] bfloat16 on {self.device}")
+        if token_mask is not None and tuple(token_mask.shape) != (x.shape[0],):
+            raise ValueError(f"token_mask has to be [{x.shape[0]}]")
+        return x.shape[0]
+
+    def _route(self, token_mask):
+        """The experts' combined rows of self.normed."""
+        T = self._T
         torch.mm(self.normed.float(), self.w_router.t(), out=self.logits)
         _lib.moe_gate_fwd(self.logits, token_mask, T, self.k, self.E, self.flags, self.ids, self.weights, self.lse,
                           self.counts, self.n_valid, self.prob_sum, self.loss, self.gate_ws)
-        return x + self.experts.forward(self.normed, self.ids, self.weights)
+        return self.experts.forward(self.normed, self.ids, self.weights)
+
+    def _route_backward(self, dy, d_loss) -> dict:
+        """The gradient of self.normed, left in self.dnormed, and those of the router's and the experts' weights."""
+        dn, dw_ug, dw_down, dweights = self.experts.backward(dy)
+        _lib.moe_gate_bwd(self.logits, self.lse, self.ids, self.weights, self.counts, self.n_valid, dweights, d_loss, self._T,
+                          self.k, self.E, self.flags, self.dlogits)
+        dw_router = torch.mm(self.dlogits.t(), self.normed.float())
+        self.dnormed.copy_(torch.addmm(dn.float(), self.dlogits, self.w_router))
+        return dict(w_router=dw_router, w_ug=dw_ug, w_down=dw_down)
 
     @torch.no_grad()
     def backward(self, dout: torch.Tensor, d_loss: torch.Tensor = None) -> dict:
         """dout [T, d] bf16, d_loss nullable [2] fp32 (the gradients of the two losses) -> the gradients
         dx (bf16), gamma, beta, w_router, w_ug, w_down (fp32) of the last forward."""
+        if not self.plain:
+            grads = self._alone.backward(dout, None if d_loss is None else [d_loss])
+            return dict(dx=grads["dx"], **grads["blocks"][0])
+        self._check_backward(dout)
+        T = self._T
+        dout = _dense(dout)
+        grads = self._route_backward(dout, d_loss)
+        _lib.moe_layer_norm_bwd(self.dnormed, self.x, _dense(self.gamma), self.mean, self.rstd, T, self.d, self.dx, self.dgamma,
+                                self.dbeta, self.norm_ws)
+        return dict(dx=self.dx + dout, gamma=self.dgamma, beta=self.dbeta, **grads)
+
+    def _check_backward(self, dout):
         if not isinstance(self.experts, ExpertLayer):
             raise TypeError("4-bit experts have no backward: train on an ExpertLayer")
         if any(_version(t) != v for t, v in self._read):
             raise RuntimeError("x, gamma or w_router was changed in place since forward(): their gradients would be wrong")
-        T = self._T
-        if tuple(dout.shape) != (T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:
-            raise ValueError(f"dout has to be [{T}, {self.d}] bfloat16 on {self.device}")
-        dout = _dense(dout)
-        dn, dw_ug, dw_down, dweights = self.experts.backward(dout)
-        _lib.moe_gate_bwd(self.logits, self.lse, self.ids, self.weights, self.counts, self.n_valid, dweights, d_loss, T,
-                          self.k, self.E, self.flags, self.dlogits)
-        dw_router = torch.mm(self.dlogits.t(), self.normed.float())
-        self.dnormed.copy_(torch.addmm(dn.float(), self.dlogits, self.w_router))
-        _lib.moe_layer_norm_bwd(self.dnormed, self.x, _dense(self.gamma), self.mean, self.rstd, T, self.d, self.dx, self.dgamma,
-                                self.dbeta, self.norm_ws)
-        return dict(dx=self.dx + dout, gamma=self.dgamma, beta=self.dbeta, w_router=dw_router, w_ug=dw_ug, w_down=dw_down)
+        if tuple(dout.shape) != (self._T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:
+            raise ValueError(f"dout has to be [{self._T}, {self.d}] bfloat16 on {self.device}")
+
+    def tensors(self) -> dict:
+        """The block's trained tensors, by the names of their gradients."""
+        every = dict(gamma=self.gamma, beta=self.beta, post_gamma=self.post_gamma, post_beta=self.post_beta, gate=self.gate,
+                     w_router=self.w_router)
+        if isinstance(self.experts, ExpertLayer):
+            every.update(w_ug=self.experts.w_ug, w_down=self.experts.w_down)
+        return {n: t for n, t in every.items() if t is not None}
+
+
+class MoEStack:
+    """Blocks of one width, one behind the other: the norm behind a block, its gate and scales, the residual addition and the
+    norm in front of the next block are one call. Every block has experts of its own."""
+
+    def __init__(self, blocks):
+        self.blocks = list(blocks)
+        if not self.blocks:
+            raise ValueError("there are no blocks")
+        first = self.blocks[0]
+        if any((b.d, b.device) != (first.d, first.device) for b in self.blocks):
+            raise ValueError("the blocks have to be of one width and on one device")
+        if len({id(b.experts) for b in self.blocks}) < len(self.blocks) or len({id(b) for b in self.blocks}) < len(self.blocks):
+            raise ValueError("every block has to have experts of its own: their buffers hold what the backward reads")
+        self.d, self._T = first.d, None
+
+    def _buffers(self, T: int):
+        for b in self.blocks:
+            b._buffers(T)
+        if self._T == T:
+            return
+        d, dev, count = self.d, self.blocks[0].device, len(self.blocks)
+        new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
+        self.rows = new(count, T, d, dtype=torch.bfloat16)       # r behind each block
+        self.stats = new(count + 1, 4, T)                        # of join i, the one in front of block i
+        self.dx, self.dy = new(T, d, dtype=torch.bfloat16), new(T, d, dtype=torch.bfloat16)
+        self.ws = new(max(1, _lib.moe_workspace_bytes(_lib.OP_RESIDUAL_NORM_BWD, T, 1, 1, d)), dtype=torch.uint8)
+        self._T = T
+
+    def _join(self, i):
+        """The weights of join i, between blocks i - 1 and i: (post, gamma, beta, gate, pre, gamma, beta), then eps and scales."""
+        behind = self.blocks[i - 1] if i > 0 else None
+        ahead = self.blocks[i] if i < len(self.blocks) else None
+        dense = lambda b, n: None if b is None or getattr(b, n) is None else _dense(getattr(b, n))  # noqa: E731
+        weights = (_NORMS[behind.post] if behind else _lib.NORM_NONE, dense(behind, "post_gamma"), dense(behind, "post_beta"),
+                   dense(behind, "gate"), _NORMS[ahead.pre] if ahead else _lib.NORM_NONE, dense(ahead, "gamma"), dense(ahead, "beta"))
+        return weights, (ahead or behind).eps, (behind.res_scale, behind.branch_scale) if behind else (1.0, 1.0)
+
+    @torch.no_grad()
+    def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
+        """x [T, d] bf16 (any row pitch) -> out [T, d] bf16, a buffer that the next forward overwrites. The blocks hold
+        their losses and counts. x and the weights are not copied: backward() reads them again and refuses when one was changed
+        in place since."""
+        T = self.blocks[0]._check(x, token_mask)
+        self._buffers(T)
+        r, y = x, None
+        self._ys = []
+        for i in range(len(self.blocks) + 1):
+            weights, eps, scales = self._join(i)
+            n = self.blocks[i].normed if i < len(self.blocks) else None
+            to = self.rows[i - 1] if i > 0 else None
+            _lib.moe_residual_norm_fwd(r, y, *weights, T, self.d, eps, *scales, to, n, self.stats[i])
+            if i > 0:
+                r = to
+            if n is not None:
+                y = self.blocks[i]._route(token_mask)
+                self._ys.append(y)
+        self.x = x
+        for b in self.blocks:
+            b._read = [(t, _version(t)) for n, t in b.tensors().items() if n not in ("w_ug", "w_down")]
+        self.blocks[0]._read.append((x, _version(x)))
+        return r
+
+    @torch.no_grad()
+    def backward(self, dout: torch.Tensor, d_loss=None) -> dict:
+        """dout [T, d] bf16, d_loss: None or for each block None or [2] fp32 -> dx (bf16) and blocks, a list of each
+        block's gradients by the names of its tensors()."""
+        if self._T is None:
+            raise RuntimeError("backward() before forward()")
+        for b in self.blocks:
+            b._check_backward(dout)
+        count, T = len(self.blocks), self._T
+        losses = [None] * count if d_loss is None else list(d_loss)
+        if len(losses) != count:
+            raise ValueError("d_loss has to have one entry for each block")
+        grads = [{} for _ in self.blocks]
+        new = lambda: torch.empty(self.d, dtype=torch.float32, device=dout.device)  # noqa: E731
+        dr, dn = _dense(dout), None
+        for i in range(count, -1, -1):
+            weights, _, scales = self._join(i)
+            out = [None] * 5   # d_post_gamma, d_post_beta, d_gate, d_pre_gamma, d_pre_beta
+            for j, (w, owner, name) in enumerate(zip(weights[1:4] + weights[5:], (i - 1,) * 3 + (i,) * 2,
+                                                     ("post_gamma", "post_beta", "gate", "gamma", "beta"))):
+                if w is not None:
+                    out[j] = grads[owner][name] = new()
+            r = None if dn is None else self.rows[i - 1] if i > 0 else self.x
+            y, dy = (self._ys[i - 1], self.dy) if i > 0 else (None, None)
+            _lib.moe_residual_norm_bwd(dn, dr, r, y, *weights[:5], weights[5], self.stats[i], T, self.d, *scales, self.dx, dy,
+                                       *out, self.ws)
+            dr = self.dx
+            if i > 0:
+                grads[i - 1].update(self.blocks[i - 1]._route_backward(self.dy, losses[i - 1]))
+                dn = self.blocks[i - 1].dnormed
+        return dict(dx=self.dx, blocks=grads)
