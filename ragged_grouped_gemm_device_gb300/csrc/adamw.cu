@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ 
       float r[VB];
 #pragma unroll
       for (int i = 0; i < VB; ++i) {
+        // Each operation rounded by itself: a stochastic rounding goes the other way where its argument differs in the last
+        // place, and m and v are to be what the formula written out gives.
         const float gc = g[i] * c;
-        m[i] = fmaf(a.b1, m[i], a.omb1 * gc);
-        v[i] = fmaf(a.b2, v[i], a.omb2 * gc * gc);
+        m[i] = __fadd_rn(__fmul_rn(a.b1, m[i]), __fmul_rn(a.omb1, gc));
+        v[i] = __fadd_rn(__fmul_rn(a.b2, v[i]), __fmul_rn(__fmul_rn(a.omb2, gc), gc));
         r[i] = sqrtf(v[i]);
         p[i] = fmaf(p[i], keep, -(step * m[i]) / fmaf(r[i], root, a.eps));
       }

@@ -145,67 +145,375 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
 }
 
 // ------------------------------------------------------------------ products
-// Row `row` of matrix m times x [K], by one warp: a lane takes eight elements at a time.
-__device__ __forceinline__ float dot(const Packed& p, int m, int row, const bf16* x, int K) {
-  const int lane = threadIdx.x & 31, r = row & 15;
-  const size_t piece0 = (static_cast<size_t>(m) * p.tiles + (row >> 4)) * p.chunks;
-  float sum = 0.f;
-  for (int i = lane; i < p.chunks * 16; i += 32) {
-    const size_t piece = piece0 + (i >> 4);
-    const int q = (i >> 2) & 3, t = i & 3, k0 = (i >> 4) * 128 + q * 32 + t * 8;
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(p.codes + piece * 1024 + (r >> 3) * 512 + ((r & 7) * 4 + t) * 16 + q * 4));
-    const size_t at = (piece * 8 + (r & 7)) * p.per + (q * p.per >> 2);
-    const uint32_t pair = __ldg(reinterpret_cast<const uint32_t*>(p.scales) + at);
-    const float s = r < 8 ? bf16_lo(pair) : bf16_hi(pair);
-    const int z = (p.zeros[at] >> (r < 8 ? 0 : 4)) & 15;
-    float part = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = static_cast<int>((w >> (4 * ((j >> 1) + 4 * (j & 1)))) & 15u) - z;
-      if (k0 + j < K) part = fmaf(static_cast<float>(c), __bfloat162float(x[k0 + j]), part);
+// D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// This lane's part of a piece: the codes of rows g and g + 8, its groups' scales (a pair of rows in a word) and zero points.
+template <int PER>
+struct Piece {
+  uint4 lo, hi;
+  uint32_t s[PER], z;
+  __device__ __forceinline__ void load(const Packed& p, size_t piece, int lane) {
+    const uint4* c = reinterpret_cast<const uint4*>(p.codes + piece * 1024) + lane;
+    lo = __ldg(c);
+    hi = __ldg(c + 32);
+    const size_t at = (piece * 8 + (lane >> 2)) * PER;
+    if constexpr (PER == 4) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p.scales + at * 4));
+      s[0] = q.x, s[1] = q.y, s[2] = q.z, s[3] = q.w;
+      z = __ldg(reinterpret_cast<const uint32_t*>(p.zeros + at));
+    } else if constexpr (PER == 2) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.scales + at * 4));
+      s[0] = q.x, s[1] = q.y;
+      z = __ldg(reinterpret_cast<const uint16_t*>(p.zeros + at));
+    } else {
+      s[0] = __ldg(reinterpret_cast<const uint32_t*>(p.scales + at * 4));
+      z = __ldg(p.zeros + at);
     }
-    sum = fmaf(s, part, sum);
   }
-  return warp_sum(sum);
-}
+};
 
-template <typename T>
-__global__ void __launch_bounds__(256) w4_matvec_kernel(const bf16* x, long long ldx, const int32_t* ids, int top_k,
-                                                        int matrices, int N, int K, const Packed w, T* y, long long ldy) {
-  grid_wait();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), s = blockIdx.y;
-  if (row >= N) return;
-  const int m = ids ? after_wait(ids)[s] : 0;
-  float v[1] = {0.f};
-  if (m >= 0 && m < matrices) v[0] = dot(w, m, row, after_wait(x) + (s / top_k) * ldx, K);
-  if ((threadIdx.x & 31) == 0) Chunk<T, 1>::store(y + s * ldy + row, v);
-}
+__device__ __forceinline__ uint32_t word(const uint4& v, int q) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; }
 
-__global__ void __launch_bounds__(256) w4_up_kernel(const bf16* x, long long ldx, const int32_t* ids, int top_k, int E, int d,
-                                                    int h, const Packed w, bf16* a) {
-  grid_wait();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), s = blockIdx.y;
-  const int e = after_wait(ids)[s];
-  if (row >= h || e < 0 || e >= E) return;
-  const bf16* xr = after_wait(x) + (s / top_k) * ldx;
-  const float g = dot(w, 2 * e, row, xr, d), u = dot(w, 2 * e + 1, row, xr, d);
-  if ((threadIdx.x & 31) == 0) a[static_cast<size_t>(s) * h + row] = __float2bfloat16_rn(g / (1.0f + expf(-g)) * u);
-}
-
-__global__ void __launch_bounds__(256) w4_down_kernel(const bf16* a, const int32_t* ids, const float* weights, int top_k, int E,
-                                                      int d, int h, const Packed w, bf16* out, long long ldo) {
-  grid_wait();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), t = blockIdx.y;
-  if (row >= d) return;
-  float v = 0.f;
-  for (int j = 0; j < top_k; ++j) {
-    const int s = t * top_k + j, e = after_wait(ids)[s];
-    if (e < 0 || e >= E) continue;
-    const float y = dot(w, e, row, after_wait(a) + static_cast<size_t>(s) * h, h);
-    v = fmaf(weights ? after_wait(weights)[s] : 1.0f, y, v);
+// Eight codes minus their zero point as four bf16 pairs: 128 + code is the code in the low bits of a bf16 whose last place is 1,
+// and the difference of two such numbers is exact. zz: 128 + zero, twice.
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t zz, uint32_t (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&zz));
+    p[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  if ((threadIdx.x & 31) == 0) out[t * ldo + row] = __float2bfloat16_rn(v);
 }
+
+// tot += factor scale (codes - zero) x of one piece: x by b(q, j), the 8 bf16 values of this lane for word q and column tile j.
+template <int PER, int NT, typename B>
+__device__ __forceinline__ void multiply(const Piece<PER>& w, float (&tot)[NT][4], float factor, const B& b) {
+  float acc[NT][4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    constexpr int RUN = 4 / PER;  // words of a group
+    const int j = q / RUN;
+    const uint32_t z = w.z >> (8 * j);
+    uint32_t pg[4], ph[4];
+    unpack8(word(w.lo, q), 0x43004300u + (z & 15u) * 0x00010001u, pg);
+    unpack8(word(w.hi, q), 0x43004300u + ((z >> 4) & 15u) * 0x00010001u, ph);
+    if (q % RUN == 0) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint4 v = b(q, t);
+      mma16816(acc[t], pg[0], ph[0], pg[1], ph[1], v.x, v.y);
+      mma16816(acc[t], pg[2], ph[2], pg[3], ph[3], v.z, v.w);
+    }
+    if (q % RUN == RUN - 1) {
+      const float sg = bf16_lo(w.s[j]) * factor, sh = bf16_hi(w.s[j]) * factor;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        tot[t][0] = fmaf(sg, acc[t][0], tot[t][0]);
+        tot[t][1] = fmaf(sg, acc[t][1], tot[t][1]);
+        tot[t][2] = fmaf(sh, acc[t][2], tot[t][2]);
+        tot[t][3] = fmaf(sh, acc[t][3], tot[t][3]);
+      }
+    }
+  }
+}
+
+// Eight bf16 of a row from column k: one 16-byte load, or single elements; zeros past K.
+template <bool VEC>
+__device__ __forceinline__ uint4 load_x(const bf16* row, int k, int K) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if constexpr (VEC) {
+    if (k < K) v = *reinterpret_cast<const uint4*>(row + k);
+  } else {
+    const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = k + i < K ? r[k + i] : 0;
+    v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+  }
+  return v;
+}
+
+struct W4Args {
+  const bf16* x;
+  long long ldx;
+  const int32_t* ids;      // nullable: matrix 0 for all
+  const float* weights;    // down: nullable
+  int slots, top_k, xdiv;  // slot s reads row s / xdiv of x
+  int E, N, K;
+  int segment;             // chunks of x in shared memory at a time
+  Packed w;
+  void* out;
+  long long ldo;
+  bool y_bf16;
+};
+
+constexpr int SEGMENT = 16;  // chunks of x in shared memory at most
+constexpr int WARPS = 4;
+
+// Slots of one expert times its weights: block (tile, group) owns 16 rows of the matrix (of both halves, gate and up, with
+// SWIGLU) and takes the slots of its expert 8 NT at a time. Its warps share the chunks of K and add up their sums in shared
+// memory, in warp order. A group is a slot that names its expert first (slots <= E), or an expert, with one more group for
+// dropped slots; of a single token every slot is one.
+template <int PER, int NT, bool SWIGLU, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
+  constexpr int TILES = SWIGLU ? 2 : 1, COLS = 8 * NT, U = NT == 1 ? 4 : 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint4* xs = reinterpret_cast<uint4*>(smem);                                    // [chunks of a segment * 4][COLS][4]
+  float* sums = reinterpret_cast<float*>(smem + a.segment * 4 * COLS * 64);        // [WARPS][TILES][NT][4][32]
+  int* list = reinterpret_cast<int*>(sums + WARPS * TILES * NT * 128);             // slots of this group
+  __shared__ int counts[WARPS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = blockIdx.x, group = blockIdx.y;
+  grid_wait();
+  const int32_t* ids = after_wait(a.ids);
+  const bool by_slot = a.slots <= a.E, single = a.ids == nullptr ? false : a.slots == a.top_k;
+  int e = a.ids == nullptr ? 0 : by_slot || single ? ids[group] : group;
+  const bool dropped = e < 0 || e >= a.E;
+  int n = 1;
+  if (single || (dropped && by_slot)) {
+    if (threadIdx.x == 0) list[0] = group;
+  } else if (a.ids == nullptr) {
+    n = a.slots;
+    for (int i = threadIdx.x; i < n; i += WARPS * 32) list[i] = i;
+  } else {
+    // the slots of expert e (of none of the experts: the last group) in order
+    const int seg = (a.slots + WARPS * 32 - 1) / (WARPS * 32) * 32;  // slots of a warp
+    const int i0 = warp * seg;
+    const auto mine = [&](int i) {
+      const int v = i < a.slots ? ids[i] : -1;
+      return i < a.slots && (dropped ? v < 0 || v >= a.E : v == e);
+    };
+    int count = 0;
+    for (int i = i0; i < i0 + seg; i += 32) count += __popc(__ballot_sync(0xffffffffu, mine(i + lane)));
+    if (lane == 0) counts[warp] = count;
+    __syncthreads();
+    int at = 0;
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+      at += w < warp ? counts[w] : 0;
+      n += counts[w];
+    }
+    for (int i = i0; i < i0 + seg; i += 32) {
+      const bool m = mine(i + lane);
+      const unsigned who = __ballot_sync(0xffffffffu, m);
+      if (m) list[at + __popc(who & ((1u << lane) - 1))] = i + lane;
+      at += __popc(who);
+    }
+  }
+  __syncthreads();
+  if (n == 0) return;
+  if (by_slot && !single && !dropped && a.ids != nullptr && list[0] != group) return;  // an earlier slot has this expert
+  if (dropped) {
+    if constexpr (!SWIGLU) {
+      for (int i = threadIdx.x; i < n * 16; i += WARPS * 32) {
+        const int row = tile * 16 + (i & 15);
+        if (row >= a.N) continue;
+        if (a.y_bf16) static_cast<bf16*>(a.out)[list[i >> 4] * a.ldo + row] = __float2bfloat16_rn(0.f);
+        else static_cast<float*>(a.out)[list[i >> 4] * a.ldo + row] = 0.f;
+      }
+    }
+    return;
+  }
+  const bf16* x = after_wait(a.x);
+  for (int r0 = 0; r0 < n; r0 += COLS) {
+    const int rows = min(COLS, n - r0);
+    float tot[TILES][NT][4];
+#pragma unroll
+    for (int h = 0; h < TILES; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[h][t][i] = 0.f;
+    size_t piece0[TILES];
+#pragma unroll
+    for (int h = 0; h < TILES; ++h) piece0[h] = (static_cast<size_t>(e * TILES + h) * a.w.tiles + tile) * a.w.chunks;
+    for (int seg0 = 0; seg0 < a.w.chunks; seg0 += a.segment) {
+      const int chunks = min(a.segment, a.w.chunks - seg0);
+      Piece<PER> p[U][TILES];
+      const auto load = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (c + u * WARPS < chunks) {
+#pragma unroll
+            for (int h = 0; h < TILES; ++h) p[u][h].load(a.w, piece0[h] + seg0 + c + u * WARPS, lane);
+          }
+      };
+      load(warp);  // on their way while x comes
+      __syncthreads();
+      for (int i = threadIdx.x; i < rows * chunks * 16; i += WARPS * 32) {
+        const int col = i / (chunks * 16), k8 = i % (chunks * 16);
+        const bf16* row = x + (list[r0 + col] / a.xdiv) * a.ldx;
+        xs[((k8 >> 2) * COLS + col) * 4 + (k8 & 3)] = load_x<VEC>(row, (seg0 * 16 + k8) * 8, a.K);
+      }
+      __syncthreads();
+      for (int c = warp; c < chunks; c += WARPS * U) {
+        if (c != warp) load(c);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (c + u * WARPS >= chunks) break;
+          const int s0 = (c + u * WARPS) * 4;
+          const auto b = [&](int q, int t) {
+            const int col = t * 8 + (lane >> 2);
+            return col < rows ? xs[((s0 + q) * COLS + col) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
+          };
+#pragma unroll
+          for (int h = 0; h < TILES; ++h) multiply<PER, NT>(p[u][h], tot[h], 1.0f, b);
+        }
+      }
+    }
+    // sums of the warps: [warp][half][column tile][register][lane]
+#pragma unroll
+    for (int h = 0; h < TILES; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[(((warp * TILES + h) * NT + t) * 4 + i) * 32 + lane] = tot[h][t][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * COLS; i += WARPS * 32) {
+      const int r = i & 15, col = i >> 4;  // consecutive threads: consecutive rows of the output
+      if (col >= rows) break;
+      // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + (c % 8) / 2
+      const int at = (((col >> 3) * 4) + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
+      float v[TILES];
+#pragma unroll
+      for (int h = 0; h < TILES; ++h) {
+        v[h] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) v[h] += sums[(w * TILES + h) * NT * 128 + at];
+      }
+      const int row = tile * 16 + r, slot = list[r0 + col];
+      if constexpr (SWIGLU) {
+        // rows past h up to the pitch: their scales are 0
+        if (row < a.ldo) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v[0] / (1.0f + expf(-v[0])) * v[1]);
+      } else if (row < a.N) {
+        if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v[0]);
+        else static_cast<float*>(a.out)[slot * a.ldo + row] = v[0];
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// The down product and the combine of one token: block (tile, token) owns 16 columns of out[t]. The chunks of the token's top_k
+// slots are one long contraction that its warps share, each slot's scales times its routing weight; no sums leave the block.
+constexpr int DOWN_WARPS = 8;
+
+template <int PER>
+__global__ void __launch_bounds__(DOWN_WARPS * 32) w4_down_token_kernel(const W4Args a) {
+  constexpr int U = 4;
+  __shared__ float sums[DOWN_WARPS][2][8];
+  __shared__ int expert[32];
+  __shared__ float weight[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = blockIdx.x, t = blockIdx.y;
+  grid_wait();
+  if (threadIdx.x < a.top_k) {
+    const int s = t * a.top_k + threadIdx.x;
+    const int e = after_wait(a.ids)[s];
+    expert[threadIdx.x] = e >= 0 && e < a.E ? e : -1;
+    weight[threadIdx.x] = a.weights ? after_wait(a.weights)[s] : 1.0f;
+  }
+  __syncthreads();
+  const int items = a.top_k * a.w.chunks;
+  float tot[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  const bf16* x = after_wait(a.x);
+  for (int i0 = warp; i0 < items; i0 += DOWN_WARPS * U) {
+    Piece<PER> p[U];
+    uint4 v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks, c = i % a.w.chunks;
+      if (i >= items || expert[j] < 0) continue;
+      p[u].load(a.w, (static_cast<size_t>(expert[j]) * a.w.tiles + tile) * a.w.chunks + c, lane);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[u][q] = lane < 4 ? load_x<true>(x + static_cast<size_t>(t * a.top_k + j) * a.ldx, c * 128 + q * 32 + lane * 8, a.K)
+                           : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks;
+      if (i >= items || expert[j] < 0) continue;
+      multiply<PER, 1>(p[u], tot, weight[j], [&](int q, int) { return v[u][q]; });
+    }
+  }
+  // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
+  if ((lane & 3) == 0) {
+    sums[warp][0][lane >> 2] = tot[0][0];
+    sums[warp][1][lane >> 2] = tot[0][2];
+  }
+  __syncthreads();
+  const int row = tile * 16 + threadIdx.x;
+  if (threadIdx.x < 16 && row < a.N) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < DOWN_WARPS; ++w) s += sums[w][threadIdx.x >> 3][threadIdx.x & 7];
+    static_cast<bf16*>(a.out)[t * a.ldo + row] = __float2bfloat16_rn(s);
+  }
+}
+
+// out[t] = sum_j weight[t, j] y[t, j] of fp32 rows, in slot order
+__global__ void __launch_bounds__(128) w4_combine_kernel(const float* y, long long ldy, const int32_t* ids, const float* weights,
+                                                         int top_k, int E, int d, bf16* out, long long ldo) {
+  grid_wait();
+  const int t = blockIdx.y;
+  y = after_wait(y);
+  for (int c = blockIdx.x * 128 + threadIdx.x; c < d; c += gridDim.x * 128) {
+    float v = 0.f;
+    for (int j = 0; j < top_k; ++j) {
+      const int s = t * top_k + j, e = after_wait(ids)[s];
+      if (e >= 0 && e < E) v = fmaf(weights ? after_wait(weights)[s] : 1.0f, y[s * ldy + c], v);
+    }
+    out[t * ldo + c] = __float2bfloat16_rn(v);
+  }
+}
+
+template <int PER, int NT, bool SWIGLU, bool VEC>
+cudaError_t launch_group_as(const W4Args& a, dim3 grid, cudaStream_t s) {
+  const int smem = a.segment * 4 * 8 * NT * 64 + WARPS * (SWIGLU ? 2 : 1) * NT * 512 + std::max(1, a.slots) * 4;
+  const auto kernel = w4_group_kernel<PER, NT, SWIGLU, VEC>;
+  if (smem > 48 * 1024) {
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), SEGMENT * 4 * 8 * NT * 64 + WARPS * 2 * NT * 512 + MAX_SLOTS * 4);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(kernel, grid, WARPS * 32, smem, s, a);
+}
+
+template <int PER, bool SWIGLU>
+cudaError_t launch_group(W4Args a, cudaStream_t s) {
+  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
+  a.segment = std::min(a.w.chunks, SEGMENT);
+  const int groups = a.ids == nullptr ? 1 : a.slots <= a.E ? a.slots : a.slots == a.top_k ? a.slots : a.E + (SWIGLU ? 0 : 1);
+  const dim3 grid(a.w.tiles, groups);
+  // tokens of an expert, on average: what one pass over its weights should take
+  const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
+  if (each <= 8) return vec ? launch_group_as<PER, 1, SWIGLU, true>(a, grid, s) : launch_group_as<PER, 1, SWIGLU, false>(a, grid, s);
+  return vec ? launch_group_as<PER, 2, SWIGLU, true>(a, grid, s) : launch_group_as<PER, 2, SWIGLU, false>(a, grid, s);
+}
+template <bool SWIGLU>
+cudaError_t launch_group(const W4Args& a, cudaStream_t s) {
+  return a.w.per == 4 ? launch_group<4, SWIGLU>(a, s) : a.w.per == 2 ? launch_group<2, SWIGLU>(a, s) : launch_group<1, SWIGLU>(a, s);
+}
+
+cudaError_t launch_down_token(const W4Args& a, int T, cudaStream_t s) {
+  const dim3 grid(a.w.tiles, T);
+  const auto kernel = a.w.per == 4 ? w4_down_token_kernel<4> : a.w.per == 2 ? w4_down_token_kernel<2> : w4_down_token_kernel<1>;
+  return launch_dependent(kernel, grid, DOWN_WARPS * 32, 0, s, a);
+}
+
+// Whether the down product takes token by token. It then reads an expert's weights once for each slot, from the L2 but the
+// first time, and saves the fp32 rows and a launch.
+bool down_by_token(long long slots, int E) { return slots <= 2LL * E; }
+int pitch_of(int h) { return (h + 7) / 8 * 8; }
 
 bool dim_ok(int v) { return v >= 1 && v <= MAX_DIM; }
 
@@ -218,7 +526,8 @@ size_t w4_weights_bytes(int matrices, int K, int N, int group) {
 }
 size_t w4_decode_workspace_bytes(long long slots, int E, int d, int h) {
   if (slots < 0 || slots > MAX_SLOTS || !dim_ok(d) || !dim_ok(h)) return 0;
-  return round256(static_cast<size_t>(slots) * h * 2);
+  // SwiGLU's rows, and the fp32 rows of the down product where it does not take token by token
+  return round256(static_cast<size_t>(slots) * pitch_of(h) * 2) + (down_by_token(slots, E) ? 0 : static_cast<size_t>(slots) * d * 4);
 }
 
 }  // namespace moe
@@ -275,14 +584,21 @@ moe_status_t moe_w4_matvec(const moe_bf16* x, long long ldx, const int32_t* ids,
     return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_device();
   if (st != MOE_OK || T == 0) return st;
-  const Packed w = packed_at(packed, matrices, N, K, group);
-  const bf16* xb = reinterpret_cast<const bf16*>(x);
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((N + 7) / 8, T * top_k);
-  const cudaError_t err =
-      y_dtype == MOE_DTYPE_BF16
-          ? launch_dependent(w4_matvec_kernel<bf16>, grid, 256, 0, s, xb, ldx, ids, top_k, matrices, N, K, w, static_cast<bf16*>(y), ldy)
-          : launch_dependent(w4_matvec_kernel<float>, grid, 256, 0, s, xb, ldx, ids, top_k, matrices, N, K, w, static_cast<float*>(y), ldy);
+  W4Args a{};
+  a.x = reinterpret_cast<const bf16*>(x);
+  a.ldx = ldx;
+  a.ids = ids;
+  a.slots = T * top_k;
+  a.top_k = top_k;
+  a.xdiv = top_k;
+  a.E = matrices;
+  a.N = N;
+  a.K = K;
+  a.w = packed_at(packed, matrices, N, K, group);
+  a.out = y;
+  a.ldo = ldy;
+  a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
+  const cudaError_t err = launch_group<false>(a, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
@@ -302,14 +618,45 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
   if (T > 0 && !ws) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_device();
   if (st != MOE_OK || T == 0) return st;
-  const Packed ug = packed_at(w_ug, 2 * E, h, d, group), dn = packed_at(w_down, E, d, h, group);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  bf16* a = static_cast<bf16*>(ws);
-  cudaError_t err = launch_dependent(w4_up_kernel, dim3((h + 7) / 8, T * top_k), 256, 0, s, reinterpret_cast<const bf16*>(x), ldx,
-                                     ids, top_k, E, d, h, ug, a);
-  if (err == cudaSuccess)
-    err = launch_dependent(w4_down_kernel, dim3((d + 7) / 8, T), 256, 0, s, static_cast<const bf16*>(a), ids, weights, top_k, E, d, h,
-                           dn, reinterpret_cast<bf16*>(out), ldo);
+  const int slots = T * top_k, pitch = pitch_of(h);
+  bf16* act = static_cast<bf16*>(ws);
+  W4Args a{};
+  a.x = reinterpret_cast<const bf16*>(x);
+  a.ldx = ldx;
+  a.ids = ids;
+  a.slots = slots;
+  a.top_k = top_k;
+  a.xdiv = top_k;
+  a.E = E;
+  a.N = h;
+  a.K = d;
+  a.w = packed_at(w_ug, 2 * E, h, d, group);
+  a.out = act;
+  a.ldo = pitch;
+  cudaError_t err = launch_group<true>(a, s);
+  if (err != cudaSuccess) return cuda_fail(err);
+  W4Args b = a;
+  b.x = act;
+  b.ldx = pitch;
+  b.weights = weights;
+  b.xdiv = 1;
+  b.N = d;
+  b.K = pitch;  // zeros from h on
+  b.w = packed_at(w_down, E, d, h, group);
+  if (down_by_token(slots, E)) {
+    b.out = out;
+    b.ldo = ldo;
+    err = launch_down_token(b, T, s);
+  } else {
+    float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(static_cast<size_t>(slots) * pitch * 2));
+    b.out = y;
+    b.ldo = d;
+    err = launch_group<false>(b, s);
+    if (err == cudaSuccess)
+      err = launch_dependent(w4_combine_kernel, dim3(std::min((d + 127) / 128, 64), T), 128, 0, s, static_cast<const float*>(y),
+                             static_cast<long long>(d), ids, weights, top_k, E, d, reinterpret_cast<bf16*>(out), ldo);
+  }
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
