@@ -667,7 +667,7 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
  *   and K up to 2^20 (rows are padded to multiples of 16 with scale 0, K to multiples of 128). Layout: for
  *   (matrix, 16-row tile, 128-element chunk) in this order 1024 bytes of codes: the word of row r and elements
  *   32 q + 8 t ..+7 at byte (r / 8) 512 + ((r % 8) 4 + t) 16 + 4 q, elements 0 2 4 6 1 3 5 7 from its lowest four
- *   bits up; then (256-byte aligned) 32 * 128 / group bytes of scales each: rows r and r + 8 of group j as a pair
+ *   bits up and the word then rotated left by 3 bits; then (256-byte aligned) 32 * 128 / group bytes of scales each: rows r and r + 8 of group j as a pair
  *   of bf16 at ((r % 8) 128 / group + j) 4; then 8 * 128 / group bytes of zero points each, likewise, row r in
  *   the low half of a byte.
  * moe_w4_matvec -- y[s] = W[ids[s]] x[s / top_k] for every slot s < T * top_k: x [T, K] bf16 (rows ldx apart, 0: one

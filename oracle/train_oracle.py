@@ -189,6 +189,7 @@ def pack4(codes, scales_bits, zeros, group):
                                     continue
                                 c = int(codes[m, row, k]) if k < K else int(zeros[m, row, first // group])
                                 word |= c << (4 * nib)
+                            word = (word << 3 | word >> 29) & 0xFFFFFFFF
                             at = i * 1024 + (r // 8) * 512 + ((r % 8) * 4 + t) * 16 + 4 * q
                             out[at:at + 4] = np.frombuffer(np.uint32(word).tobytes(), np.uint8)
                     for j in range(per):

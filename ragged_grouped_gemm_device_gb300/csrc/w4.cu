@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
             const uint32_t c = k0 + j < K ? (src[j / 2] >> (4 * (j & 1))) & 15u : z;
             w[q] |= c << (4 * ((j >> 1) + 4 * (j & 1)));
           }
+          w[q] = __funnelshift_l(w[q], w[q], 3);
         }
       }
       *reinterpret_cast<uint4*>(const_cast<uint8_t*>(p.codes) + i * 1024 + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -179,35 +180,46 @@ struct Piece {
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int q) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; }
 
-// Eight codes minus their zero point as four bf16 pairs: 128 + code is the code in the low bits of a bf16 whose last place is 1,
-// and the difference of two such numbers is exact. zz: 128 + zero, twice.
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t zz, uint32_t (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t c = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&c), *reinterpret_cast<const __nv_bfloat162*>(&zz));
-    p[i] = *reinterpret_cast<const uint32_t*>(&v);
-  }
+// Eight codes as four bf16 pairs of 16 + code: the code in the upper four mantissa bits of a bf16 in [16, 32).
+__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4]) {
+  p[0] = (w & 0x00780078u) | 0x41804180u;
+  p[1] = ((w >> 4) & 0x00780078u) | 0x41804180u;
+  p[2] = ((w >> 8) & 0x00780078u) | 0x41804180u;
+  p[3] = (__funnelshift_r(w, w, 12) & 0x00780078u) | 0x41804180u;
 }
 
-// tot += factor scale (codes - zero) x of one piece: x by b(q, j), the 8 bf16 values of this lane for word q and column tile j.
-template <int PER, int NT, typename B>
-__device__ __forceinline__ void multiply(const Piece<PER>& w, float (&tot)[NT][4], float factor, const B& b) {
+// tot += factor scale (codes - zero) x of one piece. b(q, t): the 8 bf16 values of x of this lane for word q and column tile t; nx(q, t):
+// minus the sums of x over the 32 elements of word q, of this lane's two columns. A group's sum starts at -(16 + zero) sum x, which
+// takes the codes' 16 and the zero point away without an instruction for each pair of codes: terms of up to 31 |x| instead of
+// 15 |x| in an fp32 sum.
+template <int PER, int NT, typename B, typename X>
+__device__ __forceinline__ void multiply(const Piece<PER>& w, float (&tot)[NT][4], float factor, const B& b, const X& nx) {
+  constexpr int RUN = 4 / PER;  // words of a group
   float acc[NT][4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    constexpr int RUN = 4 / PER;  // words of a group
     const int j = q / RUN;
-    const uint32_t z = w.z >> (8 * j);
-    uint32_t pg[4], ph[4];
-    unpack8(word(w.lo, q), 0x43004300u + (z & 15u) * 0x00010001u, pg);
-    unpack8(word(w.hi, q), 0x43004300u + ((z >> 4) & 15u) * 0x00010001u, ph);
     if (q % RUN == 0) {
+      const float zg = __uint_as_float(0x41800000u | ((j < 3 ? w.z << (19 - 8 * j > 0 ? 19 - 8 * j : 0) : w.z >> 5) & 0x00780000u));
+      const float zh = __uint_as_float(0x41800000u | ((j < 2 ? w.z << (15 - 8 * j > 0 ? 15 - 8 * j : 0) : w.z >> (8 * j - 15)) & 0x00780000u));
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        float2 v = nx(q, t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = 0.f;
+        for (int r = 1; r < RUN; ++r) {
+          const float2 u = nx(q + r, t);
+          v.x += u.x;
+          v.y += u.y;
+        }
+        acc[t][0] = zg * v.x;
+        acc[t][1] = zg * v.y;
+        acc[t][2] = zh * v.x;
+        acc[t][3] = zh * v.y;
+      }
     }
+    uint32_t pg[4], ph[4];
+    unpack8(word(w.lo, q), pg);
+    unpack8(word(w.hi, q), ph);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const uint4 v = b(q, t);
@@ -260,19 +272,22 @@ struct W4Args {
 constexpr int SEGMENT = 16;  // chunks of x in shared memory at most
 constexpr int WARPS = 4;
 
-// Slots of one expert times its weights: block (tile, group) owns 16 rows of the matrix (of both halves, gate and up, with
-// SWIGLU) and takes the slots of its expert 8 NT at a time. Its warps share the chunks of K and add up their sums in shared
+// Slots of one expert times its weights: WK warps of a block own 16 rows of the matrix (of both halves, gate and up, with
+// SWIGLU) and take the slots of its expert 8 NT at a time. They share the chunks of K and add up their sums in shared
 // memory, in warp order. A group is a slot that names its expert first (slots <= E), or an expert, with one more group for
 // dropped slots; of a single token every slot is one.
-template <int PER, int NT, bool SWIGLU, bool VEC>
-__global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
-  constexpr int TILES = SWIGLU ? 2 : 1, COLS = 8 * NT, U = NT == 1 ? 4 : 2;
+template <int PER, int NT, int WK, bool SWIGLU, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(const W4Args a) {
+  constexpr int TILES = SWIGLU ? 2 : 1, COLS = 8 * NT, U = 2, WT = WARPS / WK;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* xs = reinterpret_cast<uint4*>(smem);                                    // [chunks of a segment * 4][COLS][4]
-  float* sums = reinterpret_cast<float*>(smem + a.segment * 4 * COLS * 64);        // [WARPS][TILES][NT][4][32]
+  float* xsum = reinterpret_cast<float*>(smem + a.segment * 4 * COLS * 64);        // [chunks of a segment * 4][COLS]: minus the sums
+  float* sums = xsum + a.segment * 4 * COLS;                                       // [WARPS][TILES][NT][4][32]
   int* list = reinterpret_cast<int*>(sums + WARPS * TILES * NT * 128);             // slots of this group
   __shared__ int counts[WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = blockIdx.x, group = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = blockIdx.y;
+  const int wk = warp % WK, tile = blockIdx.x * WT + warp / WK;  // this warp's share of K and its rows
+  const bool live = tile < a.w.tiles;
   grid_wait();
   const int32_t* ids = after_wait(a.ids);
   const bool by_slot = a.slots <= a.E, single = a.ids == nullptr ? false : a.slots == a.top_k;
@@ -315,11 +330,11 @@ __global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
   if (by_slot && !single && !dropped && a.ids != nullptr && list[0] != group) return;  // an earlier slot has this expert
   if (dropped) {
     if constexpr (!SWIGLU) {
-      for (int i = threadIdx.x; i < n * 16; i += WARPS * 32) {
-        const int row = tile * 16 + (i & 15);
+      for (int i = threadIdx.x; i < n * 16 * WT; i += WARPS * 32) {
+        const int row = blockIdx.x * WT * 16 + i % (16 * WT), slot = list[i / (16 * WT)];
         if (row >= a.N) continue;
-        if (a.y_bf16) static_cast<bf16*>(a.out)[list[i >> 4] * a.ldo + row] = __float2bfloat16_rn(0.f);
-        else static_cast<float*>(a.out)[list[i >> 4] * a.ldo + row] = 0.f;
+        if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(0.f);
+        else static_cast<float*>(a.out)[slot * a.ldo + row] = 0.f;
       }
     }
     return;
@@ -343,31 +358,43 @@ __global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
       const auto load = [&](int c) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
-          if (c + u * WARPS < chunks) {
+          if (live && c + u * WK < chunks) {
 #pragma unroll
-            for (int h = 0; h < TILES; ++h) p[u][h].load(a.w, piece0[h] + seg0 + c + u * WARPS, lane);
+            for (int h = 0; h < TILES; ++h) p[u][h].load(a.w, piece0[h] + seg0 + c + u * WK, lane);
           }
       };
-      load(warp);  // on their way while x comes
+      load(wk);  // on their way while x comes
       __syncthreads();
-      for (int i = threadIdx.x; i < rows * chunks * 16; i += WARPS * 32) {
+      // Each thread eight elements, four threads the 32 of a sum; whole warps, because of the shuffles
+      const int units = rows * chunks * 16;
+      for (int i = threadIdx.x; i < (units + 31 & ~31); i += WARPS * 32) {
         const int col = i / (chunks * 16), k8 = i % (chunks * 16);
-        const bf16* row = x + (list[r0 + col] / a.xdiv) * a.ldx;
-        xs[((k8 >> 2) * COLS + col) * 4 + (k8 & 3)] = load_x<VEC>(row, (seg0 * 16 + k8) * 8, a.K);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (i < units) {
+          v = load_x<VEC>(x + (list[r0 + col] / a.xdiv) * a.ldx, (seg0 * 16 + k8) * 8, a.K);
+          xs[((k8 >> 2) * COLS + col) * 4 + (k8 & 3)] = v;
+        }
+        float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (i < units && (k8 & 3) == 0) xsum[(k8 >> 2) * COLS + col] = -sum;
       }
       __syncthreads();
-      for (int c = warp; c < chunks; c += WARPS * U) {
-        if (c != warp) load(c);
+      for (int c = wk; live && c < chunks; c += WK * U) {
+        if (c != wk) load(c);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (c + u * WARPS >= chunks) break;
-          const int s0 = (c + u * WARPS) * 4;
+          if (c + u * WK >= chunks) break;
+          const int s0 = (c + u * WK) * 4;
           const auto b = [&](int q, int t) {
             const int col = t * 8 + (lane >> 2);
             return col < rows ? xs[((s0 + q) * COLS + col) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
           };
+          const auto nx = [&](int q, int t) {  // columns past the last row: what lies there goes into sums that nobody reads
+            return *reinterpret_cast<const float2*>(xsum + (s0 + q) * COLS + t * 8 + 2 * (lane & 3));
+          };
 #pragma unroll
-          for (int h = 0; h < TILES; ++h) multiply<PER, NT>(p[u][h], tot[h], 1.0f, b);
+          for (int h = 0; h < TILES; ++h) multiply<PER, NT>(p[u][h], tot[h], 1.0f, b, nx);
         }
       }
     }
@@ -379,9 +406,8 @@ __global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) sums[(((warp * TILES + h) * NT + t) * 4 + i) * 32 + lane] = tot[h][t][i];
     __syncthreads();
-    for (int i = threadIdx.x; i < 16 * COLS; i += WARPS * 32) {
-      const int r = i & 15, col = i >> 4;  // consecutive threads: consecutive rows of the output
-      if (col >= rows) break;
+    for (int i = threadIdx.x; i < 16 * WT * rows; i += WARPS * 32) {
+      const int w0 = i / 16 % WT, r = i & 15, col = i / (16 * WT);  // consecutive threads: consecutive rows of the output
       // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + (c % 8) / 2
       const int at = (((col >> 3) * 4) + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
       float v[TILES];
@@ -389,9 +415,9 @@ __global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
       for (int h = 0; h < TILES; ++h) {
         v[h] = 0.f;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) v[h] += sums[(w * TILES + h) * NT * 128 + at];
+        for (int w = 0; w < WK; ++w) v[h] += sums[((w0 * WK + w) * TILES + h) * NT * 128 + at];
       }
-      const int row = tile * 16 + r, slot = list[r0 + col];
+      const int row = (blockIdx.x * WT + w0) * 16 + r, slot = list[r0 + col];
       if constexpr (SWIGLU) {
         // rows past h up to the pitch: their scales are 0
         if (row < a.ldo) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v[0] / (1.0f + expf(-v[0])) * v[1]);
@@ -409,8 +435,8 @@ __global__ void __launch_bounds__(WARPS * 32) w4_group_kernel(const W4Args a) {
 constexpr int DOWN_WARPS = 8;
 
 template <int PER>
-__global__ void __launch_bounds__(DOWN_WARPS * 32) w4_down_token_kernel(const W4Args a) {
-  constexpr int U = 4;
+__global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const W4Args a) {
+  constexpr int U = 3;
   __shared__ float sums[DOWN_WARPS][2][8];
   __shared__ int expert[32];
   __shared__ float weight[32];
@@ -443,7 +469,14 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32) w4_down_token_kernel(const W4
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
-      multiply<PER, 1>(p[u], tot, weight[j], [&](int q, int) { return v[u][q]; });
+      // the sums of x by a product with ones: column 0 of every row
+      multiply<PER, 1>(p[u], tot, weight[j], [&](int q, int) { return v[u][q]; }, [&](int q, int) {
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        constexpr uint32_t one = 0xBF80BF80u;  // -1, twice
+        mma16816(sum, one, one, one, one, v[u][q].x, v[u][q].y);
+        mma16816(sum, one, one, one, one, v[u][q].z, v[u][q].w);
+        return make_float2(sum[0], sum[1]);
+      });
     }
   }
   // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
@@ -477,27 +510,34 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const float* y, long lo
   }
 }
 
-template <int PER, int NT, bool SWIGLU, bool VEC>
-cudaError_t launch_group_as(const W4Args& a, dim3 grid, cudaStream_t s) {
-  const int smem = a.segment * 4 * 8 * NT * 64 + WARPS * (SWIGLU ? 2 : 1) * NT * 512 + std::max(1, a.slots) * 4;
-  const auto kernel = w4_group_kernel<PER, NT, SWIGLU, VEC>;
+template <int PER, int NT, int WK, bool SWIGLU, bool VEC>
+cudaError_t launch_group_as(const W4Args& a, int groups, cudaStream_t s) {
+  const int x_bytes = 4 * 8 * NT * 68, sum_bytes = WARPS * (SWIGLU ? 2 : 1) * NT * 512;
+  const auto kernel = w4_group_kernel<PER, NT, WK, SWIGLU, VEC>;
+  const int smem = a.segment * x_bytes + sum_bytes + std::max(1, a.slots) * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), SEGMENT * 4 * 8 * NT * 64 + WARPS * 2 * NT * 512 + MAX_SLOTS * 4);
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), SEGMENT * x_bytes + sum_bytes + MAX_SLOTS * 4);
     if (err != cudaSuccess) return err;
   }
-  return launch_dependent(kernel, grid, WARPS * 32, smem, s, a);
+  return launch_dependent(kernel, dim3((a.w.tiles * WK + WARPS - 1) / WARPS, groups), WARPS * 32, smem, s, a);
+}
+template <int PER, int NT, bool SWIGLU>
+cudaError_t launch_group_split(const W4Args& a, int groups, cudaStream_t s) {
+  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
+  // The warps of a block share K where that gives no more than eight blocks for each SM: few blocks leave SMs idle, many have each its
+  // share of reading ids and x.
+  const bool few = static_cast<long long>(a.w.tiles) * groups <= 8LL * device_sm_count();
+  if (few) return vec ? launch_group_as<PER, NT, 4, SWIGLU, true>(a, groups, s) : launch_group_as<PER, NT, 4, SWIGLU, false>(a, groups, s);
+  return vec ? launch_group_as<PER, NT, 1, SWIGLU, true>(a, groups, s) : launch_group_as<PER, NT, 1, SWIGLU, false>(a, groups, s);
 }
 
 template <int PER, bool SWIGLU>
 cudaError_t launch_group(W4Args a, cudaStream_t s) {
-  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
   a.segment = std::min(a.w.chunks, SEGMENT);
   const int groups = a.ids == nullptr ? 1 : a.slots <= a.E ? a.slots : a.slots == a.top_k ? a.slots : a.E + (SWIGLU ? 0 : 1);
-  const dim3 grid(a.w.tiles, groups);
   // tokens of an expert, on average: what one pass over its weights should take
   const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
-  if (each <= 8) return vec ? launch_group_as<PER, 1, SWIGLU, true>(a, grid, s) : launch_group_as<PER, 1, SWIGLU, false>(a, grid, s);
-  return vec ? launch_group_as<PER, 2, SWIGLU, true>(a, grid, s) : launch_group_as<PER, 2, SWIGLU, false>(a, grid, s);
+  return each <= 8 ? launch_group_split<PER, 1, SWIGLU>(a, groups, s) : launch_group_split<PER, 2, SWIGLU>(a, groups, s);
 }
 template <bool SWIGLU>
 cudaError_t launch_group(const W4Args& a, cudaStream_t s) {
@@ -512,7 +552,7 @@ cudaError_t launch_down_token(const W4Args& a, int T, cudaStream_t s) {
 
 // Whether the down product takes token by token. It then reads an expert's weights once for each slot, from the L2 but the
 // first time, and saves the fp32 rows and a launch.
-bool down_by_token(long long slots, int E) { return slots <= 2LL * E; }
+bool down_by_token(long long slots, int E) { return slots <= std::max(8, E / 4); }
 int pitch_of(int h) { return (h + 7) / 8 * 8; }
 
 bool dim_ok(int v) { return v >= 1 && v <= MAX_DIM; }

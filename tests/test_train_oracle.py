@@ -91,8 +91,10 @@ def test_four_bit_round_trip_and_packing():
     codes = rng.integers(0, 16, (2, 17, 130)).astype(np.uint8)
     packed = R.pack4(codes, np.ones((2, 17, 5), np.uint16), np.full((2, 17, 5), 3, np.uint8), 32)
     tiles, chunks = 2, 2
-    # matrix 1, row 16 (tile 1, row 0), element 129 (chunk 1, word 0 of quarter 0, nibble 4)
+    # matrix 1, row 16 (tile 1, row 0), chunk 1, word 0 of quarter 0, which is rotated left by 3 bits
     at = ((1 * tiles + 1) * chunks + 1) * 1024
-    assert (packed[at + 2] & 15) == codes[1, 16, 129]
+    word = int(packed[at:at + 4].view(np.uint32)[0])
+    word = word >> 3 | (word & 7) << 29
+    assert word & 15 == codes[1, 16, 128] and (word >> 16) & 15 == codes[1, 16, 129]
     # past the row's end in its last group: the zero point
-    assert (packed[at] >> 4) == 3
+    assert (word >> 4) & 15 == 3
