@@ -664,12 +664,12 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
  *   rounds to 0) gets scale 0; a group with a NaN or an infinity a NaN scale.
  * moe_w4_pack -- lay `matrices` matrices of N rows of K elements out for the products. zeros nullable (all 8).
  *   `packed`: moe_workspace_bytes(MOE_OP_W4_WEIGHTS, 0, 1, matrices, K, N, group) bytes, 256-byte aligned. Any N
- *   and K up to 2^20 (rows are padded to multiples of 16 with scale 0, K to multiples of 128). Layout: for
- *   (matrix, 16-row tile, 128-element chunk) in this order 1024 bytes of codes: the word of row r and elements
- *   32 q + 8 t ..+7 at byte (r / 8) 512 + ((r % 8) 4 + t) 16 + 4 q, elements 0 2 4 6 1 3 5 7 from its lowest four
- *   bits up and the word then rotated left by 3 bits; then (256-byte aligned) 32 * 128 / group bytes of scales each: rows r and r + 8 of group j as a pair
- *   of bf16 at ((r % 8) 128 / group + j) 4; then 8 * 128 / group bytes of zero points each, likewise, row r in
- *   the low half of a byte.
+ *   and K up to 2^20 (rows are padded to multiples of 16 with scale 0, K to multiples of 128). Layout: one piece for
+ *   (matrix, 16-row tile, 128-element chunk) in this order, of 1024 bytes of codes, the scales and the zero points of
+ *   its P = 128 / group groups, padded to a multiple of 16 bytes. Codes: the word of row r and elements 32 q + 8 t
+ *   ..+7 at byte (r / 8) 512 + ((r % 8) 4 + t) 16 + 4 q, elements 0 2 4 6 1 3 5 7 from its lowest four bits up and the
+ *   word then rotated left by 3 bits. Scales: rows r and r + 8 of group j as a pair of bf16 at 1024 + ((r % 8) P + j) 4.
+ *   Zero points: the same two at 1024 + 32 P + (r % 8) P + j, row r in the low half of the byte.
  * moe_w4_matvec -- y[s] = W[ids[s]] x[s / top_k] for every slot s < T * top_k: x [T, K] bf16 (rows ldx apart, 0: one
  *   row for all), ids [T * top_k] int32 or NULL (matrix 0 for all), y [T * top_k, N] of y_dtype (rows ldy >= N
  *   apart). A slot whose id is outside [0, matrices) gets a row of zeros.

@@ -166,15 +166,13 @@ def pack4(codes, scales_bits, zeros, group):
     element from the layout's description."""
     M, N, K = codes.shape
     tiles, chunks, per = (N + 15) // 16, (K + 127) // 128, 128 // group
-    n = M * tiles * chunks
-    r256 = lambda b: (b + 255) // 256 * 256  # noqa: E731
-    out = np.zeros(n * 1024 + r256(n * 32 * per) + r256(n * 8 * per), np.uint8)
-    sc, zo = n * 1024, n * 1024 + r256(n * 32 * per)
+    size = (1024 + 40 * per + 15) // 16 * 16
+    out = np.zeros((M * tiles * chunks * size + 255) // 256 * 256, np.uint8)
     place = [0, 2, 4, 6, 1, 3, 5, 7]   # the element whose code each nibble holds
     for m in range(M):
         for tile in range(tiles):
             for chunk in range(chunks):
-                i = (m * tiles + tile) * chunks + chunk
+                base = ((m * tiles + tile) * chunks + chunk) * size
                 for r in range(16):
                     row = tile * 16 + r
                     if row >= N:
@@ -190,15 +188,15 @@ def pack4(codes, scales_bits, zeros, group):
                                 c = int(codes[m, row, k]) if k < K else int(zeros[m, row, first // group])
                                 word |= c << (4 * nib)
                             word = (word << 3 | word >> 29) & 0xFFFFFFFF
-                            at = i * 1024 + (r // 8) * 512 + ((r % 8) * 4 + t) * 16 + 4 * q
+                            at = base + (r // 8) * 512 + ((r % 8) * 4 + t) * 16 + 4 * q
                             out[at:at + 4] = np.frombuffer(np.uint32(word).tobytes(), np.uint8)
                     for j in range(per):
                         gj = chunk * per + j
                         if gj * group >= K:
                             continue
-                        at = sc + i * 32 * per + ((r % 8) * per + j) * 4 + (r // 8) * 2
+                        at = base + 1024 + ((r % 8) * per + j) * 4 + (r // 8) * 2
                         out[at:at + 2] = np.frombuffer(np.uint16(scales_bits[m, row, gj]).tobytes(), np.uint8)
-                        out[zo + i * 8 * per + (r % 8) * per + j] |= np.uint8(int(zeros[m, row, gj]) << (4 * (r // 8)))
+                        out[base + 1024 + 32 * per + (r % 8) * per + j] |= np.uint8(int(zeros[m, row, gj]) << (4 * (r // 8)))
     return out
 
 

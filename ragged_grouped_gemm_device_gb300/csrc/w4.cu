@@ -2,8 +2,8 @@
 //
 //   matvec: y[s] = W[ids[s]] x[s / top_k];  decode: out[t] = sum_j weight[t, j] SwiGLU(x[t] W_ug,e^T) W_down,e
 //
-// Packed layout (include/moe_gg.h): tiles of 16 rows by chunks of 128 elements, 1024 bytes of codes each; the scales
-// and zero points of a tile's rows r and r + 8 lie together.
+// Packed layout (include/moe_gg.h): one piece for 16 rows by 128 elements, 1024 bytes of codes and behind them the groups'
+// scales and zero points, those of rows r and r + 8 together. A lane's 16 bytes of codes are what it multiplies.
 #include <algorithm>
 
 #include "common.cuh"
@@ -20,11 +20,10 @@ constexpr int MAX_SLOTS = 4096;
 
 // Where the pieces of packed matrices lie
 struct Packed {
-  const uint8_t* codes;
-  const uint8_t* scales;
-  const uint8_t* zeros;
+  const uint8_t* base;
   int tiles, chunks, per;  // 16-row tiles of a matrix, 128-element chunks of a row, groups of a chunk
 };
+__host__ __device__ constexpr int piece_bytes(int per) { return (1024 + 40 * per + 15) / 16 * 16; }
 
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 int groups_of(int K, int group) { return (K + group - 1) / group; }
@@ -33,16 +32,8 @@ bool group_ok(int g) { return g == 32 || g == 64 || g == 128; }
 size_t pieces(int matrices, int N, int K) {
   return static_cast<size_t>(matrices) * ((N + 15) / 16) * ((K + 127) / 128);
 }
-Packed packed_at(const void* p, int matrices, int N, int K, int group) {
-  Packed w;
-  const size_t n = pieces(matrices, N, K);
-  w.per = 128 / group;
-  w.codes = static_cast<const uint8_t*>(p);
-  w.scales = w.codes + n * 1024;
-  w.zeros = w.scales + round256(n * 32 * w.per);
-  w.tiles = (N + 15) / 16;
-  w.chunks = (K + 127) / 128;
-  return w;
+Packed packed_at(const void* p, int N, int K, int group) {
+  return {static_cast<const uint8_t*>(p), (N + 15) / 16, (K + 127) / 128, 128 / group};
 }
 
 // ------------------------------------------------------------------ preparing weights
@@ -105,6 +96,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
     const long long mt = i / p.chunks;
     const int tile = static_cast<int>(mt % p.tiles);
     const long long m = mt / p.tiles;
+    uint8_t* piece = const_cast<uint8_t*>(p.base) + i * piece_bytes(p.per);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = tile * 16 + half * 8 + g;
@@ -125,7 +117,7 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
           w[q] = __funnelshift_l(w[q], w[q], 3);
         }
       }
-      *reinterpret_cast<uint4*>(const_cast<uint8_t*>(p.codes) + i * 1024 + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(piece + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     if (t < p.per) {
       const int gi = chunk * p.per + t;
@@ -138,9 +130,8 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
         s |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(scales)[at]) << (16 * half);
         z |= (zeros ? zeros[at] & 15u : 8u) << (4 * half);
       }
-      const long long at = (i * 8 + g) * p.per + t;
-      reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(p.scales))[at] = s;
-      const_cast<uint8_t*>(p.zeros)[at] = static_cast<uint8_t>(z);
+      reinterpret_cast<uint32_t*>(piece + 1024)[g * p.per + t] = s;
+      piece[1024 + 32 * p.per + g * p.per + t] = static_cast<uint8_t>(z);
     }
   }
 }
@@ -148,34 +139,44 @@ __global__ void __launch_bounds__(256) w4_pack_kernel(const uint8_t* codes, cons
 // ------------------------------------------------------------------ products
 // D[16 x 8] += A[16 x 16] B[16 x 8], bf16 operands, fp32 sums.
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // This lane's part of a piece: the codes of rows g and g + 8, its groups' scales (a pair of rows in a word) and zero points.
+template <typename T>
+__device__ __forceinline__ T fetch_global(const uint8_t* p) {
+  return __ldg(reinterpret_cast<const T*>(p));
+}
+template <typename T>
+__device__ __forceinline__ T fetch_shared(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
+}
 template <int PER>
 struct Piece {
+  static constexpr int bytes = piece_bytes(PER);
   uint4 lo, hi;
   uint32_t s[PER], z;
-  __device__ __forceinline__ void load(const Packed& p, size_t piece, int lane) {
-    const uint4* c = reinterpret_cast<const uint4*>(p.codes + piece * 1024) + lane;
-    lo = __ldg(c);
-    hi = __ldg(c + 32);
-    const size_t at = (piece * 8 + (lane >> 2)) * PER;
-    if constexpr (PER == 4) {
-      const uint4 q = __ldg(reinterpret_cast<const uint4*>(p.scales + at * 4));
-      s[0] = q.x, s[1] = q.y, s[2] = q.z, s[3] = q.w;
-      z = __ldg(reinterpret_cast<const uint32_t*>(p.zeros + at));
-    } else if constexpr (PER == 2) {
-      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.scales + at * 4));
-      s[0] = q.x, s[1] = q.y;
-      z = __ldg(reinterpret_cast<const uint16_t*>(p.zeros + at));
-    } else {
-      s[0] = __ldg(reinterpret_cast<const uint32_t*>(p.scales + at * 4));
-      z = __ldg(p.zeros + at);
-    }
+#define W4_LOAD(fetch)                                                                   \
+  lo = fetch<uint4>(p + lane * 16);                                                      \
+  hi = fetch<uint4>(p + 512 + lane * 16);                                                \
+  const uint8_t *sc = p + 1024 + (lane >> 2) * 4 * PER, *zp = p + 1024 + 32 * PER + (lane >> 2) * PER; \
+  if constexpr (PER == 4) {                                                              \
+    const uint4 q = fetch<uint4>(sc);                                                    \
+    s[0] = q.x, s[1] = q.y, s[2] = q.z, s[3] = q.w;                                      \
+    z = fetch<uint32_t>(zp);                                                             \
+  } else if constexpr (PER == 2) {                                                       \
+    const uint2 q = fetch<uint2>(sc);                                                    \
+    s[0] = q.x, s[1] = q.y;                                                              \
+    z = fetch<uint16_t>(zp);                                                             \
+  } else {                                                                               \
+    s[0] = fetch<uint32_t>(sc);                                                          \
+    z = fetch<uint8_t>(zp);                                                              \
   }
+  __device__ __forceinline__ void load(const uint8_t* p, int lane) { W4_LOAD(fetch_global) }
+  __device__ __forceinline__ void load_shared(const uint8_t* p, int lane) { W4_LOAD(fetch_shared) }
+#undef W4_LOAD
 };
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int q) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; }
@@ -188,20 +189,19 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4]) {
   p[3] = (__funnelshift_r(w, w, 12) & 0x00780078u) | 0x41804180u;
 }
 
-// tot += factor scale (codes - zero) x of one piece. b(q, t): the 8 bf16 values of x of this lane for word q and column tile t; nx(q, t):
-// minus the sums of x over the 32 elements of word q, of this lane's two columns. A group's sum starts at -(16 + zero) sum x, which
-// takes the codes' 16 and the zero point away without an instruction for each pair of codes: terms of up to 31 |x| instead of
-// 15 |x| in an fp32 sum.
-template <int PER, int NT, typename B, typename X>
-__device__ __forceinline__ void multiply(const Piece<PER>& w, float (&tot)[NT][4], float factor, const B& b, const X& nx) {
-  constexpr int RUN = 4 / PER;  // words of a group
-  float acc[NT][4];
+// tot += factor scale (codes - zero) x of TILES pieces of the same columns. b(q, t): the 8 bf16 values of x of this lane for
+// word q and column tile t; nx(q, t): minus the sums of x over the 32 elements of word q, of this lane's two columns. A group's sum
+// starts at -(16 + zero) sum x, which takes the codes' 16 and the zero point away without an instruction for each pair of
+// codes: terms of up to 31 |x| instead of 15 |x| in an fp32 sum. A group of several words has two sums, so that a product need
+// not wait for the one before it.
+template <int PER, int NT, int TILES, typename B, typename X>
+__device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&tot)[TILES][NT][4], float factor, const B& b, const X& nx) {
+  constexpr int RUN = 4 / PER, SUMS = RUN > 1 ? 2 : 1;  // words of a group, sums of a group
+  float acc[TILES][SUMS][NT][4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int j = q / RUN;
     if (q % RUN == 0) {
-      const float zg = __uint_as_float(0x41800000u | ((j < 3 ? w.z << (19 - 8 * j > 0 ? 19 - 8 * j : 0) : w.z >> 5) & 0x00780000u));
-      const float zh = __uint_as_float(0x41800000u | ((j < 2 ? w.z << (15 - 8 * j > 0 ? 15 - 8 * j : 0) : w.z >> (8 * j - 15)) & 0x00780000u));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float2 v = nx(q, t);
@@ -211,29 +211,46 @@ __device__ __forceinline__ void multiply(const Piece<PER>& w, float (&tot)[NT][4
           v.x += u.x;
           v.y += u.y;
         }
-        acc[t][0] = zg * v.x;
-        acc[t][1] = zg * v.y;
-        acc[t][2] = zh * v.x;
-        acc[t][3] = zh * v.y;
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) {
+          // 16 + zero: its four bits to bit 19 of an fp32 in [16, 32)
+          const uint32_t z = w[h].z;
+          const float zg = __uint_as_float(0x41800000u | ((j < 3 ? z << (j < 3 ? 19 - 8 * j : 0) : z >> 5) & 0x00780000u));
+          const float zh = __uint_as_float(0x41800000u | ((j < 2 ? z << (j < 2 ? 15 - 8 * j : 0) : z >> (j < 2 ? 0 : 8 * j - 15)) & 0x00780000u));
+          acc[h][0][t][0] = zg * v.x;
+          acc[h][0][t][1] = zg * v.y;
+          acc[h][0][t][2] = zh * v.x;
+          acc[h][0][t][3] = zh * v.y;
+          if constexpr (SUMS == 2) acc[h][1][t][0] = acc[h][1][t][1] = acc[h][1][t][2] = acc[h][1][t][3] = 0.f;
+        }
       }
     }
-    uint32_t pg[4], ph[4];
-    unpack8(word(w.lo, q), pg);
-    unpack8(word(w.hi, q), ph);
+    uint4 v[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const uint4 v = b(q, t);
-      mma16816(acc[t], pg[0], ph[0], pg[1], ph[1], v.x, v.y);
-      mma16816(acc[t], pg[2], ph[2], pg[3], ph[3], v.z, v.w);
-    }
-    if (q % RUN == RUN - 1) {
-      const float sg = bf16_lo(w.s[j]) * factor, sh = bf16_hi(w.s[j]) * factor;
+    for (int t = 0; t < NT; ++t) v[t] = b(q, t);
+#pragma unroll
+    for (int h = 0; h < TILES; ++h) {
+      uint32_t pg[4], ph[4];
+      unpack8(word(w[h].lo, q), pg);
+      unpack8(word(w[h].hi, q), ph);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        tot[t][0] = fmaf(sg, acc[t][0], tot[t][0]);
-        tot[t][1] = fmaf(sg, acc[t][1], tot[t][1]);
-        tot[t][2] = fmaf(sh, acc[t][2], tot[t][2]);
-        tot[t][3] = fmaf(sh, acc[t][3], tot[t][3]);
+        mma16816(acc[h][0][t], pg[0], ph[0], pg[1], ph[1], v[t].x, v[t].y);
+        mma16816(acc[h][SUMS - 1][t], pg[2], ph[2], pg[3], ph[3], v[t].z, v[t].w);
+      }
+    }
+    if (q % RUN == RUN - 1) {
+#pragma unroll
+      for (int h = 0; h < TILES; ++h) {
+        const float sg = bf16_lo(w[h].s[j]) * factor, sh = bf16_hi(w[h].s[j]) * factor;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float sum = SUMS == 2 ? acc[h][0][t][i] + acc[h][SUMS - 1][t][i] : acc[h][0][t][i];
+            tot[h][t][i] = fmaf(i < 2 ? sg : sh, sum, tot[h][t][i]);
+          }
+        }
       }
     }
   }
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
         for (int u = 0; u < U; ++u)
           if (live && c + u * WK < chunks) {
 #pragma unroll
-            for (int h = 0; h < TILES; ++h) p[u][h].load(a.w, piece0[h] + seg0 + c + u * WK, lane);
+            for (int h = 0; h < TILES; ++h) p[u][h].load(a.w.base + (piece0[h] + seg0 + c + u * WK) * Piece<PER>::bytes, lane);
           }
       };
       load(wk);  // on their way while x comes
@@ -393,8 +410,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
           const auto nx = [&](int q, int t) {  // columns past the last row: what lies there goes into sums that nobody reads
             return *reinterpret_cast<const float2*>(xsum + (s0 + q) * COLS + t * 8 + 2 * (lane & 3));
           };
-#pragma unroll
-          for (int h = 0; h < TILES; ++h) multiply<PER, NT>(p[u][h], tot[h], 1.0f, b, nx);
+          multiply<PER, NT, TILES>(p[u], tot, 1.0f, b, nx);
         }
       }
     }
@@ -430,6 +446,248 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
   }
 }
 
+// ------------------------------------------------------------------ few slots of an expert
+// Groups of up to eight slots of one expert, each with all tiles of its weights, are one list of tasks (group, tile set) that the
+// blocks share evenly, each a run of it: an expert's weights are read once, and x of a group is fetched once or twice. A
+// warp's pieces go through a ring of its own in shared memory, filled by asynchronous copies that run ahead over tasks and
+// groups, so that the copies in flight do not depend on how far the sums are, and no warp waits for another's.
+constexpr int STREAM_WARPS = 8;
+constexpr int STREAM_THREADS = STREAM_WARPS * 32;
+
+struct StreamShape {
+  int wk;       // warps that share K; STREAM_WARPS / wk tiles (with SWIGLU pairs of tiles) are a task
+  int log_wts;  // log2 of STREAM_WARPS / wk
+  int sets;     // tasks of a group
+  int xchunks;  // chunks of x in shared memory
+};
+
+template <int PER, bool SWIGLU>
+struct StreamSmem {
+  static constexpr int TILES = SWIGLU ? 2 : 1;
+  static constexpr int step = TILES * piece_bytes(PER);  // bytes of one ring slot
+  static constexpr int depth = SWIGLU ? 3 : 4;             // slots of a warp's ring
+  static constexpr int sum_floats = STREAM_WARPS * TILES * 128;
+  int ring, x, xsum, sums, list, groups, count, total;  // byte offsets
+  __host__ __device__ StreamSmem(const W4Args& a, const StreamShape& sh) {
+    ring = 0;
+    x = ring + STREAM_WARPS * depth * step;
+    xsum = x + sh.xchunks * 4 * 8 * 64;
+    sums = xsum + sh.xchunks * 4 * 8 * 4;
+    list = sums + 2 * sum_floats * 4;
+    groups = list + (a.slots * 4 + 15) / 16 * 16;
+    count = groups + most_groups(a) * 8;
+    total = count + (a.ids == nullptr || a.slots == a.top_k ? 0 : (a.E + 1) * 4);
+  }
+  // groups at most: every slot alone, or a full group of every eight and one that is not full of every expert
+  static __host__ __device__ int most_groups(const W4Args& a) {
+    if (a.ids == nullptr) return (a.slots + 7) / 8;
+    if (a.slots == a.top_k) return a.slots;
+    const int m = a.E + a.slots / 8;
+    return m < a.slots ? m : a.slots;
+  }
+};
+
+template <int PER, bool SWIGLU, bool VEC>
+__global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Args a, const StreamShape sh) {
+  using Smem = StreamSmem<PER, SWIGLU>;
+  constexpr int TILES = Smem::TILES, BYTES = Piece<PER>::bytes;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const Smem at(a, sh);
+  uint4* xs = reinterpret_cast<uint4*>(smem + at.x);          // [chunks * 4][8][4]
+  float* xsum = reinterpret_cast<float*>(smem + at.xsum);     // [chunks * 4][8]: minus the sums
+  int* list = reinterpret_cast<int*>(smem + at.list);         // slots, expert by expert
+  int2* groups = reinterpret_cast<int2*>(smem + at.groups);   // expert, first slot in list | slots << 16
+  int* count = reinterpret_cast<int*>(smem + at.count);       // slots of each expert, of none; then where the next one goes
+  __shared__ int n_groups;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_wait();
+  const int32_t* ids = after_wait(a.ids);
+  if (a.ids == nullptr || a.slots == a.top_k) {
+    const int per = a.ids == nullptr ? 8 : 1;
+    for (int i = threadIdx.x; i < a.slots; i += STREAM_THREADS) {
+      list[i] = i;
+      if (i % per == 0) groups[i / per] = make_int2(a.ids == nullptr ? 0 : ids[i], i | min(per, a.slots - i) << 16);
+    }
+    if (threadIdx.x == 0) n_groups = (a.slots + per - 1) / per;
+  } else {
+    const auto of = [&](int i) {
+      const int e = ids[i];
+      return e >= 0 && e < a.E ? e : a.E;
+    };
+    for (int i = threadIdx.x; i <= a.E; i += STREAM_THREADS) count[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.slots; i += STREAM_THREADS) atomicAdd(count + of(i), 1);
+    __syncthreads();
+    if (warp == 0) {  // where each expert's slots begin, and the groups that they make
+      int slots = 0, made = 0;
+      for (int e0 = 0; e0 <= a.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int c = e <= a.E ? count[e] : 0;
+        const int g = e < a.E ? (c + 7) >> 3 : 0;
+        int sum = c | g << 16;  // both running sums in one word
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += v;
+        }
+        const int first = slots + (sum & 0xFFFF) - c, to = made + (sum >> 16) - g;
+        if (e <= a.E) count[e] = first;
+        for (int i = 0; i < g; ++i) groups[to + i] = make_int2(e, (first + 8 * i) | min(8, c - 8 * i) << 16);
+        sum = __shfl_sync(0xffffffffu, sum, 31);
+        slots += sum & 0xFFFF;
+        made += sum >> 16;
+      }
+      if (lane == 0) n_groups = made;
+    }
+    __syncthreads();
+    // the order of an expert's slots is left to the atomics: each is a column of its own, and no sum goes over columns
+    for (int i = threadIdx.x; i < a.slots; i += STREAM_THREADS) list[atomicAdd(count + of(i), 1)] = i;
+  }
+  __syncthreads();
+  const int wk = warp & (sh.wk - 1), wts = 1 << sh.log_wts, wt = warp * wts / STREAM_WARPS;
+  const long long tasks = static_cast<long long>(n_groups) * sh.sets;
+  const int t0 = static_cast<int>(tasks * blockIdx.x / gridDim.x), t1 = static_cast<int>(tasks * (blockIdx.x + 1) / gridDim.x);
+  constexpr int depth = Smem::depth;
+  const int chunks = a.w.chunks;
+
+  // Where this warp's copies are: the tasks not begun yet, the next one's group and set, and in the one begun the next piece and how
+  // many are left
+  const int mine = wk < chunks ? (chunks - 1 - wk) / sh.wk + 1 : 0;  // pieces of a task that are this warp's
+  int f_tasks = mine > 0 ? t1 - t0 : 0, f_group = t0 / sh.sets, f_set = t0 - f_group * sh.sets, f_left = 0;
+  const uint8_t* f_src = nullptr;
+  const size_t other = static_cast<size_t>(a.w.tiles) * chunks * BYTES;  // from a gate tile to the up tile
+  const uint32_t ring = smem_u32(smem + at.ring) + warp * depth * Smem::step, ring_end = ring + depth * Smem::step;
+  const uint32_t lane16 = lane * 16;
+  const bool tail = lane < (BYTES - 1024) / 16;
+  const int f_step = sh.wk * BYTES;
+  const auto fill = [&](uint32_t to) {
+    while (f_left == 0 && f_tasks > 0) {
+      const int e = groups[f_group].x, tile = f_set * wts + wt;
+      if (e >= 0 && e < a.E && tile < a.w.tiles) {
+        f_left = mine;
+        f_src = a.w.base + ((static_cast<size_t>(e * TILES) * a.w.tiles + tile) * chunks + wk) * BYTES + lane16;
+      }
+      --f_tasks;
+      if (++f_set == sh.sets) {
+        f_set = 0;
+        ++f_group;
+      }
+    }
+    if (f_left > 0) {
+      const uint32_t dst = to + lane16;
+#pragma unroll
+      for (int h = 0; h < TILES; ++h) {
+        const uint8_t* src = f_src + (h == 1 ? other : 0);
+        copy16_async(dst + h * BYTES, src);
+        copy16_async(dst + h * BYTES + 512, src + 512);
+        if (tail) copy16_async(dst + h * BYTES + 1024, src + 1024);
+      }
+      f_src += f_step;
+      --f_left;
+    }
+    copy_commit();
+  };
+  for (uint32_t to = ring; to != ring_end; to += Smem::step) fill(to);
+
+  const bf16* x = after_wait(a.x);
+  if constexpr (!SWIGLU) {  // rows of dropped slots
+    const auto zero_row = [&](int slot) {
+      for (int c = threadIdx.x; c < a.N; c += STREAM_THREADS) {
+        if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + c] = __float2bfloat16_rn(0.f);
+        else static_cast<float*>(a.out)[slot * a.ldo + c] = 0.f;
+      }
+    };
+    if (a.ids != nullptr)
+      for (int i = blockIdx.x; i < a.slots; i += gridDim.x) {
+        const int e = ids[i];
+        if (e < 0 || e >= a.E) zero_row(i);
+      }
+  }
+  uint32_t slot = 0;  // byte offset in this warp's ring
+  const uint8_t* const my_ring = smem + at.ring + warp * depth * Smem::step;
+  int in_group = -1, in_seg = -1, par = 0, group = t0 / sh.sets, set = t0 - group * sh.sets;
+  for (int t = t0; t < t1; ++t, ++set) {
+    if (set == sh.sets) {
+      set = 0;
+      ++group;
+    }
+    const int2 info = groups[group];
+    if (info.x < 0 || info.x >= a.E) continue;  // a dropped slot of a single token
+    const int first = info.y & 0xFFFF, rows = info.y >> 16;
+    const bool live = set * wts + wt < a.w.tiles;
+    float tot[TILES][1][4];
+#pragma unroll
+    for (int h = 0; h < TILES; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tot[h][0][i] = 0.f;
+    for (int seg0 = 0; seg0 < chunks; seg0 += sh.xchunks) {
+      const int n = min(sh.xchunks, chunks - seg0);
+      if (group != in_group || seg0 != in_seg) {
+        __syncthreads();  // x there is no longer read
+        // Eight columns, zeros where the group has fewer rows. A thread takes eight elements, four threads the 32 of a sum.
+        for (int i = threadIdx.x; i < n * 128; i += STREAM_THREADS) {
+          const int col = i / (n * 16), k8 = i - col * (n * 16);
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (col < rows) v = load_x<VEC>(x + (list[first + col] / a.xdiv) * a.ldx, (seg0 * 16 + k8) * 8, a.K);
+          xs[((k8 >> 2) * 8 + col) * 4 + (k8 & 3)] = v;
+          float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // n * 128 is a multiple of 32: whole warps
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          if ((k8 & 3) == 0) xsum[(k8 >> 2) * 8 + col] = -sum;
+        }
+        __syncthreads();
+        in_group = group;
+        in_seg = seg0;
+      }
+      if (!live) continue;
+      // chunks of this segment that are this warp's: those equal to wk modulo the warps that share K
+      const int c0 = (wk - seg0) & (sh.wk - 1);
+      const uint4* xp = xs + c0 * 128 + lane;
+      const float* sp = xsum + c0 * 32 + 2 * (lane & 3);
+      for (int c = c0; c < n; c += sh.wk, xp += sh.wk * 128, sp += sh.wk * 32) {
+        copy_wait<depth - 1>();  // younger groups of copies may be on their way
+        __syncwarp();
+        Piece<PER> p[TILES];
+#pragma unroll
+        for (int h = 0; h < TILES; ++h) p[h].load_shared(my_ring + slot + h * BYTES, lane);
+        __syncwarp();  // every lane has its part: the slot is free
+        fill(ring + slot);
+        slot = slot == (depth - 1) * Smem::step ? 0 : slot + Smem::step;
+        multiply<PER, 1, TILES>(p, tot, 1.0f, [&](int q, int) { return xp[q * 32]; },
+                                [&](int q, int) { return *reinterpret_cast<const float2*>(sp + q * 8); });
+      }
+    }
+    // the sums of the warps, in one of two buffers: [warp][half][register][lane]
+    float* sums = reinterpret_cast<float*>(smem + at.sums) + par * Smem::sum_floats;
+    par ^= 1;
+#pragma unroll
+    for (int h = 0; h < TILES; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sums[((warp * TILES + h) * 4 + i) * 32 + lane] = tot[h][0][i];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * wts * rows; i += STREAM_THREADS) {
+      const int r = i & 15, w0 = (i >> 4) & (wts - 1), col = i >> 4 >> sh.log_wts;  // consecutive threads: consecutive rows of the output
+      // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + c / 2
+      const int from = ((r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + (col >> 1);
+      float v[TILES];
+#pragma unroll
+      for (int h = 0; h < TILES; ++h) {
+        v[h] = 0.f;
+        for (int w = 0; w < sh.wk; ++w) v[h] += sums[((w0 * sh.wk + w) * TILES + h) * 128 + from];
+      }
+      const int row = (set * wts + w0) * 16 + r, s = list[first + col];
+      if constexpr (SWIGLU) {
+        // rows past h up to the pitch: their scales are 0
+        if (row < a.ldo) static_cast<bf16*>(a.out)[s * a.ldo + row] = __float2bfloat16_rn(v[0] / (1.0f + expf(-v[0])) * v[1]);
+      } else if (row < a.N) {
+        if (a.y_bf16) static_cast<bf16*>(a.out)[s * a.ldo + row] = __float2bfloat16_rn(v[0]);
+        else static_cast<float*>(a.out)[s * a.ldo + row] = v[0];
+      }
+    }
+  }
+  copy_wait<0>();
+}
+
 // The down product and the combine of one token: block (tile, token) owns 16 columns of out[t]. The chunks of the token's top_k
 // slots are one long contraction that its warps share, each slot's scales times its routing weight; no sums leave the block.
 constexpr int DOWN_WARPS = 8;
@@ -450,16 +708,16 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
   }
   __syncthreads();
   const int items = a.top_k * a.w.chunks;
-  float tot[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  float tot[1][1][4] = {{{0.f, 0.f, 0.f, 0.f}}};
   const bf16* x = after_wait(a.x);
   for (int i0 = warp; i0 < items; i0 += DOWN_WARPS * U) {
-    Piece<PER> p[U];
+    Piece<PER> p[U][1];
     uint4 v[U][4];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks, c = i % a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
-      p[u].load(a.w, (static_cast<size_t>(expert[j]) * a.w.tiles + tile) * a.w.chunks + c, lane);
+      p[u][0].load(a.w.base + ((static_cast<size_t>(expert[j]) * a.w.tiles + tile) * a.w.chunks + c) * Piece<PER>::bytes, lane);
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[u][q] = lane < 4 ? load_x<true>(x + static_cast<size_t>(t * a.top_k + j) * a.ldx, c * 128 + q * 32 + lane * 8, a.K)
@@ -470,7 +728,7 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
       // the sums of x by a product with ones: column 0 of every row
-      multiply<PER, 1>(p[u], tot, weight[j], [&](int q, int) { return v[u][q]; }, [&](int q, int) {
+      multiply<PER, 1, 1>(p[u], tot, weight[j], [&](int q, int) { return v[u][q]; }, [&](int q, int) {
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         constexpr uint32_t one = 0xBF80BF80u;  // -1, twice
         mma16816(sum, one, one, one, one, v[u][q].x, v[u][q].y);
@@ -481,8 +739,8 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
   }
   // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
   if ((lane & 3) == 0) {
-    sums[warp][0][lane >> 2] = tot[0][0];
-    sums[warp][1][lane >> 2] = tot[0][2];
+    sums[warp][0][lane >> 2] = tot[0][0][0];
+    sums[warp][1][lane >> 2] = tot[0][0][2];
   }
   __syncthreads();
   const int row = tile * 16 + threadIdx.x;
@@ -494,17 +752,29 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
   }
 }
 
-// out[t] = sum_j weight[t, j] y[t, j] of fp32 rows, in slot order
+// out[t] = sum_j weight[t, j] y[t, j] of fp32 rows, in slot order; eight rows' loads at a time
 __global__ void __launch_bounds__(128) w4_combine_kernel(const float* y, long long ldy, const int32_t* ids, const float* weights,
                                                          int top_k, int E, int d, bf16* out, long long ldo) {
+  __shared__ float weight[32];  // 0 of a dropped slot, whose row is not read
+  __shared__ bool on[32];
   grid_wait();
   const int t = blockIdx.y;
-  y = after_wait(y);
+  if (threadIdx.x < top_k) {
+    const int e = after_wait(ids)[t * top_k + threadIdx.x];
+    on[threadIdx.x] = e >= 0 && e < E;
+    weight[threadIdx.x] = weights ? after_wait(weights)[t * top_k + threadIdx.x] : 1.0f;
+  }
+  __syncthreads();
+  y = after_wait(y) + static_cast<long long>(t) * top_k * ldy;
   for (int c = blockIdx.x * 128 + threadIdx.x; c < d; c += gridDim.x * 128) {
     float v = 0.f;
-    for (int j = 0; j < top_k; ++j) {
-      const int s = t * top_k + j, e = after_wait(ids)[s];
-      if (e >= 0 && e < E) v = fmaf(weights ? after_wait(weights)[s] : 1.0f, y[s * ldy + c], v);
+    for (int j0 = 0; j0 < top_k; j0 += 8) {
+      float r[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = j0 + j < top_k && on[j0 + j] ? y[(j0 + j) * ldy + c] : 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < top_k && on[j0 + j]) v = fmaf(weight[j0 + j], r[j], v);
     }
     out[t * ldo + c] = __float2bfloat16_rn(v);
   }
@@ -531,12 +801,37 @@ cudaError_t launch_group_split(const W4Args& a, int groups, cudaStream_t s) {
   return vec ? launch_group_as<PER, NT, 1, SWIGLU, true>(a, groups, s) : launch_group_as<PER, NT, 1, SWIGLU, false>(a, groups, s);
 }
 
+template <int PER, bool SWIGLU, bool VEC>
+cudaError_t launch_stream_as(const W4Args& a, cudaStream_t s) {
+  using Smem = StreamSmem<PER, SWIGLU>;
+  StreamShape sh;
+  // Two to four chunks of a task for a warp: with fewer the sums at its end cost as much as its products, with more there are too few
+  // tasks to share evenly.
+  sh.log_wts = a.w.chunks >= 24 ? 0 : a.w.chunks >= 12 ? 1 : a.w.chunks >= 4 ? 2 : 3;
+  const int wts = 1 << sh.log_wts;
+  sh.wk = STREAM_WARPS / wts;
+  sh.sets = (a.w.tiles + wts - 1) / wts;
+  sh.xchunks = std::min(a.w.chunks, SWIGLU ? 16 : 32);
+  const int smem = Smem(a, sh).total;
+  const auto kernel = w4_stream_kernel<PER, SWIGLU, VEC>;
+  const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), 200 * 1024);
+  if (err != cudaSuccess) return err;
+  const long long most = static_cast<long long>(Smem::most_groups(a)) * sh.sets;
+  const int blocks = static_cast<int>(std::min<long long>(most, (smem <= 112 * 1024 ? 2 : 1) * static_cast<long long>(device_sm_count())));
+  return launch_dependent(kernel, blocks, STREAM_THREADS, smem, s, a, sh);
+}
+
 template <int PER, bool SWIGLU>
 cudaError_t launch_group(W4Args a, cudaStream_t s) {
   a.segment = std::min(a.w.chunks, SEGMENT);
-  const int groups = a.ids == nullptr ? 1 : a.slots <= a.E ? a.slots : a.slots == a.top_k ? a.slots : a.E + (SWIGLU ? 0 : 1);
   // tokens of an expert, on average: what one pass over its weights should take
   const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
+  // One slot (of an expert) at a time takes a block for each tile, which starts sooner than the list of tasks is made.
+  if (each <= 8 && (a.ids == nullptr ? a.slots > 1 : a.slots > a.top_k)) {
+    const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
+    return vec ? launch_stream_as<PER, SWIGLU, true>(a, s) : launch_stream_as<PER, SWIGLU, false>(a, s);
+  }
+  const int groups = a.ids == nullptr ? 1 : a.slots <= a.E ? a.slots : a.slots == a.top_k ? a.slots : a.E + (SWIGLU ? 0 : 1);
   return each <= 8 ? launch_group_split<PER, 1, SWIGLU>(a, groups, s) : launch_group_split<PER, 2, SWIGLU>(a, groups, s);
 }
 template <bool SWIGLU>
@@ -561,8 +856,7 @@ bool dim_ok(int v) { return v >= 1 && v <= MAX_DIM; }
 
 size_t w4_weights_bytes(int matrices, int K, int N, int group) {
   if (matrices < 1 || matrices > MAX_MATRICES || !dim_ok(K) || !dim_ok(N) || !group_ok(group)) return 0;
-  const size_t n = pieces(matrices, N, K), per = 128 / group;
-  return n * 1024 + round256(n * 32 * per) + round256(n * 8 * per);
+  return round256(pieces(matrices, N, K) * piece_bytes(128 / group));
 }
 size_t w4_decode_workspace_bytes(long long slots, int E, int d, int h) {
   if (slots < 0 || slots > MAX_SLOTS || !dim_ok(d) || !dim_ok(h)) return 0;
@@ -605,7 +899,7 @@ moe_status_t moe_w4_pack(const uint8_t* codes, const moe_bf16* scales, const uin
   if (st != MOE_OK) return st;
   const long long n = static_cast<long long>(pieces(matrices, N, K));
   w4_pack_kernel<<<static_cast<int>(std::min<long long>((n + 7) / 8, 1 << 20)), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      codes, reinterpret_cast<const bf16*>(scales), zeros, N, K, group, n, packed_at(packed, matrices, N, K, group));
+      codes, reinterpret_cast<const bf16*>(scales), zeros, N, K, group, n, packed_at(packed, N, K, group));
   const cudaError_t err = cudaGetLastError();
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
@@ -634,7 +928,7 @@ moe_status_t moe_w4_matvec(const moe_bf16* x, long long ldx, const int32_t* ids,
   a.E = matrices;
   a.N = N;
   a.K = K;
-  a.w = packed_at(packed, matrices, N, K, group);
+  a.w = packed_at(packed, N, K, group);
   a.out = y;
   a.ldo = ldy;
   a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
@@ -671,7 +965,7 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
   a.E = E;
   a.N = h;
   a.K = d;
-  a.w = packed_at(w_ug, 2 * E, h, d, group);
+  a.w = packed_at(w_ug, h, d, group);
   a.out = act;
   a.ldo = pitch;
   cudaError_t err = launch_group<true>(a, s);
@@ -683,7 +977,7 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
   b.xdiv = 1;
   b.N = d;
   b.K = pitch;  // zeros from h on
-  b.w = packed_at(w_down, E, d, h, group);
+  b.w = packed_at(w_down, d, h, group);
   if (down_by_token(slots, E)) {
     b.out = out;
     b.ldo = ldo;

@@ -27,11 +27,11 @@ def test_workspaces():
     assert wb(_lib.OP_RESIDUAL_NORM_BWD, 5, 1, 1, 100) == 5 * 4 * 100 * 4 + 5 * 8
     assert wb(_lib.OP_RESIDUAL_NORM_BWD, 5, 1, 1, 0) == 0 and wb(_lib.OP_RESIDUAL_NORM_BWD, 5, 1, 1, (1 << 20) + 1) == 0
     assert wb(_lib.OP_GRAD_NORM, 0, 1, 1) > 0
-    # pieces of 16 rows by 128 elements: 1024 bytes of codes, then the groups' scales and zero points
+    # pieces of 16 rows by 128 elements: 1024 bytes of codes, then the groups' scales and zero points, in multiples of 16 bytes
     n = 256 * 48 * 16
-    assert wb(_lib.OP_W4_WEIGHTS, 0, 1, 256, 2048, 768, 128) == n * (1024 + 32 + 8)
+    assert wb(_lib.OP_W4_WEIGHTS, 0, 1, 256, 2048, 768, 128) == n * (1024 + 32 + 16)
     assert wb(_lib.OP_W4_WEIGHTS, 0, 1, 2048, 33, 17, 32) == 2048 * 2 * (1024 + 128 + 32)
-    assert wb(_lib.OP_W4_WEIGHTS, 0, 1, 1, 1, 1, 32) == 1024 + 256 + 256
+    assert wb(_lib.OP_W4_WEIGHTS, 0, 1, 1, 1, 1, 32) == (1024 + 128 + 32 + 255) // 256 * 256
     for bad in ((0, 64, 64, 32), (2049, 64, 64, 32), (4, 0, 64, 32), (4, 64, 0, 32), (4, 64, 64, 48), (4, 64, 64, 0), (4, (1 << 20) + 1, 64, 32)):
         E, d, h, group = bad
         assert wb(_lib.OP_W4_WEIGHTS, 0, 1, E, d, h, group) == 0

@@ -92,7 +92,7 @@ def test_four_bit_round_trip_and_packing():
     packed = R.pack4(codes, np.ones((2, 17, 5), np.uint16), np.full((2, 17, 5), 3, np.uint8), 32)
     tiles, chunks = 2, 2
     # matrix 1, row 16 (tile 1, row 0), chunk 1, word 0 of quarter 0, which is rotated left by 3 bits
-    at = ((1 * tiles + 1) * chunks + 1) * 1024
+    at = ((1 * tiles + 1) * chunks + 1) * (1024 + 128 + 32)
     word = int(packed[at:at + 4].view(np.uint32)[0])
     word = word >> 3 | (word & 7) << 29
     assert word & 15 == codes[1, 16, 128] and (word >> 16) & 15 == codes[1, 16, 129]
