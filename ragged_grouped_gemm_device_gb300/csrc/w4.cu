@@ -181,13 +181,26 @@ struct Piece {
 
 __device__ __forceinline__ uint32_t word(const uint4& v, int q) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; }
 
-// Eight codes as four bf16 pairs of 16 + code: the code in the upper four mantissa bits of a bf16 in [16, 32).
-__device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4]) {
-  p[0] = (w & 0x00780078u) | 0x41804180u;
-  p[1] = ((w >> 4) & 0x00780078u) | 0x41804180u;
-  p[2] = ((w >> 8) & 0x00780078u) | 0x41804180u;
-  p[3] = (__funnelshift_r(w, w, 12) & 0x00780078u) | 0x41804180u;
-}
+// Eight codes as four bf16 pairs of 16 + code: the code in the upper four mantissa bits of a bf16 in [16, 32). Both constants
+// in registers, so that each pair takes one instruction behind its shift.
+struct Unpack {
+  uint32_t mask, base;
+  __device__ __forceinline__ Unpack() {
+    asm volatile("mov.b32 %0, 0x00780078;" : "=r"(mask));
+    asm volatile("mov.b32 %0, 0x41804180;" : "=r"(base));
+  }
+  __device__ __forceinline__ uint32_t pick(uint32_t w) const {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(base));  // (w & mask) | base
+    return d;
+  }
+  __device__ __forceinline__ void operator()(uint32_t w, uint32_t (&p)[4]) const {
+    p[0] = pick(w);
+    p[1] = pick(w >> 4);
+    p[2] = pick(w >> 8);
+    p[3] = pick(__funnelshift_r(w, w, 12));
+  }
+};
 
 // tot += factor scale (codes - zero) x of TILES pieces of the same columns. b(q, t): the 8 bf16 values of x of this lane for
 // word q and column tile t; nx(q, t): minus the sums of x over the 32 elements of word q, of this lane's two columns. A group's sum
@@ -195,7 +208,7 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t (&p)[4]) {
 // codes: terms of up to 31 |x| instead of 15 |x| in an fp32 sum. A group of several words has two sums, so that a product need
 // not wait for the one before it.
 template <int PER, int NT, int TILES, typename B, typename X>
-__device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&tot)[TILES][NT][4], float factor, const B& b, const X& nx) {
+__device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&tot)[TILES][NT][4], float factor, const Unpack& unpack, const B& b, const X& nx) {
   constexpr int RUN = 4 / PER, SUMS = RUN > 1 ? 2 : 1;  // words of a group, sums of a group
   float acc[TILES][SUMS][NT][4];
 #pragma unroll
@@ -231,8 +244,8 @@ __device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&t
 #pragma unroll
     for (int h = 0; h < TILES; ++h) {
       uint32_t pg[4], ph[4];
-      unpack8(word(w[h].lo, q), pg);
-      unpack8(word(w[h].hi, q), ph);
+      unpack(word(w[h].lo, q), pg);
+      unpack(word(w[h].hi, q), ph);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         mma16816(acc[h][0][t], pg[0], ph[0], pg[1], ph[1], v[t].x, v[t].y);
@@ -270,6 +283,15 @@ __device__ __forceinline__ uint4 load_x(const bf16* row, int k, int K) {
     v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
   }
   return v;
+}
+
+// Minus the sums of x over the 32 elements of a word, of this lane's two columns: a product with -1.
+__device__ __forceinline__ float2 minus_sums(const uint4& v) {
+  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+  constexpr uint32_t one = 0xBF80BF80u;  // -1, twice
+  mma16816(sum, one, one, one, one, v.x, v.y);
+  mma16816(sum, one, one, one, one, v.z, v.w);
+  return make_float2(sum[0], sum[1]);
 }
 
 struct W4Args {
@@ -357,6 +379,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
     return;
   }
   const bf16* x = after_wait(a.x);
+  const Unpack unpack;
   for (int r0 = 0; r0 < n; r0 += COLS) {
     const int rows = min(COLS, n - r0);
     float tot[TILES][NT][4];
@@ -410,7 +433,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
           const auto nx = [&](int q, int t) {  // columns past the last row: what lies there goes into sums that nobody reads
             return *reinterpret_cast<const float2*>(xsum + (s0 + q) * COLS + t * 8 + 2 * (lane & 3));
           };
-          multiply<PER, NT, TILES>(p[u], tot, 1.0f, b, nx);
+          multiply<PER, NT, TILES>(p[u], tot, 1.0f, unpack, b, nx);
         }
       }
     }
@@ -603,6 +626,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
         if (e < 0 || e >= a.E) zero_row(i);
       }
   }
+  const Unpack unpack;
   uint32_t slot = 0;  // byte offset in this warp's ring
   const uint8_t* const my_ring = smem + at.ring + warp * depth * Smem::step;
   int in_group = -1, in_seg = -1, par = 0, group = t0 / sh.sets, set = t0 - group * sh.sets;
@@ -653,7 +677,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
         __syncwarp();  // every lane has its part: the slot is free
         fill(ring + slot);
         slot = slot == (depth - 1) * Smem::step ? 0 : slot + Smem::step;
-        multiply<PER, 1, TILES>(p, tot, 1.0f, [&](int q, int) { return xp[q * 32]; },
+        multiply<PER, 1, TILES>(p, tot, 1.0f, unpack, [&](int q, int) { return xp[q * 32]; },
                                 [&](int q, int) { return *reinterpret_cast<const float2*>(sp + q * 8); });
       }
     }
@@ -710,6 +734,7 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
   const int items = a.top_k * a.w.chunks;
   float tot[1][1][4] = {{{0.f, 0.f, 0.f, 0.f}}};
   const bf16* x = after_wait(a.x);
+  const Unpack unpack;
   for (int i0 = warp; i0 < items; i0 += DOWN_WARPS * U) {
     Piece<PER> p[U][1];
     uint4 v[U][4];
@@ -727,14 +752,7 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
-      // the sums of x by a product with ones: column 0 of every row
-      multiply<PER, 1, 1>(p[u], tot, weight[j], [&](int q, int) { return v[u][q]; }, [&](int q, int) {
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        constexpr uint32_t one = 0xBF80BF80u;  // -1, twice
-        mma16816(sum, one, one, one, one, v[u][q].x, v[u][q].y);
-        mma16816(sum, one, one, one, one, v[u][q].z, v[u][q].w);
-        return make_float2(sum[0], sum[1]);
-      });
+      multiply<PER, 1, 1>(p[u], tot, weight[j], unpack, [&](int q, int) { return v[u][q]; }, [&](int q, int) { return minus_sums(v[u][q]); });
     }
   }
   // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
