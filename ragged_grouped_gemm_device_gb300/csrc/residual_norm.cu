@@ -255,6 +255,390 @@ __global__ void __launch_bounds__(256) join_wgrad_wide_kernel(const JoinArgs a) 
   for (int k = 0; k < SUMS; ++k) a.part[(static_cast<size_t>(blockIdx.y) * SUMS + k) * a.d + c] = s[k];
 }
 
+// ------------------------------------------------------------------ rows in registers
+// A row lies in the registers of its TPR threads, NCH chunks of eight elements each, so every value is read once and the
+// variances are the exact two-pass ones. The rows to come are on their way into shared memory by asynchronous copies: a ring of
+// `depth` rows that a thread (or, of fp32 tensors, a warp) fills for itself, so that it needs no barrier.
+template <int NCH, int TPR, typename... Ts>
+struct RowFeed {
+  static constexpr int NT = sizeof...(Ts);
+  static constexpr int threads = block_threads(TPR);
+  __host__ __device__ static constexpr int size(int k) {
+    constexpr int es[NT] = {static_cast<int>(sizeof(Ts))...};
+    return es[k];
+  }
+  // bytes of a slot before tensor k
+  __host__ __device__ static constexpr int before(int k) {
+    int b = 0;
+    for (int j = 0; j < k; ++j) b += NCH * threads * 8 * size(j);
+    return b;
+  }
+  static constexpr int slot_bytes = before(NT);
+  static constexpr int depth = slot_bytes <= 16 * 1024 ? 4 : slot_bytes <= 32 * 1024 ? 3 : slot_bytes <= 96 * 1024 ? 2 : 1;  // rows on their way
+  static constexpr int smem_bytes = depth * slot_bytes;
+  const uint8_t* at[NT];  // the next row to start (nullptr: no such tensor)
+  long long step[NT];     // bytes from one row of this block to its next
+  uint8_t* mem;
+  int c0, cw, lane;       // first column of this thread and of its warp
+  int d, left;
+  uint32_t slot;
+
+  __device__ __forceinline__ void init(uint8_t* smem, int t, int width, int rows) {
+    mem = smem;
+    lane = threadIdx.x & 31;
+    c0 = t * 8;
+    cw = (t & ~31) * 8;
+    d = width;
+    left = rows;
+    slot = 0;
+  }
+  __device__ __forceinline__ void tensor(int k, const void* p, long long ld, long long row0, int rows_step) {
+    at[k] = p ? static_cast<const uint8_t*>(p) + row0 * ld * size(k) : nullptr;
+    step[k] = rows_step * ld * size(k);
+  }
+  // this warp's 32 chunks of tensor k, chunk i: 256 elements
+  __device__ __forceinline__ uint8_t* chunk(uint32_t to, int k, int i) const {
+    return mem + to + before(k) + (i * threads + (threadIdx.x & ~31)) * 8 * size(k);
+  }
+  __device__ __forceinline__ void start(uint32_t to) {
+    if (left > 0) {
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        if (at[k] == nullptr) continue;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+#pragma unroll
+          for (int u = 0; u < size(k) / 2; ++u) {  // 16 bytes a lane: the whole chunk of a lane, or half of those of two
+            const int c = cw + i * TPR * 8 + (u * 32 + lane) * (16 / size(k));
+            if (c < d) copy16_async(smem_u32(chunk(to, k, i)) + (u * 32 + lane) * 16, at[k] + static_cast<size_t>(c) * size(k));
+          }
+        }
+        at[k] += step[k];
+      }
+      --left;
+    }
+    copy_commit();
+  }
+  __device__ __forceinline__ void prime() {
+#pragma unroll
+    for (int s = 0; s < depth; ++s) start(s * slot_bytes);
+  }
+  // the oldest row's copies have landed
+  __device__ __forceinline__ void wait() {
+    copy_wait<depth - 1>();
+    __syncwarp();  // lanes copy for one another
+  }
+  template <int K>
+  __device__ __forceinline__ void get(int i, float (&f)[8]) const {
+    const uint8_t* p = chunk(slot, K, i) + lane * 8 * size(K);
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    if constexpr (size(K) == 2) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = bf16_lo(w[j]);
+        f[2 * j + 1] = bf16_hi(w[j]);
+      }
+    } else {
+      const float4 r = *reinterpret_cast<const float4*>(p + 16);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(w[j]);
+      f[4] = r.x, f[5] = r.y, f[6] = r.z, f[7] = r.w;
+    }
+  }
+  // everything of the oldest row has been read: start the one that takes its place
+  __device__ __forceinline__ void next() {
+    __syncwarp();
+    start(slot);
+    slot = slot == (depth - 1) * slot_bytes ? 0 : slot + slot_bytes;
+  }
+};
+
+__device__ __forceinline__ void put8(bf16* p, const float (&f)[8]) { Chunk<bf16, 8>::store(p, f); }
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Blocks on an SM, which size the grids and bound the registers.
+constexpr int fwd_blocks(int tpr) { return 512 / block_threads(tpr); }
+constexpr int bwd_blocks(int tpr) { return tpr <= 128 ? 3 : tpr == 256 ? 1 : 1; }
+
+// BIAS: some norm has a beta.
+template <typename TX, typename TY, int NCH, int TPR, bool BIAS>
+__global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR)) join_fwd_kernel(const JoinArgs a) {
+  grid_wait();
+  constexpr int ROWS = block_threads(TPR) / TPR;
+  __shared__ __align__(16) float red[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];
+  const int t = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
+  const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
+  RowFeed<NCH, TPR, TX, TY> feed;
+  feed.init(ring, t, a.d, rows);
+  feed.tensor(0, after_wait(a.x), a.ldx, row0, step);
+  feed.tensor(1, after_wait(a.y), a.ldy, row0, step);
+  feed.prime();
+  // r = alpha x + A yhat + B;  n = rhat g2 + b2
+  float A[NCH][8], B[NCH][8], g2[NCH][8], b2[NCH][8];
+  bool in[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (i * TPR + t) * 8;
+    in[i] = c < a.d;
+    if (!in[i]) continue;
+    float gate[8];
+    load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
+    load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, A[i]);
+    load_weight<8>(after_wait(a.g2), a.w_bf16, c, 1.f, g2[i]);
+    if constexpr (BIAS) {
+      load_weight<8>(after_wait(a.b1), a.w_bf16, c, 0.f, B[i]);
+      load_weight<8>(after_wait(a.b2), a.w_bf16, c, 0.f, b2[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      A[i][j] *= a.beta * gate[j];
+      if constexpr (BIAS) B[i][j] *= a.beta * gate[j];
+    }
+  }
+  int par = 0;
+  const auto sum = [&](float v) {
+    const float s = row_sum<TPR>(v, red[par]);
+    par ^= 1;
+    return s;
+  };
+  for (int k = 0; k < rows; ++k) {
+    const long long row = row0 + static_cast<long long>(k) * step;
+    float mean1 = 0.f, rstd1 = 1.f, mean2 = 0.f, rstd2 = 1.f, s = 0.f;
+    float y[NCH][8], r[NCH][8];
+    feed.wait();
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+      if (in[i]) {
+        feed.template get<0>(i, r[i]);
+        if (a.y != nullptr) feed.template get<1>(i, y[i]);
+      }
+    feed.next();
+    const auto each = [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        if (!in[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f(i, j);
+      }
+    };
+    if (a.post == MOE_NORM_LAYER) {
+      each([&](int i, int j) { s += y[i][j]; });
+      mean1 = sum(s) * inv_d;
+      each([&](int i, int j) { y[i][j] -= mean1; });
+    }
+    if (a.post != MOE_NORM_NONE) {
+      s = 0.f;
+      each([&](int i, int j) { s = fmaf(y[i][j], y[i][j], s); });
+      rstd1 = 1.0f / sqrtf(sum(s) * inv_d + a.eps);
+    }
+    each([&](int i, int j) {
+      float v = a.alpha * r[i][j];
+      if (a.y != nullptr) v = fmaf(A[i][j], y[i][j] * rstd1, BIAS ? v + B[i][j] : v);
+      r[i][j] = rounded<TX>(v);
+    });
+    if (a.r != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) put8(static_cast<TX*>(a.r) + row * a.ldr + (i * TPR + t) * 8, r[i]);
+    }
+    if (a.pre == MOE_NORM_LAYER) {
+      s = 0.f;
+      each([&](int i, int j) { s += r[i][j]; });
+      mean2 = sum(s) * inv_d;
+      each([&](int i, int j) { r[i][j] -= mean2; });
+    }
+    if (a.pre != MOE_NORM_NONE) {
+      s = 0.f;
+      each([&](int i, int j) { s = fmaf(r[i][j], r[i][j], s); });
+      rstd2 = 1.0f / sqrtf(sum(s) * inv_d + a.eps);
+      each([&](int i, int j) { r[i][j] = fmaf(r[i][j] * rstd2, g2[i][j], BIAS ? b2[i][j] : 0.f); });
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) put8(static_cast<TY*>(a.n) + row * a.ldn + (i * TPR + t) * 8, r[i]);
+    }
+    if (t == 0 && a.stats != nullptr) {
+      const size_t T = a.T;
+      a.stats[row] = mean1;
+      a.stats[T + row] = rstd1;
+      a.stats[2 * T + row] = mean2;
+      a.stats[3 * T + row] = rstd2;
+    }
+  }
+}
+
+// BIAS: the sums over the rows that only the betas' gradients need (and, with a beta, the gate's) are wanted.
+template <typename TX, typename TY, int NCH, int TPR, bool BIAS>
+__global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_kernel(const JoinArgs a) {
+  grid_wait();
+  constexpr int ROWS = block_threads(TPR) / TPR;
+  __shared__ __align__(16) float red[2][64];
+  extern __shared__ __align__(16) uint8_t ring[];
+  const int t = ROWS > 1 ? threadIdx.x % TPR : threadIdx.x, lane = threadIdx.x & 31;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
+  const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
+  RowFeed<NCH, TPR, TY, TX, TX, TY> feed;  // dn, r, dr, y
+  feed.init(ring, t, a.d, rows);
+  feed.tensor(0, after_wait(a.dn), a.lddn, row0, step);
+  feed.tensor(1, a.pre != MOE_NORM_NONE ? after_wait(a.r) : nullptr, a.ldr, row0, step);
+  feed.tensor(2, after_wait(a.dr), a.lddr, row0, step);
+  feed.tensor(3, after_wait(a.y), a.ldy, row0, step);
+  feed.prime();
+  float A[NCH][8], g2[NCH][8], S1[NCH][8], S0[NCH][8], P1[NCH][8], P0[NCH][8];
+  bool in[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (i * TPR + t) * 8;
+    in[i] = c < a.d;
+    if (in[i]) {
+      float gate[8];
+      load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
+      load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, A[i]);
+      load_weight<8>(after_wait(a.g2), a.w_bf16, c, 1.f, g2[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) A[i][j] *= a.beta * gate[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) S1[i][j] = S0[i][j] = P1[i][j] = P0[i][j] = 0.f;
+  }
+  int par = 0;
+  const auto sums = [&](float u, float v) {
+    const float2 s = row_sum<TPR>(u, v, red[par]);
+    par ^= 1;
+    return s;
+  };
+  // lane l holds the statistics of rows l, l + 32, ... of this block: one wait in 32 rows
+  float st[4] = {0.f, 1.f, 0.f, 1.f};
+  for (int k = 0; k < rows; ++k) {
+    const long long row = row0 + static_cast<long long>(k) * step;
+    if ((k & 31) == 0 && k + lane < rows && a.stats != nullptr) {
+      const float* p = after_wait(a.stats) + row0 + static_cast<long long>(k + lane) * step;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) st[q] = __ldg(p + static_cast<size_t>(q) * a.T);
+    }
+    const float mean1 = a.post == MOE_NORM_LAYER ? __shfl_sync(0xffffffffu, st[0], k & 31) : 0.f;
+    const float rstd1 = a.post != MOE_NORM_NONE ? __shfl_sync(0xffffffffu, st[1], k & 31) : 1.f;
+    const float mean2 = a.pre == MOE_NORM_LAYER ? __shfl_sync(0xffffffffu, st[2], k & 31) : 0.f;
+    const float rstd2 = a.pre != MOE_NORM_NONE ? __shfl_sync(0xffffffffu, st[3], k & 31) : 1.f;
+    const auto each = [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        if (!in[i]) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f(i, j);
+      }
+    };
+    float D[NCH][8], h[NCH][8];  // the pre norm's gamma dn, then the gradient of r; rhat, then yhat
+    feed.wait();
+    if (a.pre != MOE_NORM_NONE) {
+      float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) {
+          feed.template get<0>(i, D[i]);
+          feed.template get<1>(i, h[i]);
+        }
+      each([&](int i, int j) {
+        h[i][j] = (h[i][j] - mean2) * rstd2;
+        P1[i][j] = fmaf(D[i][j], h[i][j], P1[i][j]);
+        if constexpr (BIAS) P0[i][j] += D[i][j];
+        D[i][j] *= g2[i][j];
+        s1 += D[i][j];
+        s2 = fmaf(D[i][j], h[i][j], s2);
+      });
+      const float2 s = sums(s1, s2);
+      const float m1 = a.pre == MOE_NORM_LAYER ? s.x * inv_d : 0.f, m2 = s.y * inv_d;
+      each([&](int i, int j) { D[i][j] = rstd2 * (D[i][j] - m1 - h[i][j] * m2); });
+    } else {
+      each([&](int i, int j) { D[i][j] = 0.f; });
+    }
+    if (a.dr != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) {
+          float v[8];
+          feed.template get<2>(i, v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) D[i][j] += v[j];
+        }
+    }
+    if (a.y != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) feed.template get<3>(i, h[i]);
+    }
+    feed.next();
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = a.alpha * D[i][j];
+          put8(static_cast<TX*>(a.dx) + row * a.lddx + (i * TPR + t) * 8, v);
+        }
+    }
+    if (a.y != nullptr) {
+      float s1 = 0.f, s2 = 0.f;
+      each([&](int i, int j) {
+        h[i][j] = (h[i][j] - mean1) * rstd1;
+        S1[i][j] = fmaf(D[i][j], h[i][j], S1[i][j]);
+        if constexpr (BIAS) S0[i][j] += D[i][j];
+        D[i][j] *= A[i][j];
+        s1 += D[i][j];
+        s2 = fmaf(D[i][j], h[i][j], s2);
+      });
+      if (a.post != MOE_NORM_NONE) {
+        const float2 s = sums(s1, s2);
+        const float m1 = a.post == MOE_NORM_LAYER ? s.x * inv_d : 0.f, m2 = s.y * inv_d;
+        each([&](int i, int j) { D[i][j] = rstd1 * (D[i][j] - m1 - h[i][j] * m2); });
+      }
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (in[i]) put8(static_cast<TY*>(a.dy) + row * a.lddy + (i * TPR + t) * 8, D[i]);
+    }
+  }
+  if (a.part == nullptr) return;
+  float* part = a.part + static_cast<size_t>(blockIdx.x) * SUMS * a.d;
+  // a block of several rows: its warps own the same columns; they are added in warp order
+  __shared__ float4 acc[ROWS > 1 ? ROWS - 1 : 1][32];
+  const int w = threadIdx.x / TPR;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    if constexpr (ROWS > 1) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        __syncthreads();
+        if (w > 0) acc[w - 1][t] = make_float4(S1[i][j], S0[i][j], P1[i][j], P0[i][j]);
+        __syncthreads();
+        if (w == 0) {
+#pragma unroll
+          for (int q = 0; q < ROWS - 1; ++q) {
+            const float4 v = acc[q][t];
+            S1[i][j] += v.x;
+            S0[i][j] += v.y;
+            P1[i][j] += v.z;
+            P0[i][j] += v.w;
+          }
+        }
+      }
+    }
+    const int c = (i * TPR + t) * 8;
+    if (w != 0 || !in[i]) continue;
+    put8(part + c, S1[i]);
+    put8(part + 2 * static_cast<size_t>(a.d) + c, P1[i]);
+    put8(part + a.d + c, S0[i]);
+    put8(part + 3 * static_cast<size_t>(a.d) + c, P0[i]);
+  }
+}
+
 struct GradOut {
   float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
 };
@@ -290,15 +674,59 @@ __global__ void __launch_bounds__(1024) join_partials_kernel(const JoinArgs a, i
   if (o.pre_beta) o.pre_beta[c] = t[3];
 }
 
+template <typename TX, typename TY, int NCH, int TPR>
+cudaError_t launch_fwd_rows(const JoinArgs& a, cudaStream_t s) {
+  constexpr int ROWS = block_threads(TPR) / TPR, smem = RowFeed<NCH, TPR, TX, TY>::smem_bytes;
+  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, fwd_blocks(TPR) * static_cast<long long>(device_sm_count())));
+  const auto kernel = a.b1 || a.b2 ? join_fwd_kernel<TX, TY, NCH, TPR, true> : join_fwd_kernel<TX, TY, NCH, TPR, false>;
+  if (smem > 40 * 1024) {  // beside the static shared memory
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(kernel, grid, block_threads(TPR), smem, s, a);
+}
+template <typename TX, typename TY, int NCH, int TPR>
+cudaError_t launch_bwd_rows(const JoinArgs& a, bool bias, cudaStream_t s, int& blocks) {
+  constexpr int ROWS = block_threads(TPR) / TPR, smem = RowFeed<NCH, TPR, TY, TX, TX, TY>::smem_bytes;
+  blocks = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, std::min(bwd_blocks(TPR) * device_sm_count(), BWD_MAX_BLOCKS)));
+  const auto kernel = bias ? join_bwd_kernel<TX, TY, NCH, TPR, true> : join_bwd_kernel<TX, TY, NCH, TPR, false>;
+  if (smem > 40 * 1024) {  // beside the static shared memory
+    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
+    if (err != cudaSuccess) return err;
+  }
+  return launch_dependent(kernel, blocks, block_threads(TPR), smem, s, a);
+}
+
+// Rows that move 16 bytes at a time go through registers up to a width of 8192, others through the kernels of any width.
+constexpr int REGISTER_WIDTH = 8192;
+
 template <typename TX, typename TY>
-cudaError_t launch_fwd(const JoinArgs& a, cudaStream_t s) {
+cudaError_t launch_fwd(const JoinArgs& a, bool vec, cudaStream_t s) {
+  const int chunks = a.d / 8;
+  if (vec && a.d <= REGISTER_WIDTH) {
+    if (chunks <= 32) return launch_fwd_rows<TX, TY, 1, 32>(a, s);
+    if (chunks <= 64) return launch_fwd_rows<TX, TY, 2, 32>(a, s);
+    if (chunks <= 128) return launch_fwd_rows<TX, TY, 1, 128>(a, s);
+    if (chunks <= 256) return launch_fwd_rows<TX, TY, 2, 128>(a, s);
+    if (chunks <= 512) return launch_fwd_rows<TX, TY, 2, 256>(a, s);
+    return launch_fwd_rows<TX, TY, 2, 512>(a, s);
+  }
   join_fwd_wide_kernel<TX, TY><<<std::min(a.T, 1 << 20), WIDE_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-// `blocks`: the rows of partial sums that the launch leaves
+// `blocks`: the rows of partial sums that the launch leaves; `bias`: all four sums are wanted
 template <typename TX, typename TY>
-cudaError_t launch_bwd(const JoinArgs& a, cudaStream_t s, int& blocks) {
+cudaError_t launch_bwd(const JoinArgs& a, bool vec, bool bias, cudaStream_t s, int& blocks) {
+  const int chunks = a.d / 8;
+  if (vec && a.d <= REGISTER_WIDTH) {
+    if (chunks <= 32) return launch_bwd_rows<TX, TY, 1, 32>(a, bias, s, blocks);
+    if (chunks <= 64) return launch_bwd_rows<TX, TY, 2, 32>(a, bias, s, blocks);
+    if (chunks <= 128) return launch_bwd_rows<TX, TY, 1, 128>(a, bias, s, blocks);
+    if (chunks <= 256) return launch_bwd_rows<TX, TY, 2, 128>(a, bias, s, blocks);
+    if (chunks <= 512) return launch_bwd_rows<TX, TY, 2, 256>(a, bias, s, blocks);
+    return launch_bwd_rows<TX, TY, 2, 512>(a, bias, s, blocks);
+  }
   const int grid = std::min(a.T, 1 << 20);
   blocks = std::min(a.T, BWD_MAX_BLOCKS);
   if (a.pre != MOE_NORM_NONE) join_bwd_means_kernel<TX, TY><<<grid, WIDE_THREADS, 0, s>>>(a);
@@ -307,6 +735,9 @@ cudaError_t launch_bwd(const JoinArgs& a, cudaStream_t s, int& blocks) {
   join_bwd_wide_kernel<TX, TY><<<grid, WIDE_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
+
+// 16-byte rows: base, pitch and width
+bool rows16(const void* p, long long ld, int es) { return p == nullptr || (aligned16(p) && ld * es % 16 == 0); }
 
 size_t part_floats(int T, int d) { return static_cast<size_t>(std::min(T, BWD_MAX_BLOCKS)) * SUMS * d; }
 
@@ -372,9 +803,11 @@ moe_status_t moe_residual_norm_fwd(const void* x, int x_dtype, long long ldx, co
   a.beta = branch_scale;
   a.stats = stats;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_fwd<bf16, bf16>(a, s)
-                          : y_dtype == MOE_DTYPE_BF16 ? launch_fwd<float, bf16>(a, s)
-                                                      : launch_fwd<float, float>(a, s);
+  const bool vec = d % 8 == 0 && rows16(x, ldx, ex) && rows16(y, ldy, ey) && rows16(r, ldr, ex) && rows16(n, ldn, ey) &&
+                   aligned16(post_gamma) && aligned16(post_beta) && aligned16(gate) && aligned16(pre_gamma) && aligned16(pre_beta);
+  const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_fwd<bf16, bf16>(a, vec, s)
+                          : y_dtype == MOE_DTYPE_BF16 ? launch_fwd<float, bf16>(a, vec, s)
+                                                      : launch_fwd<float, float>(a, vec, s);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
@@ -445,9 +878,12 @@ moe_status_t moe_residual_norm_bwd(const void* dn, long long lddn, const void* d
   a.row = static_cast<float*>(ws) + (T > 0 ? part_floats(T, d) : 0);
   int blocks = 0;
   if (T > 0) {
-    const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_bwd<bf16, bf16>(a, s, blocks)
-                            : y_dtype == MOE_DTYPE_BF16 ? launch_bwd<float, bf16>(a, s, blocks)
-                                                        : launch_bwd<float, float>(a, s, blocks);
+    const bool vec = d % 8 == 0 && rows16(dn, lddn, ey) && rows16(dr, lddr, ex) && rows16(r, ldr, ex) && rows16(y, ldy, ey) &&
+                     rows16(dx, lddx, ex) && rows16(dy, lddy, ey) && aligned16(post_gamma) && aligned16(gate) && aligned16(pre_gamma) && aligned16(ws);
+    const bool bias = d_post_beta || d_pre_beta || (d_gate && post_beta);
+    const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_bwd<bf16, bf16>(a, vec, bias, s, blocks)
+                            : y_dtype == MOE_DTYPE_BF16 ? launch_bwd<float, bf16>(a, vec, bias, s, blocks)
+                                                        : launch_bwd<float, float>(a, vec, bias, s, blocks);
     if (err != cudaSuccess) return cuda_fail(err);
   }
   if (!wgrad) return MOE_OK;
