@@ -17,6 +17,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "internal.h"
 #include "rows.cuh"
@@ -134,14 +136,16 @@ __device__ __forceinline__ float stochastic_bf16(float x, uint32_t u) {
 // ------------------------------------------------------------------ 8-bit states
 // An E4M3 magnitude is the top 7 bits below the sign of an fp32 value 2^120 times smaller: the exponent biases differ
 // by 120, and the subnormals of both types meet.
-constexpr float E4M3_UP = 0x1p120f, E4M3_DOWN = 0x1p-120f;
+constexpr float E4M3_DOWN = 0x1p-120f;
 
 __device__ __forceinline__ float block_scale(uint32_t byte) {
   return byte == 0xFF ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte == 0 ? 0x00400000u : byte << 23);
 }
-__device__ __forceinline__ float from_e4m3(uint32_t code, float scale) {
-  const float v = __uint_as_float((code & 0x7Fu) << 20) * E4M3_UP * scale;
-  return code & 0x80u ? -v : v;
+// two codes of a word
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w, float scale) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
+  const float2 v = __half22float2(__half2(h));
+  return make_float2(v.x * scale, v.y * scale);
 }
 // the scale byte of a block from the bits of its largest magnitude
 __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
@@ -151,23 +155,32 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 }
 
 // Eight values of this thread's quarter of a block into codes; returns the scale byte of the block. All threads of the warp call it.
+// KEEP: the values are not negative, and what is not 0 does not become 0.
 template <bool KEEP, int SHIFT>
 __device__ __forceinline__ uint32_t to_e4m3(const float (&x)[VB], const uint32_t (&rnd)[VB], uint32_t (&w)[2]) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < VB; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);  // by bits: a NaN is the largest
+  for (int i = 0; i < VB; ++i) top = max(top, KEEP ? __float_as_uint(x[i]) : __float_as_uint(x[i]) & 0x7FFFFFFFu);  // by bits: a NaN is the largest
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const uint32_t byte = scale_byte(top);
   w[0] = w[1] = 0;
   if (byte == 0xFF) return byte;
+  // 2^-s 2^-120 is an fp32 (subnormal from s = 7 on) up to s = 29; states above 2^38 take the two steps apart
   const float inv = __uint_as_float((254u - byte) << 23);
+  const float first = byte > 150 ? inv : 1.0f, second = byte > 150 ? E4M3_DOWN : inv * E4M3_DOWN;
   uint32_t c[VB];
+  if (byte > 150) {
+#pragma unroll
+    for (int i = 0; i < VB; ++i) c[i] = __float_as_uint(fabsf(x[i]) * first * second);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i) c[i] = __float_as_uint(fabsf(x[i]) * second);
+  }
 #pragma unroll
   for (int i = 0; i < VB; ++i) {
-    const float a = fabsf(x[i]) * inv;
-    c[i] = (__float_as_uint(a * E4M3_DOWN) + (((rnd[i] >> SHIFT) & 0xFFFFu) << 4)) >> 20;
-    if (KEEP) c[i] = a > 0.f ? max(c[i], 1u) : c[i];
+    c[i] = (c[i] + (SHIFT == 16 ? (rnd[i] >> 12) & 0xFFFF0u : (rnd[i] << 4) & 0xFFFF0u)) >> 20;
+    if (KEEP) c[i] = x[i] > 0.f ? max(c[i], 1u) : c[i];
   }
 #pragma unroll
   for (int i = 0; i < VB; i += 4) {
@@ -193,87 +206,127 @@ struct StepArgs {
   bool last;        // the call's last launch counts the step
 };
 
+// What a thread reads of one round, as it lies in memory where that takes 16-byte accesses
+template <int BITS>
+struct Raw {
+  float g[VB], p[VB], m[VB], v[VB];
+  uint32_t wm[2], wv[2], sm, sv;
+
+  __device__ __forceinline__ void load(const moe_adamw_tensor_t& q, long long i0, int k, bool wide) {
+    if (q.g_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.g) + i0, k, wide, g);
+    else load8(static_cast<const float*>(q.g) + i0, k, wide, g);
+    if (q.p_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.p) + i0, k, wide, p);
+    else load8(static_cast<const float*>(q.p) + i0, k, wide, p);
+    if constexpr (BITS == 8) {
+      load8(static_cast<const uint8_t*>(q.m) + i0, k, wide, wm);
+      load8(static_cast<const uint8_t*>(q.v) + i0, k, wide, wv);
+      sm = k > 0 ? q.m_scale[i0 >> 5] : 0;
+      sv = k > 0 ? q.v_scale[i0 >> 5] : 0;
+    } else {
+      load8(static_cast<const float*>(q.m) + i0, k, wide, m);
+      load8(static_cast<const float*>(q.v) + i0, k, wide, v);
+    }
+  }
+};
+
+struct TensorStep {
+  float c, step, root, keep;
+  uint32_t key;
+};
+
+// One round: eight elements from i0, k of them the tensor's (FULL: all, by 16-byte accesses). All threads of a warp call it.
+template <int BITS, bool FULL>
+__device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const StepArgs& a, const TensorStep& u, long long i0, int k,
+                                            bool wide, Raw<BITS>& d) {
+  if constexpr (FULL) k = VB, wide = true;
+  float r[VB];
+  if constexpr (BITS == 8) {
+    const float sm = block_scale(d.sm), sv = block_scale(d.sv);
+#pragma unroll
+    for (int i = 0; i < VB; i += 2) {
+      const float2 m = from_e4m3x2(d.wm[i >> 2] >> (8 * (i & 3)), sm), v = from_e4m3x2(d.wv[i >> 2] >> (8 * (i & 3)), sv);
+      d.m[i] = m.x, d.m[i + 1] = m.y;
+      d.v[i] = v.x * v.x, d.v[i + 1] = v.y * v.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VB; ++i) {
+    // Each operation rounded by itself: a stochastic rounding goes the other way where its argument differs in the last
+    // place, and m and v are to be what the formula written out gives.
+    const float gc = d.g[i] * u.c;
+    d.m[i] = __fadd_rn(__fmul_rn(a.b1, d.m[i]), __fmul_rn(a.omb1, gc));
+    d.v[i] = __fadd_rn(__fmul_rn(a.b2, d.v[i]), __fmul_rn(__fmul_rn(a.omb2, gc), gc));
+    r[i] = sqrtf(d.v[i]);
+    // the quotient to two units: it is a small part of p
+    d.p[i] = fmaf(d.p[i], u.keep, -__fdividef(u.step * d.m[i], fmaf(r[i], u.root, a.eps)));
+  }
+  uint32_t rnd[VB];
+  if (BITS == 8 || q.p_dtype == MOE_DTYPE_BF16) {
+    const uint32_t x0 = u.key + static_cast<uint32_t>(i0) * 0x9E3779B9u + static_cast<uint32_t>(i0 >> 32) * 0x85EBCA6Bu;
+#pragma unroll
+    for (int i = 0; i < VB; ++i) rnd[i] = mix(x0 + static_cast<uint32_t>(i) * 0x9E3779B9u);
+  }
+  if (q.p_dtype == MOE_DTYPE_BF16) {
+#pragma unroll
+    for (int i = 0; i < VB; ++i) d.p[i] = stochastic_bf16(d.p[i], (rnd[i] >> 8) & 0xFFFFu);
+    store8(static_cast<bf16*>(q.p) + i0, k, wide, d.p);
+  } else {
+    store8(static_cast<float*>(q.p) + i0, k, wide, d.p);
+    if (q.copy != nullptr) store8(static_cast<bf16*>(q.copy) + i0, k, wide, d.p);
+  }
+  if constexpr (BITS == 8) {
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int i = 0; i < VB; ++i) {  // what lies behind the tensor's end takes no part in its last block
+        d.m[i] = i < k ? d.m[i] : 0.f;
+        r[i] = i < k ? r[i] : 0.f;
+      }
+    }
+    uint32_t w[2];
+    uint32_t byte = to_e4m3<false, 0>(d.m, rnd, w);
+    store8(static_cast<uint8_t*>(q.m) + i0, k, wide, w);
+    if (k > 0 && (threadIdx.x & 3) == 0) q.m_scale[i0 >> 5] = static_cast<uint8_t>(byte);
+    byte = to_e4m3<true, 16>(r, rnd, w);
+    store8(static_cast<uint8_t*>(q.v) + i0, k, wide, w);
+    if (k > 0 && (threadIdx.x & 3) == 0) q.v_scale[i0 >> 5] = static_cast<uint8_t>(byte);
+  } else {
+    store8(static_cast<float*>(q.m) + i0, k, wide, d.m);
+    store8(static_cast<float*>(q.v) + i0, k, wide, d.v);
+  }
+}
+
 template <int BITS>
 __global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Batch batch, const StepArgs a) {
   grid_wait();
-  const float c = a.grad_scale ? *after_wait(a.grad_scale) : 1.0f;
-  if (c != c) return;  // the norm was not finite: the step is skipped
+  TensorStep u;
+  u.c = a.grad_scale ? *after_wait(a.grad_scale) : 1.0f;
+  if (u.c != u.c) return;  // the norm was not finite: the step is skipped
   const int t = *reinterpret_cast<volatile int32_t*>(a.steps) + 1;
   if (blockIdx.x < batch.chunk0[batch.count]) {
     const int j = find_tensor(batch, blockIdx.x);
     const moe_adamw_tensor_t& q = batch.t[j];
     const float lr = a.lr_scale ? a.lr * *after_wait(a.lr_scale) : a.lr;
-    const float step = lr / -expm1f(static_cast<float>(t) * a.log_b1);
-    const float root = 1.0f / sqrtf(-expm1f(static_cast<float>(t) * a.log_b2));
-    const float keep = fmaf(-lr, q.weight_decay, 1.0f);
-    const bool wide = batch.wide[j] != 0;
-    const uint32_t key = mix(a.seed ^ mix(0x9E3779B9u * static_cast<uint32_t>(t) + static_cast<uint32_t>(batch.first + j)));
+    u.step = lr / -expm1f(static_cast<float>(t) * a.log_b1);
+    u.root = 1.0f / sqrtf(-expm1f(static_cast<float>(t) * a.log_b2));
+    u.keep = fmaf(-lr, q.weight_decay, 1.0f);
+    u.key = mix(a.seed ^ mix(0x9E3779B9u * static_cast<uint32_t>(t) + static_cast<uint32_t>(batch.first + j)));
     const long long base = static_cast<long long>(blockIdx.x - batch.chunk0[j]) * CHUNK;
+    constexpr int ROUNDS = CHUNK / (THREADS * VB);
+    const long long i0 = base + threadIdx.x * VB;
+    if (batch.wide[j] != 0 && base + CHUNK <= q.n) {
+      Raw<BITS> d[ROUNDS];  // all loads before the first store
 #pragma unroll
-    for (int round = 0; round < CHUNK / (THREADS * VB); ++round) {
-      const long long i0 = base + (round * THREADS + threadIdx.x) * VB;
-      const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), q.n - i0)));  // elements of this thread
-      float g[VB], m[VB], v[VB], p[VB];
-      if (q.g_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.g) + i0, k, wide, g);
-      else load8(static_cast<const float*>(q.g) + i0, k, wide, g);
-      if (q.p_dtype == MOE_DTYPE_BF16) load8(static_cast<const bf16*>(q.p) + i0, k, wide, p);
-      else load8(static_cast<const float*>(q.p) + i0, k, wide, p);
-      if constexpr (BITS == 8) {
-        uint32_t wm[2], wv[2];
-        load8(static_cast<const uint8_t*>(q.m) + i0, k, wide, wm);
-        load8(static_cast<const uint8_t*>(q.v) + i0, k, wide, wv);
-        const float sm = k > 0 ? block_scale(q.m_scale[i0 >> 5]) : 0.f, sv = k > 0 ? block_scale(q.v_scale[i0 >> 5]) : 0.f;
+      for (int i = 0; i < ROUNDS; ++i) d[i].load(q, i0 + i * THREADS * VB, VB, true);
 #pragma unroll
-        for (int i = 0; i < VB; ++i) {
-          m[i] = from_e4m3(wm[i >> 2] >> (8 * (i & 3)), sm);
-          const float r = from_e4m3(wv[i >> 2] >> (8 * (i & 3)), sv);
-          v[i] = r * r;
-        }
-      } else {
-        load8(static_cast<const float*>(q.m) + i0, k, wide, m);
-        load8(static_cast<const float*>(q.v) + i0, k, wide, v);
-      }
-      float r[VB];
-#pragma unroll
-      for (int i = 0; i < VB; ++i) {
-        // Each operation rounded by itself: a stochastic rounding goes the other way where its argument differs in the last
-        // place, and m and v are to be what the formula written out gives.
-        const float gc = g[i] * c;
-        m[i] = __fadd_rn(__fmul_rn(a.b1, m[i]), __fmul_rn(a.omb1, gc));
-        v[i] = __fadd_rn(__fmul_rn(a.b2, v[i]), __fmul_rn(__fmul_rn(a.omb2, gc), gc));
-        r[i] = sqrtf(v[i]);
-        p[i] = fmaf(p[i], keep, -(step * m[i]) / fmaf(r[i], root, a.eps));
-      }
-      uint32_t rnd[VB];
-      if (BITS == 8 || q.p_dtype == MOE_DTYPE_BF16) {
-        const uint32_t x0 = key + static_cast<uint32_t>(i0) * 0x9E3779B9u + static_cast<uint32_t>(i0 >> 32) * 0x85EBCA6Bu;
-#pragma unroll
-        for (int i = 0; i < VB; ++i) rnd[i] = mix(x0 + static_cast<uint32_t>(i) * 0x9E3779B9u);
-      }
-      if (q.p_dtype == MOE_DTYPE_BF16) {
-#pragma unroll
-        for (int i = 0; i < VB; ++i) p[i] = stochastic_bf16(p[i], (rnd[i] >> 8) & 0xFFFFu);
-        store8(static_cast<bf16*>(q.p) + i0, k, wide, p);
-      } else {
-        store8(static_cast<float*>(q.p) + i0, k, wide, p);
-        if (q.copy != nullptr) store8(static_cast<bf16*>(q.copy) + i0, k, wide, p);
-      }
-      if constexpr (BITS == 8) {
-#pragma unroll
-        for (int i = 0; i < VB; ++i) {  // what lies behind the tensor's end takes no part in its last block
-          m[i] = i < k ? m[i] : 0.f;
-          r[i] = i < k ? r[i] : 0.f;
-        }
-        uint32_t w[2];
-        uint32_t byte = to_e4m3<false, 0>(m, rnd, w);
-        store8(static_cast<uint8_t*>(q.m) + i0, k, wide, w);
-        if (k > 0 && (threadIdx.x & 3) == 0) q.m_scale[i0 >> 5] = static_cast<uint8_t>(byte);
-        byte = to_e4m3<true, 16>(r, rnd, w);
-        store8(static_cast<uint8_t*>(q.v) + i0, k, wide, w);
-        if (k > 0 && (threadIdx.x & 3) == 0) q.v_scale[i0 >> 5] = static_cast<uint8_t>(byte);
-      } else {
-        store8(static_cast<float*>(q.m) + i0, k, wide, m);
-        store8(static_cast<float*>(q.v) + i0, k, wide, v);
+      for (int i = 0; i < ROUNDS; ++i) adamw_round<BITS, true>(q, a, u, i0 + i * THREADS * VB, VB, true, d[i]);
+    } else {
+      const bool wide = batch.wide[j] != 0;
+      for (int i = 0; i < ROUNDS; ++i) {
+        const long long at = i0 + i * THREADS * VB;
+        const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), q.n - at)));  // elements of this thread
+        Raw<BITS> d;
+        d.load(q, at, k, wide);
+        adamw_round<BITS, false>(q, a, u, at, k, wide, d);
       }
     }
   }
@@ -317,20 +370,23 @@ __global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constan
 }
 
 // The norm and the coefficient from the partial sums, in index order within each thread and by a fixed tree.
-__global__ void __launch_bounds__(1024) grad_norm_end_kernel(const double* part, int blocks, float max_norm, float* norm) {
-  __shared__ double acc[1024];
+__global__ void __launch_bounds__(256) grad_norm_end_kernel(const double* part, int blocks, float max_norm, float* norm) {
+  __shared__ double acc[8];
   grid_wait();
   part = after_wait(part);
-  double s = 0.0;
-  for (int b = threadIdx.x; b < blocks; b += 1024) s += part[b];
-  acc[threadIdx.x] = s;
+  constexpr int ROUNDS = (NORM_BLOCKS + 255) / 256;
+  double v[ROUNDS], s = 0.0;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) v[i] = threadIdx.x + 256 * i < blocks ? part[threadIdx.x + 256 * i] : 0.0;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) s += v[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) acc[threadIdx.x >> 5] = s;
   __syncthreads();
-  for (int o = 512; o > 0; o >>= 1) {
-    if (threadIdx.x < o) acc[threadIdx.x] += acc[threadIdx.x + o];
-    __syncthreads();
-  }
   if (threadIdx.x != 0) return;
-  const float n = static_cast<float>(sqrt(acc[0]));
+  s = ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+  const float n = static_cast<float>(sqrt(s));
   norm[0] = n;
   norm[1] = n <= 3.402823466e38f ? max_norm / fmaxf(n, max_norm) : __uint_as_float(0x7FC00000u);
 }
@@ -413,7 +469,7 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float m
     i += std::max(n, 1);
   }
   if (err == cudaSuccess)
-    err = launch_dependent(grad_norm_end_kernel, 1, 1024, 0, s, static_cast<const double*>(part), blocks, max_norm, norm);
+    err = launch_dependent(grad_norm_end_kernel, 1, 256, 0, s, static_cast<const double*>(part), blocks, max_norm, norm);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 

@@ -12,6 +12,7 @@
 // block order. No atomics: the results do not depend on scheduling.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -276,41 +277,52 @@ struct RowFeed {
   static constexpr int slot_bytes = before(NT);
   static constexpr int depth = slot_bytes <= 16 * 1024 ? 4 : slot_bytes <= 32 * 1024 ? 3 : slot_bytes <= 96 * 1024 ? 2 : 1;  // rows on their way
   static constexpr int smem_bytes = depth * slot_bytes;
-  const uint8_t* at[NT];  // the next row to start (nullptr: no such tensor)
+  // A lane copies 16 bytes at a time: of bf16 rows its own chunk; of fp32 rows, whose chunks are 32 bytes, one quarter of
+  // those of two lanes, so that a warp's accesses are contiguous. Its first address in the next row of each tensor:
+  const uint8_t* at[NT];
   long long step[NT];     // bytes from one row of this block to its next
-  uint8_t* mem;
-  int c0, cw, lane;       // first column of this thread and of its warp
-  int d, left;
-  uint32_t slot;
+  bool on[NT];            // there is such a tensor
+  bool in2[NCH], in4[NCH][2];  // what this lane copies lies in the row: of bf16, of fp32 rows
+  uint32_t base, slot;    // shared-memory address of the ring, byte offset of the oldest row
+  uint32_t own2, own4, get4;  // this lane's offsets: bf16 chunks, fp32 copies, fp32 chunks
+  int c2, c4, left;       // first column that this lane copies of bf16 and of fp32 rows; rows not started yet
 
-  __device__ __forceinline__ void init(uint8_t* smem, int t, int width, int rows) {
-    mem = smem;
-    lane = threadIdx.x & 31;
-    c0 = t * 8;
-    cw = (t & ~31) * 8;
-    d = width;
+  __device__ __forceinline__ void init(uint8_t* smem, int t, int d, int rows) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x & ~31;
+    base = smem_u32(smem);
+    own2 = threadIdx.x * 16;
+    own4 = warp * 32 + lane * 16;
+    get4 = threadIdx.x * 32;
+    c2 = t * 8;
+    c4 = (t & ~31) * 8 + lane * 4;
     left = rows;
     slot = 0;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      in2[i] = c2 + i * TPR * 8 < d;
+      in4[i][0] = c4 + i * TPR * 8 < d;
+      in4[i][1] = c4 + i * TPR * 8 + 128 < d;
+    }
   }
   __device__ __forceinline__ void tensor(int k, const void* p, long long ld, long long row0, int rows_step) {
-    at[k] = p ? static_cast<const uint8_t*>(p) + row0 * ld * size(k) : nullptr;
+    on[k] = p != nullptr;
+    at[k] = static_cast<const uint8_t*>(p) + (row0 * ld + (size(k) == 2 ? c2 : c4)) * size(k);
     step[k] = rows_step * ld * size(k);
-  }
-  // this warp's 32 chunks of tensor k, chunk i: 256 elements
-  __device__ __forceinline__ uint8_t* chunk(uint32_t to, int k, int i) const {
-    return mem + to + before(k) + (i * threads + (threadIdx.x & ~31)) * 8 * size(k);
   }
   __device__ __forceinline__ void start(uint32_t to) {
     if (left > 0) {
 #pragma unroll
       for (int k = 0; k < NT; ++k) {
-        if (at[k] == nullptr) continue;
+        if (!on[k]) continue;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-#pragma unroll
-          for (int u = 0; u < size(k) / 2; ++u) {  // 16 bytes a lane: the whole chunk of a lane, or half of those of two
-            const int c = cw + i * TPR * 8 + (u * 32 + lane) * (16 / size(k));
-            if (c < d) copy16_async(smem_u32(chunk(to, k, i)) + (u * 32 + lane) * 16, at[k] + static_cast<size_t>(c) * size(k));
+          const uint32_t chunk = base + to + before(k) + i * threads * 8 * size(k);
+          const uint8_t* src = at[k] + i * TPR * 8 * size(k);
+          if (size(k) == 2) {
+            if (in2[i]) copy16_async(chunk + own2, src);
+          } else {
+            if (in4[i][0]) copy16_async(chunk + own4, src);
+            if (in4[i][1]) copy16_async(chunk + own4 + 512, src + 512);
           }
         }
         at[k] += step[k];
@@ -319,7 +331,25 @@ struct RowFeed {
     }
     copy_commit();
   }
+  // What lies past the end of a row reads as zeros, so that the arithmetic need not ask.
+  __device__ __forceinline__ void clear(uint32_t p) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(p), "r"(0) : "memory");
+  }
   __device__ __forceinline__ void prime() {
+    for (int s = 0; s < depth; ++s) {
+#pragma unroll
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int i = 0; i < NCH; ++i) {
+          const uint32_t chunk = base + s * slot_bytes + before(k) + i * threads * 8 * size(k);
+          if (size(k) == 2) {
+            if (!in2[i] || !on[k]) clear(chunk + own2);
+          } else {
+            if (!in4[i][0] || !on[k]) clear(chunk + own4);
+            if (!in4[i][1] || !on[k]) clear(chunk + own4 + 512);
+          }
+        }
+    }
 #pragma unroll
     for (int s = 0; s < depth; ++s) start(s * slot_bytes);
   }
@@ -330,9 +360,9 @@ struct RowFeed {
   }
   template <int K>
   __device__ __forceinline__ void get(int i, float (&f)[8]) const {
-    const uint8_t* p = chunk(slot, K, i) + lane * 8 * size(K);
-    const uint4 q = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint32_t p = base + slot + before(K) + i * threads * 8 * size(K) + (size(K) == 2 ? own2 : get4);
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(p));
     if constexpr (size(K) == 2) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -340,10 +370,9 @@ struct RowFeed {
         f[2 * j + 1] = bf16_hi(w[j]);
       }
     } else {
-      const float4 r = *reinterpret_cast<const float4*>(p + 16);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[j] = __uint_as_float(w[j]);
-      f[4] = r.x, f[5] = r.y, f[6] = r.z, f[7] = r.w;
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[4]), "=f"(f[5]), "=f"(f[6]), "=f"(f[7]) : "r"(p + 16));
     }
   }
   // everything of the oldest row has been read: start the one that takes its place
@@ -360,9 +389,55 @@ __device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
+// Two fp32 values that one instruction takes together.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ float2 parts(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ void pairs(const float (&f)[8], F2 (&p)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = pair(f[2 * j], f[2 * j + 1]);
+}
+template <typename T>
+__device__ __forceinline__ void put8(T* p, const F2 (&v)[4]) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 q = parts(v[j]);
+    f[2 * j] = q.x;
+    f[2 * j + 1] = q.y;
+  }
+  put8(p, f);
+}
+
 // Blocks on an SM, which size the grids and bound the registers.
 constexpr int fwd_blocks(int tpr) { return 512 / block_threads(tpr); }
-constexpr int bwd_blocks(int tpr) { return tpr <= 128 ? 3 : tpr == 256 ? 1 : 1; }
+constexpr int bwd_blocks(int tpr) { return tpr <= 128 ? 3 : 1; }
 
 // BIAS: some norm has a beta.
 template <typename TX, typename TY, int NCH, int TPR, bool BIAS>
@@ -387,7 +462,11 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR)) join_fwd_
   for (int i = 0; i < NCH; ++i) {
     const int c = (i * TPR + t) * 8;
     in[i] = c < a.d;
-    if (!in[i]) continue;
+    if (!in[i]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) A[i][j] = B[i][j] = g2[i][j] = b2[i][j] = 0.f;
+      continue;
+    }
     float gate[8];
     load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
     load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, A[i]);
@@ -414,24 +493,21 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR)) join_fwd_
     float y[NCH][8], r[NCH][8];
     feed.wait();
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
-      if (in[i]) {
-        feed.template get<0>(i, r[i]);
-        if (a.y != nullptr) feed.template get<1>(i, y[i]);
-      }
+    for (int i = 0; i < NCH; ++i) {
+      feed.template get<0>(i, r[i]);
+      feed.template get<1>(i, y[i]);
+    }
     feed.next();
     const auto each = [&](auto f) {
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        if (!in[i]) continue;
+      for (int i = 0; i < NCH; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) f(i, j);
-      }
     };
     if (a.post == MOE_NORM_LAYER) {
       each([&](int i, int j) { s += y[i][j]; });
       mean1 = sum(s) * inv_d;
-      each([&](int i, int j) { y[i][j] -= mean1; });
+      each([&](int i, int j) { y[i][j] -= in[i] ? mean1 : 0.f; });
     }
     if (a.post != MOE_NORM_NONE) {
       s = 0.f;
@@ -440,7 +516,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR)) join_fwd_
     }
     each([&](int i, int j) {
       float v = a.alpha * r[i][j];
-      if (a.y != nullptr) v = fmaf(A[i][j], y[i][j] * rstd1, BIAS ? v + B[i][j] : v);
+      v = fmaf(A[i][j], y[i][j] * rstd1, BIAS ? v + B[i][j] : v);  // y reads as zeros where there is no branch
       r[i][j] = rounded<TX>(v);
     });
     if (a.r != nullptr) {
@@ -452,7 +528,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR)) join_fwd_
       s = 0.f;
       each([&](int i, int j) { s += r[i][j]; });
       mean2 = sum(s) * inv_d;
-      each([&](int i, int j) { r[i][j] -= mean2; });
+      each([&](int i, int j) { r[i][j] -= in[i] ? mean2 : 0.f; });
     }
     if (a.pre != MOE_NORM_NONE) {
       s = 0.f;
@@ -491,33 +567,40 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
   feed.tensor(2, after_wait(a.dr), a.lddr, row0, step);
   feed.tensor(3, after_wait(a.y), a.ldy, row0, step);
   feed.prime();
-  float A[NCH][8], g2[NCH][8], S1[NCH][8], S0[NCH][8], P1[NCH][8], P0[NCH][8];
+  F2 A[NCH][4], g2[NCH][4], S1[NCH][4], S0[NCH][4], P1[NCH][4], P0[NCH][4];
   bool in[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     const int c = (i * TPR + t) * 8;
     in[i] = c < a.d;
-    if (in[i]) {
-      float gate[8];
-      load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
-      load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, A[i]);
-      load_weight<8>(after_wait(a.g2), a.w_bf16, c, 1.f, g2[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) A[i][j] *= a.beta * gate[j];
+    for (int j = 0; j < 4; ++j) A[i][j] = g2[i][j] = both(0.f);
+    if (in[i]) {
+      float w[8], gate[8];
+      load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
+      load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] *= a.beta * gate[j];
+      pairs(w, A[i]);
+      load_weight<8>(after_wait(a.g2), a.w_bf16, c, 1.f, w);
+      pairs(w, g2[i]);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) S1[i][j] = S0[i][j] = P1[i][j] = P0[i][j] = 0.f;
+    for (int j = 0; j < 4; ++j) S1[i][j] = S0[i][j] = P1[i][j] = P0[i][j] = both(0.f);
   }
   int par = 0;
-  const auto sums = [&](float u, float v) {
-    const float2 s = row_sum<TPR>(u, v, red[par]);
+  const auto sums = [&](F2 u, F2 v) {
+    const float2 p = parts(u), q = parts(v);
+    const float2 s = row_sum<TPR>(p.x + p.y, q.x + q.y, red[par]);
     par ^= 1;
     return s;
   };
+  const F2 alpha = both(a.alpha);
   // lane l holds the statistics of rows l, l + 32, ... of this block: one wait in 32 rows
   float st[4] = {0.f, 1.f, 0.f, 1.f};
-  for (int k = 0; k < rows; ++k) {
-    const long long row = row0 + static_cast<long long>(k) * step;
+  TX* dx = a.dx ? static_cast<TX*>(a.dx) + row0 * a.lddx + t * 8 : nullptr;
+  TY* dy = a.dy ? static_cast<TY*>(a.dy) + row0 * a.lddy + t * 8 : nullptr;
+  for (int k = 0; k < rows; ++k, dx += step * a.lddx, dy += step * a.lddy) {
     if ((k & 31) == 0 && k + lane < rows && a.stats != nullptr) {
       const float* p = after_wait(a.stats) + row0 + static_cast<long long>(k + lane) * step;
 #pragma unroll
@@ -527,106 +610,101 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
     const float rstd1 = a.post != MOE_NORM_NONE ? __shfl_sync(0xffffffffu, st[1], k & 31) : 1.f;
     const float mean2 = a.pre == MOE_NORM_LAYER ? __shfl_sync(0xffffffffu, st[2], k & 31) : 0.f;
     const float rstd2 = a.pre != MOE_NORM_NONE ? __shfl_sync(0xffffffffu, st[3], k & 31) : 1.f;
+    // past the end of a row everything is computed from zeros and weights of 0, and nothing stored
     const auto each = [&](auto f) {
 #pragma unroll
-      for (int i = 0; i < NCH; ++i) {
-        if (!in[i]) continue;
+      for (int i = 0; i < NCH; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f(i, j);
+        for (int j = 0; j < 4; ++j) f(i, j);
+    };
+    const auto get = [&](auto which, F2 (&v)[NCH][4]) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        float f[8];
+        feed.template get<decltype(which)::value>(i, f);
+        pairs(f, v[i]);
       }
     };
-    float D[NCH][8], h[NCH][8];  // the pre norm's gamma dn, then the gradient of r; rhat, then yhat
+    F2 D[NCH][4], h[NCH][4], v[NCH][4];  // the pre norm's gamma dn, then the gradient of r; rhat, then yhat; dr
     feed.wait();
+    F2 k0 = both(0.f), k1 = k0, scale = k0;  // D = scale (gamma dn) + k1 rhat + k0 + dr
     if (a.pre != MOE_NORM_NONE) {
-      float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) {
-          feed.template get<0>(i, D[i]);
-          feed.template get<1>(i, h[i]);
-        }
+      F2 s1 = both(0.f), s2 = s1;
+      const F2 R = both(rstd2), C = both(-mean2 * rstd2);
+      get(std::integral_constant<int, 0>{}, D);
+      get(std::integral_constant<int, 1>{}, h);
       each([&](int i, int j) {
-        h[i][j] = (h[i][j] - mean2) * rstd2;
-        P1[i][j] = fmaf(D[i][j], h[i][j], P1[i][j]);
-        if constexpr (BIAS) P0[i][j] += D[i][j];
-        D[i][j] *= g2[i][j];
-        s1 += D[i][j];
-        s2 = fmaf(D[i][j], h[i][j], s2);
+        h[i][j] = fma2(h[i][j], R, C);
+        P1[i][j] = fma2(D[i][j], h[i][j], P1[i][j]);
+        if constexpr (BIAS) P0[i][j] = add2(P0[i][j], D[i][j]);
+        D[i][j] = mul2(D[i][j], g2[i][j]);
+        s1 = add2(s1, D[i][j]);
+        s2 = fma2(D[i][j], h[i][j], s2);
       });
       const float2 s = sums(s1, s2);
-      const float m1 = a.pre == MOE_NORM_LAYER ? s.x * inv_d : 0.f, m2 = s.y * inv_d;
-      each([&](int i, int j) { D[i][j] = rstd2 * (D[i][j] - m1 - h[i][j] * m2); });
+      scale = R;
+      k0 = both(a.pre == MOE_NORM_LAYER ? -s.x * inv_d * rstd2 : 0.f);
+      k1 = both(-s.y * inv_d * rstd2);
     } else {
-      each([&](int i, int j) { D[i][j] = 0.f; });
+      each([&](int i, int j) { D[i][j] = h[i][j] = both(0.f); });
     }
-    if (a.dr != nullptr) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) {
-          float v[8];
-          feed.template get<2>(i, v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) D[i][j] += v[j];
-        }
-    }
-    if (a.y != nullptr) {
-#pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) feed.template get<3>(i, h[i]);
-    }
+    get(std::integral_constant<int, 2>{}, v);
+    each([&](int i, int j) { D[i][j] = fma2(D[i][j], scale, fma2(h[i][j], k1, add2(k0, v[i][j]))); });
+    get(std::integral_constant<int, 3>{}, h);
     feed.next();
     if (a.dx != nullptr) {
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
         if (in[i]) {
-          float v[8];
+          F2 o[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = a.alpha * D[i][j];
-          put8(static_cast<TX*>(a.dx) + row * a.lddx + (i * TPR + t) * 8, v);
+          for (int j = 0; j < 4; ++j) o[j] = mul2(alpha, D[i][j]);
+          put8(dx + i * TPR * 8, o);
         }
     }
     if (a.y != nullptr) {
-      float s1 = 0.f, s2 = 0.f;
+      F2 s1 = both(0.f), s2 = s1;
+      const F2 R = both(rstd1), C = both(-mean1 * rstd1);
       each([&](int i, int j) {
-        h[i][j] = (h[i][j] - mean1) * rstd1;
-        S1[i][j] = fmaf(D[i][j], h[i][j], S1[i][j]);
-        if constexpr (BIAS) S0[i][j] += D[i][j];
-        D[i][j] *= A[i][j];
-        s1 += D[i][j];
-        s2 = fmaf(D[i][j], h[i][j], s2);
+        h[i][j] = fma2(h[i][j], R, C);
+        S1[i][j] = fma2(D[i][j], h[i][j], S1[i][j]);
+        if constexpr (BIAS) S0[i][j] = add2(S0[i][j], D[i][j]);
+        D[i][j] = mul2(D[i][j], A[i][j]);
+        s1 = add2(s1, D[i][j]);
+        s2 = fma2(D[i][j], h[i][j], s2);
       });
       if (a.post != MOE_NORM_NONE) {
         const float2 s = sums(s1, s2);
-        const float m1 = a.post == MOE_NORM_LAYER ? s.x * inv_d : 0.f, m2 = s.y * inv_d;
-        each([&](int i, int j) { D[i][j] = rstd1 * (D[i][j] - m1 - h[i][j] * m2); });
+        const F2 m0 = both(a.post == MOE_NORM_LAYER ? -s.x * inv_d * rstd1 : 0.f), m1 = both(-s.y * inv_d * rstd1);
+        each([&](int i, int j) { D[i][j] = fma2(D[i][j], R, fma2(h[i][j], m1, m0)); });
       }
 #pragma unroll
       for (int i = 0; i < NCH; ++i)
-        if (in[i]) put8(static_cast<TY*>(a.dy) + row * a.lddy + (i * TPR + t) * 8, D[i]);
+        if (in[i]) put8(dy + i * TPR * 8, D[i]);
     }
   }
   if (a.part == nullptr) return;
   float* part = a.part + static_cast<size_t>(blockIdx.x) * SUMS * a.d;
   // a block of several rows: its warps own the same columns; they are added in warp order
-  __shared__ float4 acc[ROWS > 1 ? ROWS - 1 : 1][32];
+  __shared__ F2 acc[ROWS > 1 ? ROWS - 1 : 1][SUMS][32];
   const int w = threadIdx.x / TPR;
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
     if constexpr (ROWS > 1) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
+        F2* const mine[SUMS] = {&S1[i][j], &S0[i][j], &P1[i][j], &P0[i][j]};
         __syncthreads();
-        if (w > 0) acc[w - 1][t] = make_float4(S1[i][j], S0[i][j], P1[i][j], P0[i][j]);
+        if (w > 0) {
+#pragma unroll
+          for (int q = 0; q < SUMS; ++q) acc[w - 1][q][t] = *mine[q];
+        }
         __syncthreads();
         if (w == 0) {
 #pragma unroll
-          for (int q = 0; q < ROWS - 1; ++q) {
-            const float4 v = acc[q][t];
-            S1[i][j] += v.x;
-            S0[i][j] += v.y;
-            P1[i][j] += v.z;
-            P0[i][j] += v.w;
-          }
+          for (int r = 0; r < ROWS - 1; ++r)
+#pragma unroll
+            for (int q = 0; q < SUMS; ++q) *mine[q] = add2(*mine[q], acc[r][q][t]);
         }
       }
     }
@@ -634,8 +712,10 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
     if (w != 0 || !in[i]) continue;
     put8(part + c, S1[i]);
     put8(part + 2 * static_cast<size_t>(a.d) + c, P1[i]);
-    put8(part + a.d + c, S0[i]);
-    put8(part + 3 * static_cast<size_t>(a.d) + c, P0[i]);
+    if constexpr (BIAS) {
+      put8(part + a.d + c, S0[i]);
+      put8(part + 3 * static_cast<size_t>(a.d) + c, P0[i]);
+    }
   }
 }
 
@@ -643,28 +723,35 @@ struct GradOut {
   float *post_gamma, *post_beta, *gate, *pre_gamma, *pre_beta;
 };
 
-// The weight gradients from the partial sums: 32 columns a block, 8 threads for each of a column's four sums, which
-// take every 8th partial and are added in thread order.
-__global__ void __launch_bounds__(1024) join_partials_kernel(const JoinArgs a, int blocks, const GradOut o) {
-  __shared__ float acc[SUMS][8][33];
+// The weight gradients from the partial sums: eight columns a block (a 32-byte piece of each partial row, so that there are
+// blocks for all SMs), 32 threads for each of a column's four sums, which take every 32nd partial and are added in thread order.
+constexpr int PART_COLS = 8;
+
+__global__ void __launch_bounds__(1024) join_partials_kernel(const JoinArgs a, int blocks, bool bias, const GradOut o) {
+  __shared__ float acc[SUMS][32][PART_COLS + 1];
   grid_wait();  // launched ahead of the end of the kernel that writes the partials
   const float* part = after_wait(static_cast<const float*>(a.part));
-  const int cx = threadIdx.x & 31, k = (threadIdx.x >> 5) & 3, ry = threadIdx.x >> 7;
-  const int c = blockIdx.x * 32 + cx;
-  float s = 0.f;
-  if (c < a.d) {
-#pragma unroll 8
-    for (int b = ry; b < blocks; b += 8) s += __ldcs(part + (static_cast<size_t>(b) * SUMS + k) * a.d + c);
+  const int cx = threadIdx.x % PART_COLS, k = threadIdx.x / PART_COLS % SUMS, ry = threadIdx.x / (PART_COLS * SUMS);
+  const int c = blockIdx.x * PART_COLS + cx;
+  // every load at once (a loop of a run-time length waits for each round of them)
+  constexpr int ROUNDS = (BWD_MAX_BLOCKS + 31) / 32;
+  float v[ROUNDS], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int r = ry + 32 * i;
+    v[i] = r < blocks && c < a.d && ((k & 1) == 0 || bias) ? __ldcs(part + (static_cast<size_t>(r) * SUMS + k) * a.d + c) : 0.f;
   }
+#pragma unroll
+  for (int i = 0; i < ROUNDS; ++i) s += v[i];
   acc[k][ry][cx] = s;
   __syncthreads();
-  if (threadIdx.x >= 32 || c >= a.d) return;
+  if (threadIdx.x >= PART_COLS || c >= a.d) return;
   float t[SUMS];
 #pragma unroll
   for (int q = 0; q < SUMS; ++q) {
     t[q] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[q] += acc[q][i][cx];
+    for (int i = 0; i < 32; ++i) t[q] += acc[q][i][cx];
   }
   const float g = a.beta * weight(a.gate, a.w_bf16, c, 1.f);
   if (o.post_gamma) o.post_gamma[c] = g * t[0];
@@ -877,17 +964,17 @@ moe_status_t moe_residual_norm_bwd(const void* dn, long long lddn, const void* d
   a.part = wgrad && T > 0 ? static_cast<float*>(ws) : nullptr;
   a.row = static_cast<float*>(ws) + (T > 0 ? part_floats(T, d) : 0);
   int blocks = 0;
+  const bool bias = d_post_beta || d_pre_beta || (d_gate && post_beta);
   if (T > 0) {
     const bool vec = d % 8 == 0 && rows16(dn, lddn, ey) && rows16(dr, lddr, ex) && rows16(r, ldr, ex) && rows16(y, ldy, ey) &&
                      rows16(dx, lddx, ex) && rows16(dy, lddy, ey) && aligned16(post_gamma) && aligned16(gate) && aligned16(pre_gamma) && aligned16(ws);
-    const bool bias = d_post_beta || d_pre_beta || (d_gate && post_beta);
     const cudaError_t err = x_dtype == MOE_DTYPE_BF16   ? launch_bwd<bf16, bf16>(a, vec, bias, s, blocks)
                             : y_dtype == MOE_DTYPE_BF16 ? launch_bwd<float, bf16>(a, vec, bias, s, blocks)
                                                         : launch_bwd<float, float>(a, vec, bias, s, blocks);
     if (err != cudaSuccess) return cuda_fail(err);
   }
   if (!wgrad) return MOE_OK;
-  const cudaError_t err = launch_dependent(join_partials_kernel, (d + 31) / 32, 1024, 0, s, a, blocks, o);
+  const cudaError_t err = launch_dependent(join_partials_kernel, (d + PART_COLS - 1) / PART_COLS, 1024, 0, s, a, blocks, bias, o);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
