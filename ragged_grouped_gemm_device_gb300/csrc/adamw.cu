@@ -4,8 +4,8 @@
 //   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 //
 // Bound by memory: p, m and v are read and written once, g is read once. The tensors are cut into pieces of
-// CHUNK elements, one block each; the descriptors travel in the kernel's parameters, and a block finds its tensor
-// by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
+// CHUNK elements, of which each block takes a run; the descriptors travel in the kernel's parameters, and a block finds its first
+// tensor by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
 // pointers allow it. All arithmetic is fp32; the bias corrections are -expm1(t log b), whose error is a unit in the
 // last place for small t too, where 1 - b^t cancels.
 //
@@ -29,7 +29,8 @@ namespace {
 
 constexpr int THREADS = 256;
 constexpr int VB = 8;         // elements of a thread in one round
-constexpr int CHUNK = 4096;   // elements of a block: two rounds
+constexpr int CHUNK = 4096;   // elements of a piece: two rounds
+constexpr int STEP_BLOCKS = 4;  // blocks on an SM
 constexpr int MAX_TENSORS = 128;  // of a launch: 11 KB of parameters
 constexpr int NORM_BLOCKS = 1216;
 
@@ -128,9 +129,23 @@ __device__ __forceinline__ void store8(uint8_t* p, int k, bool wide, const uint3
   }
 }
 
-// fp32 to bf16, up in magnitude where the fraction and u / 2^16 reach 1
+// fp32 to bf16, up in magnitude where the fraction and u / 2^16 reach 1: the upper half of the sum of the bits. A NaN, whose
+// sum could leave the NaNs, stays.
 __device__ __forceinline__ float stochastic_bf16(float x, uint32_t u) {
-  return x == x ? __uint_as_float((__float_as_uint(x) + u) & 0xFFFF0000u) : x;
+  return x == x ? __uint_as_float(__float_as_uint(x) + u) : x;
+}
+// the upper halves
+__device__ __forceinline__ void store8_upper(bf16* p, int k, bool wide, const float (&f)[VB]) {
+  if (wide && k == VB) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]), 0x7632);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VB; ++i)
+      if (i < k) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(__float_as_uint(f[i]) >> 16);
+  }
 }
 
 // ------------------------------------------------------------------ 8-bit states
@@ -179,8 +194,8 @@ __device__ __forceinline__ uint32_t to_e4m3(const float (&x)[VB], const uint32_t
   }
 #pragma unroll
   for (int i = 0; i < VB; ++i) {
-    c[i] = (c[i] + (SHIFT == 16 ? (rnd[i] >> 12) & 0xFFFF0u : (rnd[i] << 4) & 0xFFFF0u)) >> 20;
-    if (KEEP) c[i] = x[i] > 0.f ? max(c[i], 1u) : c[i];
+    c[i] = (c[i] + (SHIFT == 16 ? rnd[i] >> 16 : rnd[i] & 0xFFFFu) * 16u) >> 20;
+    if (KEEP) c[i] = max(c[i], min(__float_as_uint(x[i]), 1u));
   }
 #pragma unroll
   for (int i = 0; i < VB; i += 4) {
@@ -205,6 +220,24 @@ struct StepArgs {
   unsigned blocks;  // of this launch
   bool last;        // the call's last launch counts the step
 };
+
+// The square root, correctly rounded, of two values in [2^-126, inf): an estimate s from the reciprocal root y, and Newton's step s
+// + (v - s^2) y / 2 with the residual from a fused product. It equals sqrtf for every mantissa and both parities of the
+// exponent (compared for all 2^24 of them), and takes a quarter of its instructions.
+__device__ __forceinline__ F2 sqrt2(F2 v) {
+  const float2 x = parts(v);
+  float y0, y1;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(x.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(x.y));
+  const F2 y = pair(y0, y1), s = mul2(v, y);
+  return fma2(fma2(mul2(s, both(-1.0f)), s, v), mul2(y, both(0.5f)), s);
+}
+// to two units; 0 beyond 2^126
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // What a thread reads of one round, as it lies in memory where that takes 16-byte accesses
 template <int BITS>
@@ -249,16 +282,35 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
       d.v[i] = v.x * v.x, d.v[i + 1] = v.y * v.y;
     }
   }
+  // Two elements at a time. Each operation is rounded by itself: a stochastic rounding goes the other way where its argument differs
+  // in the last place, and m and v are to be what the formula written out gives.
+  const F2 c = both(u.c), b1 = both(a.b1), omb1 = both(a.omb1), b2 = both(a.b2), omb2 = both(a.omb2), keep = both(u.keep),
+           step = both(-u.step), root = both(u.root), eps = both(a.eps);
+  float least = 1.0f, most = 1.0f;
 #pragma unroll
-  for (int i = 0; i < VB; ++i) {
-    // Each operation rounded by itself: a stochastic rounding goes the other way where its argument differs in the last
-    // place, and m and v are to be what the formula written out gives.
-    const float gc = d.g[i] * u.c;
-    d.m[i] = __fadd_rn(__fmul_rn(a.b1, d.m[i]), __fmul_rn(a.omb1, gc));
-    d.v[i] = __fadd_rn(__fmul_rn(a.b2, d.v[i]), __fmul_rn(__fmul_rn(a.omb2, gc), gc));
-    r[i] = sqrtf(d.v[i]);
+  for (int i = 0; i < VB; i += 2) {
+    const F2 g = mul2(pair(d.g[i], d.g[i + 1]), c);
+    const F2 m = add2(mul2(b1, pair(d.m[i], d.m[i + 1])), mul2(omb1, g));
+    const F2 v = add2(mul2(b2, pair(d.v[i], d.v[i + 1])), mul2(mul2(omb2, g), g));
+    const float2 vv = parts(v), mm = parts(m), rr = parts(sqrt2(v));
+    r[i] = rr.x, r[i + 1] = rr.y;
+    d.m[i] = mm.x, d.m[i + 1] = mm.y;
+    d.v[i] = vv.x, d.v[i + 1] = vv.y;
+    least = fminf(least, fminf(vv.x, vv.y));
+    most = fmaxf(most, fmaxf(vv.x, vv.y));
+  }
+  // zeros, subnormals and infinities; a NaN is a NaN already
+  if (!(least >= 0x1p-126f && most <= 3.402823466e38f)) {
+#pragma unroll
+    for (int i = 0; i < VB; ++i) r[i] = sqrtf(d.v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < VB; i += 2) {
+    const float2 den = parts(fma2(pair(r[i], r[i + 1]), root, eps));
     // the quotient to two units: it is a small part of p
-    d.p[i] = fmaf(d.p[i], u.keep, -__fdividef(u.step * d.m[i], fmaf(r[i], u.root, a.eps)));
+    const F2 up = mul2(mul2(step, pair(d.m[i], d.m[i + 1])), pair(reciprocal(den.x), reciprocal(den.y)));
+    const float2 p = parts(fma2(pair(d.p[i], d.p[i + 1]), keep, up));
+    d.p[i] = p.x, d.p[i + 1] = p.y;
   }
   uint32_t rnd[VB];
   if (BITS == 8 || q.p_dtype == MOE_DTYPE_BF16) {
@@ -268,8 +320,8 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
   }
   if (q.p_dtype == MOE_DTYPE_BF16) {
 #pragma unroll
-    for (int i = 0; i < VB; ++i) d.p[i] = stochastic_bf16(d.p[i], (rnd[i] >> 8) & 0xFFFFu);
-    store8(static_cast<bf16*>(q.p) + i0, k, wide, d.p);
+    for (int i = 0; i < VB; ++i) d.p[i] = stochastic_bf16(d.p[i], __byte_perm(rnd[i], 0, 0x4421));  // the middle 16 bits
+    store8_upper(static_cast<bf16*>(q.p) + i0, k, wide, d.p);
   } else {
     store8(static_cast<float*>(q.p) + i0, k, wide, d.p);
     if (q.copy != nullptr) store8(static_cast<bf16*>(q.copy) + i0, k, wide, d.p);
@@ -296,38 +348,38 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
 }
 
 template <int BITS>
-__global__ void __launch_bounds__(THREADS) adamw_kernel(const __grid_constant__ Batch batch, const StepArgs a) {
+__global__ void __launch_bounds__(THREADS, STEP_BLOCKS) adamw_kernel(const __grid_constant__ Batch batch, const StepArgs a) {
   grid_wait();
   TensorStep u;
   u.c = a.grad_scale ? *after_wait(a.grad_scale) : 1.0f;
   if (u.c != u.c) return;  // the norm was not finite: the step is skipped
   const int t = *reinterpret_cast<volatile int32_t*>(a.steps) + 1;
-  if (blockIdx.x < batch.chunk0[batch.count]) {
-    const int j = find_tensor(batch, blockIdx.x);
-    const moe_adamw_tensor_t& q = batch.t[j];
+  const unsigned long long all = batch.chunk0[batch.count];
+  const unsigned c1 = static_cast<unsigned>(all * (blockIdx.x + 1) / gridDim.x);
+  unsigned c = static_cast<unsigned>(all * blockIdx.x / gridDim.x);
+  if (c < c1) {
     const float lr = a.lr_scale ? a.lr * *after_wait(a.lr_scale) : a.lr;
     u.step = lr / -expm1f(static_cast<float>(t) * a.log_b1);
     u.root = 1.0f / sqrtf(-expm1f(static_cast<float>(t) * a.log_b2));
-    u.keep = fmaf(-lr, q.weight_decay, 1.0f);
-    u.key = mix(a.seed ^ mix(0x9E3779B9u * static_cast<uint32_t>(t) + static_cast<uint32_t>(batch.first + j)));
-    const long long base = static_cast<long long>(blockIdx.x - batch.chunk0[j]) * CHUNK;
-    constexpr int ROUNDS = CHUNK / (THREADS * VB);
-    const long long i0 = base + threadIdx.x * VB;
-    if (batch.wide[j] != 0 && base + CHUNK <= q.n) {
-      Raw<BITS> d[ROUNDS];  // all loads before the first store
-#pragma unroll
-      for (int i = 0; i < ROUNDS; ++i) d[i].load(q, i0 + i * THREADS * VB, VB, true);
-#pragma unroll
-      for (int i = 0; i < ROUNDS; ++i) adamw_round<BITS, true>(q, a, u, i0 + i * THREADS * VB, VB, true, d[i]);
-    } else {
+    for (int j = find_tensor(batch, c); c < c1; ++j) {
+      const moe_adamw_tensor_t& q = batch.t[j];
+      const unsigned end = min(c1, batch.chunk0[j + 1]);
+      u.keep = fmaf(-lr, q.weight_decay, 1.0f);
+      u.key = mix(a.seed ^ mix(0x9E3779B9u * static_cast<uint32_t>(t) + static_cast<uint32_t>(batch.first + j)));
       const bool wide = batch.wide[j] != 0;
-      for (int i = 0; i < ROUNDS; ++i) {
-        const long long at = i0 + i * THREADS * VB;
-        const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), q.n - at)));  // elements of this thread
-        Raw<BITS> d;
-        d.load(q, at, k, wide);
-        adamw_round<BITS, false>(q, a, u, at, k, wide, d);
+      long long i0 = static_cast<long long>(c - batch.chunk0[j]) * CHUNK + threadIdx.x * VB;
+      const long long last = min(q.n, static_cast<long long>(end - batch.chunk0[j]) * CHUNK);  // of this block's run
+      Raw<BITS> d;
+      for (; i0 - threadIdx.x * VB + THREADS * VB <= last && wide; i0 += THREADS * VB) {
+        d.load(q, i0, VB, true);
+        adamw_round<BITS, true>(q, a, u, i0, VB, true, d);
       }
+      for (; i0 - threadIdx.x * VB < last; i0 += THREADS * VB) {
+        const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), last - i0)));  // elements of this thread
+        d.load(q, i0, k, wide);
+        adamw_round<BITS, false>(q, a, u, i0, k, wide, d);
+      }
+      c = end;
     }
   }
   // The last block to end counts the step: by then every thread has read the count.
@@ -503,7 +555,10 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
   for (int i = 0; i < count || i == 0;) {
     Batch b;
     const int n = fill(b, tensors, i, count, false, state_bits);
+    // 8-bit states: as many blocks as fit, since what a block computes once would be a fifth of the instructions of a piece. 32 bits,
+    // bound by memory: a block for each piece, which spread better (201 million parameters: 902 us, 1047 in runs).
     a.blocks = std::max(b.chunk0[n], 1u);
+    if (state_bits == 8) a.blocks = std::min(a.blocks, static_cast<unsigned>(STEP_BLOCKS * device_sm_count()));
     a.last = i + n >= count;
     const cudaError_t err = launch_dependent(state_bits == 8 ? adamw_kernel<8> : adamw_kernel<32>, a.blocks, THREADS, 0, s, b, a);
     if (err != cudaSuccess) return cuda_fail(err);
