@@ -129,11 +129,6 @@ __device__ __forceinline__ void store8(uint8_t* p, int k, bool wide, const uint3
   }
 }
 
-// fp32 to bf16, up in magnitude where the fraction and u / 2^16 reach 1: the upper half of the sum of the bits. A NaN, whose
-// sum could leave the NaNs, stays.
-__device__ __forceinline__ float stochastic_bf16(float x, uint32_t u) {
-  return x == x ? __uint_as_float(__float_as_uint(x) + u) : x;
-}
 // the upper halves
 __device__ __forceinline__ void store8_upper(bf16* p, int k, bool wide, const float (&f)[VB]) {
   if (wide && k == VB) {
@@ -181,32 +176,32 @@ __device__ __forceinline__ uint32_t to_e4m3(const float (&x)[VB], const uint32_t
   const uint32_t byte = scale_byte(top);
   w[0] = w[1] = 0;
   if (byte == 0xFF) return byte;
+  const auto encode = [&](auto scaled) {
+    uint32_t c[VB];
+#pragma unroll
+    for (int i = 0; i < VB; ++i) {
+      c[i] = (__float_as_uint(scaled(fabsf(x[i]))) + (SHIFT == 16 ? rnd[i] >> 16 : rnd[i] & 0xFFFFu) * 16u) >> 20;
+      if (KEEP) c[i] = max(c[i], min(__float_as_uint(x[i]), 1u));
+    }
+#pragma unroll
+    for (int i = 0; i < VB; i += 4) {
+      w[i >> 2] = __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
+      // The signs: the highest bytes of four values. (Joined to a code shifted left by 4 before the bytes are packed, nvcc
+      // 13.0.88 lost the code.)
+      if (!KEEP) {
+        const uint32_t lo = __byte_perm(__float_as_uint(x[i]), __float_as_uint(x[i + 1]), 0x0073);
+        const uint32_t hi = __byte_perm(__float_as_uint(x[i + 2]), __float_as_uint(x[i + 3]), 0x0073);
+        w[i >> 2] |= __byte_perm(lo, hi, 0x5410) & 0x80808080u;
+      }
+    }
+  };
   // 2^-s 2^-120 is an fp32 (subnormal from s = 7 on) up to s = 29; states above 2^38 take the two steps apart
   const float inv = __uint_as_float((254u - byte) << 23);
-  const float first = byte > 150 ? inv : 1.0f, second = byte > 150 ? E4M3_DOWN : inv * E4M3_DOWN;
-  uint32_t c[VB];
-  if (byte > 150) {
-#pragma unroll
-    for (int i = 0; i < VB; ++i) c[i] = __float_as_uint(fabsf(x[i]) * first * second);
+  if (byte <= 150) {
+    const float down = inv * E4M3_DOWN;
+    encode([&](float v) { return v * down; });
   } else {
-#pragma unroll
-    for (int i = 0; i < VB; ++i) c[i] = __float_as_uint(fabsf(x[i]) * second);
-  }
-#pragma unroll
-  for (int i = 0; i < VB; ++i) {
-    c[i] = (c[i] + (SHIFT == 16 ? rnd[i] >> 16 : rnd[i] & 0xFFFFu) * 16u) >> 20;
-    if (KEEP) c[i] = max(c[i], min(__float_as_uint(x[i]), 1u));
-  }
-#pragma unroll
-  for (int i = 0; i < VB; i += 4) {
-    w[i >> 2] = __byte_perm(__byte_perm(c[i], c[i + 1], 0x0040), __byte_perm(c[i + 2], c[i + 3], 0x0040), 0x5410);
-    // The signs: the highest bytes of four values. (Joined to a code shifted left by 4 before the bytes are packed, nvcc 13.0.88
-    // lost the code.)
-    if (!KEEP) {
-      const uint32_t lo = __byte_perm(__float_as_uint(x[i]), __float_as_uint(x[i + 1]), 0x0073);
-      const uint32_t hi = __byte_perm(__float_as_uint(x[i + 2]), __float_as_uint(x[i + 3]), 0x0073);
-      w[i >> 2] |= __byte_perm(lo, hi, 0x5410) & 0x80808080u;
-    }
+    encode([&](float v) { return v * inv * E4M3_DOWN; });
   }
   return byte;
 }
@@ -221,16 +216,14 @@ struct StepArgs {
   bool last;        // the call's last launch counts the step
 };
 
-// The square root, correctly rounded, of two values in [2^-126, inf): an estimate s from the reciprocal root y, and Newton's step s
+// The square root, correctly rounded, of a value in [2^-126, inf): an estimate s from the reciprocal root y, and Newton's step s
 // + (v - s^2) y / 2 with the residual from a fused product. It equals sqrtf for every mantissa and both parities of the
 // exponent (compared for all 2^24 of them), and takes a quarter of its instructions.
-__device__ __forceinline__ F2 sqrt2(F2 v) {
-  const float2 x = parts(v);
-  float y0, y1;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(x.x));
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(x.y));
-  const F2 y = pair(y0, y1), s = mul2(v, y);
-  return fma2(fma2(mul2(s, both(-1.0f)), s, v), mul2(y, both(0.5f)), s);
+__device__ __forceinline__ float sqrt_normal(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  const float s = __fmul_rn(v, y);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), 0.5f * y, s);
 }
 // to two units; 0 beyond 2^126
 __device__ __forceinline__ float reciprocal(float x) {
@@ -282,36 +275,24 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
       d.v[i] = v.x * v.x, d.v[i + 1] = v.y * v.y;
     }
   }
-  // Two elements at a time. Each operation is rounded by itself: a stochastic rounding goes the other way where its argument differs
-  // in the last place, and m and v are to be what the formula written out gives.
-  const F2 c = both(u.c), b1 = both(a.b1), omb1 = both(a.omb1), b2 = both(a.b2), omb2 = both(a.omb2), keep = both(u.keep),
-           step = both(-u.step), root = both(u.root), eps = both(a.eps);
-  float least = 1.0f, most = 1.0f;
+  // Each operation is rounded by itself: a stochastic rounding goes the other way where its argument differs in the last place, and
+  // m and v are to be what the formula written out gives.
+  float odd = 0.f;  // not 0 when a root is not finite
 #pragma unroll
-  for (int i = 0; i < VB; i += 2) {
-    const F2 g = mul2(pair(d.g[i], d.g[i + 1]), c);
-    const F2 m = add2(mul2(b1, pair(d.m[i], d.m[i + 1])), mul2(omb1, g));
-    const F2 v = add2(mul2(b2, pair(d.v[i], d.v[i + 1])), mul2(mul2(omb2, g), g));
-    const float2 vv = parts(v), mm = parts(m), rr = parts(sqrt2(v));
-    r[i] = rr.x, r[i + 1] = rr.y;
-    d.m[i] = mm.x, d.m[i + 1] = mm.y;
-    d.v[i] = vv.x, d.v[i + 1] = vv.y;
-    least = fminf(least, fminf(vv.x, vv.y));
-    most = fmaxf(most, fmaxf(vv.x, vv.y));
+  for (int i = 0; i < VB; ++i) {
+    const float gc = __fmul_rn(d.g[i], u.c);
+    d.m[i] = __fadd_rn(__fmul_rn(a.b1, d.m[i]), __fmul_rn(a.omb1, gc));
+    d.v[i] = __fadd_rn(__fmul_rn(a.b2, d.v[i]), __fmul_rn(__fmul_rn(a.omb2, gc), gc));
+    r[i] = sqrt_normal(d.v[i]);
+    odd = fmaf(r[i], 0.f, odd);
   }
-  // zeros, subnormals and infinities; a NaN is a NaN already
-  if (!(least >= 0x1p-126f && most <= 3.402823466e38f)) {
+  if (!(odd == 0.f)) {  // zeros, subnormals, infinities or NaNs among the v
 #pragma unroll
     for (int i = 0; i < VB; ++i) r[i] = sqrtf(d.v[i]);
   }
+  // the quotient to two units: it is a small part of p
 #pragma unroll
-  for (int i = 0; i < VB; i += 2) {
-    const float2 den = parts(fma2(pair(r[i], r[i + 1]), root, eps));
-    // the quotient to two units: it is a small part of p
-    const F2 up = mul2(mul2(step, pair(d.m[i], d.m[i + 1])), pair(reciprocal(den.x), reciprocal(den.y)));
-    const float2 p = parts(fma2(pair(d.p[i], d.p[i + 1]), keep, up));
-    d.p[i] = p.x, d.p[i + 1] = p.y;
-  }
+  for (int i = 0; i < VB; ++i) d.p[i] = fmaf(d.p[i], u.keep, -(u.step * d.m[i]) * reciprocal(fmaf(r[i], u.root, a.eps)));
   uint32_t rnd[VB];
   if (BITS == 8 || q.p_dtype == MOE_DTYPE_BF16) {
     const uint32_t x0 = u.key + static_cast<uint32_t>(i0) * 0x9E3779B9u + static_cast<uint32_t>(i0 >> 32) * 0x85EBCA6Bu;
@@ -319,8 +300,19 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
     for (int i = 0; i < VB; ++i) rnd[i] = mix(x0 + static_cast<uint32_t>(i) * 0x9E3779B9u);
   }
   if (q.p_dtype == MOE_DTYPE_BF16) {
+    // To bf16, up in magnitude where the fraction and u / 2^16 reach 1: the upper half of the sum of the bits. A NaN, whose sum could
+    // leave the NaNs, stays.
+    float nan = 0.f;
 #pragma unroll
-    for (int i = 0; i < VB; ++i) d.p[i] = stochastic_bf16(d.p[i], __byte_perm(rnd[i], 0, 0x4421));  // the middle 16 bits
+    for (int i = 0; i < VB; ++i) nan = fmaf(d.p[i], 0.f, nan);
+    if (nan == 0.f) {
+#pragma unroll
+      for (int i = 0; i < VB; ++i) d.p[i] = __uint_as_float(__float_as_uint(d.p[i]) + __byte_perm(rnd[i], 0, 0x4421));  // the middle 16 bits
+    } else {
+#pragma unroll
+      for (int i = 0; i < VB; ++i)
+        if (d.p[i] == d.p[i]) d.p[i] = __uint_as_float(__float_as_uint(d.p[i]) + __byte_perm(rnd[i], 0, 0x4421));
+    }
     store8_upper(static_cast<bf16*>(q.p) + i0, k, wide, d.p);
   } else {
     store8(static_cast<float*>(q.p) + i0, k, wide, d.p);
