@@ -147,11 +147,16 @@ def load(path: str = None):
 COMPILED = ("moe_layer_norm_fwd", "moe_layer_norm_bwd", "moe_gate_fwd", "moe_gate_bwd", "moe_mx4_quantize_rows",
             "moe_mx4_dequantize_rows", "moe_permute_mxfp4", "moe_grouped_swiglu_fwd_mxfp4", "moe_unpermute_combine",
             "moe_route_offsets")
-PYTHON_BINDING = {}  # the functions that they replaced
+# ... and those of a block's joins, of an optimizer step and of the 4-bit integer experts
+COMPILED_STEP = ("moe_residual_norm_fwd", "moe_residual_norm_bwd", "moe_grad_norm", "moe_adamw_step", "moe_w4_matvec",
+                 "moe_w4_swiglu_decode")
+PYTHON_BINDING = {}       # the functions that they replaced
+PYTHON_BINDING_STEP = {}
+adamw_pointers = None     # the extension's loop over AdamW's tensors
 
 
 def _install_binding():
-    """Replace the functions of COMPILED by the CPython extension's, which make the same checks and call
+    """Replace the functions of COMPILED and COMPILED_STEP by the CPython extension's, which make the same checks and call
     the same entry points of the loaded library with less marshalling time. Without the extension (or
     without torch, when only host functions are called) the Python functions below stay."""
     import sys
@@ -163,11 +168,13 @@ def _install_binding():
     except ImportError:
         return
 
-    entry_points = COMPILED + ("moe_workspace_bytes",)
+    entry_points = COMPILED + COMPILED_STEP + ("moe_workspace_bytes",)
     _binding.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in entry_points}, _check)
-    for n in COMPILED:
-        PYTHON_BINDING[n] = globals()[n]
-        globals()[n] = getattr(_binding, n)
+    for names, replaced in ((COMPILED, PYTHON_BINDING), (COMPILED_STEP, PYTHON_BINDING_STEP)):
+        for n in names:
+            replaced[n] = globals()[n]
+            globals()[n] = getattr(_binding, n)
+    globals()["adamw_pointers"] = _binding.adamw_pointers
 
 
 def _ptr(t):

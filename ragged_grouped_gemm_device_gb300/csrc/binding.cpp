@@ -1,4 +1,4 @@
-// The binding's calls that a decode step makes, as a CPython extension: the same checks and
+// The binding's calls that a decode or optimizer step makes, as a CPython extension: the same checks and
 // arguments as the Python functions of the same names in _lib.py, which stay the reference and are
 // used where this extension has not been built. Marshalling a call in Python takes 3 to 8 us, more
 // than most of these calls' kernels run for few tokens. Here it takes 0.2 to 0.3 us, a tenth of a
@@ -21,7 +21,8 @@
 #define FUNCTIONS(X)                                                                                         \
   X(moe_layer_norm_fwd) X(moe_layer_norm_bwd) X(moe_gate_fwd) X(moe_gate_bwd) X(moe_mx4_quantize_rows)        \
   X(moe_mx4_dequantize_rows) X(moe_permute_mxfp4) X(moe_grouped_swiglu_fwd_mxfp4) X(moe_unpermute_combine)    \
-  X(moe_route_offsets) X(moe_workspace_bytes)
+  X(moe_route_offsets) X(moe_residual_norm_fwd) X(moe_residual_norm_bwd) X(moe_grad_norm) X(moe_adamw_step)        \
+  X(moe_w4_matvec) X(moe_w4_swiglu_decode) X(moe_workspace_bytes)
 #define DECLARE(f) static __typeof__(&f) p_##f;
 FUNCTIONS(DECLARE)
 
@@ -420,6 +421,252 @@ PyObject* route_offsets(ARGS) {
   });
 }
 
+// rows(), or None: no pointer and a pitch of 0
+int rows_or_none(PyObject* o, int T, int width, Any* p, long long* ld) {
+  p->p = nullptr;
+  *ld = 0;
+  return o == Py_None ? 0 : rows(o, T, width, p, ld);
+}
+
+// those of the n objects that are not None are of one type
+int one_type(PyObject* const* o, int n, const char* what) {
+  PyObject* first = nullptr;
+  for (int i = 0; i < n; ++i) {
+    if (o[i] == Py_None) continue;
+    if (first != nullptr && same_type(first, o[i], what) < 0) return -1;
+    first = o[i];
+  }
+  return 0;
+}
+
+PyObject* first_of(PyObject* a, PyObject* b, PyObject* c) { return a != Py_None ? a : b != Py_None ? b : c; }
+
+int as_float(PyObject* o, double* v) {
+  *v = PyFloat_AsDouble(o);
+  return *v == -1.0 && PyErr_Occurred() ? -1 : 0;
+}
+
+PyObject* residual_norm_fwd(ARGS) {
+  COLLECT("moe_residual_norm_fwd", 16, "x", "y", "post", "post_gamma", "post_beta", "gate", "pre", "pre_gamma", "pre_beta", "T", "d",
+          "eps", "res_scale", "branch_scale", "r", "n", "stats", "stream");
+  int T, d, post, pre, xt, yt, wt;
+  double eps, al, be;
+  Any x, y, r, n, pg, pb, gate, qg, qb, stats;
+  long long ldx, ldy, ldr, ldn;
+  moe_stream_t s;
+  if (as_int(a[2], &post) < 0 || as_int(a[6], &pre) < 0 || as_int(a[9], &T) < 0 || as_int(a[10], &d) < 0 || as_float(a[11], &eps) < 0 ||
+      as_float(a[12], &al) < 0 || as_float(a[13], &be) < 0)
+    return nullptr;
+  PyObject *const stream_rows[] = {a[0], a[14]}, *const branch_rows[] = {a[1], a[15]}, *const w[] = {a[3], a[4], a[5], a[7], a[8]};
+  PyObject* branch = first_of(a[1], a[15], a[0]);
+  if (rows(a[0], T, d, &x, &ldx) < 0 || rows_or_none(a[1], T, d, &y, &ldy) < 0 || rows_or_none(a[14], T, d, &r, &ldr) < 0 ||
+      rows_or_none(a[15], T, d, &n, &ldn) < 0 || one_type(stream_rows, 2, "x and r have to have one type") < 0 ||
+      one_type(branch_rows, 2, "y and n have to have one type") < 0 || element_type(a[0], &xt) < 0 || element_type(branch, &yt) < 0 ||
+      plain(a[3], &pg) < 0 || plain(a[4], &pb) < 0 || plain(a[5], &gate) < 0 || plain(a[7], &qg) < 0 || plain(a[8], &qb) < 0 ||
+      weight_type(w, 5, d, &wt) < 0 || typed(a[16], at::kFloat, 4LL * T, "stats", &stats) < 0 || as_stream(a[17], &s) < 0)
+    return nullptr;
+  return finish("moe_residual_norm_fwd", [&] {
+    return p_moe_residual_norm_fwd(x, xt, ldx, y, yt, ldy, post, pg, pb, gate, pre, qg, qb, wt, T, d, (float)eps, (float)al, (float)be, r,
+                                   ldr, n, ldn, stats, s);
+  });
+}
+
+PyObject* residual_norm_bwd(ARGS) {
+  COLLECT("moe_residual_norm_bwd", 17, "dn", "dr", "r", "y", "post", "post_gamma", "post_beta", "gate", "pre", "pre_gamma", "stats", "T", "d",
+          "res_scale", "branch_scale", "dx", "dy", "d_post_gamma", "d_post_beta", "d_gate", "d_pre_gamma", "d_pre_beta", "ws", "stream");
+  int T, d, post, pre, xt, yt, wt;
+  double al, be;
+  Any dn, dr, r, y, dx, dy, pg, pb, gate, qg, stats, g[5], ws;
+  long long lddn, lddr, ldr, ldy, lddx, lddy;
+  size_t n;
+  moe_stream_t s;
+  static const char* const names_g[] = {"d_post_gamma", "d_post_beta", "d_gate", "d_pre_gamma", "d_pre_beta"};
+  if (as_int(a[4], &post) < 0 || as_int(a[8], &pre) < 0 || as_int(a[11], &T) < 0 || as_int(a[12], &d) < 0 || as_float(a[13], &al) < 0 ||
+      as_float(a[14], &be) < 0)
+    return nullptr;
+  PyObject *const stream_rows[] = {a[1], a[2], a[15]}, *const branch_rows[] = {a[0], a[3], a[16]}, *const w[] = {a[5], a[6], a[7], a[9]};
+  PyObject *sl = first_of(a[1], a[2], a[15]), *bl = first_of(a[0], a[3], a[16]);
+  if (sl == Py_None) sl = bl;
+  if (bl == Py_None) bl = sl;
+  if (sl == Py_None) {
+    PyErr_SetString(PyExc_ValueError, "neither gradients nor rows were given");
+    return nullptr;
+  }
+  if (rows_or_none(a[0], T, d, &dn, &lddn) < 0 || rows_or_none(a[1], T, d, &dr, &lddr) < 0 || rows_or_none(a[2], T, d, &r, &ldr) < 0 ||
+      rows_or_none(a[3], T, d, &y, &ldy) < 0 || rows_or_none(a[15], T, d, &dx, &lddx) < 0 || rows_or_none(a[16], T, d, &dy, &lddy) < 0 ||
+      one_type(stream_rows, 3, "dr, r and dx have to have one type") < 0 || one_type(branch_rows, 3, "dn, y and dy have to have one type") < 0 ||
+      element_type(sl, &xt) < 0 || element_type(bl, &yt) < 0 || plain(a[5], &pg) < 0 || plain(a[6], &pb) < 0 || plain(a[7], &gate) < 0 ||
+      plain(a[9], &qg) < 0 || weight_type(w, 4, d, &wt) < 0 || typed(a[10], at::kFloat, 4LL * T, "stats", &stats) < 0)
+    return nullptr;
+  for (int i = 0; i < 5; ++i)
+    if (typed(a[17 + i], at::kFloat, d, names_g[i], &g[i]) < 0) return nullptr;
+  if (plain(a[22], &ws) < 0 || bytes_of(a[22], &n) < 0 || as_stream(a[23], &s) < 0) return nullptr;
+  return finish("moe_residual_norm_bwd", [&] {
+    return p_moe_residual_norm_bwd(dn, lddn, dr, lddr, r, ldr, xt, y, ldy, yt, post, pg, pb, gate, pre, qg, wt, stats, T, d, (float)al,
+                                   (float)be, dx, lddx, dy, lddy, g[0], g[1], g[2], g[3], g[4], ws, n, s);
+  });
+}
+
+// a ctypes array of moe_adamw_tensor_t, held for the scope
+struct Table {
+  Py_buffer view{};
+  bool held = false;
+  int get(PyObject* o) {
+    if (PyObject_GetBuffer(o, &view, PyBUF_SIMPLE) < 0) return -1;
+    held = true;
+    if (view.len % sizeof(moe_adamw_tensor_t) != 0 || view.len / sizeof(moe_adamw_tensor_t) > INT_MAX) {
+      PyErr_SetString(PyExc_ValueError, "tensors has to be an array of AdamWTensor");
+      return -1;
+    }
+    return 0;
+  }
+  ~Table() {
+    if (held) PyBuffer_Release(&view);
+  }
+  moe_adamw_tensor_t* data() const { return static_cast<moe_adamw_tensor_t*>(view.buf); }
+  int count() const { return static_cast<int>(view.len / sizeof(moe_adamw_tensor_t)); }
+};
+
+PyObject* grad_norm(ARGS) {
+  COLLECT("moe_grad_norm", 4, "tensors", "max_norm", "norm", "ws", "stream");
+  Table t;
+  double most;
+  Any norm, ws;
+  size_t n;
+  moe_stream_t s;
+  if (t.get(a[0]) < 0 || as_float(a[1], &most) < 0 || typed(a[2], at::kFloat, 2, "norm", &norm) < 0 || plain(a[3], &ws) < 0 ||
+      bytes_of(a[3], &n) < 0 || as_stream(a[4], &s) < 0)
+    return nullptr;
+  return finish("moe_grad_norm", [&] { return p_moe_grad_norm(t.data(), t.count(), (float)most, norm, ws, n, s); });
+}
+
+PyObject* adamw_step(ARGS) {
+  COLLECT("moe_adamw_step", 8, "tensors", "state_bits", "lr", "beta1", "beta2", "eps", "seed", "steps", "lr_scale", "grad_scale", "stream");
+  Table t;
+  int bits;
+  double lr, b1, b2, eps;
+  Any steps, ls, gs;
+  moe_stream_t s;
+  if (t.get(a[0]) < 0 || as_int(a[1], &bits) < 0 || as_float(a[2], &lr) < 0 || as_float(a[3], &b1) < 0 || as_float(a[4], &b2) < 0 ||
+      as_float(a[5], &eps) < 0)
+    return nullptr;
+  const unsigned long seed = PyLong_AsUnsignedLongMask(a[6]);
+  if (PyErr_Occurred() || typed(a[7], at::kInt, 2, "steps", &steps) < 0 || typed(a[8], at::kFloat, 1, "lr_scale", &ls) < 0 ||
+      typed(a[9], at::kFloat, 1, "grad_scale", &gs) < 0 || as_stream(a[10], &s) < 0)
+    return nullptr;
+  return finish("moe_adamw_step", [&] {
+    return p_moe_adamw_step(t.data(), t.count(), bits, lr, b1, b2, eps, (uint32_t)seed, steps, ls, gs, s);
+  });
+}
+
+// adamw_pointers(tensors, device, params, copies, grads): what AdamW.step writes into its table, with its checks; the parameters' and
+// copies' versions are counted up.
+PyObject* adamw_pointers(ARGS) {
+  COLLECT("adamw_pointers", 5, "tensors", "device", "params", "copies", "grads");
+  Table t;
+  int device;
+  if (t.get(a[0]) < 0 || as_int(a[1], &device) < 0) return nullptr;
+  PyObject* lists[3] = {a[2], a[3], a[4]};
+  for (PyObject*& l : lists) {
+    if ((!PyList_Check(l) && !PyTuple_Check(l)) || PySequence_Fast_GET_SIZE(l) != t.count()) {
+      PyErr_Format(PyExc_ValueError, "expected a list of %d tensors", t.count());
+      return nullptr;
+    }
+  }
+  const auto dense = [&](const at::Tensor& x, const char* what) {
+    if (x.is_cuda() && x.is_contiguous() && x.get_device() == device && (x.scalar_type() == at::kFloat || x.scalar_type() == at::kBFloat16))
+      return true;
+    PyErr_Format(PyExc_ValueError, "%s has to be a dense bfloat16 or float32 tensor on cuda:%d", what, device);
+    return false;
+  };
+  for (int i = 0; i < t.count(); ++i) {
+    const at::Tensor* g = tensor(PySequence_Fast_GET_ITEM(lists[2], i));
+    const at::Tensor* p = tensor(PySequence_Fast_GET_ITEM(lists[0], i));
+    if (g == nullptr || p == nullptr || !dense(*g, "a gradient")) return nullptr;
+    moe_adamw_tensor_t& q = t.data()[i];
+    if (g->numel() != q.n) {
+      PyErr_Format(PyExc_ValueError, "a gradient has %lld elements, its parameter %lld", (long long)g->numel(), q.n);
+      return nullptr;
+    }
+    if (!dense(*p, "a parameter")) return nullptr;
+    if (p->numel() != q.n || (p->scalar_type() == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16) != q.p_dtype) {
+      PyErr_SetString(PyExc_ValueError, "a parameter's size or type has changed");
+      return nullptr;
+    }
+  }
+  for (int i = 0; i < t.count(); ++i) {
+    const at::Tensor& g = THPVariable_Unpack(PySequence_Fast_GET_ITEM(lists[2], i));
+    const at::Tensor& p = THPVariable_Unpack(PySequence_Fast_GET_ITEM(lists[0], i));
+    PyObject* c = PySequence_Fast_GET_ITEM(lists[1], i);
+    moe_adamw_tensor_t& q = t.data()[i];
+    q.g = g.const_data_ptr();
+    q.g_dtype = g.scalar_type() == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16;
+    q.p = p.mutable_data_ptr();
+    q.copy = nullptr;
+    if (!p.is_inference()) p.unsafeGetTensorImpl()->bump_version();
+    if (c != Py_None) {
+      const at::Tensor& x = THPVariable_Unpack(c);
+      q.copy = x.mutable_data_ptr();
+      if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+    }
+  }
+  Py_RETURN_NONE;
+}
+
+long long w4_bytes(int matrices, int K, int N, int group) {
+  return static_cast<long long>(p_moe_workspace_bytes(MOE_OP_W4_WEIGHTS, 0, 1, matrices, K, N, group));
+}
+
+int bf16_rows(PyObject* o, const char* what) {
+  const at::Tensor* t = tensor(o);
+  if (t == nullptr) return -1;
+  if (t->scalar_type() == at::kBFloat16) return 0;
+  PyErr_SetString(PyExc_ValueError, what);
+  return -1;
+}
+
+PyObject* w4_matvec(ARGS) {
+  COLLECT("moe_w4_matvec", 10, "x", "ids", "T", "top_k", "matrices", "N", "K", "group", "packed", "y", "stream");
+  int T, k, m, out, in, group, yt;
+  Any x, ids, w, y;
+  long long ldx, ldy;
+  moe_stream_t s;
+  if (bf16_rows(a[0], "x has to be bfloat16") < 0 || as_int(a[2], &T) < 0 || as_int(a[3], &k) < 0 || as_int(a[4], &m) < 0 ||
+      as_int(a[5], &out) < 0 || as_int(a[6], &in) < 0 || as_int(a[7], &group) < 0)
+    return nullptr;
+  const long long slots = (long long)T * k;
+  if (slots > INT_MAX || slots < INT_MIN) {
+    PyErr_SetString(PyExc_OverflowError, "an argument does not fit a C int");
+    return nullptr;
+  }
+  if (rows(a[0], T, in, &x, &ldx) < 0 || rows(a[9], (int)slots, out, &y, &ldy) < 0 || typed(a[1], at::kInt, slots, "ids", &ids) < 0 ||
+      raw(a[8], w4_bytes(m, in, out, group), "packed", &w) < 0 || element_type(a[9], &yt) < 0 || as_stream(a[10], &s) < 0)
+    return nullptr;
+  return finish("moe_w4_matvec", [&] { return p_moe_w4_matvec(x, ldx, ids, T, k, m, out, in, group, w, y, yt, ldy, s); });
+}
+
+PyObject* w4_swiglu_decode(ARGS) {
+  COLLECT("moe_w4_swiglu_decode", 13, "x", "ids", "weights", "T", "top_k", "E", "d", "h", "group", "w_ug", "w_down", "out", "ws", "stream");
+  int T, k, E, d, h, group;
+  Any x, ids, w, ug, down, out, ws;
+  long long ldx, ldo;
+  size_t n;
+  moe_stream_t s;
+  static const char* const types = "x and out have to be bfloat16";
+  if (bf16_rows(a[0], types) < 0 || bf16_rows(a[11], types) < 0 || as_int(a[3], &T) < 0 || as_int(a[4], &k) < 0 || as_int(a[5], &E) < 0 ||
+      as_int(a[6], &d) < 0 || as_int(a[7], &h) < 0 || as_int(a[8], &group) < 0)
+    return nullptr;
+  const long long slots = (long long)T * k;
+  const int both = E > INT_MAX / 2 || E < 0 ? -1 : 2 * E;
+  if (rows(a[0], T, d, &x, &ldx) < 0 || rows(a[11], T, d, &out, &ldo) < 0 || typed(a[1], at::kInt, slots, "ids", &ids) < 0 ||
+      typed(a[2], at::kFloat, slots, "weights", &w) < 0 || raw(a[9], w4_bytes(both, d, h, group), "w_ug", &ug) < 0 ||
+      raw(a[10], w4_bytes(E, h, d, group), "w_down", &down) < 0 || plain(a[12], &ws) < 0 || bytes_of(a[12], &n) < 0 || as_stream(a[13], &s) < 0)
+    return nullptr;
+  return finish("moe_w4_swiglu_decode", [&] {
+    return p_moe_w4_swiglu_decode(x, ldx, ids, w, T, k, E, d, h, group, ug, down, out, ldo, ws, n, s);
+  });
+}
+
 // ------------------------------------------------------------------ module
 // bind(addresses: dict, raise_)
 PyObject* bind(PyObject* self, PyObject* args) {
@@ -467,6 +714,14 @@ PyMethodDef methods[] = {{"bind", bind, METH_VARARGS, nullptr},
                                 CALL(grouped_swiglu_fwd_mxfp4),
                                 CALL(unpermute_combine),
                                 CALL(route_offsets),
+                                CALL(residual_norm_fwd),
+                                CALL(residual_norm_bwd),
+                                CALL(grad_norm),
+                                CALL(adamw_step),
+                                CALL(w4_matvec),
+                                CALL(w4_swiglu_decode),
+                                {"adamw_pointers", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<adamw_pointers>)),
+                                 METH_FASTCALL | METH_KEYWORDS, nullptr},
                                 {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

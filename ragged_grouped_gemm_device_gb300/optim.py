@@ -18,6 +18,26 @@ from . import _lib
 BLOCK = 32  # elements of a scale of the 8-bit states
 
 
+def _dense(t, device, what):
+    if not t.is_cuda or not t.is_contiguous() or t.get_device() != device or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{what} has to be a dense bfloat16 or float32 tensor on cuda:{device}")
+
+
+def _pointers(table, device, params, copies, grads):
+    """Write where a step's tensors lie into the table (at every step: an assignment to .data moves a parameter) and count their
+    versions up. The extension's adamw_pointers does the same."""
+    for q, p, g in zip(table, params, grads):
+        _dense(g, device, "a gradient")
+        if g.numel() != q.n:
+            raise ValueError(f"a gradient has {g.numel()} elements, its parameter {q.n}")
+        _dense(p, device, "a parameter")
+        if p.numel() != q.n or _lib._dtype(p) != q.p_dtype:
+            raise ValueError("a parameter's size or type has changed")
+    for q, p, c, g in zip(table, params, copies, grads):
+        q.g, q.g_dtype, q.p, q.copy = g.data_ptr(), _lib._dtype(g), p.data_ptr(), None if c is None else c.data_ptr()
+    torch.autograd.graph.increment_version([t for t in (*params, *copies) if t is not None and not t.is_inference()])
+
+
 class AdamW:
     """params: dense CUDA tensors of one device, bf16 or fp32, updated in place. weight_decay: one number, or one for each
     parameter. copies: for each parameter None or a bf16 tensor of its shape (fp32 parameters only). max_norm: the
@@ -41,11 +61,11 @@ class AdamW:
             raise ValueError("weight_decay and copies have to have one entry for each parameter")
         self.device = params[0].device
         for p, c in zip(params, copies):
-            self._dense(p, "a parameter")
+            _dense(p, self.device.index, "a parameter")
             if c is not None and (c.dtype != torch.bfloat16 or c.shape != p.shape or p.dtype != torch.float32):
                 raise ValueError("a copy has to be bfloat16, of the shape of its float32 parameter")
             if c is not None:
-                self._dense(c, "a copy")
+                _dense(c, self.device.index, "a copy")
         if max_norm is not None and not 0 < max_norm < float("inf"):
             raise ValueError("max_norm has to be positive and finite")
         self.params, self.copies, self.state_bits = params, copies, state_bits
@@ -71,10 +91,6 @@ class AdamW:
             if state_bits == 8:
                 q.m_scale, q.v_scale = self.m_scale.data_ptr() + at // BLOCK, self.v_scale.data_ptr() + at // BLOCK
 
-    def _dense(self, t, what):
-        if not t.is_cuda or not t.is_contiguous() or t.device != self.device or t.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"{what} has to be a dense bfloat16 or float32 tensor on {self.device}")
-
     @property
     def steps(self) -> int:
         """Steps done (reads the device)."""
@@ -90,18 +106,12 @@ class AdamW:
         (a tensor of no dimension that the next step overwrites), or None without max_norm."""
         if len(grads) != len(self.params):
             raise ValueError(f"expected {len(self.params)} gradients, not {len(grads)}")
-        for q, p, c, g in zip(self._table, self.params, self.copies, grads):
-            self._dense(g, "a gradient")
-            if g.numel() != q.n:
-                raise ValueError(f"a gradient has {g.numel()} elements, its parameter {q.n}")
-            q.g, q.g_dtype = g.data_ptr(), _lib._dtype(g)
-            # read at every step: an assignment to .data moves a parameter
-            q.p, q.copy = p.data_ptr(), None if c is None else c.data_ptr()
+        _lib.load()
+        (_lib.adamw_pointers or _pointers)(self._table, self.device.index, self.params, self.copies, grads)
         scale = None
         if self.max_norm is not None:
             _lib.moe_grad_norm(self._table, self.max_norm, self._norm, self._ws, stream)
             scale = self._norm[1:]
         _lib.moe_adamw_step(self._table, self.state_bits, self.lr, *self.betas, self.eps, self.seed, self._steps,
                             self.lr_scale, scale, stream)
-        torch.autograd.graph.increment_version([t for t in (*self.params, *self.copies) if t is not None and not t.is_inference()])
         return None if scale is None else self._norm[0]
