@@ -31,19 +31,22 @@ constexpr int THREADS = 256;
 constexpr int VB = 8;         // elements of a thread in one round
 constexpr int CHUNK = 4096;   // elements of a piece: two rounds
 constexpr int STEP_BLOCKS = 4;  // blocks on an SM
-constexpr int MAX_TENSORS = 128;  // of a launch: 11 KB of parameters
+// Tensors of a launch: 12 KB of parameters, or 1.5 KB for the few tensors of one block, whose launch would wait for them.
+constexpr int MAX_TENSORS = 128, FEW_TENSORS = 16;
 constexpr int NORM_BLOCKS = 1216;
 
+template <int N>
 struct Batch {
   int count;
   int first;                          // index of the first tensor in the call
-  unsigned chunk0[MAX_TENSORS + 1];   // first piece of each tensor, and the end
-  moe_adamw_tensor_t t[MAX_TENSORS];
-  unsigned char wide[MAX_TENSORS];    // 1: 16-byte accesses
+  unsigned chunk0[N + 1];   // first piece of each tensor, and the end
+  moe_adamw_tensor_t t[N];
+  unsigned char wide[N];    // 1: 16-byte accesses
 };
 
 // the tensor of piece c: the last one that starts at or before it and is not empty
-__device__ __forceinline__ int find_tensor(const Batch& b, unsigned c) {
+template <int N>
+__device__ __forceinline__ int find_tensor(const Batch<N>& b, unsigned c) {
   int lo = 0, hi = b.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -339,8 +342,8 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(THREADS, STEP_BLOCKS) adamw_kernel(const __grid_constant__ Batch batch, const StepArgs a) {
+template <int BITS, int N>
+__global__ void __launch_bounds__(THREADS, STEP_BLOCKS) adamw_kernel(const __grid_constant__ Batch<N> batch, const StepArgs a) {
   grid_wait();
   TensorStep u;
   u.c = a.grad_scale ? *after_wait(a.grad_scale) : 1.0f;
@@ -387,7 +390,8 @@ __global__ void __launch_bounds__(THREADS, STEP_BLOCKS) adamw_kernel(const __gri
 
 // Partial sums of g^2, one fp64 per block: the pieces blockIdx.x, blockIdx.x + gridDim.x, ... of a launch's tensors, added to
 // what the launches before it left.
-__global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Batch batch, double* part, bool first) {
+template <int N>
+__global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constant__ Batch<N> batch, double* part, bool first) {
   __shared__ __align__(16) float red[2][32];
   grid_wait();
   double sum = 0.0;
@@ -459,8 +463,9 @@ moe_status_t check_tensors(const moe_adamw_tensor_t* t, int count, bool grads, i
 }
 
 // the tensors i, i + 1, ... that one launch takes
-int fill(Batch& b, const moe_adamw_tensor_t* t, int i, int count, bool grads, int bits) {
-  const int n = std::min(count - i, MAX_TENSORS);
+template <int N>
+int fill(Batch<N>& b, const moe_adamw_tensor_t* t, int i, int count, bool grads, int bits) {
+  const int n = std::min(count - i, N);
   b.count = n;
   b.first = i;
   unsigned at = 0;
@@ -474,6 +479,35 @@ int fill(Batch& b, const moe_adamw_tensor_t* t, int i, int count, bool grads, in
   }
   b.chunk0[n] = at;
   return n;
+}
+
+template <int N>
+cudaError_t launch_norm(const moe_adamw_tensor_t* tensors, int count, int blocks, double* part, cudaStream_t s) {
+  for (int i = 0; i < count || i == 0;) {
+    Batch<N> b;
+    const int n = fill(b, tensors, i, count, true, 0);
+    const cudaError_t err = launch_dependent(grad_norm_kernel<N>, blocks, THREADS, 0, s, b, part, i == 0);
+    if (err != cudaSuccess) return err;
+    i += std::max(n, 1);
+  }
+  return cudaSuccess;
+}
+
+template <int N>
+cudaError_t launch_step(StepArgs a, const moe_adamw_tensor_t* tensors, int count, int state_bits, cudaStream_t s) {
+  for (int i = 0; i < count || i == 0;) {
+    Batch<N> b;
+    const int n = fill(b, tensors, i, count, false, state_bits);
+    // 8-bit states: as many blocks as fit, since what a block computes once would be a fifth of the instructions of a piece. 32 bits,
+    // bound by memory: a block for each piece, which spread better (201 million parameters: 902 us, 1047 in runs).
+    a.blocks = std::max(b.chunk0[n], 1u);
+    if (state_bits == 8) a.blocks = std::min(a.blocks, static_cast<unsigned>(STEP_BLOCKS * device_sm_count()));
+    a.last = i + n >= count;
+    const cudaError_t err = launch_dependent(state_bits == 8 ? adamw_kernel<8, N> : adamw_kernel<32, N>, a.blocks, THREADS, 0, s, b, a);
+    if (err != cudaSuccess) return err;
+    i += std::max(n, 1);
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -505,13 +539,8 @@ moe_status_t moe_grad_norm(const moe_adamw_tensor_t* tensors, int count, float m
     most = std::max(most, chunks);
   }
   const int blocks = static_cast<int>(std::min<unsigned>(most, NORM_BLOCKS));
-  cudaError_t err = cudaSuccess;
-  for (int i = 0; err == cudaSuccess && (i < count || i == 0);) {
-    Batch b;
-    const int n = fill(b, tensors, i, count, true, 0);
-    err = launch_dependent(grad_norm_kernel, blocks, THREADS, 0, s, b, part, i == 0);
-    i += std::max(n, 1);
-  }
+  cudaError_t err = count <= FEW_TENSORS ? launch_norm<FEW_TENSORS>(tensors, count, blocks, part, s)
+                                           : launch_norm<MAX_TENSORS>(tensors, count, blocks, part, s);
   if (err == cudaSuccess)
     err = launch_dependent(grad_norm_end_kernel, 1, 256, 0, s, static_cast<const double*>(part), blocks, max_norm, norm);
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
@@ -544,19 +573,9 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
   a.lr_scale = lr_scale;
   a.grad_scale = grad_scale;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  for (int i = 0; i < count || i == 0;) {
-    Batch b;
-    const int n = fill(b, tensors, i, count, false, state_bits);
-    // 8-bit states: as many blocks as fit, since what a block computes once would be a fifth of the instructions of a piece. 32 bits,
-    // bound by memory: a block for each piece, which spread better (201 million parameters: 902 us, 1047 in runs).
-    a.blocks = std::max(b.chunk0[n], 1u);
-    if (state_bits == 8) a.blocks = std::min(a.blocks, static_cast<unsigned>(STEP_BLOCKS * device_sm_count()));
-    a.last = i + n >= count;
-    const cudaError_t err = launch_dependent(state_bits == 8 ? adamw_kernel<8> : adamw_kernel<32>, a.blocks, THREADS, 0, s, b, a);
-    if (err != cudaSuccess) return cuda_fail(err);
-    i += std::max(n, 1);
-  }
-  return MOE_OK;
+  const cudaError_t err = count <= FEW_TENSORS ? launch_step<FEW_TENSORS>(a, tensors, count, state_bits, s)
+                                               : launch_step<MAX_TENSORS>(a, tensors, count, state_bits, s);
+  return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
 }  // extern "C"

@@ -306,6 +306,7 @@ struct W4Args {
   void* out;
   long long ldo;
   bool y_bf16;
+  bool early;              // ids are from before the kernel ahead, which only made x
 };
 
 constexpr int SEGMENT = 16;  // chunks of x in shared memory at most
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = blockIdx.y;
   const int wk = warp % WK, tile = blockIdx.x * WT + warp / WK;  // this warp's share of K and its rows
   const bool live = tile < a.w.tiles;
-  grid_wait();
+  if (!a.early) grid_wait();
   const int32_t* ids = after_wait(a.ids);
   const bool by_slot = a.slots <= a.E, single = a.ids == nullptr ? false : a.slots == a.top_k;
   int e = a.ids == nullptr ? 0 : by_slot || single ? ids[group] : group;
@@ -404,6 +405,8 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
           }
       };
       load(wk);  // on their way while x comes
+      if constexpr (SWIGLU) grid_release();  // the down product reads the ids and its first weights meanwhile
+      if (a.early) grid_wait();
       __syncthreads();
       // Each thread eight elements, four threads the 32 of a sum; whole warps, because of the shuffles
       const int units = rows * chunks * 16;
@@ -523,7 +526,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
   int* count = reinterpret_cast<int*>(smem + at.count);       // slots of each expert, of none; then where the next one goes
   __shared__ int n_groups;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  grid_wait();
+  if (!a.early) grid_wait();
   const int32_t* ids = after_wait(a.ids);
   if (a.ids == nullptr || a.slots == a.top_k) {
     const int per = a.ids == nullptr ? 8 : 1;
@@ -612,6 +615,8 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
   };
   for (uint32_t to = ring; to != ring_end; to += Smem::step) fill(to);
 
+  if constexpr (SWIGLU) grid_release();  // the down product reads the ids and its first weights meanwhile
+  if (a.early) grid_wait();
   const bf16* x = after_wait(a.x);
   if constexpr (!SWIGLU) {  // rows of dropped slots
     const auto zero_row = [&](int slot) {
@@ -723,7 +728,7 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
   __shared__ int expert[32];
   __shared__ float weight[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = blockIdx.x, t = blockIdx.y;
-  grid_wait();
+  // the ids and weights are from before the kernel ahead, which only made x
   if (threadIdx.x < a.top_k) {
     const int s = t * a.top_k + threadIdx.x;
     const int e = after_wait(a.ids)[s];
@@ -733,8 +738,9 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
   __syncthreads();
   const int items = a.top_k * a.w.chunks;
   float tot[1][1][4] = {{{0.f, 0.f, 0.f, 0.f}}};
-  const bf16* x = after_wait(a.x);
   const Unpack unpack;
+  bool waited = false;
+  const bf16* x = a.x;
   for (int i0 = warp; i0 < items; i0 += DOWN_WARPS * U) {
     Piece<PER> p[U][1];
     uint4 v[U][4];
@@ -743,6 +749,16 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks, c = i % a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
       p[u][0].load(a.w.base + ((static_cast<size_t>(expert[j]) * a.w.tiles + tile) * a.w.chunks + c) * Piece<PER>::bytes, lane);
+    }
+    if (!waited) {
+      grid_wait();
+      x = after_wait(a.x);
+      waited = true;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks, c = i % a.w.chunks;
+      if (i >= items || expert[j] < 0) continue;
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[u][q] = lane < 4 ? load_x<true>(x + static_cast<size_t>(t * a.top_k + j) * a.ldx, c * 128 + q * 32 + lane * 8, a.K)
@@ -752,9 +768,11 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
+      // the sums of x by a product with ones: column 0 of every row
       multiply<PER, 1, 1>(p[u], tot, weight[j], unpack, [&](int q, int) { return v[u][q]; }, [&](int q, int) { return minus_sums(v[u][q]); });
     }
   }
+  if (!waited) grid_wait();
   // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
   if ((lane & 3) == 0) {
     sums[warp][0][lane >> 2] = tot[0][0][0];
@@ -995,6 +1013,7 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
   b.xdiv = 1;
   b.N = d;
   b.K = pitch;  // zeros from h on
+  b.early = true;
   b.w = packed_at(w_down, d, h, group);
   if (down_by_token(slots, E)) {
     b.out = out;
