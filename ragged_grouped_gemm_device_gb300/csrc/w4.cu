@@ -310,15 +310,15 @@ struct W4Args {
 };
 
 constexpr int SEGMENT = 16;  // chunks of x in shared memory at most
-constexpr int WARPS = 4;
 
 // Slots of one expert times its weights: WK warps of a block own 16 rows of the matrix (of both halves, gate and up, with
 // SWIGLU) and take the slots of its expert 8 NT at a time. They share the chunks of K and add up their sums in shared
 // memory, in warp order. A group is a slot that names its expert first (slots <= E), or an expert, with one more group for
 // dropped slots; of a single token every slot is one.
-template <int PER, int NT, int WK, bool SWIGLU, bool VEC>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(const W4Args a) {
-  constexpr int TILES = SWIGLU ? 2 : 1, COLS = 8 * NT, U = 2, WT = WARPS / WK;
+// U: pieces (pairs of pieces) of a warp on their way at once.
+template <int PER, int NT, int WARPS, int WK, int U, bool SWIGLU, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : U == 4 ? 3 : NT == 1 ? 5 : 4) w4_group_kernel(const W4Args a) {
+  constexpr int TILES = SWIGLU ? 2 : 1, COLS = 8 * NT, WT = WARPS / WK;
   extern __shared__ __align__(16) uint8_t smem[];
   uint4* xs = reinterpret_cast<uint4*>(smem);                                    // [chunks of a segment * 4][COLS][4]
   float* xsum = reinterpret_cast<float*>(smem + a.segment * 4 * COLS * 64);        // [chunks of a segment * 4][COLS]: minus the sums
@@ -405,8 +405,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 5 : 4) w4_group_kernel(c
           }
       };
       load(wk);  // on their way while x comes
-      if constexpr (SWIGLU) grid_release();  // the down product reads the ids and its first weights meanwhile
-      if (a.early) grid_wait();
+      if (a.early && seg0 == 0 && r0 == 0) grid_wait();
       __syncthreads();
       // Each thread eight elements, four threads the 32 of a sum; whole warps, because of the shuffles
       const int units = rows * chunks * 16;
@@ -816,12 +815,13 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const float* y, long lo
   }
 }
 
-template <int PER, int NT, int WK, bool SWIGLU, bool VEC>
+template <int PER, int NT, int WARPS, int WK, int U, bool SWIGLU>
 cudaError_t launch_group_as(const W4Args& a, int groups, cudaStream_t s) {
+  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
   const int x_bytes = 4 * 8 * NT * 68, sum_bytes = WARPS * (SWIGLU ? 2 : 1) * NT * 512;
-  const auto kernel = w4_group_kernel<PER, NT, WK, SWIGLU, VEC>;
+  const auto kernel = vec ? w4_group_kernel<PER, NT, WARPS, WK, U, SWIGLU, true> : w4_group_kernel<PER, NT, WARPS, WK, U, SWIGLU, false>;
   const int smem = a.segment * x_bytes + sum_bytes + std::max(1, a.slots) * 4;
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {  // beside the static shared memory
     const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), SEGMENT * x_bytes + sum_bytes + MAX_SLOTS * 4);
     if (err != cudaSuccess) return err;
   }
@@ -829,21 +829,19 @@ cudaError_t launch_group_as(const W4Args& a, int groups, cudaStream_t s) {
 }
 template <int PER, int NT, bool SWIGLU>
 cudaError_t launch_group_split(const W4Args& a, int groups, cudaStream_t s) {
-  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
   // The warps of a block share K where that gives no more than eight blocks for each SM: few blocks leave SMs idle, many have each its
   // share of reading ids and x.
   const bool few = static_cast<long long>(a.w.tiles) * groups <= 8LL * device_sm_count();
-  if (few) return vec ? launch_group_as<PER, NT, 4, SWIGLU, true>(a, groups, s) : launch_group_as<PER, NT, 4, SWIGLU, false>(a, groups, s);
-  return vec ? launch_group_as<PER, NT, 1, SWIGLU, true>(a, groups, s) : launch_group_as<PER, NT, 1, SWIGLU, false>(a, groups, s);
+  return few ? launch_group_as<PER, NT, 4, 4, 2, SWIGLU>(a, groups, s) : launch_group_as<PER, NT, 4, 1, 2, SWIGLU>(a, groups, s);
 }
 
 template <int PER, bool SWIGLU, bool VEC>
 cudaError_t launch_stream_as(const W4Args& a, cudaStream_t s) {
   using Smem = StreamSmem<PER, SWIGLU>;
   StreamShape sh;
-  // Two to four chunks of a task for a warp: with fewer the sums at its end cost as much as its products, with more there are too few
-  // tasks to share evenly.
-  sh.log_wts = a.w.chunks >= 24 ? 0 : a.w.chunks >= 12 ? 1 : a.w.chunks >= 4 ? 2 : 3;
+  // Long rows are shared, three or four chunks a warp: with fewer the sums at the end of a task cost as much as its products, with more there are
+  // too few tasks to share evenly. Short rows go to one warp each.
+  sh.log_wts = a.w.chunks >= 24 ? 0 : a.w.chunks >= 12 ? 1 : 3;
   const int wts = 1 << sh.log_wts;
   sh.wk = STREAM_WARPS / wts;
   sh.sets = (a.w.tiles + wts - 1) / wts;
@@ -868,6 +866,9 @@ cudaError_t launch_group(W4Args a, cudaStream_t s) {
     return vec ? launch_stream_as<PER, SWIGLU, true>(a, s) : launch_stream_as<PER, SWIGLU, false>(a, s);
   }
   const int groups = a.ids == nullptr ? 1 : a.slots <= a.E ? a.slots : a.slots == a.top_k ? a.slots : a.E + (SWIGLU ? 0 : 1);
+  // A single token: as many warps and loads that all weights of a tile are on their way at once (up to K = 4096 with eight warps, 2048
+  // of gate and up with four, of which three blocks fit on an SM: 4096 x 4096 takes 4.5 us, 5.6 with two loads of four warps each).
+  if (a.slots == (a.ids == nullptr ? 1 : a.top_k)) return launch_group_as<PER, 1, SWIGLU ? 4 : 8, SWIGLU ? 4 : 8, 4, SWIGLU>(a, groups, s);
   return each <= 8 ? launch_group_split<PER, 1, SWIGLU>(a, groups, s) : launch_group_split<PER, 2, SWIGLU>(a, groups, s);
 }
 template <bool SWIGLU>
