@@ -563,10 +563,19 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
         made += sum >> 16;
       }
       if (lane == 0) n_groups = made;
+      // The slots in order, by one warp: every block has to find the same slots in the same group.
+      for (int i0 = 0; i0 < a.slots; i0 += 32) {
+        const int i = i0 + lane, e = i < a.slots ? of(i) : a.E + 1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1)), at_e = i < a.slots ? count[e] : 0;
+        __syncwarp();
+        if (i < a.slots) {
+          list[at_e + rank] = i;
+          if (rank == 0) count[e] = at_e + __popc(same);
+        }
+        __syncwarp();
+      }
     }
-    __syncthreads();
-    // the order of an expert's slots is left to the atomics: each is a column of its own, and no sum goes over columns
-    for (int i = threadIdx.x; i < a.slots; i += STREAM_THREADS) list[atomicAdd(count + of(i), 1)] = i;
   }
   __syncthreads();
   const int wk = warp & (sh.wk - 1), wts = 1 << sh.log_wts, wt = warp * wts / STREAM_WARPS;

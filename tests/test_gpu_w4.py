@@ -185,6 +185,31 @@ def test_the_same_expert_twice(lib):
     _check_decode(x, ids, weights, gate, up, wd, layer.forward(x, ids, weights))
 
 
+@pytest.mark.parametrize("E,k,d,h,group", [(40, 8, 256, 1024, 64), (24, 4, 1024, 300, 32), (64, 8, 136, 520, 128)])
+def test_popular_experts_in_many_blocks(lib, E, k, d, h, group):
+    """Experts with more slots than a group of eight takes, whose tiles are spread over many blocks: every block has to find the
+    same slots in a group, or some are left out. Work and output buffers start as NaN."""
+    ug, down, gate, up, wd = _experts(E, d, h, group)
+    layer = Int4ExpertLayer.from_checkpoint(ug, down, E, d, h, group)
+    T = 48
+    x = _x(T, d)
+    g = torch.Generator().manual_seed(E)
+    ids = torch.sort(torch.randn(T, E, generator=g) + 2.0 * torch.randn(E, generator=g), dim=1, descending=True).indices[:, :k].to(torch.int32)
+    assert int(torch.bincount(ids.flatten().long()).max()) > 16
+    weights = torch.rand(T, k, generator=g).cuda()
+    layer._buffers(T, k)
+    layer.ws.fill_(255)
+    layer.out.fill_(float("nan"))
+    first = layer.forward(x, ids.cuda(), weights).clone()
+    _check_decode(x, ids.cuda(), weights, gate, up, wd, first)
+    layer.ws.fill_(255)
+    assert torch.equal(first, layer.forward(x, ids.cuda(), weights))
+    y = torch.full((T * k, h), float("nan"), device="cuda")
+    _lib.moe_w4_matvec(x, ids.cuda(), T, k, 2 * E, h, d, group, layer.w_ug, y)
+    w = np.stack([gate, up], axis=1).reshape(2 * E, h, d)
+    _check_matvec(x, ids.cuda(), k, w, y)
+
+
 def test_more_slots_than_one_call_takes(lib):
     E, d, h, group, T, k = 5, 64, 32, 32, 700, 8
     ug, down, gate, up, wd = _experts(E, d, h, group)
