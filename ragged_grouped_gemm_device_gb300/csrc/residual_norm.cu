@@ -406,12 +406,12 @@ __device__ __forceinline__ void put8(T* p, const F2 (&v)[4]) {
 }
 
 // Blocks on an SM, which size the grids and bound the registers.
-constexpr int fwd_blocks(int tpr) { return 512 / block_threads(tpr); }
+constexpr int fwd_blocks(int tpr, int nch, bool bias) { return tpr == 256 && nch == 1 ? (bias ? 2 : 3) : 512 / block_threads(tpr); }
 constexpr int bwd_blocks(int tpr) { return tpr <= 128 ? 3 : 1; }
 
 // BIAS: some norm has a beta.
 template <typename TX, typename TY, int NCH, int TPR, bool BIAS>
-__global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR)) join_fwd_kernel(const JoinArgs a) {
+__global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)) join_fwd_kernel(const JoinArgs a) {
   grid_wait();
   constexpr int ROWS = block_threads(TPR) / TPR;
   __shared__ __align__(16) float red[2][32];
@@ -734,8 +734,9 @@ __global__ void __launch_bounds__(1024) join_partials_kernel(const JoinArgs a, i
 template <typename TX, typename TY, int NCH, int TPR>
 cudaError_t launch_fwd_rows(const JoinArgs& a, cudaStream_t s) {
   constexpr int ROWS = block_threads(TPR) / TPR, smem = RowFeed<NCH, TPR, TX, TY>::smem_bytes;
-  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, fwd_blocks(TPR) * static_cast<long long>(device_sm_count())));
-  const auto kernel = a.b1 || a.b2 ? join_fwd_kernel<TX, TY, NCH, TPR, true> : join_fwd_kernel<TX, TY, NCH, TPR, false>;
+  const bool bias = a.b1 || a.b2;
+  const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, fwd_blocks(TPR, NCH, bias) * static_cast<long long>(device_sm_count())));
+  const auto kernel = bias ? join_fwd_kernel<TX, TY, NCH, TPR, true> : join_fwd_kernel<TX, TY, NCH, TPR, false>;
   if (smem > 40 * 1024) {  // beside the static shared memory
     const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (err != cudaSuccess) return err;
@@ -764,7 +765,7 @@ cudaError_t launch_fwd(const JoinArgs& a, bool vec, cudaStream_t s) {
     if (chunks <= 32) return launch_fwd_rows<TX, TY, 1, 32>(a, s);
     if (chunks <= 64) return launch_fwd_rows<TX, TY, 2, 32>(a, s);
     if (chunks <= 128) return launch_fwd_rows<TX, TY, 1, 128>(a, s);
-    if (chunks <= 256) return launch_fwd_rows<TX, TY, 2, 128>(a, s);
+    if (chunks <= 256) return launch_fwd_rows<TX, TY, 1, 256>(a, s);
     if (chunks <= 512) return launch_fwd_rows<TX, TY, 2, 256>(a, s);
     return launch_fwd_rows<TX, TY, 2, 512>(a, s);
   }
