@@ -701,18 +701,20 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
     for (int h = 0; h < TILES; ++h)
 #pragma unroll
       for (int i = 0; i < 4; ++i) sums[((warp * TILES + h) * 4 + i) * 32 + lane] = tot[h][0][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * wts * rows; i += STREAM_THREADS) {
-      const int r = i & 15, w0 = (i >> 4) & (wts - 1), col = i >> 4 >> sh.log_wts;  // consecutive threads: consecutive rows of the output
+    // only the warps that share a tile's K wait for one another
+    if (sh.wk == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(sh.wk * 32) : "memory");
+    for (int i = wk * 32 + lane; i < 16 * rows; i += sh.wk * 32) {
+      const int r = i & 15, col = i >> 4;  // consecutive threads: consecutive rows of the output
       // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + c / 2
       const int from = ((r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + (col >> 1);
       float v[TILES];
 #pragma unroll
       for (int h = 0; h < TILES; ++h) {
         v[h] = 0.f;
-        for (int w = 0; w < sh.wk; ++w) v[h] += sums[((w0 * sh.wk + w) * TILES + h) * 128 + from];
+        for (int w = 0; w < sh.wk; ++w) v[h] += sums[((wt * sh.wk + w) * TILES + h) * 128 + from];
       }
-      const int row = (set * wts + w0) * 16 + r, s = list[first + col];
+      const int row = (set * wts + wt) * 16 + r, s = list[first + col];
       if constexpr (SWIGLU) {
         // rows past h up to the pitch: their scales are 0
         if (row < a.ldo) static_cast<bf16*>(a.out)[s * a.ldo + row] = __float2bfloat16_rn(v[0] / (1.0f + expf(-v[0])) * v[1]);
