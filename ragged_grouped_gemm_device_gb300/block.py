@@ -59,7 +59,7 @@ class MoEBlock:
         self.experts, self.E, self.d, self.k, self.eps = experts, E, d, top_k, eps
         self.flags = _lib.GATE_RENORM if renorm else 0
         self.device = w_router.device
-        self._T = None
+        self._T = self._ran = None
         self._alone = None if self.plain else MoEStack([self])
 
     def _buffers(self, T: int):
@@ -89,6 +89,7 @@ class MoEBlock:
         self._buffers(T)
         self.x = x  # read again by backward(), like gamma and w_router
         self._read = [(t, _version(t)) for t in (x, self.gamma, self.w_router)]
+        self._ran = self
         _lib.moe_layer_norm_fwd(x, _dense(self.gamma), _dense(self.beta), T, self.d, self.eps, self.normed, self.mean, self.rstd)
         return x + self._route(token_mask)
 
@@ -123,7 +124,7 @@ class MoEBlock:
         if not self.plain:
             grads = self._alone.backward(dout, None if d_loss is None else [d_loss])
             return dict(dx=grads["dx"], **grads["blocks"][0])
-        self._check_backward(dout)
+        self._check_backward(dout, self)
         T = self._T
         dout = _dense(dout)
         grads = self._route_backward(dout, d_loss)
@@ -131,9 +132,11 @@ class MoEBlock:
                                 self.dbeta, self.norm_ws)
         return dict(dx=self.dx + dout, gamma=self.dgamma, beta=self.dbeta, **grads)
 
-    def _check_backward(self, dout):
+    def _check_backward(self, dout, owner):
         if not isinstance(self.experts, ExpertLayer):
             raise TypeError("4-bit experts have no backward: train on an ExpertLayer")
+        if self._ran is not owner:
+            raise RuntimeError("the block's buffers hold another run, by itself or in another stack")
         if any(_version(t) != v for t, v in self._read):
             raise RuntimeError("x, gamma or w_router was changed in place since forward(): their gradients would be wrong")
         if tuple(dout.shape) != (self._T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:
@@ -161,6 +164,9 @@ class MoEStack:
             raise ValueError("the blocks have to be of one width and on one device")
         if len({id(b.experts) for b in self.blocks}) < len(self.blocks) or len({id(b) for b in self.blocks}) < len(self.blocks):
             raise ValueError("every block has to have experts of its own: their buffers hold what the backward reads")
+        # a join has one eps for the norms on both its sides
+        if any(a.post != "none" and a.eps != b.eps for a, b in zip(self.blocks, self.blocks[1:])):
+            raise ValueError("a block with a norm behind it has to have the eps of the next block")
         self.d, self._T = first.d, None
 
     def _buffers(self, T: int):
@@ -207,17 +213,18 @@ class MoEStack:
         self.x = x
         for b in self.blocks:
             b._read = [(t, _version(t)) for n, t in b.tensors().items() if n not in ("w_ug", "w_down")]
+            b._ran = self
         self.blocks[0]._read.append((x, _version(x)))
         return r
 
     @torch.no_grad()
     def backward(self, dout: torch.Tensor, d_loss=None) -> dict:
         """dout [T, d] bf16, d_loss: None or for each block None or [2] fp32 -> dx (bf16) and blocks, a list of each
-        block's gradients by the names of its tensors()."""
+        block's gradients by the names of its tensors(); dx is a buffer that the next backward overwrites."""
         if self._T is None:
             raise RuntimeError("backward() before forward()")
         for b in self.blocks:
-            b._check_backward(dout)
+            b._check_backward(dout, self)
         count, T = len(self.blocks), self._T
         losses = [None] * count if d_loss is None else list(d_loss)
         if len(losses) != count:

@@ -222,6 +222,34 @@ def test_refusals(lib):
     a.gate.mul_(2.0)
     with pytest.raises(RuntimeError, match="in place"):
         stack.backward(x)
+    # one eps for the norms on both sides of a join
+    b.eps = 1e-3
+    with pytest.raises(ValueError, match="eps"):
+        MoEStack([a, b])
+    MoEStack([b])
     for bad in (dict(pre="none"), dict(post="norm"), dict(post="none"), dict(post="rms", post_beta=a.gate)):
         with pytest.raises(AssertionError):
             MoEBlock(**{**dict(gamma=a.gamma, beta=None, w_router=a.w_router, experts=a.experts, top_k=2, pre="rms", post="rms", post_gamma=a.gate), **bad})
+
+
+def test_backward_of_a_run_that_is_gone(lib):
+    """A block's buffers hold its last run, whoever asked for it."""
+    p, q = _parameters(5, "rms", "rms"), _parameters(6, "layer", "none")
+    a, b = _block(p, "rms", "rms"), _block(p, "rms", "rms")
+    plain = MoEBlock(*(q[n].cuda() for n in ("gamma", "beta", "w_router")), ExpertLayer(q["w_ug"].cuda(), q["w_down"].cuda()), k)
+    stack, x = MoEStack([plain, a, b]), torch.randn(5, d, device="cuda").bfloat16()
+    with pytest.raises(RuntimeError):
+        plain.backward(x)
+    for alone in (plain, a):
+        stack.forward(x)
+        with pytest.raises(RuntimeError):
+            alone.backward(x)
+        alone.forward(x)
+        with pytest.raises(RuntimeError, match="another"):
+            stack.backward(x)
+        alone.backward(x)
+    MoEStack([b, a]).forward(x)
+    with pytest.raises(RuntimeError, match="another"):
+        stack.backward(x)
+    stack.forward(x)
+    stack.backward(x)
