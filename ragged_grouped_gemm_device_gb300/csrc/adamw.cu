@@ -219,9 +219,10 @@ struct StepArgs {
   bool last;        // the call's last launch counts the step
 };
 
-// The square root, correctly rounded, of a value in [2^-126, inf): an estimate s from the reciprocal root y, and Newton's step s
-// + (v - s^2) y / 2 with the residual from a fused product. It equals sqrtf for every mantissa and both parities of the
-// exponent (compared for all 2^24 of them), and takes a quarter of its instructions.
+// The square root of a value in [2^-126, inf): an estimate s from the reciprocal root y, and Newton's step s + (v - s^2) y / 2 with
+// the residual from a fused product. It equals sqrtf for every mantissa and both parities of the exponent (compared for all 2^24 of
+// them) as long as the residual is a normal number, v from 2^-80 on; below that it is within a unit. It takes a quarter of
+// sqrtf's instructions.
 __device__ __forceinline__ float sqrt_normal(float v) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
@@ -567,7 +568,7 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
   a.omb2 = static_cast<float>(1.0 - beta2);
   a.log_b1 = static_cast<float>(std::log(beta1));
   a.log_b2 = static_cast<float>(std::log(beta2));
-  a.eps = static_cast<float>(eps);
+  a.eps = eps > 0.0 ? std::max(static_cast<float>(eps), 1.17549435e-38f) : 0.f;  // the quotient takes subnormals for 0
   a.seed = seed;
   a.steps = steps;
   a.lr_scale = lr_scale;

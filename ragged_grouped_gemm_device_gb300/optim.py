@@ -45,8 +45,8 @@ class AdamW:
     lr_scale: nullable fp32 [1] on the device, a factor of lr that is read when the step runs.
 
     `m`, `v` (and `m_scale`, `v_scale` of 8-bit states) are flat buffers in which parameter i has the elements
-    starts[i] to starts[i] + numel, starts[i] a multiple of 32; they and `steps` are what a checkpoint keeps. What lies
-    between two parameters stays 0."""
+    starts[i] to starts[i] + numel, starts[i] a multiple of 32; they and `steps` are what a checkpoint keeps and what is
+    copied back into them. What lies between two parameters stays 0."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01,
                  state_bits: int = 32, copies=None, max_norm: float = None, seed: int = 0, lr_scale: torch.Tensor = None):
@@ -66,6 +66,9 @@ class AdamW:
                 raise ValueError("a copy has to be bfloat16, of the shape of its float32 parameter")
             if c is not None:
                 _dense(c, self.device.index, "a copy")
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (*params, *copies) if t is not None and t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise ValueError("parameters and copies may not overlap: a step would update the shared elements twice")
         if max_norm is not None and not 0 < max_norm < float("inf"):
             raise ValueError("max_norm has to be positive and finite")
         self.params, self.copies, self.state_bits = params, copies, state_bits

@@ -118,6 +118,30 @@ def test_steps_match_the_reference(lib, bits, p, g_dtype, offset):
     assert (opt.m.cpu()[~live] == 0).all() and (opt.v.cpu()[~live] == 0).all()
 
 
+@pytest.mark.parametrize("size", [1e18, 1e-12])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_of_any_size(lib, bits, size):
+    """Gradients of about 1e15, whose 8-bit scales are above 2^38, and of 1e-15."""
+    sizes = [100, 4500]
+    params, grads = _make(sizes, torch.float32, torch.float32, seed=4)
+    grads = [g * size for g in grads]
+    opt = AdamW(params, lr=1e-3, state_bits=bits, seed=5)
+    for t in (1, 2):
+        before = _state(opt, sizes, t)
+        opt.step(grads)
+        _check_step(opt, grads, sizes, before)
+
+
+def test_no_gradient_and_the_smallest_eps(lib):
+    """0 / eps is 0 for every eps above 0."""
+    for bits in (32, 8):
+        for eps in (1e-8, 1e-37, 1e-40, 1e-300):
+            p = torch.ones(70, device="cuda")
+            opt = AdamW([p], eps=eps, weight_decay=0.0, state_bits=bits)
+            opt.step([torch.zeros_like(p)])
+            assert (p == 1.0).all()
+
+
 def test_more_tensors_than_one_launch_takes(lib):
     sizes = [1 + (i * 37) % 300 for i in range(300)]
     for bits in (32, 8):
@@ -263,7 +287,8 @@ def test_refusals(lib):
     p, g = torch.zeros(10, device="cuda"), torch.zeros(10, device="cuda")
     for bad in (dict(params=[]), dict(params=[p.half()]), dict(params=[p.cpu()]), dict(params=[torch.zeros(4, 4, device="cuda").t()[1:]]),
                 dict(params=[p], state_bits=16), dict(params=[p], weight_decay=[0.1, 0.2]), dict(params=[p], copies=[g]),
-                dict(params=[p.bfloat16()], copies=[p.bfloat16()]), dict(params=[p], max_norm=0.0)):
+                dict(params=[p.bfloat16()], copies=[p.bfloat16()]), dict(params=[p], max_norm=0.0),
+                dict(params=[p, g, p]), dict(params=[p[:6], p[5:]]), dict(params=[p], copies=[p.view(torch.bfloat16)[:10]])):
         with pytest.raises(ValueError):
             AdamW(**bad)
     opt = AdamW([p])
@@ -274,3 +299,4 @@ def test_refusals(lib):
         AdamW([p], betas=(1.0, 0.9)).step([g])
     with pytest.raises(_lib.MoEError):
         AdamW([p], lr=float("nan")).step([g])
+    AdamW([p[:5], p[5:], p[5:5]]).step([g[:5], g[5:], g[5:5]])
