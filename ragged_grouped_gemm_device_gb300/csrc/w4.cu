@@ -301,7 +301,6 @@ struct W4Args {
   const float* weights;    // down: nullable
   int slots, top_k, xdiv;  // slot s reads row s / xdiv of x
   int E, N, K;
-  int segment;             // chunks of x in shared memory at a time
   Packed w;
   void* out;
   long long ldo;
@@ -309,217 +308,150 @@ struct W4Args {
   bool early;              // ids are from before the kernel ahead, which only made x
 };
 
-constexpr int SEGMENT = 16;  // chunks of x in shared memory at most
+constexpr int SEGMENT = 16;  // chunks of x in shared memory at a time
 
-// Slots of one expert times its weights: WK warps of a block own 16 rows of the matrix (of both halves, gate and up, with
-// SWIGLU) and take the slots of its expert 8 NT at a time. They share the chunks of K and add up their sums in shared
-// memory, in warp order. A group is a slot that names its expert first (slots <= E), or an expert, with one more group for
-// dropped slots; of a single token every slot is one.
-// U: pieces (pairs of pieces) of a warp on their way at once.
-template <int PER, int NT, int WARPS, int WK, int U, bool SWIGLU, bool VEC>
-__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : U == 4 ? 3 : NT == 1 ? 5 : 4) w4_group_kernel(const W4Args a) {
-  constexpr int TILES = SWIGLU ? 2 : 1, COLS = 8 * NT, WT = WARPS / WK;
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint4* xs = reinterpret_cast<uint4*>(smem);                                    // [chunks of a segment * 4][COLS][4]
-  float* xsum = reinterpret_cast<float*>(smem + a.segment * 4 * COLS * 64);        // [chunks of a segment * 4][COLS]: minus the sums
-  float* sums = xsum + a.segment * 4 * COLS;                                       // [WARPS][TILES][NT][4][32]
-  int* list = reinterpret_cast<int*>(sums + WARPS * TILES * NT * 128);             // slots of this group
-  __shared__ int counts[WARPS];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = blockIdx.y;
-  const int wk = warp % WK, tile = blockIdx.x * WT + warp / WK;  // this warp's share of K and its rows
-  const bool live = tile < a.w.tiles;
+__device__ __forceinline__ void put_out(const W4Args& a, int slot, int row, float v) {
+  if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v);
+  else static_cast<float*>(a.out)[slot * a.ldo + row] = v;
+}
+// SwiGLU's output. Rows past h up to the pitch: their scales are 0.
+__device__ __forceinline__ void put_swiglu(const W4Args& a, int slot, int row, float gate, float up) {
+  if (row < a.ldo) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up);
+}
+
+// ------------------------------------------------------------------ one token
+// Block (tile, slot) owns 16 rows of the slot's matrix (with SWIGLU of both halves, gate and up). Its warps share the chunks of K, U
+// pieces (pairs of pieces) each on their way at once, and add up their sums in shared memory, in warp order.
+template <int PER, int WARPS, int U, bool SWIGLU, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel(const W4Args a) {
+  constexpr int TILES = SWIGLU ? 2 : 1;
+  __shared__ uint4 xs[SEGMENT * 4][4];
+  __shared__ float xsum[SEGMENT * 4];  // minus the sums
+  __shared__ float sums[WARPS][TILES][16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = blockIdx.x, slot = blockIdx.y;
   if (!a.early) grid_wait();
-  const int32_t* ids = after_wait(a.ids);
-  const bool by_slot = a.slots <= a.E, single = a.ids == nullptr ? false : a.slots == a.top_k;
-  int e = a.ids == nullptr ? 0 : by_slot || single ? ids[group] : group;
-  const bool dropped = e < 0 || e >= a.E;
-  int n = 1;
-  if (single || (dropped && by_slot)) {
-    if (threadIdx.x == 0) list[0] = group;
-  } else if (a.ids == nullptr) {
-    n = a.slots;
-    for (int i = threadIdx.x; i < n; i += WARPS * 32) list[i] = i;
-  } else {
-    // the slots of expert e (of none of the experts: the last group) in order
-    const int seg = (a.slots + WARPS * 32 - 1) / (WARPS * 32) * 32;  // slots of a warp
-    const int i0 = warp * seg;
-    const auto mine = [&](int i) {
-      const int v = i < a.slots ? ids[i] : -1;
-      return i < a.slots && (dropped ? v < 0 || v >= a.E : v == e);
-    };
-    int count = 0;
-    for (int i = i0; i < i0 + seg; i += 32) count += __popc(__ballot_sync(0xffffffffu, mine(i + lane)));
-    if (lane == 0) counts[warp] = count;
-    __syncthreads();
-    int at = 0;
-    n = 0;
+  const int e = a.ids == nullptr ? 0 : after_wait(a.ids)[slot];
+  if (e < 0 || e >= a.E) {
+    if (a.early) grid_wait();
+    const int row = tile * 16 + threadIdx.x;
+    if (!SWIGLU && threadIdx.x < 16 && row < a.N) put_out(a, slot, row, 0.f);
+    return;
+  }
+  const bf16* x = after_wait(a.x) + (slot / a.xdiv) * a.ldx;
+  const Unpack unpack;
+  float tot[TILES][1][4];
+  const uint8_t* piece0[TILES];
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      at += w < warp ? counts[w] : 0;
-      n += counts[w];
+  for (int h = 0; h < TILES; ++h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) tot[h][0][i] = 0.f;
+    piece0[h] = a.w.base + (static_cast<size_t>(e * TILES + h) * a.w.tiles + tile) * a.w.chunks * Piece<PER>::bytes;
+  }
+  for (int seg0 = 0; seg0 < a.w.chunks; seg0 += SEGMENT) {
+    const int chunks = min(SEGMENT, a.w.chunks - seg0);
+    Piece<PER> p[U][TILES];
+    const auto load = [&](int c) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c + u * WARPS < chunks) {
+#pragma unroll
+          for (int h = 0; h < TILES; ++h) p[u][h].load(piece0[h] + static_cast<size_t>(seg0 + c + u * WARPS) * Piece<PER>::bytes, lane);
+        }
+    };
+    load(warp);  // on their way while x comes
+    if (a.early && seg0 == 0) grid_wait();
+    __syncthreads();
+    // Each thread eight elements, four threads the 32 of a sum; chunks * 16 is a multiple of 16, so whole groups of four
+    for (int i = threadIdx.x; i < (chunks * 16 + 31 & ~31); i += WARPS * 32) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (i < chunks * 16) {
+        v = load_x<VEC>(x, (seg0 * 16 + i) * 8, a.K);
+        xs[i >> 2][i & 3] = v;
+      }
+      float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (i < chunks * 16 && (i & 3) == 0) xsum[i >> 2] = -sum;
     }
-    for (int i = i0; i < i0 + seg; i += 32) {
-      const bool m = mine(i + lane);
-      const unsigned who = __ballot_sync(0xffffffffu, m);
-      if (m) list[at + __popc(who & ((1u << lane) - 1))] = i + lane;
-      at += __popc(who);
+    __syncthreads();
+    for (int c = warp; c < chunks; c += WARPS * U) {
+      if (c != warp) load(c);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (c + u * WARPS >= chunks) break;
+        const int s0 = (c + u * WARPS) * 4;
+        // column 0 of eight; the others' sums are not read
+        multiply<PER, 1, TILES>(p[u], tot, 1.0f, unpack, [&](int q, int) { return lane < 4 ? xs[s0 + q][lane] : make_uint4(0, 0, 0, 0); },
+                                [&](int q, int) { return make_float2(xsum[s0 + q], 0.f); });
+      }
+    }
+  }
+  // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
+  if ((lane & 3) == 0) {
+#pragma unroll
+    for (int h = 0; h < TILES; ++h) {
+      sums[warp][h][lane >> 2] = tot[h][0][0];
+      sums[warp][h][8 + (lane >> 2)] = tot[h][0][2];
     }
   }
   __syncthreads();
-  if (n == 0) return;
-  if (by_slot && !single && !dropped && a.ids != nullptr && list[0] != group) return;  // an earlier slot has this expert
-  if (dropped) {
-    if constexpr (!SWIGLU) {
-      for (int i = threadIdx.x; i < n * 16 * WT; i += WARPS * 32) {
-        const int row = blockIdx.x * WT * 16 + i % (16 * WT), slot = list[i / (16 * WT)];
-        if (row >= a.N) continue;
-        if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(0.f);
-        else static_cast<float*>(a.out)[slot * a.ldo + row] = 0.f;
-      }
-    }
-    return;
+  if (threadIdx.x >= 16) return;
+  float v[TILES];
+#pragma unroll
+  for (int h = 0; h < TILES; ++h) {
+    v[h] = 0.f;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) v[h] += sums[w][h][threadIdx.x];
   }
-  const bf16* x = after_wait(a.x);
-  const Unpack unpack;
-  for (int r0 = 0; r0 < n; r0 += COLS) {
-    const int rows = min(COLS, n - r0);
-    float tot[TILES][NT][4];
-#pragma unroll
-    for (int h = 0; h < TILES; ++h)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tot[h][t][i] = 0.f;
-    size_t piece0[TILES];
-#pragma unroll
-    for (int h = 0; h < TILES; ++h) piece0[h] = (static_cast<size_t>(e * TILES + h) * a.w.tiles + tile) * a.w.chunks;
-    for (int seg0 = 0; seg0 < a.w.chunks; seg0 += a.segment) {
-      const int chunks = min(a.segment, a.w.chunks - seg0);
-      Piece<PER> p[U][TILES];
-      const auto load = [&](int c) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (live && c + u * WK < chunks) {
-#pragma unroll
-            for (int h = 0; h < TILES; ++h) p[u][h].load(a.w.base + (piece0[h] + seg0 + c + u * WK) * Piece<PER>::bytes, lane);
-          }
-      };
-      load(wk);  // on their way while x comes
-      if (a.early && seg0 == 0 && r0 == 0) grid_wait();
-      __syncthreads();
-      // Each thread eight elements, four threads the 32 of a sum; whole warps, because of the shuffles
-      const int units = rows * chunks * 16;
-      for (int i = threadIdx.x; i < (units + 31 & ~31); i += WARPS * 32) {
-        const int col = i / (chunks * 16), k8 = i % (chunks * 16);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (i < units) {
-          v = load_x<VEC>(x + (list[r0 + col] / a.xdiv) * a.ldx, (seg0 * 16 + k8) * 8, a.K);
-          xs[((k8 >> 2) * COLS + col) * 4 + (k8 & 3)] = v;
-        }
-        float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (i < units && (k8 & 3) == 0) xsum[(k8 >> 2) * COLS + col] = -sum;
-      }
-      __syncthreads();
-      for (int c = wk; live && c < chunks; c += WK * U) {
-        if (c != wk) load(c);
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (c + u * WK >= chunks) break;
-          const int s0 = (c + u * WK) * 4;
-          const auto b = [&](int q, int t) {
-            const int col = t * 8 + (lane >> 2);
-            return col < rows ? xs[((s0 + q) * COLS + col) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
-          };
-          const auto nx = [&](int q, int t) {  // columns past the last row: what lies there goes into sums that nobody reads
-            return *reinterpret_cast<const float2*>(xsum + (s0 + q) * COLS + t * 8 + 2 * (lane & 3));
-          };
-          multiply<PER, NT, TILES>(p[u], tot, 1.0f, unpack, b, nx);
-        }
-      }
-    }
-    // sums of the warps: [warp][half][column tile][register][lane]
-#pragma unroll
-    for (int h = 0; h < TILES; ++h)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sums[(((warp * TILES + h) * NT + t) * 4 + i) * 32 + lane] = tot[h][t][i];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * WT * rows; i += WARPS * 32) {
-      const int w0 = i / 16 % WT, r = i & 15, col = i / (16 * WT);  // consecutive threads: consecutive rows of the output
-      // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + (c % 8) / 2
-      const int at = (((col >> 3) * 4) + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
-      float v[TILES];
-#pragma unroll
-      for (int h = 0; h < TILES; ++h) {
-        v[h] = 0.f;
-#pragma unroll
-        for (int w = 0; w < WK; ++w) v[h] += sums[((w0 * WK + w) * TILES + h) * NT * 128 + at];
-      }
-      const int row = (blockIdx.x * WT + w0) * 16 + r, slot = list[r0 + col];
-      if constexpr (SWIGLU) {
-        // rows past h up to the pitch: their scales are 0
-        if (row < a.ldo) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v[0] / (1.0f + expf(-v[0])) * v[1]);
-      } else if (row < a.N) {
-        if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v[0]);
-        else static_cast<float*>(a.out)[slot * a.ldo + row] = v[0];
-      }
-    }
-    __syncthreads();
-  }
+  const int row = tile * 16 + threadIdx.x;
+  if constexpr (SWIGLU) put_swiglu(a, slot, row, v[0], v[1]);
+  else if (row < a.N) put_out(a, slot, row, v[0]);
 }
 
-// ------------------------------------------------------------------ few slots of an expert
-// Groups of up to eight slots of one expert, each with all tiles of its weights, are one list of tasks (group, tile set) that the
+// ------------------------------------------------------------------ several tokens
+// Groups of up to 8 NT slots of one expert, each with all tiles of its weights, are one list of tasks (group, tile set) that the
 // blocks share evenly, each a run of it: an expert's weights are read once, and x of a group is fetched once or twice. A
 // warp's pieces go through a ring of its own in shared memory, filled by asynchronous copies that run ahead over tasks and
 // groups, so that the copies in flight do not depend on how far the sums are, and no warp waits for another's.
-constexpr int STREAM_WARPS = 8;
-constexpr int STREAM_THREADS = STREAM_WARPS * 32;
-
 struct StreamShape {
-  int wk;       // warps that share K; STREAM_WARPS / wk tiles (with SWIGLU pairs of tiles) are a task
-  int log_wts;  // log2 of STREAM_WARPS / wk
+  int wk;       // warps that share K; WARPS / wk tiles (with SWIGLU pairs of tiles) are a task
   int sets;     // tasks of a group
   int xchunks;  // chunks of x in shared memory
 };
 
-template <int PER, bool SWIGLU>
+template <int PER, int NT, int WARPS, bool SWIGLU>
 struct StreamSmem {
   static constexpr int TILES = SWIGLU ? 2 : 1;
   static constexpr int step = TILES * piece_bytes(PER);  // bytes of one ring slot
-  static constexpr int depth = SWIGLU ? 3 : 4;             // slots of a warp's ring
-  static constexpr int sum_floats = STREAM_WARPS * TILES * 128;
+  static constexpr int depth = WARPS == 16 ? 2 : SWIGLU ? 3 : 4;  // slots of a warp's ring
+  static constexpr int sum_floats = WARPS * TILES * NT * 128, buffers = WARPS == 16 ? 1 : 2;
   int ring, x, xsum, sums, list, groups, count, total;  // byte offsets
   __host__ __device__ StreamSmem(const W4Args& a, const StreamShape& sh) {
     ring = 0;
-    x = ring + STREAM_WARPS * depth * step;
-    xsum = x + sh.xchunks * 4 * 8 * 64;
-    sums = xsum + sh.xchunks * 4 * 8 * 4;
-    list = sums + 2 * sum_floats * 4;
+    x = ring + WARPS * depth * step;
+    xsum = x + sh.xchunks * 4 * 8 * NT * 64;
+    sums = xsum + sh.xchunks * 4 * 8 * NT * 4;
+    list = sums + buffers * sum_floats * 4;
     groups = list + (a.slots * 4 + 15) / 16 * 16;
     count = groups + most_groups(a) * 8;
-    total = count + (a.ids == nullptr || a.slots == a.top_k ? 0 : (a.E + 1) * 4);
+    total = count + (a.ids == nullptr ? 0 : (a.E + 1) * 4);
   }
-  // groups at most: every slot alone, or a full group of every eight and one that is not full of every expert
+  // groups at most: every slot alone, or as many full groups as the slots make and one that is not full of every expert
   static __host__ __device__ int most_groups(const W4Args& a) {
-    if (a.ids == nullptr) return (a.slots + 7) / 8;
-    if (a.slots == a.top_k) return a.slots;
-    const int m = a.E + a.slots / 8;
+    if (a.ids == nullptr) return (a.slots + 8 * NT - 1) / (8 * NT);
+    const int m = a.E + a.slots / (8 * NT);
     return m < a.slots ? m : a.slots;
   }
 };
 
-template <int PER, bool SWIGLU, bool VEC>
-__global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Args a, const StreamShape sh) {
-  using Smem = StreamSmem<PER, SWIGLU>;
-  constexpr int TILES = Smem::TILES, BYTES = Piece<PER>::bytes;
+template <int PER, int NT, int WARPS, bool SWIGLU, bool VEC>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_kernel(const W4Args a, const StreamShape sh) {
+  using Smem = StreamSmem<PER, NT, WARPS, SWIGLU>;
+  constexpr int TILES = Smem::TILES, BYTES = Piece<PER>::bytes, COLS = 8 * NT, STREAM_THREADS = WARPS * 32;
   extern __shared__ __align__(16) uint8_t smem[];
   const Smem at(a, sh);
-  uint4* xs = reinterpret_cast<uint4*>(smem + at.x);          // [chunks * 4][8][4]
-  float* xsum = reinterpret_cast<float*>(smem + at.xsum);     // [chunks * 4][8]: minus the sums
+  uint4* xs = reinterpret_cast<uint4*>(smem + at.x);          // [chunks * 4][COLS][4]
+  float* xsum = reinterpret_cast<float*>(smem + at.xsum);     // [chunks * 4][COLS]: minus the sums
   int* list = reinterpret_cast<int*>(smem + at.list);         // slots, expert by expert
   int2* groups = reinterpret_cast<int2*>(smem + at.groups);   // expert, first slot in list | slots << 16
   int* count = reinterpret_cast<int*>(smem + at.count);       // slots of each expert, of none; then where the next one goes
@@ -527,13 +459,12 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!a.early) grid_wait();
   const int32_t* ids = after_wait(a.ids);
-  if (a.ids == nullptr || a.slots == a.top_k) {
-    const int per = a.ids == nullptr ? 8 : 1;
+  if (a.ids == nullptr) {
     for (int i = threadIdx.x; i < a.slots; i += STREAM_THREADS) {
       list[i] = i;
-      if (i % per == 0) groups[i / per] = make_int2(a.ids == nullptr ? 0 : ids[i], i | min(per, a.slots - i) << 16);
+      if (i % COLS == 0) groups[i / COLS] = make_int2(0, i | min(COLS, a.slots - i) << 16);
     }
-    if (threadIdx.x == 0) n_groups = (a.slots + per - 1) / per;
+    if (threadIdx.x == 0) n_groups = (a.slots + COLS - 1) / COLS;
   } else {
     const auto of = [&](int i) {
       const int e = ids[i];
@@ -548,7 +479,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
       for (int e0 = 0; e0 <= a.E; e0 += 32) {
         const int e = e0 + lane;
         const int c = e <= a.E ? count[e] : 0;
-        const int g = e < a.E ? (c + 7) >> 3 : 0;
+        const int g = e < a.E ? (c + COLS - 1) / COLS : 0;
         int sum = c | g << 16;  // both running sums in one word
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -557,7 +488,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
         }
         const int first = slots + (sum & 0xFFFF) - c, to = made + (sum >> 16) - g;
         if (e <= a.E) count[e] = first;
-        for (int i = 0; i < g; ++i) groups[to + i] = make_int2(e, (first + 8 * i) | min(8, c - 8 * i) << 16);
+        for (int i = 0; i < g; ++i) groups[to + i] = make_int2(e, (first + COLS * i) | min(COLS, c - COLS * i) << 16);
         sum = __shfl_sync(0xffffffffu, sum, 31);
         slots += sum & 0xFFFF;
         made += sum >> 16;
@@ -578,7 +509,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
     }
   }
   __syncthreads();
-  const int wk = warp & (sh.wk - 1), wts = 1 << sh.log_wts, wt = warp * wts / STREAM_WARPS;
+  const int wk = warp & (sh.wk - 1), wts = WARPS / sh.wk, wt = warp / sh.wk;
   const long long tasks = static_cast<long long>(n_groups) * sh.sets;
   const int t0 = static_cast<int>(tasks * blockIdx.x / gridDim.x), t1 = static_cast<int>(tasks * (blockIdx.x + 1) / gridDim.x);
   constexpr int depth = Smem::depth;
@@ -597,7 +528,7 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
   const auto fill = [&](uint32_t to) {
     while (f_left == 0 && f_tasks > 0) {
       const int e = groups[f_group].x, tile = f_set * wts + wt;
-      if (e >= 0 && e < a.E && tile < a.w.tiles) {
+      if (tile < a.w.tiles) {
         f_left = mine;
         f_src = a.w.base + ((static_cast<size_t>(e * TILES) * a.w.tiles + tile) * chunks + wk) * BYTES + lane16;
       }
@@ -626,18 +557,12 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
   if constexpr (SWIGLU) grid_release();  // the down product reads the ids and its first weights meanwhile
   if (a.early) grid_wait();
   const bf16* x = after_wait(a.x);
-  if constexpr (!SWIGLU) {  // rows of dropped slots
-    const auto zero_row = [&](int slot) {
-      for (int c = threadIdx.x; c < a.N; c += STREAM_THREADS) {
-        if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + c] = __float2bfloat16_rn(0.f);
-        else static_cast<float*>(a.out)[slot * a.ldo + c] = 0.f;
-      }
-    };
-    if (a.ids != nullptr)
-      for (int i = blockIdx.x; i < a.slots; i += gridDim.x) {
-        const int e = ids[i];
-        if (e < 0 || e >= a.E) zero_row(i);
-      }
+  if (!SWIGLU && a.ids != nullptr) {  // rows of dropped slots
+    for (int i = blockIdx.x; i < a.slots; i += gridDim.x) {
+      const int e = ids[i];
+      if (e >= 0 && e < a.E) continue;
+      for (int c = threadIdx.x; c < a.N; c += STREAM_THREADS) put_out(a, i, c, 0.f);
+    }
   }
   const Unpack unpack;
   uint32_t slot = 0;  // byte offset in this warp's ring
@@ -649,28 +574,29 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
       ++group;
     }
     const int2 info = groups[group];
-    if (info.x < 0 || info.x >= a.E) continue;  // a dropped slot of a single token
     const int first = info.y & 0xFFFF, rows = info.y >> 16;
     const bool live = set * wts + wt < a.w.tiles;
-    float tot[TILES][1][4];
+    float tot[TILES][NT][4];
 #pragma unroll
     for (int h = 0; h < TILES; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tot[h][0][i] = 0.f;
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tot[h][t][i] = 0.f;
     for (int seg0 = 0; seg0 < chunks; seg0 += sh.xchunks) {
       const int n = min(sh.xchunks, chunks - seg0);
       if (group != in_group || seg0 != in_seg) {
         __syncthreads();  // x there is no longer read
-        // Eight columns, zeros where the group has fewer rows. A thread takes eight elements, four threads the 32 of a sum.
-        for (int i = threadIdx.x; i < n * 128; i += STREAM_THREADS) {
+        // All columns, zeros where the group has fewer rows. A thread takes eight elements, four threads the 32 of a sum.
+        for (int i = threadIdx.x; i < n * 16 * COLS; i += STREAM_THREADS) {
           const int col = i / (n * 16), k8 = i - col * (n * 16);
           uint4 v = make_uint4(0, 0, 0, 0);
           if (col < rows) v = load_x<VEC>(x + (list[first + col] / a.xdiv) * a.ldx, (seg0 * 16 + k8) * 8, a.K);
-          xs[((k8 >> 2) * 8 + col) * 4 + (k8 & 3)] = v;
+          xs[((k8 >> 2) * COLS + col) * 4 + (k8 & 3)] = v;
           float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
-          sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // n * 128 is a multiple of 32: whole warps
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // the bound is a multiple of 32: whole warps
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          if ((k8 & 3) == 0) xsum[(k8 >> 2) * 8 + col] = -sum;
+          if ((k8 & 3) == 0) xsum[(k8 >> 2) * COLS + col] = -sum;
         }
         __syncthreads();
         in_group = group;
@@ -679,9 +605,9 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
       if (!live) continue;
       // chunks of this segment that are this warp's: those equal to wk modulo the warps that share K
       const int c0 = (wk - seg0) & (sh.wk - 1);
-      const uint4* xp = xs + c0 * 128 + lane;
-      const float* sp = xsum + c0 * 32 + 2 * (lane & 3);
-      for (int c = c0; c < n; c += sh.wk, xp += sh.wk * 128, sp += sh.wk * 32) {
+      const uint4* xp = xs + c0 * 16 * COLS + lane;
+      const float* sp = xsum + c0 * 4 * COLS + 2 * (lane & 3);
+      for (int c = c0; c < n; c += sh.wk, xp += sh.wk * 16 * COLS, sp += sh.wk * 4 * COLS) {
         copy_wait<depth - 1>();  // younger groups of copies may be on their way
         __syncwarp();
         Piece<PER> p[TILES];
@@ -690,39 +616,40 @@ __global__ void __launch_bounds__(STREAM_THREADS, 2) w4_stream_kernel(const W4Ar
         __syncwarp();  // every lane has its part: the slot is free
         fill(ring + slot);
         slot = slot == (depth - 1) * Smem::step ? 0 : slot + Smem::step;
-        multiply<PER, 1, TILES>(p, tot, 1.0f, unpack, [&](int q, int) { return xp[q * 32]; },
-                                [&](int q, int) { return *reinterpret_cast<const float2*>(sp + q * 8); });
+        multiply<PER, NT, TILES>(p, tot, 1.0f, unpack, [&](int q, int t) { return xp[(q * NT + t) * 32]; },
+                                 [&](int q, int t) { return *reinterpret_cast<const float2*>(sp + (q * NT + t) * 8); });
       }
     }
-    // the sums of the warps, in one of two buffers: [warp][half][register][lane]
+    // the sums of the warps: [warp][half][column tile][register][lane]
     float* sums = reinterpret_cast<float*>(smem + at.sums) + par * Smem::sum_floats;
-    par ^= 1;
+    par ^= Smem::buffers - 1;
 #pragma unroll
     for (int h = 0; h < TILES; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sums[((warp * TILES + h) * 4 + i) * 32 + lane] = tot[h][0][i];
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[(((warp * TILES + h) * NT + c) * 4 + i) * 32 + lane] = tot[h][c][i];
     // only the warps that share a tile's K wait for one another
-    if (sh.wk == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(sh.wk * 32) : "memory");
+    const auto meet = [&] {
+      if (sh.wk == 1) __syncwarp();
+      else asm volatile("bar.sync %0, %1;" ::"r"(1 + wt), "r"(sh.wk * 32) : "memory");
+    };
+    meet();
     for (int i = wk * 32 + lane; i < 16 * rows; i += sh.wk * 32) {
       const int r = i & 15, col = i >> 4;  // consecutive threads: consecutive rows of the output
-      // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + c / 2
-      const int from = ((r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + (col >> 1);
+      // row r, column c of a tile lie in register (r / 8) 2 + c % 2 of lane (r % 8) 4 + (c % 8) / 2
+      const int from = ((col >> 3) * 4 + (r >> 3) * 2 + (col & 1)) * 32 + (r & 7) * 4 + ((col & 7) >> 1);
       float v[TILES];
 #pragma unroll
       for (int h = 0; h < TILES; ++h) {
         v[h] = 0.f;
-        for (int w = 0; w < sh.wk; ++w) v[h] += sums[((wt * sh.wk + w) * TILES + h) * 128 + from];
+        for (int w = 0; w < sh.wk; ++w) v[h] += sums[((wt * sh.wk + w) * TILES + h) * NT * 128 + from];
       }
       const int row = (set * wts + wt) * 16 + r, s = list[first + col];
-      if constexpr (SWIGLU) {
-        // rows past h up to the pitch: their scales are 0
-        if (row < a.ldo) static_cast<bf16*>(a.out)[s * a.ldo + row] = __float2bfloat16_rn(v[0] / (1.0f + expf(-v[0])) * v[1]);
-      } else if (row < a.N) {
-        if (a.y_bf16) static_cast<bf16*>(a.out)[s * a.ldo + row] = __float2bfloat16_rn(v[0]);
-        else static_cast<float*>(a.out)[s * a.ldo + row] = v[0];
-      }
+      if constexpr (SWIGLU) put_swiglu(a, s, row, v[0], v[1]);
+      else if (row < a.N) put_out(a, s, row, v[0]);
     }
+    if (Smem::buffers == 1) meet();
   }
   copy_wait<0>();
 }
@@ -826,65 +753,47 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const float* y, long lo
   }
 }
 
-template <int PER, int NT, int WARPS, int WK, int U, bool SWIGLU>
-cudaError_t launch_group_as(const W4Args& a, int groups, cudaStream_t s) {
-  const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
-  const int x_bytes = 4 * 8 * NT * 68, sum_bytes = WARPS * (SWIGLU ? 2 : 1) * NT * 512;
-  const auto kernel = vec ? w4_group_kernel<PER, NT, WARPS, WK, U, SWIGLU, true> : w4_group_kernel<PER, NT, WARPS, WK, U, SWIGLU, false>;
-  const int smem = a.segment * x_bytes + sum_bytes + std::max(1, a.slots) * 4;
-  if (smem > 40 * 1024) {  // beside the static shared memory
-    const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), SEGMENT * x_bytes + sum_bytes + MAX_SLOTS * 4);
-    if (err != cudaSuccess) return err;
-  }
-  return launch_dependent(kernel, dim3((a.w.tiles * WK + WARPS - 1) / WARPS, groups), WARPS * 32, smem, s, a);
-}
-template <int PER, int NT, bool SWIGLU>
-cudaError_t launch_group_split(const W4Args& a, int groups, cudaStream_t s) {
-  // The warps of a block share K where that gives no more than eight blocks for each SM: few blocks leave SMs idle, many have each its
-  // share of reading ids and x.
-  const bool few = static_cast<long long>(a.w.tiles) * groups <= 8LL * device_sm_count();
-  return few ? launch_group_as<PER, NT, 4, 4, 2, SWIGLU>(a, groups, s) : launch_group_as<PER, NT, 4, 1, 2, SWIGLU>(a, groups, s);
-}
+bool vec_x(const W4Args& a) { return a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x); }
 
-template <int PER, bool SWIGLU, bool VEC>
-cudaError_t launch_stream_as(const W4Args& a, cudaStream_t s) {
-  using Smem = StreamSmem<PER, SWIGLU>;
+template <int PER, int NT, bool SWIGLU>
+cudaError_t launch_stream(const W4Args& a, cudaStream_t s) {
+  constexpr int WARPS = NT == 1 ? 8 : 16;
+  using Smem = StreamSmem<PER, NT, WARPS, SWIGLU>;
   StreamShape sh;
   // Long rows are shared, three or four chunks a warp: with fewer the sums at the end of a task cost as much as its products, with more there are
   // too few tasks to share evenly. Short rows go to one warp each.
-  sh.log_wts = a.w.chunks >= 24 ? 0 : a.w.chunks >= 12 ? 1 : 3;
-  const int wts = 1 << sh.log_wts;
-  sh.wk = STREAM_WARPS / wts;
+  sh.wk = a.w.chunks >= 24 ? 8 : a.w.chunks >= 12 ? 4 : 1;
+  const int wts = WARPS / sh.wk;
   sh.sets = (a.w.tiles + wts - 1) / wts;
-  sh.xchunks = std::min(a.w.chunks, SWIGLU ? 16 : 32);
+  sh.xchunks = std::min(a.w.chunks, SWIGLU || NT == 2 ? 16 : 32);
   const int smem = Smem(a, sh).total;
-  const auto kernel = w4_stream_kernel<PER, SWIGLU, VEC>;
-  const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), 200 * 1024);
+  const auto kernel = vec_x(a) ? w4_stream_kernel<PER, NT, WARPS, SWIGLU, true> : w4_stream_kernel<PER, NT, WARPS, SWIGLU, false>;
+  const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), 220 * 1024);
   if (err != cudaSuccess) return err;
   const long long most = static_cast<long long>(Smem::most_groups(a)) * sh.sets;
-  const int blocks = static_cast<int>(std::min<long long>(most, (smem <= 112 * 1024 ? 2 : 1) * static_cast<long long>(device_sm_count())));
-  return launch_dependent(kernel, blocks, STREAM_THREADS, smem, s, a, sh);
+  const int blocks = static_cast<int>(std::min<long long>(most, (NT == 1 && smem <= 112 * 1024 ? 2 : 1) * static_cast<long long>(device_sm_count())));
+  return launch_dependent(kernel, blocks, WARPS * 32, smem, s, a, sh);
 }
 
 template <int PER, bool SWIGLU>
-cudaError_t launch_group(W4Args a, cudaStream_t s) {
-  a.segment = std::min(a.w.chunks, SEGMENT);
-  // tokens of an expert, on average: what one pass over its weights should take
-  const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
-  // One slot (of an expert) at a time takes a block for each tile, which starts sooner than the list of tasks is made.
-  if (each <= 8 && (a.ids == nullptr ? a.slots > 1 : a.slots > a.top_k)) {
-    const bool vec = a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x);
-    return vec ? launch_stream_as<PER, SWIGLU, true>(a, s) : launch_stream_as<PER, SWIGLU, false>(a, s);
+cudaError_t launch_product(const W4Args& a, cudaStream_t s) {
+  // A single token: a block for each tile, which starts sooner than a list of tasks is made, with as many warps and loads that all
+  // weights of a tile are on their way at once (up to K = 4096 with eight warps, 2048 of gate and up with four, of which three blocks
+  // fit on an SM: 4096 x 4096 takes 4.5 us, 5.6 with two loads of four warps each).
+  if (a.slots == (a.ids == nullptr ? 1 : a.top_k)) {
+    constexpr int WARPS = SWIGLU ? 4 : 8;
+    const auto kernel = vec_x(a) ? w4_slot_kernel<PER, WARPS, 4, SWIGLU, true> : w4_slot_kernel<PER, WARPS, 4, SWIGLU, false>;
+    return launch_dependent(kernel, dim3(a.w.tiles, a.slots), WARPS * 32, 0, s, a);
   }
-  const int groups = a.ids == nullptr ? 1 : a.slots <= a.E ? a.slots : a.slots == a.top_k ? a.slots : a.E + (SWIGLU ? 0 : 1);
-  // A single token: as many warps and loads that all weights of a tile are on their way at once (up to K = 4096 with eight warps, 2048
-  // of gate and up with four, of which three blocks fit on an SM: 4096 x 4096 takes 4.5 us, 5.6 with two loads of four warps each).
-  if (a.slots == (a.ids == nullptr ? 1 : a.top_k)) return launch_group_as<PER, 1, SWIGLU ? 4 : 8, SWIGLU ? 4 : 8, 4, SWIGLU>(a, groups, s);
-  return each <= 8 ? launch_group_split<PER, 1, SWIGLU>(a, groups, s) : launch_group_split<PER, 2, SWIGLU>(a, groups, s);
+  // Tokens of an expert, on average. With more than eight of them groups of 16 slots unpack its weights half as often, in one block of 16
+  // warps, whose shared memory x fills (128 tokens, 8 of 64 experts of 2048 x 768: 133 us, 155 in groups of eight; with eight tokens
+  // an expert both take 99 to 101, with four the larger groups 86 instead of 76).
+  const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
+  return each <= 8 ? launch_stream<PER, 1, SWIGLU>(a, s) : launch_stream<PER, 2, SWIGLU>(a, s);
 }
 template <bool SWIGLU>
-cudaError_t launch_group(const W4Args& a, cudaStream_t s) {
-  return a.w.per == 4 ? launch_group<4, SWIGLU>(a, s) : a.w.per == 2 ? launch_group<2, SWIGLU>(a, s) : launch_group<1, SWIGLU>(a, s);
+cudaError_t launch_product(const W4Args& a, cudaStream_t s) {
+  return a.w.per == 4 ? launch_product<4, SWIGLU>(a, s) : a.w.per == 2 ? launch_product<2, SWIGLU>(a, s) : launch_product<1, SWIGLU>(a, s);
 }
 
 cudaError_t launch_down_token(const W4Args& a, int T, cudaStream_t s) {
@@ -980,7 +889,7 @@ moe_status_t moe_w4_matvec(const moe_bf16* x, long long ldx, const int32_t* ids,
   a.out = y;
   a.ldo = ldy;
   a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
-  const cudaError_t err = launch_group<false>(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t err = launch_product<false>(a, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
@@ -1016,7 +925,7 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
   a.w = packed_at(w_ug, h, d, group);
   a.out = act;
   a.ldo = pitch;
-  cudaError_t err = launch_group<true>(a, s);
+  cudaError_t err = launch_product<true>(a, s);
   if (err != cudaSuccess) return cuda_fail(err);
   W4Args b = a;
   b.x = act;
@@ -1035,7 +944,7 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
     float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(static_cast<size_t>(slots) * pitch * 2));
     b.out = y;
     b.ldo = d;
-    err = launch_group<false>(b, s);
+    err = launch_product<false>(b, s);
     if (err == cudaSuccess)
       err = launch_dependent(w4_combine_kernel, dim3(std::min((d + 127) / 128, 64), T), 128, 0, s, static_cast<const float*>(y),
                              static_cast<long long>(d), ids, weights, top_k, E, d, reinterpret_cast<bf16*>(out), ldo);
