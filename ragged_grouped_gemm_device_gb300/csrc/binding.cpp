@@ -21,10 +21,14 @@
 #define FUNCTIONS(X)                                                                                         \
   X(moe_layer_norm_fwd) X(moe_layer_norm_bwd) X(moe_gate_fwd) X(moe_gate_bwd) X(moe_mx4_quantize_rows)        \
   X(moe_mx4_dequantize_rows) X(moe_permute_mxfp4) X(moe_grouped_swiglu_fwd_mxfp4) X(moe_unpermute_combine)    \
-  X(moe_route_offsets) X(moe_residual_norm_fwd) X(moe_residual_norm_bwd) X(moe_grad_norm) X(moe_adamw_step)        \
-  X(moe_w4_matvec) X(moe_w4_swiglu_decode) X(moe_workspace_bytes)
+  X(moe_route_offsets) X(moe_workspace_bytes)
+// may be left out of a table: the calls then raise
+#define STEP_FUNCTIONS(X)                                                                                    \
+  X(moe_residual_norm_fwd) X(moe_residual_norm_bwd) X(moe_grad_norm) X(moe_adamw_step) X(moe_w4_matvec)      \
+  X(moe_w4_swiglu_decode)
 #define DECLARE(f) static __typeof__(&f) p_##f;
 FUNCTIONS(DECLARE)
+STEP_FUNCTIONS(DECLARE)
 
 PyObject* g_raise;
 
@@ -237,6 +241,8 @@ int weight_type(PyObject* const* w, int n, int d, int* v) {
   PyObject* a[N];                                                                         \
   (void)self;                                                                             \
   if (collect(fn, names, N, required, args, nargs, kwnames, a) < 0) return nullptr
+#define BOUND(f) \
+  if (p_##f == nullptr) return PyErr_Format(PyExc_RuntimeError, "%s is not bound", #f)
 
 // ------------------------------------------------------------------ the calls
 PyObject* layer_norm_fwd(ARGS) {
@@ -449,6 +455,7 @@ int as_float(PyObject* o, double* v) {
 PyObject* residual_norm_fwd(ARGS) {
   COLLECT("moe_residual_norm_fwd", 16, "x", "y", "post", "post_gamma", "post_beta", "gate", "pre", "pre_gamma", "pre_beta", "T", "d",
           "eps", "res_scale", "branch_scale", "r", "n", "stats", "stream");
+  BOUND(moe_residual_norm_fwd);
   int T, d, post, pre, xt, yt, wt;
   double eps, al, be;
   Any x, y, r, n, pg, pb, gate, qg, qb, stats;
@@ -474,6 +481,7 @@ PyObject* residual_norm_fwd(ARGS) {
 PyObject* residual_norm_bwd(ARGS) {
   COLLECT("moe_residual_norm_bwd", 17, "dn", "dr", "r", "y", "post", "post_gamma", "post_beta", "gate", "pre", "pre_gamma", "stats", "T", "d",
           "res_scale", "branch_scale", "dx", "dy", "d_post_gamma", "d_post_beta", "d_gate", "d_pre_gamma", "d_pre_beta", "ws", "stream");
+  BOUND(moe_residual_norm_bwd);
   int T, d, post, pre, xt, yt, wt;
   double al, be;
   Any dn, dr, r, y, dx, dy, pg, pb, gate, qg, stats, g[5], ws;
@@ -529,6 +537,7 @@ struct Table {
 
 PyObject* grad_norm(ARGS) {
   COLLECT("moe_grad_norm", 4, "tensors", "max_norm", "norm", "ws", "stream");
+  BOUND(moe_grad_norm);
   Table t;
   double most;
   Any norm, ws;
@@ -542,6 +551,7 @@ PyObject* grad_norm(ARGS) {
 
 PyObject* adamw_step(ARGS) {
   COLLECT("moe_adamw_step", 8, "tensors", "state_bits", "lr", "beta1", "beta2", "eps", "seed", "steps", "lr_scale", "grad_scale", "stream");
+  BOUND(moe_adamw_step);
   Table t;
   int bits;
   double lr, b1, b2, eps;
@@ -627,6 +637,7 @@ int bf16_rows(PyObject* o, const char* what) {
 
 PyObject* w4_matvec(ARGS) {
   COLLECT("moe_w4_matvec", 10, "x", "ids", "T", "top_k", "matrices", "N", "K", "group", "packed", "y", "stream");
+  BOUND(moe_w4_matvec);
   int T, k, m, out, in, group, yt;
   Any x, ids, w, y;
   long long ldx, ldy;
@@ -647,6 +658,7 @@ PyObject* w4_matvec(ARGS) {
 
 PyObject* w4_swiglu_decode(ARGS) {
   COLLECT("moe_w4_swiglu_decode", 13, "x", "ids", "weights", "T", "top_k", "E", "d", "h", "group", "w_ug", "w_down", "out", "ws", "stream");
+  BOUND(moe_w4_swiglu_decode);
   int T, k, E, d, h, group;
   Any x, ids, w, ug, down, out, ws;
   long long ldx, ldo;
@@ -673,17 +685,20 @@ PyObject* bind(PyObject* self, PyObject* args) {
   (void)self;
   PyObject *table, *raise;
   if (!PyArg_ParseTuple(args, "O!O", &PyDict_Type, &table, &raise)) return nullptr;
-#define ADDRESS(f)                                                        \
+#define ADDRESS(f, required)                                              \
   {                                                                       \
     PyObject* o = PyDict_GetItemString(table, #f);                        \
     void* p = o ? PyLong_AsVoidPtr(o) : nullptr;                             \
-    if (p == nullptr) {                                                      \
+    if (p == nullptr && (required || PyErr_Occurred())) {                    \
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_KeyError, #f);         \
       return nullptr;                                                        \
     }                                                                     \
     p_##f = (__typeof__(p_##f))p;                                         \
   }
-  FUNCTIONS(ADDRESS)
+#define REQUIRED(f) ADDRESS(f, true)
+#define OPTIONAL(f) ADDRESS(f, false)
+  FUNCTIONS(REQUIRED)
+  STEP_FUNCTIONS(OPTIONAL)
   Py_INCREF(raise);
   Py_XSETREF(g_raise, raise);
   Py_RETURN_NONE;

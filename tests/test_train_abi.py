@@ -116,3 +116,22 @@ def test_w4_refusals(lib):
         assert e(**bad) == INVALID, bad
     assert e(E=1025) == SHAPE and e(T=4097, top_k=1) == SHAPE and e(group=8) == SHAPE
     assert e(n=_lib.moe_workspace_bytes(_lib.OP_W4_DECODE, 2, 2, 3, 64, 32) - 1) == WS
+
+
+def test_binding_without_an_entry_point(tmp_path):
+    """An extension that is bound to a table without an entry point refuses its call instead of jumping nowhere."""
+    import importlib.util
+    import shutil
+
+    path = build.build_binding()
+    if path is None:
+        pytest.skip("no compiler or headers for the extension")
+    shutil.copy(path, tmp_path / "_binding.so")
+    spec = importlib.util.spec_from_file_location("_binding", tmp_path / "_binding.so")
+    binding = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(binding)
+    binding.bind({n: 1 for n in _lib.COMPILED + ("moe_workspace_bytes",)}, _lib._check)
+    with pytest.raises(RuntimeError, match="not bound"):
+        binding.moe_w4_matvec(*[None] * 10)
+    with pytest.raises(KeyError):
+        binding.bind({n: 1 for n in _lib.COMPILED}, _lib._check)
