@@ -3,7 +3,10 @@
 //   g' = c g;  m = b1 m + (1 - b1) g';  v = b2 v + (1 - b2) g'^2
 //   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 //
-// Bound by memory: p, m and v are read and written once, g is read once. The tensors are cut into pieces of
+// Bound by memory with fp32 states: p, m and v are read and written once, g is read once (28 bytes an element, 30 with a bf16 copy:
+// 201 million elements 900 us, 6.7 TB/s, and the norm before, which reads g once more, 122). Bound by instructions with 8-bit states:
+// 12 bytes an element, but about 80 instructions, the random roundings among them (192 million elements 521 us, 4.5 TB/s).
+// Many small tensors: 72 tensors 34 us, the time of their bytes. The tensors are cut into pieces of
 // CHUNK elements, of which each block takes a run; the descriptors travel in the kernel's parameters, and a block finds its first
 // tensor by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
 // pointers allow it. All arithmetic is fp32; the bias corrections are -expm1(t log b), whose error is a unit in the
