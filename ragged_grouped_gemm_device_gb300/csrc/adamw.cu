@@ -5,7 +5,7 @@
 //
 // Bound by memory with fp32 states: p, m and v are read and written once, g is read once (28 bytes an element, 30 with a bf16 copy:
 // 201 million elements 900 us, 6.7 TB/s, and the norm before, which reads g once more, 122). Bound by instructions with 8-bit states:
-// 12 bytes an element, but about 80 instructions, the random roundings among them (192 million elements 521 us, 4.5 TB/s).
+// 12 bytes an element, but about 80 instructions, the random roundings among them (192 million elements 487 us, 4.8 TB/s).
 // Many small tensors: 72 tensors 34 us, the time of their bytes. The tensors are cut into pieces of
 // CHUNK elements, of which each block takes a run; the descriptors travel in the kernel's parameters, and a block finds its first
 // tensor by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
@@ -33,7 +33,7 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int VB = 8;         // elements of a thread in one round
 constexpr int CHUNK = 4096;   // elements of a piece: two rounds
-constexpr int STEP_BLOCKS = 4;  // blocks on an SM
+constexpr int step_blocks(int bits) { return bits == 8 ? 3 : 4; }  // on an SM; four of 8-bit states would spill
 // Tensors of a launch: 12 KB of parameters, or 1.5 KB for the few tensors of one block, whose launch would wait for them.
 constexpr int MAX_TENSORS = 128, FEW_TENSORS = 16;
 constexpr int NORM_BLOCKS = 1216;
@@ -149,6 +149,11 @@ __device__ __forceinline__ void store8_upper(bf16* p, int k, bool wide, const fl
   }
 }
 
+// Asynchronous 8-byte copy global -> shared
+__device__ __forceinline__ void copy8_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
 // ------------------------------------------------------------------ 8-bit states
 // An E4M3 magnitude is the top 7 bits below the sign of an fp32 value 2^120 times smaller: the exponent biases differ
 // by 120, and the subnormals of both types meet.
@@ -262,6 +267,81 @@ struct Raw {
   }
 };
 
+// What the next round of 8-bit states reads, on its way into shared memory during the arithmetic of this one: 487 us for 192 million
+// elements, 520 with four blocks on an SM that load as they go; in registers it would spill, two rounds ahead take 512. A warp copies its 256 elements' gradients and parameters as they lie, 16 bytes a lane, and of m and v each lane its own eight
+// bytes; the scales, single bytes, wait in registers.
+struct Ahead {
+  static constexpr int WARP = 32 * (32 + 32 + 8 + 8), BYTES = THREADS / 32 * WARP;
+  const uint8_t *g, *p, *m, *v, *ms, *vs;  // of this lane's next copies
+  uint32_t at, sm, sv;                     // this warp's shared memory; scales
+  int eg, ep, left;                        // element bytes, rounds not begun
+
+  __device__ __forceinline__ void start() {
+    if (left > 0) {
+      const uint32_t lane = threadIdx.x & 31;
+      copy16_async(at + lane * 16, g);
+      if (eg == 4) copy16_async(at + 512 + lane * 16, g + 512);
+      copy16_async(at + 1024 + lane * 16, p);
+      if (ep == 4) copy16_async(at + 1536 + lane * 16, p + 512);
+      copy8_async(at + 2048 + lane * 8, m);
+      copy8_async(at + 2304 + lane * 8, v);
+      sm = *ms, sv = *vs;
+      constexpr int n = THREADS * VB;
+      g += n * eg, p += n * ep, m += n, v += n, ms += n / 32, vs += n / 32;
+      --left;
+    }
+    copy_commit();
+  }
+  // this lane's first element, and the rounds
+  __device__ __forceinline__ void begin(const moe_adamw_tensor_t& q, long long i0, int rounds, uint8_t* smem) {
+    const int lane = threadIdx.x & 31;
+    const long long w0 = i0 - lane * VB;
+    eg = q.g_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    ep = q.p_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    g = static_cast<const uint8_t*>(q.g) + w0 * eg + lane * 16;
+    p = static_cast<const uint8_t*>(q.p) + w0 * ep + lane * 16;
+    m = static_cast<const uint8_t*>(q.m) + i0;
+    v = static_cast<const uint8_t*>(q.v) + i0;
+    ms = q.m_scale + (i0 >> 5);
+    vs = q.v_scale + (i0 >> 5);
+    left = rounds;
+    at = smem_u32(smem) + (threadIdx.x >> 5) * WARP;
+    start();
+  }
+  __device__ __forceinline__ void get(uint32_t from, int es, float (&f)[VB]) const {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t w[4];
+    if (es == 2) {
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + lane * 16));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(from + lane * 32 + j * 16));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[4 * j + i] = __uint_as_float(w[i]);
+      }
+    }
+  }
+  template <typename R>
+  __device__ __forceinline__ void take(R& d) {
+    copy_wait<0>();
+    __syncwarp();  // lanes copy for one another
+    const uint32_t lane = threadIdx.x & 31;
+    get(at, eg, d.g);
+    get(at + 1024, ep, d.p);
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(d.wm[0]), "=r"(d.wm[1]) : "r"(at + 2048 + lane * 8));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(d.wv[0]), "=r"(d.wv[1]) : "r"(at + 2304 + lane * 8));
+    d.sm = sm, d.sv = sv;
+    __syncwarp();
+    start();
+  }
+};
+
 struct TensorStep {
   float c, step, root, keep;
   uint32_t key;
@@ -347,7 +427,8 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
 }
 
 template <int BITS, int N>
-__global__ void __launch_bounds__(THREADS, STEP_BLOCKS) adamw_kernel(const __grid_constant__ Batch<N> batch, const StepArgs a) {
+__global__ void __launch_bounds__(THREADS, step_blocks(BITS)) adamw_kernel(const __grid_constant__ Batch<N> batch, const StepArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];  // 8-bit states: Ahead::BYTES
   grid_wait();
   TensorStep u;
   u.c = a.grad_scale ? *after_wait(a.grad_scale) : 1.0f;
@@ -369,9 +450,19 @@ __global__ void __launch_bounds__(THREADS, STEP_BLOCKS) adamw_kernel(const __gri
       long long i0 = static_cast<long long>(c - batch.chunk0[j]) * CHUNK + threadIdx.x * VB;
       const long long last = min(q.n, static_cast<long long>(end - batch.chunk0[j]) * CHUNK);  // of this block's run
       Raw<BITS> d;
-      for (; i0 - threadIdx.x * VB + THREADS * VB <= last && wide; i0 += THREADS * VB) {
-        d.load(q, i0, VB, true);
-        adamw_round<BITS, true>(q, a, u, i0, VB, true, d);
+      if constexpr (BITS == 8) {
+        const int rounds = wide ? static_cast<int>((last - (i0 - threadIdx.x * VB)) / (THREADS * VB)) : 0;
+        Ahead ahead;
+        if (rounds > 0) ahead.begin(q, i0, rounds, smem);
+        for (int k = 0; k < rounds; ++k, i0 += THREADS * VB) {
+          ahead.take(d);
+          adamw_round<BITS, true>(q, a, u, i0, VB, true, d);
+        }
+      } else {
+        for (; i0 - threadIdx.x * VB + THREADS * VB <= last && wide; i0 += THREADS * VB) {
+          d.load(q, i0, VB, true);
+          adamw_round<BITS, true>(q, a, u, i0, VB, true, d);
+        }
       }
       for (; i0 - threadIdx.x * VB < last; i0 += THREADS * VB) {
         const int k = static_cast<int>(max(0LL, min(static_cast<long long>(VB), last - i0)));  // elements of this thread
@@ -505,9 +596,9 @@ cudaError_t launch_step(StepArgs a, const moe_adamw_tensor_t* tensors, int count
     // 8-bit states: as many blocks as fit, since what a block computes once would be a fifth of the instructions of a piece. 32 bits,
     // bound by memory: a block for each piece, which spread better (201 million parameters: 902 us, 1047 in runs).
     a.blocks = std::max(b.chunk0[n], 1u);
-    if (state_bits == 8) a.blocks = std::min(a.blocks, static_cast<unsigned>(STEP_BLOCKS * device_sm_count()));
+    if (state_bits == 8) a.blocks = std::min(a.blocks, static_cast<unsigned>(step_blocks(8) * device_sm_count()));
     a.last = i + n >= count;
-    const cudaError_t err = launch_dependent(state_bits == 8 ? adamw_kernel<8, N> : adamw_kernel<32, N>, a.blocks, THREADS, 0, s, b, a);
+    const cudaError_t err = launch_dependent(state_bits == 8 ? adamw_kernel<8, N> : adamw_kernel<32, N>, a.blocks, THREADS, state_bits == 8 ? Ahead::BYTES : 0, s, b, a);
     if (err != cudaSuccess) return err;
     i += std::max(n, 1);
   }
