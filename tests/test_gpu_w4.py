@@ -210,6 +210,28 @@ def test_popular_experts_in_many_blocks(lib, E, k, d, h, group):
     _check_matvec(x, ids.cuda(), k, w, y)
 
 
+# rows whose x goes through shared memory in several segments (one token, few and many of an expert, either product), and the
+# limits of slots and experts
+@pytest.mark.parametrize("T,E,k,d,h,group", [(1, 4, 2, 4400, 4300, 64), (6, 4, 2, 4400, 136, 32), (12, 3, 1, 64, 4300, 128), (30, 2, 2, 4400, 2200, 64),
+                                             (25, 2, 1, 2064, 2056, 32), (128, 1024, 32, 64, 16, 32), (128, 400, 32, 40, 24, 64)])
+def test_long_rows_and_limits(lib, T, E, k, d, h, group):
+    ug, down, gate, up, wd = _experts(E, d, h, group)
+    layer = Int4ExpertLayer.from_checkpoint(ug, down, E, d, h, group)
+    x = _x(T, d)
+    ids, weights = _route(T, E, k)
+    layer._buffers(T, k)
+    layer.ws.fill_(255)
+    out = layer.forward(x, ids, weights).clone()
+    _check_decode(x, ids, weights, gate, up, wd, out)
+    layer.ws.fill_(255)
+    assert torch.equal(out, layer.forward(x, ids, weights))
+    y = torch.full((T * k, h), float("nan"), device="cuda")
+    ids2 = torch.where(ids >= 0, 2 * ids + 1, ids)  # the up matrices
+    _lib.moe_w4_matvec(x, ids2, T, k, 2 * E, h, d, group, layer.w_ug, y)
+    w = np.stack([gate, up], axis=1).reshape(2 * E, h, d)
+    _check_matvec(x, ids2, k, w, y)
+
+
 def test_more_slots_than_one_call_takes(lib):
     E, d, h, group, T, k = 5, 64, 32, 32, 700, 8
     ug, down, gate, up, wd = _experts(E, d, h, group)
