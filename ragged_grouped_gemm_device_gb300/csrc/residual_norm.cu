@@ -16,6 +16,7 @@
 // us (5.25 TB/s), of which the sum of the partials 6. 16 x 2048: 3 us, a launch and a round trip to memory.
 #include <algorithm>
 #include <cmath>
+#include <tuple>
 #include <type_traits>
 
 #include "common.cuh"
@@ -57,8 +58,8 @@ struct JoinArgs {
 };
 
 // ------------------------------------------------------------------ rows of any width
-// One block a row, single elements, one pass over the row for each reduction (the later ones from L2). Widths that are not a
-// multiple of 8, rows off the 16-byte grid and rows wider than 8192: bound by the instructions of single elements.
+// Rows wider than 8192: one block a row, single elements, one pass over the row for each reduction (the later ones from L2), bound by
+// the instructions of single elements (2048 x 10000 bf16: forward 155 us, backward 453).
 constexpr int WIDE_THREADS = 512;
 
 template <typename T>
@@ -388,6 +389,63 @@ struct RowFeed {
   }
 };
 
+// The same for rows that do not lie on the 16-byte grid: single elements from memory, neighbouring lanes neighbouring columns.
+template <int NCH, int TPR, typename... Ts>
+struct RowDirect {
+  static constexpr int NT = sizeof...(Ts), smem_bytes = 0;
+  const void* p[NT];
+  long long ld[NT], row;
+  int t, d, step;
+
+  __device__ __forceinline__ void init(uint8_t*, int t_, int d_, int) {
+    t = t_;
+    d = d_;
+  }
+  __device__ __forceinline__ void tensor(int k, const void* p_, long long ld_, long long row0, int rows_step) {
+    p[k] = p_;
+    ld[k] = ld_;
+    row = row0;
+    step = rows_step;
+  }
+  __device__ __forceinline__ void prime() {}
+  __device__ __forceinline__ void wait() {}
+  __device__ __forceinline__ void next() { row += step; }
+  template <int K>
+  __device__ __forceinline__ void get(int i, float (&f)[8]) const {
+    using T = std::tuple_element_t<K, std::tuple<Ts...>>;
+    const T* at = static_cast<const T*>(p[K]) + row * ld[K];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = (i * 8 + j) * TPR + t;
+      f[j] = p[K] != nullptr && c < d ? moe::get(at + c) : 0.f;
+    }
+  }
+};
+template <bool VEC, int NCH, int TPR, typename... Ts>
+using Feed = std::conditional_t<VEC, RowFeed<NCH, TPR, Ts...>, RowDirect<NCH, TPR, Ts...>>;
+
+// The column of element j of thread t's chunk i
+template <bool VEC, int TPR>
+__device__ __forceinline__ int column(int t, int i, int j) {
+  return VEC ? (i * TPR + t) * 8 + j : (i * 8 + j) * TPR + t;
+}
+// Eight weights of a chunk, 0 past the row's end
+template <bool VEC, int TPR>
+__device__ __forceinline__ void weights8(const void* w, bool w_bf16, int t, int i, int d, float fill, float (&f)[8]) {
+  if constexpr (VEC) {
+    const int c = column<true, TPR>(t, i, 0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.f;
+    if (c < d) load_weight<8>(w, w_bf16, c, fill, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = column<false, TPR>(t, i, j);
+      f[j] = c < d ? weight(w, w_bf16, c, fill) : 0.f;
+    }
+  }
+}
+
 __device__ __forceinline__ void put8(bf16* p, const float (&f)[8]) { Chunk<bf16, 8>::store(p, f); }
 __device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
@@ -398,8 +456,22 @@ __device__ __forceinline__ void pairs(const float (&f)[8], F2 (&p)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) p[j] = pair(f[2 * j], f[2 * j + 1]);
 }
-template <typename T>
-__device__ __forceinline__ void put8(T* p, const F2 (&v)[4]) {
+// a chunk to its place in a row
+template <bool VEC, int TPR, typename T>
+__device__ __forceinline__ void put_chunk(T* row, int t, int i, int d, const float (&f)[8]) {
+  if constexpr (VEC) {
+    const int c = column<true, TPR>(t, i, 0);
+    if (c < d) put8(row + c, f);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = column<false, TPR>(t, i, j);
+      if (c < d) put(row + c, f[j]);
+    }
+  }
+}
+template <bool VEC, int TPR, typename T>
+__device__ __forceinline__ void put_chunk(T* row, int t, int i, int d, const F2 (&v)[4]) {
   float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -407,7 +479,7 @@ __device__ __forceinline__ void put8(T* p, const F2 (&v)[4]) {
     f[2 * j] = q.x;
     f[2 * j + 1] = q.y;
   }
-  put8(p, f);
+  put_chunk<VEC, TPR>(row, t, i, d, f);
 }
 
 // Blocks on an SM, which size the grids and bound the registers. Forward: rows of 256 chunks go to 256 threads with one chunk each,
@@ -418,7 +490,7 @@ constexpr int fwd_blocks(int tpr, int nch, bool bias) { return tpr == 256 && nch
 constexpr int bwd_blocks(int tpr) { return tpr <= 128 ? 3 : 1; }
 
 // The variances are of the rows in registers, after the mean: no cancellation. BIAS: some norm has a beta.
-template <typename TX, typename TY, int NCH, int TPR, bool BIAS>
+template <typename TX, typename TY, int NCH, int TPR, bool BIAS, bool VEC>
 __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)) join_fwd_kernel(const JoinArgs a) {
   grid_wait();
   constexpr int ROWS = block_threads(TPR) / TPR;
@@ -428,30 +500,22 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
   const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
-  RowFeed<NCH, TPR, TX, TY> feed;
+  Feed<VEC, NCH, TPR, TX, TY> feed;
   feed.init(ring, t, a.d, rows);
   feed.tensor(0, after_wait(a.x), a.ldx, row0, step);
   feed.tensor(1, after_wait(a.y), a.ldy, row0, step);
   feed.prime();
   // r = alpha x + A yhat + B;  n = rhat g2 + b2
   float A[NCH][8], B[NCH][8], g2[NCH][8], b2[NCH][8];
-  bool in[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = (i * TPR + t) * 8;
-    in[i] = c < a.d;
-    if (!in[i]) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) A[i][j] = B[i][j] = g2[i][j] = b2[i][j] = 0.f;
-      continue;
-    }
     float gate[8];
-    load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
-    load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, A[i]);
-    load_weight<8>(after_wait(a.g2), a.w_bf16, c, 1.f, g2[i]);
+    weights8<VEC, TPR>(after_wait(a.gate), a.w_bf16, t, i, a.d, 1.f, gate);
+    weights8<VEC, TPR>(after_wait(a.g1), a.w_bf16, t, i, a.d, 1.f, A[i]);
+    weights8<VEC, TPR>(after_wait(a.g2), a.w_bf16, t, i, a.d, 1.f, g2[i]);
     if constexpr (BIAS) {
-      load_weight<8>(after_wait(a.b1), a.w_bf16, c, 0.f, B[i]);
-      load_weight<8>(after_wait(a.b2), a.w_bf16, c, 0.f, b2[i]);
+      weights8<VEC, TPR>(after_wait(a.b1), a.w_bf16, t, i, a.d, 0.f, B[i]);
+      weights8<VEC, TPR>(after_wait(a.b2), a.w_bf16, t, i, a.d, 0.f, b2[i]);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -459,6 +523,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)
       if constexpr (BIAS) B[i][j] *= a.beta * gate[j];
     }
   }
+  const auto in = [&](int i, int j) { return column<VEC, TPR>(t, i, VEC ? 0 : j) < a.d; };
   int par = 0;
   const auto sum = [&](float v) {
     const float s = row_sum<TPR>(v, red[par]);
@@ -485,7 +550,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)
     if (a.post == MOE_NORM_LAYER) {
       each([&](int i, int j) { s += y[i][j]; });
       mean1 = sum(s) * inv_d;
-      each([&](int i, int j) { y[i][j] -= in[i] ? mean1 : 0.f; });
+      each([&](int i, int j) { y[i][j] -= in(i, j) ? mean1 : 0.f; });
     }
     if (a.post != MOE_NORM_NONE) {
       s = 0.f;
@@ -499,14 +564,13 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)
     });
     if (a.r != nullptr) {
 #pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) put8(static_cast<TX*>(a.r) + row * a.ldr + (i * TPR + t) * 8, r[i]);
+      for (int i = 0; i < NCH; ++i) put_chunk<VEC, TPR>(static_cast<TX*>(a.r) + row * a.ldr, t, i, a.d, r[i]);
     }
     if (a.pre == MOE_NORM_LAYER) {
       s = 0.f;
       each([&](int i, int j) { s += r[i][j]; });
       mean2 = sum(s) * inv_d;
-      each([&](int i, int j) { r[i][j] -= in[i] ? mean2 : 0.f; });
+      each([&](int i, int j) { r[i][j] -= in(i, j) ? mean2 : 0.f; });
     }
     if (a.pre != MOE_NORM_NONE) {
       s = 0.f;
@@ -514,8 +578,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)
       rstd2 = 1.0f / sqrtf(sum(s) * inv_d + a.eps);
       each([&](int i, int j) { r[i][j] = fmaf(r[i][j] * rstd2, g2[i][j], BIAS ? b2[i][j] : 0.f); });
 #pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) put8(static_cast<TY*>(a.n) + row * a.ldn + (i * TPR + t) * 8, r[i]);
+      for (int i = 0; i < NCH; ++i) put_chunk<VEC, TPR>(static_cast<TY*>(a.n) + row * a.ldn, t, i, a.d, r[i]);
     }
     if (t == 0 && a.stats != nullptr) {
       const size_t T = a.T;
@@ -529,7 +592,7 @@ __global__ void __launch_bounds__(block_threads(TPR), fwd_blocks(TPR, NCH, BIAS)
 
 // Arithmetic in pairs of fp32, one instruction for two, and without branches: single values and a branch for each kind of norm took
 // more instructions than memory leaves time for (16384 x 2048: 93 us, 77 so). BIAS: the sums over the rows that only the betas' gradients need (and, with a beta, the gate's) are wanted.
-template <typename TX, typename TY, int NCH, int TPR, bool BIAS>
+template <typename TX, typename TY, int NCH, int TPR, bool BIAS, bool VEC>
 __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_kernel(const JoinArgs a) {
   grid_wait();
   constexpr int ROWS = block_threads(TPR) / TPR;
@@ -539,7 +602,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
   const float inv_d = 1.0f / static_cast<float>(a.d);
   const int row0 = blockIdx.x * ROWS + (ROWS > 1 ? threadIdx.x / TPR : 0), step = gridDim.x * ROWS;
   const int rows = row0 < a.T ? (a.T - 1 - row0) / step + 1 : 0;
-  RowFeed<NCH, TPR, TY, TX, TX, TY> feed;  // dn, r, dr, y
+  Feed<VEC, NCH, TPR, TY, TX, TX, TY> feed;  // dn, r, dr, y
   feed.init(ring, t, a.d, rows);
   feed.tensor(0, after_wait(a.dn), a.lddn, row0, step);
   feed.tensor(1, a.pre != MOE_NORM_NONE ? after_wait(a.r) : nullptr, a.ldr, row0, step);
@@ -547,23 +610,16 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
   feed.tensor(3, after_wait(a.y), a.ldy, row0, step);
   feed.prime();
   F2 A[NCH][4], g2[NCH][4], S1[NCH][4], S0[NCH][4], P1[NCH][4], P0[NCH][4];
-  bool in[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = (i * TPR + t) * 8;
-    in[i] = c < a.d;
+    float w[8], gate[8];
+    weights8<VEC, TPR>(after_wait(a.gate), a.w_bf16, t, i, a.d, 1.f, gate);
+    weights8<VEC, TPR>(after_wait(a.g1), a.w_bf16, t, i, a.d, 1.f, w);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A[i][j] = g2[i][j] = both(0.f);
-    if (in[i]) {
-      float w[8], gate[8];
-      load_weight<8>(after_wait(a.gate), a.w_bf16, c, 1.f, gate);
-      load_weight<8>(after_wait(a.g1), a.w_bf16, c, 1.f, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] *= a.beta * gate[j];
-      pairs(w, A[i]);
-      load_weight<8>(after_wait(a.g2), a.w_bf16, c, 1.f, w);
-      pairs(w, g2[i]);
-    }
+    for (int j = 0; j < 8; ++j) w[j] *= a.beta * gate[j];
+    pairs(w, A[i]);
+    weights8<VEC, TPR>(after_wait(a.g2), a.w_bf16, t, i, a.d, 1.f, w);
+    pairs(w, g2[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) S1[i][j] = S0[i][j] = P1[i][j] = P0[i][j] = both(0.f);
   }
@@ -577,8 +633,8 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
   const F2 alpha = both(a.alpha);
   // lane l holds the statistics of rows l, l + 32, ... of this block: one wait in 32 rows
   float st[4] = {0.f, 1.f, 0.f, 1.f};
-  TX* dx = a.dx ? static_cast<TX*>(a.dx) + row0 * a.lddx + t * 8 : nullptr;
-  TY* dy = a.dy ? static_cast<TY*>(a.dy) + row0 * a.lddy + t * 8 : nullptr;
+  TX* dx = a.dx ? static_cast<TX*>(a.dx) + row0 * a.lddx : nullptr;
+  TY* dy = a.dy ? static_cast<TY*>(a.dy) + row0 * a.lddy : nullptr;
   for (int k = 0; k < rows; ++k, dx += step * a.lddx, dy += step * a.lddy) {
     if ((k & 31) == 0 && k + lane < rows && a.stats != nullptr) {
       const float* p = after_wait(a.stats) + row0 + static_cast<long long>(k + lane) * step;
@@ -633,13 +689,12 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
     feed.next();
     if (a.dx != nullptr) {
 #pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) {
-          F2 o[4];
+      for (int i = 0; i < NCH; ++i) {
+        F2 o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = mul2(alpha, D[i][j]);
-          put8(dx + i * TPR * 8, o);
-        }
+        for (int j = 0; j < 4; ++j) o[j] = mul2(alpha, D[i][j]);
+        put_chunk<VEC, TPR>(dx, t, i, a.d, o);
+      }
     }
     if (a.y != nullptr) {
       F2 s1 = both(0.f), s2 = s1;
@@ -658,8 +713,7 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
         each([&](int i, int j) { D[i][j] = fma2(D[i][j], R, fma2(h[i][j], m1, m0)); });
       }
 #pragma unroll
-      for (int i = 0; i < NCH; ++i)
-        if (in[i]) put8(dy + i * TPR * 8, D[i]);
+      for (int i = 0; i < NCH; ++i) put_chunk<VEC, TPR>(dy, t, i, a.d, D[i]);
     }
   }
   if (a.part == nullptr) return;
@@ -687,13 +741,13 @@ __global__ void __launch_bounds__(block_threads(TPR), bwd_blocks(TPR)) join_bwd_
         }
       }
     }
-    const int c = (i * TPR + t) * 8;
-    if (w != 0 || !in[i]) continue;
-    put8(part + c, S1[i]);
-    put8(part + 2 * static_cast<size_t>(a.d) + c, P1[i]);
+    if (w != 0) continue;
+    const size_t d = a.d;
+    put_chunk<VEC, TPR>(part, t, i, a.d, S1[i]);
+    put_chunk<VEC, TPR>(part + 2 * d, t, i, a.d, P1[i]);
     if constexpr (BIAS) {
-      put8(part + a.d + c, S0[i]);
-      put8(part + 3 * static_cast<size_t>(a.d) + c, P0[i]);
+      put_chunk<VEC, TPR>(part + d, t, i, a.d, S0[i]);
+      put_chunk<VEC, TPR>(part + 3 * d, t, i, a.d, P0[i]);
     }
   }
 }
@@ -740,23 +794,23 @@ __global__ void __launch_bounds__(1024) join_partials_kernel(const JoinArgs a, i
   if (o.pre_beta) o.pre_beta[c] = t[3];
 }
 
-template <typename TX, typename TY, int NCH, int TPR>
+template <bool VEC, typename TX, typename TY, int NCH, int TPR>
 cudaError_t launch_fwd_rows(const JoinArgs& a, cudaStream_t s) {
-  constexpr int ROWS = block_threads(TPR) / TPR, smem = RowFeed<NCH, TPR, TX, TY>::smem_bytes;
+  constexpr int ROWS = block_threads(TPR) / TPR, smem = Feed<VEC, NCH, TPR, TX, TY>::smem_bytes;
   const bool bias = a.b1 || a.b2;
   const int grid = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, fwd_blocks(TPR, NCH, bias) * static_cast<long long>(device_sm_count())));
-  const auto kernel = bias ? join_fwd_kernel<TX, TY, NCH, TPR, true> : join_fwd_kernel<TX, TY, NCH, TPR, false>;
+  const auto kernel = bias ? join_fwd_kernel<TX, TY, NCH, TPR, true, VEC> : join_fwd_kernel<TX, TY, NCH, TPR, false, VEC>;
   if (smem > 40 * 1024) {  // beside the static shared memory
     const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (err != cudaSuccess) return err;
   }
   return launch_dependent(kernel, grid, block_threads(TPR), smem, s, a);
 }
-template <typename TX, typename TY, int NCH, int TPR>
+template <bool VEC, typename TX, typename TY, int NCH, int TPR>
 cudaError_t launch_bwd_rows(const JoinArgs& a, bool bias, cudaStream_t s, int& blocks) {
-  constexpr int ROWS = block_threads(TPR) / TPR, smem = RowFeed<NCH, TPR, TY, TX, TX, TY>::smem_bytes;
+  constexpr int ROWS = block_threads(TPR) / TPR, smem = Feed<VEC, NCH, TPR, TY, TX, TX, TY>::smem_bytes;
   blocks = static_cast<int>(std::min<long long>((static_cast<long long>(a.T) + ROWS - 1) / ROWS, std::min(bwd_blocks(TPR) * device_sm_count(), BWD_MAX_BLOCKS)));
-  const auto kernel = bias ? join_bwd_kernel<TX, TY, NCH, TPR, true> : join_bwd_kernel<TX, TY, NCH, TPR, false>;
+  const auto kernel = bias ? join_bwd_kernel<TX, TY, NCH, TPR, true, VEC> : join_bwd_kernel<TX, TY, NCH, TPR, false, VEC>;
   if (smem > 40 * 1024) {  // beside the static shared memory
     const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
     if (err != cudaSuccess) return err;
@@ -764,36 +818,41 @@ cudaError_t launch_bwd_rows(const JoinArgs& a, bool bias, cudaStream_t s, int& b
   return launch_dependent(kernel, blocks, block_threads(TPR), smem, s, a);
 }
 
-// Rows that move 16 bytes at a time go through registers up to a width of 8192, others through the kernels of any width.
+// Rows go through registers up to a width of 8192, wider ones through the kernels of any width. Off the 16-byte grid the registers
+// are filled by single elements (16384 x 2047 bf16: forward 80 us, backward 148; through the kernels of any width 414 and 677).
 constexpr int REGISTER_WIDTH = 8192;
 
+template <bool VEC, typename TX, typename TY>
+cudaError_t launch_fwd_registers(const JoinArgs& a, cudaStream_t s) {
+  const int chunks = (a.d + 7) / 8;
+  if (chunks <= 32) return launch_fwd_rows<VEC, TX, TY, 1, 32>(a, s);
+  if (chunks <= 64) return launch_fwd_rows<VEC, TX, TY, 2, 32>(a, s);
+  if (chunks <= 128) return launch_fwd_rows<VEC, TX, TY, 1, 128>(a, s);
+  if (chunks <= 256) return launch_fwd_rows<VEC, TX, TY, 1, 256>(a, s);
+  if (chunks <= 512) return launch_fwd_rows<VEC, TX, TY, 2, 256>(a, s);
+  return launch_fwd_rows<VEC, TX, TY, 2, 512>(a, s);
+}
 template <typename TX, typename TY>
 cudaError_t launch_fwd(const JoinArgs& a, bool vec, cudaStream_t s) {
-  const int chunks = a.d / 8;
-  if (vec && a.d <= REGISTER_WIDTH) {
-    if (chunks <= 32) return launch_fwd_rows<TX, TY, 1, 32>(a, s);
-    if (chunks <= 64) return launch_fwd_rows<TX, TY, 2, 32>(a, s);
-    if (chunks <= 128) return launch_fwd_rows<TX, TY, 1, 128>(a, s);
-    if (chunks <= 256) return launch_fwd_rows<TX, TY, 1, 256>(a, s);
-    if (chunks <= 512) return launch_fwd_rows<TX, TY, 2, 256>(a, s);
-    return launch_fwd_rows<TX, TY, 2, 512>(a, s);
-  }
+  if (a.d <= REGISTER_WIDTH) return vec ? launch_fwd_registers<true, TX, TY>(a, s) : launch_fwd_registers<false, TX, TY>(a, s);
   join_fwd_wide_kernel<TX, TY><<<std::min(a.T, 1 << 20), WIDE_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 // `blocks`: the rows of partial sums that the launch leaves; `bias`: all four sums are wanted
+template <bool VEC, typename TX, typename TY>
+cudaError_t launch_bwd_registers(const JoinArgs& a, bool bias, cudaStream_t s, int& blocks) {
+  const int chunks = (a.d + 7) / 8;
+  if (chunks <= 32) return launch_bwd_rows<VEC, TX, TY, 1, 32>(a, bias, s, blocks);
+  if (chunks <= 64) return launch_bwd_rows<VEC, TX, TY, 2, 32>(a, bias, s, blocks);
+  if (chunks <= 128) return launch_bwd_rows<VEC, TX, TY, 1, 128>(a, bias, s, blocks);
+  if (chunks <= 256) return launch_bwd_rows<VEC, TX, TY, 2, 128>(a, bias, s, blocks);
+  if (chunks <= 512) return launch_bwd_rows<VEC, TX, TY, 2, 256>(a, bias, s, blocks);
+  return launch_bwd_rows<VEC, TX, TY, 2, 512>(a, bias, s, blocks);
+}
 template <typename TX, typename TY>
 cudaError_t launch_bwd(const JoinArgs& a, bool vec, bool bias, cudaStream_t s, int& blocks) {
-  const int chunks = a.d / 8;
-  if (vec && a.d <= REGISTER_WIDTH) {
-    if (chunks <= 32) return launch_bwd_rows<TX, TY, 1, 32>(a, bias, s, blocks);
-    if (chunks <= 64) return launch_bwd_rows<TX, TY, 2, 32>(a, bias, s, blocks);
-    if (chunks <= 128) return launch_bwd_rows<TX, TY, 1, 128>(a, bias, s, blocks);
-    if (chunks <= 256) return launch_bwd_rows<TX, TY, 2, 128>(a, bias, s, blocks);
-    if (chunks <= 512) return launch_bwd_rows<TX, TY, 2, 256>(a, bias, s, blocks);
-    return launch_bwd_rows<TX, TY, 2, 512>(a, bias, s, blocks);
-  }
+  if (a.d <= REGISTER_WIDTH) return vec ? launch_bwd_registers<true, TX, TY>(a, bias, s, blocks) : launch_bwd_registers<false, TX, TY>(a, bias, s, blocks);
   const int grid = std::min(a.T, 1 << 20);
   blocks = std::min(a.T, BWD_MAX_BLOCKS);
   if (a.pre != MOE_NORM_NONE) join_bwd_means_kernel<TX, TY><<<grid, WIDE_THREADS, 0, s>>>(a);

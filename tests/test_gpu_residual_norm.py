@@ -160,6 +160,20 @@ def test_every_pair_of_norms(lib, d, post, pre):
     Case(5, d, "fp32", "bf16", post, pre, bias=False).check()
 
 
+# rows off the 16-byte grid in every register layout, with several rows a block
+@pytest.mark.parametrize("stream,branch", [("bf16", "bf16"), ("fp32", "bf16"), ("fp32", "fp32")])
+@pytest.mark.parametrize("T,d", [(2100, 255), (2000, 257), (1900, 511), (1000, 513), (1000, 1023), (1000, 1025), (950, 2047), (400, 2049), (350, 4095),
+                                 (310, 4097), (310, 7001)])
+def test_odd_widths_of_every_layout(lib, T, d, stream, branch):
+    Case(T, d, stream, branch, *NORMS[(T + d) % 4]).check()
+
+
+# more than 32 rows a block: the backward fetches their statistics 32 rows at a time
+@pytest.mark.parametrize("T,d", [(60000, 16), (60000, 9), (15000, 520), (15000, 521)])
+def test_many_rows_a_block(lib, T, d):
+    Case(T, d, "bf16", "bf16", "layer", "layer").check()
+
+
 @pytest.mark.parametrize("w", ["bf16", "fp32"])
 @pytest.mark.parametrize("d", [100, 1024])
 def test_weights_of_both_types(lib, d, w):
