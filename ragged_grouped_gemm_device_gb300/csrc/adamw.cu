@@ -343,7 +343,7 @@ struct Ahead {
 };
 
 struct TensorStep {
-  float c, step, root, keep;
+  float c, step, root, decay;
   uint32_t key;
 };
 
@@ -377,9 +377,13 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
 #pragma unroll
     for (int i = 0; i < VB; ++i) r[i] = sqrtf(d.v[i]);
   }
-  // the quotient to two units: it is a small part of p
+  // What is taken from p, the quotient to two units: a small part of p. A bf16 p is rounded by its fraction, of which only whole units
+  // matter there: cut off, not rounded, so that this rounding decides none.
 #pragma unroll
-  for (int i = 0; i < VB; ++i) d.p[i] = fmaf(d.p[i], u.keep, -(u.step * d.m[i]) * reciprocal(fmaf(r[i], u.root, a.eps)));
+  for (int i = 0; i < VB; ++i) {
+    const float less = fmaf(d.p[i], u.decay, (u.step * d.m[i]) * reciprocal(fmaf(r[i], u.root, a.eps)));
+    d.p[i] = q.p_dtype == MOE_DTYPE_BF16 ? __fsub_rz(d.p[i], less) : d.p[i] - less;
+  }
   uint32_t rnd[VB];
   if (BITS == 8 || q.p_dtype == MOE_DTYPE_BF16) {
     const uint32_t x0 = u.key + static_cast<uint32_t>(i0) * 0x9E3779B9u + static_cast<uint32_t>(i0 >> 32) * 0x85EBCA6Bu;
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(THREADS, step_blocks(BITS)) adamw_kernel(const
     for (int j = find_tensor(batch, c); c < c1; ++j) {
       const moe_adamw_tensor_t& q = batch.t[j];
       const unsigned end = min(c1, batch.chunk0[j + 1]);
-      u.keep = fmaf(-lr, q.weight_decay, 1.0f);
+      u.decay = lr * q.weight_decay;
       u.key = mix(a.seed ^ mix(0x9E3779B9u * static_cast<uint32_t>(t) + static_cast<uint32_t>(batch.first + j)));
       const bool wide = batch.wide[j] != 0;
       long long i0 = static_cast<long long>(c - batch.chunk0[j]) * CHUNK + threadIdx.x * VB;
