@@ -5,7 +5,7 @@
 //
 // Bound by memory with fp32 states: p, m and v are read and written once, g is read once (28 bytes an element, 30 with a bf16 copy:
 // 201 million elements 900 us, 6.7 TB/s, and the norm before, which reads g once more, 122). Bound by instructions with 8-bit states:
-// 12 bytes an element, but about 80 instructions, the random roundings among them (192 million elements 487 us, 4.8 TB/s).
+// 12 bytes an element, but about 80 instructions, the random roundings among them (192 million elements 499 us, 4.7 TB/s).
 // Many small tensors: 72 tensors 34 us, the time of their bytes. The tensors are cut into pieces of
 // CHUNK elements, of which each block takes a run; the descriptors travel in the kernel's parameters, and a block finds its first
 // tensor by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
@@ -267,8 +267,8 @@ struct Raw {
   }
 };
 
-// What the next round of 8-bit states reads, on its way into shared memory during the arithmetic of this one: 487 us for 192 million
-// elements, 520 with four blocks on an SM that load as they go; in registers it would spill, two rounds ahead take 512. A warp copies its 256 elements' gradients and parameters as they lie, 16 bytes a lane, and of m and v each lane its own eight
+// What the next round of 8-bit states reads, on its way into shared memory during the arithmetic of this one (192 million elements:
+// 520 us with four blocks on an SM that load as they go, 487 so; in registers it would spill, two rounds ahead took 512). A warp copies its 256 elements' gradients and parameters as they lie, 16 bytes a lane, and of m and v each lane its own eight
 // bytes; the scales, single bytes, wait in registers.
 struct Ahead {
   static constexpr int WARP = 32 * (32 + 32 + 8 + 8), BYTES = THREADS / 32 * WARP;
@@ -378,7 +378,7 @@ __device__ __forceinline__ void adamw_round(const moe_adamw_tensor_t& q, const S
     for (int i = 0; i < VB; ++i) r[i] = sqrtf(d.v[i]);
   }
   // What is taken from p, the quotient to two units: a small part of p. A bf16 p is rounded by its fraction, of which only whole units
-  // matter there: cut off, not rounded, so that this rounding decides none.
+  // matter there: cut off, not rounded, so that this rounding decides none (486 -> 499 us for 192 million elements with 8-bit states).
 #pragma unroll
   for (int i = 0; i < VB; ++i) {
     const float less = fmaf(d.p[i], u.decay, (u.step * d.m[i]) * reciprocal(fmaf(r[i], u.root, a.eps)));
