@@ -56,7 +56,8 @@ struct Chunk<bf16, 1> {
 template <>
 struct Chunk<float, 1> {
   float v;
-  __device__ __forceinline__ void load(const float* p) { v = __ldg(p); }
+  // not __ldg: an output may lie over the rows, and the join reads back what it has stored
+  __device__ __forceinline__ void load(const float* p) { v = *p; }
   __device__ __forceinline__ void unpack(float (&f)[1]) const { f[0] = v; }
   static __device__ __forceinline__ void store(float* p, const float (&f)[1]) { *p = f[0]; }
 };
