@@ -677,8 +677,8 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
  *   apart). A slot whose id is outside [0, matrices) gets a row of zeros.
  * moe_w4_swiglu_decode -- out[t] = sum_j weights[t, j] SwiGLU(x[t] W_ug,e^T) W_down,e with e = ids[t, j]: w_ug packs 2 E
  *   matrices of h rows of d elements (matrix 2e: gate of expert e, 2e + 1: up), w_down E matrices of d rows of h
- *   elements (the transpose of W_down,e). SwiGLU's output is rounded to bf16, as in the BF16 forward; out [T, d]
- *   bf16 is summed over the slots in order in fp32 and rounded once. weights [T * top_k] fp32, nullable (ones).
+ *   elements (the transpose of W_down,e). SwiGLU's output reaches the down product as a sum of two bf16 values (off by at most
+ *   2^-16 of it); out [T, d] bf16 is summed over the slots in order in fp32 and rounded once. weights [T * top_k] fp32, nullable (ones).
  *   Slots with ids outside [0, E) are dropped. ws: moe_workspace_bytes(MOE_OP_W4_DECODE, T, top_k, E, d, h, 0)
  *   bytes, 256-byte aligned; it may not be shared by calls that can overlap.
  * Limits: T * top_k <= 4096 (prompts run in pieces), E <= 1024, matrices <= 2048, top_k <= 32. Results are

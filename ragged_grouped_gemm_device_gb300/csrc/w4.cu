@@ -8,8 +8,8 @@
 // 16 rows by 8 columns by 16 elements are one matrix instruction on bf16 values 16 + code, which a code becomes by one instruction
 // for two; so few tokens' columns are mostly empty, but a weight is unpacked once for up to eight tokens, and unpacking is what
 // bounds these products besides memory: 7 instructions of the half-rate pipe for eight codes. One token, 4096 x 4096: 3.7 us
-// (2.4 TB/s; a launch and three round trips to memory). 16 tokens, 8 of 128 experts of 2048 x 768, groups of 32: 63 us (3.5 TB/s;
-// without the arithmetic the two products take 30 and 23, without the loads 37 and 34).
+// (2.4 TB/s; a launch and three round trips to memory). 16 tokens, 8 of 128 experts of 2048 x 768, groups of 32: 66.9 us (3.3 TB/s;
+// measured before SwiGLU's output had two parts, at 63: without the arithmetic the two products take 30 and 23, without the loads 37 and 34).
 #include <algorithm>
 
 #include "common.cuh"
@@ -209,12 +209,14 @@ struct Unpack {
 };
 
 // tot += factor scale (codes - zero) x of TILES pieces of the same columns. b(q, t): the 8 bf16 values of x of this lane for
-// word q and column tile t; nx(q, t): minus the sums of x over the 32 elements of word q, of this lane's two columns. A group's sum
+// word q and column tile t, with SPLIT and `full` in tiles NT + t what is added to them; nx(q, t): minus the sums of x over the 32
+// elements of word q, of this lane's two columns. A group's sum
 // starts at -(16 + zero) sum x, which takes the codes' 16 and the zero point away without an instruction for each pair of
 // codes: terms of up to 31 |x| instead of 15 |x| in an fp32 sum. A group of several words has two sums, so that a product need
 // not wait for the one before it.
-template <int PER, int NT, int TILES, typename B, typename X>
-__device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&tot)[TILES][NT][4], float factor, const Unpack& unpack, const B& b, const X& nx) {
+template <int PER, int NT, int TILES, bool SPLIT, typename B, typename X>
+__device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&tot)[TILES][NT][4], float factor, const Unpack& unpack, const B& b, const X& nx,
+                                         bool full = false) {
   constexpr int RUN = 4 / PER, SUMS = RUN > 1 ? 2 : 1;  // words of a group, sums of a group
   float acc[TILES][SUMS][NT][4];
 #pragma unroll
@@ -244,9 +246,14 @@ __device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&t
         }
       }
     }
-    uint4 v[NT];
+    constexpr int XT = SPLIT ? 2 * NT : NT;
+    uint4 v[XT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) v[t] = b(q, t);
+    if (SPLIT && full) {
+#pragma unroll
+      for (int t = NT; t < XT; ++t) v[t] = b(q, t);
+    }
 #pragma unroll
     for (int h = 0; h < TILES; ++h) {
       uint32_t pg[4], ph[4];
@@ -256,6 +263,13 @@ __device__ __forceinline__ void multiply(const Piece<PER> (&w)[TILES], float (&t
       for (int t = 0; t < NT; ++t) {
         mma16816(acc[h][0][t], pg[0], ph[0], pg[1], ph[1], v[t].x, v[t].y);
         mma16816(acc[h][SUMS - 1][t], pg[2], ph[2], pg[3], ph[3], v[t].z, v[t].w);
+      }
+      if (SPLIT && full) {
+#pragma unroll
+        for (int t = NT; t < XT; ++t) {
+          mma16816(acc[h][0][t - NT], pg[0], ph[0], pg[1], ph[1], v[t].x, v[t].y);
+          mma16816(acc[h][SUMS - 1][t - NT], pg[2], ph[2], pg[3], ph[3], v[t].z, v[t].w);
+        }
       }
     }
     if (q % RUN == RUN - 1) {
@@ -291,6 +305,10 @@ __device__ __forceinline__ uint4 load_x(const bf16* row, int k, int K) {
   return v;
 }
 
+__device__ __forceinline__ float sum8(const uint4& v) {
+  return ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+}
+
 // Minus the sums of x over the 32 elements of a word, of this lane's two columns: a product with -1.
 __device__ __forceinline__ float2 minus_sums(const uint4& v) {
   float sum[4] = {0.f, 0.f, 0.f, 0.f};
@@ -310,6 +328,7 @@ struct W4Args {
   Packed w;
   void* out;
   long long ldo;
+  int pitch;               // SWIGLU: values of a row of the output
   bool y_bf16;
   bool early;              // ids are from before the kernel ahead, which only made x
 };
@@ -320,18 +339,25 @@ __device__ __forceinline__ void put_out(const W4Args& a, int slot, int row, floa
   if (a.y_bf16) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(v);
   else static_cast<float*>(a.out)[slot * a.ldo + row] = v;
 }
-// SwiGLU's output. Rows past h up to the pitch: their scales are 0.
+// SwiGLU's output, as a sum of two bf16 values (off by at most 2^-16 of it; one bf16 by 2^-8, which was most of the decode step's
+// error before its output is rounded): a row of the upper ones, then one of the lower. Rows past h up to the pitch: their scales are 0.
 __device__ __forceinline__ void put_swiglu(const W4Args& a, int slot, int row, float gate, float up) {
-  if (row < a.ldo) static_cast<bf16*>(a.out)[slot * a.ldo + row] = __float2bfloat16_rn(gate / (1.0f + expf(-gate)) * up);
+  if (row >= a.pitch) return;
+  const float v = gate / (1.0f + expf(-gate)) * up;
+  const bf16 hi = __float2bfloat16_rn(v);
+  bf16* o = static_cast<bf16*>(a.out) + slot * a.ldo + row;
+  o[0] = hi;
+  o[a.pitch] = __float2bfloat16_rn(v - __bfloat162float(hi));
 }
 
 // ------------------------------------------------------------------ one token
 // Block (tile, slot) owns 16 rows of the slot's matrix (with SWIGLU of both halves, gate and up). Its warps share the chunks of K, U
-// pieces (pairs of pieces) each on their way at once, and add up their sums in shared memory, in warp order.
-template <int PER, int WARPS, int U, bool SWIGLU, bool VEC>
+// pieces (pairs of pieces) each on their way at once, and add up their sums in shared memory, in warp order. SPLIT: x is a sum of two
+// rows, the second behind the first, which take the first two columns of the eight.
+template <int PER, int WARPS, int U, bool SWIGLU, bool SPLIT, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel(const W4Args a) {
-  constexpr int TILES = SWIGLU ? 2 : 1;
-  __shared__ uint4 xs[SEGMENT * 4][4];
+  constexpr int TILES = SWIGLU ? 2 : 1, PARTS = SPLIT ? 2 : 1;
+  __shared__ uint4 xs[SEGMENT * 4][PARTS * 4];
   __shared__ float xsum[SEGMENT * 4];  // minus the sums
   __shared__ float sums[WARPS][TILES][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tile = blockIdx.x, slot = blockIdx.y;
@@ -369,12 +395,15 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel
     __syncthreads();
     // Each thread eight elements, four threads the 32 of a sum; chunks * 16 is a multiple of 16, so whole groups of four
     for (int i = threadIdx.x; i < (chunks * 16 + 31 & ~31); i += WARPS * 32) {
-      uint4 v = make_uint4(0, 0, 0, 0);
+      float sum = 0.f;
       if (i < chunks * 16) {
-        v = load_x<VEC>(x, (seg0 * 16 + i) * 8, a.K);
-        xs[i >> 2][i & 3] = v;
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          const uint4 v = load_x<VEC>(x + part * a.K, (seg0 * 16 + i) * 8, a.K);
+          xs[i >> 2][part * 4 + (i & 3)] = v;
+          sum += sum8(v);
+        }
       }
-      float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
       if (i < chunks * 16 && (i & 3) == 0) xsum[i >> 2] = -sum;
@@ -386,18 +415,19 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel
       for (int u = 0; u < U; ++u) {
         if (c + u * WARPS >= chunks) break;
         const int s0 = (c + u * WARPS) * 4;
-        // column 0 of eight; the others' sums are not read
-        multiply<PER, 1, TILES>(p[u], tot, 1.0f, unpack, [&](int q, int) { return lane < 4 ? xs[s0 + q][lane] : make_uint4(0, 0, 0, 0); },
-                                [&](int q, int) { return make_float2(xsum[s0 + q], 0.f); });
+        // the first columns of eight; the others' sums are not read
+        multiply<PER, 1, TILES, false>(p[u], tot, 1.0f, unpack,
+                                       [&](int q, int) { return lane < PARTS * 4 ? xs[s0 + q][lane] : make_uint4(0, 0, 0, 0); },
+                                       [&](int q, int) { return make_float2(xsum[s0 + q], 0.f); });
       }
     }
   }
-  // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
+  // columns 0 and 1: registers 0 and 2, 1 and 3 of the lanes with (lane & 3) = 0
   if ((lane & 3) == 0) {
 #pragma unroll
     for (int h = 0; h < TILES; ++h) {
-      sums[warp][h][lane >> 2] = tot[h][0][0];
-      sums[warp][h][8 + (lane >> 2)] = tot[h][0][2];
+      sums[warp][h][lane >> 2] = SPLIT ? tot[h][0][0] + tot[h][0][1] : tot[h][0][0];
+      sums[warp][h][8 + (lane >> 2)] = SPLIT ? tot[h][0][2] + tot[h][0][3] : tot[h][0][2];
     }
   }
   __syncthreads();
@@ -425,9 +455,9 @@ struct StreamShape {
   int xchunks;  // chunks of x in shared memory
 };
 
-template <int PER, int NT, int WARPS, bool SWIGLU>
+template <int PER, int NT, int WARPS, bool SWIGLU, bool SPLIT>
 struct StreamSmem {
-  static constexpr int TILES = SWIGLU ? 2 : 1;
+  static constexpr int TILES = SWIGLU ? 2 : 1, XT = SPLIT ? 2 * NT : NT;  // XT: column tiles of x
   static constexpr int step = TILES * piece_bytes(PER);  // bytes of one ring slot
   static constexpr int depth = WARPS == 16 ? 2 : SWIGLU ? 3 : 4;  // slots of a warp's ring
   static constexpr int sum_floats = WARPS * TILES * NT * 128, buffers = WARPS == 16 ? 1 : 2;
@@ -435,7 +465,7 @@ struct StreamSmem {
   __host__ __device__ StreamSmem(const W4Args& a, const StreamShape& sh) {
     ring = 0;
     x = ring + WARPS * depth * step;
-    xsum = x + sh.xchunks * 4 * 8 * NT * 64;
+    xsum = x + sh.xchunks * 4 * 8 * XT * 64;
     sums = xsum + sh.xchunks * 4 * 8 * NT * 4;
     list = sums + buffers * sum_floats * 4;
     groups = list + (a.slots * 4 + 15) / 16 * 16;
@@ -450,13 +480,16 @@ struct StreamSmem {
   }
 };
 
-template <int PER, int NT, int WARPS, bool SWIGLU, bool VEC>
+// SPLIT: x is a sum of two rows, the second behind the first. The second rows take the other half of the columns where a group leaves
+// that free, and column tiles of their own where not, which is twice the matrix instructions (16 tokens, 8 of 128 experts: 66.9 us; 68.3
+// with tiles of their own for all, 65.0 without the second rows. 128 tokens, 8 of 64, whose groups are full: 145.8 and 134.6 without).
+template <int PER, int NT, int WARPS, bool SWIGLU, bool SPLIT, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_kernel(const W4Args a, const StreamShape sh) {
-  using Smem = StreamSmem<PER, NT, WARPS, SWIGLU>;
-  constexpr int TILES = Smem::TILES, BYTES = Piece<PER>::bytes, COLS = 8 * NT, STREAM_THREADS = WARPS * 32;
+  using Smem = StreamSmem<PER, NT, WARPS, SWIGLU, SPLIT>;
+  constexpr int TILES = Smem::TILES, BYTES = Piece<PER>::bytes, COLS = 8 * NT, XT = Smem::XT, STREAM_THREADS = WARPS * 32;
   extern __shared__ __align__(16) uint8_t smem[];
   const Smem at(a, sh);
-  uint4* xs = reinterpret_cast<uint4*>(smem + at.x);          // [chunks * 4][COLS][4]
+  uint4* xs = reinterpret_cast<uint4*>(smem + at.x);          // [chunks * 4][8 XT][4]
   float* xsum = reinterpret_cast<float*>(smem + at.xsum);     // [chunks * 4][COLS]: minus the sums
   int* list = reinterpret_cast<int*>(smem + at.list);         // slots, expert by expert
   int2* groups = reinterpret_cast<int2*>(smem + at.groups);   // expert, first slot in list | slots << 16
@@ -581,7 +614,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_ker
     }
     const int2 info = groups[group];
     const int first = info.y & 0xFFFF, rows = info.y >> 16;
-    const bool live = set * wts + wt < a.w.tiles;
+    const bool live = set * wts + wt < a.w.tiles, half = SPLIT && rows <= COLS / 2;
     float tot[TILES][NT][4];
 #pragma unroll
     for (int h = 0; h < TILES; ++h)
@@ -596,10 +629,16 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_ker
         // All columns, zeros where the group has fewer rows. A thread takes eight elements, four threads the 32 of a sum.
         for (int i = threadIdx.x; i < n * 16 * COLS; i += STREAM_THREADS) {
           const int col = i / (n * 16), k8 = i - col * (n * 16);
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (col < rows) v = load_x<VEC>(x + (list[first + col] / a.xdiv) * a.ldx, (seg0 * 16 + k8) * 8, a.K);
-          xs[((k8 >> 2) * COLS + col) * 4 + (k8 & 3)] = v;
-          float sum = ((bf16_lo(v.x) + bf16_hi(v.x)) + (bf16_lo(v.y) + bf16_hi(v.y))) + ((bf16_lo(v.z) + bf16_hi(v.z)) + (bf16_lo(v.w) + bf16_hi(v.w)));
+          float sum = 0.f;
+#pragma unroll
+          for (int part = 0; part < XT / NT; ++part) {
+            if (part == 1 && half) break;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            const int c = half ? col & (COLS / 2 - 1) : col;
+            if (c < rows) v = load_x<VEC>(x + (list[first + c] / a.xdiv) * a.ldx + (part == 1 || c != col ? a.K : 0), (seg0 * 16 + k8) * 8, a.K);
+            xs[((k8 >> 2) * 8 * XT + part * COLS + col) * 4 + (k8 & 3)] = v;
+            sum += sum8(v);
+          }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);  // the bound is a multiple of 32: whole warps
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
           if ((k8 & 3) == 0) xsum[(k8 >> 2) * COLS + col] = -sum;
@@ -611,9 +650,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_ker
       if (!live) continue;
       // chunks of this segment that are this warp's: those equal to wk modulo the warps that share K
       const int c0 = (wk - seg0) & (sh.wk - 1);
-      const uint4* xp = xs + c0 * 16 * COLS + lane;
+      const uint4* xp = xs + c0 * 128 * XT + lane;
       const float* sp = xsum + c0 * 4 * COLS + 2 * (lane & 3);
-      for (int c = c0; c < n; c += sh.wk, xp += sh.wk * 16 * COLS, sp += sh.wk * 4 * COLS) {
+      for (int c = c0; c < n; c += sh.wk, xp += sh.wk * 128 * XT, sp += sh.wk * 4 * COLS) {
         copy_wait<depth - 1>();  // younger groups of copies may be on their way
         __syncwarp();
         Piece<PER> p[TILES];
@@ -622,8 +661,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_ker
         __syncwarp();  // every lane has its part: the slot is free
         fill(ring + slot);
         slot = slot == (depth - 1) * Smem::step ? 0 : slot + Smem::step;
-        multiply<PER, NT, TILES>(p, tot, 1.0f, unpack, [&](int q, int t) { return xp[(q * NT + t) * 32]; },
-                                 [&](int q, int t) { return *reinterpret_cast<const float2*>(sp + (q * NT + t) * 8); });
+        const auto b = [&](int q, int t) { return xp[(q * XT + t) * 32]; };
+        const auto nx = [&](int q, int t) { return *reinterpret_cast<const float2*>(sp + (q * NT + t) * 8); };
+        multiply<PER, NT, TILES, SPLIT>(p, tot, 1.0f, unpack, b, nx, !half);
       }
     }
     // the sums of the warps: [warp][half][column tile][register][lane]
@@ -649,7 +689,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 16 ? 1 : 2) w4_stream_ker
 #pragma unroll
       for (int h = 0; h < TILES; ++h) {
         v[h] = 0.f;
-        for (int w = 0; w < sh.wk; ++w) v[h] += sums[((wt * sh.wk + w) * TILES + h) * NT * 128 + from];
+        for (int w = 0; w < sh.wk; ++w) {
+          const float* part = sums + ((wt * sh.wk + w) * TILES + h) * NT * 128 + from;
+          v[h] += half ? part[0] + part[NT == 1 ? 2 : 128] : part[0];  // half of the columns further
+        }
       }
       const int row = (set * wts + wt) * 16 + r, s = list[first + col];
       if constexpr (SWIGLU) put_swiglu(a, s, row, v[0], v[1]);
@@ -703,23 +746,23 @@ __global__ void __launch_bounds__(DOWN_WARPS * 32, 2) w4_down_token_kernel(const
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks, c = i % a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        v[u][q] = lane < 4 ? load_x<true>(x + static_cast<size_t>(t * a.top_k + j) * a.ldx, c * 128 + q * 32 + lane * 8, a.K)
+      for (int q = 0; q < 4; ++q)  // SwiGLU's upper values in column 0, the lower ones in column 1
+        v[u][q] = lane < 8 ? load_x<true>(x + static_cast<size_t>(t * a.top_k + j) * a.ldx + (lane >> 2) * a.K, c * 128 + q * 32 + (lane & 3) * 8, a.K)
                            : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * DOWN_WARPS, j = i / a.w.chunks;
       if (i >= items || expert[j] < 0) continue;
-      // the sums of x by a product with ones: column 0 of every row
-      multiply<PER, 1, 1>(p[u], tot, weight[j], unpack, [&](int q, int) { return v[u][q]; }, [&](int q, int) { return minus_sums(v[u][q]); });
+      // the sums of x by a product with ones: columns 0 and 1 of every row
+      multiply<PER, 1, 1, false>(p[u], tot, weight[j], unpack, [&](int q, int) { return v[u][q]; }, [&](int q, int) { return minus_sums(v[u][q]); });
     }
   }
   if (!waited) grid_wait();
-  // column 0: registers 0 and 2 of the lanes with (lane & 3) = 0
+  // columns 0 and 1: registers 0 and 2, 1 and 3 of the lanes with (lane & 3) = 0
   if ((lane & 3) == 0) {
-    sums[warp][0][lane >> 2] = tot[0][0][0];
-    sums[warp][1][lane >> 2] = tot[0][0][2];
+    sums[warp][0][lane >> 2] = tot[0][0][0] + tot[0][0][1];
+    sums[warp][1][lane >> 2] = tot[0][0][2] + tot[0][0][3];
   }
   __syncthreads();
   const int row = tile * 16 + threadIdx.x;
@@ -761,19 +804,19 @@ __global__ void __launch_bounds__(128) w4_combine_kernel(const float* y, long lo
 
 bool vec_x(const W4Args& a) { return a.K % 8 == 0 && a.ldx % 8 == 0 && aligned16(a.x); }
 
-template <int PER, int NT, bool SWIGLU>
+template <int PER, int NT, bool SWIGLU, bool SPLIT>
 cudaError_t launch_stream(const W4Args& a, cudaStream_t s) {
   constexpr int WARPS = NT == 1 ? 8 : 16;
-  using Smem = StreamSmem<PER, NT, WARPS, SWIGLU>;
+  using Smem = StreamSmem<PER, NT, WARPS, SWIGLU, SPLIT>;
   StreamShape sh;
   // Long rows are shared, three or four chunks a warp: with fewer the sums at the end of a task cost as much as its products, with more there are
   // too few tasks to share evenly. Short rows go to one warp each.
   sh.wk = a.w.chunks >= 24 ? 8 : a.w.chunks >= 12 ? 4 : 1;
   const int wts = WARPS / sh.wk;
   sh.sets = (a.w.tiles + wts - 1) / wts;
-  sh.xchunks = std::min(a.w.chunks, SWIGLU || NT == 2 ? 16 : 32);
+  sh.xchunks = std::min(a.w.chunks, SWIGLU || SPLIT || NT == 2 ? 16 : 32);
   const int smem = Smem(a, sh).total;
-  const auto kernel = vec_x(a) ? w4_stream_kernel<PER, NT, WARPS, SWIGLU, true> : w4_stream_kernel<PER, NT, WARPS, SWIGLU, false>;
+  const auto kernel = SPLIT || vec_x(a) ? w4_stream_kernel<PER, NT, WARPS, SWIGLU, SPLIT, true> : w4_stream_kernel<PER, NT, WARPS, SWIGLU, SPLIT, SPLIT>;
   const cudaError_t err = ensure_max_dynamic_smem(reinterpret_cast<const void*>(kernel), 220 * 1024);
   if (err != cudaSuccess) return err;
   const long long most = static_cast<long long>(Smem::most_groups(a)) * sh.sets;
@@ -781,25 +824,28 @@ cudaError_t launch_stream(const W4Args& a, cudaStream_t s) {
   return launch_dependent(kernel, blocks, WARPS * 32, smem, s, a, sh);
 }
 
-template <int PER, bool SWIGLU>
+template <int PER, bool SWIGLU, bool SPLIT>
 cudaError_t launch_product(const W4Args& a, cudaStream_t s) {
   // A single token: a block for each tile, which starts sooner than a list of tasks is made, with as many warps and loads that all
   // weights of a tile are on their way at once (up to K = 4096 with eight warps, 2048 of gate and up with four, of which three blocks
   // fit on an SM: 4096 x 4096: 5.6 us with two loads of four warps each, 4.5 so).
   if (a.slots == (a.ids == nullptr ? 1 : a.top_k)) {
     constexpr int WARPS = SWIGLU ? 4 : 8;
-    const auto kernel = vec_x(a) ? w4_slot_kernel<PER, WARPS, 4, SWIGLU, true> : w4_slot_kernel<PER, WARPS, 4, SWIGLU, false>;
+    const auto kernel = SPLIT || vec_x(a) ? w4_slot_kernel<PER, WARPS, 4, SWIGLU, SPLIT, true> : w4_slot_kernel<PER, WARPS, 4, SWIGLU, SPLIT, SPLIT>;
     return launch_dependent(kernel, dim3(a.w.tiles, a.slots), WARPS * 32, 0, s, a);
   }
   // Tokens of an expert, on average. With more than eight of them groups of 16 slots unpack its weights half as often, in one block of 16
   // warps, whose shared memory x fills (128 tokens, 8 of 64 experts of 2048 x 768: 133 us, 155 in groups of eight; with eight tokens
   // an expert both take 99 to 101, with four the larger groups 86 instead of 76).
   const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
-  return each <= 8 ? launch_stream<PER, 1, SWIGLU>(a, s) : launch_stream<PER, 2, SWIGLU>(a, s);
+  return each <= 8 ? launch_stream<PER, 1, SWIGLU, SPLIT>(a, s) : launch_stream<PER, 2, SWIGLU, SPLIT>(a, s);
 }
-template <bool SWIGLU>
+// SPLIT: x is a sum of two rows of K values, as put_swiglu() leaves them: 16-byte rows
+template <bool SWIGLU, bool SPLIT>
 cudaError_t launch_product(const W4Args& a, cudaStream_t s) {
-  return a.w.per == 4 ? launch_product<4, SWIGLU>(a, s) : a.w.per == 2 ? launch_product<2, SWIGLU>(a, s) : launch_product<1, SWIGLU>(a, s);
+  return a.w.per == 4   ? launch_product<4, SWIGLU, SPLIT>(a, s)
+         : a.w.per == 2 ? launch_product<2, SWIGLU, SPLIT>(a, s)
+                        : launch_product<1, SWIGLU, SPLIT>(a, s);
 }
 
 cudaError_t launch_down_token(const W4Args& a, int T, cudaStream_t s) {
@@ -824,7 +870,7 @@ size_t w4_weights_bytes(int matrices, int K, int N, int group) {
 size_t w4_decode_workspace_bytes(long long slots, int E, int d, int h) {
   if (slots < 0 || slots > MAX_SLOTS || !dim_ok(d) || !dim_ok(h)) return 0;
   // SwiGLU's rows, and the fp32 rows of the down product where it does not take token by token
-  return round256(static_cast<size_t>(slots) * pitch_of(h) * 2) + (down_by_token(slots, E) ? 0 : static_cast<size_t>(slots) * d * 4);
+  return round256(static_cast<size_t>(slots) * pitch_of(h) * 4) + (down_by_token(slots, E) ? 0 : static_cast<size_t>(slots) * d * 4);
 }
 
 }  // namespace moe
@@ -895,7 +941,7 @@ moe_status_t moe_w4_matvec(const moe_bf16* x, long long ldx, const int32_t* ids,
   a.out = y;
   a.ldo = ldy;
   a.y_bf16 = y_dtype == MOE_DTYPE_BF16;
-  const cudaError_t err = launch_product<false>(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t err = launch_product<false, false>(a, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? MOE_OK : cuda_fail(err);
 }
 
@@ -930,12 +976,13 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
   a.K = d;
   a.w = packed_at(w_ug, h, d, group);
   a.out = act;
-  a.ldo = pitch;
-  cudaError_t err = launch_product<true>(a, s);
+  a.ldo = 2 * pitch;
+  a.pitch = pitch;
+  cudaError_t err = launch_product<true, false>(a, s);
   if (err != cudaSuccess) return cuda_fail(err);
   W4Args b = a;
   b.x = act;
-  b.ldx = pitch;
+  b.ldx = 2 * pitch;
   b.weights = weights;
   b.xdiv = 1;
   b.N = d;
@@ -947,10 +994,10 @@ moe_status_t moe_w4_swiglu_decode(const moe_bf16* x, long long ldx, const int32_
     b.ldo = ldo;
     err = launch_down_token(b, T, s);
   } else {
-    float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(static_cast<size_t>(slots) * pitch * 2));
+    float* y = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + round256(static_cast<size_t>(slots) * pitch * 4));
     b.out = y;
     b.ldo = d;
-    err = launch_product<false>(b, s);
+    err = launch_product<false, true>(b, s);
     if (err == cudaSuccess)
       err = launch_dependent(w4_combine_kernel, dim3(std::min((d + 127) / 128, 64), T), 128, 0, s, static_cast<const float*>(y),
                              static_cast<long long>(d), ids, weights, top_k, E, d, reinterpret_cast<bf16*>(out), ldo);
