@@ -81,14 +81,14 @@ class MoEBlock:
     def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
         """x [T, d] bf16 (any row pitch) -> out [T, d] bf16. token_mask nullable [T] bool: padding tokens
         (False) are routed nowhere, count in no loss and pass through the residual unchanged. `loss`
-        holds the balance and the z loss, `counts` the slots per expert. x, gamma and w_router are not copied:
-        backward() reads them again and refuses when one was changed in place since."""
+        holds the balance and the z loss, `counts` the slots per expert. x and the weights, the experts' among them, are not
+        copied: backward() reads them again and refuses when one was changed in place since."""
         if not self.plain:
             return self._alone.forward(x, token_mask)
         T = self._check(x, token_mask)
         self._buffers(T)
-        self.x = x  # read again by backward(), like gamma and w_router
-        self._read = [(t, _version(t)) for t in (x, self.gamma, self.w_router)]
+        self.x = x  # read again by backward(), like the weights
+        self._read = [(t, _version(t)) for t in (x, *self.tensors().values())]
         self._ran = self
         _lib.moe_layer_norm_fwd(x, _dense(self.gamma), _dense(self.beta), T, self.d, self.eps, self.normed, self.mean, self.rstd)
         return x + self._route(token_mask)
@@ -138,7 +138,7 @@ class MoEBlock:
         if self._ran is not owner:
             raise RuntimeError("the block's buffers hold another run, by itself or in another stack")
         if any(_version(t) != v for t, v in self._read):
-            raise RuntimeError("x, gamma or w_router was changed in place since forward(): their gradients would be wrong")
+            raise RuntimeError("x or a weight was changed in place since forward(): the gradients would be wrong")
         if tuple(dout.shape) != (self._T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:
             raise ValueError(f"dout has to be [{self._T}, {self.d}] bfloat16 on {self.device}")
 
@@ -212,7 +212,7 @@ class MoEStack:
                 self._ys.append(y)
         self.x = x
         for b in self.blocks:
-            b._read = [(t, _version(t)) for n, t in b.tensors().items() if n not in ("w_ug", "w_down")]
+            b._read = [(t, _version(t)) for t in b.tensors().values()]
             b._ran = self
         self.blocks[0]._read.append((x, _version(x)))
         return r

@@ -1,0 +1,55 @@
+"""What a block's or a stack's backward needs of the run before it: the same weights, whole buffers."""
+import pytest
+import torch
+
+from ragged_grouped_gemm_device_gb300.block import MoEBlock, MoEStack
+from ragged_grouped_gemm_device_gb300.layer import ExpertLayer
+from ragged_grouped_gemm_device_gb300.optim import AdamW
+
+pytestmark = pytest.mark.gpu
+
+T, E, k, d, h = 24, 6, 2, 64, 40
+
+
+def _block(kind, seed=1):
+    g = torch.Generator("cuda").manual_seed(seed)
+    n = lambda *s, dtype=torch.float32: torch.randn(*s, generator=g, device="cuda").to(dtype)
+    experts = ExpertLayer(n(E, 2 * h, d, dtype=torch.bfloat16) / 8, n(E, h, d, dtype=torch.bfloat16) / 6)
+    gamma, w_router = 1 + 0.2 * n(d), n(E, d) / 8
+    if kind == "plain":
+        return MoEBlock(gamma, 0.1 * n(d), w_router, experts, k)
+    return MoEBlock(gamma, None, w_router, experts, k, pre="rms", post="layer", post_gamma=1 + 0.2 * n(d), post_beta=0.3 * n(d),
+                    gate=0.5 + 0.2 * n(d), res_scale=0.75, branch_scale=0.5)
+
+
+def _rows(seed=2, rows=T):
+    return torch.randn(rows, d, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").bfloat16()
+
+
+def _model(kind):
+    """(what has forward() and backward(), its blocks)"""
+    if kind == "stack":
+        blocks = [_block("plain"), _block("norms", 3)]
+        return MoEStack(blocks), blocks
+    block = _block(kind)
+    return block, [block]
+
+
+@pytest.mark.parametrize("kind", ["plain", "norms", "stack"])
+def test_experts_changed_before_the_backward(lib, kind):
+    """The backward multiplies by the experts' weights again: those of another step with this one's activations would give
+    gradients of no function."""
+    model, blocks = _model(kind)
+    x, dout = _rows(), _rows(5)
+    for b in blocks:
+        for w in (b.experts.w_ug, b.experts.w_down):
+            model.forward(x)
+            w.mul_(1.5)
+            with pytest.raises(RuntimeError, match="in place"):
+                model.backward(dout)
+            model.forward(x)
+            model.backward(dout)
+    model.forward(x)
+    AdamW([blocks[-1].experts.w_down]).step([torch.ones_like(blocks[-1].experts.w_down)])
+    with pytest.raises(RuntimeError, match="in place"):
+        model.backward(dout)
