@@ -87,11 +87,13 @@ class MoEBlock:
             return self._alone.forward(x, token_mask)
         T = self._check(x, token_mask)
         self._buffers(T)
+        self._ran = None  # until all of it has run: a call that raises leaves buffers of two runs
         self.x = x  # read again by backward(), like the weights
         self._read = [(t, _version(t)) for t in (x, *self.tensors().values())]
-        self._ran = self
         _lib.moe_layer_norm_fwd(x, _dense(self.gamma), _dense(self.beta), T, self.d, self.eps, self.normed, self.mean, self.rstd)
-        return x + self._route(token_mask)
+        out = x + self._route(token_mask)
+        self._ran = self
+        return out
 
     def _check(self, x, token_mask) -> int:
         if x.dim() != 2 or x.shape[1] != self.d or x.dtype != torch.bfloat16 or x.device != self.device:
@@ -136,7 +138,7 @@ class MoEBlock:
         if not isinstance(self.experts, ExpertLayer):
             raise TypeError("4-bit experts have no backward: train on an ExpertLayer")
         if self._ran is not owner:
-            raise RuntimeError("the block's buffers hold another run, by itself or in another stack")
+            raise RuntimeError("the block's buffers hold no whole run of this model: another one followed, or its forward() raised")
         if any(_version(t) != v for t, v in self._read):
             raise RuntimeError("x or a weight was changed in place since forward(): the gradients would be wrong")
         if tuple(dout.shape) != (self._T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:
@@ -198,6 +200,8 @@ class MoEStack:
         in place since."""
         T = self.blocks[0]._check(x, token_mask)
         self._buffers(T)
+        for b in self.blocks:
+            b._ran = None
         r, y = x, None
         self._ys = []
         for i in range(len(self.blocks) + 1):

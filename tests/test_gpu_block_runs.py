@@ -53,3 +53,17 @@ def test_experts_changed_before_the_backward(lib, kind):
     AdamW([blocks[-1].experts.w_down]).step([torch.ones_like(blocks[-1].experts.w_down)])
     with pytest.raises(RuntimeError, match="in place"):
         model.backward(dout)
+
+
+@pytest.mark.parametrize("kind", ["plain", "norms", "stack"])
+def test_a_forward_that_raises_leaves_no_run(lib, kind):
+    """A mask of a wrong type is found behind the first norm, whose rows and statistics are another run's then."""
+    model, _ = _model(kind)
+    x, dout = _rows(), _rows(5)
+    model.forward(x)
+    with pytest.raises(ValueError):
+        model.forward(_rows(6), torch.ones(T, device="cuda"))
+    with pytest.raises(RuntimeError, match="forward"):
+        model.backward(dout)
+    model.forward(x)
+    model.backward(dout)
