@@ -202,6 +202,8 @@ class MoEStack:
         self._buffers(T)
         for b in self.blocks:
             b._ran = None
+        if x.untyped_storage().data_ptr() == self.rows.untyped_storage().data_ptr():
+            x = x.clone()  # an earlier output: this forward writes there, and backward() reads x again
         r, y = x, None
         self._ys = []
         for i in range(len(self.blocks) + 1):

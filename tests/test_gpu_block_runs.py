@@ -67,3 +67,21 @@ def test_a_forward_that_raises_leaves_no_run(lib, kind):
         model.backward(dout)
     model.forward(x)
     model.backward(dout)
+
+
+@pytest.mark.parametrize("kind", ["norms", "stack"])
+def test_an_output_goes_in_again(lib, kind):
+    """A stack's output, whole or one row of it for all tokens, is the next input: forward and backward are
+    those of a copy of it."""
+    dout = _rows(5)
+    for take in (lambda r: r, lambda r: r[3:4].expand(T, d)):
+        results = []
+        for copy in (False, True):
+            model, _ = _model(kind)
+            x = take(model.forward(_rows()))
+            x = x.clone() if copy else x
+            out = model.forward(x).clone()
+            got = model.backward(dout)
+            blocks = got["blocks"] if kind == "stack" else [{n: t for n, t in got.items() if n != "dx"}]
+            results.append([out, got["dx"].clone()] + [b[n].clone() for b in blocks for n in sorted(b)])
+        assert all(torch.equal(a, b) for a, b in zip(*results))
