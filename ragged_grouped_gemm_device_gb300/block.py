@@ -221,6 +221,8 @@ class MoEStack:
             b._read = [(t, _version(t)) for t in b.tensors().values()]
             b._ran = self
         self.blocks[0]._read.append((x, _version(x)))
+        if not self.rows.is_inference():  # whoever holds an earlier output for a backward learns that it has changed
+            torch.autograd.graph.increment_version(self.rows)
         return r
 
     @torch.no_grad()

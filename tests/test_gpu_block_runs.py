@@ -85,3 +85,20 @@ def test_an_output_goes_in_again(lib, kind):
             blocks = got["blocks"] if kind == "stack" else [{n: t for n, t in got.items() if n != "dx"}]
             results.append([out, got["dx"].clone()] + [b[n].clone() for b in blocks for n in sorted(b)])
         assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("behind", ["plain", "norms", "stack"])
+def test_an_output_overwritten_before_the_next_models_backward(lib, behind):
+    """The rows that a second model holds as its input are the first one's buffer: when that runs again the second one's backward
+    would read other rows."""
+    first, _ = _model("norms")
+    second, _ = _model(behind)
+    dout = _rows(5)
+    second.forward(first.forward(_rows()))
+    second.backward(dout)
+    first.forward(_rows(6))
+    with pytest.raises(RuntimeError, match="in place"):
+        second.backward(dout)
+    with torch.inference_mode():
+        first.forward(_rows(7))
+    first.forward(_rows(7))
