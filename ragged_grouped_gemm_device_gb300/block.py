@@ -108,7 +108,9 @@ class MoEBlock:
         torch.mm(self.normed.float(), self.w_router.t(), out=self.logits)
         _lib.moe_gate_fwd(self.logits, token_mask, T, self.k, self.E, self.flags, self.ids, self.weights, self.lse,
                           self.counts, self.n_valid, self.prob_sum, self.loss, self.gate_ws)
-        return self.experts.forward(self.normed, self.ids, self.weights)
+        y = self.experts.forward(self.normed, self.ids, self.weights)
+        self._experts_run = getattr(self.experts, "runs", None)
+        return y
 
     def _route_backward(self, dy, d_loss) -> dict:
         """The gradient of self.normed, left in self.dnormed, and those of the router's and the experts' weights."""
@@ -139,6 +141,8 @@ class MoEBlock:
             raise TypeError("4-bit experts have no backward: train on an ExpertLayer")
         if self._ran is not owner:
             raise RuntimeError("the block's buffers hold no whole run of this model: another one followed, or its forward() raised")
+        if self._experts_run != self.experts.runs:
+            raise RuntimeError("the experts' buffers hold another run: their forward() was called by itself or by another block")
         if any(_version(t) != v for t, v in self._read):
             raise RuntimeError("x or a weight was changed in place since forward(): the gradients would be wrong")
         if tuple(dout.shape) != (self._T, self.d) or dout.dtype != torch.bfloat16 or dout.device != self.device:

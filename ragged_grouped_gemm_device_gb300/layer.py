@@ -38,6 +38,7 @@ class ExpertLayer:
         self.w_ug, self.w_down = w_ug.contiguous(), w_down.contiguous()
         self.device = w_ug.device
         self._key = None
+        self.runs = 0  # forwards begun: each one overwrites what the backward of the one before reads
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def _buffers(self, T: int, k: int):
@@ -72,6 +73,7 @@ class ExpertLayer:
     def forward(self, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, stream=None):
         """x [T, d] bf16, ids [T, k] int32, weights [T, k] fp32 -> out [T, d] bf16."""
         T, k = ids.shape
+        self.runs += 1
         with _on(stream):
             x, ids, weights = _dense(x), _dense(ids), _dense(weights)
             self._buffers(T, k)

@@ -102,3 +102,21 @@ def test_an_output_overwritten_before_the_next_models_backward(lib, behind):
     with torch.inference_mode():
         first.forward(_rows(7))
     first.forward(_rows(7))
+
+
+@pytest.mark.parametrize("kind", ["plain", "norms", "stack"])
+def test_experts_that_ran_for_someone_else(lib, kind):
+    """The experts' buffers hold their last run: by itself, or for another block that shares them."""
+    model, blocks = _model(kind)
+    x, dout = _rows(), _rows(5)
+    b = blocks[-1]
+    other = MoEBlock(b.gamma.clone(), torch.zeros_like(b.gamma), b.w_router.clone(), b.experts, k)
+    for use in (lambda: b.experts.forward(_rows(8, 7), *(torch.zeros(7, 1, dtype=t, device="cuda") for t in (torch.int32, torch.float32))),
+                lambda: other.forward(_rows(8))):
+        model.forward(x)
+        use()
+        with pytest.raises(RuntimeError, match="experts"):
+            model.backward(dout)
+        model.forward(x)
+        model.backward(dout)
+        model.backward(dout)
