@@ -26,6 +26,8 @@ import torch
 from . import _lib
 from .layer import ExpertLayer, _dense
 
+_ITSELF = "itself"  # who asked for a plain block's last run
+
 _NORMS = {"none": _lib.NORM_NONE, "layer": _lib.NORM_LAYER, "rms": _lib.NORM_RMS}
 
 
@@ -60,7 +62,7 @@ class MoEBlock:
         self.flags = _lib.GATE_RENORM if renorm else 0
         self.device = w_router.device
         self._T = self._ran = None
-        self._alone = None if self.plain else MoEStack([self])
+        self._joins = None if self.plain else _Joins()
 
     def _buffers(self, T: int):
         if self._T == T:
@@ -84,7 +86,7 @@ class MoEBlock:
         holds the balance and the z loss, `counts` the slots per expert. x and the weights, the experts' among them, are not
         copied: backward() reads them again and refuses when one was changed in place since."""
         if not self.plain:
-            return self._alone.forward(x, token_mask)
+            return self._joins.forward([self], x, token_mask)
         T = self._check(x, token_mask)
         self._buffers(T)
         self._ran = None  # until all of it has run: a call that raises leaves buffers of two runs
@@ -92,7 +94,7 @@ class MoEBlock:
         self._read = [(t, _version(t)) for t in (x, *self.tensors().values())]
         _lib.moe_layer_norm_fwd(x, _dense(self.gamma), _dense(self.beta), T, self.d, self.eps, self.normed, self.mean, self.rstd)
         out = x + self._route(token_mask)
-        self._ran = self
+        self._ran = _ITSELF
         return out
 
     def _check(self, x, token_mask) -> int:
@@ -126,9 +128,9 @@ class MoEBlock:
         """dout [T, d] bf16, d_loss nullable [2] fp32 (the gradients of the two losses) -> the gradients
         dx (bf16), gamma, beta, w_router, w_ug, w_down (fp32) of the last forward."""
         if not self.plain:
-            grads = self._alone.backward(dout, None if d_loss is None else [d_loss])
+            grads = self._joins.backward([self], dout, None if d_loss is None else [d_loss])
             return dict(dx=grads["dx"], **grads["blocks"][0])
-        self._check_backward(dout, self)
+        self._check_backward(dout, _ITSELF)
         T = self._T
         dout = _dense(dout)
         grads = self._route_backward(dout, d_loss)
@@ -157,6 +159,96 @@ class MoEBlock:
         return {n: t for n, t in every.items() if t is not None}
 
 
+class _Joins:
+    """The joins of a run through blocks, and their buffers. It holds no block, whose memory would wait for the garbage
+    collector if the block held it."""
+
+    def __init__(self):
+        self._T = None
+
+    def _buffers(self, blocks, T: int):
+        for b in blocks:
+            b._buffers(T)
+        if self._T == T:
+            return
+        d, dev, count = blocks[0].d, blocks[0].device, len(blocks)
+        new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
+        self.rows = new(count, T, d, dtype=torch.bfloat16)       # r behind each block
+        self.stats = new(count + 1, 4, T)                        # of join i, the one in front of block i
+        self.dx, self.dy = new(T, d, dtype=torch.bfloat16), new(T, d, dtype=torch.bfloat16)
+        self.ws = new(max(1, _lib.moe_workspace_bytes(_lib.OP_RESIDUAL_NORM_BWD, T, 1, 1, d)), dtype=torch.uint8)
+        self._T = T
+
+    @staticmethod
+    def _join(blocks, i):
+        """The weights of join i, between blocks i - 1 and i: (post, gamma, beta, gate, pre, gamma, beta), then eps and scales."""
+        behind = blocks[i - 1] if i > 0 else None
+        ahead = blocks[i] if i < len(blocks) else None
+        dense = lambda b, n: None if b is None or getattr(b, n) is None else _dense(getattr(b, n))  # noqa: E731
+        weights = (_NORMS[behind.post] if behind else _lib.NORM_NONE, dense(behind, "post_gamma"), dense(behind, "post_beta"),
+                   dense(behind, "gate"), _NORMS[ahead.pre] if ahead else _lib.NORM_NONE, dense(ahead, "gamma"), dense(ahead, "beta"))
+        return weights, (ahead or behind).eps, (behind.res_scale, behind.branch_scale) if behind else (1.0, 1.0)
+
+    @torch.no_grad()
+    def forward(self, blocks, x: torch.Tensor, token_mask: torch.Tensor) -> torch.Tensor:
+        T, d = blocks[0]._check(x, token_mask), blocks[0].d
+        self._buffers(blocks, T)
+        for b in blocks:
+            b._ran = None
+        if x.untyped_storage().data_ptr() == self.rows.untyped_storage().data_ptr():
+            x = x.clone()  # an earlier output: this forward writes there, and backward() reads x again
+        r, y = x, None
+        self._ys = []
+        for i in range(len(blocks) + 1):
+            weights, eps, scales = self._join(blocks, i)
+            n = blocks[i].normed if i < len(blocks) else None
+            to = self.rows[i - 1] if i > 0 else None
+            _lib.moe_residual_norm_fwd(r, y, *weights, T, d, eps, *scales, to, n, self.stats[i])
+            if i > 0:
+                r = to
+            if n is not None:
+                y = blocks[i]._route(token_mask)
+                self._ys.append(y)
+        self.x = x
+        for b in blocks:
+            b._read = [(t, _version(t)) for t in b.tensors().values()]
+            b._ran = self
+        blocks[0]._read.append((x, _version(x)))
+        if not self.rows.is_inference():  # whoever holds an earlier output for a backward learns that it has changed
+            torch.autograd.graph.increment_version(self.rows)
+        return r
+
+    @torch.no_grad()
+    def backward(self, blocks, dout: torch.Tensor, d_loss) -> dict:
+        if self._T is None:
+            raise RuntimeError("backward() before forward()")
+        for b in blocks:
+            b._check_backward(dout, self)
+        count, T, d = len(blocks), self._T, blocks[0].d
+        losses = [None] * count if d_loss is None else list(d_loss)
+        if len(losses) != count:
+            raise ValueError("d_loss has to have one entry for each block")
+        grads = [{} for _ in blocks]
+        new = lambda: torch.empty(d, dtype=torch.float32, device=dout.device)  # noqa: E731
+        dr, dn = _dense(dout), None
+        for i in range(count, -1, -1):
+            weights, _, scales = self._join(blocks, i)
+            out = [None] * 5   # d_post_gamma, d_post_beta, d_gate, d_pre_gamma, d_pre_beta
+            for j, (w, owner, name) in enumerate(zip(weights[1:4] + weights[5:], (i - 1,) * 3 + (i,) * 2,
+                                                     ("post_gamma", "post_beta", "gate", "gamma", "beta"))):
+                if w is not None:
+                    out[j] = grads[owner][name] = new()
+            r = None if dn is None else self.rows[i - 1] if i > 0 else self.x
+            y, dy = (self._ys[i - 1], self.dy) if i > 0 else (None, None)
+            _lib.moe_residual_norm_bwd(dn, dr, r, y, *weights[:5], weights[5], self.stats[i], T, d, *scales, self.dx, dy,
+                                       *out, self.ws)
+            dr = self.dx
+            if i > 0:
+                grads[i - 1].update(blocks[i - 1]._route_backward(self.dy, losses[i - 1]))
+                dn = blocks[i - 1].dnormed
+        return dict(dx=self.dx, blocks=grads)
+
+
 class MoEStack:
     """Blocks of one width, one behind the other: the norm behind a block, its gate and scales, the residual addition and the
     norm in front of the next block are one call. Every block has experts of its own."""
@@ -173,90 +265,15 @@ class MoEStack:
         # a join has one eps for the norms on both its sides
         if any(a.post != "none" and a.eps != b.eps for a, b in zip(self.blocks, self.blocks[1:])):
             raise ValueError("a block with a norm behind it has to have the eps of the next block")
-        self.d, self._T = first.d, None
+        self.d, self._joins = first.d, _Joins()
 
-    def _buffers(self, T: int):
-        for b in self.blocks:
-            b._buffers(T)
-        if self._T == T:
-            return
-        d, dev, count = self.d, self.blocks[0].device, len(self.blocks)
-        new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
-        self.rows = new(count, T, d, dtype=torch.bfloat16)       # r behind each block
-        self.stats = new(count + 1, 4, T)                        # of join i, the one in front of block i
-        self.dx, self.dy = new(T, d, dtype=torch.bfloat16), new(T, d, dtype=torch.bfloat16)
-        self.ws = new(max(1, _lib.moe_workspace_bytes(_lib.OP_RESIDUAL_NORM_BWD, T, 1, 1, d)), dtype=torch.uint8)
-        self._T = T
-
-    def _join(self, i):
-        """The weights of join i, between blocks i - 1 and i: (post, gamma, beta, gate, pre, gamma, beta), then eps and scales."""
-        behind = self.blocks[i - 1] if i > 0 else None
-        ahead = self.blocks[i] if i < len(self.blocks) else None
-        dense = lambda b, n: None if b is None or getattr(b, n) is None else _dense(getattr(b, n))  # noqa: E731
-        weights = (_NORMS[behind.post] if behind else _lib.NORM_NONE, dense(behind, "post_gamma"), dense(behind, "post_beta"),
-                   dense(behind, "gate"), _NORMS[ahead.pre] if ahead else _lib.NORM_NONE, dense(ahead, "gamma"), dense(ahead, "beta"))
-        return weights, (ahead or behind).eps, (behind.res_scale, behind.branch_scale) if behind else (1.0, 1.0)
-
-    @torch.no_grad()
     def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
         """x [T, d] bf16 (any row pitch) -> out [T, d] bf16, a buffer that the next forward overwrites. The blocks hold
         their losses and counts. x and the weights are not copied: backward() reads them again and refuses when one was changed
         in place since."""
-        T = self.blocks[0]._check(x, token_mask)
-        self._buffers(T)
-        for b in self.blocks:
-            b._ran = None
-        if x.untyped_storage().data_ptr() == self.rows.untyped_storage().data_ptr():
-            x = x.clone()  # an earlier output: this forward writes there, and backward() reads x again
-        r, y = x, None
-        self._ys = []
-        for i in range(len(self.blocks) + 1):
-            weights, eps, scales = self._join(i)
-            n = self.blocks[i].normed if i < len(self.blocks) else None
-            to = self.rows[i - 1] if i > 0 else None
-            _lib.moe_residual_norm_fwd(r, y, *weights, T, self.d, eps, *scales, to, n, self.stats[i])
-            if i > 0:
-                r = to
-            if n is not None:
-                y = self.blocks[i]._route(token_mask)
-                self._ys.append(y)
-        self.x = x
-        for b in self.blocks:
-            b._read = [(t, _version(t)) for t in b.tensors().values()]
-            b._ran = self
-        self.blocks[0]._read.append((x, _version(x)))
-        if not self.rows.is_inference():  # whoever holds an earlier output for a backward learns that it has changed
-            torch.autograd.graph.increment_version(self.rows)
-        return r
+        return self._joins.forward(self.blocks, x, token_mask)
 
-    @torch.no_grad()
     def backward(self, dout: torch.Tensor, d_loss=None) -> dict:
         """dout [T, d] bf16, d_loss: None or for each block None or [2] fp32 -> dx (bf16) and blocks, a list of each
         block's gradients by the names of its tensors(); dx is a buffer that the next backward overwrites."""
-        if self._T is None:
-            raise RuntimeError("backward() before forward()")
-        for b in self.blocks:
-            b._check_backward(dout, self)
-        count, T = len(self.blocks), self._T
-        losses = [None] * count if d_loss is None else list(d_loss)
-        if len(losses) != count:
-            raise ValueError("d_loss has to have one entry for each block")
-        grads = [{} for _ in self.blocks]
-        new = lambda: torch.empty(self.d, dtype=torch.float32, device=dout.device)  # noqa: E731
-        dr, dn = _dense(dout), None
-        for i in range(count, -1, -1):
-            weights, _, scales = self._join(i)
-            out = [None] * 5   # d_post_gamma, d_post_beta, d_gate, d_pre_gamma, d_pre_beta
-            for j, (w, owner, name) in enumerate(zip(weights[1:4] + weights[5:], (i - 1,) * 3 + (i,) * 2,
-                                                     ("post_gamma", "post_beta", "gate", "gamma", "beta"))):
-                if w is not None:
-                    out[j] = grads[owner][name] = new()
-            r = None if dn is None else self.rows[i - 1] if i > 0 else self.x
-            y, dy = (self._ys[i - 1], self.dy) if i > 0 else (None, None)
-            _lib.moe_residual_norm_bwd(dn, dr, r, y, *weights[:5], weights[5], self.stats[i], T, self.d, *scales, self.dx, dy,
-                                       *out, self.ws)
-            dr = self.dx
-            if i > 0:
-                grads[i - 1].update(self.blocks[i - 1]._route_backward(self.dy, losses[i - 1]))
-                dn = self.blocks[i - 1].dnormed
-        return dict(dx=self.dx, blocks=grads)
+        return self._joins.backward(self.blocks, dout, d_loss)
