@@ -82,7 +82,9 @@ class MoEBlock:
     @torch.no_grad()
     def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
         """x [T, d] bf16 (any row pitch) -> out [T, d] bf16. token_mask nullable [T] bool: padding tokens
-        (False) are routed nowhere, count in no loss and pass through the residual unchanged. `loss`
+        (False) are routed nowhere and count in no loss; their y is a row of zeros, and out is what the formula makes of
+        it: x, with scales and a norm behind the block res_scale x + branch_scale gate post(0), where a layer norm's post(0)
+        is post_beta. They have a share in the gradients of post_beta and of the gate there unless dout is 0 in their rows. `loss`
         holds the balance and the z loss, `counts` the slots per expert. x and the weights, the experts' among them, are not
         copied: backward() reads them again and refuses when one was changed in place since."""
         if not self.plain:
@@ -268,7 +270,8 @@ class MoEStack:
         self.d, self._joins = first.d, _Joins()
 
     def forward(self, x: torch.Tensor, token_mask: torch.Tensor = None) -> torch.Tensor:
-        """x [T, d] bf16 (any row pitch) -> out [T, d] bf16, a buffer that the next forward overwrites. The blocks hold
+        """x [T, d] bf16 (any row pitch) -> out [T, d] bf16, a buffer that the next forward overwrites. token_mask as in
+        MoEBlock.forward: a padding token's rows take part in no block's experts or losses, but in its joins. The blocks hold
         their losses and counts. x and the weights are not copied: backward() reads them again and refuses when one was changed
         in place since."""
         return self._joins.forward(self.blocks, x, token_mask)
