@@ -13,8 +13,12 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
+#include <cstdint>
 #include <exception>
+#include <utility>
+#include <vector>
 
 #include "../../include/moe_gg.h"
 
@@ -570,7 +574,7 @@ PyObject* adamw_step(ARGS) {
 }
 
 // adamw_pointers(tensors, device, params, copies, grads): what AdamW.step writes into its table, with its checks; the parameters' and
-// copies' versions are counted up.
+// copies' versions are counted up. Overlaps are looked for when something has moved: a sort of all addresses takes as long as the rest.
 PyObject* adamw_pointers(ARGS) {
   COLLECT("adamw_pointers", 5, "tensors", "device", "params", "copies", "grads");
   Table t;
@@ -589,10 +593,13 @@ PyObject* adamw_pointers(ARGS) {
     PyErr_Format(PyExc_ValueError, "%s has to be a dense bfloat16 or float32 tensor on cuda:%d", what, device);
     return false;
   };
+  bool moved = false;
   for (int i = 0; i < t.count(); ++i) {
     const at::Tensor* g = tensor(PySequence_Fast_GET_ITEM(lists[2], i));
     const at::Tensor* p = tensor(PySequence_Fast_GET_ITEM(lists[0], i));
-    if (g == nullptr || p == nullptr || !dense(*g, "a gradient")) return nullptr;
+    PyObject* copy = PySequence_Fast_GET_ITEM(lists[1], i);
+    const at::Tensor* c = copy == Py_None ? nullptr : tensor(copy);
+    if (g == nullptr || p == nullptr || (copy != Py_None && c == nullptr) || !dense(*g, "a gradient")) return nullptr;
     moe_adamw_tensor_t& q = t.data()[i];
     if (g->numel() != q.n) {
       PyErr_Format(PyExc_ValueError, "a gradient has %lld elements, its parameter %lld", (long long)g->numel(), q.n);
@@ -602,6 +609,32 @@ PyObject* adamw_pointers(ARGS) {
     if (p->numel() != q.n || (p->scalar_type() == at::kFloat ? MOE_DTYPE_F32 : MOE_DTYPE_BF16) != q.p_dtype) {
       PyErr_SetString(PyExc_ValueError, "a parameter's size or type has changed");
       return nullptr;
+    }
+    if (c != nullptr) {
+      if (!dense(*c, "a copy")) return nullptr;
+      if (c->numel() != q.n || c->scalar_type() != at::kBFloat16) {
+        PyErr_SetString(PyExc_ValueError, "a copy's size or type has changed");
+        return nullptr;
+      }
+    }
+    moved |= p->const_data_ptr() != q.p || (c == nullptr ? nullptr : c->const_data_ptr()) != q.copy;
+  }
+  if (moved) {
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+    for (int k = 0; k < 2; ++k)
+      for (int i = 0; i < t.count(); ++i) {
+        PyObject* o = PySequence_Fast_GET_ITEM(lists[k], i);
+        if (o == Py_None) continue;
+        const at::Tensor& x = THPVariable_Unpack(o);
+        const uintptr_t at = reinterpret_cast<uintptr_t>(x.const_data_ptr());
+        if (x.numel() > 0) spans.emplace_back(at, at + x.numel() * x.element_size());
+      }
+    std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i) {
+      if (spans[i - 1].second > spans[i].first) {
+        PyErr_SetString(PyExc_ValueError, "parameters and copies may not overlap: a step would update the shared elements twice");
+        return nullptr;
+      }
     }
   }
   for (int i = 0; i < t.count(); ++i) {

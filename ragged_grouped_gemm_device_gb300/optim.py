@@ -23,16 +23,32 @@ def _dense(t, device, what):
         raise ValueError(f"{what} has to be a dense bfloat16 or float32 tensor on cuda:{device}")
 
 
+def _apart(tensors):
+    """A step would update elements that two tensors share twice."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t is not None and t.numel())
+    if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+        raise ValueError("parameters and copies may not overlap: a step would update the shared elements twice")
+
+
 def _pointers(table, device, params, copies, grads):
-    """Write where a step's tensors lie into the table (at every step: an assignment to .data moves a parameter) and count their
-    versions up. The extension's adamw_pointers does the same."""
-    for q, p, g in zip(table, params, grads):
+    """Write where a step's tensors lie into the table (at every step: an assignment to .data moves a parameter or a copy) and count
+    their versions up. What has moved is checked like what the constructor was given. The extension's adamw_pointers does the
+    same."""
+    moved = False
+    for q, p, c, g in zip(table, params, copies, grads):
         _dense(g, device, "a gradient")
         if g.numel() != q.n:
             raise ValueError(f"a gradient has {g.numel()} elements, its parameter {q.n}")
         _dense(p, device, "a parameter")
         if p.numel() != q.n or _lib._dtype(p) != q.p_dtype:
             raise ValueError("a parameter's size or type has changed")
+        if c is not None:
+            _dense(c, device, "a copy")
+            if c.numel() != q.n or c.dtype != torch.bfloat16:
+                raise ValueError("a copy's size or type has changed")
+        moved |= p.data_ptr() != (q.p or 0) or (0 if c is None else c.data_ptr()) != (q.copy or 0)
+    if moved:
+        _apart((*params, *copies))
     for q, p, c, g in zip(table, params, copies, grads):
         q.g, q.g_dtype, q.p, q.copy = g.data_ptr(), _lib._dtype(g), p.data_ptr(), None if c is None else c.data_ptr()
     torch.autograd.graph.increment_version([t for t in (*params, *copies) if t is not None and not t.is_inference()])
@@ -66,9 +82,7 @@ class AdamW:
                 raise ValueError("a copy has to be bfloat16, of the shape of its float32 parameter")
             if c is not None:
                 _dense(c, self.device.index, "a copy")
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (*params, *copies) if t is not None and t.numel())
-        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
-            raise ValueError("parameters and copies may not overlap: a step would update the shared elements twice")
+        _apart((*params, *copies))
         if max_norm is not None and not 0 < max_norm < float("inf"):
             raise ValueError("max_norm has to be positive and finite")
         self.params, self.copies, self.state_bits = params, copies, state_bits
