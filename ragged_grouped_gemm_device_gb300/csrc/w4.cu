@@ -351,12 +351,12 @@ __device__ __forceinline__ void put_swiglu(const W4Args& a, int slot, int row, f
 }
 
 // ------------------------------------------------------------------ one token
-// Block (tile, slot) owns 16 rows of the slot's matrix (with SWIGLU of both halves, gate and up). Its warps share the chunks of K, U
-// pieces (pairs of pieces) each on their way at once, and add up their sums in shared memory, in warp order. SPLIT: x is a sum of two
+// Block (tile, slot) owns 16 rows of the slot's matrix (with SWIGLU of both halves, gate and up). Its warps share the chunks of a
+// segment, U pieces (pairs of pieces) each, which are on their way at once, and add up their sums in shared memory, in warp order. SPLIT: x is a sum of two
 // rows, the second behind the first, which take the first two columns of the eight.
-template <int PER, int WARPS, int U, bool SWIGLU, bool SPLIT, bool VEC>
+template <int PER, int WARPS, bool SWIGLU, bool SPLIT, bool VEC>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel(const W4Args a) {
-  constexpr int TILES = SWIGLU ? 2 : 1, PARTS = SPLIT ? 2 : 1;
+  constexpr int U = SEGMENT / WARPS, TILES = SWIGLU ? 2 : 1, PARTS = SPLIT ? 2 : 1;
   __shared__ uint4 xs[SEGMENT * 4][PARTS * 4];
   __shared__ float xsum[SEGMENT * 4];  // minus the sums
   __shared__ float sums[WARPS][TILES][16];
@@ -382,15 +382,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel
   for (int seg0 = 0; seg0 < a.w.chunks; seg0 += SEGMENT) {
     const int chunks = min(SEGMENT, a.w.chunks - seg0);
     Piece<PER> p[U][TILES];
-    const auto load = [&](int c) {
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (c + u * WARPS < chunks) {
+    for (int u = 0; u < U; ++u)  // on their way while x comes
+      if (warp + u * WARPS < chunks) {
 #pragma unroll
-          for (int h = 0; h < TILES; ++h) p[u][h].load(piece0[h] + static_cast<size_t>(seg0 + c + u * WARPS) * Piece<PER>::bytes, lane);
-        }
-    };
-    load(warp);  // on their way while x comes
+        for (int h = 0; h < TILES; ++h) p[u][h].load(piece0[h] + static_cast<size_t>(seg0 + warp + u * WARPS) * Piece<PER>::bytes, lane);
+      }
     if (a.early && seg0 == 0) grid_wait();
     __syncthreads();
     // Each thread eight elements, four threads the 32 of a sum; chunks * 16 is a multiple of 16, so whole groups of four
@@ -409,17 +406,14 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel
       if (i < chunks * 16 && (i & 3) == 0) xsum[i >> 2] = -sum;
     }
     __syncthreads();
-    for (int c = warp; c < chunks; c += WARPS * U) {
-      if (c != warp) load(c);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (c + u * WARPS >= chunks) break;
-        const int s0 = (c + u * WARPS) * 4;
-        // the first columns of eight; the others' sums are not read
-        multiply<PER, 1, TILES, false>(p[u], tot, 1.0f, unpack,
-                                       [&](int q, int) { return lane < PARTS * 4 ? xs[s0 + q][lane] : make_uint4(0, 0, 0, 0); },
-                                       [&](int q, int) { return make_float2(xsum[s0 + q], 0.f); });
-      }
+    for (int u = 0; u < U; ++u) {
+      if (warp + u * WARPS >= chunks) break;
+      const int s0 = (warp + u * WARPS) * 4;
+      // the first columns of eight; the others' sums are not read
+      multiply<PER, 1, TILES, false>(p[u], tot, 1.0f, unpack,
+                                     [&](int q, int) { return lane < PARTS * 4 ? xs[s0 + q][lane] : make_uint4(0, 0, 0, 0); },
+                                     [&](int q, int) { return make_float2(xsum[s0 + q], 0.f); });
     }
   }
   // columns 0 and 1: registers 0 and 2, 1 and 3 of the lanes with (lane & 3) = 0
@@ -826,12 +820,13 @@ cudaError_t launch_stream(const W4Args& a, cudaStream_t s) {
 
 template <int PER, bool SWIGLU, bool SPLIT>
 cudaError_t launch_product(const W4Args& a, cudaStream_t s) {
-  // A single token: a block for each tile, which starts sooner than a list of tasks is made, with as many warps and loads that all
-  // weights of a tile are on their way at once (up to K = 4096 with eight warps, 2048 of gate and up with four, of which three blocks
-  // fit on an SM: 4096 x 4096: 5.6 us with two loads of four warps each, 4.5 so).
+  // A single token: a block for each tile, which starts sooner than a list of tasks is made. All weights of a tile's segment of 2048
+  // elements are on their way at once: two pieces for each of eight warps, four pairs for each of four warps of gate and up, of which three
+  // blocks fit on an SM (4096 x 4096: 5.6 us with four warps of two pieces, 3.9 so, with the second segment's weights a second
+  // round trip to memory).
   if (a.slots == (a.ids == nullptr ? 1 : a.top_k)) {
     constexpr int WARPS = SWIGLU ? 4 : 8;
-    const auto kernel = SPLIT || vec_x(a) ? w4_slot_kernel<PER, WARPS, 4, SWIGLU, SPLIT, true> : w4_slot_kernel<PER, WARPS, 4, SWIGLU, SPLIT, SPLIT>;
+    const auto kernel = SPLIT || vec_x(a) ? w4_slot_kernel<PER, WARPS, SWIGLU, SPLIT, true> : w4_slot_kernel<PER, WARPS, SWIGLU, SPLIT, SPLIT>;
     return launch_dependent(kernel, dim3(a.w.tiles, a.slots), WARPS * 32, 0, s, a);
   }
   // Tokens of an expert, on average. With more than eight of them groups of 16 slots unpack its weights half as often, in one block of 16
