@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "root.cuh"
 #include "rows.cuh"
 #include "trace.h"
 
@@ -206,7 +207,8 @@ __device__ __forceinline__ uint32_t to_e4m3(const float (&x)[VB], const uint32_t
       }
     }
   };
-  // 2^-s 2^-120 is an fp32 (subnormal from s = 7 on) up to s = 29; states above 2^38 take the two steps apart
+  // 2^-s 2^-120 is an fp32 (subnormal from s = 7 on) up to s = 29; blocks from s = 24 on, whose largest state is above 224 * 2^24, take
+  // the two steps apart
   const float inv = __uint_as_float((254u - byte) << 23);
   if (byte <= 150) {
     const float down = inv * E4M3_DOWN;
@@ -227,16 +229,6 @@ struct StepArgs {
   bool last;        // the call's last launch counts the step
 };
 
-// The square root of a value in [2^-126, inf): an estimate s from the reciprocal root y, and Newton's step s + (v - s^2) y / 2 with
-// the residual from a fused product. It equals sqrtf for every mantissa and both parities of the exponent (compared for all 2^24 of
-// them) as long as the residual is a normal number, v from 2^-80 on; below that it is within a unit. It takes a quarter of
-// sqrtf's instructions.
-__device__ __forceinline__ float sqrt_normal(float v) {
-  float y;
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-  const float s = __fmul_rn(v, y);
-  return __fmaf_rn(__fmaf_rn(-s, s, v), 0.5f * y, s);
-}
 // to two units; 0 beyond 2^126
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
