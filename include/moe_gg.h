@@ -629,7 +629,7 @@ moe_status_t moe_residual_norm_bwd(const void* dn, long long lddn, const void* d
  *   tensor may not be updated by two calls at a time. An eps above 0 counts as 2^-126 at least.
  * moe_grad_norm: norm[0] = sqrt(sum of all g^2), norm[1] = min(1, max_norm / norm[0]) (NaN where norm[0] is not
  * finite): a grad_scale that clips. Summed in a fixed order, in fp64 over pieces of 4096 summed in fp32 (where a
- * piece's sum of squares passes 2^128, the norm is not finite); reads
+ * piece's sum of squares passes 2^128, the norm is not finite; squares below 2^-149 count as 0); reads
  * only g, g_dtype and n of the descriptors. ws: moe_workspace_bytes(MOE_OP_GRAD_NORM, 0, 1, 1, 0, 0, 0) bytes.
  * Pointers are aligned to their element size. Elements in all: below 2^43.
  */
@@ -657,7 +657,8 @@ moe_status_t moe_adamw_step(const moe_adamw_tensor_t* tensors, int count, int st
  * 4-bit integer weights with group scales (serving of few tokens): w = scale (code - zero), codes and zeros 0 to
  * 15, one bf16 scale and one zero point for each `group` (32, 64 or 128) consecutive elements of a row along the
  * contraction. Activations stay bf16; products of codes and activations are exact and summed in fp32, a group's
- * sum is scaled in fp32.
+ * sum is scaled in fp32. The sum runs over (16 + code) x from -(16 + zero) sum x: terms of up to 31 |x|. Where sum |x|
+ * of a group passes 2^122 it may overflow, and an activation that is not finite gives infinities or NaNs in its token's rows.
  *
  * moe_w4_quantize_rows -- rows of a bf16 matrix w [rows, K] into codes [rows, ceil(K / 2)] (element 2i in the low
  *   half of byte i; a last half byte is 0), scales and zeros [rows, ceil(K / group)]: with lo = min(0, min w) and

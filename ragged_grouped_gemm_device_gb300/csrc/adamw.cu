@@ -6,7 +6,7 @@
 // Bound by memory with fp32 states: p, m and v are read and written once, g is read once (28 bytes an element, 30 with a bf16 copy:
 // 201 million elements 900 us, 6.7 TB/s, and the norm before, which reads g once more, 122). Bound by instructions with 8-bit states:
 // 12 bytes an element, but about 80 instructions, the random roundings among them (192 million elements 499 us, 4.7 TB/s).
-// Many small tensors: 72 tensors 34 us, the time of their bytes. The tensors are cut into pieces of
+// Many small tensors: 72 tensors 34 us, 28 for their bytes. The tensors are cut into pieces of
 // CHUNK elements, of which each block takes a run; the descriptors travel in the kernel's parameters, and a block finds its first
 // tensor by bisecting the first pieces. A thread owns eight consecutive elements, moved 16 bytes at a time where the
 // pointers allow it. All arithmetic is fp32; the bias corrections are -expm1(t log b), whose error is a unit in the

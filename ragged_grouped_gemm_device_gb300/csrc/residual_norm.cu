@@ -59,7 +59,7 @@ struct JoinArgs {
 
 // ------------------------------------------------------------------ rows of any width
 // Rows wider than 8192: one block a row, single elements, one pass over the row for each reduction (the later ones from L2), bound by
-// the instructions of single elements (2048 x 10000 bf16: forward 155 us, backward 453).
+// the instructions of single elements (2048 x 10000 bf16, RMS norms and gate: forward 181 us, backward with every gradient 466).
 constexpr int WIDE_THREADS = 512;
 
 template <typename T>
@@ -281,7 +281,10 @@ struct RowFeed {
     return b;
   }
   static constexpr int slot_bytes = before(NT);
-  static constexpr int depth = slot_bytes <= 16 * 1024 ? 4 : slot_bytes <= 32 * 1024 ? 3 : slot_bytes <= 96 * 1024 ? 2 : 1;  // rows on their way
+  // Rows on their way: as many as leave room for the blocks of an SM. One, whose copies then start behind the row before, is left for the
+  // backward of fp32 streams and branches wider than 4096 (4096 x 8192 with every gradient: 227 us, 119 for its bytes; 8192 x 4096
+  // with two rows 132).
+  static constexpr int depth = slot_bytes <= 16 * 1024 ? 4 : slot_bytes <= 32 * 1024 ? 3 : slot_bytes <= 96 * 1024 ? 2 : 1;
   static constexpr int smem_bytes = depth * slot_bytes;
   // A lane copies 16 bytes at a time: of bf16 rows its own chunk; of fp32 rows, whose chunks are 32 bytes, one quarter of
   // those of two lanes, so that a warp's accesses are contiguous. Its first address in the next row of each tensor:
@@ -819,7 +822,8 @@ cudaError_t launch_bwd_rows(const JoinArgs& a, bool bias, cudaStream_t s, int& b
 }
 
 // Rows go through registers up to a width of 8192, wider ones through the kernels of any width. Off the 16-byte grid the registers
-// are filled by single elements (16384 x 2047 bf16: forward 80 us, backward 148; through the kernels of any width 414 and 677).
+// are filled by single elements (16384 x 2047 bf16, RMS norms and gate: forward 80 us, backward with every gradient 149; through the kernels
+// of any width 414 and 677).
 constexpr int REGISTER_WIDTH = 8192;
 
 template <bool VEC, typename TX, typename TY>

@@ -8,8 +8,9 @@
 // 16 rows by 8 columns by 16 elements are one matrix instruction on bf16 values 16 + code, which a code becomes by one instruction
 // for two; so few tokens' columns are mostly empty, but a weight is unpacked once for up to eight tokens, and unpacking is what
 // bounds these products besides memory: 7 instructions of the half-rate pipe for eight codes. One token, 4096 x 4096: 3.7 us
-// (2.4 TB/s; a launch and three round trips to memory). 16 tokens, 8 of 128 experts of 2048 x 768, groups of 32: 66.9 us (3.3 TB/s;
-// measured before SwiGLU's output had two parts, at 63: without the arithmetic the two products take 30 and 23, without the loads 37 and 34).
+// (2.4 TB/s; a launch and two round trips to memory, one for each segment of 2048 elements of the weights). 16 tokens, 8 of 128
+// experts of 2048 x 768, groups of 32: 66.9 us (3.3 TB/s). At 63 us, before SwiGLU's output had two parts, the two products took 30 and 23
+// without the arithmetic and 37 and 34 without the loads.
 #include <algorithm>
 
 #include "common.cuh"
@@ -440,8 +441,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 3) w4_slot_kernel
 
 // ------------------------------------------------------------------ several tokens
 // Groups of up to 8 NT slots of one expert, each with all tiles of its weights, are one list of tasks (group, tile set) that the
-// blocks share evenly, each a run of it: an expert's weights are read once, and x of a group is fetched once or twice. A
-// warp's pieces go through a ring of its own in shared memory, filled by asynchronous copies that run ahead over tasks and
+// blocks share evenly, each a run of it: an expert's weights are read once for each of its groups. x of a group is fetched once or twice
+// by a block while it fits shared memory, and for each task where it is longer (K above 2048, of
+// moe_w4_matvec's groups of eight above 4096; 16 tokens, 8 of 64 experts of 4096 x 2048, groups of 128: 330 us for both products, 109 for their
+// bytes). A warp's pieces go through a ring of its own in shared memory, filled by asynchronous copies that run ahead over tasks and
 // groups, so that the copies in flight do not depend on how far the sums are, and no warp waits for another's.
 struct StreamShape {
   int wk;       // warps that share K; WARPS / wk tiles (with SWIGLU pairs of tiles) are a task
@@ -831,7 +834,8 @@ cudaError_t launch_product(const W4Args& a, cudaStream_t s) {
   }
   // Tokens of an expert, on average. With more than eight of them groups of 16 slots unpack its weights half as often, in one block of 16
   // warps, whose shared memory x fills (128 tokens, 8 of 64 experts of 2048 x 768: 133 us, 155 in groups of eight; with eight tokens
-  // an expert both take 99 to 101, with four the larger groups 86 instead of 76).
+  // an expert both take 99 to 101, with four the larger groups 86 instead of 76; all before SwiGLU's output had two parts, with
+  // which the 133 are 146).
   const int each = a.ids == nullptr ? a.slots : a.slots / a.E;
   return each <= 8 ? launch_stream<PER, 1, SWIGLU, SPLIT>(a, s) : launch_stream<PER, 2, SWIGLU, SPLIT>(a, s);
 }
@@ -850,7 +854,9 @@ cudaError_t launch_down_token(const W4Args& a, int T, cudaStream_t s) {
 }
 
 // Whether the down product takes token by token. It then reads an expert's weights once for each slot, from the L2 but the
-// first time, and saves the fp32 rows and a launch.
+// first time, and saves the fp32 rows and a launch. The decode step so and by the list of tasks (us): 128 experts of 2048 x 768, 8 slots 10.5
+// and 13.4, 32 slots 33.1 and 35.3, 48 slots 40.0 and 37.5, 128 slots 76.9 and 60.0; 256 of 2048 x 512, 32 slots 30.1 and 32.9, 64 slots
+// 43.0 and 42.4; 8 of 2048 x 1024, 8 slots 16.8 and 21.6, 16 slots 22.4 and 23.1.
 bool down_by_token(long long slots, int E) { return slots <= std::max(8, E / 4); }
 int pitch_of(int h) { return (h + 7) / 8 * 8; }
 
