@@ -24,7 +24,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .layer import ExpertLayer, _dense
+from .layer import ExpertLayer, _dense, _hold_captured
 
 _ITSELF = "itself"  # who asked for a plain block's last run
 
@@ -65,8 +65,12 @@ class MoEBlock:
         self._joins = None if self.plain else _Joins()
 
     def _buffers(self, T: int):
-        if self._T == T:
-            return
+        if self._T != T:
+            self._allocate(T)
+        _hold_captured(self, self.normed, self.mean, self.rstd, self.logits, self.ids, self.weights, self.lse, self.counts, self.n_valid,
+                       self.prob_sum, self.loss, self.gate_ws, self.norm_ws, self.dlogits, self.dnormed, self.dx, self.dgamma, self.dbeta)
+
+    def _allocate(self, T: int):
         f32, i32, bf = torch.float32, torch.int32, torch.bfloat16
         E, d, k = self.E, self.d, self.k
         new = lambda *shape, dtype=f32: torch.empty(*shape, dtype=dtype, device=self.device)  # noqa: E731
@@ -171,8 +175,11 @@ class _Joins:
     def _buffers(self, blocks, T: int):
         for b in blocks:
             b._buffers(T)
-        if self._T == T:
-            return
+        if self._T != T:
+            self._allocate(blocks, T)
+        _hold_captured(self, self.rows, self.stats, self.dx, self.dy, self.ws)
+
+    def _allocate(self, blocks, T: int):
         d, dev, count = blocks[0].d, blocks[0].device, len(blocks)
         new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
         self.rows = new(count, T, d, dtype=torch.bfloat16)       # r behind each block

@@ -27,6 +27,15 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
+def _hold_captured(owner, *buffers):
+    """Called wherever `owner` is about to use `buffers`: while a graph is captured they are kept as long as owner lives, because calls
+    of other sizes put others in their place and the graph goes on to use these."""
+    if torch.cuda.is_current_stream_capturing():
+        held = owner.__dict__.setdefault("_captured", [])
+        if not any(h[0] is buffers[0] for h in held):
+            held.append(buffers)
+
+
 class ExpertLayer:
     """Holds the expert weights W_ug [E, 2h, d] and W_down [E, h, d] (bf16, on the device)."""
 
@@ -42,8 +51,12 @@ class ExpertLayer:
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def _buffers(self, T: int, k: int):
-        if self._key == (T, k):
-            return
+        if self._key != (T, k):
+            self._allocate(T, k)
+        _hold_captured(self, self.out, self.counts, self.offsets, self.sorted_src, self.inv_map, self.route_ws, self.xp, self.y, self.a,
+                       self.saved, self.dy, self.dxp, self.dx, self.dw_ug, self.dw_down, self.dw_route, self.fwd_ws, self.bwd_ws)
+
+    def _allocate(self, T: int, k: int):
         dev, E, d, h, n = self.device, self.E, self.d, self.h, T * k
         i32, bf = torch.int32, torch.bfloat16
         self.counts = torch.empty(E, dtype=i32, device=dev)
@@ -132,8 +145,12 @@ class Mxfp4ExpertLayer:
         self._key = None
 
     def _buffers(self, T: int, k: int):
-        if self._key == (T, k):
-            return
+        if self._key != (T, k):
+            self._allocate(T, k)
+        _hold_captured(self, self.out, self.counts, self.offsets, self.sorted_src, self.inv_map, self.route_ws, self.fwd_ws, self.xq,
+                       self.xsf, self.y)
+
+    def _allocate(self, T: int, k: int):
         E, d, h, n = self.E, self.d, self.h, T * k
         new = lambda *shape, dtype: torch.empty(*shape, dtype=dtype, device=self.device)  # noqa: E731
         room = lambda op: new(max(1, _lib.moe_workspace_bytes(op, T, k, E, d, h)), dtype=torch.uint8)  # noqa: E731
@@ -218,8 +235,11 @@ class Int4ExpertLayer:
         self._key = None
 
     def _buffers(self, T: int, k: int):
-        if self._key == (T, k):
-            return
+        if self._key != (T, k):
+            self._allocate(T, k)
+        _hold_captured(self, self.out, self.ws)
+
+    def _allocate(self, T: int, k: int):
         piece = min(T, _lib.W4_MAX_SLOTS // k)
         n = _lib.moe_workspace_bytes(_lib.OP_W4_DECODE, piece, k, self.E, self.d, self.h)
         self.ws = torch.empty(max(n, 1), dtype=torch.uint8, device=self.device)
