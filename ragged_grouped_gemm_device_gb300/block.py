@@ -67,8 +67,7 @@ class MoEBlock:
     def _buffers(self, T: int):
         if self._T != T:
             self._allocate(T)
-        _hold_captured(self, self.normed, self.mean, self.rstd, self.logits, self.ids, self.weights, self.lse, self.counts, self.n_valid,
-                       self.prob_sum, self.loss, self.gate_ws, self.norm_ws, self.dlogits, self.dnormed, self.dx, self.dgamma, self.dbeta)
+        _hold_captured(self)
 
     def _allocate(self, T: int):
         f32, i32, bf = torch.float32, torch.int32, torch.bfloat16
@@ -177,7 +176,7 @@ class _Joins:
             b._buffers(T)
         if self._T != T:
             self._allocate(blocks, T)
-        _hold_captured(self, self.rows, self.stats, self.dx, self.dy, self.ws)
+        _hold_captured(self)
 
     def _allocate(self, blocks, T: int):
         d, dev, count = blocks[0].d, blocks[0].device, len(blocks)

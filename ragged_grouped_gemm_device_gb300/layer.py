@@ -27,13 +27,11 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _hold_captured(owner, *buffers):
-    """Called wherever `owner` is about to use `buffers`: while a graph is captured they are kept as long as owner lives, because calls
-    of other sizes put others in their place and the graph goes on to use these."""
+def _hold_captured(owner):
+    """Called wherever `owner` is about to use its buffers: while a graph is captured they are kept as long as owner lives, because
+    calls of other sizes put others in their place and the graph goes on to use these."""
     if torch.cuda.is_current_stream_capturing():
-        held = owner.__dict__.setdefault("_captured", [])
-        if not any(h[0] is buffers[0] for h in held):
-            held.append(buffers)
+        owner.__dict__.setdefault("_captured", []).append([t for t in vars(owner).values() if isinstance(t, torch.Tensor)])
 
 
 class ExpertLayer:
@@ -53,8 +51,7 @@ class ExpertLayer:
     def _buffers(self, T: int, k: int):
         if self._key != (T, k):
             self._allocate(T, k)
-        _hold_captured(self, self.out, self.counts, self.offsets, self.sorted_src, self.inv_map, self.route_ws, self.xp, self.y, self.a,
-                       self.saved, self.dy, self.dxp, self.dx, self.dw_ug, self.dw_down, self.dw_route, self.fwd_ws, self.bwd_ws)
+        _hold_captured(self)
 
     def _allocate(self, T: int, k: int):
         dev, E, d, h, n = self.device, self.E, self.d, self.h, T * k
@@ -147,8 +144,7 @@ class Mxfp4ExpertLayer:
     def _buffers(self, T: int, k: int):
         if self._key != (T, k):
             self._allocate(T, k)
-        _hold_captured(self, self.out, self.counts, self.offsets, self.sorted_src, self.inv_map, self.route_ws, self.fwd_ws, self.xq,
-                       self.xsf, self.y)
+        _hold_captured(self)
 
     def _allocate(self, T: int, k: int):
         E, d, h, n = self.E, self.d, self.h, T * k
@@ -237,7 +233,7 @@ class Int4ExpertLayer:
     def _buffers(self, T: int, k: int):
         if self._key != (T, k):
             self._allocate(T, k)
-        _hold_captured(self, self.out, self.ws)
+        _hold_captured(self)
 
     def _allocate(self, T: int, k: int):
         piece = min(T, _lib.W4_MAX_SLOTS // k)
