@@ -626,7 +626,8 @@ moe_status_t moe_residual_norm_bwd(const void* dn, long long lddn, const void* d
  *   mix(key + i 0x9E3779B9 + (i >> 32) 0x85EBCA6B),  key = mix(seed ^ mix(0x9E3779B9 t + j))
  * for element i of tensor j of the call, mod 2^32, mix the finalizer of MurmurHash3: the low 16 bits for m, the
  * high for v, the middle for p. Results are deterministic. The tensors of a call may not overlap, and one
- *   tensor may not be updated by two calls at a time. An eps above 0 counts as 2^-126 at least.
+ *   tensor may not be updated by two calls at a time. An eps above 0 counts as 2^-126 at least. The quotient is
+ *   a product with a reciprocal, off by at most two units of its last place.
  * moe_grad_norm: norm[0] = sqrt(sum of all g^2), norm[1] = min(1, max_norm / norm[0]) (NaN where norm[0] is not
  * finite): a grad_scale that clips. Summed in a fixed order, in fp64 over pieces of 4096 summed in fp32 (where a
  * piece's sum of squares passes 2^128, the norm is not finite; squares below 2^-149 count as 0); reads
